@@ -3,6 +3,15 @@
 The CUDA library (liblilicorr.so, built in-tree by build.build()) holds the whole path;
 this package marshals arguments to its C ABI.
 """
+from .decode import (  # noqa: F401
+    KV8Cache,
+    beam_reorder,
+    beam_select,
+    beam_select_workspace,
+    kv8_append,
+    kv8_attention,
+    kv8_attention_workspace,
+)
 from .api import (  # noqa: F401
     LilicorrError,
     Weights,

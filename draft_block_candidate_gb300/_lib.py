@@ -48,6 +48,20 @@ SIGNATURES = {
                                                       C.c_int32]),
     "lilicorr_lm_head_topk_lse": (C.c_int, [_P, _P, C.c_int64, C.c_int64, C.c_int32, C.c_int32,
                                             _P, _P, _P, _P, C.c_size_t, _P]),
+    "lilicorr_beam_select_workspace_bytes": (C.c_size_t, [C.c_int64, C.c_int32, C.c_int64,
+                                                          C.c_int32, C.c_int]),
+    "lilicorr_beam_select": (C.c_int, [_P, C.c_int, C.c_int64, C.c_int32, C.c_int64, C.c_int64,
+                                       C.c_int32, _P, _P, C.c_int32, _P, _P, _P, _P, C.c_size_t,
+                                       _P]),
+    "lilicorr_beam_reorder": (C.c_int, [_P, C.c_int32, _P, C.c_int64, C.c_int32, _P]),
+    "lilicorr_kv8_append": (C.c_int, [_P, _P, C.c_int64, C.c_int64, _P, C.c_int64, C.c_int64,
+                                      C.c_int64, _P, _P, C.c_int64, _P, C.c_int64, C.c_int32,
+                                      C.c_int32, _P, _P]),
+    "lilicorr_kv8_attention_workspace_bytes": (C.c_size_t, [C.c_int32, C.c_int32, C.c_int32,
+                                                            C.c_int32]),
+    "lilicorr_kv8_attention": (C.c_int, [_P, _P, C.c_int64, C.c_int64, C.c_int64, C.c_int32, _P,
+                                         _P, C.c_int64, _P, C.c_int64, C.c_int32, C.c_int32,
+                                         C.c_float, _P, _P, _P, C.c_size_t, _P]),
     "lilicorr_status_string": (C.c_char_p, [C.c_int]),
     "lilicorr_last_error": (C.c_char_p, []),
     "lilicorr_launch_count": (C.c_uint64, []),
@@ -70,6 +84,19 @@ class Dims(C.Structure):
 class Tensor(C.Structure):
     _fields_ = [("name", C.c_char_p), ("host_data", C.c_void_p), ("dtype", C.c_int),
                 ("ndim", C.c_int32), ("shape", C.c_int64 * 4)]
+
+
+class BeamState(C.Structure):
+    _fields_ = [("src", C.c_void_p), ("dst", C.c_void_p)] + [
+        (n, C.c_int64) for n in ("src_batch_stride", "src_beam_stride", "src_seg_stride",
+                                 "dst_batch_stride", "dst_beam_stride", "dst_seg_stride",
+                                 "segments", "seg_bytes")]
+
+
+class Kv8CacheDesc(C.Structure):
+    _fields_ = [("k_pages", C.c_void_p), ("v_pages", C.c_void_p), ("k_scale", C.c_void_p),
+                ("v_scale", C.c_void_p), ("n_pages", C.c_int64), ("kv_heads", C.c_int32),
+                ("page", C.c_int32), ("head_dim", C.c_int32)]
 
 
 class Taps(C.Structure):

@@ -1,0 +1,403 @@
+// Beam search next to the rerank: the choice over beams and vocabulary from one step's
+// logits (the logit pass of step a1 followed by a merge over the beams), and the gather
+// of per-beam states by the chosen parents.
+#include <climits>
+#include <cmath>
+
+#include <algorithm>
+
+#include "kernels.cuh"
+
+namespace lilicorr {
+
+static __device__ uint32_t g_err_beam;
+
+// ------------------------------------------------------------------------------ selection
+// s(i, v) = score_i + x_iv - log sum_u exp x_iu, the M best of a batch entry's beams by
+// (s desc, i * V + v asc).  Within a beam the order is that of its logits, so a beam's part
+// of the M best are among its own M best logits, which the logit pass leaves in the beam's
+// row record beside (m2, S), sum_u exp x_iu = S 2^m2 in units of base 2.  The merge takes
+// the best head of the beams' sorted lists M times.
+//
+// Ranks are decided in double: two beams' candidates may differ by less than the float
+// rounding of a score of a few tens (2e-6), and then a float score would rank them by its
+// rounding.  The score is rounded to float once, as it is stored.  The logit pass scales its
+// logits by the float nearest log2 e, so (m2 + log2 S) is divided by that same float.
+//
+// One warp per batch entry, lane i = beam i, records staged in shared memory by the whole
+// CTA.  Each of the M steps is two 32-bit warp maxima (the high and the low word of an
+// order-preserving integer key of the double) and a ballot for the lowest beam.
+
+// Order-preserving key: unsigned comparison of keys = comparison of the doubles.
+__device__ __forceinline__ uint64_t double_key(double d) {
+  const int64_t b = __double_as_longlong(d + 0.0);
+  return b < 0 ? ~static_cast<uint64_t>(b) : static_cast<uint64_t>(b) | (1ull << 63);
+}
+
+constexpr int BM_THREADS = 128;
+constexpr int BM_MAX = 32;  // beams, and entries taken
+
+__global__ void __launch_bounds__(BM_THREADS)
+    beam_merge_kernel(const char* __restrict__ records, const float* __restrict__ scores,
+                      const uint8_t* __restrict__ finished, int beams, int K, int M, int pad_id,
+                      float* __restrict__ out_score, int32_t* __restrict__ out_token,
+                      int32_t* __restrict__ out_parent) {
+  __shared__ float s_v[BM_MAX][BM_MAX + 1];
+  __shared__ int s_id[BM_MAX][BM_MAX + 1];
+  __shared__ float s_m[BM_MAX], s_s[BM_MAX];
+  const int64_t b = blockIdx.x;
+  const int tid = threadIdx.x;
+  pdl_wait();
+  pdl_trigger();
+  // record of a row: {f32 m2, f32 S, f32 v[K], i32 id[K]}
+  const int words = 2 * K + 2;
+  const int32_t* rec = reinterpret_cast<const int32_t*>(records) + b * beams * words;
+  for (int i = tid; i < beams * words; i += BM_THREADS) {
+    const int w = i / words, j = i % words;
+    const int32_t x = __ldcg(rec + i);
+    if (j == 0) s_m[w] = __int_as_float(x);
+    else if (j == 1) s_s[w] = __int_as_float(x);
+    else if (j < 2 + K) s_v[w][j - 2] = __int_as_float(x);
+    else s_id[w][j - 2 - K] = x;
+  }
+  __syncthreads();
+  if (tid >= 32) return;
+
+  const int lane = tid;
+  constexpr double NONE = -INFINITY;
+  double score = NONE, norm = 0.0;  // this beam's own score; its log-partition
+  int left = 0, at = 0;              // candidates of the list; the list's head
+  bool done = false;
+  if (lane < beams) {
+    score = static_cast<double>(scores[b * beams + lane]);
+    done = finished && finished[b * beams + lane];
+    if (score > NONE) {
+      if (done) {
+        left = 1;
+      } else if (s_s[lane] > 0.f) {  // a row with no finite logit has no candidate
+        left = K;
+        norm = (static_cast<double>(s_m[lane]) + log2(static_cast<double>(s_s[lane]))) /
+               static_cast<double>(1.4426950408889634f);
+      }
+    }
+  }
+  auto head = [&]() -> double {
+    if (at >= left) return NONE;
+    if (done) return score;
+    const double s = score + (static_cast<double>(s_v[lane][at]) - norm);
+    return s == s ? s : NONE;
+  };
+  double mine = head();
+  float r_score = -INFINITY;
+  int r_token = pad_id, r_parent = 0;
+  for (int j = 0; j < M; ++j) {
+    const uint64_t key = double_key(mine);
+    const uint32_t hi = static_cast<uint32_t>(key >> 32), lo = static_cast<uint32_t>(key);
+    const uint32_t mhi = __reduce_max_sync(FULL_MASK, hi);
+    const uint32_t mlo = __reduce_max_sync(FULL_MASK, hi == mhi ? lo : 0u);
+    const unsigned who = __ballot_sync(FULL_MASK, hi == mhi && lo == mlo);
+    const int win = __ffs(who) - 1;
+    const double best = __shfl_sync(FULL_MASK, mine, win);
+    if (!(best > NONE)) break;  // no candidate is left: the rest are fillers
+    const int pos = __shfl_sync(FULL_MASK, at, win);
+    const bool wdone = __shfl_sync(FULL_MASK, done ? 1 : 0, win) != 0;
+    if (lane == j) {
+      r_score = static_cast<float>(best);
+      r_token = wdone ? pad_id : s_id[win][pos];
+      r_parent = win;
+    }
+    if (lane == win) {
+      ++at;
+      mine = head();
+    }
+  }
+  if (lane < M) {
+    out_score[b * M + lane] = r_score;
+    out_token[b * M + lane] = r_token;
+    out_parent[b * M + lane] = r_parent;
+  }
+}
+
+// ---------------------------------------------------------------------------- reordering
+// dst[b, j] = src[b, parent[b, j]] for every state.  A thread owns one column (a vector of
+// up to 16 bytes at the same place of every beam's row) of a batch entry: it reads the
+// column of every wanted parent, then writes every beam's, so a gather in place needs no
+// second buffer and no order between threads; a beam that keeps its own row in place is
+// neither read nor written.  Bound by HBM; several parents' reads of one line meet in L1.
+constexpr int BR_MAX_STATES = 16;
+constexpr int BR_THREADS = 256;
+
+struct ReorderState {
+  const char* src;
+  char* dst;
+  int64_t s_batch, s_beam, s_seg, d_batch, d_beam, d_seg;  // bytes
+  int64_t segs;
+  uint32_t seg_cols;   // vectors of a segment
+  int vec;             // bytes of a vector: 16, 8, 4, 2 or 1
+  int64_t cols;        // vectors of a row: segs * seg_cols
+  int64_t first_tile;  // of the whole grid; tiles of BR_THREADS columns, batch-major
+  int64_t tiles;       // of one batch entry
+};
+struct ReorderParams {
+  ReorderState st[BR_MAX_STATES];
+  int n;
+  const int32_t* parent;
+  int64_t batch;
+  int beams;
+};
+
+template <typename T, int W>
+__device__ __forceinline__ void reorder_column(const ReorderState& s, const int* par, int beams,
+                                               int64_t b, int64_t seg, int64_t off) {
+  const char* src = s.src + b * s.s_batch + seg * s.s_seg + off;
+  char* dst = s.dst + b * s.d_batch + seg * s.d_seg + off;
+  const bool inplace = s.src == s.dst;
+  T v[W];
+#pragma unroll
+  for (int j = 0; j < W; ++j) {
+    if (j < beams) {
+      const int p = par[j];
+      if (p >= 0 && !(inplace && p == j)) v[j] = *reinterpret_cast<const T*>(src + p * s.s_beam);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < W; ++j) {
+    if (j < beams) {
+      const int p = par[j];
+      if (p >= 0 && !(inplace && p == j)) *reinterpret_cast<T*>(dst + j * s.d_beam) = v[j];
+    }
+  }
+}
+
+template <int W>
+__global__ void __launch_bounds__(BR_THREADS) beam_reorder_kernel(const __grid_constant__ ReorderParams p) {
+  __shared__ int s_par[W];
+  const int64_t tile = blockIdx.x;
+  int k = 0;
+  while (k + 1 < p.n && tile >= p.st[k + 1].first_tile) ++k;
+  const ReorderState& s = p.st[k];
+  const int64_t t = tile - s.first_tile;
+  const int64_t b = t / s.tiles;
+  const int64_t col = (t % s.tiles) * BR_THREADS + threadIdx.x;
+  if (threadIdx.x < p.beams) {
+    int q = p.parent[b * p.beams + threadIdx.x];
+    if (q < 0 || q >= p.beams) {  // no such beam: its row stays as it is
+      atomicOr(&g_err_beam, ERR_BEAM_PARENT);
+      q = -1;
+    }
+    s_par[threadIdx.x] = q;
+  }
+  __syncthreads();
+  if (col >= s.cols) return;
+  const int64_t seg = col / s.seg_cols;
+  const int64_t off = (col - seg * s.seg_cols) * s.vec;
+  switch (s.vec) {
+    case 16: reorder_column<uint4, W>(s, s_par, p.beams, b, seg, off); break;
+    case 8: reorder_column<uint2, W>(s, s_par, p.beams, b, seg, off); break;
+    case 4: reorder_column<uint32_t, W>(s, s_par, p.beams, b, seg, off); break;
+    case 2: reorder_column<uint16_t, W>(s, s_par, p.beams, b, seg, off); break;
+    default: reorder_column<uint8_t, W>(s, s_par, p.beams, b, seg, off); break;
+  }
+}
+
+cudaError_t beam_read_device_error(uint32_t* code) {
+  uint32_t v = 0, zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(&v, g_err_beam, sizeof(v));
+  if (e != cudaSuccess) return e;
+  if (v) e = cudaMemcpyToSymbol(g_err_beam, &zero, sizeof(zero));
+  *code |= v;
+  return e;
+}
+
+namespace {
+
+size_t align256(size_t n) { return (n + 255) / 256 * 256; }
+
+struct SelectPlan {
+  size_t records, pass, total;  // offsets of the row records and of the logit pass's part
+};
+
+bool select_sizes_ok(int64_t batch, int32_t beams, int64_t V, int32_t M, lilicorr_dtype dt) {
+  if (dt != LILICORR_F32 && dt != LILICORR_BF16) return false;
+  if (batch < 1 || beams < 1 || beams > BM_MAX || M < 1 || M > BM_MAX) return false;
+  const int es = dt == LILICORR_BF16 ? 2 : 4;
+  if (V < 1 || V > (int64_t(1) << 31) - 2 || V * es > (int64_t(1) << 31) - 64) return false;
+  // one CTA per row, or up to 90 when there are few rows
+  return batch <= ((int64_t(1) << 31) - 2) / beams;
+}
+
+SelectPlan select_plan(int64_t batch, int32_t beams, int64_t V, int32_t M, int es) {
+  const int64_t rows = batch * beams;
+  const int K = static_cast<int>(std::min<int64_t>(M, V));
+  SelectPlan pl{};
+  pl.records = 0;
+  pl.pass = align256(size_t(rows) * k1_shard_record_bytes(K));
+  pl.total = pl.pass + align256(k1_workspace_bytes(1, static_cast<int>(rows + 1), V, es));
+  return pl;
+}
+
+// Whether the byte ranges that (batch, beam, segment) strides reach from one base are
+// apart from one another: nested by stride, each stride at least what lies under it.
+bool strides_apart(int64_t batch, int64_t sb, int64_t beams, int64_t sw, int64_t segs, int64_t ss,
+                   int64_t bytes) {
+  std::pair<int64_t, int64_t> d[3] = {{sb, batch}, {sw, beams}, {ss, segs}};
+  std::sort(d, d + 3);
+  int64_t extent = bytes;
+  for (const auto& x : d) {
+    if (x.second <= 1) continue;
+    if (x.first < extent) return false;
+    extent += (x.second - 1) * x.first;
+  }
+  return true;
+}
+
+cudaError_t reorder_launch(const ReorderParams& prm, int64_t tiles, cudaStream_t stream) {
+  const dim3 grid(static_cast<unsigned>(tiles));
+  if (prm.beams <= 4) beam_reorder_kernel<4><<<grid, BR_THREADS, 0, stream>>>(prm);
+  else if (prm.beams <= 8) beam_reorder_kernel<8><<<grid, BR_THREADS, 0, stream>>>(prm);
+  else if (prm.beams <= 16) beam_reorder_kernel<16><<<grid, BR_THREADS, 0, stream>>>(prm);
+  else beam_reorder_kernel<32><<<grid, BR_THREADS, 0, stream>>>(prm);
+  note_launch();
+  return cudaGetLastError();
+}
+
+lilicorr_status fail(lilicorr_status st, const char* msg) {
+  set_last_error(msg);
+  return st;
+}
+
+}  // namespace
+}  // namespace lilicorr
+
+using namespace lilicorr;
+
+extern "C" {
+
+size_t lilicorr_beam_select_workspace_bytes(int64_t batch, int32_t beams, int64_t V, int32_t M,
+                                            lilicorr_dtype ldtype) {
+  if (!select_sizes_ok(batch, beams, V, M, ldtype)) return 0;
+  return select_plan(batch, beams, V, M, ldtype == LILICORR_BF16 ? 2 : 4).total;
+}
+
+lilicorr_status lilicorr_beam_select(const void* logits, lilicorr_dtype ldtype, int64_t batch,
+                                     int32_t beams, int64_t V, int64_t row_stride, int32_t M,
+                                     const float* scores, const uint8_t* finished, int32_t pad_id,
+                                     float* out_score, int32_t* out_token, int32_t* out_parent,
+                                     void* workspace, size_t workspace_bytes, void* stream_) {
+  if (!logits || !scores || !out_score || !out_token || !out_parent)
+    return fail(LILICORR_ERR_INVALID_ARG, "lilicorr_beam_select: null pointer");
+  if (!select_sizes_ok(batch, beams, V, M, ldtype) || row_stride < V ||
+      row_stride > (int64_t(1) << 40))
+    return fail(LILICORR_ERR_INVALID_ARG, "lilicorr_beam_select: a size is out of range");
+  const int es = ldtype == LILICORR_BF16 ? 2 : 4;
+  if (reinterpret_cast<uintptr_t>(logits) % es)
+    return fail(LILICORR_ERR_INVALID_ARG, "lilicorr_beam_select: misaligned logits");
+  const SelectPlan pl = select_plan(batch, beams, V, M, es);
+  if (!workspace || workspace_bytes < pl.total || reinterpret_cast<uintptr_t>(workspace) % 256)
+    return fail(LILICORR_ERR_WORKSPACE, "lilicorr_beam_select: workspace missing, too small or misaligned");
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+  char* ws = static_cast<char*>(workspace);
+  const int64_t rows = batch * beams;
+  const int K = static_cast<int>(std::min<int64_t>(M, V));
+  // The logit pass leaves row 0 of a block of B rows unread: one block of rows + 1 whose
+  // row 0 would lie before the logits.
+  const void* before = reinterpret_cast<const void*>(reinterpret_cast<uintptr_t>(logits) -
+                                                     uintptr_t(row_stride) * es);
+  cudaError_t e = k1_launch(before, es, 1, static_cast<int>(rows + 1), V, K, nullptr, nullptr,
+                            nullptr, ws + pl.pass, stream, row_stride, 0, ws + pl.records,
+                            WAIT_LIMIT_CYCLES, false, scores, finished);
+  if (e == cudaSuccess) {
+    PdlScope pdl(true);
+    e = launch_k(beam_merge_kernel, dim3(static_cast<unsigned>(batch)), dim3(BM_THREADS), 0,
+                 stream, static_cast<const char*>(ws + pl.records), scores, finished,
+                 static_cast<int>(beams), K, static_cast<int>(M), static_cast<int>(pad_id),
+                 out_score, out_token, out_parent);
+    if (e == cudaSuccess) note_launch();
+  }
+  if (e != cudaSuccess) return fail(LILICORR_ERR_CUDA, cudaGetErrorString(e));
+  return LILICORR_OK;
+}
+
+lilicorr_status lilicorr_beam_reorder(const lilicorr_beam_state* states, int32_t n_states,
+                                      const int32_t* parent, int64_t batch, int32_t beams,
+                                      void* stream) {
+  if (!states || !parent || n_states < 1)
+    return fail(LILICORR_ERR_INVALID_ARG, "lilicorr_beam_reorder: null pointer or no states");
+  if (batch < 1 || beams < 1 || beams > BM_MAX)
+    return fail(LILICORR_ERR_INVALID_ARG, "lilicorr_beam_reorder: 1 <= beams <= 32 and batch >= 1");
+  constexpr int64_t LIM = int64_t(1) << 46;  // keeps every byte offset far inside 64 bits
+  auto bad = [&](int64_t n) { return n < 0 || n > LIM; };
+  for (int i = 0; i < n_states; ++i) {
+    const lilicorr_beam_state& s = states[i];
+    if (!s.src || !s.dst || s.segments < 1 || s.seg_bytes < 1 || s.segments > LIM ||
+        s.seg_bytes > (int64_t(1) << 32) - 16 || bad(s.src_batch_stride) ||
+        bad(s.src_beam_stride) || bad(s.src_seg_stride) || bad(s.dst_batch_stride) ||
+        bad(s.dst_beam_stride) || bad(s.dst_seg_stride))
+      return fail(LILICORR_ERR_INVALID_ARG, "lilicorr_beam_reorder: a state's pointer, size or stride is out of range");
+    if (!strides_apart(batch, s.dst_batch_stride, beams, s.dst_beam_stride, s.segments,
+                       s.dst_seg_stride, s.seg_bytes))
+      return fail(LILICORR_ERR_INVALID_ARG, "lilicorr_beam_reorder: a state's destination rows overlap");
+    if (s.src == s.dst) {
+      if (s.src_batch_stride != s.dst_batch_stride || s.src_beam_stride != s.dst_beam_stride ||
+          s.src_seg_stride != s.dst_seg_stride)
+        return fail(LILICORR_ERR_INVALID_ARG, "lilicorr_beam_reorder: in place, the strides of source and destination are the same");
+    } else {
+      auto end = [&](const void* p, int64_t sb, int64_t sw, int64_t ss) {
+        return reinterpret_cast<uintptr_t>(p) + uintptr_t((batch - 1) * sb + (beams - 1) * sw +
+                                                          (s.segments - 1) * ss + s.seg_bytes);
+      };
+      const uintptr_t a0 = reinterpret_cast<uintptr_t>(s.src), b0 = reinterpret_cast<uintptr_t>(s.dst);
+      const uintptr_t a1 = end(s.src, s.src_batch_stride, s.src_beam_stride, s.src_seg_stride);
+      const uintptr_t b1 = end(s.dst, s.dst_batch_stride, s.dst_beam_stride, s.dst_seg_stride);
+      if (a0 < b1 && b0 < a1)
+        return fail(LILICORR_ERR_INVALID_ARG, "lilicorr_beam_reorder: source and destination overlap without being the same");
+    }
+  }
+  ReorderParams prm{};
+  int64_t tiles = 0;
+  auto flush = [&]() -> cudaError_t {
+    if (!prm.n) return cudaSuccess;
+    prm.parent = parent;
+    prm.batch = batch;
+    prm.beams = beams;
+    const cudaError_t e = reorder_launch(prm, tiles, static_cast<cudaStream_t>(stream));
+    prm = ReorderParams{};
+    tiles = 0;
+    return e;
+  };
+  for (int i = 0; i < n_states; ++i) {
+    const lilicorr_beam_state& s = states[i];
+    // the widest vector that every address and length is a multiple of
+    const uint64_t all = reinterpret_cast<uintptr_t>(s.src) | reinterpret_cast<uintptr_t>(s.dst) |
+                         uint64_t(s.src_batch_stride) | uint64_t(s.src_beam_stride) |
+                         uint64_t(s.src_seg_stride) | uint64_t(s.dst_batch_stride) |
+                         uint64_t(s.dst_beam_stride) | uint64_t(s.dst_seg_stride) |
+                         uint64_t(s.seg_bytes);
+    const int vec = all % 16 == 0 ? 16 : all % 8 == 0 ? 8 : all % 4 == 0 ? 4 : all % 2 == 0 ? 2 : 1;
+    ReorderState r{};
+    r.src = static_cast<const char*>(s.src);
+    r.dst = static_cast<char*>(s.dst);
+    r.s_batch = s.src_batch_stride; r.s_beam = s.src_beam_stride; r.s_seg = s.src_seg_stride;
+    r.d_batch = s.dst_batch_stride; r.d_beam = s.dst_beam_stride; r.d_seg = s.dst_seg_stride;
+    r.segs = s.segments;
+    r.vec = vec;
+    r.seg_cols = static_cast<uint32_t>(s.seg_bytes / vec);
+    r.cols = r.segs * int64_t(r.seg_cols);
+    r.tiles = (r.cols + BR_THREADS - 1) / BR_THREADS;
+    constexpr int64_t GRID = (int64_t(1) << 31) - 1;
+    if (r.tiles > GRID / batch)
+      return fail(LILICORR_ERR_INVALID_ARG, "lilicorr_beam_reorder: a state is too large for one call");
+    if (prm.n == BR_MAX_STATES || tiles > GRID - batch * r.tiles) {
+      const cudaError_t e = flush();
+      if (e != cudaSuccess) return fail(LILICORR_ERR_CUDA, cudaGetErrorString(e));
+    }
+    r.first_tile = tiles;
+    prm.st[prm.n++] = r;
+    tiles += batch * r.tiles;
+  }
+  const cudaError_t e = flush();
+  if (e != cudaSuccess) return fail(LILICORR_ERR_CUDA, cudaGetErrorString(e));
+  return LILICORR_OK;
+}
+
+}  // extern "C"

@@ -18,6 +18,9 @@ enum ErrSite : uint32_t {
   ERR_K1_FULL_WAIT = 1u << 0,
   ERR_K1_DRAIN = 1u << 1,
   ERR_K1_EMPTY_WAIT = 1u << 2,
+  ERR_BEAM_PARENT = 1u << 24,   // a parent index out of range
+  ERR_KV8_PAGE = 1u << 25,      // a page index out of range
+  ERR_KV8_LENGTH = 1u << 26,    // a length or row range out of range
 };
 
 // About one second at GB300 clocks: any wait longer than this is treated as a failure.

@@ -15,11 +15,15 @@ cudaError_t k1_launch(const void* logits, int esize, int64_t batch, int B, int64
                       int32_t* cand_id, float* cand_logit, float* lse, void* ws,
                       cudaStream_t stream, int64_t row_stride = 0, int id_offset = 0,
                       void* records = nullptr, long long wait_limit = WAIT_LIMIT_CYCLES,
-                      bool withhold_first = false);
+                      bool withhold_first = false, const float* row_score = nullptr,
+                      const uint8_t* row_done = nullptr);
 size_t k1_shard_record_bytes(int K);
 cudaError_t k1_merge_launch(const void* records, int n, int64_t rows, int K, int32_t* cand_id,
                             float* cand_logit, float* lse, cudaStream_t stream);
 cudaError_t k1_read_device_error(uint32_t* code);
+// beam selection and reordering (beam.cu), 8-bit cache (kv8.cu)
+cudaError_t beam_read_device_error(uint32_t* code);
+cudaError_t kv8_read_device_error(uint32_t* code);
 
 // message returned by lilicorr_last_error() for this thread (lilicorr_api.cu)
 void set_last_error(const char* msg);

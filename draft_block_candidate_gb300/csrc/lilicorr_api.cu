@@ -281,6 +281,8 @@ lilicorr_status lilicorr_device_error(uint32_t* code) {
   LC_CUDA(k1_read_device_error(code), "read device error");
   LC_CUDA(tc_read_device_error(code), "read device error");
   LC_CUDA(at_read_device_error(code), "read device error");
+  LC_CUDA(beam_read_device_error(code), "read device error");
+  LC_CUDA(kv8_read_device_error(code), "read device error");
   return *code ? LILICORR_ERR_DEVICE : LILICORR_OK;
 }
 

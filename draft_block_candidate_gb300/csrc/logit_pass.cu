@@ -119,6 +119,8 @@ struct K1Params {
   int withhold_first;    // self-check only: stage 0's copy is announced but never issued
   int64_t prefetch_ahead;  // > 0: at its last refill a CTA prefetches into L2 the first
                            // stage of unit blockIdx + prefetch_ahead (co-resident CTAs)
+  const float* row_score;   // beam search, nullable: rows whose score is -inf (or NaN) or
+  const uint8_t* row_done;  // (nullable) that are marked are not read and get no record
 };
 
 // Packed per-row record of a vocabulary shard: {m2, s, v[K], id[K]}, K * 8 + 8 bytes.
@@ -430,6 +432,7 @@ __global__ void __launch_bounds__(K1_THREADS, K1_MIN_BLOCKS) logit_pass_kernel(c
   __syncthreads();
   pdl_wait();
   pdl_trigger();
+  if (p.row_score && (!(p.row_score[r] > -INFINITY) || (p.row_done && p.row_done[r]))) return;
 
   float m2 = M2_INIT, ssum = 0.f;
   WarpQueue q;  // this warp's running top-32 (one entry per lane, sorted)
@@ -857,7 +860,8 @@ size_t k1_workspace_bytes(int64_t batch, int B, int64_t V, int esize) {
 cudaError_t k1_launch(const void* logits, int esize, int64_t batch, int B, int64_t V, int K,
                       int32_t* cand_id, float* cand_logit, float* lse, void* ws,
                       cudaStream_t stream, int64_t row_stride, int id_offset, void* records,
-                      long long wait_limit, bool withhold_first) {
+                      long long wait_limit, bool withhold_first, const float* row_score,
+                      const uint8_t* row_done) {
   const K1Plan pl = k1_plan(batch, B, V, esize);
   K1Params prm;
   prm.logits = static_cast<const char*>(logits);
@@ -877,6 +881,8 @@ cudaError_t k1_launch(const void* logits, int esize, int64_t batch, int B, int64
   prm.records = static_cast<char*>(records);
   prm.wait_limit = wait_limit;
   prm.withhold_first = withhold_first ? 1 : 0;
+  prm.row_score = row_score;
+  prm.row_done = row_done;
   {
     const int64_t resident = int64_t(K1_MIN_BLOCKS) * device_sm_count();
     prm.prefetch_ahead = batch * (B - 1) * pl.P > resident ? resident : 0;

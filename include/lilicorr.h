@@ -283,6 +283,129 @@ lilicorr_status lilicorr_sample_walk(const float* pair_scores, const int32_t* ca
                                      int32_t K, int32_t* tokens, int32_t* choice,
                                      float* path_score, float* proposal, void* stream);
 
+/* ---- Decoding around the rerank: several hypotheses, and the cache the target reads ----
+ * (the pages have no counterpart; these stand beside lilicorr_topk_lse, the walks and
+ * lilicorr_lm_head_topk_lse: the choice over beams and vocabulary, the states that follow
+ * it, and the attention by which a target checks a committed block over its cache.) */
+
+/* Beam search's choice over beams and vocabulary.  With x = logits and, for every live beam i
+ * of a batch entry,
+ *   s(i, v) = scores[i] + x[i,v] - log sum_u exp(x[i,u]),
+ * out_score / out_token / out_parent [batch, M] are the M best (s, v, i) by (s descending,
+ * i * V + v ascending); ranks are decided in double, the score is rounded to f32 once.
+ *   logits    [batch, beams, V] F32 or BF16, rows row_stride >= V elements apart, element
+ *             aligned; -inf marks a token that may not be taken; a row without a finite
+ *             logit has no candidates
+ *   scores    [batch, beams] f32 cumulative log-probabilities; a beam at -inf (or NaN) is
+ *             dead: it has no candidates and its logits are not read
+ *   finished  nullable [batch, beams]: a nonzero beam goes on as itself, with the one
+ *             candidate (scores[i], pad_id, i); its logits are not read
+ * Where fewer than M candidates exist the rest are (-inf, pad_id, 0).
+ * 1 <= beams <= 32, 1 <= M <= 32, 1 <= V < 2^31 - 1, a row under 2 GiB.  Workspace:
+ * lilicorr_beam_select_workspace_bytes (0 for unsupported sizes), 256-byte aligned.
+ * Errors: LILICORR_ERR_INVALID_ARG, LILICORR_ERR_WORKSPACE, LILICORR_ERR_CUDA. */
+size_t lilicorr_beam_select_workspace_bytes(int64_t batch, int32_t beams, int64_t V, int32_t M,
+                                            lilicorr_dtype ldtype);
+lilicorr_status lilicorr_beam_select(const void* logits, lilicorr_dtype ldtype, int64_t batch,
+                                     int32_t beams, int64_t V, int64_t row_stride, int32_t M,
+                                     const float* scores, const uint8_t* finished, int32_t pad_id,
+                                     float* out_score, int32_t* out_token, int32_t* out_parent,
+                                     void* workspace, size_t workspace_bytes, void* stream);
+
+/* One per-beam state of lilicorr_beam_reorder: row (b, j) starts at src + b * src_batch_stride
+ * + j * src_beam_stride and is `segments` pieces of seg_bytes, src_seg_stride apart (the used
+ * part of a longer cache, say); likewise dst.  Strides in bytes, not negative. */
+typedef struct {
+  const void* src;
+  void* dst;
+  int64_t src_batch_stride, src_beam_stride, src_seg_stride;
+  int64_t dst_batch_stride, dst_beam_stride, dst_seg_stride;
+  int64_t segments, seg_bytes;
+} lilicorr_beam_state;
+
+/* dst[b, j] = src[b, parent[b, j]] for every state, in as few launches as there are groups of
+ * 16 states.  src == dst (with equal strides) gathers in place, with no second buffer; src
+ * and dst that overlap in any other way are refused, and so are destination rows that overlap
+ * one another.  Different states must not share bytes that are written.  parent [batch, beams]
+ * is device memory; a parent outside 0..beams-1 leaves its row of dst as it was and sets bit 24
+ * of the device error word.  `states` is host memory, read before the call returns.
+ * 1 <= beams <= 32.  Errors: LILICORR_ERR_INVALID_ARG, LILICORR_ERR_CUDA. */
+lilicorr_status lilicorr_beam_reorder(const lilicorr_beam_state* states, int32_t n_states,
+                                      const int32_t* parent, int64_t batch, int32_t beams,
+                                      void* stream);
+
+/* A paged key / value cache held in 8 bits: codes are e4m3 (bias 7, largest 448, no infinity,
+ * 0x7F / 0xFF NaN), and what a code stands for is code * scale[page, head].
+ *   k_pages, v_pages  [n_pages, kv_heads, page, head_dim] codes, 16-byte aligned
+ *   k_scale, v_scale  [n_pages, kv_heads] f32, positive and finite (powers of two where
+ *                     lilicorr_kv8_append wrote them)
+ *   page in {16, 32, 64, 128} tokens, head_dim in {32, 64, 128}, 1 <= kv_heads <= 1024
+ * A sequence's tokens t lie in page block_table[b, t / page] at row t % page.  Device memory,
+ * the caller's; the struct itself is host memory. */
+typedef struct {
+  void *k_pages, *v_pages;
+  float *k_scale, *v_scale;
+  int64_t n_pages;
+  int32_t kv_heads, page, head_dim;
+} lilicorr_kv8_cache;
+
+/* What both cache entry points take of a batch of sequences (device memory but for the sizes):
+ *   q_start      [batch + 1] int32: sequence b's new tokens are rows q_start[b] ..
+ *                q_start[b+1] - 1 of the `total` rows given; rows outside are not touched
+ *   kv_len       [batch] int32: its tokens in the cache, the new ones among them
+ *   block_table  [batch, cols] int32, rows table_stride elements apart
+ *   max_new      at least every sequence's number of new tokens
+ * A sequence whose row range or length is out of range (decreasing q_start, rows behind
+ * `total`, more than max_new new tokens, a length over cols * page) is left out, and one with
+ * a page index outside 0..n_pages-1 has that page left out; bit 26 or 25 of the device error
+ * word is set.
+ *
+ * lilicorr_kv8_append writes the new tokens' keys and values (bf16, element strides by token
+ * and head, multiples of 8, 16-byte aligned) into the cache at positions kv_len - n ..
+ * kv_len - 1.  Each page and head that grows takes as its scale the smallest power of two
+ * 2^k >= 2^-60 with which its new rows' largest finite magnitude is at most 448, or the scale
+ * it has from earlier rows where that is larger (earlier codes then move to the new scale);
+ * codes are rounded to nearest even, +-inf becomes +-448, NaN stays NaN.  Rows behind the last
+ * token are left as they were.
+ *   tail_src  nullable [batch]: the page that holds the rows before the first new token, where
+ *             that is not the table's own (a beam that starts to write beside others after a
+ *             reorder); its earlier rows are copied into the table's page.  < 0: the table's own.
+ * No page may be written for two sequences, or be written for one and be the tail_src of another,
+ * in one call.  lilicorr_kv8_append needs kv_len >= the new tokens (else bit 26). */
+lilicorr_status lilicorr_kv8_append(const lilicorr_kv8_cache* cache, const void* k,
+                                    int64_t k_token_stride, int64_t k_head_stride, const void* v,
+                                    int64_t v_token_stride, int64_t v_head_stride, int64_t total,
+                                    const int32_t* q_start, const int32_t* kv_len, int64_t batch,
+                                    const int32_t* block_table, int64_t table_stride, int32_t cols,
+                                    int32_t max_new, const int32_t* tail_src, void* stream);
+
+/* Attention of the new tokens over the cache:
+ *   out[r, j] = sum_t softmax_t(scale * q[r, j] . k[t, j / group]) v[t, j / group],
+ * group = q_heads / kv_heads; new token i of a sequence's n sees tokens t < kv_len - n + i + 1
+ * (all that came before the block, and the block's up to itself).  lse [total, q_heads]
+ * (nullable, f32) is the natural-log sum of the exponentials.  A row that sees no token has
+ * out 0 and lse -inf.  What lies behind a row's last token (other rows of the block, unwritten
+ * page rows) has no influence on it, NaN codes included.
+ *   q    [total, q_heads, head_dim] bf16, element strides by token and head, multiples of 8,
+ *        16-byte aligned
+ *   out  [total, q_heads, head_dim] bf16, contiguous, 16-byte aligned; rows outside the
+ *        sequences are left as they were
+ * Sums, maxima and products are f32; the softmax weights are rounded to f16 before the second
+ * product (relative to the row's largest weight times value scale).  Workspace:
+ * lilicorr_kv8_attention_workspace_bytes (0 for unsupported sizes; by the current device),
+ * 256-byte aligned, no initial contents.  Calls that overlap must not share it.
+ * Errors: LILICORR_ERR_INVALID_ARG, LILICORR_ERR_WORKSPACE, LILICORR_ERR_CUDA. */
+size_t lilicorr_kv8_attention_workspace_bytes(int32_t max_new, int32_t q_heads, int32_t kv_heads,
+                                              int32_t head_dim);
+lilicorr_status lilicorr_kv8_attention(const lilicorr_kv8_cache* cache, const void* q,
+                                       int64_t q_token_stride, int64_t q_head_stride,
+                                       int64_t total, int32_t q_heads, const int32_t* q_start,
+                                       const int32_t* kv_len, int64_t batch,
+                                       const int32_t* block_table, int64_t table_stride,
+                                       int32_t cols, int32_t max_new, float scale, void* out,
+                                       float* lse, void* workspace, size_t workspace_bytes,
+                                       void* stream);
+
 /* Human-readable name of a status; never NULL. */
 const char* lilicorr_status_string(lilicorr_status s);
 /* Message of the most recent CUDA failure in this thread ("" if none). */
@@ -291,7 +414,9 @@ const char* lilicorr_last_error(void);
 uint64_t lilicorr_launch_count(void);
 /* Read and clear the device-side error words of the current device (synchronises the
  * device): 0 = no error; otherwise one bit per wait site that gave up (bits 0-7 the logit
- * pass, bits 8-15 the tensor-core GEMM, bits 16-23 the tensor-core attention). */
+ * pass, bits 8-15 the tensor-core GEMM, bits 16-23 the tensor-core attention, bits 27-31
+ * the cache attention), and of the decoding entry points one bit each for an index or length in
+ * device memory that was out of range (24 a parent, 25 a page, 26 a length or row range). */
 lilicorr_status lilicorr_device_error(uint32_t* code);
 /* Self-check of the device-side timeouts (a diagnostic of this library; the pages have no
  * counterpart).  Runs the logit pass on one row of V bf16 logits (device memory, 16-byte
