@@ -15,18 +15,20 @@ static __device__ uint32_t g_err_beam;
 // ------------------------------------------------------------------------------ selection
 // s(i, v) = score_i + x_iv - log sum_u exp x_iu, the M best of a batch entry's beams by
 // (s desc, i * V + v asc).  Within a beam the order is that of its logits, so a beam's part
-// of the M best are among its own M best logits, which the logit pass leaves in the beam's
-// row record beside (m2, S), sum_u exp x_iu = S 2^m2 in units of base 2.  The merge takes
-// the best head of the beams' sorted lists M times.
+// of the M best are among its own M best logits, which the logit pass leaves, for every
+// segment of a beam's row, in a record beside (m2, S): the segment's sum_u exp x_iu is S 2^m2.
 //
 // Ranks are decided in double: two beams' candidates may differ by less than the float
 // rounding of a score of a few tens (2e-6), and then a float score would rank them by its
-// rounding.  The score is rounded to float once, as it is stored.  The logit pass scales its
-// logits by the float nearest log2 e, so (m2 + log2 S) is divided by that same float.
+// rounding.  The score is rounded to float once, as it is stored.  Double arithmetic is slow
+// on this part, so the log-partition is put together from floats, log2 S = e + log2 f with f
+// near 1, and only the sums m2 + e + log2 f, the division by the float nearest log2 e that the
+// logit pass scales its logits by, and the scores themselves are doubles.
 //
-// One warp per batch entry, lane i = beam i, records staged in shared memory by the whole
-// CTA.  Each of the M steps is two 32-bit warp maxima (the high and the low word of an
-// order-preserving integer key of the double) and a ballot for the lowest beam.
+// One CTA per batch entry; bound by latency.  A few warps for each beam join its segments'
+// sorted lists (the records of four segments are read at a time); then a thread for each
+// candidate finds its rank, the number of better ones, by a binary search in each beam's list,
+// so that no step waits for the one before as in a merge that takes one candidate at a time.
 
 // Order-preserving key: unsigned comparison of keys = comparison of the doubles.
 __device__ __forceinline__ uint64_t double_key(double d) {
@@ -34,87 +36,144 @@ __device__ __forceinline__ uint64_t double_key(double d) {
   return b < 0 ? ~static_cast<uint64_t>(b) : static_cast<uint64_t>(b) | (1ull << 63);
 }
 
-constexpr int BM_THREADS = 128;
-constexpr int BM_MAX = 32;  // beams, and entries taken
+constexpr int BM_MAX = 32;   // beams, and entries taken
+constexpr int BM_WARPS = 8;  // at least as many warps join lists
 
-__global__ void __launch_bounds__(BM_THREADS)
+// (m, s) takes (om, os): s 2^m + os 2^om.
+__device__ __forceinline__ void join_sum(float& m, float& s, float om, float os) {
+  const float M = fmaxf(m, om);
+  s = s * ex2(m - M) + os * ex2(om - M);
+  m = M;
+}
+
+__global__ void __launch_bounds__(32 * BM_MAX)
     beam_merge_kernel(const char* __restrict__ records, const float* __restrict__ scores,
-                      const uint8_t* __restrict__ finished, int beams, int K, int M, int pad_id,
-                      float* __restrict__ out_score, int32_t* __restrict__ out_token,
+                      const uint8_t* __restrict__ finished, int beams, int P, int K, int M,
+                      int pad_id, float* __restrict__ out_score, int32_t* __restrict__ out_token,
                       int32_t* __restrict__ out_parent) {
-  __shared__ float s_v[BM_MAX][BM_MAX + 1];
-  __shared__ int s_id[BM_MAX][BM_MAX + 1];
+  // lists as the warps leave them, [beam * warps of a beam][32]
+  __shared__ float s_v[BM_MAX][32];
+  __shared__ int s_id[BM_MAX][32];
   __shared__ float s_m[BM_MAX], s_s[BM_MAX];
+  // candidates, [beam][K]
+  __shared__ uint64_t s_key[BM_MAX][BM_MAX];
+  __shared__ int s_left[BM_MAX];
+  __shared__ float o_score[BM_MAX];
+  __shared__ int o_token[BM_MAX], o_parent[BM_MAX];
   const int64_t b = blockIdx.x;
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (blockDim.x >> 5) / beams;  // warps of a beam
+  const int w = warp / per, part = warp - w * per;
+  constexpr double NONE = -INFINITY;
+  // scores and marks were there before the logit pass began
+  const double score = w < beams ? static_cast<double>(__ldg(scores + b * beams + w)) : NONE;
+  const bool live = score > NONE;  // a NaN is dead too
+  const bool done = live && finished && finished[b * beams + w];
   pdl_wait();
   pdl_trigger();
-  // record of a row: {f32 m2, f32 S, f32 v[K], i32 id[K]}
-  const int words = 2 * K + 2;
-  const int32_t* rec = reinterpret_cast<const int32_t*>(records) + b * beams * words;
-  for (int i = tid; i < beams * words; i += BM_THREADS) {
-    const int w = i / words, j = i % words;
-    const int32_t x = __ldcg(rec + i);
-    if (j == 0) s_m[w] = __int_as_float(x);
-    else if (j == 1) s_s[w] = __int_as_float(x);
-    else if (j < 2 + K) s_v[w][j - 2] = __int_as_float(x);
-    else s_id[w][j - 2 - K] = x;
+  if (tid < M) {
+    o_score[tid] = -INFINITY;
+    o_token[tid] = pad_id;
+    o_parent[tid] = 0;
+  }
+  if (w < beams && live && !done) {
+    const int words = 2 * K + 2;
+    const int32_t* rec = reinterpret_cast<const int32_t*>(records) + (b * beams + w) * P * words;
+    float v = -INFINITY, m = -1e30f, s = 0.f;
+    int id = INT_MAX;
+    for (int k0 = part; k0 < P; k0 += 4 * per) {
+      float bv[4];
+      int bi[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int k = k0 + i * per;
+        const bool has = lane < K && k < P;
+        bv[i] = has ? __int_as_float(__ldcg(rec + k * words + 2 + lane)) : -INFINITY;
+        bi[i] = has ? __ldcg(rec + k * words + 2 + K + lane) : INT_MAX;
+      }
+      if (k0 + lane * per < P && lane < 4) {
+        const float2 ms = __ldcg(reinterpret_cast<const float2*>(rec + (k0 + lane * per) * words));
+        join_sum(m, s, ms.x, ms.y);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (k0 + i * per < P) bitonic_merge(v, id, bv[i], bi[i], lane);
+    }
+#pragma unroll
+    for (int o = 2; o >= 1; o >>= 1)
+      join_sum(m, s, __shfl_xor_sync(FULL_MASK, m, o), __shfl_xor_sync(FULL_MASK, s, o));
+    s_v[warp][lane] = v;
+    s_id[warp][lane] = id;
+    if (lane == 0) {
+      s_m[warp] = m;
+      s_s[warp] = s;
+    }
   }
   __syncthreads();
-  if (tid >= 32) return;
-
-  const int lane = tid;
-  constexpr double NONE = -INFINITY;
-  double score = NONE, norm = 0.0;  // this beam's own score; its log-partition
-  int left = 0, at = 0;              // candidates of the list; the list's head
-  bool done = false;
-  if (lane < beams) {
-    score = static_cast<double>(scores[b * beams + lane]);
-    done = finished && finished[b * beams + lane];
-    if (score > NONE) {
-      if (done) {
+  const int i = warp;  // from here a warp for each beam
+  int left = 0;
+  uint64_t key = 0;
+  float value = 0.f;
+  int token = 0;
+  if (i < beams) {
+    const double own = static_cast<double>(__ldg(scores + b * beams + i));
+    if (own > NONE) {
+      if (finished && finished[b * beams + i]) {
         left = 1;
-      } else if (s_s[lane] > 0.f) {  // a row with no finite logit has no candidate
-        left = K;
-        norm = (static_cast<double>(s_m[lane]) + log2(static_cast<double>(s_s[lane]))) /
-               static_cast<double>(1.4426950408889634f);
+        token = pad_id;
+        key = double_key(own);
+        value = static_cast<float>(own);
+      } else {
+        float v = s_v[i * per][lane], m = s_m[i * per], s = s_s[i * per];
+        int id = s_id[i * per][lane];
+        for (int k = 1; k < per; ++k) {
+          bitonic_merge(v, id, s_v[i * per + k][lane], s_id[i * per + k][lane], lane);
+          join_sum(m, s, s_m[i * per + k], s_s[i * per + k]);
+        }
+        if (s > 0.f) {  // a row with no finite logit has no candidate
+          int e;
+          float f = frexpf(s, &e);
+          if (f < 0.70710678f) { f *= 2.f; --e; }
+          const double norm = (static_cast<double>(m) + static_cast<double>(e) + static_cast<double>(log2f(f))) *
+                              (1.0 / static_cast<double>(1.4426950408889634f));
+          const double c = own + (static_cast<double>(v) - norm);
+          const bool there = lane < K && c > NONE;
+          left = __popc(__ballot_sync(FULL_MASK, there));  // the list is sorted
+          key = double_key(c);
+          value = static_cast<float>(c);
+          token = id;
+        }
       }
     }
+    s_key[i][lane] = lane < left ? key : 0;
+    if (lane == 0) s_left[i] = left;
   }
-  auto head = [&]() -> double {
-    if (at >= left) return NONE;
-    if (done) return score;
-    const double s = score + (static_cast<double>(s_v[lane][at]) - norm);
-    return s == s ? s : NONE;
-  };
-  double mine = head();
-  float r_score = -INFINITY;
-  int r_token = pad_id, r_parent = 0;
-  for (int j = 0; j < M; ++j) {
-    const uint64_t key = double_key(mine);
-    const uint32_t hi = static_cast<uint32_t>(key >> 32), lo = static_cast<uint32_t>(key);
-    const uint32_t mhi = __reduce_max_sync(FULL_MASK, hi);
-    const uint32_t mlo = __reduce_max_sync(FULL_MASK, hi == mhi ? lo : 0u);
-    const unsigned who = __ballot_sync(FULL_MASK, hi == mhi && lo == mlo);
-    const int win = __ffs(who) - 1;
-    const double best = __shfl_sync(FULL_MASK, mine, win);
-    if (!(best > NONE)) break;  // no candidate is left: the rest are fillers
-    const int pos = __shfl_sync(FULL_MASK, at, win);
-    const bool wdone = __shfl_sync(FULL_MASK, done ? 1 : 0, win) != 0;
-    if (lane == j) {
-      r_score = static_cast<float>(best);
-      r_token = wdone ? pad_id : s_id[win][pos];
-      r_parent = win;
+  __syncthreads();
+  if (i < beams && lane < left) {
+    int rank = lane;
+    for (int j = 0; j < beams && rank < M; ++j) {
+      if (j == i) continue;
+      // entries of beam j's list before this candidate: better, or equal in a lower beam
+      int lo = 0, hi = s_left[j];
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        const uint64_t x = s_key[j][mid];
+        if (x > key || (x == key && j < i)) lo = mid + 1;
+        else hi = mid;
+      }
+      rank += lo;
     }
-    if (lane == win) {
-      ++at;
-      mine = head();
+    if (rank < M) {
+      o_score[rank] = value;
+      o_token[rank] = token;
+      o_parent[rank] = i;
     }
   }
-  if (lane < M) {
-    out_score[b * M + lane] = r_score;
-    out_token[b * M + lane] = r_token;
-    out_parent[b * M + lane] = r_parent;
+  __syncthreads();
+  if (tid < M) {
+    out_score[b * M + tid] = o_score[tid];
+    out_token[b * M + tid] = o_token[tid];
+    out_parent[b * M + tid] = o_parent[tid];
   }
 }
 
@@ -214,7 +273,8 @@ namespace {
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
 struct SelectPlan {
-  size_t records, pass, total;  // offsets of the row records and of the logit pass's part
+  int K, P;      // entries of a record, segments of a row
+  size_t total;  // bytes of the records
 };
 
 bool select_sizes_ok(int64_t batch, int32_t beams, int64_t V, int32_t M, lilicorr_dtype dt) {
@@ -222,17 +282,16 @@ bool select_sizes_ok(int64_t batch, int32_t beams, int64_t V, int32_t M, lilicor
   if (batch < 1 || beams < 1 || beams > BM_MAX || M < 1 || M > BM_MAX) return false;
   const int es = dt == LILICORR_BF16 ? 2 : 4;
   if (V < 1 || V > (int64_t(1) << 31) - 2 || V * es > (int64_t(1) << 31) - 64) return false;
-  // one CTA per row, or up to 90 when there are few rows
   return batch <= ((int64_t(1) << 31) - 2) / beams;
 }
 
 SelectPlan select_plan(int64_t batch, int32_t beams, int64_t V, int32_t M, int es) {
   const int64_t rows = batch * beams;
-  const int K = static_cast<int>(std::min<int64_t>(M, V));
   SelectPlan pl{};
-  pl.records = 0;
-  pl.pass = align256(size_t(rows) * k1_shard_record_bytes(K));
-  pl.total = pl.pass + align256(k1_workspace_bytes(1, static_cast<int>(rows + 1), V, es));
+  pl.K = static_cast<int>(std::min<int64_t>(M, V));
+  const int64_t want = rows >= K1_SPLIT_BELOW_ROWS ? 1 : K1_SPLIT_BELOW_ROWS / rows;
+  pl.P = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(want, V * es / 4096)));
+  pl.total = align256(size_t(rows) * pl.P * k1_shard_record_bytes(pl.K));
   return pl;
 }
 
@@ -296,22 +355,15 @@ lilicorr_status lilicorr_beam_select(const void* logits, lilicorr_dtype ldtype, 
   if (!workspace || workspace_bytes < pl.total || reinterpret_cast<uintptr_t>(workspace) % 256)
     return fail(LILICORR_ERR_WORKSPACE, "lilicorr_beam_select: workspace missing, too small or misaligned");
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
-  char* ws = static_cast<char*>(workspace);
   const int64_t rows = batch * beams;
-  const int K = static_cast<int>(std::min<int64_t>(M, V));
-  // The logit pass leaves row 0 of a block of B rows unread: one block of rows + 1 whose
-  // row 0 would lie before the logits.
-  const void* before = reinterpret_cast<const void*>(reinterpret_cast<uintptr_t>(logits) -
-                                                     uintptr_t(row_stride) * es);
-  cudaError_t e = k1_launch(before, es, 1, static_cast<int>(rows + 1), V, K, nullptr, nullptr,
-                            nullptr, ws + pl.pass, stream, row_stride, 0, ws + pl.records,
-                            WAIT_LIMIT_CYCLES, false, scores, finished);
+  cudaError_t e = k1_launch_beams(logits, es, rows, V, row_stride, pl.K, pl.P, workspace, scores,
+                                  finished, stream);
   if (e == cudaSuccess) {
     PdlScope pdl(true);
-    e = launch_k(beam_merge_kernel, dim3(static_cast<unsigned>(batch)), dim3(BM_THREADS), 0,
-                 stream, static_cast<const char*>(ws + pl.records), scores, finished,
-                 static_cast<int>(beams), K, static_cast<int>(M), static_cast<int>(pad_id),
-                 out_score, out_token, out_parent);
+    e = launch_k(beam_merge_kernel, dim3(static_cast<unsigned>(batch)), dim3(32 * beams * std::max(1, BM_WARPS / beams)), 0,
+                 stream, static_cast<const char*>(workspace), scores, finished, static_cast<int>(beams),
+                 pl.P, pl.K, static_cast<int>(M), static_cast<int>(pad_id), out_score, out_token,
+                 out_parent);
     if (e == cudaSuccess) note_launch();
   }
   if (e != cudaSuccess) return fail(LILICORR_ERR_CUDA, cudaGetErrorString(e));

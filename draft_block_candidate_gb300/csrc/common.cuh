@@ -21,6 +21,9 @@ enum ErrSite : uint32_t {
   ERR_BEAM_PARENT = 1u << 24,   // a parent index out of range
   ERR_KV8_PAGE = 1u << 25,      // a page index out of range
   ERR_KV8_LENGTH = 1u << 26,    // a length or row range out of range
+  ERR_KV8_FULL_WAIT = 1u << 27,
+  ERR_KV8_EMPTY_WAIT = 1u << 28,
+  ERR_KV8_DRAIN = 1u << 29,
 };
 
 // About one second at GB300 clocks: any wait longer than this is treated as a failure.
@@ -45,6 +48,13 @@ __device__ __forceinline__ void mbar_arrive_expect_tx(uint64_t* bar, uint32_t by
       "mbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1;\n\t}" ::"r"(smem_addr(bar)),
       "r"(bytes)
       : "memory");
+}
+
+// Announces bytes to the current phase without arriving on it.
+__device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(bar)),
+               "r"(bytes)
+               : "memory");
 }
 
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
@@ -117,6 +127,39 @@ __device__ __forceinline__ int float_key(float f) {
 }
 __device__ __forceinline__ float key_float(int k) {
   return __int_as_float(k >= 0 ? k : (k ^ 0x7fffffff));
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// (va, ia) ranks before (vb, ib): larger value, then smaller id.
+__device__ __forceinline__ bool better(float va, int ia, float vb, int ib) {
+  return va > vb || (va == vb && ia < ib);
+}
+
+// Merge sorted list (bv, bi) (one entry per lane, descending) into (v, id): afterwards
+// (v, id) holds the best 32 of the union, sorted.
+__device__ __forceinline__ void bitonic_merge(float& v, int& id, float bv, int bi, int lane) {
+  const float rv = __shfl_sync(FULL_MASK, bv, 31 - lane);
+  const int ri = __shfl_sync(FULL_MASK, bi, 31 - lane);
+  if (better(rv, ri, v, id)) {
+    v = rv;
+    id = ri;
+  }
+#pragma unroll
+  for (int st = 16; st >= 1; st >>= 1) {
+    const float ov = __shfl_xor_sync(FULL_MASK, v, st);
+    const int oi = __shfl_xor_sync(FULL_MASK, id, st);
+    const bool ob = better(ov, oi, v, id);
+    const bool lower = (lane & st) == 0;
+    if (lower ? ob : !ob) {
+      v = ov;
+      id = oi;
+    }
+  }
 }
 
 // Split an f32 value into bf16 hi + bf16 lo with hi + lo == v to ~16 significant bits.

@@ -15,8 +15,10 @@ cudaError_t k1_launch(const void* logits, int esize, int64_t batch, int B, int64
                       int32_t* cand_id, float* cand_logit, float* lse, void* ws,
                       cudaStream_t stream, int64_t row_stride = 0, int id_offset = 0,
                       void* records = nullptr, long long wait_limit = WAIT_LIMIT_CYCLES,
-                      bool withhold_first = false, const float* row_score = nullptr,
-                      const uint8_t* row_done = nullptr);
+                      bool withhold_first = false);
+cudaError_t k1_launch_beams(const void* logits, int esize, int64_t rows, int64_t V,
+                            int64_t row_stride, int K, int P, void* records,
+                            const float* row_score, const uint8_t* row_done, cudaStream_t stream);
 size_t k1_shard_record_bytes(int K);
 cudaError_t k1_merge_launch(const void* records, int n, int64_t rows, int K, int32_t* cand_id,
                             float* cand_logit, float* lse, cudaStream_t stream);

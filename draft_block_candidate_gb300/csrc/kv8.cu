@@ -231,7 +231,7 @@ struct AttnParams {
   int q_heads, group;
   const int32_t *q_start, *kv_len, *table;
   int64_t batch, table_stride;
-  int cols, max_new;
+  int cols, max_new, page_log2;
   float scale2;  // softmax scale * log2 e
   __nv_bfloat16* out;  // [total, q_heads, D]
   float* lse;          // [total, q_heads] or null
@@ -245,7 +245,7 @@ struct SeqUnits {
 template <int RT>
 __device__ __forceinline__ SeqUnits seq_units(const AttnParams& p, int64_t b) {
   const SeqRange r = seq_range(p.q_start, p.kv_len, b, p.total, p.max_new,
-                               int64_t(p.cols) * p.c.page);
+                               int64_t(p.cols) << p.page_log2);
   SeqUnits u;
   u.n = r.n;
   u.len = r.len;
@@ -256,44 +256,84 @@ __device__ __forceinline__ SeqUnits seq_units(const AttnParams& p, int64_t b) {
   return u;
 }
 
-// Sum of all sequences' units, by the whole CTA.
-template <int RT, int THREADS>
-__device__ __forceinline__ int64_t all_units(const AttnParams& p, int64_t* s_sum) {
-  int64_t t = 0;
-  for (int64_t b = threadIdx.x; b < p.batch; b += THREADS) t += seq_units<RT>(p, b).units;
+// The units of all sequences, and where the run of CTA `run` begins: every warp works it out
+// for itself.  The counts of the first 128 sequences stay in registers between the two passes.
+struct Run {
+  int64_t units, per;  // all units; units of a run
+  int64_t u, u_end;    // this run's units
+  int64_t b, first;    // the sequence of unit u, and that sequence's first unit
+};
+template <int RT>
+__device__ __forceinline__ Run find_run(const AttnParams& p, int64_t run, int64_t runs) {
+  constexpr int KEEP = 4;
+  const int lane = threadIdx.x & 31;
+  auto count = [&](int64_t b) { return b < p.batch ? seq_units<RT>(p, b).units : int64_t(0); };
+  int64_t kept[KEEP], t = 0;
+#pragma unroll
+  for (int i = 0; i < KEEP; ++i) {
+    kept[i] = i * 32 < p.batch ? count(i * 32 + lane) : 0;
+    t += kept[i];
+  }
+  for (int64_t b = KEEP * 32 + lane; b < p.batch; b += 32) t += count(b);
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) t += __shfl_xor_sync(FULL_MASK, t, o);
-  if ((threadIdx.x & 31) == 0) s_sum[threadIdx.x >> 5] = t;
-  __syncthreads();
-  t = 0;
-  for (int i = 0; i < THREADS / 32; ++i) t += s_sum[i];
-  return t;
-}
-
-// The sequence that holds unit u, and the first unit of it, by one warp (all lanes).
-template <int RT>
-__device__ __forceinline__ void find_seq(const AttnParams& p, int64_t u, int64_t& b, int64_t& first) {
-  const int lane = threadIdx.x & 31;
+  Run r;
+  r.units = t;
+  r.per = (t + runs - 1) / runs;
+  r.u = run * r.per;
+  r.u_end = min(t, r.u + r.per);
+  r.b = p.batch;
+  r.first = 0;
+  if (r.u >= r.u_end) return r;
   int64_t base = 0;
-  for (int64_t b0 = 0; b0 < p.batch; b0 += 32) {
-    const int64_t mine = b0 + lane < p.batch ? seq_units<RT>(p, b0 + lane).units : 0;
+  auto look = [&](int64_t b0, int64_t mine) {  // whether unit u is among these 32 sequences'
     int64_t sum = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int64_t x = __shfl_up_sync(FULL_MASK, sum, o);
       if (lane >= o) sum += x;
     }
-    const unsigned past = __ballot_sync(FULL_MASK, base + sum > u);
+    const unsigned past = __ballot_sync(FULL_MASK, base + sum > r.u);
     if (past) {
       const int l = __ffs(past) - 1;
-      b = b0 + l;
-      first = base + __shfl_sync(FULL_MASK, sum - mine, l);
-      return;
+      r.b = b0 + l;
+      r.first = base + __shfl_sync(FULL_MASK, sum - mine, l);
+      return true;
     }
     base += __shfl_sync(FULL_MASK, sum, 31);
+    return false;
+  };
+#pragma unroll
+  for (int i = 0; i < KEEP; ++i)
+    if (i * 32 < p.batch && look(i * 32, kept[i])) return r;
+  for (int64_t b0 = KEEP * 32; b0 < p.batch; b0 += 32)
+    if (look(b0, count(b0 + lane))) return r;
+  return r;
+}
+
+// The pieces of a run: the chunks [c0, c1) of one tile each.
+struct Piece {
+  SeqUnits sq;
+  int64_t b, first;  // the sequence, and its first unit
+  int h, tile, c0, c1;
+  int end;           // tokens that the tile's last row sees
+  bool whole;        // all of the tile's chunks
+};
+template <int RT>
+__device__ __forceinline__ void piece_at(const AttnParams& p, int64_t u, int64_t u_end, Piece& x) {
+  while (u >= x.first + x.sq.units) {
+    x.first += x.sq.units;
+    x.sq = seq_units<RT>(p, ++x.b);
   }
-  b = p.batch;
-  first = base;
+  const uint32_t in = static_cast<uint32_t>(u - x.first);  // a sequence's units fit 32 bits (host)
+  const uint32_t item = in / x.sq.chunks;
+  x.c0 = static_cast<int>(in - item * x.sq.chunks);
+  x.c1 = static_cast<int>(min(int64_t(x.sq.chunks), x.c0 + (u_end - u)));
+  x.h = item / x.sq.tiles;
+  x.tile = item - x.h * x.sq.tiles;
+  const int last = min((x.tile + 1) * RT, x.sq.n * p.group) - 1;
+  x.end = min(x.sq.len, x.sq.len - x.sq.n + last / p.group + 1);
+  x.whole = x.c0 == 0 && x.c1 == x.sq.chunks;
 }
 
 __device__ __forceinline__ float ex2f(float x) {
@@ -323,25 +363,6 @@ __device__ __forceinline__ void mma_f16(float (&d)[2 * NR], const uint32_t (&a)[
   }
 }
 
-// N consecutive bytes (4, 8, 16 or 32 at a stride of 64) of a lane as words.
-template <int WORDS>
-__device__ __forceinline__ void load_words(uint32_t (&w)[WORDS], const uint8_t* p) {
-  if constexpr (WORDS == 8) {
-    const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
-    const uint4 b = __ldg(reinterpret_cast<const uint4*>(p + 64));
-    w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
-    w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
-  } else if constexpr (WORDS == 4) {
-    const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
-    w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
-  } else if constexpr (WORDS == 2) {
-    const uint2 a = __ldg(reinterpret_cast<const uint2*>(p));
-    w[0] = a.x; w[1] = a.y;
-  } else {
-    w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
-  }
-}
-
 __device__ __forceinline__ bool any_nan4(uint32_t w) {
   return __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0;
 }
@@ -349,46 +370,144 @@ __device__ __forceinline__ uint32_t no_nan4(uint32_t w) {
   return w & ~__vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu);
 }
 
-// Rows of one tile held by one warp, in the matrix instruction's accumulator layout: lane
-// (g, t) = (lane / 4, lane % 4) holds rows g and g + 8.  D = head dimension, RT = rows (8
-// or 16: with 8 the upper half of every product is zero and takes no registers).
+// Writes a row's outputs: D / 32 columns a lane (x), their sum of weights and maximum.
+template <int N>
+__device__ __forceinline__ void store_row(const AttnParams& p, int64_t at, int D, int d,
+                                          const float (&x)[N], float sum, float m) {
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;  // no token seen: 0
+  __nv_bfloat16* o = p.out + at * D + d;
+  if constexpr (N == 4) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(x[0] * inv, x[1] * inv);
+    const __nv_bfloat162 c = __floats2bfloat162_rn(x[2] * inv, x[3] * inv);
+    *reinterpret_cast<uint2*>(o) = make_uint2(*reinterpret_cast<const uint32_t*>(&a),
+                                              *reinterpret_cast<const uint32_t*>(&c));
+  } else if constexpr (N == 2) {
+    *reinterpret_cast<__nv_bfloat162*>(o) = __floats2bfloat162_rn(x[0] * inv, x[1] * inv);
+  } else {
+    *o = __float2bfloat16_rn(x[0] * inv);
+  }
+  if (p.lse && d == 0) p.lse[at] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * LN2_F;
+}
+
 template <int D, int RT>
-__global__ void __launch_bounds__(32 * AT_WARPS) kv8_attention_kernel(const AttnParams p) {
+struct AttnShape {
+  static constexpr int STAGES = RT == 8 ? 5 : 4;
+  static constexpr int CTAS = 2;                        // per SM
+  static constexpr int TILE = AT_CHUNK * D;             // bytes of a chunk's keys, or values
+  static constexpr int RING = STAGES * 2 * TILE;
+  static constexpr int SMEM = RING + AT_WARPS * RT * (D + 4) * 4;
+};
+
+struct ChunkScale {  // of 16 tokens
+  float k, log2_v, inv_v;
+  int ok;  // the page exists
+};
+
+// Four warps work on the chunks that a fifth brings into a ring of shared-memory stages by bulk
+// copies.  Rows of a tile in the matrix instruction's accumulator layout: lane (g, t) =
+// (lane / 4, lane % 4) holds rows g and g + 8.  D = head dimension, RT = rows (8 or 16: with 8
+// the upper half of every product is zero and takes no registers).
+template <int D, int RT>
+__global__ void __launch_bounds__(32 * AT_WARPS + 32, AttnShape<D, RT>::CTAS)
+    kv8_attention_kernel(const AttnParams p) {
+  using Shape = AttnShape<D, RT>;
   constexpr int KW = D / 16;  // words of a key row a lane reads = steps of 16 of q . k
   constexpr int VW = D / 32;  // words of a value row a lane reads
   constexpr int NU = D / 8;   // output column groups
   constexpr int NR = RT / 8;  // rows a lane holds
-  __shared__ int64_t s_sum[AT_WARPS];
+  constexpr int ST = Shape::STAGES;
+  extern __shared__ __align__(128) uint8_t at_smem[];
+  __shared__ __align__(8) uint64_t full[ST], empty[ST];
+  __shared__ ChunkScale s_scale[ST][AT_WARPS];
   __shared__ float s_m[AT_WARPS][RT], s_l[AT_WARPS][RT];
-  __shared__ __align__(16) float s_o[RT][D + 4];
+  __shared__ int s_abort;
+  float(*s_o)[RT][D + 4] = reinterpret_cast<float(*)[RT][D + 4]>(at_smem + Shape::RING);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int g = lane >> 2, t = lane & 3;
+  if (tid == 0) {
+    for (int i = 0; i < ST; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], AT_WARPS);
+    }
+    fence_mbar_init();
+    s_abort = 0;
+  }
   pdl_wait();
   pdl_trigger();
-  const int64_t units = all_units<RT, 32 * AT_WARPS>(p, s_sum);
-  const int64_t per = (units + gridDim.x - 1) / gridDim.x;
-  int64_t u = blockIdx.x * per;
-  const int64_t u_end = min(units, u + per);
-  if (u >= u_end) return;
-  int64_t b, first;
-  find_seq<RT>(p, u, b, first);
-  SeqUnits sq = seq_units<RT>(p, b);
-  const int page = p.c.page;
+  const Run run = find_run<RT>(p, blockIdx.x, gridDim.x);
+  __syncthreads();
+  if (run.u >= run.u_end) return;
+  Piece x;
+  x.b = run.b;
+  x.first = run.first;
+  x.sq = seq_units<RT>(p, run.b);
+  volatile int* abort_flag = &s_abort;
+  // A wait that gives up marks the CTA; from then on nothing waits or computes, but every
+  // barrier between the warps is still met, so the kernel ends.
+  auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t site) -> bool {
+    if (*abort_flag) return false;
+    if (mbar_wait_bounded(bar, parity, &g_err_kv8, site)) return true;
+    *abort_flag = 1;
+    return false;
+  };
 
-  bool first_piece = true;
-  while (u < u_end) {
-    while (u >= first + sq.units) {
-      first += sq.units;
-      sq = seq_units<RT>(p, ++b);
+  if (warp == AT_WARPS) {
+    // ================= copies: lane i brings the i-th page part of a chunk =================
+    const int part = min(p.c.page, AT_CHUNK);  // tokens
+    const int parts = AT_CHUNK / part;
+    const int bytes = part * D;
+    int it = 0;
+    for (int64_t u = run.u; u < run.u_end; u += x.c1 - x.c0) {
+      piece_at<RT>(p, u, run.u_end, x);
+      const int32_t* tab = p.table + x.b * p.table_stride;
+      auto page_of = [&](int c) {
+        const int tok = c * AT_CHUNK + lane * part;
+        return lane < parts && tok < x.end ? __ldg(tab + (tok >> p.page_log2)) : -2;
+      };
+      int next = page_of(x.c0);
+      for (int c = x.c0; c < x.c1; ++c, ++it) {
+        if (c * AT_CHUNK >= x.end) {  // nothing of this chunk is seen: the tile's rows end here
+          break;
+        }
+        const int st = it % ST;
+        const int id = next;
+        if (c + 1 < x.c1) next = page_of(c + 1);
+        if (it >= ST && !wait(&empty[st], ((it / ST) - 1) & 1, ERR_KV8_EMPTY_WAIT)) break;
+        const bool ok = id >= 0 && id < p.c.n_pages;
+        if (id != -2 && !ok) atomicOr(&g_err_kv8, ERR_KV8_PAGE);
+        const unsigned have = __ballot_sync(FULL_MASK, ok);
+        if (lane == 0) mbar_expect_tx(&full[st], 2u * bytes * __popc(have));
+        __syncwarp();
+        if (ok) {
+          const int tok = c * AT_CHUNK + lane * part;
+          const int64_t ph = int64_t(id) * p.c.heads + x.h;
+          const int64_t off = (ph * p.c.page + (tok & (p.c.page - 1))) * D;
+          uint8_t* dst = at_smem + st * 2 * Shape::TILE + lane * bytes;
+          bulk_g2s(dst, p.c.k + off, bytes, &full[st]);
+          bulk_g2s(dst + Shape::TILE, p.c.v + off, bytes, &full[st]);
+          const float ks = __ldg(p.c.ks + ph), vs = __ldg(p.c.vs + ph);
+          const ChunkScale sc{ks, log2f(vs), 1.f / vs, 1};
+          for (int w = 0; w < part / 16; ++w) s_scale[st][lane * (part / 16) + w] = sc;
+        } else if (lane < parts) {
+          for (int w = 0; w < part / 16; ++w) s_scale[st][lane * (part / 16) + w].ok = 0;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[st]);
+      }
     }
-    // the piece: chunks [c0, c1) of a tile
-    const int64_t item = (u - first) / sq.chunks;
-    const int c0 = static_cast<int>((u - first) % sq.chunks);
-    const int c1 = static_cast<int>(min(int64_t(sq.chunks), c0 + (u_end - u)));
-    const int h = static_cast<int>(item / sq.tiles), tile = static_cast<int>(item % sq.tiles);
-    const int row0 = tile * RT, rows = sq.n * p.group;
-    const int last_row = min(row0 + RT, rows) - 1;
-    const int end = min(sq.len, sq.len - sq.n + last_row / p.group + 1);  // tokens this tile sees
+    // after a wait gave up: what was issued and not waited for by the others has to land
+    if (*abort_flag)
+      for (int i = max(0, it - ST); i < it; ++i)
+        mbar_wait_bounded(&full[i % ST], (i / ST) & 1, &g_err_kv8, ERR_KV8_DRAIN);
+    return;
+  }
+
+  const int g = lane >> 2, t = lane & 3;
+  bool first_piece = true;
+  int it = 0;
+  for (int64_t u = run.u; u < run.u_end; u += x.c1 - x.c0, first_piece = false) {
+    piece_at<RT>(p, u, run.u_end, x);
+    const SeqUnits& sq = x.sq;
+    const int row0 = x.tile * RT, rows = sq.n * p.group, end = x.end;
 
     // q of this lane's rows, as f16 of the row's largest power of two
     uint32_t qf[KW][4];
@@ -400,9 +519,9 @@ __global__ void __launch_bounds__(32 * AT_WARPS) kv8_attention_kernel(const Attn
     for (int r = 0; r < NR; ++r) {
       const int row = row0 + g + 8 * r;
       const bool has = row < rows;
-      const int i = has ? row / p.group : 0, j = has ? row % p.group : 0;
-      seen[r] = has ? sq.len - sq.n + i + 1 : 0;
-      const __nv_bfloat16* qr = p.q + (sq.q0 + i) * p.q_tok + (h * p.group + j) * p.q_head;
+      const int i = has ? row / p.group : 0, j = has ? row - i * p.group : 0;
+      seen[r] = has ? min(sq.len - sq.n + i + 1, end) : 0;
+      const __nv_bfloat16* qr = p.q + (sq.q0 + i) * p.q_tok + (x.h * p.group + j) * p.q_head;
       uint2 raw[KW];
       uint32_t top = 0;
 #pragma unroll
@@ -438,231 +557,249 @@ __global__ void __launch_bounds__(32 * AT_WARPS) kv8_attention_kernel(const Attn
 #pragma unroll
       for (int e = 0; e < 2 * NR; ++e) o[n][e] = 0.f;
 
-    const int32_t* tab = p.table + b * p.table_stride;
-    for (int c = c0; c < c1; ++c) {
+    for (int c = x.c0; c < x.c1; ++c, ++it) {
+      if (c * AT_CHUNK >= end) break;
+      const int st = it % ST;
+      const bool landed = wait(&full[st], (it / ST) & 1, ERR_KV8_FULL_WAIT);
       const int tok0 = c * AT_CHUNK + warp * 16;
-      if (tok0 >= end) break;
-      const int id = __ldg(tab + tok0 / page);
-      if (id < 0 || id >= p.c.n_pages) {  // its tokens count as masked
-        if (lane == 0) atomicOr(&g_err_kv8, ERR_KV8_PAGE);
-        continue;
-      }
-      const int64_t ph = int64_t(id) * p.c.heads + h;
-      const int64_t off = (ph * page + tok0 % page) * D;
-      const float ks = __ldg(p.c.ks + ph), vs = __ldg(p.c.vs + ph);
-      uint32_t kw[2][KW], vw[4][VW];
+      const ChunkScale sc = s_scale[st][warp];
+      if (landed && tok0 < end && sc.ok) {
+        const uint8_t* kt = at_smem + st * 2 * Shape::TILE + warp * 16 * D;
+        const uint8_t* vt = kt + Shape::TILE;
+        float s[2][2 * NR];
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
-        load_words<KW>(kw[j], p.c.k + off + (8 * j + g) * D + t * (D >= 64 ? 16 : 8));
+        for (int j = 0; j < 2; ++j) {
+          uint32_t kw[KW];
+          const uint8_t* kr = kt + (8 * j + g) * D;
+          if constexpr (D == 128) {
+            // 128-byte rows share banks: odd rows take the other half first
+            const int sw = (g & 1) * 64;
+            const uint4 a = *reinterpret_cast<const uint4*>(kr + t * 16 + sw);
+            const uint4 b = *reinterpret_cast<const uint4*>(kr + t * 16 + 64 - sw);
+            const uint4 lo = sw ? b : a, hi = sw ? a : b;
+            kw[0] = lo.x; kw[1] = lo.y; kw[2] = lo.z; kw[3] = lo.w;
+            kw[4] = hi.x; kw[5] = hi.y; kw[6] = hi.z; kw[7] = hi.w;
+          } else if constexpr (D == 64) {
+            const uint4 a = *reinterpret_cast<const uint4*>(kr + t * 16);
+            kw[0] = a.x; kw[1] = a.y; kw[2] = a.z; kw[3] = a.w;
+          } else {
+            const uint2 a = *reinterpret_cast<const uint2*>(kr + t * 8);
+            kw[0] = a.x; kw[1] = a.y;
+          }
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        load_words<VW>(vw[j], p.c.v + off + (2 * t + (j & 1) + 8 * (j >> 1)) * D + g * (D / 8));
-
-      float s[2][2 * NR];
+          for (int e = 0; e < 2 * NR; ++e) s[j][e] = 0.f;
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-#pragma unroll
-        for (int e = 0; e < 2 * NR; ++e) s[j][e] = 0.f;
-#pragma unroll
-        for (int k = 0; k < KW; ++k)
-          mma_f16<NR>(s[j], qf[k], e4m3x2_to_f16x2(static_cast<uint16_t>(kw[j][k])),
-                  e4m3x2_to_f16x2(static_cast<uint16_t>(kw[j][k] >> 16)));
-      }
-      const float lv = log2f(vs), iv = 1.f / vs;
-      uint32_t pf[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-      for (int r = 0; r < NR; ++r) {
-        const float f = f_row[r] * ks;
-        float x[4];
+          for (int k = 0; k < KW; ++k)
+            mma_f16<NR>(s[j], qf[k], e4m3x2_to_f16x2(static_cast<uint16_t>(kw[k])),
+                        e4m3x2_to_f16x2(static_cast<uint16_t>(kw[k] >> 16)));
+        }
+        uint32_t vw[4][VW];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const int tk = tok0 + 2 * t + (j & 1) + 8 * (j >> 1);
-          x[j] = tk < seen[r] && tk < end ? fmaf(s[j >> 1][2 * r + (j & 1)], f, lv) : -INFINITY;
-        }
-        float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
-        mx = fmaxf(mx, __shfl_xor_sync(FULL_MASK, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(FULL_MASK, mx, 2));
-        const float nm = fmaxf(m[r], mx);
-        const float base = nm == -INFINITY ? 0.f : nm;
-        if (nm != m[r]) {  // uniform over the four lanes of the row
-          const float back = ex2f(m[r] - base);
-          l[r] *= back;
-#pragma unroll
-          for (int n = 0; n < NU; ++n) { o[n][2 * r] *= back; o[n][2 * r + 1] *= back; }
-          m[r] = nm;
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) x[j] = ex2f(x[j] - base);
-        l[r] = fmaf((x[0] + x[1]) + (x[2] + x[3]), iv, l[r]);
-        const __half2 a = __floats2half2_rn(x[0], x[1]), d = __floats2half2_rn(x[2], x[3]);
-        pf[r] = *reinterpret_cast<const uint32_t*>(&a);
-        pf[2 + r] = *reinterpret_cast<const uint32_t*>(&d);
-      }
-      // Tokens that some row of the tile does not see (the causal edge, and what lies behind
-      // the last token): 0 * NaN is NaN, so their values take part without NaN, and rows that
-      // do see a NaN get it afterwards.
-      bool fix = false;
-      if (tok0 + 16 > sq.len - sq.n) {
-        bool nan = false;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const bool in = tok0 + 2 * t + (j & 1) + 8 * (j >> 1) < end;
-#pragma unroll
-          for (int k = 0; k < VW; ++k) {
-            if (!in) vw[j][k] = 0u;
-            nan |= any_nan4(vw[j][k]);
-            vw[j][k] = no_nan4(vw[j][k]);
+          const uint8_t* vr = vt + (2 * t + (j & 1) + 8 * (j >> 1)) * D + g * (D / 8);
+          if constexpr (D == 128) {
+            const uint4 a = *reinterpret_cast<const uint4*>(vr);
+            vw[j][0] = a.x; vw[j][1] = a.y; vw[j][2] = a.z; vw[j][3] = a.w;
+          } else if constexpr (D == 64) {
+            const uint2 a = *reinterpret_cast<const uint2*>(vr);
+            vw[j][0] = a.x; vw[j][1] = a.y;
+          } else {
+            vw[j][0] = *reinterpret_cast<const uint32_t*>(vr);
           }
         }
-        fix = __any_sync(FULL_MASK, nan);
-      }
+        uint32_t pf[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-      for (int k = 0; k < VW; ++k) {
-        const uint32_t a0 = __byte_perm(vw[0][k], vw[1][k], 0x5140), a1 = __byte_perm(vw[0][k], vw[1][k], 0x7362);
-        const uint32_t b0 = __byte_perm(vw[2][k], vw[3][k], 0x5140), b1 = __byte_perm(vw[2][k], vw[3][k], 0x7362);
-        mma_f16<NR>(o[4 * k], pf, e4m3x2_to_f16x2(static_cast<uint16_t>(a0)), e4m3x2_to_f16x2(static_cast<uint16_t>(b0)));
-        mma_f16<NR>(o[4 * k + 1], pf, e4m3x2_to_f16x2(static_cast<uint16_t>(a0 >> 16)), e4m3x2_to_f16x2(static_cast<uint16_t>(b0 >> 16)));
-        mma_f16<NR>(o[4 * k + 2], pf, e4m3x2_to_f16x2(static_cast<uint16_t>(a1)), e4m3x2_to_f16x2(static_cast<uint16_t>(b1)));
-        mma_f16<NR>(o[4 * k + 3], pf, e4m3x2_to_f16x2(static_cast<uint16_t>(a1 >> 16)), e4m3x2_to_f16x2(static_cast<uint16_t>(b1 >> 16)));
-      }
-      if (fix) {
-        for (int tk = 0; tk < 16 && tok0 + tk < end; ++tk)
+        for (int r = 0; r < NR; ++r) {
+          const float f = f_row[r] * sc.k;
+          float y[4];
 #pragma unroll
-          for (int n = 0; n < 2; ++n)
+          for (int j = 0; j < 4; ++j) {
+            const int tk = tok0 + 2 * t + (j & 1) + 8 * (j >> 1);
+            y[j] = tk < seen[r] ? fmaf(s[j >> 1][2 * r + (j & 1)], f, sc.log2_v) : -INFINITY;
+          }
+          float mx = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
+          mx = fmaxf(mx, __shfl_xor_sync(FULL_MASK, mx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(FULL_MASK, mx, 2));
+          const float nm = fmaxf(m[r], mx);
+          const float base = nm == -INFINITY ? 0.f : nm;
+          if (nm != m[r]) {  // uniform over the four lanes of the row
+            const float back = ex2f(m[r] - base);
+            l[r] *= back;
 #pragma unroll
-            for (int d = 0; d < NU; ++d) {
-              const uint8_t code = p.c.v[off + tk * D + (2 * t + n) * NU + d];
-              if ((code & 0x7f) == 0x7f)
+            for (int n = 0; n < NU; ++n) { o[n][2 * r] *= back; o[n][2 * r + 1] *= back; }
+            m[r] = nm;
+          }
 #pragma unroll
-                for (int r = 0; r < NR; ++r)
-                  if (tok0 + tk < seen[r]) o[d][2 * r + n] = NAN;
+          for (int j = 0; j < 4; ++j) y[j] = ex2f(y[j] - base);
+          l[r] = fmaf((y[0] + y[1]) + (y[2] + y[3]), sc.inv_v, l[r]);
+          const __half2 a = __floats2half2_rn(y[0], y[1]), d = __floats2half2_rn(y[2], y[3]);
+          pf[r] = *reinterpret_cast<const uint32_t*>(&a);
+          pf[2 + r] = *reinterpret_cast<const uint32_t*>(&d);
+        }
+        // Tokens that some row of the tile does not see (the causal edge, and what lies behind
+        // the last token): 0 * NaN is NaN, so their values take part without NaN, and rows that
+        // do see a NaN get it afterwards.
+        bool fix = false;
+        if (tok0 + 16 > sq.len - sq.n) {
+          bool nan = false;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const bool in = tok0 + 2 * t + (j & 1) + 8 * (j >> 1) < end;
+#pragma unroll
+            for (int k = 0; k < VW; ++k) {
+              if (!in) vw[j][k] = 0u;
+              nan |= any_nan4(vw[j][k]);
+              vw[j][k] = no_nan4(vw[j][k]);
             }
+          }
+          fix = __any_sync(FULL_MASK, nan);
+        }
+#pragma unroll
+        for (int k = 0; k < VW; ++k) {
+          const uint32_t a0 = __byte_perm(vw[0][k], vw[1][k], 0x5140), a1 = __byte_perm(vw[0][k], vw[1][k], 0x7362);
+          const uint32_t b0 = __byte_perm(vw[2][k], vw[3][k], 0x5140), b1 = __byte_perm(vw[2][k], vw[3][k], 0x7362);
+          mma_f16<NR>(o[4 * k], pf, e4m3x2_to_f16x2(static_cast<uint16_t>(a0)), e4m3x2_to_f16x2(static_cast<uint16_t>(b0)));
+          mma_f16<NR>(o[4 * k + 1], pf, e4m3x2_to_f16x2(static_cast<uint16_t>(a0 >> 16)), e4m3x2_to_f16x2(static_cast<uint16_t>(b0 >> 16)));
+          mma_f16<NR>(o[4 * k + 2], pf, e4m3x2_to_f16x2(static_cast<uint16_t>(a1)), e4m3x2_to_f16x2(static_cast<uint16_t>(b1)));
+          mma_f16<NR>(o[4 * k + 3], pf, e4m3x2_to_f16x2(static_cast<uint16_t>(a1 >> 16)), e4m3x2_to_f16x2(static_cast<uint16_t>(b1 >> 16)));
+        }
+        if (fix) {
+          for (int tk = 0; tk < 16 && tok0 + tk < end; ++tk)
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+              for (int d = 0; d < NU; ++d)
+                if ((vt[tk * D + (2 * t + n) * NU + d] & 0x7f) == 0x7f)
+#pragma unroll
+                  for (int r = 0; r < NR; ++r)
+                    if (tok0 + tk < seen[r]) o[d][2 * r + n] = NAN;
+        }
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[st]);
     }
 
-    // ---- join the warps: maxima, then sums and products through shared memory in warp order
+    // ---- join the warps: each scales its products to the row's largest maximum; added in order
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
       l[r] += __shfl_xor_sync(FULL_MASK, l[r], 1);
       l[r] += __shfl_xor_sync(FULL_MASK, l[r], 2);
       if (t == 0) { s_m[warp][g + 8 * r] = m[r]; s_l[warp][g + 8 * r] = l[r]; }
     }
-    __syncthreads();
-    float M[NR], L[NR];
 #pragma unroll
-    for (int r = 0; r < NR; ++r) {
-      float mx = -INFINITY, sum = 0.f;
+    for (int r = 0; r < NR; ++r)
 #pragma unroll
-      for (int w = 0; w < AT_WARPS; ++w) mx = fmaxf(mx, s_m[w][g + 8 * r]);
+      for (int e = 0; e < 2; ++e) {
+        float* dst = &s_o[warp][g + 8 * r][(2 * t + e) * NU];
+#pragma unroll
+        for (int n = 0; n < NU; n += 4)
+          *reinterpret_cast<float4*>(dst + n) = make_float4(o[n][2 * r + e], o[n + 1][2 * r + e],
+                                                            o[n + 2][2 * r + e], o[n + 3][2 * r + e]);
+      }
+    named_bar_sync(1, 32 * AT_WARPS);
+    constexpr int N = D / 32;  // columns a lane takes of a row
+    for (int r = warp; r < RT; r += AT_WARPS) {
+      float mx = -INFINITY, sum = 0.f, y[N];
+#pragma unroll
+      for (int w = 0; w < AT_WARPS; ++w) mx = fmaxf(mx, s_m[w][r]);
       const float base = mx == -INFINITY ? 0.f : mx;
 #pragma unroll
-      for (int w = 0; w < AT_WARPS; ++w) sum += s_l[w][g + 8 * r] * ex2f(s_m[w][g + 8 * r] - base);
-      M[r] = mx;
-      L[r] = sum;
-      const float back = ex2f(m[r] - base);
+      for (int n = 0; n < N; ++n) y[n] = 0.f;
 #pragma unroll
-      for (int n = 0; n < NU; ++n) { o[n][2 * r] *= back; o[n][2 * r + 1] *= back; }
-    }
-    for (int w = 0; w < AT_WARPS; ++w) {
-      if (warp == w) {
+      for (int w = 0; w < AT_WARPS; ++w) {
+        const float back = ex2f(s_m[w][r] - base);
+        sum = fmaf(s_l[w][r], back, sum);
 #pragma unroll
-        for (int r = 0; r < NR; ++r)
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-#pragma unroll
-            for (int n = 0; n < NU; ++n) {
-              float& x = s_o[g + 8 * r][(2 * t + e) * NU + n];
-              x = w == 0 ? o[n][2 * r + e] : x + o[n][2 * r + e];
-            }
+        for (int n = 0; n < N; ++n) y[n] = fmaf(s_o[w][r][lane * N + n], back, y[n]);
       }
-      __syncthreads();
-    }
-    if (warp == 0 && t == 0) {
-#pragma unroll
-      for (int r = 0; r < NR; ++r) { s_m[0][g + 8 * r] = M[r]; s_l[0][g + 8 * r] = L[r]; }
-    }
-    __syncthreads();
-    const bool whole = c0 == 0 && c1 == sq.chunks;
-    if (whole) {
-      for (int i = tid; i < RT * (D / 4); i += 32 * AT_WARPS) {
-        const int r = i / (D / 4), d = (i % (D / 4)) * 4;
+      if (x.whole) {
         const int row = row0 + r;
         if (row < rows) {
-          const float sum = s_l[0][r];
-          const float inv = sum == 0.f ? 0.f : 1.f / sum;
-          const float4 x = *reinterpret_cast<const float4*>(&s_o[r][d]);
-          const int64_t at = ((sq.q0 + row / p.group) * p.q_heads + h * p.group + row % p.group);
-          const __nv_bfloat162 a = __floats2bfloat162_rn(x.x * inv, x.y * inv);
-          const __nv_bfloat162 c = __floats2bfloat162_rn(x.z * inv, x.w * inv);
-          *reinterpret_cast<uint2*>(p.out + at * D + d) =
-              make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&c));
-          if (p.lse && d == 0)
-            p.lse[at] = sum == 0.f ? -INFINITY : (s_m[0][r] + log2f(sum)) * LN2_F;
+          const int i = row / p.group;
+          store_row<N>(p, (sq.q0 + i) * p.q_heads + x.h * p.group + (row - i * p.group), D,
+                       lane * N, y, sum, mx);
+        }
+      } else {
+        float* part = p.part + (int64_t(blockIdx.x) * 2 + (first_piece ? 0 : 1)) * RT * (D + 2);
+#pragma unroll
+        for (int n = 0; n < N; ++n) part[r * D + lane * N + n] = y[n];
+        if (lane == 0) {
+          part[RT * D + r] = mx;
+          part[RT * D + RT + r] = sum;
         }
       }
-    } else {
-      float* part = p.part + (int64_t(blockIdx.x) * 2 + (first_piece ? 0 : 1)) * RT * (D + 2);
-      for (int i = tid; i < RT * D; i += 32 * AT_WARPS) part[i] = s_o[i / D][i % D];
-      for (int i = tid; i < RT; i += 32 * AT_WARPS) {
-        part[RT * D + i] = s_m[0][i];
-        part[RT * D + RT + i] = s_l[0][i];
-      }
     }
-    __syncthreads();
-    u += c1 - c0;
-    first_piece = false;
+    named_bar_sync(1, 32 * AT_WARPS);
   }
 }
 
 // Joins the parts of the tiles that several CTAs hold.  One CTA per boundary between two runs
 // of units; the CTA of the first boundary inside a tile joins that tile, from the run that
-// holds its first chunk to the one that holds its last, in that order.
+// holds its first chunk to the one that holds its last, in that order: a warp for each row,
+// the weights of 32 parts at a time worked out side by side, then the parts added up.
 template <int D, int RT>
-__global__ void __launch_bounds__(128) kv8_join_kernel(const AttnParams p, int grid) {
-  __shared__ int64_t s_sum[4];
-  pdl_wait();
-  pdl_trigger();
-  const int64_t units = all_units<RT, 128>(p, s_sum);
-  const int64_t per = (units + grid - 1) / grid;
-  const int64_t edge = (int64_t(blockIdx.x) + 1) * per;  // first unit of run blockIdx.x + 1
-  if (edge >= units) return;
-  int64_t b, first;
-  find_seq<RT>(p, edge, b, first);
-  const SeqUnits sq = seq_units<RT>(p, b);
-  const int64_t item = (edge - first) / sq.chunks;
-  const int64_t i0 = first + item * sq.chunks, i1 = i0 + sq.chunks;  // the tile's units
-  if (edge == i0) return;               // the boundary lies between two tiles
-  if (edge - per > i0) return;          // an earlier boundary lies inside this tile too
-  const int64_t r0 = i0 / per, r1 = (i1 - 1) / per;  // runs that hold parts
+__global__ void __launch_bounds__(32 * RT) kv8_join_kernel(const AttnParams p, int grid) {
+  constexpr int N = D / 32;
+  const int lane = threadIdx.x & 31, r = threadIdx.x >> 5;
+  // Lengths and row ranges were there before the attention began: they are read, and the
+  // tile is found, while it still runs.
+  const Run run = find_run<RT>(p, int64_t(blockIdx.x) + 1, grid);
+  const int64_t edge = run.u;  // first unit of run blockIdx.x + 1
+  if (edge >= run.u_end) return;
+  const SeqUnits sq = seq_units<RT>(p, run.b);
+  const int64_t item = (edge - run.first) / sq.chunks;
+  const int64_t i0 = run.first + item * sq.chunks, i1 = i0 + sq.chunks;  // the tile's units
+  if (edge == i0) return;                  // the boundary lies between two tiles
+  if (edge - run.per > i0) return;         // an earlier boundary lies inside this tile too
+  const int64_t r0 = i0 / run.per, r1 = (i1 - 1) / run.per;  // runs that hold parts
   const int h = static_cast<int>(item / sq.tiles), tile = static_cast<int>(item % sq.tiles);
-  const int rows = sq.n * p.group;
+  const int row = tile * RT + r;
+  if (row >= sq.n * p.group) return;
   constexpr int64_t STEP = RT * (D + 2);
-  auto part_of = [&](int64_t r) { return p.part + (r * 2 + (r * per >= i0 ? 0 : 1)) * STEP; };
-  for (int i = threadIdx.x; i < RT * (D / 4); i += 128) {
-    const int r = i / (D / 4), d = (i % (D / 4)) * 4;
-    const int row = tile * RT + r;
-    if (row >= rows) continue;
-    float mx = -INFINITY;
-    for (int64_t k = r0; k <= r1; ++k) mx = fmaxf(mx, __ldcg(part_of(k) + RT * D + r));
-    const float base = mx == -INFINITY ? 0.f : mx;
-    float sum = 0.f;
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int64_t k = r0; k <= r1; ++k) {
-      const float* q = part_of(k);
-      const float w = ex2f(__ldcg(q + RT * D + r) - base);
-      sum = fmaf(__ldcg(q + RT * D + RT + r), w, sum);
-      const float4 y = __ldcg(reinterpret_cast<const float4*>(q + r * D + d));
-      x.x = fmaf(y.x, w, x.x); x.y = fmaf(y.y, w, x.y);
-      x.z = fmaf(y.z, w, x.z); x.w = fmaf(y.w, w, x.w);
+  // the run that holds the tile's first chunk may hold another tile's part before it
+  const float* parts = p.part + r0 * 2 * STEP;
+  const int64_t lead = r0 * run.per >= i0 ? 0 : STEP;
+  pdl_wait();
+  float mx = -INFINITY, sum = 0.f, y[N];
+#pragma unroll
+  for (int n = 0; n < N; ++n) y[n] = 0.f;
+  const int count = static_cast<int>(r1 - r0) + 1;
+  for (int k0 = 0; k0 < count; k0 += 32) {
+    const int mine = k0 + lane;
+    const float* q = parts + mine * 2 * STEP + (mine == 0 ? lead : 0);
+    const float m = mine < count ? __ldcg(q + RT * D + r) : -INFINITY;
+    const float s = mine < count ? __ldcg(q + RT * D + RT + r) : 0.f;
+    float nm = fmaxf(m, mx);
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) nm = fmaxf(nm, __shfl_xor_sync(FULL_MASK, nm, o));
+    const float base = nm == -INFINITY ? 0.f : nm;
+    const float w = ex2f(m - base), back = ex2f(mx - base);
+    float add = s * w;
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) add += __shfl_xor_sync(FULL_MASK, add, o);
+    sum = fmaf(sum, back, add);
+#pragma unroll
+    for (int n = 0; n < N; ++n) y[n] *= back;
+    mx = nm;
+    const int here = min(32, count - k0);
+#pragma unroll 8
+    for (int k = 0; k < here; ++k) {
+      const float wk = __shfl_sync(FULL_MASK, w, k);
+      const float* src = parts + (k0 + k) * 2 * STEP + (k0 + k == 0 ? lead : 0) + r * D + lane * N;
+      if constexpr (N == 4) {
+        const float4 z = __ldcg(reinterpret_cast<const float4*>(src));
+        y[0] = fmaf(z.x, wk, y[0]); y[1] = fmaf(z.y, wk, y[1]);
+        y[2] = fmaf(z.z, wk, y[2]); y[3] = fmaf(z.w, wk, y[3]);
+      } else if constexpr (N == 2) {
+        const float2 z = __ldcg(reinterpret_cast<const float2*>(src));
+        y[0] = fmaf(z.x, wk, y[0]); y[1] = fmaf(z.y, wk, y[1]);
+      } else {
+        y[0] = fmaf(__ldcg(src), wk, y[0]);
+      }
     }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    const int64_t at = ((sq.q0 + row / p.group) * p.q_heads + h * p.group + row % p.group);
-    const __nv_bfloat162 a = __floats2bfloat162_rn(x.x * inv, x.y * inv);
-    const __nv_bfloat162 c = __floats2bfloat162_rn(x.z * inv, x.w * inv);
-    *reinterpret_cast<uint2*>(p.out + at * D + d) =
-        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&c));
-    if (p.lse && d == 0) p.lse[at] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * LN2_F;
   }
+  const int i = row / p.group;
+  store_row<N>(p, (sq.q0 + i) * p.q_heads + h * p.group + (row - i * p.group), D, lane * N, y, sum, mx);
 }
 
 cudaError_t kv8_read_device_error(uint32_t* code) {
@@ -727,18 +864,21 @@ struct AttnPlan {
 AttnPlan attn_plan(int32_t max_new, int group, int D) {
   AttnPlan pl{};
   pl.rt = int64_t(max_new) * group <= 8 ? 8 : 16;
-  pl.grid = 3 * device_sm_count();
+  pl.grid = (pl.rt == 8 ? AttnShape<128, 8>::CTAS : AttnShape<128, 16>::CTAS) * device_sm_count();
   pl.ws = size_t(pl.grid) * 2 * pl.rt * (D + 2) * sizeof(float);
   return pl;
 }
 
 template <int D, int RT>
 cudaError_t attention_launch(const AttnParams& prm, int grid, cudaStream_t stream) {
-  kv8_attention_kernel<D, RT><<<grid, 32 * AT_WARPS, 0, stream>>>(prm);
-  cudaError_t e = cudaGetLastError();
+  constexpr int smem = AttnShape<D, RT>::SMEM;
+  cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void*>(kv8_attention_kernel<D, RT>), smem);
+  if (e != cudaSuccess) return e;
+  kv8_attention_kernel<D, RT><<<grid, 32 * AT_WARPS + 32, smem, stream>>>(prm);
+  e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   PdlScope pdl(true);
-  e = launch_k(kv8_join_kernel<D, RT>, dim3(grid), dim3(128), 0, stream, prm, grid);
+  e = launch_k(kv8_join_kernel<D, RT>, dim3(grid), dim3(32 * RT), 0, stream, prm, grid);
   if (e == cudaSuccess) note_launch(2);
   return e;
 }
@@ -813,7 +953,10 @@ lilicorr_status lilicorr_kv8_attention(const lilicorr_kv8_cache* cache, const vo
   if (!why && (!out || reinterpret_cast<uintptr_t>(out) % 16)) why = "out is null or not 16-byte aligned";
   if (!why && (q_heads < 1 || q_heads % cache->kv_heads || q_heads / cache->kv_heads > 1024))
     why = "q_heads is a multiple of kv_heads, at most 1024 times it";
-  if (!why && int64_t(max_new) * (q_heads / cache->kv_heads) > (1 << 28)) why = "max_new * group is too large";
+  // one sequence's work units (tiles x heads x chunks of 64 tokens) are counted in 32 bits
+  if (!why && (int64_t(max_new) * (q_heads / cache->kv_heads) / 8 + 1) * cache->kv_heads *
+                  ((int64_t(cols) * cache->page + 63) / 64) > UINT_MAX)
+    why = "max_new * q_heads * the table's tokens are too large";
   if (!why && !std::isfinite(scale)) why = "scale is not finite";
   if (why) return fail(LILICORR_ERR_INVALID_ARG, why);
   const int D = cache->head_dim, group = q_heads / cache->kv_heads;
@@ -832,6 +975,7 @@ lilicorr_status lilicorr_kv8_attention(const lilicorr_kv8_cache* cache, const vo
   prm.table_stride = table_stride;
   prm.cols = cols;
   prm.max_new = max_new;
+  prm.page_log2 = cache->page == 16 ? 4 : cache->page == 32 ? 5 : cache->page == 64 ? 6 : 7;
   prm.scale2 = scale * LOG2E_F;
   prm.out = static_cast<__nv_bfloat16*>(out);
   prm.lse = lse;

@@ -121,6 +121,7 @@ struct K1Params {
                            // stage of unit blockIdx + prefetch_ahead (co-resident CTAs)
   const float* row_score;   // beam search, nullable: rows whose score is -inf (or NaN) or
   const uint8_t* row_done;  // (nullable) that are marked are not read and get no record
+  int unit_records;         // a record for every segment, not joined into one for its row
 };
 
 // Packed per-row record of a vocabulary shard: {m2, s, v[K], id[K]}, K * 8 + 8 bytes.
@@ -129,17 +130,6 @@ struct K1Params {
 __host__ __device__ constexpr size_t k1_record_bytes(int K) { return 8 + size_t(K) * 8; }
 
 __device__ __forceinline__ int64_t i64min(int64_t a, int64_t b) { return a < b ? a : b; }
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// (va, ia) ranks before (vb, ib): larger value, then smaller id.
-__device__ __forceinline__ bool better(float va, int ia, float vb, int ib) {
-  return va > vb || (va == vb && ia < ib);
-}
 
 struct WarpQueue {
   float qv;   // this lane's entry (lane = position in the sorted queue)
@@ -154,28 +144,6 @@ struct WarpQueue {
     tid = INT_MAX;
   }
 };
-
-// Merge sorted list (bv, bi) (one entry per lane, descending) into (v, id): afterwards
-// (v, id) holds the best 32 of the union, sorted.
-__device__ __forceinline__ void bitonic_merge(float& v, int& id, float bv, int bi, int lane) {
-  const float rv = __shfl_sync(FULL_MASK, bv, 31 - lane);
-  const int ri = __shfl_sync(FULL_MASK, bi, 31 - lane);
-  if (better(rv, ri, v, id)) {
-    v = rv;
-    id = ri;
-  }
-#pragma unroll
-  for (int st = 16; st >= 1; st >>= 1) {
-    const float ov = __shfl_xor_sync(FULL_MASK, v, st);
-    const int oi = __shfl_xor_sync(FULL_MASK, id, st);
-    const bool ob = better(ov, oi, v, id);
-    const bool lower = (lane & st) == 0;
-    if (lower ? ob : !ob) {
-      v = ov;
-      id = oi;
-    }
-  }
-}
 
 __device__ __forceinline__ void lse_merge(float& m2, float& s, float om2, float os) {
   const float M = fmaxf(m2, om2);
@@ -750,7 +718,7 @@ __global__ void __launch_bounds__(K1_THREADS, K1_MIN_BLOCKS) logit_pass_kernel(c
     lse_merge(M, S, om, os);
   }
 
-  if (p.P > 1) {
+  if (p.P > 1 && !p.unit_records) {
     K1Partial* part = p.partials + u;
     part->v[lane] = v;
     part->id[lane] = id;
@@ -778,7 +746,7 @@ __global__ void __launch_bounds__(K1_THREADS, K1_MIN_BLOCKS) logit_pass_kernel(c
   }
 
   if (p.records) {
-    char* rec = p.records + r * k1_record_bytes(K);
+    char* rec = p.records + (p.unit_records ? u : r) * k1_record_bytes(K);
     if (lane == 0) {
       reinterpret_cast<float*>(rec)[0] = M;
       reinterpret_cast<float*>(rec)[1] = S;
@@ -857,13 +825,26 @@ size_t k1_workspace_bytes(int64_t batch, int B, int64_t V, int esize) {
   return k1_plan(batch, B, V, esize).ws_bytes;
 }
 
+static cudaError_t k1_run(const K1Params& prm, int64_t units, int esize, cudaStream_t stream) {
+  constexpr int dyn = K1_NSTAGES * K1_STAGE_BYTES;
+  const bool wide = prm.K > K1_WIDE_ABOVE_K;
+  void (*kern)(const K1Params) =
+      esize == 2 ? (wide ? logit_pass_kernel<__nv_bfloat16, true> : logit_pass_kernel<__nv_bfloat16, false>)
+                 : (wide ? logit_pass_kernel<float, true> : logit_pass_kernel<float, false>);
+  cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void*>(kern), dyn);
+  if (e != cudaSuccess) return e;
+  e = launch_k(kern, dim3(static_cast<unsigned>(units)), dim3(K1_THREADS), dyn, stream, prm);
+  if (e != cudaSuccess) return e;
+  note_launch();
+  return cudaGetLastError();
+}
+
 cudaError_t k1_launch(const void* logits, int esize, int64_t batch, int B, int64_t V, int K,
                       int32_t* cand_id, float* cand_logit, float* lse, void* ws,
                       cudaStream_t stream, int64_t row_stride, int id_offset, void* records,
-                      long long wait_limit, bool withhold_first, const float* row_score,
-                      const uint8_t* row_done) {
+                      long long wait_limit, bool withhold_first) {
   const K1Plan pl = k1_plan(batch, B, V, esize);
-  K1Params prm;
+  K1Params prm{};
   prm.logits = static_cast<const char*>(logits);
   prm.batch = batch;
   prm.B = B;
@@ -881,8 +862,6 @@ cudaError_t k1_launch(const void* logits, int esize, int64_t batch, int B, int64
   prm.records = static_cast<char*>(records);
   prm.wait_limit = wait_limit;
   prm.withhold_first = withhold_first ? 1 : 0;
-  prm.row_score = row_score;
-  prm.row_done = row_done;
   {
     const int64_t resident = int64_t(K1_MIN_BLOCKS) * device_sm_count();
     prm.prefetch_ahead = batch * (B - 1) * pl.P > resident ? resident : 0;
@@ -895,20 +874,36 @@ cudaError_t k1_launch(const void* logits, int esize, int64_t batch, int B, int64
     cudaError_t e = cudaMemsetAsync(prm.counters, 0, size_t(rows) * sizeof(unsigned), stream);
     if (e != cudaSuccess) return e;
   }
-  const dim3 grid(static_cast<unsigned>(rows * pl.P));
-  constexpr int dyn = K1_NSTAGES * K1_STAGE_BYTES;
-  const bool wide = K > K1_WIDE_ABOVE_K;
-  void (*kern)(const K1Params) =
-      esize == 2 ? (wide ? logit_pass_kernel<__nv_bfloat16, true> : logit_pass_kernel<__nv_bfloat16, false>)
-                 : (wide ? logit_pass_kernel<float, true> : logit_pass_kernel<float, false>);
-  {
-    cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void*>(kern), dyn);
-    if (e != cudaSuccess) return e;
-  }
-  const cudaError_t e = launch_k(kern, grid, dim3(K1_THREADS), dyn, stream, prm);
-  if (e != cudaSuccess) return e;
-  note_launch();
-  return cudaGetLastError();
+  return k1_run(prm, rows * pl.P, esize, stream);
+}
+
+// The logit pass of beam search: rows of one step's logits, each row in P segments, and one
+// record for each segment (no join by the last CTA of a row, so no counters to clear).
+cudaError_t k1_launch_beams(const void* logits, int esize, int64_t rows, int64_t V,
+                            int64_t row_stride, int K, int P, void* records,
+                            const float* row_score, const uint8_t* row_done,
+                            cudaStream_t stream) {
+  K1Params prm{};
+  // Row 0 of a block of B rows is not read: one block of rows + 1 whose row 0 would lie
+  // before the logits.
+  prm.logits = reinterpret_cast<const char*>(reinterpret_cast<uintptr_t>(logits) -
+                                             uintptr_t(row_stride) * esize);
+  prm.batch = 1;
+  prm.B = static_cast<int>(rows + 1);
+  prm.V = V;
+  prm.K = K;
+  prm.P = P;
+  const int64_t seg = (V * esize + P - 1) / P;
+  prm.seg_bytes = std::max<int64_t>(16, (seg + 15) / 16 * 16);
+  prm.row_stride = row_stride;
+  prm.records = static_cast<char*>(records);
+  prm.wait_limit = WAIT_LIMIT_CYCLES;
+  prm.row_score = row_score;
+  prm.row_done = row_done;
+  prm.unit_records = 1;
+  const int64_t resident = int64_t(K1_MIN_BLOCKS) * device_sm_count();
+  prm.prefetch_ahead = rows * P > resident ? resident : 0;
+  return k1_run(prm, rows * P, esize, stream);
 }
 
 size_t k1_shard_record_bytes(int K) { return k1_record_bytes(K); }

@@ -6,13 +6,17 @@ kv8_append, kv8_attention).  Tensors may lie on any one device: the call runs th
 `stream` or on that device's current stream, and what it allocates belongs to that stream.
 Functions raise ValueError on tensors that do not fit the call and LilicorrError on a
 non-OK status.
+
+A call on one token's work takes a few microseconds on the device, so what the host does
+per call matters: a tensor that fits is passed by one test (_want), and layouts that take
+some working out are kept by shape and strides (_state_layout).
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes as C
 import functools
 import math
+import struct
 from typing import Optional, Sequence
 
 import torch
@@ -20,20 +24,23 @@ import torch
 from . import _lib as L
 from .api import LilicorrError, _check, _ldtype
 
-_HERE = contextlib.nullcontext()
 
-
-def _run_on(dev: torch.device, stream):
-    """Context in which `dev` and `stream` are current, and the raw stream."""
+def _run_on(dev: int, stream):
+    """The raw stream, and a context that makes the device and the stream current where they
+    are not (else None)."""
     if stream is None:
-        raw = torch.cuda.current_stream(dev).cuda_stream
-        return (_HERE if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)), raw
-    if stream.device != dev:
-        raise ValueError(f"the stream is on {stream.device}, the tensors are on {dev}")
-    return torch.cuda.stream(stream), stream.cuda_stream
+        raw = torch._C._cuda_getCurrentRawStream(dev)
+        return raw, (None if torch._C._cuda_getDevice() == dev else torch.cuda.device(dev))
+    if stream.device.index != dev:
+        raise ValueError(f"the stream is on {stream.device}, the tensors are on cuda:{dev}")
+    return stream.cuda_stream, torch.cuda.stream(stream)
 
 
-def _want(t, name: str, dtype, shape, dev=None, contiguous: bool = True) -> None:
+def _want(t, name: str, dtype, shape, dev: Optional[int], contiguous: bool = True) -> None:
+    """Refuses a tensor of another type, shape (None: any extent), device or layout."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.get_device() == dev and t.is_contiguous()):
+        return
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name} must be a tensor")
     if t.dtype != dtype:
@@ -42,20 +49,16 @@ def _want(t, name: str, dtype, shape, dev=None, contiguous: bool = True) -> None
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be on a GPU")
-    if dev is not None and t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if dev is not None and t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
     if contiguous and not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
 
 
-def _workspace(ws: Optional[torch.Tensor], need: int, dev: torch.device, what: str) -> torch.Tensor:
-    """The caller's workspace, looked over, or a new one."""
+def _new_workspace(need: int, dev, what: str) -> torch.Tensor:
     if need == 0:
         raise LilicorrError(1, what)
-    if ws is None:
-        return torch.empty(need, dtype=torch.uint8, device=dev)
-    _want(ws, "workspace", torch.uint8, (None,), dev)
-    return ws
+    return torch.empty(need, dtype=torch.uint8, device=dev)
 
 
 # ----------------------------------------------------------------------------- beam search
@@ -78,8 +81,9 @@ def _beam_rows(logits: torch.Tensor):
 def beam_select_workspace(logits: torch.Tensor, n_out: int) -> torch.Tensor:
     """A workspace for beam_select of logits of this shape."""
     batch, beams, V, _, ld = _beam_rows(logits)
-    n = int(L.lib().lilicorr_beam_select_workspace_bytes(batch, beams, V, n_out, ld))
-    return _workspace(None, n, logits.device, "lilicorr_beam_select_workspace_bytes")
+    with torch.cuda.device(logits.device):
+        n = int(L.lib().lilicorr_beam_select_workspace_bytes(batch, beams, V, n_out, ld))
+        return _new_workspace(n, logits.device, "lilicorr_beam_select_workspace_bytes")
 
 
 def beam_select(logits: torch.Tensor, scores: torch.Tensor, n_out: int,
@@ -92,36 +96,50 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, n_out: int,
     (score [batch, n_out] f32, token int32, parent int32), best first; `out` may hold the
     three preallocated."""
     batch, beams, V, row, ld = _beam_rows(logits)
-    dev = logits.device
+    dev = logits.get_device()
     _want(scores, "scores", torch.float32, (batch, beams), dev)
     if finished is not None:
         _want(finished, "finished", torch.bool, (batch, beams), dev)
+    if workspace is not None:
+        _want(workspace, "workspace", torch.uint8, (workspace.numel(),), dev)
+    if out is not None:
+        if len(out) != 3:
+            raise ValueError("out must hold score, token and parent")
+        _want(out[0], "score", torch.float32, (batch, n_out), dev)
+        _want(out[1], "token", torch.int32, (batch, n_out), dev)
+        _want(out[2], "parent", torch.int32, (batch, n_out), dev)
+    if not 1 <= n_out <= 32 or beams > 32:
+        raise ValueError("1 <= n_out <= 32 and at most 32 beams")
     if not -(1 << 31) <= pad_id < (1 << 31):
         raise ValueError("pad_id must fit 32 bits")
-    ctx, raw = _run_on(dev, stream)
-    with ctx:
-        if out is None:
-            ids = torch.empty(2, batch, max(n_out, 1), dtype=torch.int32, device=dev)
-            out = (torch.empty(batch, max(n_out, 1), dtype=torch.float32, device=dev), ids[0], ids[1])
-        else:
-            for t, name, dt in zip(out, ("score", "token", "parent"),
-                                   (torch.float32, torch.int32, torch.int32)):
-                _want(t, name, dt, (batch, n_out), dev)
+    raw, ctx = _run_on(dev, stream)
+
+    def call():
         lib = L.lib()
-        if workspace is None:
-            workspace = _workspace(None, int(lib.lilicorr_beam_select_workspace_bytes(
-                batch, beams, V, n_out, ld)), dev, "lilicorr_beam_select")
-        else:
-            _want(workspace, "workspace", torch.uint8, (None,), dev)
+        ws, o = workspace, out
+        if o is None:
+            shape, where = (batch, n_out), logits.device
+            o = (torch.empty(shape, dtype=torch.float32, device=where),
+                 torch.empty(shape, dtype=torch.int32, device=where),
+                 torch.empty(shape, dtype=torch.int32, device=where))
+        if ws is None:
+            ws = _new_workspace(int(lib.lilicorr_beam_select_workspace_bytes(
+                batch, beams, V, n_out, ld)), logits.device, "lilicorr_beam_select")
         st = lib.lilicorr_beam_select(
             logits.data_ptr(), ld, batch, beams, V, row, n_out, scores.data_ptr(),
-            None if finished is None else finished.data_ptr(), pad_id, out[0].data_ptr(),
-            out[1].data_ptr(), out[2].data_ptr(), workspace.data_ptr(), workspace.numel(), raw)
-    _check(st, "lilicorr_beam_select")
-    return out
+            None if finished is None else finished.data_ptr(), pad_id, o[0].data_ptr(),
+            o[1].data_ptr(), o[2].data_ptr(), ws.data_ptr(), ws.numel(), raw)
+        if st:
+            _check(st, "lilicorr_beam_select")
+        return o
+
+    if ctx is None:
+        return call()
+    with ctx:
+        return call()
 
 
-@functools.lru_cache(maxsize=1024)
+@functools.lru_cache(maxsize=4096)
 def _state_layout(shape, sa, sb, esize: int):
     """(strides and sizes in bytes) of a state's rows as segments that are contiguous in both
     layouts, or None.  shape, strides: behind [batch, beams], in elements."""
@@ -139,6 +157,19 @@ def _state_layout(shape, sa, sb, esize: int):
     return da * esize, db * esize, segs, seg * esize
 
 
+_PAIR, _REST = struct.Struct("=QQ"), struct.Struct("=8q")
+
+
+@functools.lru_cache(maxsize=4096)
+def _state_fields(shape, sa, sb, esize: int):
+    """lilicorr_beam_state behind its two pointers, as bytes, for a state of these strides."""
+    lay = _state_layout(shape[2:], sa[2:], sb[2:], esize)
+    if lay is None:
+        raise ValueError("a state's layout behind the beams is not equal contiguous pieces a "
+                         "uniform stride apart")
+    return _REST.pack(sa[0] * esize, sa[1] * esize, lay[0], sb[0] * esize, sb[1] * esize, *lay[1:])
+
+
 def beam_reorder(states: Sequence[torch.Tensor], parent: torch.Tensor,
                  out: Optional[Sequence[torch.Tensor]] = None, stream=None):
     """lilicorr_beam_reorder: state[b, j] becomes state[b, parent[b, j]] for every state.
@@ -148,43 +179,38 @@ def beam_reorder(states: Sequence[torch.Tensor], parent: torch.Tensor,
     of a contiguous cache does).  out: tensors of the same shapes and types to write
     instead; without it the states are gathered in place.  parent [batch, beams] int32.
     Returns the list of written tensors."""
-    states = list(states)
-    if not states:
-        raise ValueError("no states")
-    into = states if out is None else list(out)
-    if len(into) != len(states):
-        raise ValueError("out must hold one tensor for each state")
+    into = list(states if out is None else out)
+    if not into or len(into) != len(states):
+        raise ValueError("there must be states, and out must hold one tensor for each")
     if not isinstance(parent, torch.Tensor) or parent.dim() != 2:
         raise ValueError("parent must be a tensor [batch, beams]")
-    batch, beams = parent.shape
-    dev = parent.device
-    _want(parent, "parent", torch.int32, (batch, beams))
-    arr = (L.BeamState * len(states))()
-    n = 0
+    batch, beams = rows = parent.shape
+    dev = parent.get_device()
+    _want(parent, "parent", torch.int32, rows, dev)
+    if dev < 0:
+        raise ValueError("parent must be on a GPU")
+    packed = []
     for s, o in zip(states, into):
-        if s.dim() < 2 or s.shape[0] != batch or s.shape[1] != beams:
-            raise ValueError(f"a state must have shape [{batch}, {beams}, ...], got {tuple(s.shape)}")
-        if s.device != dev or o.device != dev:
-            raise ValueError(f"states must be on {dev}")
-        if o is not s and (o.shape != s.shape or o.dtype != s.dtype):
+        shape = s.shape
+        if shape[:2] != rows:
+            raise ValueError(f"a state must have shape [{batch}, {beams}, ...], got {tuple(shape)}")
+        if s.get_device() != dev or o.get_device() != dev:
+            raise ValueError(f"states must be on cuda:{dev}")
+        if o is not s and (o.shape != shape or o.dtype != s.dtype):
             raise ValueError("out must have the states' shapes and types")
-        if s.numel() == 0:
-            continue
-        sa, sb = s.stride(), o.stride()
-        es = s.element_size()
-        lay = _state_layout(s.shape[2:], sa[2:], sb[2:], es)
-        if lay is None:
-            raise ValueError("a state's layout behind the beams is not equal contiguous pieces a "
-                             "uniform stride apart")
-        arr[n] = L.BeamState(s.data_ptr(), o.data_ptr(), sa[0] * es, sa[1] * es, lay[0],
-                             sb[0] * es, sb[1] * es, lay[1], lay[2], lay[3])
-        n += 1
-    if n == 0:
-        return into
-    ctx, raw = _run_on(dev, stream)
-    with ctx:
-        st = L.lib().lilicorr_beam_reorder(arr, n, parent.data_ptr(), batch, beams, raw)
-    _check(st, "lilicorr_beam_reorder")
+        if s.numel():
+            packed.append(_PAIR.pack(s.data_ptr(), o.data_ptr()))
+            packed.append(_state_fields(shape, s.stride(), o.stride(), s.element_size()))
+    if packed:
+        raw, ctx = _run_on(dev, stream)
+        args = (b"".join(packed), len(packed) // 2, parent.data_ptr(), batch, beams, raw)
+        if ctx is None:
+            st = L.lib().lilicorr_beam_reorder(*args)
+        else:
+            with ctx:
+                st = L.lib().lilicorr_beam_reorder(*args)
+        if st:
+            _check(st, "lilicorr_beam_reorder")
     return into
 
 
@@ -213,10 +239,13 @@ class KV8Cache:
     def _hold(self, k, v, k_scale, v_scale):
         if not isinstance(k, torch.Tensor) or k.dim() != 4:
             raise ValueError("k must be a tensor [n_pages, kv_heads, page, head_dim]")
-        _want(k, "k", torch.float8_e4m3fn, (None,) * 4)
-        _want(v, "v", torch.float8_e4m3fn, k.shape, k.device)
-        _want(k_scale, "k_scale", torch.float32, k.shape[:2], k.device)
-        _want(v_scale, "v_scale", torch.float32, k.shape[:2], k.device)
+        dev = k.get_device()
+        _want(k, "k", torch.float8_e4m3fn, k.shape, dev)
+        _want(v, "v", torch.float8_e4m3fn, k.shape, dev)
+        _want(k_scale, "k_scale", torch.float32, k.shape[:2], dev)
+        _want(v_scale, "v_scale", torch.float32, k.shape[:2], dev)
+        if not k.is_cuda:
+            raise ValueError("the cache must be on a GPU")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.n_pages, self.kv_heads, self.page, self.head_dim = k.shape
         self.device = k.device
@@ -225,27 +254,32 @@ class KV8Cache:
                              f"{self.page} and {self.head_dim}")
         self._desc = L.Kv8CacheDesc(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(),
                                     v_scale.data_ptr(), *k.shape)
-
-    @property
-    def desc(self):
-        return C.byref(self._desc)
+        self._ref = C.addressof(self._desc)
 
 
-def _rows(t, name: str, heads: Optional[int], D: int, total, dev) -> tuple:
+def _rows(t, name: str, heads: Optional[int], D: int, total: Optional[int], dev: int) -> tuple:
     """Token and head strides of rows [total, heads, D] whose last dimension is contiguous."""
-    _want(t, name, torch.bfloat16, (total, heads, D), dev, contiguous=False)
+    if (not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16 or t.dim() != 3
+            or t.get_device() != dev or t.shape[2] != D or (heads is not None and t.shape[1] != heads)
+            or (total is not None and t.shape[0] != total)):
+        _want(t, name, torch.bfloat16, (total, heads, D), dev, contiguous=False)
     st, sh, sd = t.stride()
     if sd != 1:
         raise ValueError(f"{name}'s last dimension must be contiguous")
     # a dimension of one has no stride of its own
-    return (0 if t.shape[0] <= 1 else st), (0 if t.shape[1] == 1 else sh)
+    n, h, _ = t.shape
+    return (st if n > 1 else 0), (sh if h > 1 else 0)
 
 
-def _sequences(q_start, kv_len, block_table, dev):
-    _want(kv_len, "kv_len", torch.int32, (None,), dev)
+def _sequences(q_start, kv_len, block_table, dev: int) -> tuple:
+    if not isinstance(kv_len, torch.Tensor) or kv_len.dim() != 1:
+        raise ValueError("kv_len must be a tensor [batch]")
     batch = kv_len.shape[0]
+    _want(kv_len, "kv_len", torch.int32, (batch,), dev)
     _want(q_start, "q_start", torch.int32, (batch + 1,), dev)
-    _want(block_table, "block_table", torch.int32, (batch, None), dev, contiguous=False)
+    if (not isinstance(block_table, torch.Tensor) or block_table.dtype is not torch.int32
+            or block_table.dim() != 2 or block_table.get_device() != dev or block_table.shape[0] != batch):
+        _want(block_table, "block_table", torch.int32, (batch, None), dev, contiguous=False)
     rows, step = block_table.stride()
     cols = block_table.shape[1]
     if step != 1 and cols > 1:
@@ -263,30 +297,36 @@ def kv8_append(cache: KV8Cache, k: torch.Tensor, v: torch.Tensor, q_start: torch
     kv_len[b]; block_table [batch, cols] int32 names its pages; max_new bounds the new
     tokens of a sequence; tail_src [batch] int32 the page to copy the rows before the first
     new token from (-1: the table's own)."""
-    dev = cache.device
+    dev = cache.device.index
     kt, kh = _rows(k, "k", cache.kv_heads, cache.head_dim, None, dev)
-    vt, vh = _rows(v, "v", cache.kv_heads, cache.head_dim, k.shape[0], dev)
+    total = k.shape[0]
+    vt, vh = _rows(v, "v", cache.kv_heads, cache.head_dim, total, dev)
     batch, rows, cols = _sequences(q_start, kv_len, block_table, dev)
     if tail_src is not None:
         _want(tail_src, "tail_src", torch.int32, (batch,), dev)
-    if batch == 0 or k.shape[0] == 0:
+    if batch == 0 or total == 0:
         return
-    ctx, raw = _run_on(dev, stream)
-    with ctx:
-        st = L.lib().lilicorr_kv8_append(
-            cache.desc, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, k.shape[0], q_start.data_ptr(),
+    raw, ctx = _run_on(dev, stream)
+    args = (cache._ref, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, total, q_start.data_ptr(),
             kv_len.data_ptr(), batch, block_table.data_ptr(), rows, cols, max_new,
             None if tail_src is None else tail_src.data_ptr(), raw)
-    _check(st, "lilicorr_kv8_append")
+    if ctx is None:
+        st = L.lib().lilicorr_kv8_append(*args)
+    else:
+        with ctx:
+            st = L.lib().lilicorr_kv8_append(*args)
+    if st:
+        _check(st, "lilicorr_kv8_append")
 
 
 def kv8_attention_workspace(q: torch.Tensor, cache: KV8Cache, block_table: torch.Tensor,
                             max_new: int) -> torch.Tensor:
-    """A workspace for kv8_attention of these heads and at most max_new tokens a sequence."""
+    """A workspace for kv8_attention of q's heads, these sequences and at most max_new new
+    tokens of each."""
     with torch.cuda.device(cache.device):
-        n = int(L.lib().lilicorr_kv8_attention_workspace_bytes(max_new, q.shape[1], cache.kv_heads,
-                                                               cache.head_dim))
-        return _workspace(None, n, cache.device, "lilicorr_kv8_attention_workspace_bytes")
+        n = int(L.lib().lilicorr_kv8_attention_workspace_bytes(
+            max_new, q.shape[1], cache.kv_heads, cache.head_dim))
+        return _new_workspace(n, cache.device, "lilicorr_kv8_attention_workspace_bytes")
 
 
 def kv8_attention(q: torch.Tensor, cache: KV8Cache, q_start: torch.Tensor, kv_len: torch.Tensor,
@@ -301,35 +341,44 @@ def kv8_attention(q: torch.Tensor, cache: KV8Cache, q_start: torch.Tensor, kv_le
     the sequences keep what they hold; a new one holds zeros there).  lse: True, or a tensor
     [total, q_heads] f32 to write the natural-log sums of exponentials to (True: -inf outside
     the sequences).  Returns out, or (out, lse)."""
-    dev = cache.device
+    dev = cache.device.index
     qt, qh = _rows(q, "q", None, cache.head_dim, None, dev)
     total, q_heads, D = q.shape
     batch, rows, cols = _sequences(q_start, kv_len, block_table, dev)
     if scale is None:
         scale = 1.0 / math.sqrt(D)
-    ctx, raw = _run_on(dev, stream)
-    with ctx:
-        if out is None:
-            out = torch.zeros(total, q_heads, D, dtype=torch.bfloat16, device=dev)
-        else:
-            _want(out, "out", torch.bfloat16, (total, q_heads, D), dev)
-        if lse is True:
-            lse = torch.full((total, q_heads), -math.inf, dtype=torch.float32, device=dev)
-        elif lse is False:
-            lse = None
-        elif lse is not None:
-            _want(lse, "lse", torch.float32, (total, q_heads), dev)
+    if out is not None:
+        _want(out, "out", torch.bfloat16, (total, q_heads, D), dev)
+    if workspace is not None:
+        _want(workspace, "workspace", torch.uint8, (workspace.numel(),), dev)
+    new_lse = lse is True
+    if isinstance(lse, bool):
+        lse = None
+    elif lse is not None:
+        _want(lse, "lse", torch.float32, (total, q_heads), dev)
+    raw, ctx = _run_on(dev, stream)
+
+    def call():
+        lib = L.lib()
+        o, norm, ws = out, lse, workspace
+        if o is None:
+            o = torch.zeros(total, q_heads, D, dtype=torch.bfloat16, device=cache.device)
+        if new_lse:
+            norm = torch.full((total, q_heads), -math.inf, dtype=torch.float32, device=cache.device)
         if batch > 0 and total > 0:
-            lib = L.lib()
-            if workspace is None:
-                workspace = _workspace(None, int(lib.lilicorr_kv8_attention_workspace_bytes(
-                    max_new, q_heads, cache.kv_heads, D)), dev, "lilicorr_kv8_attention")
-            else:
-                _want(workspace, "workspace", torch.uint8, (None,), dev)
+            if ws is None:
+                ws = _new_workspace(int(lib.lilicorr_kv8_attention_workspace_bytes(
+                    max_new, q_heads, cache.kv_heads, D)), cache.device, "lilicorr_kv8_attention")
             st = lib.lilicorr_kv8_attention(
-                cache.desc, q.data_ptr(), qt, qh, total, q_heads, q_start.data_ptr(),
+                cache._ref, q.data_ptr(), qt, qh, total, q_heads, q_start.data_ptr(),
                 kv_len.data_ptr(), batch, block_table.data_ptr(), rows, cols, max_new, scale,
-                out.data_ptr(), None if lse is None else lse.data_ptr(), workspace.data_ptr(),
-                workspace.numel(), raw)
-            _check(st, "lilicorr_kv8_attention")
-    return out if lse is None else (out, lse)
+                o.data_ptr(), None if norm is None else norm.data_ptr(), ws.data_ptr(),
+                ws.numel(), raw)
+            if st:
+                _check(st, "lilicorr_kv8_attention")
+        return o if norm is None else (o, norm)
+
+    if ctx is None:
+        return call()
+    with ctx:
+        return call()
