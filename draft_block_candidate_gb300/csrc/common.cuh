@@ -21,9 +21,10 @@ enum ErrSite : uint32_t {
   ERR_BEAM_PARENT = 1u << 24,   // a parent index out of range
   ERR_KV8_PAGE = 1u << 25,      // a page index out of range
   ERR_KV8_LENGTH = 1u << 26,    // a length or row range out of range
-  ERR_KV8_FULL_WAIT = 1u << 27,
+  ERR_KV8_FULL_WAIT = 1u << 27,  // waits of the cache attention
   ERR_KV8_EMPTY_WAIT = 1u << 28,
-  ERR_KV8_DRAIN = 1u << 29,
+  ERR_KV8_S_WAIT = 1u << 29,
+  ERR_KV8_PV_WAIT = 1u << 30,
 };
 
 // About one second at GB300 clocks: any wait longer than this is treated as a failure.
@@ -48,13 +49,6 @@ __device__ __forceinline__ void mbar_arrive_expect_tx(uint64_t* bar, uint32_t by
       "mbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1;\n\t}" ::"r"(smem_addr(bar)),
       "r"(bytes)
       : "memory");
-}
-
-// Announces bytes to the current phase without arriving on it.
-__device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
-  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(bar)),
-               "r"(bytes)
-               : "memory");
 }
 
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
