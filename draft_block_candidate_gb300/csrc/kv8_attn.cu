@@ -246,14 +246,15 @@ __device__ __forceinline__ void tmem_st16(uint32_t t, const float* v) {
       : "memory");
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
-// OR of a flag over the 128 threads of named barrier `id`.
+// OR of a flag over the THREADS threads of named barrier `id`.
+template <int THREADS>
 __device__ __forceinline__ bool bar_or(int id, bool flag) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %2, 0;\n\t"
-      "barrier.cta.red.or.pred p, %1, 128, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      "barrier.cta.red.or.pred p, %1, %3, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(r)
-      : "r"(id), "r"(flag ? 1u : 0u)
+      : "r"(id), "r"(flag ? 1u : 0u), "n"(THREADS)
       : "memory");
   return r != 0;
 }
@@ -301,11 +302,13 @@ struct AttnShape {
   static constexpr int OFF_Q = OFF_P + PB * PT;
   static constexpr int SMEM = 1024 + OFF_Q + QB * 2 * QT;
   static constexpr int TMEM = N == 16 ? 64 : 4 * N;    // two S' and one O' of N columns
+  // Softmax warps: a warp can read the 32 lanes (tokens) of tensor memory of its place among
+  // four; with 64 rows and more, two warps share the columns (rows) of each 32 tokens.
+  static constexpr int GROUPS = N >= 64 ? 2 : 1, SOFT = 4 * GROUPS, COLS = N / GROUPS;
+  static constexpr int LOAD_WARP = SOFT + 4, MMA_WARP = SOFT + 5, THREADS = 32 * (SOFT + 6);
 };
 
-constexpr int AT_SOFT = 4, AT_CONV = 4;  // warps
-constexpr int AT_LOAD_WARP = AT_SOFT + AT_CONV, AT_MMA_WARP = AT_LOAD_WARP + 1;
-constexpr int AT_THREADS = 32 * (AT_MMA_WARP + 1);
+constexpr int AT_CONV = 4;                  // warps
 constexpr int SC_RING = 8, PIECE_RING = 4;  // deeper than any warp runs ahead of the softmax
 constexpr float RAISE = 8.f;                // log2 of how far a score may pass its reference
 
@@ -314,19 +317,34 @@ struct PageScale {  // of the tokens of one page
   int ok;  // the page was loaded
 };
 
+// The rest of a wait that did not end at once, at most WAIT_LIMIT_CYCLES.  The first one of a CTA
+// that gives up makes every later one give up soon.  (Out of line: the roles' loops share the
+// SM's instruction cache, and measured half as fast when their code did not fit it.)
+__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, uint32_t site, volatile int* fail) {
+  const long long t0 = clock64();
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 63) == 0 && (*fail || clock64() - t0 > WAIT_LIMIT_CYCLES)) {
+      atomicOr(&g_err_kv8_attn, site);
+      *fail = 1;
+      return false;
+    }
+  }
+}
+
 template <int D, int N>
-__global__ void __launch_bounds__(AT_THREADS, 1)
+__global__ void __launch_bounds__(AttnShape<D, N>::THREADS, 1)
     kv8_attention_kernel(const __grid_constant__ CUtensorMap tm, const AttnParams p) {
   using S = AttnShape<D, N>;
   constexpr int ST = S::STAGES, PB = S::PB, QB = S::QB;
-  constexpr int W = N < 32 ? 16 : 32;  // columns a softmax thread takes at a time
+  constexpr int COLS = S::COLS, W = COLS < 32 ? 16 : 32;  // columns of a softmax thread, and at a time
   extern __shared__ uint8_t at_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(at_raw) + 1023) & ~uintptr_t(1023));
   __shared__ __align__(8) uint64_t full[ST], empty[ST], sready[2], sfree[2], vready[2], pready[PB],
       pvdone[2], qready[QB], qfree[QB], scready[SC_RING], frready[PIECE_RING];
   __shared__ PageScale s_sc[SC_RING][8];
   __shared__ __align__(16) float s_fr[PIECE_RING][N], s_nref[N];
-  __shared__ float s_raw[N], s_fac[N], s_red[AT_SOFT][N];
+  __shared__ float s_raw[N], s_fac[N], s_red[4][N];
   __shared__ int s_nan[PIECE_RING];
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_fail;
@@ -336,11 +354,11 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
     for (int i = 0; i < ST; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1 + AT_CONV); }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sready[i], 1);
-      mbar_init(&sfree[i], AT_SOFT);
+      mbar_init(&sfree[i], S::SOFT);
       mbar_init(&vready[i], AT_CONV);
       mbar_init(&pvdone[i], 1);
     }
-    for (int i = 0; i < PB; ++i) mbar_init(&pready[i], AT_SOFT);
+    for (int i = 0; i < PB; ++i) mbar_init(&pready[i], S::SOFT);
     for (int i = 0; i < QB; ++i) { mbar_init(&qready[i], AT_CONV); mbar_init(&qfree[i], 1); }
     for (int i = 0; i < SC_RING; ++i) mbar_init(&scready[i], 1);
     for (int i = 0; i < PIECE_RING; ++i) { mbar_init(&frready[i], AT_CONV); s_nan[i] = 0; }
@@ -370,18 +388,8 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
   // Every wait is bounded, and the first that gives up makes every later one of the CTA give up
   // at once, so that all warps still run through their loops and meet at their barriers.
   auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t site) -> bool {
-    if (mbar_try_wait(bar, parity)) return true;
-    const long long t0 = clock64();
-    for (uint32_t i = 1;; ++i) {
-      if (mbar_try_wait(bar, parity)) return true;
-      if ((i & 63) == 0 && (s_fail || clock64() - t0 > WAIT_LIMIT_CYCLES)) {
-        atomicOr(&g_err_kv8_attn, site);
-        s_fail = 1;
-        return false;
-      }
-    }
+    return mbar_try_wait(bar, parity) || wait_slow(bar, parity, site, &s_fail);
   };
-
   // ... by all lanes of a warp, which go on together.
   auto wait_warp = [&](uint64_t* bar, uint32_t parity, uint32_t site) {
     const bool ok = wait(bar, parity, site);
@@ -389,7 +397,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
     return ok;
   };
 
-  if (warp == AT_LOAD_WARP) {
+  if (warp == S::LOAD_WARP) {
     // ================= loads: lane i brings the i-th page (part) of a chunk =================
     const int part = min(p.c.page, AT_CHUNK), parts = AT_CHUNK >> min(p.page_log2, 7);
     const int bytes = part * D;
@@ -435,11 +443,14 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
     if (!ok_run || s_fail)  // what is in flight has to land
       for (int i = max(0, it - ST); i < it; ++i)
         mbar_wait_bounded(&full[i % ST], (i / ST) & 1, &g_err_kv8_attn, ERR_KV8_EMPTY_WAIT);
-  } else if (warp == AT_MMA_WARP) {
+  } else if (warp == S::MMA_WARP) {
     // ================= products =================
     if (lane == 0) {
       constexpr uint32_t ID_S = tc_idesc(128, N, false, false), ID_O = tc_idesc(128, N, true, true);
       constexpr int VB = D < 64 ? 64 : 128, PBY = N < 64 ? 2 * N : 128;  // bytes of a tile's row
+      const uint64_t d_v = tile_desc<VB>(sm + S::OFF_V, D == 128 ? AT_CHUNK * 128 : 0);
+      const uint64_t d_p = tile_desc<PBY>(sm + S::OFF_P, AT_CHUNK * 128);
+      const uint64_t d_k = tile_desc<D>(sm, 16), d_q = tile_desc<D>(sm + S::OFF_Q, 16);
       int it = 0, pi = 0;
       int pend = -1;          // chunk whose O' product is still to come
       bool pend_first = false;
@@ -450,12 +461,11 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
         ok = wait(&vready[b], (pend >> 1) & 1, ERR_KV8_PV_WAIT) && ok;
         if (ok) {
           tc_fence_after();
-          const uint8_t* v = sm + S::OFF_V + b * S::VW;
-          const uint8_t* pp = sm + S::OFF_P + pb * S::PT;
-#pragma unroll
-          for (int k = 0; k < AT_CHUNK / 16; ++k)
-            mma_f16(t_o, tile_desc<VB>(v + k * 16 * VB, D == 128 ? AT_CHUNK * 128 : 0),
-                    tile_desc<PBY>(pp + k * 16 * PBY, AT_CHUNK * 128), ID_O, !(pend_first && k == 0));
+          // (16 tokens further: the address field, in units of 16 bytes, moves on)
+          uint64_t v = d_v + (b * S::VW >> 4), pp = d_p + (pb * S::PT >> 4);
+#pragma unroll 2
+          for (int k = 0; k < AT_CHUNK / 16; ++k, v += VB, pp += PBY)
+            mma_f16(t_o, v, pp, ID_O, !(pend_first && k == 0));
         }
         tc_commit(&pvdone[b]);
         pend = -1;
@@ -463,7 +473,6 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
       for (int64_t u = run.u; u < run.u_end; u += x.c1 - x.c0) {
         piece_at<N>(p, u, run.u_end, x);
         if (x.c0 >= x.cn) continue;
-        const uint8_t* q = sm + S::OFF_Q + (pi % QB) * 2 * S::QT;
         bool ok = wait(&qready[pi % QB], (pi / QB) & 1, ERR_KV8_S_WAIT);
         for (int c = x.c0; c < x.cn; ++c, ++it) {
           const int st = it % ST, b = it & 1;
@@ -471,13 +480,12 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
           if (it >= 2) ok = wait(&sfree[b], ((it >> 1) - 1) & 1, ERR_KV8_S_WAIT) && ok;
           if (ok) {
             tc_fence_after();
-            const uint8_t* k = sm + st * 2 * S::KT;
+            const uint64_t k = d_k + (st * 2 * S::KT >> 4);
+            uint64_t q = d_q + ((pi % QB) * 2 * S::QT >> 4);
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half, q += S::QT >> 4)
 #pragma unroll
-            for (int half = 0; half < 2; ++half)
-#pragma unroll
-              for (int d = 0; d < D / 32; ++d)
-                mma_f8(tmem + b * N, tile_desc<D>(k + d * 32, 16), tile_desc<D>(q + half * S::QT + d * 32, 16),
-                       ID_S, half + d > 0);
+              for (int d = 0; d < D / 32; ++d) mma_f8(tmem + b * N, k + 2 * d, q + 2 * d, ID_S, half + d > 0);
           }
           tc_commit(&sready[b]);
           tc_commit(&empty[st]);
@@ -491,9 +499,9 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
       product_o();
     }
     __syncwarp();
-  } else if (warp >= AT_SOFT) {
+  } else if (warp >= S::SOFT) {
     // ================= widening of V, and the split of q =================
-    const int cw = warp - AT_SOFT, ct = tid - 32 * AT_SOFT;
+    const int cw = warp - S::SOFT, ct = tid - 32 * S::SOFT;
     int it = 0, pi = 0;
     for (int64_t u = run.u; u < run.u_end; u += x.c1 - x.c0) {
       piece_at<N>(p, u, run.u_end, x);
@@ -568,7 +576,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
         constexpr int LPR = UPR < 4 ? UPR : 4;          // lanes on a row
         constexpr int TOKS = 32 / LPR;                  // rows of one round
         bool nan = false;
-#pragma unroll
+#pragma unroll 2
         for (int k = 0; k < UPR; ++k) {
           const int tok = cw * 32 + (k % (32 / TOKS)) * TOKS + lane / LPR;
           const int piece = lane % LPR + (k / (32 / TOKS)) * LPR;
@@ -604,8 +612,11 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
     }
   } else {
     // ================= softmax: thread = token of the chunk; then thread = column of D =======
-    const uint32_t t_lane = static_cast<uint32_t>(warp * 32) << 16;
+    const int quarter = warp & 3, col0 = (warp >> 2) * COLS;  // its tokens, its columns
+    const int in = quarter * 32 + lane;
+    const uint32_t t_lane = static_cast<uint32_t>(quarter * 32) << 16;
     const int part_log2 = min(p.page_log2, 7);
+    auto sync_soft = [&]() { named_bar_sync(1, 32 * S::SOFT); };
     int it = 0, pi = 0;
     bool first_piece = true;
     for (int64_t u = run.u; u < run.u_end; u += x.c1 - x.c0, first_piece = false) {
@@ -613,36 +624,36 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
       const SeqUnits& sq = x.sq;
       const int row0 = x.tile * N, rows = min(N, sq.n * p.group - row0);
       const bool any_chunk = x.c0 < x.cn;
-      float2 l2[N / 2];  // this thread's part of each row's sum
+      float2 l2[COLS / 2];  // this thread's part of each row's sum
 #pragma unroll
-      for (int i = 0; i < N / 2; ++i) l2[i] = make_float2(0.f, 0.f);
+      for (int i = 0; i < COLS / 2; ++i) l2[i] = make_float2(0.f, 0.f);
       if (any_chunk) wait_warp(&frready[pi % PIECE_RING], (pi / PIECE_RING) & 1, ERR_KV8_S_WAIT);
-      const float* fr = s_fr[pi % PIECE_RING];
+      const float* fr = s_fr[pi % PIECE_RING] + col0;
+      const float* nref = s_nref + col0;
       bool force = true;
       for (int c = x.c0; c < x.cn; ++c, ++it) {
         const int b = it & 1, slot = it % SC_RING, pb = it % PB;
         wait_warp(&scready[slot], (it / SC_RING) & 1, ERR_KV8_FULL_WAIT);
-        const int in = warp * 32 + lane, tok = c * AT_CHUNK + in;
+        const int tok = c * AT_CHUNK + in;
         const PageScale sc = s_sc[slot][in >> part_log2];
-        bool lacks = false;  // a page of the chunk is missing: its rows' maxima are not known yet
-        for (int i = 0; i < (AT_CHUNK >> part_log2); ++i) lacks |= !s_sc[slot][i].ok;
+        // a page of the chunk is missing: its rows' maxima are not known yet
+        const bool lacks = __any_sync(FULL_MASK, lane < (AT_CHUNK >> part_log2) && !s_sc[slot][lane & 7].ok);
         // rows below `hid` do not see this token
         const int after = tok - (sq.len - sq.n);
         const int hid = !sc.ok || tok >= sq.len ? N : after <= 0 ? 0 : min(N, max(0, after * p.group - row0));
         const bool masks = __any_sync(FULL_MASK, hid > 0);
         wait_warp(&sready[b], (it >> 1) & 1, ERR_KV8_S_WAIT);
         tc_fence_after();
-        const uint32_t t_s = tmem + b * N + t_lane;
+        const uint32_t t_s = tmem + b * N + col0 + t_lane;
         const float2 ks2 = make_float2(sc.k, sc.k), lv2 = make_float2(sc.log2_v, sc.log2_v);
         float s[W];
-        // scores of columns [w0, w0 + W) in s, relative to the rows' references (or not)
-        auto scores = [&](int w0, bool relative) {
+        // scores of columns [w0, w0 + W) in s, relative to the rows' references
+        auto scores = [&](int w0) {
           tmem_ld<W>(t_s + w0, s);
 #pragma unroll
           for (int i = 0; i < W; i += 4) {
             const float4 f = *reinterpret_cast<const float4*>(fr + w0 + i);
-            float4 n = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (relative) n = *reinterpret_cast<const float4*>(s_nref + w0 + i);
+            const float4 n = *reinterpret_cast<const float4*>(nref + w0 + i);
             const float2 a = __ffma2_rn(make_float2(s[i], s[i + 1]), __fmul2_rn(make_float2(f.x, f.y), ks2),
                                         __fadd2_rn(make_float2(n.x, n.y), lv2));
             const float2 d = __ffma2_rn(make_float2(s[i + 2], s[i + 3]), __fmul2_rn(make_float2(f.z, f.w), ks2),
@@ -652,71 +663,74 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
           if (masks) {
 #pragma unroll
             for (int i = 0; i < W; ++i)
-              if (w0 + i < hid) s[i] = -INFINITY;
+              if (col0 + w0 + i < hid) s[i] = -INFINITY;
           }
         };
         bool raise = force;
         if (!force) {
           float top = -INFINITY;
 #pragma unroll
-          for (int w0 = 0; w0 < N; w0 += W) {
-            scores(w0, true);
+          for (int w0 = 0; w0 < COLS; w0 += W) {
+            scores(w0);
 #pragma unroll
             for (int i = 0; i < W; ++i) top = fmaxf(top, s[i]);
           }
           raise = top > RAISE;
         }
-        if (bar_or(2, raise)) {
+        if (bar_or<32 * S::SOFT>(2, raise)) {
           // new references: the rows' maxima over the chunk and before
 #pragma unroll 1
-          for (int w0 = 0; w0 < N; w0 += W) {
-            scores(w0, false);
+          for (int w0 = 0; w0 < COLS; w0 += 16) {
+            float y[16];
+            tmem_ld16(t_s + w0, y);
             int mine = 0;
 #pragma unroll
-            for (int i = 0; i < W; ++i) {
-              const int k = __reduce_max_sync(FULL_MASK, float_key(s[i]));
+            for (int i = 0; i < 16; ++i) {
+              float z = fmaf(y[i], fr[w0 + i] * sc.k, sc.log2_v);
+              if (col0 + w0 + i < hid) z = -INFINITY;
+              const int k = __reduce_max_sync(FULL_MASK, float_key(z));
               if (lane == i) mine = k;
             }
-            if (lane < W) s_red[warp][w0 + lane] = key_float(mine);
+            if (lane < 16) s_red[quarter][col0 + w0 + lane] = key_float(mine);
           }
-          named_bar_sync(1, 32 * AT_SOFT);
+          sync_soft();
           if (tid < N) {
-            float m = c == x.c0 ? -INFINITY : s_raw[tid];
-            const float old = m;
-#pragma unroll
-            for (int w = 0; w < AT_SOFT; ++w) m = fmaxf(m, s_red[w][tid]);
+            const float old = c == x.c0 ? -INFINITY : s_raw[tid];
+            const float m = fmaxf(fmaxf(fmaxf(s_red[0][tid], s_red[1][tid]), fmaxf(s_red[2][tid], s_red[3][tid])), old);
             s_fac[tid] = m == -INFINITY ? 1.f : ex2(old - m);
             s_raw[tid] = m;
             s_nref[tid] = m == -INFINITY ? 0.f : -m;
           }
-          named_bar_sync(1, 32 * AT_SOFT);
+          sync_soft();
           if (c != x.c0) {
 #pragma unroll
-            for (int i = 0; i < N / 2; ++i)
-              l2[i] = __fmul2_rn(l2[i], make_float2(s_fac[2 * i], s_fac[2 * i + 1]));
+            for (int i = 0; i < COLS / 2; ++i)
+              l2[i] = __fmul2_rn(l2[i], make_float2(s_fac[col0 + 2 * i], s_fac[col0 + 2 * i + 1]));
             wait_warp(&pvdone[(it - 1) & 1], ((it - 1) >> 1) & 1, ERR_KV8_PV_WAIT);
             tc_fence_after();
 #pragma unroll 1
-            for (int w0 = 0; w0 < N; w0 += 16) {
+            for (int w0 = 0; w0 < COLS; w0 += 16) {
               float o[16];
-              tmem_ld16(t_o + t_lane + w0, o);
+              tmem_ld16(t_o + t_lane + col0 + w0, o);
 #pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] *= s_fac[w0 + i];
-              tmem_st16(t_o + t_lane + w0, o);
+              for (int i = 0; i < 16; ++i) o[i] *= s_fac[col0 + w0 + i];
+              tmem_st16(t_o + t_lane + col0 + w0, o);
             }
           }
+          force = true;  // the scores in registers are of the old references, or none
         }
-        force = lacks;
         if (it >= PB) {
           const int j = it - PB;
           wait_warp(&pvdone[j & 1], (j >> 1) & 1, ERR_KV8_PV_WAIT);
         }
         const float2 iv2 = make_float2(sc.inv_v, sc.inv_v);
         uint8_t* pt = sm + S::OFF_P + pb * S::PT;
+        constexpr int RB = N < 64 ? 2 * N : 128;
+        const int f = swz<RB>(in);
 #pragma unroll
-        for (int w0 = 0; w0 < N; w0 += W) {
-          scores(w0, true);
-          if (w0 + W == N) {  // S' is read for the last time
+        for (int w0 = 0; w0 < COLS; w0 += W) {
+          if (COLS > W || force) scores(w0);
+          if (w0 + W == COLS) {  // S' is read for the last time
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sfree[b]);
@@ -729,15 +743,15 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
             const __half2 hh = __floats2half2_rn(e.x, e.y);
             h[i / 2] = *reinterpret_cast<const uint32_t*>(&hh);
           }
-          constexpr int RB = N < 64 ? 2 * N : 128;
 #pragma unroll
           for (int k = 0; k < W / 8; ++k) {
-            const int piece = w0 / 8 + k;
+            const int piece = (col0 + w0) / 8 + k;
             uint8_t* row = pt + (piece / 8) * (AT_CHUNK * 128) + in * RB;
-            *reinterpret_cast<uint4*>(row + (((piece % 8) ^ swz<RB>(in)) << 4)) =
+            *reinterpret_cast<uint4*>(row + (((piece % 8) ^ f) << 4)) =
                 make_uint4(h[4 * k], h[4 * k + 1], h[4 * k + 2], h[4 * k + 3]);
           }
         }
+        force = lacks;
         fence_async_smem();
         tc_fence_before();
         __syncwarp();
@@ -745,9 +759,9 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
       }
 
       // ---- the piece's sums, and its outputs or part
-      float l[W];
 #pragma unroll
-      for (int w0 = 0; w0 < N; w0 += W) {
+      for (int w0 = 0; w0 < COLS; w0 += W) {
+        float l[W];
 #pragma unroll
         for (int i = 0; i < W; i += 2) { l[i] = l2[(w0 + i) / 2].x; l[i + 1] = l2[(w0 + i) / 2].y; }
         // halves of the columns go to the other half of the lanes, until lane i holds column i
@@ -761,10 +775,10 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
           }
         }
         if (W == 16) l[0] += __shfl_xor_sync(FULL_MASK, l[0], 16);
-        if (lane < W) s_red[warp][w0 + lane] = l[0];
+        if (lane < W) s_red[quarter][col0 + w0 + lane] = l[0];
       }
-      named_bar_sync(1, 32 * AT_SOFT);
-      const int d = warp * 32 + lane;  // this thread's column of the head dimension
+      sync_soft();
+      const int d = in;  // this thread's column of the head dimension
       const bool mine = d < D;
       float* part = p.part + (int64_t(blockIdx.x) * 2 + (first_piece ? 0 : 1)) * N * (D + 2);
       if (tid < N) {
@@ -794,27 +808,27 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
             if (id < 0 || id >= p.c.n_pages) continue;
             const int64_t at = ((int64_t(id) * p.c.heads + x.h) * p.c.page + (t & (p.c.page - 1))) * D + d;
             if ((p.c.v[at] & 0x7f) == 0x7f) {
-              nan_row = min(nan_row, max(0, (t - edge) * p.group - row0));
+              nan_row = max(0, (t - edge) * p.group - row0);
               break;  // later tokens are seen by fewer rows
             }
           }
         }
       }
-      named_bar_sync(1, 32 * AT_SOFT);
+      sync_soft();
       if (any_chunk && tid == 0) s_nan[pi % PIECE_RING] = 0;
-      int i = row0 / p.group, j = row0 - i * p.group;  // new token and head of a row
+      int i = (row0 + col0) / p.group, j = row0 + col0 - i * p.group;  // new token and head of a row
 #pragma unroll 1
-      for (int w0 = 0; w0 < rows; w0 += 16) {
+      for (int r0 = col0; r0 < min(rows, col0 + COLS); r0 += 16) {
         float o[16];
         if (any_chunk) {
-          tmem_ld16(t_o + t_lane + w0, o);
+          tmem_ld16(t_o + t_lane + r0, o);
         } else {
 #pragma unroll
           for (int k = 0; k < 16; ++k) o[k] = 0.f;
         }
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
-          const int r = w0 + k;
+          const int r = r0 + k;
           if (r < rows && mine) {
             const float y = r >= nan_row ? NAN : o[k];
             if (x.whole)
@@ -826,7 +840,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
         }
       }
       tc_fence_before();
-      named_bar_sync(1, 32 * AT_SOFT);  // s_red and s_fac are read
+      sync_soft();  // s_red and s_fac are read
       if (any_chunk) ++pi;
     }
   }
@@ -952,7 +966,7 @@ cudaError_t launch(const CUtensorMap& tm, const AttnParams& prm, int grid, cudaS
   constexpr int smem = AttnShape<D, N>::SMEM;
   cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void*>(kv8_attention_kernel<D, N>), smem);
   if (e != cudaSuccess) return e;
-  kv8_attention_kernel<D, N><<<grid, AT_THREADS, smem, stream>>>(tm, prm);
+  kv8_attention_kernel<D, N><<<grid, AttnShape<D, N>::THREADS, smem, stream>>>(tm, prm);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   PdlScope pdl(true);
