@@ -82,8 +82,7 @@ __device__ __forceinline__ SeqUnits seq_units(const AttnParams& p, int64_t b) {
   return u;
 }
 
-// The units of all sequences, and where run `run` of `runs` begins: every warp works it out for
-// itself.  The counts of the first 128 sequences stay in registers between the two passes.
+// The units of all sequences, and where run `run` of `runs` begins, by one warp.
 struct Run {
   int64_t per;       // units of a run
   int64_t u, u_end;  // this run's units
@@ -91,16 +90,10 @@ struct Run {
 };
 template <int N>
 __device__ __forceinline__ Run find_run(const AttnParams& p, int64_t run, int runs) {
-  constexpr int KEEP = 4;
   const int lane = threadIdx.x & 31;
-  auto count = [&](int64_t b) { return b < p.batch ? seq_units<N>(p, b).units : int64_t(0); };
-  int64_t kept[KEEP], t = 0;
-#pragma unroll
-  for (int i = 0; i < KEEP; ++i) {
-    kept[i] = i * 32 < p.batch ? count(i * 32 + lane) : 0;
-    t += kept[i];
-  }
-  for (int64_t b = KEEP * 32 + lane; b < p.batch; b += 32) t += count(b);
+  int64_t t = 0;
+#pragma unroll 1
+  for (int64_t b = lane; b < p.batch; b += 32) t += seq_units<N>(p, b).units;
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) t += __shfl_xor_sync(FULL_MASK, t, o);
   Run r;
@@ -111,29 +104,24 @@ __device__ __forceinline__ Run find_run(const AttnParams& p, int64_t run, int ru
   r.b = p.batch;
   r.first = 0;
   if (r.u >= r.u_end) return r;
-  int64_t base = 0;
-  auto look = [&](int64_t b0, int64_t mine) {  // whether unit u is among these 32 sequences'
+#pragma unroll 1
+  for (int64_t b0 = 0; b0 < p.batch; b0 += 32) {  // the 32 sequences among whose units u is
+    const int64_t mine = b0 + lane < p.batch ? seq_units<N>(p, b0 + lane).units : 0;
     int64_t sum = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int64_t x = __shfl_up_sync(FULL_MASK, sum, o);
       if (lane >= o) sum += x;
     }
-    const unsigned past = __ballot_sync(FULL_MASK, base + sum > r.u);
+    const unsigned past = __ballot_sync(FULL_MASK, r.first + sum > r.u);
     if (past) {
       const int l = __ffs(past) - 1;
       r.b = b0 + l;
-      r.first = base + __shfl_sync(FULL_MASK, sum - mine, l);
-      return true;
+      r.first += __shfl_sync(FULL_MASK, sum - mine, l);
+      break;
     }
-    base += __shfl_sync(FULL_MASK, sum, 31);
-    return false;
-  };
-#pragma unroll
-  for (int i = 0; i < KEEP; ++i)
-    if (i * 32 < p.batch && look(i * 32, kept[i])) return r;
-  for (int64_t b0 = KEEP * 32; b0 < p.batch; b0 += 32)
-    if (look(b0, count(b0 + lane))) return r;
+    r.first += __shfl_sync(FULL_MASK, sum, 31);
+  }
   return r;
 }
 
@@ -237,6 +225,11 @@ __device__ __forceinline__ void tmem_ld(uint32_t t, float* v) {
   if constexpr (W == 16) tmem_ld16(t, v);
   else tmem_ld32(t, v);
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 __device__ __forceinline__ void tmem_st16(uint32_t t, const float* v) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
@@ -290,27 +283,32 @@ __device__ __forceinline__ uint32_t nan_codes(uint32_t w) {  // 0xff in each byt
 
 template <int D, int N>
 struct AttnShape {
+  static constexpr int CTAS = N == 16 ? 2 : 1;         // per SM
   static constexpr int KT = AT_CHUNK * D;              // bytes of a chunk's keys, or values
-  static constexpr int STAGES = D < 128 ? 4 : N == 16 ? 4 : N == 128 ? 2 : 3;
-  static constexpr int VW = 2 * KT;                    // widened values; two buffers
-  static constexpr int PB = N == 128 ? 1 : 2;          // buffers of p'
+  static constexpr int STAGES = CTAS == 2 ? 2 : D < 128 ? 4 : N == 128 ? 2 : 3;
+  static constexpr int VW = 2 * KT;                    // widened values
+  static constexpr int VB = CTAS == 2 ? 1 : 2;         // buffers of them
+  static constexpr int PB = CTAS == 2 || N == 128 ? 1 : 2;  // buffers of p'
   static constexpr int PT = AT_CHUNK * N * 2;
-  static constexpr int QB = N >= 64 ? 1 : 2;           // buffers of q hi, lo
+  static constexpr int QB = N == 32 ? 2 : 1;           // buffers of q hi, lo
   static constexpr int QT = N * D;                     // bytes of one of the two
   static constexpr int OFF_V = STAGES * 2 * KT;
-  static constexpr int OFF_P = OFF_V + 2 * VW;
+  static constexpr int OFF_P = OFF_V + VB * VW;
   static constexpr int OFF_Q = OFF_P + PB * PT;
   static constexpr int SMEM = 1024 + OFF_Q + QB * 2 * QT;
   static constexpr int TMEM = N == 16 ? 64 : 4 * N;    // two S' and one O' of N columns
   // Softmax warps: a warp can read the 32 lanes (tokens) of tensor memory of its place among
   // four; with 64 rows and more, two warps share the columns (rows) of each 32 tokens.
   static constexpr int GROUPS = N >= 64 ? 2 : 1, SOFT = 4 * GROUPS, COLS = N / GROUPS;
-  static constexpr int LOAD_WARP = SOFT + 4, MMA_WARP = SOFT + 5, THREADS = 32 * (SOFT + 6);
+  // then four that widen V, and one each for loads, S' and O'
+  static constexpr int LOAD_WARP = SOFT + 4, S_WARP = SOFT + 5, O_WARP = SOFT + 6;
+  static constexpr int THREADS = 32 * (SOFT + 7);
 };
 
-constexpr int AT_CONV = 4;                  // warps
+constexpr int AT_CONV = 4;                  // warps that widen V
 constexpr int SC_RING = 8, PIECE_RING = 4;  // deeper than any warp runs ahead of the softmax
-constexpr float RAISE = 8.f;                // log2 of how far a score may pass its reference
+constexpr float RAISE = 14.f;               // log2 of how far a score may pass its reference
+constexpr float ANEW = 0x1p-100f;
 
 struct PageScale {  // of the tokens of one page
   float k, log2_v, inv_v;
@@ -333,20 +331,21 @@ __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, uint32_t 
 }
 
 template <int D, int N>
-__global__ void __launch_bounds__(AttnShape<D, N>::THREADS, 1)
+__global__ void __launch_bounds__(AttnShape<D, N>::THREADS, AttnShape<D, N>::CTAS)
     kv8_attention_kernel(const __grid_constant__ CUtensorMap tm, const AttnParams p) {
   using S = AttnShape<D, N>;
-  constexpr int ST = S::STAGES, PB = S::PB, QB = S::QB;
-  constexpr int COLS = S::COLS, W = COLS < 32 ? 16 : 32;  // columns of a softmax thread, and at a time
+  constexpr int ST = S::STAGES, VB = S::VB, PB = S::PB, QB = S::QB;
+  constexpr int COLS = S::COLS, W = COLS < 32 ? 16 : 32;  // columns of a softmax thread, and of them at a time
   extern __shared__ uint8_t at_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(at_raw) + 1023) & ~uintptr_t(1023));
-  __shared__ __align__(8) uint64_t full[ST], empty[ST], sready[2], sfree[2], vready[2], pready[PB],
-      pvdone[2], qready[QB], qfree[QB], scready[SC_RING], frready[PIECE_RING];
+  __shared__ __align__(8) uint64_t full[ST], empty[ST], sready[2], sfree[2], vready[VB], pready[PB],
+      pvdone[2], qready[QB], qfree[QB], frready[PIECE_RING];
   __shared__ PageScale s_sc[SC_RING][8];
   __shared__ __align__(16) float s_fr[PIECE_RING][N], s_nref[N];
   __shared__ float s_raw[N], s_fac[N], s_red[4][N];
-  __shared__ int s_nan[PIECE_RING];
+  __shared__ int s_nan[PIECE_RING][2];  // a NaN was taken out of V, for either group
   __shared__ uint32_t s_tmem;
+  __shared__ Run s_run;
   __shared__ volatile int s_fail;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -355,13 +354,12 @@ __global__ void __launch_bounds__(AttnShape<D, N>::THREADS, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sready[i], 1);
       mbar_init(&sfree[i], S::SOFT);
-      mbar_init(&vready[i], AT_CONV);
       mbar_init(&pvdone[i], 1);
     }
+    for (int i = 0; i < VB; ++i) mbar_init(&vready[i], AT_CONV);
     for (int i = 0; i < PB; ++i) mbar_init(&pready[i], S::SOFT);
     for (int i = 0; i < QB; ++i) { mbar_init(&qready[i], AT_CONV); mbar_init(&qfree[i], 1); }
-    for (int i = 0; i < SC_RING; ++i) mbar_init(&scready[i], 1);
-    for (int i = 0; i < PIECE_RING; ++i) { mbar_init(&frready[i], AT_CONV); s_nan[i] = 0; }
+    for (int i = 0; i < PIECE_RING; ++i) { mbar_init(&frready[i], AT_CONV); s_nan[i][0] = s_nan[i][1] = 0; }
     fence_mbar_init();
     s_fail = 0;
   }
@@ -372,14 +370,18 @@ __global__ void __launch_bounds__(AttnShape<D, N>::THREADS, 1)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  pdl_wait();
+  pdl_trigger();
+  if (warp == 1) {
+    const Run r = find_run<N>(p, blockIdx.x, gridDim.x);
+    if (lane == 0) s_run = r;
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_tmem;  // S' of even and odd chunks, O'
   const uint32_t t_o = tmem + 2 * N;
-  pdl_wait();
-  pdl_trigger();
-  const Run run = find_run<N>(p, blockIdx.x, gridDim.x);
+  const Run run = s_run;
   Piece x;
   x.b = run.b;
   x.first = run.first;
@@ -410,24 +412,35 @@ __global__ void __launch_bounds__(AttnShape<D, N>::THREADS, 1)
         const int tok = c * AT_CHUNK + lane * part;
         return lane < parts && tok < x.end ? __ldg(tab + (tok >> p.page_log2)) : -2;
       };
-      int next = x.c0 < x.cn ? page_of(x.c0) : -2;
+      // page indices are read two chunks ahead, scales one
+      auto exists = [&](int i) { return i >= 0 && i < p.c.n_pages; };
+      float ks1 = 0.f, vs1 = 1.f;
+      auto read_scales = [&](int i) {
+        if (!exists(i)) return;
+        const int64_t ph = int64_t(i) * p.c.heads + x.h;
+        ks1 = __ldg(p.c.ks + ph);
+        vs1 = __ldg(p.c.vs + ph);
+      };
+      int id1 = x.c0 < x.cn ? page_of(x.c0) : -2, id2 = x.c0 + 1 < x.cn ? page_of(x.c0 + 1) : -2;
+      read_scales(id1);
       for (int c = x.c0; c < x.cn; ++c, ++it) {
         const int st = it % ST, slot = it % SC_RING;
-        const int id = next;
-        if (c + 1 < x.cn) next = page_of(c + 1);
-        const bool ok = id >= 0 && id < p.c.n_pages;
+        const int id = id1;
+        const float ks = ks1, vs = vs1;
+        id1 = id2;
+        read_scales(id1);
+        id2 = c + 2 < x.cn ? page_of(c + 2) : -2;
+        const bool ok = exists(id);
         if (id != -2 && !ok) atomicOr(&g_err_kv8_attn, ERR_KV8_PAGE);
         const int64_t ph = int64_t(ok ? id : 0) * p.c.heads + x.h;
-        float ks = 0.f, vs = 1.f;
-        if (ok) {
-          ks = __ldg(p.c.ks + ph);
-          vs = __ldg(p.c.vs + ph);
-        }
         const unsigned have = __ballot_sync(FULL_MASK, ok);
         if (it >= ST && !__all_sync(FULL_MASK, wait_warp(&empty[st], ((it / ST) - 1) & 1, ERR_KV8_EMPTY_WAIT))) {
           ok_run = false;
           break;
         }
+        // (whoever waits for the stage, or for what is made from it, sees its scales)
+        if (lane < 8) s_sc[slot][lane] = PageScale{ks, log2f(vs), 1.f / vs, ok ? 1 : 0};
+        __syncwarp();
         uint8_t* dst = sm + st * 2 * S::KT + lane * bytes;
         if (lane == 0) mbar_arrive_expect_tx(&full[st], 2u * bytes * __popc(have));
         __syncwarp();
@@ -435,41 +448,18 @@ __global__ void __launch_bounds__(AttnShape<D, N>::THREADS, 1)
           tma_load3(dst, &tm, 0, 0, static_cast<int>(ph), &full[st]);
           bulk_g2s(dst + S::KT, p.c.v + ph * bytes, bytes, &full[st]);
         }
-        if (lane < 8) s_sc[slot][lane] = PageScale{ks, log2f(vs), 1.f / vs, ok ? 1 : 0};
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&scready[slot]);
       }
     }
     if (!ok_run || s_fail)  // what is in flight has to land
       for (int i = max(0, it - ST); i < it; ++i)
         mbar_wait_bounded(&full[i % ST], (i / ST) & 1, &g_err_kv8_attn, ERR_KV8_EMPTY_WAIT);
-  } else if (warp == S::MMA_WARP) {
-    // ================= products =================
+  } else if (warp == S::S_WARP) {
+    // ================= S' = K Q^T, hi and lo =================
+    // (a thread takes 80 cycles or so to issue a product, so the two kinds have one each)
     if (lane == 0) {
-      constexpr uint32_t ID_S = tc_idesc(128, N, false, false), ID_O = tc_idesc(128, N, true, true);
-      constexpr int VB = D < 64 ? 64 : 128, PBY = N < 64 ? 2 * N : 128;  // bytes of a tile's row
-      const uint64_t d_v = tile_desc<VB>(sm + S::OFF_V, D == 128 ? AT_CHUNK * 128 : 0);
-      const uint64_t d_p = tile_desc<PBY>(sm + S::OFF_P, AT_CHUNK * 128);
+      constexpr uint32_t ID = tc_idesc(128, N, false, false);
       const uint64_t d_k = tile_desc<D>(sm, 16), d_q = tile_desc<D>(sm + S::OFF_Q, 16);
       int it = 0, pi = 0;
-      int pend = -1;          // chunk whose O' product is still to come
-      bool pend_first = false;
-      auto product_o = [&]() {
-        if (pend < 0) return;
-        const int b = pend & 1, pb = pend % PB;
-        bool ok = wait(&pready[pb], (pend / PB) & 1, ERR_KV8_PV_WAIT);
-        ok = wait(&vready[b], (pend >> 1) & 1, ERR_KV8_PV_WAIT) && ok;
-        if (ok) {
-          tc_fence_after();
-          // (16 tokens further: the address field, in units of 16 bytes, moves on)
-          uint64_t v = d_v + (b * S::VW >> 4), pp = d_p + (pb * S::PT >> 4);
-#pragma unroll 2
-          for (int k = 0; k < AT_CHUNK / 16; ++k, v += VB, pp += PBY)
-            mma_f16(t_o, v, pp, ID_O, !(pend_first && k == 0));
-        }
-        tc_commit(&pvdone[b]);
-        pend = -1;
-      };
       for (int64_t u = run.u; u < run.u_end; u += x.c1 - x.c0) {
         piece_at<N>(p, u, run.u_end, x);
         if (x.c0 >= x.cn) continue;
@@ -481,22 +471,45 @@ __global__ void __launch_bounds__(AttnShape<D, N>::THREADS, 1)
           if (ok) {
             tc_fence_after();
             const uint64_t k = d_k + (st * 2 * S::KT >> 4);
-            uint64_t q = d_q + ((pi % QB) * 2 * S::QT >> 4);
-#pragma unroll 1
-            for (int half = 0; half < 2; ++half, q += S::QT >> 4)
+            const uint64_t q = d_q + ((pi % QB) * 2 * S::QT >> 4);
 #pragma unroll
-              for (int d = 0; d < D / 32; ++d) mma_f8(tmem + b * N, k + 2 * d, q + 2 * d, ID_S, half + d > 0);
+            for (int d = 0; d < D / 32; ++d) mma_f8(tmem + b * N, k + 2 * d, q + 2 * d, ID, d > 0);
+#pragma unroll
+            for (int d = 0; d < D / 32; ++d) mma_f8(tmem + b * N, k + 2 * d, q + (S::QT >> 4) + 2 * d, ID, true);
           }
           tc_commit(&sready[b]);
           tc_commit(&empty[st]);
           if (c + 1 == x.cn) tc_commit(&qfree[pi % QB]);
-          product_o();
-          pend = it;
-          pend_first = c == x.c0;
         }
         ++pi;
       }
-      product_o();
+    }
+    __syncwarp();
+  } else if (warp == S::O_WARP) {
+    // ================= O' += V^T P' =================
+    if (lane == 0) {
+      constexpr uint32_t ID = tc_idesc(128, N, true, true);
+      constexpr int VBY = D < 64 ? 64 : 128, PBY = N < 64 ? 2 * N : 128;  // bytes of a tile's row
+      const uint64_t d_v = tile_desc<VBY>(sm + S::OFF_V, D == 128 ? AT_CHUNK * 128 : 0);
+      const uint64_t d_p = tile_desc<PBY>(sm + S::OFF_P, AT_CHUNK * 128);
+      int it = 0;
+      for (int64_t u = run.u; u < run.u_end; u += x.c1 - x.c0) {
+        piece_at<N>(p, u, run.u_end, x);
+        for (int c = x.c0; c < x.cn; ++c, ++it) {
+          const int vb = it % VB, pb = it % PB;
+          bool ok = wait(&vready[vb], (it / VB) & 1, ERR_KV8_PV_WAIT);
+          ok = wait(&pready[pb], (it / PB) & 1, ERR_KV8_PV_WAIT) && ok;
+          if (ok) {
+            tc_fence_after();
+            const uint64_t v = d_v + (vb * S::VW >> 4), pp = d_p + (pb * S::PT >> 4);
+            // (16 tokens further: the address field, in units of 16 bytes, moves on)
+#pragma unroll
+            for (int k = 0; k < AT_CHUNK / 16; ++k)
+              mma_f16(t_o, v + k * VBY, pp + k * PBY, ID, k > 0 || c != x.c0);
+          }
+          tc_commit(&pvdone[it & 1]);
+        }
+      }
     }
     __syncwarp();
   } else if (warp >= S::SOFT) {
@@ -561,46 +574,58 @@ __global__ void __launch_bounds__(AttnShape<D, N>::THREADS, 1)
       }
       const int part_log2 = min(p.page_log2, 7);
       for (int c = x.c0; c < x.cn; ++c, ++it) {
-        const int st = it % ST, b = it & 1, slot = it % SC_RING;
-        wait_warp(&scready[slot], (it / SC_RING) & 1, ERR_KV8_FULL_WAIT);
+        const int st = it % ST, b = it % VB, slot = it % SC_RING;
         wait_warp(&full[st], (it / ST) & 1, ERR_KV8_FULL_WAIT);
-        if (it >= 2) wait_warp(&pvdone[b], ((it >> 1) - 1) & 1, ERR_KV8_PV_WAIT);
+        if (it >= VB) wait_warp(&pvdone[(it - VB) & 1], ((it - VB) >> 1) & 1, ERR_KV8_PV_WAIT);
         const uint8_t* src = sm + st * 2 * S::KT + S::KT;
         uint8_t* dst = sm + S::OFF_V + b * S::VW;
         // Chunks with tokens that some row does not see (the causal edge), with rows behind the
         // last token or with pages that were not loaded: 0 * NaN is NaN, so there V takes part
         // without NaN, and rows that do see a NaN get it at the end.
         bool edge = (c + 1) * AT_CHUNK > x.sq.len - x.sq.n;
-        for (int i = 0; i < (AT_CHUNK >> part_log2); ++i) edge |= !s_sc[slot][i].ok;
+        edge |= __any_sync(FULL_MASK, lane < (AT_CHUNK >> part_log2) && !s_sc[slot][lane & 7].ok);
         constexpr int UPR = D / 16;                     // 16-byte pieces of a row
         constexpr int LPR = UPR < 4 ? UPR : 4;          // lanes on a row
         constexpr int TOKS = 32 / LPR;                  // rows of one round
         bool nan = false;
-#pragma unroll 2
-        for (int k = 0; k < UPR; ++k) {
-          const int tok = cw * 32 + (k % (32 / TOKS)) * TOKS + lane / LPR;
-          const int piece = lane % LPR + (k / (32 / TOKS)) * LPR;
-          uint4 w = *reinterpret_cast<const uint4*>(src + tok * D + piece * 16);
-          if (edge) {
-            if (c * AT_CHUNK + tok >= x.end || !s_sc[slot][tok >> part_log2].ok) w = make_uint4(0u, 0u, 0u, 0u);
-            const uint32_t n0 = nan_codes(w.x), n1 = nan_codes(w.y), n2 = nan_codes(w.z), n3 = nan_codes(w.w);
-            nan |= (n0 | n1 | n2 | n3) != 0;
-            w.x &= ~n0; w.y &= ~n1; w.z &= ~n2; w.w &= ~n3;
-          }
-          const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-          uint32_t o[8];
+        constexpr int RB = D < 64 ? 64 : 128;
+        constexpr int STEP = UPR < 4 ? UPR : 4;  // pieces of a lane in flight
+#pragma unroll 1
+        for (int k0 = 0; k0 < UPR; k0 += STEP) {
+          uint4 w[STEP];
+          int tok[STEP];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            o[2 * i] = e4m3x2_to_f16x2(static_cast<uint16_t>(in[i]));
-            o[2 * i + 1] = e4m3x2_to_f16x2(static_cast<uint16_t>(in[i] >> 16));
+          for (int i = 0; i < STEP; ++i) {
+            const int k = k0 + i;
+            tok[i] = cw * 32 + (k % (32 / TOKS)) * TOKS + lane / LPR;
+            w[i] = *reinterpret_cast<const uint4*>(src + tok[i] * D + (lane % LPR + (k / (32 / TOKS)) * LPR) * 16);
           }
-          constexpr int RB = D < 64 ? 64 : 128;
-          uint8_t* row = dst + (piece / 4) * (AT_CHUNK * 128) + tok * RB;
-          const int q0 = (piece % 4) * 2, f = swz<RB>(tok);
-          *reinterpret_cast<uint4*>(row + ((q0 ^ f) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-          *reinterpret_cast<uint4*>(row + (((q0 + 1) ^ f) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+          if (edge) {
+#pragma unroll
+            for (int i = 0; i < STEP; ++i) {
+              if (c * AT_CHUNK + tok[i] >= x.end || !s_sc[slot][tok[i] >> part_log2].ok) w[i] = make_uint4(0u, 0u, 0u, 0u);
+              const uint32_t n0 = nan_codes(w[i].x), n1 = nan_codes(w[i].y), n2 = nan_codes(w[i].z), n3 = nan_codes(w[i].w);
+              nan |= (n0 | n1 | n2 | n3) != 0;
+              w[i].x &= ~n0; w[i].y &= ~n1; w[i].z &= ~n2; w[i].w &= ~n3;
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < STEP; ++i) {
+            const int piece = lane % LPR + ((k0 + i) / (32 / TOKS)) * LPR;
+            const uint32_t in[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+            uint32_t o[8];
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+              o[2 * n] = e4m3x2_to_f16x2(static_cast<uint16_t>(in[n]));
+              o[2 * n + 1] = e4m3x2_to_f16x2(static_cast<uint16_t>(in[n] >> 16));
+            }
+            uint8_t* row = dst + (piece / 4) * (AT_CHUNK * 128) + tok[i] * RB;
+            const int q0 = (piece % 4) * 2, f = swz<RB>(tok[i]);
+            *reinterpret_cast<uint4*>(row + ((q0 ^ f) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4*>(row + (((q0 + 1) ^ f) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+          }
         }
-        if (nan) s_nan[pi % PIECE_RING] = 1;
+        if (nan) s_nan[pi % PIECE_RING][0] = s_nan[pi % PIECE_RING][1] = 1;
         fence_async_smem();
         __syncwarp();
         if (lane == 0) {
@@ -616,7 +641,8 @@ __global__ void __launch_bounds__(AttnShape<D, N>::THREADS, 1)
     const int in = quarter * 32 + lane;
     const uint32_t t_lane = static_cast<uint32_t>(quarter * 32) << 16;
     const int part_log2 = min(p.page_log2, 7);
-    auto sync_soft = [&]() { named_bar_sync(1, 32 * S::SOFT); };
+    const int gt = tid & 127;  // the thread's place in its group, which has its own rows and barriers
+    auto sync_group = [&]() { named_bar_sync(1 + (warp >> 2), 128); };
     int it = 0, pi = 0;
     bool first_piece = true;
     for (int64_t u = run.u; u < run.u_end; u += x.c1 - x.c0, first_piece = false) {
@@ -633,52 +659,75 @@ __global__ void __launch_bounds__(AttnShape<D, N>::THREADS, 1)
       bool force = true;
       for (int c = x.c0; c < x.cn; ++c, ++it) {
         const int b = it & 1, slot = it % SC_RING, pb = it % PB;
-        wait_warp(&scready[slot], (it / SC_RING) & 1, ERR_KV8_FULL_WAIT);
-        const int tok = c * AT_CHUNK + in;
-        const PageScale sc = s_sc[slot][in >> part_log2];
-        // a page of the chunk is missing: its rows' maxima are not known yet
-        const bool lacks = __any_sync(FULL_MASK, lane < (AT_CHUNK >> part_log2) && !s_sc[slot][lane & 7].ok);
-        // rows below `hid` do not see this token
-        const int after = tok - (sq.len - sq.n);
-        const int hid = !sc.ok || tok >= sq.len ? N : after <= 0 ? 0 : min(N, max(0, after * p.group - row0));
-        const bool masks = __any_sync(FULL_MASK, hid > 0);
         wait_warp(&sready[b], (it >> 1) & 1, ERR_KV8_S_WAIT);
         tc_fence_after();
-        const uint32_t t_s = tmem + b * N + col0 + t_lane;
+        const PageScale sc = s_sc[slot][in >> part_log2];
         const float2 ks2 = make_float2(sc.k, sc.k), lv2 = make_float2(sc.log2_v, sc.log2_v);
-        float s[W];
-        // scores of columns [w0, w0 + W) in s, relative to the rows' references
-        auto scores = [&](int w0) {
-          tmem_ld<W>(t_s + w0, s);
-#pragma unroll
-          for (int i = 0; i < W; i += 4) {
-            const float4 f = *reinterpret_cast<const float4*>(fr + w0 + i);
-            const float4 n = *reinterpret_cast<const float4*>(nref + w0 + i);
-            const float2 a = __ffma2_rn(make_float2(s[i], s[i + 1]), __fmul2_rn(make_float2(f.x, f.y), ks2),
-                                        __fadd2_rn(make_float2(n.x, n.y), lv2));
-            const float2 d = __ffma2_rn(make_float2(s[i + 2], s[i + 3]), __fmul2_rn(make_float2(f.z, f.w), ks2),
-                                        __fadd2_rn(make_float2(n.z, n.w), lv2));
-            s[i] = a.x; s[i + 1] = a.y; s[i + 2] = d.x; s[i + 3] = d.y;
-          }
-          if (masks) {
-#pragma unroll
-            for (int i = 0; i < W; ++i)
-              if (col0 + w0 + i < hid) s[i] = -INFINITY;
-          }
-        };
-        bool raise = force;
-        if (!force) {
-          float top = -INFINITY;
+        const float2 iv2 = make_float2(sc.inv_v, sc.inv_v);
+        // rows below `hid` do not see this token
+        const int tok = c * AT_CHUNK + in, after = tok - (sq.len - sq.n);
+        const int hid = !sc.ok || tok >= sq.len ? N : after <= 0 ? 0 : min(N, max(0, after * p.group - row0));
+        const bool masks = __any_sync(FULL_MASK, hid > 0);
+        const uint32_t t_s = tmem + b * N + col0 + t_lane;
+        constexpr int RB = N < 64 ? 2 * N : 128;
+        uint8_t* pt = sm + S::OFF_P + pb * S::PT + in * RB;
+        const int f = swz<RB>(in);
+        bool free_p = it < PB;
+        float top;
+        // The weights of this thread's columns to shared memory and to the rows' sums; a second
+        // time, after a raise, only to the sums of rows that start anew.
+        auto weights = [&](bool again) {
+          top = -INFINITY;
 #pragma unroll
           for (int w0 = 0; w0 < COLS; w0 += W) {
-            scores(w0);
+            float s[W];
+            tmem_ld<W>(t_s + w0, s);
 #pragma unroll
-            for (int i = 0; i < W; ++i) top = fmaxf(top, s[i]);
+            for (int i = 0; i < W; i += 4) {
+              const float4 g = *reinterpret_cast<const float4*>(fr + w0 + i);
+              const float4 n = *reinterpret_cast<const float4*>(nref + w0 + i);
+              const float2 a = __ffma2_rn(make_float2(s[i], s[i + 1]), __fmul2_rn(make_float2(g.x, g.y), ks2),
+                                          __fadd2_rn(make_float2(n.x, n.y), lv2));
+              const float2 d = __ffma2_rn(make_float2(s[i + 2], s[i + 3]), __fmul2_rn(make_float2(g.z, g.w), ks2),
+                                          __fadd2_rn(make_float2(n.z, n.w), lv2));
+              s[i] = a.x; s[i + 1] = a.y; s[i + 2] = d.x; s[i + 3] = d.y;
+            }
+            if (masks) {
+#pragma unroll
+              for (int i = 0; i < W; ++i)
+                if (col0 + w0 + i < hid) s[i] = -INFINITY;
+            }
+            if (!free_p) {
+              wait_warp(&pvdone[(it - PB) & 1], ((it - PB) >> 1) & 1, ERR_KV8_PV_WAIT);
+              free_p = true;
+            }
+#pragma unroll
+            for (int k = 0; k < W / 8; ++k) {
+              uint32_t h[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float2 y = make_float2(s[8 * k + 2 * i], s[8 * k + 2 * i + 1]);
+                top = max3(top, y.x, y.y);
+                const float2 e = make_float2(ex2(y.x), ex2(y.y));
+                float2& l = l2[(w0 + 8 * k) / 2 + i];
+                if (!again) {
+                  l = __ffma2_rn(e, iv2, l);
+                } else {
+                  const int r = col0 + w0 + 8 * k + 2 * i;
+                  if (s_fac[r] < ANEW) l.x = fmaf(e.x, sc.inv_v, l.x);
+                  if (s_fac[r + 1] < ANEW) l.y = fmaf(e.y, sc.inv_v, l.y);
+                }
+                const __half2 hh = __floats2half2_rn(e.x, e.y);
+                h[i] = *reinterpret_cast<const uint32_t*>(&hh);
+              }
+              const int piece = (col0 + w0) / 8 + k;
+              *reinterpret_cast<uint4*>(pt + (piece / 8) * (AT_CHUNK * 128) + (((piece % 8) ^ f) << 4)) =
+                  make_uint4(h[0], h[1], h[2], h[3]);
+            }
           }
-          raise = top > RAISE;
-        }
-        if (bar_or<32 * S::SOFT>(2, raise)) {
-          // new references: the rows' maxima over the chunk and before
+        };
+        // New references: the rows' maxima over this chunk and before.
+        auto raise = [&]() {
 #pragma unroll 1
           for (int w0 = 0; w0 < COLS; w0 += 16) {
             float y[16];
@@ -693,69 +742,57 @@ __global__ void __launch_bounds__(AttnShape<D, N>::THREADS, 1)
             }
             if (lane < 16) s_red[quarter][col0 + w0 + lane] = key_float(mine);
           }
-          sync_soft();
-          if (tid < N) {
-            const float old = c == x.c0 ? -INFINITY : s_raw[tid];
-            const float m = fmaxf(fmaxf(fmaxf(s_red[0][tid], s_red[1][tid]), fmaxf(s_red[2][tid], s_red[3][tid])), old);
-            s_fac[tid] = m == -INFINITY ? 1.f : ex2(old - m);
-            s_raw[tid] = m;
-            s_nref[tid] = m == -INFINITY ? 0.f : -m;
+          sync_group();
+          if (gt < COLS) {
+            const int r = col0 + gt;
+            const float old = c == x.c0 ? -INFINITY : s_raw[r];
+            const float m = fmaxf(max3(s_red[0][r], s_red[1][r], s_red[2][r]), fmaxf(s_red[3][r], old));
+            s_fac[r] = m == -INFINITY ? 1.f : ex2(old - m);
+            s_raw[r] = m;
+            s_nref[r] = m == -INFINITY ? 0.f : -m;
           }
-          sync_soft();
-          if (c != x.c0) {
+          sync_group();
+          if (c == x.c0) return;
 #pragma unroll
-            for (int i = 0; i < COLS / 2; ++i)
-              l2[i] = __fmul2_rn(l2[i], make_float2(s_fac[col0 + 2 * i], s_fac[col0 + 2 * i + 1]));
-            wait_warp(&pvdone[(it - 1) & 1], ((it - 1) >> 1) & 1, ERR_KV8_PV_WAIT);
-            tc_fence_after();
+          for (int i = 0; i < COLS; ++i) {
+            // a row whose reference moved that far starts anew: what it had is nothing beside
+            // what it gets, and its weights of this chunk may have passed the floats
+            float& l = i & 1 ? l2[i / 2].y : l2[i / 2].x;
+            const float g = s_fac[col0 + i];
+            l = g < ANEW ? 0.f : l * g;
+          }
+          wait_warp(&pvdone[(it - 1) & 1], ((it - 1) >> 1) & 1, ERR_KV8_PV_WAIT);
+          tc_fence_after();
 #pragma unroll 1
-            for (int w0 = 0; w0 < COLS; w0 += 16) {
-              float o[16];
-              tmem_ld16(t_o + t_lane + col0 + w0, o);
+          for (int w0 = 0; w0 < COLS; w0 += 16) {
+            float o[16];
+            tmem_ld16(t_o + t_lane + col0 + w0, o);
 #pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] *= s_fac[col0 + w0 + i];
-              tmem_st16(t_o + t_lane + col0 + w0, o);
-            }
+            for (int i = 0; i < 16; ++i) o[i] *= s_fac[col0 + w0 + i];
+            tmem_st16(t_o + t_lane + col0 + w0, o);
           }
-          force = true;  // the scores in registers are of the old references, or none
-        }
-        if (it >= PB) {
-          const int j = it - PB;
-          wait_warp(&pvdone[j & 1], (j >> 1) & 1, ERR_KV8_PV_WAIT);
-        }
-        const float2 iv2 = make_float2(sc.inv_v, sc.inv_v);
-        uint8_t* pt = sm + S::OFF_P + pb * S::PT;
-        constexpr int RB = N < 64 ? 2 * N : 128;
-        const int f = swz<RB>(in);
-#pragma unroll
-        for (int w0 = 0; w0 < COLS; w0 += W) {
-          if (COLS > W || force) scores(w0);
-          if (w0 + W == COLS) {  // S' is read for the last time
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sfree[b]);
-          }
-          uint32_t h[W / 2];
-#pragma unroll
-          for (int i = 0; i < W; i += 2) {
-            const float2 e = make_float2(ex2(s[i]), ex2(s[i + 1]));
-            l2[(w0 + i) / 2] = __ffma2_rn(e, iv2, l2[(w0 + i) / 2]);
-            const __half2 hh = __floats2half2_rn(e.x, e.y);
-            h[i / 2] = *reinterpret_cast<const uint32_t*>(&hh);
-          }
-#pragma unroll
-          for (int k = 0; k < W / 8; ++k) {
-            const int piece = (col0 + w0) / 8 + k;
-            uint8_t* row = pt + (piece / 8) * (AT_CHUNK * 128) + in * RB;
-            *reinterpret_cast<uint4*>(row + (((piece % 8) ^ f) << 4)) =
-                make_uint4(h[4 * k], h[4 * k + 1], h[4 * k + 2], h[4 * k + 3]);
-          }
-        }
-        force = lacks;
+        };
+        if (force) raise();
+        weights(false);
         fence_async_smem();
+        // Mostly no score is far above its reference and no page is missing.
+        force = false;
+        const bool lacks = c + 1 < x.cn && __any_sync(FULL_MASK, lane < (AT_CHUNK >> part_log2) && !s_sc[slot][lane & 7].ok);
+        if (bar_or<128>(3 + (warp >> 2), top > RAISE || lacks)) {
+          const bool up = bar_or<128>(3 + (warp >> 2), top > RAISE);
+          force = bar_or<128>(3 + (warp >> 2), lacks);  // rows' maxima may not be known yet
+          if (up) {
+            raise();
+            weights(true);
+            fence_async_smem();
+          }
+        }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&pready[pb]);
+        if (lane == 0) {
+          mbar_arrive(&sfree[b]);
+          mbar_arrive(&pready[pb]);
+        }
       }
 
       // ---- the piece's sums, and its outputs or part
@@ -777,30 +814,31 @@ __global__ void __launch_bounds__(AttnShape<D, N>::THREADS, 1)
         if (W == 16) l[0] += __shfl_xor_sync(FULL_MASK, l[0], 16);
         if (lane < W) s_red[quarter][col0 + w0 + lane] = l[0];
       }
-      sync_soft();
+      sync_group();
       const int d = in;  // this thread's column of the head dimension
       const bool mine = d < D;
       float* part = p.part + (int64_t(blockIdx.x) * 2 + (first_piece ? 0 : 1)) * N * (D + 2);
-      if (tid < N) {
-        const float m = any_chunk ? s_raw[tid] : -INFINITY;
-        const float sum = any_chunk ? (s_red[0][tid] + s_red[1][tid]) + (s_red[2][tid] + s_red[3][tid]) : 0.f;
+      if (gt < COLS) {
+        const int r = col0 + gt;
+        const float m = any_chunk ? s_raw[r] : -INFINITY;
+        const float sum = any_chunk ? (s_red[0][r] + s_red[1][r]) + (s_red[2][r] + s_red[3][r]) : 0.f;
         if (x.whole) {
-          s_fac[tid] = sum == 0.f ? 0.f : 1.f / sum;  // no token seen: 0
-          if (p.lse && tid < rows) {
-            const int i = (row0 + tid) / p.group;
-            p.lse[(sq.q0 + i) * p.q_heads + x.h * p.group + (row0 + tid - i * p.group)] =
+          s_fac[r] = sum == 0.f ? 0.f : 1.f / sum;  // no token seen: 0
+          if (p.lse && r < rows) {
+            const int i = (row0 + r) / p.group;
+            p.lse[(sq.q0 + i) * p.q_heads + x.h * p.group + (row0 + r - i * p.group)] =
                 sum == 0.f ? -INFINITY : (m + log2f(sum)) * LN2_F;
           }
         } else {
-          part[N * D + tid] = m;
-          part[N * D + N + tid] = sum;
+          part[N * D + r] = m;
+          part[N * D + N + r] = sum;
         }
       }
       int nan_row = N;  // rows from here on see a NaN in this column
       if (any_chunk) {
         wait_warp(&pvdone[(it - 1) & 1], ((it - 1) >> 1) & 1, ERR_KV8_PV_WAIT);
         tc_fence_after();
-        if (s_nan[pi % PIECE_RING] && mine) {
+        if (s_nan[pi % PIECE_RING][warp >> 2] && mine) {
           const int edge = sq.len - sq.n;
           const int from = max(x.c0, max(edge, 0) / AT_CHUNK) * AT_CHUNK, to = min(x.end, x.cn * AT_CHUNK);
           for (int t = from; t < to; ++t) {
@@ -814,8 +852,8 @@ __global__ void __launch_bounds__(AttnShape<D, N>::THREADS, 1)
           }
         }
       }
-      sync_soft();
-      if (any_chunk && tid == 0) s_nan[pi % PIECE_RING] = 0;
+      sync_group();
+      if (any_chunk && gt == 0) s_nan[pi % PIECE_RING][warp >> 2] = 0;
       int i = (row0 + col0) / p.group, j = row0 + col0 - i * p.group;  // new token and head of a row
 #pragma unroll 1
       for (int r0 = col0; r0 < min(rows, col0 + COLS); r0 += 16) {
@@ -840,7 +878,7 @@ __global__ void __launch_bounds__(AttnShape<D, N>::THREADS, 1)
         }
       }
       tc_fence_before();
-      sync_soft();  // s_red and s_fac are read
+      sync_group();  // s_red and s_fac are read
       if (any_chunk) ++pi;
     }
   }
@@ -961,6 +999,10 @@ int tile_rows(int max_new, int group) {
   return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
 }
 
+int attn_grid(int n) {
+  return device_sm_count() * (n == 16 ? AttnShape<128, 16>::CTAS : 1);
+}
+
 template <int D, int N>
 cudaError_t launch(const CUtensorMap& tm, const AttnParams& prm, int grid, cudaStream_t stream) {
   constexpr int smem = AttnShape<D, N>::SMEM;
@@ -978,7 +1020,8 @@ cudaError_t launch(const CUtensorMap& tm, const AttnParams& prm, int grid, cudaS
 }  // namespace
 
 size_t kv8_attention_workspace(int max_new, int group, int D) {
-  return size_t(device_sm_count()) * 2 * tile_rows(max_new, group) * (D + 2) * sizeof(float);
+  const int n = tile_rows(max_new, group);
+  return size_t(attn_grid(n)) * 2 * n * (D + 2) * sizeof(float);
 }
 
 cudaError_t kv8_attention_launch(const Kv8Attention& a, cudaStream_t stream) {
@@ -1010,7 +1053,7 @@ cudaError_t kv8_attention_launch(const Kv8Attention& a, cudaStream_t stream) {
   prm.out = a.out;
   prm.lse = a.lse;
   prm.part = static_cast<float*>(a.workspace);
-  const int grid = device_sm_count(), n = tile_rows(a.max_new, a.group);
+  const int n = tile_rows(a.max_new, a.group), grid = attn_grid(n);
 #define LC_N(DD)                                                            \
   (n == 16 ? launch<DD, 16>(tm, prm, grid, stream)                          \
            : n == 32 ? launch<DD, 32>(tm, prm, grid, stream)                \
