@@ -3,34 +3,41 @@
 // For new token i of a sequence's n, and query head j of the group that shares a key / value
 // head:  o = softmax_t(scale q . k_t) v_t  over the cached tokens t < len - n + i + 1.
 //
-// The n * group rows of a (sequence, key / value head) are taken in tiles of N (16, 32, 64 or
-// 128) rows; a work unit is one tile against one chunk of 128 cached tokens.  The units of a
-// call, laid out by (sequence, head, tile, chunk), are dealt in equal contiguous runs to one
-// CTA per SM, so that ragged lengths, and few rows over a long axis, load the SMs alike.  A CTA
-// that holds a part of a tile's chunks leaves its maxima, sums and products in the workspace,
-// and a second kernel joins the parts in order: no atomics, the same bits every time.
+// The n * group rows of a (sequence, key / value head) are taken in tiles of 32 or 128 rows; a
+// work unit is one tile against one chunk of 128 cached tokens.  The units of a call, laid out
+// by (sequence, head, tile, chunk), are dealt in equal contiguous runs to one CTA per SM, so
+// that ragged lengths, and few rows over a long axis, load the SMs alike.  A CTA that holds a
+// part of a tile's chunks leaves its maxima, sums and products in the workspace, and a second
+// kernel joins the parts in order: no atomics, the same bits every time.
 //
-// A single token's few rows would leave most of a tensor-core tile empty if the rows were its M,
-// so the products are turned round, with the tokens, and the head dimension, as the 128 rows:
-//     S'[128 tokens, N] = K Q^T         kind::f8f6f4: K as it lies in the cache, q as the sum of
-//                                       two e4m3 values (two products into one accumulator)
-//     O'[D, N]         += V^T P'        kind::f16: V widened from e4m3 (exact), P' in f16
-// One warp brings chunks (K through a swizzled tensor map, V by plain bulk copies) into a ring
-// of stages, one issues the products, four widen V (and split the tile's q), four take the
-// softmax: a thread holds one token's N scores.  The two scores' and the two V buffers let
-// K Q^T and the widening of chunk c + 1 run under the softmax of chunk c.
+// Per chunk, on the tensor cores, rows = the tile's (up to 128) query rows:
+//     S[rows, 128 tokens] = Q K^T    kind::f8f6f4: K as it lies in the cache, q as the sum of
+//                                    two e4m3 values (two products into one accumulator)
+//     O[rows, D]         += P V      kind::f16: P from tensor memory, V widened from e4m3 (exact)
+// Warps: one deals out the pieces of the CTA's run and brings their chunks (K through a swizzled
+// tensor map, V by plain bulk copies) into a ring of stages; one issues the S products and one
+// the O products (a thread takes some 80 cycles to issue one, so each kind has its own); four
+// widen V and split the tile's q; and two groups take the softmax, a thread a row.  The groups
+// take turns at the chunks, each with its own S, its own running maximum and sums and its own O
+// in tensor memory, so that neither waits for the other; the two are put together at the
+// tile's end.  A group has four warps for 128 rows, one for 32 (a warp reaches the 32 lanes of
+// tensor memory of its place among four).
 //
-// The softmax keeps one reference m per row, the maximum of the tile's first chunk, and raises
-// it only where a score passes it by more than 2^8: p' is then at most 256, far inside f16, and
-// the accumulated O' is scaled in tensor memory only then, by the threads that own its lanes.
-// The page's key scale multiplies the scores; the logarithm of its value scale is added to
-// them, so that p' = scale_v exp(s - m) is what the second product takes and the sums take
+// A row's maximum m moves only where a score passes it by more than 2^14: weights are then at
+// most 2^14, inside f16, and O is scaled in tensor memory only then, by the warp that owns its
+// lanes.  Weights are formed with the old m and thrown away in that case, while S still
+// stands.  The page's key scale multiplies the scores; the logarithm of its value scale is added
+// to them, so that p' = scale_v exp(s - m) is what the second product takes, and the sums take
 // p' / scale_v.
 //
 // Roundings below f32: q (bf16) is moved by a power of two of its row to at most 256 and split
 // into hi + lo, exactly but for values 2^-9 below the row's largest, which are off by at most
-// 2^-17 of it; p' is rounded to f16 (2^-11 of its value, 2^-25 of the row's reference weight
-// below 2^-14); out is rounded to bf16.
+// 2^-17 of it; p' is rounded to f16 (2^-11 of its value, 2^-25 of the weight of m below 2^-14);
+// out is rounded to bf16.
+//
+// The roles' loops share the SM's instruction cache: their code is kept small (waits that do
+// not end at once are out of line, one warp works out the pieces for all), which measured a
+// factor of two.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -125,32 +132,17 @@ __device__ __forceinline__ Run find_run(const AttnParams& p, int64_t run, int ru
   return r;
 }
 
-// The pieces of a run: the chunks [c0, c1) of one tile each, of which [c0, cn) are seen by some
-// row of it.
+// A piece of a run: the chunks [c0, c1) of one tile, of which [c0, cn) are seen by some row of
+// it.  The loading warp works the pieces out and leaves them in a ring for the others.
 struct Piece {
-  SeqUnits sq;
-  int64_t b, first;  // the sequence, and its first unit
-  int h, tile, c0, c1, cn;
-  int end;           // tokens that the tile's last row sees
-  bool whole;        // all of the tile's chunks
+  int64_t q0;         // the sequence's first row of q
+  int64_t table;      // its row of the block table, as an offset
+  int n, len;         // its new tokens and its cached ones
+  int h, row0, rows;  // key / value head; the tile's first row and its rows
+  int c0, cn, end;    // tokens that the tile's last row sees
+  int whole;          // 1: all of the tile's chunks; 0: a part; -1: there is no further piece
+  int slot;           // of the workspace, for a part
 };
-template <int N>
-__device__ __forceinline__ void piece_at(const AttnParams& p, int64_t u, int64_t u_end, Piece& x) {
-  while (u >= x.first + x.sq.units) {
-    x.first += x.sq.units;
-    x.sq = seq_units<N>(p, ++x.b);
-  }
-  const uint32_t in = static_cast<uint32_t>(u - x.first);  // a sequence's units fit 32 bits (host)
-  const uint32_t item = in / x.sq.chunks;
-  x.c0 = static_cast<int>(in - item * x.sq.chunks);
-  x.c1 = static_cast<int>(min(int64_t(x.sq.chunks), x.c0 + (u_end - u)));
-  x.h = item / x.sq.tiles;
-  x.tile = item - x.h * x.sq.tiles;
-  const int last = min((x.tile + 1) * N, x.sq.n * p.group) - 1;
-  x.end = max(0, min(x.sq.len, x.sq.len - x.sq.n + last / p.group + 1));
-  x.cn = max(x.c0, min(x.c1, (x.end + AT_CHUNK - 1) / AT_CHUNK));
-  x.whole = x.c0 == 0 && x.c1 == x.sq.chunks;
-}
 
 // ------------------------------------------------------------------- tensor-core plumbing
 
@@ -184,11 +176,12 @@ __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint3
       "l"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u)
       : "memory");
 }
-__device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+// A from tensor memory (packed f16 pairs, one row a lane), B from shared memory.
+__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u)
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u)
       : "memory");
 }
 __device__ __forceinline__ void tmem_ld16(uint32_t t, float* v) {
@@ -220,11 +213,6 @@ __device__ __forceinline__ void tmem_ld32(uint32_t t, float* v) {
 #pragma unroll
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
-template <int W>
-__device__ __forceinline__ void tmem_ld(uint32_t t, float* v) {
-  if constexpr (W == 16) tmem_ld16(t, v);
-  else tmem_ld32(t, v);
-}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -239,17 +227,16 @@ __device__ __forceinline__ void tmem_st16(uint32_t t, const float* v) {
       : "memory");
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
-// OR of a flag over the THREADS threads of named barrier `id`.
-template <int THREADS>
-__device__ __forceinline__ bool bar_or(int id, bool flag) {
-  uint32_t r;
+__device__ __forceinline__ void tmem_st32(uint32_t t, const uint32_t* v) {
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %2, 0;\n\t"
-      "barrier.cta.red.or.pred p, %1, %3, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(r)
-      : "r"(id), "r"(flag ? 1u : 0u), "n"(THREADS)
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(t),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]),
+      "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]),
+      "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
       : "memory");
-  return r != 0;
 }
 
 // Shared-memory tiles of rows of 32, 64 or 128 bytes (wider ones are several tiles of 128), in
@@ -260,8 +247,7 @@ __device__ __forceinline__ int swz(int r) {
   return BYTES == 128 ? r & 7 : BYTES == 64 ? (r >> 1) & 3 : (r >> 2) & 1;
 }
 // Its matrix descriptor.  Row groups are 8 * BYTES apart; `next` is the distance to the next
-// tile of an operand whose rows are the summed index (0: the same tile again, for rows of the
-// product that nothing reads).
+// tile of an operand whose rows are the summed index.
 template <int BYTES>
 __device__ __forceinline__ uint64_t tile_desc(const void* p, uint32_t next) {
   constexpr uint64_t MODE = BYTES == 128 ? 2 : BYTES == 64 ? 4 : 6;
@@ -281,34 +267,46 @@ __device__ __forceinline__ uint32_t nan_codes(uint32_t w) {  // 0xff in each byt
 
 // --------------------------------------------------------------------------- the kernel
 
-template <int D, int N>
+template <int D, int ROWS>
 struct AttnShape {
-  static constexpr int CTAS = N == 16 ? 2 : 1;         // per SM
-  static constexpr int KT = AT_CHUNK * D;              // bytes of a chunk's keys, or values
-  static constexpr int STAGES = CTAS == 2 ? 2 : D < 128 ? 4 : N == 128 ? 2 : 3;
-  static constexpr int VW = 2 * KT;                    // widened values
-  static constexpr int VB = CTAS == 2 ? 1 : 2;         // buffers of them
-  static constexpr int PB = CTAS == 2 || N == 128 ? 1 : 2;  // buffers of p'
-  static constexpr int PT = AT_CHUNK * N * 2;
-  static constexpr int QB = N == 32 ? 2 : 1;           // buffers of q hi, lo
-  static constexpr int QT = N * D;                     // bytes of one of the two
+  static constexpr int KT = AT_CHUNK * D;               // bytes of a chunk's keys, or values
+  static constexpr int STAGES = D < 128 || ROWS == 32 ? 4 : 3;
+  static constexpr int VW = 2 * KT;                     // widened values; two buffers
+  static constexpr int QB = ROWS == 32 ? 2 : 1;         // buffers of q
+  static constexpr int QT = ROWS * D;                   // bytes of q hi, or lo
   static constexpr int OFF_V = STAGES * 2 * KT;
-  static constexpr int OFF_P = OFF_V + VB * VW;
-  static constexpr int OFF_Q = OFF_P + PB * PT;
-  static constexpr int SMEM = 1024 + OFF_Q + QB * 2 * QT;
-  static constexpr int TMEM = N == 16 ? 64 : 4 * N;    // two S' and one O' of N columns
-  // Softmax warps: a warp can read the 32 lanes (tokens) of tensor memory of its place among
-  // four; with 64 rows and more, two warps share the columns (rows) of each 32 tokens.
-  static constexpr int GROUPS = N >= 64 ? 2 : 1, SOFT = 4 * GROUPS, COLS = N / GROUPS;
-  // then four that widen V, and one each for loads, S' and O'
-  static constexpr int LOAD_WARP = SOFT + 4, S_WARP = SOFT + 5, O_WARP = SOFT + 6;
-  static constexpr int THREADS = 32 * (SOFT + 7);
+  static constexpr int OFF_Q = OFF_V + 2 * VW;
+  // a product reads 128 rows of q, whatever lies behind a tile of 32
+  static constexpr int SMEM = 1024 + OFF_Q + QB * 2 * QT + (128 - ROWS) * D;
+  static constexpr int QUARTERS = ROWS / 32;            // softmax warps of a group
+  static constexpr int WARPS = 2 * QUARTERS + 7;
+  static constexpr int CONSUMERS = WARPS - 1;           // warps that read the pieces
 };
+constexpr int TMEM_COLS = 512, TMEM_S = 128, TMEM_O = 256;  // S of chunk i at 128 (i % 2), O at 256 + 128 (i % 2)
 
-constexpr int AT_CONV = 4;                  // warps that widen V
+enum Role : int { SOFT0, SOFT1, CONV, LOAD, S_MMA, O_MMA };
+// Role of a warp and its number within it.  Softmax warps sit where their quarter of the lanes
+// is (warp % 4): 0..3 and 4..7 for 128 rows, 0 and 4 for 32.
+template <int ROWS>
+__device__ __forceinline__ Role role_of(int warp, int& k) {
+  if (ROWS == 128) {
+    k = warp & 3;
+    if (warp < 8) return warp < 4 ? SOFT0 : SOFT1;
+    if (warp < 12) return CONV;
+    return static_cast<Role>(LOAD + warp - 12);
+  }
+  k = 0;
+  if (warp == 0) return SOFT0;
+  if (warp == 4) return SOFT1;
+  if (warp < 6) {
+    k = warp < 4 ? warp - 1 : 3;
+    return CONV;
+  }
+  return static_cast<Role>(LOAD + warp - 6);
+}
+
 constexpr int SC_RING = 8, PIECE_RING = 4;  // deeper than any warp runs ahead of the softmax
 constexpr float RAISE = 14.f;               // log2 of how far a score may pass its reference
-constexpr float ANEW = 0x1p-100f;
 
 struct PageScale {  // of the tokens of one page
   float k, log2_v, inv_v;
@@ -316,8 +314,7 @@ struct PageScale {  // of the tokens of one page
 };
 
 // The rest of a wait that did not end at once, at most WAIT_LIMIT_CYCLES.  The first one of a CTA
-// that gives up makes every later one give up soon.  (Out of line: the roles' loops share the
-// SM's instruction cache, and measured half as fast when their code did not fit it.)
+// that gives up makes every later one give up soon, and the roles' loops end.
 __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, uint32_t site, volatile int* fail) {
   const long long t0 = clock64();
   for (uint32_t i = 1;; ++i) {
@@ -330,111 +327,140 @@ __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, uint32_t 
   }
 }
 
-template <int D, int N>
-__global__ void __launch_bounds__(AttnShape<D, N>::THREADS, AttnShape<D, N>::CTAS)
+template <int D, int ROWS>
+__global__ void __launch_bounds__(32 * AttnShape<D, ROWS>::WARPS, 1)
     kv8_attention_kernel(const __grid_constant__ CUtensorMap tm, const AttnParams p) {
-  using S = AttnShape<D, N>;
-  constexpr int ST = S::STAGES, VB = S::VB, PB = S::PB, QB = S::QB;
-  constexpr int COLS = S::COLS, W = COLS < 32 ? 16 : 32;  // columns of a softmax thread, and of them at a time
+  using S = AttnShape<D, ROWS>;
+  constexpr int ST = S::STAGES, QB = S::QB, NQ = S::QUARTERS;
   extern __shared__ uint8_t at_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(at_raw) + 1023) & ~uintptr_t(1023));
-  __shared__ __align__(8) uint64_t full[ST], empty[ST], sready[2], sfree[2], vready[VB], pready[PB],
-      pvdone[2], qready[QB], qfree[QB], frready[PIECE_RING];
+  __shared__ __align__(8) uint64_t full[ST], empty[ST], sready[2], vready[2], pready[2], pvdone[2],
+      qready[QB], qfree[QB], pc_full[PIECE_RING], pc_empty[PIECE_RING], met[NQ], left[NQ];
+  __shared__ Piece s_piece[PIECE_RING];
   __shared__ PageScale s_sc[SC_RING][8];
-  __shared__ __align__(16) float s_fr[PIECE_RING][N], s_nref[N];
-  __shared__ float s_raw[N], s_fac[N], s_red[4][N];
-  __shared__ int s_nan[PIECE_RING][2];  // a NaN was taken out of V, for either group
+  __shared__ float s_fr[PIECE_RING][ROWS], s_m[2][ROWS], s_l[2][ROWS];
+  __shared__ int s_nan[PIECE_RING];  // a NaN was taken out of V
   __shared__ uint32_t s_tmem;
-  __shared__ Run s_run;
   __shared__ volatile int s_fail;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  int k;
+  const Role role = role_of<ROWS>(warp, k);
   if (tid == 0) {
-    for (int i = 0; i < ST; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1 + AT_CONV); }
+    for (int i = 0; i < ST; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1 + 4); }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sready[i], 1);
-      mbar_init(&sfree[i], S::SOFT);
+      mbar_init(&vready[i], 4);
+      mbar_init(&pready[i], NQ);
       mbar_init(&pvdone[i], 1);
     }
-    for (int i = 0; i < VB; ++i) mbar_init(&vready[i], AT_CONV);
-    for (int i = 0; i < PB; ++i) mbar_init(&pready[i], S::SOFT);
-    for (int i = 0; i < QB; ++i) { mbar_init(&qready[i], AT_CONV); mbar_init(&qfree[i], 1); }
-    for (int i = 0; i < PIECE_RING; ++i) { mbar_init(&frready[i], AT_CONV); s_nan[i][0] = s_nan[i][1] = 0; }
+    for (int i = 0; i < QB; ++i) { mbar_init(&qready[i], 4); mbar_init(&qfree[i], 1); }
+    for (int i = 0; i < PIECE_RING; ++i) {
+      mbar_init(&pc_full[i], 1);
+      mbar_init(&pc_empty[i], S::CONSUMERS);
+      s_nan[i] = 0;
+    }
+    for (int i = 0; i < NQ; ++i) { mbar_init(&met[i], 2); mbar_init(&left[i], 2); }
     fence_mbar_init();
     s_fail = 0;
   }
   if (warp == 0) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_addr(&s_tmem)),
-                 "r"(S::TMEM)
+                 "r"(TMEM_COLS)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-  }
-  pdl_wait();
-  pdl_trigger();
-  if (warp == 1) {
-    const Run r = find_run<N>(p, blockIdx.x, gridDim.x);
-    if (lane == 0) s_run = r;
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = s_tmem;  // S' of even and odd chunks, O'
-  const uint32_t t_o = tmem + 2 * N;
-  const Run run = s_run;
-  Piece x;
-  x.b = run.b;
-  x.first = run.first;
-  if (run.u < run.u_end) x.sq = seq_units<N>(p, run.b);
+  const uint32_t tmem = s_tmem;
+  pdl_wait();
+  pdl_trigger();
 
-  // Every wait is bounded, and the first that gives up makes every later one of the CTA give up
-  // at once, so that all warps still run through their loops and meet at their barriers.
   auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t site) -> bool {
     return mbar_try_wait(bar, parity) || wait_slow(bar, parity, site, &s_fail);
   };
-  // ... by all lanes of a warp, which go on together.
-  auto wait_warp = [&](uint64_t* bar, uint32_t parity, uint32_t site) {
-    const bool ok = wait(bar, parity, site);
-    __syncwarp();
-    return ok;
+  auto wait_warp = [&](uint64_t* bar, uint32_t parity, uint32_t site) -> bool {
+    return __all_sync(FULL_MASK, wait(bar, parity, site));
   };
+  // The next piece, read by a warp (lanes: all, or one of a warp whose others do nothing).
+  auto next_piece = [&](int pi, Piece& x) -> bool {
+    const int e = pi % PIECE_RING;
+    if (!wait(&pc_full[e], (pi / PIECE_RING) & 1, ERR_KV8_FULL_WAIT)) return false;
+    x = s_piece[e];
+    return x.whole >= 0;
+  };
+  auto piece_read = [&](int pi) { mbar_arrive(&pc_empty[pi % PIECE_RING]); };
 
-  if (warp == S::LOAD_WARP) {
-    // ================= loads: lane i brings the i-th page (part) of a chunk =================
-    const int part = min(p.c.page, AT_CHUNK), parts = AT_CHUNK >> min(p.page_log2, 7);
-    const int bytes = part * D;
-    int it = 0;
+  if (role == LOAD) {
+    // ====== the run's pieces, and their chunks: lane i brings the i-th page of a chunk ======
+    const Run run = find_run<ROWS>(p, blockIdx.x, gridDim.x);
+    const int part = p.c.page, parts = AT_CHUNK >> p.page_log2, bytes = part * D;
+    int64_t b = run.b, u = run.u;
+    SeqUnits sq{};
+    int tile = 0, h = 0, c0 = 0;
+    if (u < run.u_end) {
+      sq = seq_units<ROWS>(p, b);
+      const uint32_t in = static_cast<uint32_t>(u - run.first);  // a sequence's units fit 32 bits (host)
+      const uint32_t item = in / sq.chunks;
+      c0 = static_cast<int>(in - item * sq.chunks);
+      h = item / sq.tiles;
+      tile = item - h * sq.tiles;
+    }
+    int it = 0, pi = 0;
     bool ok_run = true;
-    for (int64_t u = run.u; u < run.u_end && ok_run; u += x.c1 - x.c0) {
-      piece_at<N>(p, u, run.u_end, x);
-      const int32_t* tab = p.table + x.b * p.table_stride;
+    while (ok_run) {
+      const int e = pi % PIECE_RING;
+      if (pi >= PIECE_RING) ok_run = wait_warp(&pc_empty[e], ((pi / PIECE_RING) - 1) & 1, ERR_KV8_EMPTY_WAIT);
+      if (!ok_run || u >= run.u_end) {
+        if (lane == 0) s_piece[e].whole = -1;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&pc_full[e]);
+        break;
+      }
+      while (sq.units == 0) sq = seq_units<ROWS>(p, ++b);  // sequences without new tokens
+      const int c1 = static_cast<int>(min(int64_t(sq.chunks), c0 + (run.u_end - u)));
+      const int rows = min(ROWS, sq.n * p.group - tile * ROWS);
+      const int end = max(0, min(sq.len, sq.len - sq.n + (tile * ROWS + rows - 1) / p.group + 1));
+      const int cn = max(c0, min(c1, (end + AT_CHUNK - 1) / AT_CHUNK));
+      const int64_t table = b * p.table_stride;
+      if (lane == 0)
+        s_piece[e] = Piece{sq.q0, table, sq.n, sq.len, h, tile * ROWS, rows, c0, cn, end,
+                           c0 == 0 && c1 == sq.chunks ? 1 : 0, 2 * static_cast<int>(blockIdx.x) + (pi > 0)};
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&pc_full[e]);
+      ++pi;
+
+      const int32_t* tab = p.table + table;
       auto page_of = [&](int c) {
         const int tok = c * AT_CHUNK + lane * part;
-        return lane < parts && tok < x.end ? __ldg(tab + (tok >> p.page_log2)) : -2;
+        return lane < parts && c < cn && tok < end ? __ldg(tab + (tok >> p.page_log2)) : -2;
       };
-      // page indices are read two chunks ahead, scales one
       auto exists = [&](int i) { return i >= 0 && i < p.c.n_pages; };
+      // page indices are read two chunks ahead, scales one
       float ks1 = 0.f, vs1 = 1.f;
       auto read_scales = [&](int i) {
         if (!exists(i)) return;
-        const int64_t ph = int64_t(i) * p.c.heads + x.h;
+        const int64_t ph = int64_t(i) * p.c.heads + h;
         ks1 = __ldg(p.c.ks + ph);
         vs1 = __ldg(p.c.vs + ph);
       };
-      int id1 = x.c0 < x.cn ? page_of(x.c0) : -2, id2 = x.c0 + 1 < x.cn ? page_of(x.c0 + 1) : -2;
+      int id1 = page_of(c0), id2 = page_of(c0 + 1);
       read_scales(id1);
-      for (int c = x.c0; c < x.cn; ++c, ++it) {
+#pragma unroll 1
+      for (int c = c0; c < cn; ++c, ++it) {
         const int st = it % ST, slot = it % SC_RING;
         const int id = id1;
         const float ks = ks1, vs = vs1;
         id1 = id2;
         read_scales(id1);
-        id2 = c + 2 < x.cn ? page_of(c + 2) : -2;
+        id2 = page_of(c + 2);
         const bool ok = exists(id);
         if (id != -2 && !ok) atomicOr(&g_err_kv8_attn, ERR_KV8_PAGE);
-        const int64_t ph = int64_t(ok ? id : 0) * p.c.heads + x.h;
+        const int64_t ph = int64_t(ok ? id : 0) * p.c.heads + h;
         const unsigned have = __ballot_sync(FULL_MASK, ok);
-        if (it >= ST && !__all_sync(FULL_MASK, wait_warp(&empty[st], ((it / ST) - 1) & 1, ERR_KV8_EMPTY_WAIT))) {
+        if (it >= ST && !wait_warp(&empty[st], ((it / ST) - 1) & 1, ERR_KV8_EMPTY_WAIT)) {
           ok_run = false;
           break;
         }
@@ -449,161 +475,166 @@ __global__ void __launch_bounds__(AttnShape<D, N>::THREADS, AttnShape<D, N>::CTA
           bulk_g2s(dst + S::KT, p.c.v + ph * bytes, bytes, &full[st]);
         }
       }
+      // on to the next tile
+      u += c1 - c0;
+      c0 = c1;
+      if (c0 == sq.chunks) {
+        c0 = 0;
+        if (++tile == sq.tiles) {
+          tile = 0;
+          if (++h == p.c.heads) {
+            h = 0;
+            if (u < run.u_end) sq = seq_units<ROWS>(p, ++b);
+          }
+        }
+      }
     }
     if (!ok_run || s_fail)  // what is in flight has to land
       for (int i = max(0, it - ST); i < it; ++i)
         mbar_wait_bounded(&full[i % ST], (i / ST) & 1, &g_err_kv8_attn, ERR_KV8_EMPTY_WAIT);
-  } else if (warp == S::S_WARP) {
-    // ================= S' = K Q^T, hi and lo =================
-    // (a thread takes 80 cycles or so to issue a product, so the two kinds have one each)
+  } else if (role == S_MMA) {
+    // ================= S = Q K^T, hi and lo =================
     if (lane == 0) {
-      constexpr uint32_t ID = tc_idesc(128, N, false, false);
+      constexpr uint32_t ID = tc_idesc(128, AT_CHUNK, false, false);
       const uint64_t d_k = tile_desc<D>(sm, 16), d_q = tile_desc<D>(sm + S::OFF_Q, 16);
-      int it = 0, pi = 0;
-      for (int64_t u = run.u; u < run.u_end; u += x.c1 - x.c0) {
-        piece_at<N>(p, u, run.u_end, x);
+      int it = 0, qi = 0;
+      Piece x;
+      for (int pi = 0; next_piece(pi, x); ++pi) {
+        piece_read(pi);
         if (x.c0 >= x.cn) continue;
-        bool ok = wait(&qready[pi % QB], (pi / QB) & 1, ERR_KV8_S_WAIT);
+        bool ok = wait(&qready[qi % QB], (qi / QB) & 1, ERR_KV8_S_WAIT);
+        const uint64_t q = d_q + ((qi % QB) * 2 * S::QT >> 4);
+#pragma unroll 1
         for (int c = x.c0; c < x.cn; ++c, ++it) {
           const int st = it % ST, b = it & 1;
           ok = wait(&full[st], (it / ST) & 1, ERR_KV8_FULL_WAIT) && ok;
-          if (it >= 2) ok = wait(&sfree[b], ((it >> 1) - 1) & 1, ERR_KV8_S_WAIT) && ok;
+          if (it >= 2) ok = wait(&pvdone[b], ((it >> 1) - 1) & 1, ERR_KV8_S_WAIT) && ok;
           if (ok) {
             tc_fence_after();
-            const uint64_t k = d_k + (st * 2 * S::KT >> 4);
-            const uint64_t q = d_q + ((pi % QB) * 2 * S::QT >> 4);
+            const uint64_t kk = d_k + (st * 2 * S::KT >> 4);
 #pragma unroll
-            for (int d = 0; d < D / 32; ++d) mma_f8(tmem + b * N, k + 2 * d, q + 2 * d, ID, d > 0);
+            for (int d = 0; d < D / 32; ++d) mma_f8(tmem + b * TMEM_S, q + 2 * d, kk + 2 * d, ID, d > 0);
 #pragma unroll
-            for (int d = 0; d < D / 32; ++d) mma_f8(tmem + b * N, k + 2 * d, q + (S::QT >> 4) + 2 * d, ID, true);
+            for (int d = 0; d < D / 32; ++d)
+              mma_f8(tmem + b * TMEM_S, q + (S::QT >> 4) + 2 * d, kk + 2 * d, ID, true);
           }
           tc_commit(&sready[b]);
           tc_commit(&empty[st]);
-          if (c + 1 == x.cn) tc_commit(&qfree[pi % QB]);
         }
-        ++pi;
+        tc_commit(&qfree[qi % QB]);
+        ++qi;
       }
     }
     __syncwarp();
-  } else if (warp == S::O_WARP) {
-    // ================= O' += V^T P' =================
+  } else if (role == O_MMA) {
+    // ================= O += P V =================
     if (lane == 0) {
-      constexpr uint32_t ID = tc_idesc(128, N, true, true);
-      constexpr int VBY = D < 64 ? 64 : 128, PBY = N < 64 ? 2 * N : 128;  // bytes of a tile's row
-      const uint64_t d_v = tile_desc<VBY>(sm + S::OFF_V, D == 128 ? AT_CHUNK * 128 : 0);
-      const uint64_t d_p = tile_desc<PBY>(sm + S::OFF_P, AT_CHUNK * 128);
+      constexpr uint32_t ID = tc_idesc(128, D, false, true);
+      constexpr int VBY = D < 64 ? 64 : 128;  // bytes of a row of a tile of V
+      const uint64_t d_v = tile_desc<VBY>(sm + S::OFF_V, AT_CHUNK * 128);
       int it = 0;
-      for (int64_t u = run.u; u < run.u_end; u += x.c1 - x.c0) {
-        piece_at<N>(p, u, run.u_end, x);
+      Piece x;
+      for (int pi = 0; next_piece(pi, x); ++pi) {
+        piece_read(pi);
+#pragma unroll 1
         for (int c = x.c0; c < x.cn; ++c, ++it) {
-          const int vb = it % VB, pb = it % PB;
-          bool ok = wait(&vready[vb], (it / VB) & 1, ERR_KV8_PV_WAIT);
-          ok = wait(&pready[pb], (it / PB) & 1, ERR_KV8_PV_WAIT) && ok;
+          const int b = it & 1;
+          bool ok = wait(&vready[b], (it >> 1) & 1, ERR_KV8_PV_WAIT);
+          ok = wait(&pready[b], (it >> 1) & 1, ERR_KV8_PV_WAIT) && ok;
           if (ok) {
             tc_fence_after();
-            const uint64_t v = d_v + (vb * S::VW >> 4), pp = d_p + (pb * S::PT >> 4);
-            // (16 tokens further: the address field, in units of 16 bytes, moves on)
+            const uint64_t v = d_v + (b * S::VW >> 4);
+            // (16 tokens further: 8 columns of P; the address field of V, in units of 16 bytes)
 #pragma unroll
-            for (int k = 0; k < AT_CHUNK / 16; ++k)
-              mma_f16(t_o, v + k * VBY, pp + k * PBY, ID, k > 0 || c != x.c0);
+            for (int i = 0; i < AT_CHUNK / 16; ++i)
+              mma_f16_ts(tmem + TMEM_O + b * 128, tmem + b * TMEM_S + 8 * i, v + i * VBY, ID, i > 0 || c - x.c0 >= 2);
           }
-          tc_commit(&pvdone[it & 1]);
+          tc_commit(&pvdone[b]);
         }
       }
     }
     __syncwarp();
-  } else if (warp >= S::SOFT) {
+  } else if (role == CONV) {
     // ================= widening of V, and the split of q =================
-    const int cw = warp - S::SOFT, ct = tid - 32 * S::SOFT;
-    int it = 0, pi = 0;
-    for (int64_t u = run.u; u < run.u_end; u += x.c1 - x.c0) {
-      piece_at<N>(p, u, run.u_end, x);
+    int it = 0, qi = 0;
+    Piece x;
+    for (int pi = 0; __all_sync(FULL_MASK, next_piece(pi, x)); ++pi) {
+      if (lane == 0) piece_read(pi);
       if (x.c0 >= x.cn) continue;
       {
-        constexpr int TPR = 128 / N, E = D / TPR;  // threads of a row, elements of a thread
-        if (pi >= QB) wait_warp(&qfree[pi % QB], ((pi / QB) - 1) & 1, ERR_KV8_S_WAIT);
-        const int r = ct / TPR, e0 = (ct % TPR) * E;
-        const int row = x.tile * N + r;
-        const bool has = row < x.sq.n * p.group;
-        const int i = has ? row / p.group : 0, j = has ? row - i * p.group : 0;
-        const __nv_bfloat16* qr = p.q + (x.sq.q0 + i) * p.q_tok + (x.h * p.group + j) * p.q_head + e0;
-        uint32_t top = 0;
-        // E elements in pieces of 4 (at least: D = 32 with 8 threads of a row)
+        constexpr int LPR = D / 4, RPW = 32 / LPR;  // lanes of a row (4 values each), rows of a warp at a time
+        if (qi >= QB) wait_warp(&qfree[qi % QB], ((qi / QB) - 1) & 1, ERR_KV8_S_WAIT);
+        uint8_t* qh = sm + S::OFF_Q + (qi % QB) * 2 * S::QT;
+        const int col = (lane % LPR) * 4;
+#pragma unroll 2
+        for (int r = k * RPW + lane / LPR; r < ((x.rows + 4 * RPW - 1) & ~(4 * RPW - 1)); r += 4 * RPW) {
+          const bool has = r < x.rows;
+          const int row = has ? x.row0 + r : 0, i = row / p.group;
+          const uint2 w = has ? __ldg(reinterpret_cast<const uint2*>(
+                                    p.q + (x.q0 + i) * p.q_tok + (x.h * p.group + row - i * p.group) * p.q_head + col))
+                              : make_uint2(0u, 0u);
+          uint32_t top = max(max(w.x & 0x7fffu, (w.x >> 16) & 0x7fffu), max(w.y & 0x7fffu, (w.y >> 16) & 0x7fffu));
 #pragma unroll
-        for (int e = 0; e < E; e += 4) {
-          const uint2 w = has ? __ldg(reinterpret_cast<const uint2*>(qr + e)) : make_uint2(0u, 0u);
-          top = max(max(top, w.x & 0x7fffu), (w.x >> 16) & 0x7fffu);
-          top = max(max(top, w.y & 0x7fffu), (w.y >> 16) & 0x7fffu);
-        }
-#pragma unroll
-        for (int o = TPR / 2; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(FULL_MASK, top, o));
-        // the largest moves to [128, 256)
-        const int ex = min(max(static_cast<int>(top >> 7), 1), 254) - 127;
-        const int sh = min(7 - ex, 120);
-        const float up = __uint_as_float(static_cast<uint32_t>(127 + sh) << 23);
-        if (e0 == 0)
-          s_fr[pi % PIECE_RING][r] = has ? p.scale2 * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23) : 0.f;
-        uint8_t* qh = sm + S::OFF_Q + (pi % QB) * 2 * S::QT + r * D;
-#pragma unroll
-        for (int e = 0; e < E; e += 4) {
-          const uint2 w = has ? __ldg(reinterpret_cast<const uint2*>(qr + e)) : make_uint2(0u, 0u);
+          for (int o = LPR / 2; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(FULL_MASK, top, o));
+          // the largest moves to [128, 256)
+          const int sh = min(7 - (min(max(static_cast<int>(top >> 7), 1), 254) - 127), 120);
+          const float up = __uint_as_float(static_cast<uint32_t>(127 + sh) << 23);
+          if (has && col == 0)
+            s_fr[qi % PIECE_RING][r] = p.scale2 * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
           const float y[4] = {__uint_as_float(w.x << 16) * up, __uint_as_float(w.x & 0xffff0000u) * up,
                               __uint_as_float(w.y << 16) * up, __uint_as_float(w.y & 0xffff0000u) * up};
           uint32_t hi = 0, lo = 0;
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const uint16_t h2 = f32x2_to_e4m3x2(y[2 * k], y[2 * k + 1]);
+          for (int n = 0; n < 2; ++n) {
+            const uint16_t h2 = f32x2_to_e4m3x2(y[2 * n], y[2 * n + 1]);
             const uint32_t b2 = e4m3x2_to_f16x2(h2);
             const float2 f2 = __half22float2(*reinterpret_cast<const __half2*>(&b2));
-            hi |= uint32_t(h2) << (16 * k);
+            hi |= uint32_t(h2) << (16 * n);
             // a row with an infinity keeps it as NaN: 448 would be a value like any other
-            const float l0 = y[2 * k] - f2.x, l1 = y[2 * k + 1] - f2.y;
-            lo |= uint32_t(f32x2_to_e4m3x2(isinf(l0) ? NAN : l0, isinf(l1) ? NAN : l1)) << (16 * k);
+            const float l0 = y[2 * n] - f2.x, l1 = y[2 * n + 1] - f2.y;
+            lo |= uint32_t(f32x2_to_e4m3x2(isinf(l0) ? NAN : l0, isinf(l1) ? NAN : l1)) << (16 * n);
           }
-          const int col = e0 + e;
-          const int at = (((col >> 4) ^ swz<D>(r)) << 4) | (col & 15);
-          *reinterpret_cast<uint32_t*>(qh + at) = hi;
-          *reinterpret_cast<uint32_t*>(qh + S::QT + at) = lo;
+          if (r < ROWS) {
+            const int at = r * D + ((((col >> 4) ^ swz<D>(r)) << 4) | (col & 15));
+            *reinterpret_cast<uint32_t*>(qh + at) = hi;
+            *reinterpret_cast<uint32_t*>(qh + S::QT + at) = lo;
+          }
         }
         fence_async_smem();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&qready[pi % QB]);
-          mbar_arrive(&frready[pi % PIECE_RING]);
-        }
+        if (lane == 0) mbar_arrive(&qready[qi % QB]);
       }
-      const int part_log2 = min(p.page_log2, 7);
+#pragma unroll 1
       for (int c = x.c0; c < x.cn; ++c, ++it) {
-        const int st = it % ST, b = it % VB, slot = it % SC_RING;
+        const int st = it % ST, b = it & 1, slot = it % SC_RING;
         wait_warp(&full[st], (it / ST) & 1, ERR_KV8_FULL_WAIT);
-        if (it >= VB) wait_warp(&pvdone[(it - VB) & 1], ((it - VB) >> 1) & 1, ERR_KV8_PV_WAIT);
+        if (it >= 2) wait_warp(&pvdone[b], ((it >> 1) - 1) & 1, ERR_KV8_PV_WAIT);
         const uint8_t* src = sm + st * 2 * S::KT + S::KT;
         uint8_t* dst = sm + S::OFF_V + b * S::VW;
         // Chunks with tokens that some row does not see (the causal edge), with rows behind the
         // last token or with pages that were not loaded: 0 * NaN is NaN, so there V takes part
         // without NaN, and rows that do see a NaN get it at the end.
-        bool edge = (c + 1) * AT_CHUNK > x.sq.len - x.sq.n;
-        edge |= __any_sync(FULL_MASK, lane < (AT_CHUNK >> part_log2) && !s_sc[slot][lane & 7].ok);
+        const bool edge = (c + 1) * AT_CHUNK > x.len - x.n ||
+                          __any_sync(FULL_MASK, lane < (AT_CHUNK >> p.page_log2) && !s_sc[slot][lane & 7].ok);
         constexpr int UPR = D / 16;                     // 16-byte pieces of a row
         constexpr int LPR = UPR < 4 ? UPR : 4;          // lanes on a row
         constexpr int TOKS = 32 / LPR;                  // rows of one round
-        bool nan = false;
         constexpr int RB = D < 64 ? 64 : 128;
-        constexpr int STEP = UPR < 4 ? UPR : 4;  // pieces of a lane in flight
+        constexpr int STEP = UPR < 4 ? UPR : 4;         // pieces of a lane in flight
+        bool nan = false;
 #pragma unroll 1
         for (int k0 = 0; k0 < UPR; k0 += STEP) {
           uint4 w[STEP];
           int tok[STEP];
 #pragma unroll
           for (int i = 0; i < STEP; ++i) {
-            const int k = k0 + i;
-            tok[i] = cw * 32 + (k % (32 / TOKS)) * TOKS + lane / LPR;
-            w[i] = *reinterpret_cast<const uint4*>(src + tok[i] * D + (lane % LPR + (k / (32 / TOKS)) * LPR) * 16);
+            tok[i] = k * 32 + ((k0 + i) % (32 / TOKS)) * TOKS + lane / LPR;
+            w[i] = *reinterpret_cast<const uint4*>(src + tok[i] * D + (lane % LPR + ((k0 + i) / (32 / TOKS)) * LPR) * 16);
           }
           if (edge) {
 #pragma unroll
             for (int i = 0; i < STEP; ++i) {
-              if (c * AT_CHUNK + tok[i] >= x.end || !s_sc[slot][tok[i] >> part_log2].ok) w[i] = make_uint4(0u, 0u, 0u, 0u);
+              if (c * AT_CHUNK + tok[i] >= x.end || !s_sc[slot][tok[i] >> p.page_log2].ok) w[i] = make_uint4(0u, 0u, 0u, 0u);
               const uint32_t n0 = nan_codes(w[i].x), n1 = nan_codes(w[i].y), n2 = nan_codes(w[i].z), n3 = nan_codes(w[i].w);
               nan |= (n0 | n1 | n2 | n3) != 0;
               w[i].x &= ~n0; w[i].y &= ~n1; w[i].z &= ~n2; w[i].w &= ~n3;
@@ -625,7 +656,7 @@ __global__ void __launch_bounds__(AttnShape<D, N>::THREADS, AttnShape<D, N>::CTA
             *reinterpret_cast<uint4*>(row + (((q0 + 1) ^ f) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
           }
         }
-        if (nan) s_nan[pi % PIECE_RING][0] = s_nan[pi % PIECE_RING][1] = 1;
+        if (nan) s_nan[qi % PIECE_RING] = 1;
         fence_async_smem();
         __syncwarp();
         if (lane == 0) {
@@ -633,260 +664,213 @@ __global__ void __launch_bounds__(AttnShape<D, N>::THREADS, AttnShape<D, N>::CTA
           mbar_arrive(&empty[st]);
         }
       }
-      ++pi;
+      ++qi;
     }
   } else {
-    // ================= softmax: thread = token of the chunk; then thread = column of D =======
-    const int quarter = warp & 3, col0 = (warp >> 2) * COLS;  // its tokens, its columns
-    const int in = quarter * 32 + lane;
-    const uint32_t t_lane = static_cast<uint32_t>(quarter * 32) << 16;
-    const int part_log2 = min(p.page_log2, 7);
-    const int gt = tid & 127;  // the thread's place in its group, which has its own rows and barriers
-    auto sync_group = [&]() { named_bar_sync(1 + (warp >> 2), 128); };
-    int it = 0, pi = 0;
-    bool first_piece = true;
-    for (int64_t u = run.u; u < run.u_end; u += x.c1 - x.c0, first_piece = false) {
-      piece_at<N>(p, u, run.u_end, x);
-      const SeqUnits& sq = x.sq;
-      const int row0 = x.tile * N, rows = min(N, sq.n * p.group - row0);
-      const bool any_chunk = x.c0 < x.cn;
-      float2 l2[COLS / 2];  // this thread's part of each row's sum
-#pragma unroll
-      for (int i = 0; i < COLS / 2; ++i) l2[i] = make_float2(0.f, 0.f);
-      if (any_chunk) wait_warp(&frready[pi % PIECE_RING], (pi / PIECE_RING) & 1, ERR_KV8_S_WAIT);
-      const float* fr = s_fr[pi % PIECE_RING] + col0;
-      const float* nref = s_nref + col0;
-      bool force = true;
-      for (int c = x.c0; c < x.cn; ++c, ++it) {
-        const int b = it & 1, slot = it % SC_RING, pb = it % PB;
-        wait_warp(&sready[b], (it >> 1) & 1, ERR_KV8_S_WAIT);
+    // ================= softmax: group g, rows 32 k + lane =================
+    const int g = role == SOFT0 ? 0 : 1, r = 32 * k + lane;
+    const uint32_t t_lane = static_cast<uint32_t>(32 * k) << 16;
+    const uint32_t t_s = tmem + t_lane + g * TMEM_S, t_o = tmem + t_lane + TMEM_O;
+    int it0 = 0, qi = 0;  // the piece's first chunk; pieces with chunks
+    Piece x;
+    for (int pi = 0; __all_sync(FULL_MASK, next_piece(pi, x)); ++pi) {
+      if (lane == 0) piece_read(pi);
+      const int chunks = x.cn - x.c0;
+      const bool has = r < x.rows;
+      const int i = has ? (x.row0 + r) / p.group : 0, j = has ? x.row0 + r - i * p.group : 0;
+      const int seen = x.len - x.n + i + 1;
+      float m = has && seen > 0 ? -INFINITY : 0.f, l = 0.f;  // a row that sees nothing needs no maximum
+#pragma unroll 1
+      for (int d = (it0 ^ g) & 1; d < chunks; d += 2) {
+        const int it = it0 + d, slot = it % SC_RING;
+        const int lim = has ? seen - (x.c0 + d) * AT_CHUNK : AT_CHUNK;  // tokens of the chunk that the row sees
+        wait_warp(&sready[g], (it >> 1) & 1, ERR_KV8_S_WAIT);
+        // the tile before may still be read from O, by the other group too
+        if (d < 2 && qi > 0) wait_warp(&left[k], (qi - 1) & 1, ERR_KV8_PV_WAIT);
         tc_fence_after();
-        const PageScale sc = s_sc[slot][in >> part_log2];
-        const float2 ks2 = make_float2(sc.k, sc.k), lv2 = make_float2(sc.log2_v, sc.log2_v);
-        const float2 iv2 = make_float2(sc.inv_v, sc.inv_v);
-        // rows below `hid` do not see this token
-        const int tok = c * AT_CHUNK + in, after = tok - (sq.len - sq.n);
-        const int hid = !sc.ok || tok >= sq.len ? N : after <= 0 ? 0 : min(N, max(0, after * p.group - row0));
-        const bool masks = __any_sync(FULL_MASK, hid > 0);
-        const uint32_t t_s = tmem + b * N + col0 + t_lane;
-        constexpr int RB = N < 64 ? 2 * N : 128;
-        uint8_t* pt = sm + S::OFF_P + pb * S::PT + in * RB;
-        const int f = swz<RB>(in);
-        bool free_p = it < PB;
-        float top;
-        // The weights of this thread's columns to shared memory and to the rows' sums; a second
-        // time, after a raise, only to the sums of rows that start anew.
-        auto weights = [&](bool again) {
-          top = -INFINITY;
+        const float fr = s_fr[qi % PIECE_RING][has ? r : 0];
+        const bool masks = __any_sync(FULL_MASK, lim < AT_CHUNK || (lane < (AT_CHUNK >> p.page_log2) && !s_sc[slot][lane & 7].ok));
+        // 16 scores from w0 on, in units of log2, with a reference or without
+        auto score16 = [&](int w0, float* s, const PageScale& sc, float nref) {
+          const float a = fr * sc.k, b = sc.log2_v + nref;
+          const float2 a2 = make_float2(a, a), b2 = make_float2(b, b);
 #pragma unroll
-          for (int w0 = 0; w0 < COLS; w0 += W) {
-            float s[W];
-            tmem_ld<W>(t_s + w0, s);
+          for (int n = 0; n < 16; n += 2) {
+            const float2 y = __ffma2_rn(make_float2(s[n], s[n + 1]), a2, b2);
+            s[n] = y.x;
+            s[n + 1] = y.y;
+          }
+          if (masks) {
+            const int see = sc.ok ? lim - w0 : 0;
 #pragma unroll
-            for (int i = 0; i < W; i += 4) {
-              const float4 g = *reinterpret_cast<const float4*>(fr + w0 + i);
-              const float4 n = *reinterpret_cast<const float4*>(nref + w0 + i);
-              const float2 a = __ffma2_rn(make_float2(s[i], s[i + 1]), __fmul2_rn(make_float2(g.x, g.y), ks2),
-                                          __fadd2_rn(make_float2(n.x, n.y), lv2));
-              const float2 d = __ffma2_rn(make_float2(s[i + 2], s[i + 3]), __fmul2_rn(make_float2(g.z, g.w), ks2),
-                                          __fadd2_rn(make_float2(n.z, n.w), lv2));
-              s[i] = a.x; s[i + 1] = a.y; s[i + 2] = d.x; s[i + 3] = d.y;
+            for (int n = 0; n < 16; ++n)
+              if (n >= see) s[n] = -INFINITY;
+          }
+        };
+        uint32_t h[AT_CHUNK / 2];  // the weights as f16 pairs
+        float sum;
+        bool anew = m == -INFINITY && lim > 0;  // (rows that are not there have m = 0)
+        for (;;) {
+          if (__any_sync(FULL_MASK, anew)) {
+            // new maxima, over this chunk and before; S stays as it is
+            float top = m;
+#pragma unroll 1
+            for (int w0 = 0; w0 < AT_CHUNK; w0 += 16) {
+              float s[16];
+              tmem_ld16(t_s + w0, s);
+              score16(w0, s, s_sc[slot][w0 >> p.page_log2], 0.f);
+#pragma unroll
+              for (int n = 0; n < 16; n += 2) top = max3(top, s[n], s[n + 1]);
             }
-            if (masks) {
+            const float f = top == -INFINITY ? 1.f : ex2(m - top);
+            m = top;
+            l *= f;
+            if (d >= 2) {  // (S of this chunk could only come after the group's last product)
+#pragma unroll 1
+              for (int w0 = 0; w0 < D; w0 += 16) {
+                float o[16];
+                tmem_ld16(t_o + g * 128 + w0, o);
 #pragma unroll
-              for (int i = 0; i < W; ++i)
-                if (col0 + w0 + i < hid) s[i] = -INFINITY;
-            }
-            if (!free_p) {
-              wait_warp(&pvdone[(it - PB) & 1], ((it - PB) >> 1) & 1, ERR_KV8_PV_WAIT);
-              free_p = true;
-            }
-#pragma unroll
-            for (int k = 0; k < W / 8; ++k) {
-              uint32_t h[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const float2 y = make_float2(s[8 * k + 2 * i], s[8 * k + 2 * i + 1]);
-                top = max3(top, y.x, y.y);
-                const float2 e = make_float2(ex2(y.x), ex2(y.y));
-                float2& l = l2[(w0 + 8 * k) / 2 + i];
-                if (!again) {
-                  l = __ffma2_rn(e, iv2, l);
-                } else {
-                  const int r = col0 + w0 + 8 * k + 2 * i;
-                  if (s_fac[r] < ANEW) l.x = fmaf(e.x, sc.inv_v, l.x);
-                  if (s_fac[r + 1] < ANEW) l.y = fmaf(e.y, sc.inv_v, l.y);
-                }
-                const __half2 hh = __floats2half2_rn(e.x, e.y);
-                h[i] = *reinterpret_cast<const uint32_t*>(&hh);
+                for (int n = 0; n < 16; ++n) o[n] *= f;
+                tmem_st16(t_o + g * 128 + w0, o);
               }
-              const int piece = (col0 + w0) / 8 + k;
-              *reinterpret_cast<uint4*>(pt + (piece / 8) * (AT_CHUNK * 128) + (((piece % 8) ^ f) << 4)) =
-                  make_uint4(h[0], h[1], h[2], h[3]);
             }
           }
-        };
-        // New references: the rows' maxima over this chunk and before.
-        auto raise = [&]() {
-#pragma unroll 1
-          for (int w0 = 0; w0 < COLS; w0 += 16) {
-            float y[16];
-            tmem_ld16(t_s + w0, y);
-            int mine = 0;
+          const float nref = m == -INFINITY ? 0.f : -m;
+          float top = -INFINITY;
+          sum = 0.f;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              float z = fmaf(y[i], fr[w0 + i] * sc.k, sc.log2_v);
-              if (col0 + w0 + i < hid) z = -INFINITY;
-              const int k = __reduce_max_sync(FULL_MASK, float_key(z));
-              if (lane == i) mine = k;
+          for (int w0 = 0; w0 < AT_CHUNK; w0 += 32) {
+            float s[32];
+            tmem_ld32(t_s + w0, s);
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              const PageScale sc = s_sc[slot][(w0 + 16 * q) >> p.page_log2];
+              score16(w0 + 16 * q, s + 16 * q, sc, nref);
+              float2 part = make_float2(0.f, 0.f);
+#pragma unroll
+              for (int n = 16 * q; n < 16 * q + 16; n += 2) {
+                top = max3(top, s[n], s[n + 1]);
+                const float2 e = make_float2(ex2(s[n]), ex2(s[n + 1]));
+                part = __fadd2_rn(part, e);
+                const __half2 hh = __floats2half2_rn(e.x, e.y);
+                h[(w0 + n) / 2] = *reinterpret_cast<const uint32_t*>(&hh);
+              }
+              sum = fmaf(part.x + part.y, sc.inv_v, sum);
             }
-            if (lane < 16) s_red[quarter][col0 + w0 + lane] = key_float(mine);
           }
-          sync_group();
-          if (gt < COLS) {
-            const int r = col0 + gt;
-            const float old = c == x.c0 ? -INFINITY : s_raw[r];
-            const float m = fmaxf(max3(s_red[0][r], s_red[1][r], s_red[2][r]), fmaxf(s_red[3][r], old));
-            s_fac[r] = m == -INFINITY ? 1.f : ex2(old - m);
-            s_raw[r] = m;
-            s_nref[r] = m == -INFINITY ? 0.f : -m;
-          }
-          sync_group();
-          if (c == x.c0) return;
-#pragma unroll
-          for (int i = 0; i < COLS; ++i) {
-            // a row whose reference moved that far starts anew: what it had is nothing beside
-            // what it gets, and its weights of this chunk may have passed the floats
-            float& l = i & 1 ? l2[i / 2].y : l2[i / 2].x;
-            const float g = s_fac[col0 + i];
-            l = g < ANEW ? 0.f : l * g;
-          }
-          wait_warp(&pvdone[(it - 1) & 1], ((it - 1) >> 1) & 1, ERR_KV8_PV_WAIT);
-          tc_fence_after();
-#pragma unroll 1
-          for (int w0 = 0; w0 < COLS; w0 += 16) {
-            float o[16];
-            tmem_ld16(t_o + t_lane + col0 + w0, o);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] *= s_fac[col0 + w0 + i];
-            tmem_st16(t_o + t_lane + col0 + w0, o);
-          }
-        };
-        if (force) raise();
-        weights(false);
-        fence_async_smem();
-        // Mostly no score is far above its reference and no page is missing.
-        force = false;
-        const bool lacks = c + 1 < x.cn && __any_sync(FULL_MASK, lane < (AT_CHUNK >> part_log2) && !s_sc[slot][lane & 7].ok);
-        if (bar_or<128>(3 + (warp >> 2), top > RAISE || lacks)) {
-          const bool up = bar_or<128>(3 + (warp >> 2), top > RAISE);
-          force = bar_or<128>(3 + (warp >> 2), lacks);  // rows' maxima may not be known yet
-          if (up) {
-            raise();
-            weights(true);
-            fence_async_smem();
-          }
+          anew = has && top > RAISE;
+          if (!__any_sync(FULL_MASK, anew)) break;
         }
+        l += sum;
+        tmem_st32(t_s, h);
+        tmem_st32(t_s + 32, h + 32);
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&sfree[b]);
-          mbar_arrive(&pready[pb]);
-        }
+        if (lane == 0) mbar_arrive(&pready[g]);
       }
 
-      // ---- the piece's sums, and its outputs or part
-#pragma unroll
-      for (int w0 = 0; w0 < COLS; w0 += W) {
-        float l[W];
-#pragma unroll
-        for (int i = 0; i < W; i += 2) { l[i] = l2[(w0 + i) / 2].x; l[i + 1] = l2[(w0 + i) / 2].y; }
-        // halves of the columns go to the other half of the lanes, until lane i holds column i
-#pragma unroll
-        for (int o = W / 2; o >= 1; o >>= 1) {
-          const bool up = lane & o;
-#pragma unroll
-          for (int i = 0; i < o; ++i) {
-            const float keep = up ? l[i + o] : l[i], give = up ? l[i] : l[i + o];
-            l[i] = keep + __shfl_xor_sync(FULL_MASK, give, o);
-          }
-        }
-        if (W == 16) l[0] += __shfl_xor_sync(FULL_MASK, l[0], 16);
-        if (lane < W) s_red[quarter][col0 + w0 + lane] = l[0];
-      }
-      sync_group();
-      const int d = in;  // this thread's column of the head dimension
-      const bool mine = d < D;
-      float* part = p.part + (int64_t(blockIdx.x) * 2 + (first_piece ? 0 : 1)) * N * (D + 2);
-      if (gt < COLS) {
-        const int r = col0 + gt;
-        const float m = any_chunk ? s_raw[r] : -INFINITY;
-        const float sum = any_chunk ? (s_red[0][r] + s_red[1][r]) + (s_red[2][r] + s_red[3][r]) : 0.f;
-        if (x.whole) {
-          s_fac[r] = sum == 0.f ? 0.f : 1.f / sum;  // no token seen: 0
-          if (p.lse && r < rows) {
-            const int i = (row0 + r) / p.group;
-            p.lse[(sq.q0 + i) * p.q_heads + x.h * p.group + (row0 + r - i * p.group)] =
-                sum == 0.f ? -INFINITY : (m + log2f(sum)) * LN2_F;
-          }
-        } else {
-          part[N * D + r] = m;
-          part[N * D + N + r] = sum;
-        }
-      }
-      int nan_row = N;  // rows from here on see a NaN in this column
-      if (any_chunk) {
-        wait_warp(&pvdone[(it - 1) & 1], ((it - 1) >> 1) & 1, ERR_KV8_PV_WAIT);
+      // ---- the two groups' halves of the tile together; each writes half of the columns
+      if (chunks > 0 && qi > 0) wait_warp(&left[k], (qi - 1) & 1, ERR_KV8_PV_WAIT);
+      float m1 = -INFINITY, l1 = 0.f;
+      const int mine = (chunks + 1 - ((it0 ^ g) & 1)) / 2;  // this group's chunks
+      if (chunks > 0) {
+        s_m[g][r] = m;
+        s_l[g][r] = l;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&met[k]);
+        wait_warp(&met[k], qi & 1, ERR_KV8_PV_WAIT);
+        m1 = s_m[g ^ 1][r];
+        l1 = s_l[g ^ 1][r];
+        // both groups' last products
+        const int last = it0 + chunks - 1;
+        wait_warp(&pvdone[last & 1], (last >> 1) & 1, ERR_KV8_PV_WAIT);
+        if (chunks > 1) wait_warp(&pvdone[(last - 1) & 1], ((last - 1) >> 1) & 1, ERR_KV8_PV_WAIT);
         tc_fence_after();
-        if (s_nan[pi % PIECE_RING][warp >> 2] && mine) {
-          const int edge = sq.len - sq.n;
-          const int from = max(x.c0, max(edge, 0) / AT_CHUNK) * AT_CHUNK, to = min(x.end, x.cn * AT_CHUNK);
-          for (int t = from; t < to; ++t) {
-            const int id = __ldg(p.table + x.b * p.table_stride + (t >> p.page_log2));
-            if (id < 0 || id >= p.c.n_pages) continue;
-            const int64_t at = ((int64_t(id) * p.c.heads + x.h) * p.c.page + (t & (p.c.page - 1))) * D + d;
-            if ((p.c.v[at] & 0x7f) == 0x7f) {
-              nan_row = max(0, (t - edge) * p.group - row0);
-              break;  // later tokens are seen by fewer rows
-            }
-          }
+      }
+      if (l == 0.f) m = -INFINITY;  // (a NaN stays)
+      if (l1 == 0.f) m1 = -INFINITY;
+      const float top = fmaxf(m, m1), base = top == -INFINITY ? 0.f : top;
+      float f0 = ex2(m - base), f1 = ex2(m1 - base);
+      const float total = fmaf(l, f0, l1 * f1);
+      const int64_t at = (x.q0 + i) * p.q_heads + x.h * p.group + j;
+      float* part = p.part + int64_t(x.slot) * ROWS * (D + 2);
+      if (x.whole) {
+        const float inv = total == 0.f ? 0.f : 1.f / total;  // no token seen: 0
+        f0 *= inv;
+        f1 *= inv;
+      }
+      if (has && g == 0) {
+        if (!x.whole) {
+          part[ROWS * D + r] = top;
+          part[ROWS * D + ROWS + r] = total;
+        } else if (p.lse) {
+          p.lse[at] = total == 0.f ? -INFINITY : (top + log2f(total)) * LN2_F;
         }
       }
-      sync_group();
-      if (any_chunk && gt == 0) s_nan[pi % PIECE_RING][warp >> 2] = 0;
-      int i = (row0 + col0) / p.group, j = row0 + col0 - i * p.group;  // new token and head of a row
+      const bool nans = chunks > 0 && s_nan[qi % PIECE_RING];
 #pragma unroll 1
-      for (int r0 = col0; r0 < min(rows, col0 + COLS); r0 += 16) {
-        float o[16];
-        if (any_chunk) {
-          tmem_ld16(t_o + t_lane + r0, o);
-        } else {
+      for (int w0 = g * (D / 2); w0 < (g + 1) * (D / 2); w0 += 16) {
+        float y[16];
 #pragma unroll
-          for (int k = 0; k < 16; ++k) o[k] = 0.f;
+        for (int n = 0; n < 16; ++n) y[n] = 0.f;
+        if (mine > 0) {
+          float o[16];
+          tmem_ld16(t_o + g * 128 + w0, o);
+#pragma unroll
+          for (int n = 0; n < 16; ++n) y[n] = o[n] * f0;
         }
+        if (chunks > mine) {
+          float o[16];
+          tmem_ld16(t_o + (g ^ 1) * 128 + w0, o);
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const int r = r0 + k;
-          if (r < rows && mine) {
-            const float y = r >= nan_row ? NAN : o[k];
-            if (x.whole)
-              p.out[((sq.q0 + i) * p.q_heads + x.h * p.group + j) * D + d] = __float2bfloat16_rn(y * s_fac[r]);
-            else
-              part[r * D + d] = y;
+          for (int n = 0; n < 16; ++n) y[n] = fmaf(o[n], f1, y[n]);
+        }
+        if (nans) {
+          // NaN codes of V that this row sees, among the tokens where they were taken out
+          const int from = max(x.c0, max(x.len - x.n, 0) / AT_CHUNK) * AT_CHUNK;
+          for (int t = from; t < min(seen, x.cn * AT_CHUNK) && has; ++t) {
+            const int id = __ldg(p.table + x.table + (t >> p.page_log2));
+            if (id < 0 || id >= p.c.n_pages) continue;
+            const uint8_t* v = p.c.v + ((int64_t(id) * p.c.heads + x.h) * p.c.page + (t & (p.c.page - 1))) * D + w0;
+#pragma unroll
+            for (int n = 0; n < 16; ++n)
+              if ((v[n] & 0x7f) == 0x7f) y[n] = NAN;
           }
-          if (++j == p.group) { j = 0; ++i; }
+        }
+        if (has) {
+          if (x.whole) {
+            uint32_t o[8];
+#pragma unroll
+            for (int n = 0; n < 8; ++n) {
+              const __nv_bfloat162 v = __floats2bfloat162_rn(y[2 * n], y[2 * n + 1]);
+              o[n] = *reinterpret_cast<const uint32_t*>(&v);
+            }
+            uint4* dst = reinterpret_cast<uint4*>(p.out + at * D + w0);
+            dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+            dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+          } else {
+            float4* dst = reinterpret_cast<float4*>(part + r * D + w0);
+#pragma unroll
+            for (int n = 0; n < 4; ++n) dst[n] = make_float4(y[4 * n], y[4 * n + 1], y[4 * n + 2], y[4 * n + 3]);
+          }
         }
       }
-      tc_fence_before();
-      sync_group();  // s_red and s_fac are read
-      if (any_chunk) ++pi;
+      if (chunks > 0) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&left[k]);
+        it0 += chunks;
+        ++qi;
+      }
     }
   }
   tc_fence_before();
   __syncthreads();
   if (warp == 0) {
     tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(S::TMEM)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TMEM_COLS)
                  : "memory");
   }
 }
@@ -994,25 +978,21 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-int tile_rows(int max_new, int group) {
-  const int64_t rows = int64_t(max_new) * group;
-  return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
-}
+// 128 rows where there are more than 32: a tile of either takes the same time on the tensor cores
+// for a chunk, and fewer tiles read the cache fewer times; 32 rows leave room for one more stage
+// and a second q, and need one softmax warp a group.
+int tile_rows(int max_new, int group) { return int64_t(max_new) * group <= 32 ? 32 : 128; }
 
-int attn_grid(int n) {
-  return device_sm_count() * (n == 16 ? AttnShape<128, 16>::CTAS : 1);
-}
-
-template <int D, int N>
+template <int D, int ROWS>
 cudaError_t launch(const CUtensorMap& tm, const AttnParams& prm, int grid, cudaStream_t stream) {
-  constexpr int smem = AttnShape<D, N>::SMEM;
-  cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void*>(kv8_attention_kernel<D, N>), smem);
+  constexpr int smem = AttnShape<D, ROWS>::SMEM;
+  cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void*>(kv8_attention_kernel<D, ROWS>), smem);
   if (e != cudaSuccess) return e;
-  kv8_attention_kernel<D, N><<<grid, AttnShape<D, N>::THREADS, smem, stream>>>(tm, prm);
+  kv8_attention_kernel<D, ROWS><<<grid, 32 * AttnShape<D, ROWS>::WARPS, smem, stream>>>(tm, prm);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   PdlScope pdl(true);
-  e = launch_k(kv8_join_kernel<D, N>, dim3(grid, N / JOIN_ROWS), dim3(32 * JOIN_ROWS), 0, stream, prm, grid);
+  e = launch_k(kv8_join_kernel<D, ROWS>, dim3(grid, ROWS / JOIN_ROWS), dim3(32 * JOIN_ROWS), 0, stream, prm, grid);
   if (e == cudaSuccess) note_launch(2);
   return e;
 }
@@ -1020,8 +1000,7 @@ cudaError_t launch(const CUtensorMap& tm, const AttnParams& prm, int grid, cudaS
 }  // namespace
 
 size_t kv8_attention_workspace(int max_new, int group, int D) {
-  const int n = tile_rows(max_new, group);
-  return size_t(attn_grid(n)) * 2 * n * (D + 2) * sizeof(float);
+  return size_t(device_sm_count()) * 2 * tile_rows(max_new, group) * (D + 2) * sizeof(float);
 }
 
 cudaError_t kv8_attention_launch(const Kv8Attention& a, cudaStream_t stream) {
@@ -1053,14 +1032,11 @@ cudaError_t kv8_attention_launch(const Kv8Attention& a, cudaStream_t stream) {
   prm.out = a.out;
   prm.lse = a.lse;
   prm.part = static_cast<float*>(a.workspace);
-  const int n = tile_rows(a.max_new, a.group), grid = attn_grid(n);
-#define LC_N(DD)                                                            \
-  (n == 16 ? launch<DD, 16>(tm, prm, grid, stream)                          \
-           : n == 32 ? launch<DD, 32>(tm, prm, grid, stream)                \
-                     : n == 64 ? launch<DD, 64>(tm, prm, grid, stream)      \
-                               : launch<DD, 128>(tm, prm, grid, stream))
-  return D == 128 ? LC_N(128) : D == 64 ? LC_N(64) : LC_N(32);
-#undef LC_N
+  const int grid = device_sm_count();
+  const bool small = tile_rows(a.max_new, a.group) == 32;
+#define LC_ROWS(DD) (small ? launch<DD, 32>(tm, prm, grid, stream) : launch<DD, 128>(tm, prm, grid, stream))
+  return D == 128 ? LC_ROWS(128) : D == 64 ? LC_ROWS(64) : LC_ROWS(32);
+#undef LC_ROWS
 }
 
 cudaError_t kv8_attention_read_device_error(uint32_t* code) {
