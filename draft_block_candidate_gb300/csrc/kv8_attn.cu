@@ -227,15 +227,12 @@ __device__ __forceinline__ void tmem_st16(uint32_t t, const float* v) {
       : "memory");
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t t, const uint32_t* v) {
+__device__ __forceinline__ void tmem_st16u(uint32_t t, const uint32_t* v) {  // (not waited for)
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(t),
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(t),
       "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
-      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]),
-      "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]),
-      "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
 }
 
@@ -707,64 +704,58 @@ __global__ void __launch_bounds__(32 * AttnShape<D, ROWS>::WARPS, 1)
               if (n >= see) s[n] = -INFINITY;
           }
         };
-        uint32_t h[AT_CHUNK / 2];  // the weights as f16 pairs
-        float sum;
-        bool anew = m == -INFINITY && lim > 0;  // (rows that are not there have m = 0)
-        for (;;) {
-          if (__any_sync(FULL_MASK, anew)) {
-            // new maxima, over this chunk and before; S stays as it is
-            float top = m;
+        // 1. The row's largest score of the chunk, and whether it asks for a new maximum.
+        float nref = m == -INFINITY ? 0.f : -m, top = -INFINITY;
 #pragma unroll 1
-            for (int w0 = 0; w0 < AT_CHUNK; w0 += 16) {
-              float s[16];
-              tmem_ld16(t_s + w0, s);
-              score16(w0, s, s_sc[slot][w0 >> p.page_log2], 0.f);
+        for (int w0 = 0; w0 < AT_CHUNK; w0 += 32) {
+          float s[32];
+          tmem_ld32(t_s + w0, s);
+          score16(w0, s, s_sc[slot][w0 >> p.page_log2], nref);
+          score16(w0 + 16, s + 16, s_sc[slot][(w0 + 16) >> p.page_log2], nref);
 #pragma unroll
-              for (int n = 0; n < 16; n += 2) top = max3(top, s[n], s[n + 1]);
-            }
-            const float f = top == -INFINITY ? 1.f : ex2(m - top);
-            m = top;
-            l *= f;
-            if (d >= 2) {  // (S of this chunk could only come after the group's last product)
-#pragma unroll 1
-              for (int w0 = 0; w0 < D; w0 += 16) {
-                float o[16];
-                tmem_ld16(t_o + g * 128 + w0, o);
-#pragma unroll
-                for (int n = 0; n < 16; ++n) o[n] *= f;
-                tmem_st16(t_o + g * 128 + w0, o);
-              }
-            }
-          }
-          const float nref = m == -INFINITY ? 0.f : -m;
-          float top = -INFINITY;
-          sum = 0.f;
-#pragma unroll
-          for (int w0 = 0; w0 < AT_CHUNK; w0 += 32) {
-            float s[32];
-            tmem_ld32(t_s + w0, s);
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              const PageScale sc = s_sc[slot][(w0 + 16 * q) >> p.page_log2];
-              score16(w0 + 16 * q, s + 16 * q, sc, nref);
-              float2 part = make_float2(0.f, 0.f);
-#pragma unroll
-              for (int n = 16 * q; n < 16 * q + 16; n += 2) {
-                top = max3(top, s[n], s[n + 1]);
-                const float2 e = make_float2(ex2(s[n]), ex2(s[n + 1]));
-                part = __fadd2_rn(part, e);
-                const __half2 hh = __floats2half2_rn(e.x, e.y);
-                h[(w0 + n) / 2] = *reinterpret_cast<const uint32_t*>(&hh);
-              }
-              sum = fmaf(part.x + part.y, sc.inv_v, sum);
-            }
-          }
-          anew = has && top > RAISE;
-          if (!__any_sync(FULL_MASK, anew)) break;
+          for (int n = 0; n < 32; n += 2) top = max3(top, s[n], s[n + 1]);
         }
-        l += sum;
-        tmem_st32(t_s, h);
-        tmem_st32(t_s + 32, h + 32);
+        // (rows that are not there have m = 0)
+        const bool anew = (has && top > RAISE) || (m == -INFINITY && lim > 0);
+        if (__any_sync(FULL_MASK, anew)) {
+          top = fmaxf(top - nref, m);
+          const float f = top == -INFINITY ? 1.f : ex2(m - top);
+          m = top;
+          nref = m == -INFINITY ? 0.f : -m;
+          l *= f;
+          if (d >= 2) {  // (S of this chunk could only come after the group's last product)
+#pragma unroll 1
+            for (int w0 = 0; w0 < D; w0 += 16) {
+              float o[16];
+              tmem_ld16(t_o + g * 128 + w0, o);
+#pragma unroll
+              for (int n = 0; n < 16; ++n) o[n] *= f;
+              tmem_st16(t_o + g * 128 + w0, o);
+            }
+          }
+        }
+        // 2. The weights, over the scores that have been read (16 columns of pairs for 32 of S).
+#pragma unroll 1
+        for (int w0 = 0; w0 < AT_CHUNK; w0 += 32) {
+          float s[32];
+          uint32_t h[16];
+          tmem_ld32(t_s + w0, s);
+#pragma unroll
+          for (int q = 0; q < 32; q += 16) {
+            const PageScale sc = s_sc[slot][(w0 + q) >> p.page_log2];
+            score16(w0 + q, s + q, sc, nref);
+            float2 part = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int n = q; n < q + 16; n += 2) {
+              const float2 e = make_float2(ex2(s[n]), ex2(s[n + 1]));
+              part = __fadd2_rn(part, e);
+              const __half2 hh = __floats2half2_rn(e.x, e.y);
+              h[n / 2] = *reinterpret_cast<const uint32_t*>(&hh);
+            }
+            l = fmaf(part.x + part.y, sc.inv_v, l);
+          }
+          tmem_st16u(t_s + w0 / 2, h);
+        }
         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
         tc_fence_before();
         __syncwarp();
