@@ -44,105 +44,9 @@
 #include <algorithm>
 #include <cmath>
 
-#include "kv8.cuh"
+#include "kv8_attn.cuh"
 
 namespace lilicorr {
-
-static __device__ uint32_t g_err_kv8_attn;
-
-constexpr int AT_CHUNK = 128;
-constexpr float LOG2E_F = 1.4426950408889634f;
-constexpr float LN2_F = 0.6931471805599453f;
-
-struct AttnParams {
-  Kv8 c;
-  const __nv_bfloat16* q;
-  int64_t q_tok, q_head;  // elements
-  int64_t total;
-  int q_heads, group;
-  const int32_t *q_start, *kv_len, *table;
-  int64_t batch, table_stride;
-  int cols, max_new, page_log2;
-  float scale2;  // softmax scale * log2 e
-  __nv_bfloat16* out;  // [total, q_heads, D]
-  float* lse;          // [total, q_heads] or null
-  float* part;         // [2 * grid][N * (D + 2)]: products, maxima, sums
-};
-
-// ------------------------------------------------------------------------ the deal of work
-
-struct SeqUnits {
-  int n, len, tiles, chunks;
-  int64_t q0, units;
-};
-template <int N>
-__device__ __forceinline__ SeqUnits seq_units(const AttnParams& p, int64_t b) {
-  const SeqRange r = seq_range(p.q_start, p.kv_len, b, p.total, p.max_new,
-                               int64_t(p.cols) << p.page_log2, &g_err_kv8_attn);
-  SeqUnits u;
-  u.n = r.n;
-  u.len = r.len;
-  u.q0 = r.q0;
-  u.tiles = (r.n * p.group + N - 1) / N;
-  u.chunks = max(1, (r.len + AT_CHUNK - 1) / AT_CHUNK);
-  u.units = int64_t(u.tiles) * p.c.heads * u.chunks;
-  return u;
-}
-
-// The units of all sequences, and where run `run` of `runs` begins, by one warp.
-struct Run {
-  int64_t per;       // units of a run
-  int64_t u, u_end;  // this run's units
-  int64_t b, first;  // the sequence of unit u, and that sequence's first unit
-};
-template <int N>
-__device__ __forceinline__ Run find_run(const AttnParams& p, int64_t run, int runs) {
-  const int lane = threadIdx.x & 31;
-  int64_t t = 0;
-#pragma unroll 1
-  for (int64_t b = lane; b < p.batch; b += 32) t += seq_units<N>(p, b).units;
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) t += __shfl_xor_sync(FULL_MASK, t, o);
-  Run r;
-  r.per = t < INT_MAX / 2 ? int64_t((static_cast<uint32_t>(t) + runs - 1) / static_cast<uint32_t>(runs))
-                          : (t + runs - 1) / runs;
-  r.u = run * r.per;
-  r.u_end = min(t, r.u + r.per);
-  r.b = p.batch;
-  r.first = 0;
-  if (r.u >= r.u_end) return r;
-#pragma unroll 1
-  for (int64_t b0 = 0; b0 < p.batch; b0 += 32) {  // the 32 sequences among whose units u is
-    const int64_t mine = b0 + lane < p.batch ? seq_units<N>(p, b0 + lane).units : 0;
-    int64_t sum = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t x = __shfl_up_sync(FULL_MASK, sum, o);
-      if (lane >= o) sum += x;
-    }
-    const unsigned past = __ballot_sync(FULL_MASK, r.first + sum > r.u);
-    if (past) {
-      const int l = __ffs(past) - 1;
-      r.b = b0 + l;
-      r.first += __shfl_sync(FULL_MASK, sum - mine, l);
-      break;
-    }
-    r.first += __shfl_sync(FULL_MASK, sum, 31);
-  }
-  return r;
-}
-
-// A piece of a run: the chunks [c0, c1) of one tile, of which [c0, cn) are seen by some row of
-// it.  The loading warp works the pieces out and leaves them in a ring for the others.
-struct Piece {
-  int64_t q0;         // the sequence's first row of q
-  int64_t table;      // its row of the block table, as an offset
-  int n, len;         // its new tokens and its cached ones
-  int h, row0, rows;  // key / value head; the tile's first row and its rows
-  int c0, cn, end;    // tokens that the tile's last row sees
-  int whole;          // 1: all of the tile's chunks; 0: a part; -1: there is no further piece
-  int slot;           // of the workspace, for a part
-};
 
 // ------------------------------------------------------------------- tensor-core plumbing
 
@@ -267,7 +171,7 @@ __device__ __forceinline__ uint32_t nan_codes(uint32_t w) {  // 0xff in each byt
 template <int D, int ROWS>
 struct AttnShape {
   static constexpr int KT = AT_CHUNK * D;               // bytes of a chunk's keys, or values
-  static constexpr int STAGES = D < 128 || ROWS == 32 ? 4 : 3;
+  static constexpr int STAGES = D < 128 ? 4 : 3;
   static constexpr int VW = 2 * KT;                     // widened values; two buffers
   static constexpr int QB = ROWS == 32 ? 2 : 1;         // buffers of q
   static constexpr int QT = ROWS * D;                   // bytes of q hi, or lo
@@ -304,25 +208,6 @@ __device__ __forceinline__ Role role_of(int warp, int& k) {
 
 constexpr int SC_RING = 8, PIECE_RING = 4;  // deeper than any warp runs ahead of the softmax
 constexpr float RAISE = 14.f;               // log2 of how far a score may pass its reference
-
-struct PageScale {  // of the tokens of one page
-  float k, log2_v, inv_v;
-  int ok;  // the page was loaded
-};
-
-// The rest of a wait that did not end at once, at most WAIT_LIMIT_CYCLES.  The first one of a CTA
-// that gives up makes every later one give up soon, and the roles' loops end.
-__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, uint32_t site, volatile int* fail) {
-  const long long t0 = clock64();
-  for (uint32_t i = 1;; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((i & 63) == 0 && (*fail || clock64() - t0 > WAIT_LIMIT_CYCLES)) {
-      atomicOr(&g_err_kv8_attn, site);
-      *fail = 1;
-      return false;
-    }
-  }
-}
 
 template <int D, int ROWS>
 __global__ void __launch_bounds__(32 * AttnShape<D, ROWS>::WARPS, 1)
@@ -866,91 +751,6 @@ __global__ void __launch_bounds__(32 * AttnShape<D, ROWS>::WARPS, 1)
   }
 }
 
-// Joins the parts of the tiles that several CTAs hold.  One CTA per boundary between two runs
-// of units and 16 rows; the CTAs of the first boundary inside a tile join that tile, from the run
-// that holds its first chunk to the one that holds its last, in that order: a warp for each
-// row, the weights of 32 parts at a time worked out side by side, then the parts added up.
-constexpr int JOIN_ROWS = 16;
-
-template <int D, int N>
-__global__ void __launch_bounds__(32 * JOIN_ROWS) kv8_join_kernel(const AttnParams p, int runs) {
-  constexpr int E = D / 32;  // columns of a lane
-  const int lane = threadIdx.x & 31, r = blockIdx.y * JOIN_ROWS + (threadIdx.x >> 5);
-  // Lengths and row ranges were there before the attention began: they are read, and the
-  // tile is found, while it still runs.
-  const Run run = find_run<N>(p, int64_t(blockIdx.x) + 1, runs);
-  const int64_t edge = run.u;  // first unit of run blockIdx.x + 1
-  if (edge >= run.u_end) return;
-  const SeqUnits sq = seq_units<N>(p, run.b);
-  const uint32_t in = static_cast<uint32_t>(edge - run.first);
-  const uint32_t item = in / sq.chunks;
-  const int64_t i0 = run.first + int64_t(item) * sq.chunks, i1 = i0 + sq.chunks;  // the tile's units
-  if (edge == i0) return;                  // the boundary lies between two tiles
-  if (edge - run.per > i0) return;         // an earlier boundary lies inside this tile too
-  const int64_t r0 = blockIdx.x, r1 = (i1 - 1) / run.per;  // runs that hold parts
-  const int h = item / sq.tiles, tile = item - h * sq.tiles;
-  const int row = tile * N + r;
-  if (row >= sq.n * p.group) return;
-  constexpr int64_t STEP = N * (D + 2);
-  // the run that holds the tile's first chunk may hold another tile's part before it
-  const float* parts = p.part + r0 * 2 * STEP;
-  const int64_t lead = r0 * run.per >= i0 ? 0 : STEP;
-  pdl_wait();
-  float mx = -INFINITY, sum = 0.f, y[E];
-#pragma unroll
-  for (int n = 0; n < E; ++n) y[n] = 0.f;
-  const int count = static_cast<int>(r1 - r0) + 1;
-  for (int k0 = 0; k0 < count; k0 += 32) {
-    const int mine = k0 + lane;
-    const float* q = parts + mine * 2 * STEP + (mine == 0 ? lead : 0);
-    const float m = mine < count ? __ldcg(q + N * D + r) : -INFINITY;
-    const float s = mine < count ? __ldcg(q + N * D + N + r) : 0.f;
-    float nm = fmaxf(m, mx);
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) nm = fmaxf(nm, __shfl_xor_sync(FULL_MASK, nm, o));
-    const float base = nm == -INFINITY ? 0.f : nm;
-    const float w = ex2(m - base), back = ex2(mx - base);
-    float add = s * w;
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) add += __shfl_xor_sync(FULL_MASK, add, o);
-    sum = fmaf(sum, back, add);
-#pragma unroll
-    for (int n = 0; n < E; ++n) y[n] *= back;
-    mx = nm;
-    const int here = min(32, count - k0);
-#pragma unroll 8
-    for (int k = 0; k < here; ++k) {
-      const float wk = __shfl_sync(FULL_MASK, w, k);
-      const float* src = parts + (k0 + k) * 2 * STEP + (k0 + k == 0 ? lead : 0) + r * D + lane * E;
-      if constexpr (E == 4) {
-        const float4 z = __ldcg(reinterpret_cast<const float4*>(src));
-        y[0] = fmaf(z.x, wk, y[0]); y[1] = fmaf(z.y, wk, y[1]);
-        y[2] = fmaf(z.z, wk, y[2]); y[3] = fmaf(z.w, wk, y[3]);
-      } else if constexpr (E == 2) {
-        const float2 z = __ldcg(reinterpret_cast<const float2*>(src));
-        y[0] = fmaf(z.x, wk, y[0]); y[1] = fmaf(z.y, wk, y[1]);
-      } else {
-        y[0] = fmaf(__ldcg(src), wk, y[0]);
-      }
-    }
-  }
-  const int i = row / p.group;
-  const int64_t at = (sq.q0 + i) * p.q_heads + h * p.group + (row - i * p.group);
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;  // no token seen: 0
-  __nv_bfloat16* o = p.out + at * D + lane * E;
-  if constexpr (E == 4) {
-    const __nv_bfloat162 a = __floats2bfloat162_rn(y[0] * inv, y[1] * inv);
-    const __nv_bfloat162 c = __floats2bfloat162_rn(y[2] * inv, y[3] * inv);
-    *reinterpret_cast<uint2*>(o) = make_uint2(*reinterpret_cast<const uint32_t*>(&a),
-                                              *reinterpret_cast<const uint32_t*>(&c));
-  } else if constexpr (E == 2) {
-    *reinterpret_cast<__nv_bfloat162*>(o) = __floats2bfloat162_rn(y[0] * inv, y[1] * inv);
-  } else {
-    *o = __float2bfloat16_rn(y[0] * inv);
-  }
-  if (p.lse && lane == 0) p.lse[at] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * LN2_F;
-}
-
 // -------------------------------------------------------------------------------- host
 
 namespace {
@@ -969,10 +769,12 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// 128 rows where there are more than 32: a tile of either takes the same time on the tensor cores
-// for a chunk, and fewer tiles read the cache fewer times; 32 rows leave room for one more stage
-// and a second q, and need one softmax warp a group.
-int tile_rows(int max_new, int group) { return int64_t(max_new) * group <= 32 ? 32 : 128; }
+// Rows of a tile.  Up to 16 go to the kernel of kv8_attn_few.cu (8 where that is all).
+int tile_rows(int max_new, int group) {
+  const int64_t rows = int64_t(max_new) * group;
+  return rows <= 8 ? 8 : rows <= 16 ? 16 : 128;
+}
+int runs_of(int rows) { return rows <= 16 ? kv8_few_runs(rows) : device_sm_count(); }
 
 template <int D, int ROWS>
 cudaError_t launch(const CUtensorMap& tm, const AttnParams& prm, int grid, cudaStream_t stream) {
@@ -983,7 +785,7 @@ cudaError_t launch(const CUtensorMap& tm, const AttnParams& prm, int grid, cudaS
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   PdlScope pdl(true);
-  e = launch_k(kv8_join_kernel<D, ROWS>, dim3(grid, ROWS / JOIN_ROWS), dim3(32 * JOIN_ROWS), 0, stream, prm, grid);
+  e = launch_k(kv8_join_kernel<D, ROWS>, dim3(grid, ROWS / JOIN_ROWS<ROWS>), dim3(32 * JOIN_ROWS<ROWS>), 0, stream, prm, grid);
   if (e == cudaSuccess) note_launch(2);
   return e;
 }
@@ -991,24 +793,12 @@ cudaError_t launch(const CUtensorMap& tm, const AttnParams& prm, int grid, cudaS
 }  // namespace
 
 size_t kv8_attention_workspace(int max_new, int group, int D) {
-  return size_t(device_sm_count()) * 2 * tile_rows(max_new, group) * (D + 2) * sizeof(float);
+  const int rows = tile_rows(max_new, group);
+  return size_t(runs_of(rows)) * 2 * rows * (D + 2) * sizeof(float);
 }
 
 cudaError_t kv8_attention_launch(const Kv8Attention& a, cudaStream_t stream) {
-  auto fn = encode_fn();
-  const int64_t tiles = a.c.n_pages * a.c.heads;
-  if (!fn || tiles > INT_MAX) return cudaErrorInvalidValue;
-  const int D = a.D, page = a.c.page;
-  CUtensorMap tm;
-  const cuuint64_t dims[3] = {cuuint64_t(D), cuuint64_t(page), cuuint64_t(tiles)};
-  const cuuint64_t strides[2] = {cuuint64_t(D), cuuint64_t(D) * page};
-  const cuuint32_t box[3] = {cuuint32_t(D), cuuint32_t(page), 1};
-  const cuuint32_t estr[3] = {1, 1, 1};
-  if (fn(&tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, a.c.k, dims, strides, box, estr,
-         CU_TENSOR_MAP_INTERLEAVE_NONE,
-         D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B,
-         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-    return cudaErrorInvalidValue;
+  const int D = a.D, page = a.c.page, rows = tile_rows(a.max_new, a.group);
   AttnParams prm{};
   prm.c = a.c;
   prm.q = a.q;
@@ -1023,11 +813,24 @@ cudaError_t kv8_attention_launch(const Kv8Attention& a, cudaStream_t stream) {
   prm.out = a.out;
   prm.lse = a.lse;
   prm.part = static_cast<float*>(a.workspace);
-  const int grid = device_sm_count();
-  const bool small = tile_rows(a.max_new, a.group) == 32;
-#define LC_ROWS(DD) (small ? launch<DD, 32>(tm, prm, grid, stream) : launch<DD, 128>(tm, prm, grid, stream))
-  return D == 128 ? LC_ROWS(128) : D == 64 ? LC_ROWS(64) : LC_ROWS(32);
-#undef LC_ROWS
+  if (rows <= 16) return kv8_few_launch(prm, D, rows, stream);
+  auto fn = encode_fn();
+  const int64_t tiles = a.c.n_pages * a.c.heads;
+  if (!fn || tiles > INT_MAX) return cudaErrorInvalidValue;
+  CUtensorMap tm;
+  const cuuint64_t dims[3] = {cuuint64_t(D), cuuint64_t(page), cuuint64_t(tiles)};
+  const cuuint64_t strides[2] = {cuuint64_t(D), cuuint64_t(D) * page};
+  const cuuint32_t box[3] = {cuuint32_t(D), cuuint32_t(page), 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  if (fn(&tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, a.c.k, dims, strides, box, estr,
+         CU_TENSOR_MAP_INTERLEAVE_NONE,
+         D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B,
+         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
+  const int grid = runs_of(rows);
+  return D == 128 ? launch<128, 128>(tm, prm, grid, stream)
+         : D == 64 ? launch<64, 128>(tm, prm, grid, stream)
+                   : launch<32, 128>(tm, prm, grid, stream);
 }
 
 cudaError_t kv8_attention_read_device_error(uint32_t* code) {
@@ -1036,7 +839,7 @@ cudaError_t kv8_attention_read_device_error(uint32_t* code) {
   if (e != cudaSuccess) return e;
   if (v) e = cudaMemcpyToSymbol(g_err_kv8_attn, &zero, sizeof(zero));
   *code |= v;
-  return e;
+  return e == cudaSuccess ? kv8_few_read_device_error(code) : e;
 }
 
 }  // namespace lilicorr

@@ -97,12 +97,15 @@ def attention(q, k_pages, v_pages, k_scale, v_scale, q_start, kv_len, table, sca
     """(out, lse, tolerance of out, tolerance of lse), float64, rows outside the sequences NaN.
 
     Tolerances: with p the softmax weights and D the head dimension,
-      * a score is an f32 sum of D exact products and one f32 fma: it is off by at most
-        e = (D + 4) 2^-24 (scale sum|q k|) + 2^-23 |score| + 2^-23 |log2 of the value scale|,
+      * q is split into two e4m3 values, exactly but for 2^-17 of its row's largest; a score is
+        an f32 sum of 2 D products and one f32 fma: it is off by at most
+        e = (2 D + 4) 2^-24 (scale sum|q k|) + 2^-17 max|q| (scale sum|k|) + 2^-23 |score|
+            + 2^-23 |log2 of the value scale|,
         and so is the lse, with one rounding of the lse and a few of exp2, log2 and their sum
         (each below 2^-21) on top;
-      * a weight is off by that relative amount and by its rounding to f16 (2^-11), or by
-        2^-25 of the row's largest weight times value scale where it is f16-subnormal;
+      * a weight is off by that relative amount and by its rounding: to f16 (2^-11 of its value,
+        or 2^-25 of the row's largest weight times value scale where it is f16-subnormal), or to
+        f16 and then to a sum of three e5m2 values of 3 bits (2^-12 + 2^-9 of its value);
       * the f32 sums over T tokens in runs of 16: (T / 16 + 40) 2^-24 of sum p |v|;
       * out is rounded to bf16 once: half a step, 2^-8 of its value."""
     total, q_heads, D = q.shape
@@ -137,11 +140,12 @@ def attention(q, k_pages, v_pages, k_scale, v_scale, q_start, kv_len, table, sca
                     p = p / z
                     out[r, c] = p @ v[:t]
                     lse[r, c] = m + torch.log(z)
-                    e = float(((D + 4) * 2.0 ** -24 * mag + 2.0 ** -23 * s.abs()
+                    qk = k[:t].abs().sum(1) * float(q[r, c].abs().max()) * abs(scale)
+                    e = float(((2 * D + 4) * 2.0 ** -24 * mag + 2.0 ** -17 * qk + 2.0 ** -23 * s.abs()
                                + 2.0 ** -23 * torch.log2(vs[:t]).abs()).max())
                     pv = p @ v[:t].abs()
                     codes = (v[:t].abs() / vs[:t, None]).sum(0)
-                    to[r, c] = (2.0 ** -8 * out[r, c].abs() + (2 * e + 2.0 ** -11 + (t / 16 + 40) * 2.0 ** -24) * pv
+                    to[r, c] = (2.0 ** -8 * out[r, c].abs() + (2 * e + 2.0 ** -9 + 2.0 ** -11 + (t / 16 + 40) * 2.0 ** -24) * pv
                                 + 2.0 ** -25 * float((p * vs[:t]).max()) * codes + 1e-30)
                     tl[r, c] = e + 2.0 ** -24 * lse[r, c].abs() + 2.0 ** -20
     return out, lse, to, tl
