@@ -5,15 +5,17 @@
 // kv8_attn.cu took 400 us where this one takes 200 (128 sequences of up to 8,192 tokens, 32
 // query heads on 8, head dim 128).
 //
-// Here the products are warp-level e4m3 products (m16n8k32, 4.2 cycles each on an SM quarter,
-// four times the f16 rate per value), which take the cache's codes as they lie in shared memory:
-//     s = (q_hi + q_lo) . k      q split into two e4m3 values, as in kv8_attn.cu
-//     o += (p1 + p2 + p3) v      p in units of 2^-14 of the row's largest, as three e5m2 values
-//                                (3 significant bits each: off by at most 2^-9 of its value,
-//                                2^-31 of the largest)
-// so that no code is widened; V's bytes are put into the order of the instruction, four tokens
-// of one column to a register, by byte permutations.  The summation index of q . k and the output
-// columns of p v may be taken in any order, which lets each lane read 16 contiguous bytes.
+// Here the products are warp-level f16 products (m16n8k16) with the tokens, and the head
+// dimension, as the 16 rows and 8 query rows as the columns, so that none of a tile is empty:
+//     s'[16 tokens, 8 rows] = k q^T,   o'[16 of D, 8 rows] += v^T p'
+// Codes are widened to f16 in registers (exact) as they come from shared memory.  The summation
+// index of k q^T and the rows of v^T may be taken in any order, which lets each lane read 16
+// contiguous bytes; the weights get from the layout of s' to that of p' by a transposition of
+// 8 x 8 tiles.  q (bf16) is moved to f16 by a power of two of its row (exact but for values
+// 2^-29 below the row's largest); weights are 2^14 of their size, rounded to f16 (2^-11 of their
+// value, 2^-39 of the largest).  (Products of e4m3 values as they are would need no widening,
+// but this part has them only on tcgen05: the warp-level form took 16 cycles for what two f16
+// products take, and its own widening.)
 //
 // A fifth warp deals out the pieces of the CTA's run and keeps a ring of stages of 64 tokens
 // filled by bulk copies; the four others work on them in pairs, 32 tokens a warp, with a
@@ -31,7 +33,7 @@ constexpr int FW_WARPS = 4;
 constexpr int FW_HALF = 64;             // tokens of a stage
 constexpr int FW_CTAS = 2;              // per SM
 constexpr int FW_SC_RING = 16, FW_PIECES = 4;
-constexpr float P_LOG2 = 14.f;          // log2 of the largest weight's value
+constexpr float P_LOG2 = 14.f;          // log2 of the largest weight as it is held
 
 template <int D, int RT>
 struct FewShape {
@@ -48,65 +50,34 @@ struct FewPiece {
   int whole, slot;  // as in kv8_attn.cu; chunks
 };
 
-// d += a b for a 16 x 32 tile a and a 32 x 8 tile b of 8-bit values; with NR = 1 the upper 8 rows
-// of a are zero, and their part of d is neither read nor kept.
-template <int NR>
-__device__ __forceinline__ void mma_k(float (&d)[2 * NR], const uint32_t (&a)[2 * NR], uint32_t b0, uint32_t b1) {
-  if constexpr (NR == 1) {
-    float z0, z1;
-    asm(
-        "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%6,%5,%6}, {%7,%8}, "
-        "{%0,%1,%9,%9};"
-        : "+f"(d[0]), "+f"(d[1]), "=f"(z0), "=f"(z1)
-        : "r"(a[0]), "r"(a[1]), "r"(0u), "r"(b0), "r"(b1), "f"(0.f));
-  } else {
-    asm(
-        "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-        "{%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[2]), "r"(a[1]), "r"(a[3]), "r"(b0), "r"(b1));
-  }
+// d += a b for a 16 x 16 tile a and a 16 x 8 tile b.
+__device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                      uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-template <int NR>
-__device__ __forceinline__ void mma_v(float (&d)[2 * NR], const uint32_t (&a)[2 * NR], uint32_t b0, uint32_t b1) {
-  if constexpr (NR == 1) {
-    float z0, z1;
-    asm(
-        "mma.sync.aligned.m16n8k32.row.col.f32.e5m2.e4m3.f32 {%0,%1,%2,%3}, {%4,%6,%5,%6}, {%7,%8}, "
-        "{%0,%1,%9,%9};"
-        : "+f"(d[0]), "+f"(d[1]), "=f"(z0), "=f"(z1)
-        : "r"(a[0]), "r"(a[1]), "r"(0u), "r"(b0), "r"(b1), "f"(0.f));
-  } else {
-    asm(
-        "mma.sync.aligned.m16n8k32.row.col.f32.e5m2.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-        "{%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[2]), "r"(a[1]), "r"(a[3]), "r"(b0), "r"(b1));
-  }
-}
-__device__ __forceinline__ uint16_t f16x2_to_e5m2x2(uint32_t x) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(r) : "r"(x));
-  return r;
-}
-__device__ __forceinline__ uint32_t e5m2x2_to_f16x2(uint16_t x) {
+// An 8 x 8 tile of 16-bit values, a row's pair a lane, transposed.
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
   uint32_t r;
-  asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(r) : "h"(x));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
 }
+__device__ __forceinline__ uint32_t lo_f16(uint32_t w) { return e4m3x2_to_f16x2(static_cast<uint16_t>(w)); }
+__device__ __forceinline__ uint32_t hi_f16(uint32_t w) { return e4m3x2_to_f16x2(static_cast<uint16_t>(w >> 16)); }
 __device__ __forceinline__ uint32_t any_nan4(uint32_t w) { return __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu); }
 
-// Rows of a tile in the matrix instruction's accumulator layout: lane (g, t) = (lane / 4, lane % 4)
-// holds rows g and g + 8.  D = head dimension, RT = rows (8 or 16: with 8 the upper half of
-// every product is zero and takes no registers).
+// In the products' layouts lane (g, t) = (lane / 4, lane % 4) holds the scores of tokens g and
+// g + 8 of a block of 16 against rows 2t and 2t + 1 (of 8), and of o' the columns g D / 8 ..
+// of the same rows.  D = head dimension, RT = rows (8 or 16).
 template <int D, int RT>
 __global__ void __launch_bounds__(32 * FW_WARPS + 32, FW_CTAS) kv8_few_kernel(const AttnParams p) {
   using S = FewShape<D, RT>;
-  constexpr int KW = D / 16;  // words of a key row a lane reads
-  constexpr int KS = D / 32;  // steps of 32 of q . k
+  constexpr int KW = D / 16;  // words of a key row a lane reads = steps of 16 of k q^T
   constexpr int VW = D / 32;  // words of a value row a lane reads
-  constexpr int NU = D / 8;   // output column groups
-  constexpr int NR = RT / 8;  // rows a lane holds
+  constexpr int NU = D / 16;  // tiles of o'
+  constexpr int NT = RT / 8;  // groups of 8 rows
   constexpr int ST = S::STAGES;
   extern __shared__ __align__(128) uint8_t fw_smem[];
   __shared__ __align__(8) uint64_t full[ST], empty[ST], pc_full[FW_PIECES], pc_empty[FW_PIECES], met, left;
@@ -252,16 +223,16 @@ __global__ void __launch_bounds__(32 * FW_WARPS + 32, FW_CTAS) kv8_few_kernel(co
     __syncwarp();
     if (lane == 0) mbar_arrive(&pc_empty[e]);
 
-    // q of this lane's rows, hi and lo, with the row's largest in [128, 256)
-    uint32_t qh[KS][2 * NR], ql[KS][2 * NR];
-    float f_row[NR];
-    int seen[NR];
+    // q of row g of each 8, as f16 of the row's largest power of two; rows 2t, 2t + 1 for the softmax
+    uint32_t qf[NT][KW][2];
+    float f_row[2 * NT];
+    int seen[2 * NT];
 #pragma unroll
-    for (int r = 0; r < NR; ++r) {
-      const int row = x.row0 + g + 8 * r;
-      const bool has = g + 8 * r < x.rows;
+    for (int n = 0; n < NT; ++n) {
+      const int row = x.row0 + 8 * n + g;
+      const bool has = 8 * n + g < x.rows;
       const int i = has ? row / p.group : 0, j = has ? row - i * p.group : 0;
-      seen[r] = has ? min(x.len - x.n + i + 1, x.end) : 0;
+      const int sees = has ? min(x.len - x.n + i + 1, x.end) : 0;
       const __nv_bfloat16* qr = p.q + (x.q0 + i) * p.q_tok + (x.h * p.group + j) * p.q_head;
       uint2 raw[KW];
       uint32_t top = 0;
@@ -274,36 +245,33 @@ __global__ void __launch_bounds__(32 * FW_WARPS + 32, FW_CTAS) kv8_few_kernel(co
       }
       top = max(top, __shfl_xor_sync(FULL_MASK, top, 1));
       top = max(top, __shfl_xor_sync(FULL_MASK, top, 2));
-      const int sh = min(7 - (min(max(static_cast<int>(top >> 7), 1), 254) - 127), 120);
+      // the largest moves to [2^14, 2^15); an infinite or NaN row stays so whatever the power
+      const int sh = min(14 - (min(max(static_cast<int>(top >> 7), 1), 254) - 127), 120);
       const float up = __uint_as_float(static_cast<uint32_t>(127 + sh) << 23);
-      f_row[r] = p.scale2 * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
+      const float f = p.scale2 * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
 #pragma unroll
       for (int k = 0; k < KW; ++k) {
-        const float y[4] = {__uint_as_float(raw[k].x << 16) * up, __uint_as_float(raw[k].x & 0xffff0000u) * up,
-                            __uint_as_float(raw[k].y << 16) * up, __uint_as_float(raw[k].y & 0xffff0000u) * up};
-        uint32_t hi = 0, lo = 0;
+        const __half2 a = __floats2half2_rn(__uint_as_float(raw[k].x << 16) * up,
+                                            __uint_as_float(raw[k].x & 0xffff0000u) * up);
+        const __half2 c = __floats2half2_rn(__uint_as_float(raw[k].y << 16) * up,
+                                            __uint_as_float(raw[k].y & 0xffff0000u) * up);
+        qf[n][k][0] = *reinterpret_cast<const uint32_t*>(&a);
+        qf[n][k][1] = *reinterpret_cast<const uint32_t*>(&c);
+      }
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          const uint16_t h2 = f32x2_to_e4m3x2(y[2 * n], y[2 * n + 1]);
-          const uint32_t b2 = e4m3x2_to_f16x2(h2);
-          const float2 f2 = __half22float2(*reinterpret_cast<const __half2*>(&b2));
-          hi |= uint32_t(h2) << (16 * n);
-          // a row with an infinity keeps it as NaN: 448 would be a value like any other
-          const float l0 = y[2 * n] - f2.x, l1 = y[2 * n + 1] - f2.y;
-          lo |= uint32_t(f32x2_to_e4m3x2(isinf(l0) ? NAN : l0, isinf(l1) ? NAN : l1)) << (16 * n);
-        }
-        qh[k / 2][2 * r + (k & 1)] = hi;
-        ql[k / 2][2 * r + (k & 1)] = lo;
+      for (int r = 0; r < 2; ++r) {
+        f_row[2 * n + r] = __shfl_sync(FULL_MASK, f, 4 * (2 * t + r));
+        seen[2 * n + r] = __shfl_sync(FULL_MASK, sees, 4 * (2 * t + r));
       }
     }
 
-    float m[NR], l[NR], o[NU][2 * NR];
+    float m[2 * NT], l[2 * NT], o[NT][NU][4];
 #pragma unroll
-    for (int r = 0; r < NR; ++r) { m[r] = -INFINITY; l[r] = 0.f; }
+    for (int r = 0; r < 2 * NT; ++r) { m[r] = -INFINITY; l[r] = 0.f; }
 #pragma unroll
-    for (int n = 0; n < NU; ++n)
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int k = 0; k < 2 * NR; ++k) o[n][k] = 0.f;
+      for (int c = 0; c < NU; ++c) o[n][c][0] = o[n][c][1] = o[n][c][2] = o[n][c][3] = 0.f;
 
     const int stages = x.hn - x.h0;
 #pragma unroll 1
@@ -311,160 +279,158 @@ __global__ void __launch_bounds__(32 * FW_WARPS + 32, FW_CTAS) kv8_few_kernel(co
       const int it = it0 + d, st = it % ST, slot = it % FW_SC_RING;
       const bool landed = wait(&full[st], (it / ST) & 1, ERR_KV8_FULL_WAIT);
       const int tok0 = (x.h0 + d) * FW_HALF + (warp & 1) * 32;
-      const PageScale sc[2] = {s_sc[slot][(warp & 1) * 2], s_sc[slot][(warp & 1) * 2 + 1]};
       if (landed && tok0 < x.end) {
+        const PageScale sc[2] = {s_sc[slot][(warp & 1) * 2], s_sc[slot][(warp & 1) * 2 + 1]};
         const uint8_t* kt = fw_smem + st * 2 * S::TILE + (warp & 1) * 32 * D;
         const uint8_t* vt = kt + S::TILE;
-        // ---- s of 32 tokens, in four groups of 8
-        float s[4][2 * NR];
+        // ---- s' of two blocks of 16 tokens
+        float s[NT][2][4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint32_t kw[KW];
-          const uint8_t* kr = kt + (8 * j + g) * D;
-          if constexpr (D == 128) {
-            // 128-byte rows share banks: odd rows take the other half first
-            const int sw = (g & 1) * 64;
-            const uint4 a = *reinterpret_cast<const uint4*>(kr + t * 16 + sw);
-            const uint4 b = *reinterpret_cast<const uint4*>(kr + t * 16 + 64 - sw);
-            const uint4 lo = sw ? b : a, hi = sw ? a : b;
-            kw[0] = lo.x; kw[1] = lo.y; kw[2] = lo.z; kw[3] = lo.w;
-            kw[4] = hi.x; kw[5] = hi.y; kw[6] = hi.z; kw[7] = hi.w;
-          } else if constexpr (D == 64) {
-            const uint4 a = *reinterpret_cast<const uint4*>(kr + t * 16);
-            kw[0] = a.x; kw[1] = a.y; kw[2] = a.z; kw[3] = a.w;
-          } else {
-            const uint2 a = *reinterpret_cast<const uint2*>(kr + t * 8);
-            kw[0] = a.x; kw[1] = a.y;
+        for (int k = 0; k < 2; ++k) {
+          uint32_t kw[2][KW];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const uint8_t* kr = kt + (16 * k + 8 * j + g) * D;
+            if constexpr (D == 128) {
+              // 128-byte rows share banks: odd rows take the other half first
+              const int sw = (g & 1) * 64;
+              const uint4 a = *reinterpret_cast<const uint4*>(kr + t * 16 + sw);
+              const uint4 b = *reinterpret_cast<const uint4*>(kr + t * 16 + 64 - sw);
+              const uint4 lo = sw ? b : a, hi = sw ? a : b;
+              kw[j][0] = lo.x; kw[j][1] = lo.y; kw[j][2] = lo.z; kw[j][3] = lo.w;
+              kw[j][4] = hi.x; kw[j][5] = hi.y; kw[j][6] = hi.z; kw[j][7] = hi.w;
+            } else if constexpr (D == 64) {
+              const uint4 a = *reinterpret_cast<const uint4*>(kr + t * 16);
+              kw[j][0] = a.x; kw[j][1] = a.y; kw[j][2] = a.z; kw[j][3] = a.w;
+            } else {
+              const uint2 a = *reinterpret_cast<const uint2*>(kr + t * 8);
+              kw[j][0] = a.x; kw[j][1] = a.y;
+            }
           }
 #pragma unroll
-          for (int k = 0; k < 2 * NR; ++k) s[j][k] = 0.f;
+          for (int n = 0; n < NT; ++n) s[n][k][0] = s[n][k][1] = s[n][k][2] = s[n][k][3] = 0.f;
 #pragma unroll
-          for (int k = 0; k < KS; ++k) {
-            mma_k<NR>(s[j], qh[k], kw[2 * k], kw[2 * k + 1]);
-            mma_k<NR>(s[j], ql[k], kw[2 * k], kw[2 * k + 1]);
+          for (int i = 0; i < KW; ++i) {
+            const uint32_t a0 = lo_f16(kw[0][i]), a1 = lo_f16(kw[1][i]), a2 = hi_f16(kw[0][i]), a3 = hi_f16(kw[1][i]);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma16(s[n][k], a0, a1, a2, a3, qf[n][i][0], qf[n][i][1]);
           }
         }
-        // ---- softmax, and the weights as three e5m2 values
-        uint32_t p1[2 * NR], p2[2 * NR], p3[2 * NR];
+        // ---- softmax
         const bool masks = tok0 + 32 > x.len - x.n || !sc[0].ok || !sc[1].ok;
+        uint32_t pf[NT][2][2];
 #pragma unroll
-        for (int r = 0; r < NR; ++r) {
-          float y[8];
+        for (int n = 0; n < NT; ++n) {
+          float y[2][4];  // of row 2t + r: tokens g, g + 8 of either block
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const float f = f_row[r] * sc[k].k;
+          for (int r = 0; r < 2; ++r) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) y[4 * k + i] = fmaf(s[2 * k + (i >> 1)][2 * r + (i & 1)], f, sc[k].log2_v);
+            for (int k = 0; k < 2; ++k) {
+              const float f = f_row[2 * n + r] * sc[k].k;
+              y[r][2 * k] = fmaf(s[n][k][r], f, sc[k].log2_v);
+              y[r][2 * k + 1] = fmaf(s[n][k][2 + r], f, sc[k].log2_v);
+            }
+            if (masks) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (tok0 + 8 * i + g >= seen[2 * n + r] || !sc[i >> 1].ok) y[r][i] = -INFINITY;
+            }
           }
+          float mx[2];
+#pragma unroll
+          for (int r = 0; r < 2; ++r) mx[r] = fmaxf(fmaxf(y[r][0], y[r][1]), fmaxf(y[r][2], y[r][3]));
+#pragma unroll
+          for (int q = 4; q < 32; q <<= 1) {
+            mx[0] = fmaxf(mx[0], __shfl_xor_sync(FULL_MASK, mx[0], q));
+            mx[1] = fmaxf(mx[1], __shfl_xor_sync(FULL_MASK, mx[1], q));
+          }
+          float* mr = m + 2 * n;
+          float* lr = l + 2 * n;
+          if (mx[0] > mr[0] || mx[1] > mr[1]) {
+            const float n0 = fmaxf(mr[0], mx[0]), n1 = fmaxf(mr[1], mx[1]);
+            const float f0 = n0 == -INFINITY ? 1.f : ex2(mr[0] - n0), f1 = n1 == -INFINITY ? 1.f : ex2(mr[1] - n1);
+            lr[0] *= f0;
+            lr[1] *= f1;
+#pragma unroll
+            for (int c = 0; c < NU; ++c) { o[n][c][0] *= f0; o[n][c][1] *= f1; o[n][c][2] *= f0; o[n][c][3] *= f1; }
+            mr[0] = n0;
+            mr[1] = n1;
+          }
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const float base = mr[r] == -INFINITY ? 0.f : P_LOG2 - mr[r];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) y[r][i] = ex2(y[r][i] + base);
+            lr[r] = fmaf(y[r][0] + y[r][1], sc[0].inv_v, lr[r]);
+            lr[r] = fmaf(y[r][2] + y[r][3], sc[1].inv_v, lr[r]);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const __half2 h = __floats2half2_rn(y[0][i], y[1][i]);
+            pf[n][i >> 1][i & 1] = transposed(*reinterpret_cast<const uint32_t*>(&h));
+          }
+        }
+        // ---- o' += v^T p', by blocks of 16 tokens
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          uint32_t vw[4][VW];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint8_t* vr = vt + (16 * k + 2 * t + (j & 1) + 8 * (j >> 1)) * D + g * (D / 8);
+            if constexpr (D == 128) {
+              const uint4 a = *reinterpret_cast<const uint4*>(vr);
+              vw[j][0] = a.x; vw[j][1] = a.y; vw[j][2] = a.z; vw[j][3] = a.w;
+            } else if constexpr (D == 64) {
+              const uint2 a = *reinterpret_cast<const uint2*>(vr);
+              vw[j][0] = a.x; vw[j][1] = a.y;
+            } else {
+              vw[j][0] = *reinterpret_cast<const uint32_t*>(vr);
+            }
+          }
+          // Tokens that some row of the tile does not see (the causal edge, what lies behind the
+          // last token, and pages that were not loaded): 0 * NaN is NaN, so their values take part
+          // without NaN, and rows that do see a NaN get it afterwards.
+          bool fix = false;
           if (masks) {
+            uint32_t nan = 0;
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              if (tok0 + 8 * (i >> 1) + 2 * t + (i & 1) >= seen[r] || !sc[i >> 2].ok) y[i] = -INFINITY;
-          }
-          float mx = fmaxf(fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])), fmaxf(fmaxf(y[4], y[5]), fmaxf(y[6], y[7])));
-          mx = fmaxf(mx, __shfl_xor_sync(FULL_MASK, mx, 1));
-          mx = fmaxf(mx, __shfl_xor_sync(FULL_MASK, mx, 2));
-          const float nm = fmaxf(m[r], mx);
-          if (nm != m[r]) {  // uniform over the four lanes of the row
-            const float back = ex2(m[r] - nm);
-            l[r] *= back;
+            for (int j = 0; j < 4; ++j) {
+              const bool in = tok0 + 16 * k + 2 * t + (j & 1) + 8 * (j >> 1) < x.end && sc[k].ok;
 #pragma unroll
-            for (int n = 0; n < NU; ++n) { o[n][2 * r] *= back; o[n][2 * r + 1] *= back; }
-            m[r] = nm;
-          }
-          const float base = nm == -INFINITY ? 0.f : P_LOG2 - nm;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) y[i] = ex2(y[i] + base);
-          l[r] = fmaf((y[0] + y[1]) + (y[2] + y[3]), sc[0].inv_v, l[r]);
-          l[r] = fmaf((y[4] + y[5]) + (y[6] + y[7]), sc[1].inv_v, l[r]);
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            uint32_t w[3] = {0u, 0u, 0u};
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              __half2 rest = __floats2half2_rn(y[4 * k + 2 * i], y[4 * k + 2 * i + 1]);
-#pragma unroll
-              for (int n = 0; n < 3; ++n) {
-                const uint16_t c2 = f16x2_to_e5m2x2(*reinterpret_cast<const uint32_t*>(&rest));
-                w[n] |= uint32_t(c2) << (16 * i);
-                if (n < 2) {
-                  const uint32_t b2 = e5m2x2_to_f16x2(c2);
-                  rest = __hsub2(rest, *reinterpret_cast<const __half2*>(&b2));
-                }
+              for (int i = 0; i < VW; ++i) {
+                if (!in) vw[j][i] = 0u;
+                const uint32_t bad = any_nan4(vw[j][i]);
+                nan |= bad;
+                vw[j][i] &= ~bad;
               }
             }
-            p1[2 * r + k] = w[0];
-            p2[2 * r + k] = w[1];
-            p3[2 * r + k] = w[2];
+            fix = __any_sync(FULL_MASK, nan != 0);
           }
-        }
-        // ---- o += p v, V in two halves of 16 tokens (the first and the second register of b)
-        uint32_t vw[8][VW];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const uint8_t* vr = vt + (2 * t + (j & 1) + 8 * (j >> 1)) * D + g * (D / 8);
-          if constexpr (D == 128) {
-            const uint4 a = *reinterpret_cast<const uint4*>(vr);
-            vw[j][0] = a.x; vw[j][1] = a.y; vw[j][2] = a.z; vw[j][3] = a.w;
-          } else if constexpr (D == 64) {
-            const uint2 a = *reinterpret_cast<const uint2*>(vr);
-            vw[j][0] = a.x; vw[j][1] = a.y;
-          } else {
-            vw[j][0] = *reinterpret_cast<const uint32_t*>(vr);
-          }
-        }
-        // Tokens that some row of the tile does not see (the causal edge, what lies behind the last
-        // token, and pages that were not loaded): 0 * NaN is NaN, so their values take part
-        // without NaN, and rows that do see a NaN get it afterwards.
-        bool fix = false;
-        if (masks) {
-          uint32_t nan = 0;
+          for (int i = 0; i < VW; ++i) {
+            const uint32_t a = __byte_perm(vw[0][i], vw[1][i], 0x5140), b = __byte_perm(vw[2][i], vw[3][i], 0x5140);
+            const uint32_t c = __byte_perm(vw[0][i], vw[1][i], 0x7362), e2 = __byte_perm(vw[2][i], vw[3][i], 0x7362);
+            const uint32_t a0 = lo_f16(a), a1 = hi_f16(a), a2 = lo_f16(b), a3 = hi_f16(b);
+            const uint32_t c0 = lo_f16(c), c1 = hi_f16(c), c2 = lo_f16(e2), c3 = hi_f16(e2);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const bool in = tok0 + 2 * t + (j & 1) + 8 * (j >> 1) < x.end && sc[j >> 2].ok;
-#pragma unroll
-            for (int k = 0; k < VW; ++k) {
-              if (!in) vw[j][k] = 0u;
-              const uint32_t bad = any_nan4(vw[j][k]);
-              nan |= bad;
-              vw[j][k] &= ~bad;
+            for (int n = 0; n < NT; ++n) {
+              mma16(o[n][2 * i], a0, a1, a2, a3, pf[n][k][0], pf[n][k][1]);
+              mma16(o[n][2 * i + 1], c0, c1, c2, c3, pf[n][k][0], pf[n][k][1]);
             }
           }
-          fix = __any_sync(FULL_MASK, nan != 0);
-        }
-#pragma unroll
-        for (int k = 0; k < VW; ++k) {
-          uint32_t b[2][4];  // of columns 4k .. 4k + 3 of this lane's, four tokens a register
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            const uint32_t a0 = __byte_perm(vw[4 * q][k], vw[4 * q + 1][k], 0x5140);
-            const uint32_t a1 = __byte_perm(vw[4 * q + 2][k], vw[4 * q + 3][k], 0x5140);
-            const uint32_t c0 = __byte_perm(vw[4 * q][k], vw[4 * q + 1][k], 0x7362);
-            const uint32_t c1 = __byte_perm(vw[4 * q + 2][k], vw[4 * q + 3][k], 0x7362);
-            b[q][0] = __byte_perm(a0, a1, 0x5410);
-            b[q][1] = __byte_perm(a0, a1, 0x7632);
-            b[q][2] = __byte_perm(c0, c1, 0x5410);
-            b[q][3] = __byte_perm(c0, c1, 0x7632);
-          }
-#pragma unroll
-          for (int n = 0; n < 4; ++n) mma_v<NR>(o[4 * k + n], p1, b[0][n], b[1][n]);
-#pragma unroll
-          for (int n = 0; n < 4; ++n) mma_v<NR>(o[4 * k + n], p2, b[0][n], b[1][n]);
-#pragma unroll
-          for (int n = 0; n < 4; ++n) mma_v<NR>(o[4 * k + n], p3, b[0][n], b[1][n]);
-        }
-        if (fix) {
+          if (fix) {
 #pragma unroll 1
-          for (int tk = 0; tk < 32 && tok0 + tk < x.end; ++tk) {
-            if (!sc[tk >> 4].ok) continue;
-#pragma unroll
-            for (int n = 0; n < 2; ++n)
+            for (int tk = 0; tk < 16 && tok0 + 16 * k + tk < x.end; ++tk)
 #pragma unroll
               for (int c = 0; c < NU; ++c)
-                if ((vt[tk * D + (2 * t + n) * NU + c] & 0x7f) == 0x7f)
 #pragma unroll
-                  for (int r = 0; r < NR; ++r)
-                    if (tok0 + tk < seen[r]) o[c][2 * r + n] = NAN;
+                for (int i = 0; i < 2; ++i)
+                  if ((vt[(16 * k + tk) * D + g * (D / 8) + 2 * c + i] & 0x7f) == 0x7f)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                      for (int r = 0; r < 2; ++r)
+                        if (tok0 + 16 * k + tk < seen[2 * n + r]) o[n][c][2 * i + r] = NAN;
           }
         }
       }
@@ -474,20 +440,18 @@ __global__ void __launch_bounds__(32 * FW_WARPS + 32, FW_CTAS) kv8_few_kernel(co
 
     // ---- the warps together: each scales its products to the row's largest maximum; in order
 #pragma unroll
-    for (int r = 0; r < NR; ++r) {
-      l[r] += __shfl_xor_sync(FULL_MASK, l[r], 1);
-      l[r] += __shfl_xor_sync(FULL_MASK, l[r], 2);
-      if (t == 0) { s_m[warp][g + 8 * r] = m[r]; s_l[warp][g + 8 * r] = l[r]; }
-    }
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-    for (int r = 0; r < NR; ++r)
+      for (int r = 0; r < 2; ++r) {
+        float sum = l[2 * n + r];
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        float* dst = &s_o[warp][g + 8 * r][(2 * t + k) * NU];
+        for (int q = 4; q < 32; q <<= 1) sum += __shfl_xor_sync(FULL_MASK, sum, q);
+        const int row = 8 * n + 2 * t + r;
+        if (g == 0) { s_m[warp][row] = m[2 * n + r]; s_l[warp][row] = sum; }
+        float* dst = &s_o[warp][row][g * (D / 8)];
 #pragma unroll
-        for (int n = 0; n < NU; n += 4)
-          *reinterpret_cast<float4*>(dst + n) = make_float4(o[n][2 * r + k], o[n + 1][2 * r + k],
-                                                            o[n + 2][2 * r + k], o[n + 3][2 * r + k]);
+        for (int c = 0; c < NU; c += 2)
+          *reinterpret_cast<float4*>(dst + 2 * c) = make_float4(o[n][c][r], o[n][c][2 + r], o[n][c + 1][r], o[n][c + 1][2 + r]);
       }
     __syncwarp();
     if (lane == 0) mbar_arrive(&met);
