@@ -162,6 +162,11 @@ constexpr uint32_t tc_idesc(int M, int N, bool a_mn, bool b_mn) {
          (uint32_t(M >> 4) << 24);
 }
 
+__device__ __forceinline__ uint16_t f16x2_to_e4m3x2(uint32_t x) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(x));
+  return r;
+}
 __device__ __forceinline__ uint32_t nan_codes(uint32_t w) {  // 0xff in each byte that is NaN
   return __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu);
 }
@@ -444,42 +449,52 @@ __global__ void __launch_bounds__(32 * AttnShape<D, ROWS>::WARPS, 1)
       if (lane == 0) piece_read(pi);
       if (x.c0 >= x.cn) continue;
       {
-        constexpr int LPR = D / 4, RPW = 32 / LPR;  // lanes of a row (4 values each), rows of a warp at a time
+        // lanes of a row (8 values each), rows of a warp at a time, and of all four
+        constexpr int LPR = D / 8, RPW = 32 / LPR, STEP = 4 * RPW;
         if (qi >= QB) wait_warp(&qfree[qi % QB], ((qi / QB) - 1) & 1, ERR_KV8_S_WAIT);
         uint8_t* qh = sm + S::OFF_Q + (qi % QB) * 2 * S::QT;
-        const int col = (lane % LPR) * 4;
-#pragma unroll 2
-        for (int r = k * RPW + lane / LPR; r < ((x.rows + 4 * RPW - 1) & ~(4 * RPW - 1)); r += 4 * RPW) {
-          const bool has = r < x.rows;
-          const int row = has ? x.row0 + r : 0, i = row / p.group;
-          const uint2 w = has ? __ldg(reinterpret_cast<const uint2*>(
-                                    p.q + (x.q0 + i) * p.q_tok + (x.h * p.group + row - i * p.group) * p.q_head + col))
-                              : make_uint2(0u, 0u);
-          uint32_t top = max(max(w.x & 0x7fffu, (w.x >> 16) & 0x7fffu), max(w.y & 0x7fffu, (w.y >> 16) & 0x7fffu));
+        const int col = (lane % LPR) * 8, r0 = k * RPW + lane / LPR;
+        int i = (x.row0 + r0) / p.group, j = x.row0 + r0 - i * p.group;
+#pragma unroll 1
+        for (int rb = 0; rb < x.rows; rb += 4 * STEP) {
+          uint4 w[4];
 #pragma unroll
-          for (int o = LPR / 2; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(FULL_MASK, top, o));
-          // the largest moves to [128, 256)
-          const int sh = min(7 - (min(max(static_cast<int>(top >> 7), 1), 254) - 127), 120);
-          const float up = __uint_as_float(static_cast<uint32_t>(127 + sh) << 23);
-          if (has && col == 0)
-            s_fr[qi % PIECE_RING][r] = p.scale2 * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
-          const float y[4] = {__uint_as_float(w.x << 16) * up, __uint_as_float(w.x & 0xffff0000u) * up,
-                              __uint_as_float(w.y << 16) * up, __uint_as_float(w.y & 0xffff0000u) * up};
-          uint32_t hi = 0, lo = 0;
-#pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            const uint16_t h2 = f32x2_to_e4m3x2(y[2 * n], y[2 * n + 1]);
-            const uint32_t b2 = e4m3x2_to_f16x2(h2);
-            const float2 f2 = __half22float2(*reinterpret_cast<const __half2*>(&b2));
-            hi |= uint32_t(h2) << (16 * n);
-            // a row with an infinity keeps it as NaN: 448 would be a value like any other
-            const float l0 = y[2 * n] - f2.x, l1 = y[2 * n + 1] - f2.y;
-            lo |= uint32_t(f32x2_to_e4m3x2(isinf(l0) ? NAN : l0, isinf(l1) ? NAN : l1)) << (16 * n);
+          for (int n = 0; n < 4; ++n) {  // (the loads of four rounds together)
+            w[n] = make_uint4(0u, 0u, 0u, 0u);
+            if (rb + n * STEP + r0 < x.rows)
+              w[n] = __ldg(reinterpret_cast<const uint4*>(p.q + (x.q0 + i) * p.q_tok + (x.h * p.group + j) * p.q_head + col));
+            for (j += STEP; j >= p.group; j -= p.group) ++i;
           }
-          if (r < ROWS) {
-            const int at = r * D + ((((col >> 4) ^ swz<D>(r)) << 4) | (col & 15));
-            *reinterpret_cast<uint32_t*>(qh + at) = hi;
-            *reinterpret_cast<uint32_t*>(qh + S::QT + at) = lo;
+#pragma unroll
+          for (int n = 0; n < 4; ++n) {
+            const int r = rb + n * STEP + r0;
+            const uint32_t in[4] = {w[n].x, w[n].y, w[n].z, w[n].w};
+            uint32_t top = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) top = max(top, max(in[e] & 0x7fffu, (in[e] >> 16) & 0x7fffu));
+#pragma unroll
+            for (int o = LPR / 2; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(FULL_MASK, top, o));
+            // the largest moves to [128, 256); a row with an infinity or a NaN is all NaN
+            const int sh = min(7 - (min(max(static_cast<int>(top >> 7), 1), 254) - 127), 120);
+            const float up = __uint_as_float(static_cast<uint32_t>(127 + sh) << 23);
+            uint32_t hi[2] = {0u, 0u}, lo[2] = {0u, 0u};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const __half2 y = __floats2half2_rn(__uint_as_float(in[e] << 16) * up,
+                                                  __uint_as_float(in[e] & 0xffff0000u) * up);
+              const uint16_t h2 = f16x2_to_e4m3x2(*reinterpret_cast<const uint32_t*>(&y));
+              const uint32_t b2 = e4m3x2_to_f16x2(h2);
+              const __half2 rest = __hsub2(y, *reinterpret_cast<const __half2*>(&b2));
+              hi[e >> 1] |= uint32_t(h2) << (16 * (e & 1));
+              lo[e >> 1] |= uint32_t(f16x2_to_e4m3x2(*reinterpret_cast<const uint32_t*>(&rest))) << (16 * (e & 1));
+            }
+            if (r < x.rows) {
+              if (col == 0)
+                s_fr[qi % PIECE_RING][r] = top >= 0x7f80u ? NAN : p.scale2 * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
+              const int at = r * D + ((((col >> 4) ^ swz<D>(r)) << 4) | (col & 15));
+              *reinterpret_cast<uint2*>(qh + at) = make_uint2(hi[0], hi[1]);
+              *reinterpret_cast<uint2*>(qh + S::QT + at) = make_uint2(lo[0], lo[1]);
+            }
           }
         }
         fence_async_smem();
