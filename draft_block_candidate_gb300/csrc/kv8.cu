@@ -278,9 +278,10 @@ lilicorr_status lilicorr_kv8_attention(const lilicorr_kv8_cache* cache, const vo
   if (!why && (!out || reinterpret_cast<uintptr_t>(out) % 16)) why = "out is null or not 16-byte aligned";
   if (!why && (q_heads < 1 || q_heads % cache->kv_heads || q_heads / cache->kv_heads > 1024))
     why = "q_heads is a multiple of kv_heads, at most 1024 times it";
-  // one sequence's work units (tiles x heads x chunks of 64 tokens) are counted in 32 bits
+  // one sequence's work units (tiles x heads x chunks of tokens, and some for each tile) are
+  // counted in 32 bits
   if (!why && (int64_t(max_new) * (q_heads / cache->kv_heads) / 8 + 1) * cache->kv_heads *
-                  ((int64_t(cols) * cache->page + 63) / 64) > UINT_MAX)
+                  ((int64_t(cols) * cache->page + 127) / 128 + 4) > UINT_MAX)
     why = "max_new * q_heads * the table's tokens are too large";
   if (!why && !std::isfinite(scale)) why = "scale is not finite";
   if (why) return fail(LILICORR_ERR_INVALID_ARG, why);

@@ -67,24 +67,28 @@ __device__ __forceinline__ void tc_fence_after() {
 __device__ __forceinline__ void fence_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
+// (products and commits are called by a whole warp and issued by one elected lane: with the
+// warp together the compiler keeps their operands in uniform registers, where an issue by a
+// single lane took 80 cycles each)
 __device__ __forceinline__ void tc_commit(uint64_t* bar) {
   asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
           smem_addr(bar))
       : "memory");
 }
 __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
       "l"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u)
       : "memory");
 }
 // A from tensor memory (packed f16 pairs, one row a lane), B from shared memory.
 __device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
       "r"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u)
       : "memory");
 }
@@ -101,21 +105,30 @@ __device__ __forceinline__ void tmem_ld16(uint32_t t, float* v) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
-__device__ __forceinline__ void tmem_ld32(uint32_t t, float* v) {
-  uint32_t r[32];
+// The same for 32 columns in two steps: what is read may be used after tmem_ld_end of it, which
+// ends all reads of the warp.
+__device__ __forceinline__ void tmem_ld32_begin(uint32_t t, float* v) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
       "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
       "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
-        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
-        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
+        "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]),
+        "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]),
+        "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]),
+        "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
       : "r"(t));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_ld_end(float* v) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]),
+                 "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]),
+                 "+f"(v[14]), "+f"(v[15]), "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]),
+                 "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]), "+f"(v[24]), "+f"(v[25]),
+                 "+f"(v[26]), "+f"(v[27]), "+f"(v[28])
+               :
+               : "memory");
+  asm volatile("" : "+f"(v[29]), "+f"(v[30]), "+f"(v[31]));
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
@@ -176,9 +189,9 @@ __device__ __forceinline__ uint32_t nan_codes(uint32_t w) {  // 0xff in each byt
 template <int D, int ROWS>
 struct AttnShape {
   static constexpr int KT = AT_CHUNK * D;               // bytes of a chunk's keys, or values
-  static constexpr int STAGES = D < 128 ? 4 : 3;
+  static constexpr int STAGES = D < 128 ? 4 : 2;
   static constexpr int VW = 2 * KT;                     // widened values; two buffers
-  static constexpr int QB = ROWS == 32 ? 2 : 1;         // buffers of q
+  static constexpr int QB = 2;                          // buffers of q
   static constexpr int QT = ROWS * D;                   // bytes of q hi, or lo
   static constexpr int OFF_V = STAGES * 2 * KT;
   static constexpr int OFF_Q = OFF_V + 2 * VW;
@@ -214,6 +227,17 @@ __device__ __forceinline__ Role role_of(int warp, int& k) {
 constexpr int SC_RING = 8, PIECE_RING = 4;  // deeper than any warp runs ahead of the softmax
 constexpr float RAISE = 14.f;               // log2 of how far a score may pass its reference
 
+// A piece of the CTA's run: the chunks [c0, cn) of a tile that some row of it sees.
+struct Piece {
+  int64_t q0;         // the sequence's first row of q
+  int64_t table;      // its row of the block table, as an offset
+  int n, len;         // its new tokens and its cached ones
+  int h, row0, rows;  // key / value head; the tile's first row and its rows
+  int c0, cn, end;    // tokens that the tile's last row sees
+  int whole;          // 1: all of the tile's chunks; 0: a part; -1: there is no further piece
+  int slot;           // of the workspace, for a part
+};
+
 template <int D, int ROWS>
 __global__ void __launch_bounds__(32 * AttnShape<D, ROWS>::WARPS, 1)
     kv8_attention_kernel(const __grid_constant__ CUtensorMap tm, const AttnParams p) {
@@ -226,11 +250,11 @@ __global__ void __launch_bounds__(32 * AttnShape<D, ROWS>::WARPS, 1)
   __shared__ Piece s_piece[PIECE_RING];
   __shared__ PageScale s_sc[SC_RING][8];
   __shared__ float s_fr[PIECE_RING][ROWS], s_m[2][ROWS], s_l[2][ROWS];
-  __shared__ int s_nan[PIECE_RING];  // a NaN was taken out of V
+  __shared__ int s_nan[PIECE_RING];  // 1 + the piece in whose V a NaN was taken out
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_fail;
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(FULL_MASK, tid >> 5, 0), lane = tid & 31;
   int k;
   const Role role = role_of<ROWS>(warp, k);
   if (tid == 0) {
@@ -261,7 +285,7 @@ __global__ void __launch_bounds__(32 * AttnShape<D, ROWS>::WARPS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = s_tmem;
+  const uint32_t tmem = __shfl_sync(FULL_MASK, s_tmem, 0);
   pdl_wait();
   pdl_trigger();
 
@@ -284,42 +308,33 @@ __global__ void __launch_bounds__(32 * AttnShape<D, ROWS>::WARPS, 1)
     // ====== the run's pieces, and their chunks: lane i brings the i-th page of a chunk ======
     const Run run = find_run<ROWS>(p, blockIdx.x, gridDim.x);
     const int part = p.c.page, parts = AT_CHUNK >> p.page_log2, bytes = part * D;
-    int64_t b = run.b, u = run.u;
-    SeqUnits sq{};
-    int tile = 0, h = 0, c0 = 0;
-    if (u < run.u_end) {
-      sq = seq_units<ROWS>(p, b);
-      const uint32_t in = static_cast<uint32_t>(u - run.first);  // a sequence's units fit 32 bits (host)
-      const uint32_t item = in / sq.chunks;
-      c0 = static_cast<int>(in - item * sq.chunks);
-      h = item / sq.tiles;
-      tile = item - h * sq.tiles;
-    }
+    Pieces<ROWS> w(p, run);
     int it = 0, pi = 0;
-    bool ok_run = true;
-    while (ok_run) {
+    // Pieces are left one ahead of the one that is loaded, so that its q can be made ready.
+    auto leave = [&](Piece& x) -> bool {
       const int e = pi % PIECE_RING;
-      if (pi >= PIECE_RING) ok_run = wait_warp(&pc_empty[e], ((pi / PIECE_RING) - 1) & 1, ERR_KV8_EMPTY_WAIT);
-      if (!ok_run || u >= run.u_end) {
-        if (lane == 0) s_piece[e].whole = -1;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&pc_full[e]);
-        break;
+      bool ok = pi < PIECE_RING || wait_warp(&pc_empty[e], ((pi / PIECE_RING) - 1) & 1, ERR_KV8_EMPTY_WAIT);
+      ok = ok && w.next();
+      if (ok) {
+        const int end = w.end(), cn = max(w.c0, min(w.c1, (end + AT_CHUNK - 1) / AT_CHUNK));
+        x = Piece{w.psq.q0, w.pb * p.table_stride, w.psq.n, w.psq.len, w.ph, w.ptile * ROWS, w.rows(),
+                  w.c0, cn, end, w.whole(), w.slot()};
+      } else {
+        x.whole = -1;
       }
-      while (sq.units == 0) sq = seq_units<ROWS>(p, ++b);  // sequences without new tokens
-      const int c1 = static_cast<int>(min(int64_t(sq.chunks), c0 + (run.u_end - u)));
-      const int rows = min(ROWS, sq.n * p.group - tile * ROWS);
-      const int end = max(0, min(sq.len, sq.len - sq.n + (tile * ROWS + rows - 1) / p.group + 1));
-      const int cn = max(c0, min(c1, (end + AT_CHUNK - 1) / AT_CHUNK));
-      const int64_t table = b * p.table_stride;
-      if (lane == 0)
-        s_piece[e] = Piece{sq.q0, table, sq.n, sq.len, h, tile * ROWS, rows, c0, cn, end,
-                           c0 == 0 && c1 == sq.chunks ? 1 : 0, 2 * static_cast<int>(blockIdx.x) + (pi > 0)};
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&pc_full[e]);
+      if (lane == 0) {
+        s_piece[e] = x;
+        mbar_arrive(&pc_full[e]);
+      }
       ++pi;
-
-      const int32_t* tab = p.table + table;
+      return ok;
+    };
+    Piece now{}, next{};
+    bool ok_run = leave(now);
+    while (ok_run) {
+      const bool more = leave(next);
+      const int c0 = now.c0, cn = now.cn, end = now.end, h = now.h;
+      const int32_t* tab = p.table + now.table;
       auto page_of = [&](int c) {
         const int tok = c * AT_CHUNK + lane * part;
         return lane < parts && c < cn && tok < end ? __ldg(tab + (tok >> p.page_log2)) : -2;
@@ -362,145 +377,143 @@ __global__ void __launch_bounds__(32 * AttnShape<D, ROWS>::WARPS, 1)
           bulk_g2s(dst + S::KT, p.c.v + ph * bytes, bytes, &full[st]);
         }
       }
-      // on to the next tile
-      u += c1 - c0;
-      c0 = c1;
-      if (c0 == sq.chunks) {
-        c0 = 0;
-        if (++tile == sq.tiles) {
-          tile = 0;
-          if (++h == p.c.heads) {
-            h = 0;
-            if (u < run.u_end) sq = seq_units<ROWS>(p, ++b);
-          }
-        }
-      }
+      now = next;
+      ok_run = ok_run && more;
     }
-    if (!ok_run || s_fail)  // what is in flight has to land
+    if (s_fail)  // what is in flight has to land
       for (int i = max(0, it - ST); i < it; ++i)
         mbar_wait_bounded(&full[i % ST], (i / ST) & 1, &g_err_kv8_attn, ERR_KV8_EMPTY_WAIT);
   } else if (role == S_MMA) {
     // ================= S = Q K^T, hi and lo =================
-    if (lane == 0) {
-      constexpr uint32_t ID = tc_idesc(128, AT_CHUNK, false, false);
-      const uint64_t d_k = tile_desc<D>(sm, 16), d_q = tile_desc<D>(sm + S::OFF_Q, 16);
-      int it = 0, qi = 0;
-      Piece x;
-      for (int pi = 0; next_piece(pi, x); ++pi) {
-        piece_read(pi);
-        if (x.c0 >= x.cn) continue;
-        bool ok = wait(&qready[qi % QB], (qi / QB) & 1, ERR_KV8_S_WAIT);
-        const uint64_t q = d_q + ((qi % QB) * 2 * S::QT >> 4);
-#pragma unroll 1
-        for (int c = x.c0; c < x.cn; ++c, ++it) {
-          const int st = it % ST, b = it & 1;
-          ok = wait(&full[st], (it / ST) & 1, ERR_KV8_FULL_WAIT) && ok;
-          if (it >= 2) ok = wait(&pvdone[b], ((it >> 1) - 1) & 1, ERR_KV8_S_WAIT) && ok;
-          if (ok) {
-            tc_fence_after();
-            const uint64_t kk = d_k + (st * 2 * S::KT >> 4);
-#pragma unroll
-            for (int d = 0; d < D / 32; ++d) mma_f8(tmem + b * TMEM_S, q + 2 * d, kk + 2 * d, ID, d > 0);
-#pragma unroll
-            for (int d = 0; d < D / 32; ++d)
-              mma_f8(tmem + b * TMEM_S, q + (S::QT >> 4) + 2 * d, kk + 2 * d, ID, true);
-          }
-          tc_commit(&sready[b]);
-          tc_commit(&empty[st]);
-        }
-        tc_commit(&qfree[qi % QB]);
-        ++qi;
-      }
-    }
-    __syncwarp();
-  } else if (role == O_MMA) {
-    // ================= O += P V =================
-    if (lane == 0) {
-      constexpr uint32_t ID = tc_idesc(128, D, false, true);
-      constexpr int VBY = D < 64 ? 64 : 128;  // bytes of a row of a tile of V
-      const uint64_t d_v = tile_desc<VBY>(sm + S::OFF_V, AT_CHUNK * 128);
-      int it = 0;
-      Piece x;
-      for (int pi = 0; next_piece(pi, x); ++pi) {
-        piece_read(pi);
-#pragma unroll 1
-        for (int c = x.c0; c < x.cn; ++c, ++it) {
-          const int b = it & 1;
-          bool ok = wait(&vready[b], (it >> 1) & 1, ERR_KV8_PV_WAIT);
-          ok = wait(&pready[b], (it >> 1) & 1, ERR_KV8_PV_WAIT) && ok;
-          if (ok) {
-            tc_fence_after();
-            const uint64_t v = d_v + (b * S::VW >> 4);
-            // (16 tokens further: 8 columns of P; the address field of V, in units of 16 bytes)
-#pragma unroll
-            for (int i = 0; i < AT_CHUNK / 16; ++i)
-              mma_f16_ts(tmem + TMEM_O + b * 128, tmem + b * TMEM_S + 8 * i, v + i * VBY, ID, i > 0 || c - x.c0 >= 2);
-          }
-          tc_commit(&pvdone[b]);
-        }
-      }
-    }
-    __syncwarp();
-  } else if (role == CONV) {
-    // ================= widening of V, and the split of q =================
+    constexpr uint32_t ID = tc_idesc(128, AT_CHUNK, false, false);
+    const uint64_t d_k = tile_desc<D>(sm, 16), d_q = tile_desc<D>(sm + S::OFF_Q, 16);
     int it = 0, qi = 0;
     Piece x;
     for (int pi = 0; __all_sync(FULL_MASK, next_piece(pi, x)); ++pi) {
       if (lane == 0) piece_read(pi);
-      if (x.c0 >= x.cn) continue;
-      {
-        // lanes of a row (8 values each), rows of a warp at a time, and of all four
-        constexpr int LPR = D / 8, RPW = 32 / LPR, STEP = 4 * RPW;
-        if (qi >= QB) wait_warp(&qfree[qi % QB], ((qi / QB) - 1) & 1, ERR_KV8_S_WAIT);
-        uint8_t* qh = sm + S::OFF_Q + (qi % QB) * 2 * S::QT;
-        const int col = (lane % LPR) * 8, r0 = k * RPW + lane / LPR;
-        int i = (x.row0 + r0) / p.group, j = x.row0 + r0 - i * p.group;
+      const int chunks = __shfl_sync(FULL_MASK, x.cn - x.c0, 0);
+      if (chunks <= 0) continue;
+      bool ok = wait_warp(&qready[qi % QB], (qi / QB) & 1, ERR_KV8_S_WAIT);
+      const uint64_t q = d_q + ((qi % QB) * 2 * S::QT >> 4);
 #pragma unroll 1
-        for (int rb = 0; rb < x.rows; rb += 4 * STEP) {
-          uint4 w[4];
+      for (int c = 0; c < chunks; ++c, ++it) {
+        const int st = it % ST, b = it & 1;
+        ok = wait_warp(&full[st], (it / ST) & 1, ERR_KV8_FULL_WAIT) && ok;
+        if (it >= 2) ok = wait_warp(&pvdone[b], ((it >> 1) - 1) & 1, ERR_KV8_S_WAIT) && ok;
+        if (ok) {
+          tc_fence_after();
+          const uint64_t kk = d_k + (st * 2 * S::KT >> 4);
 #pragma unroll
-          for (int n = 0; n < 4; ++n) {  // (the loads of four rounds together)
-            w[n] = make_uint4(0u, 0u, 0u, 0u);
-            if (rb + n * STEP + r0 < x.rows)
-              w[n] = __ldg(reinterpret_cast<const uint4*>(p.q + (x.q0 + i) * p.q_tok + (x.h * p.group + j) * p.q_head + col));
-            for (j += STEP; j >= p.group; j -= p.group) ++i;
+          for (int d = 0; d < D / 32; ++d) mma_f8(tmem + b * TMEM_S, q + 2 * d, kk + 2 * d, ID, d > 0);
+#pragma unroll
+          for (int d = 0; d < D / 32; ++d)
+            mma_f8(tmem + b * TMEM_S, q + (S::QT >> 4) + 2 * d, kk + 2 * d, ID, true);
+        }
+        tc_commit(&sready[b]);
+        tc_commit(&empty[st]);
+      }
+      tc_commit(&qfree[qi % QB]);
+      ++qi;
+    }
+  } else if (role == O_MMA) {
+    // ================= O += P V =================
+    constexpr uint32_t ID = tc_idesc(128, D, false, true);
+    constexpr int VBY = D < 64 ? 64 : 128;  // bytes of a row of a tile of V
+    const uint64_t d_v = tile_desc<VBY>(sm + S::OFF_V, AT_CHUNK * 128);
+    int it = 0;
+    Piece x;
+    for (int pi = 0; __all_sync(FULL_MASK, next_piece(pi, x)); ++pi) {
+      if (lane == 0) piece_read(pi);
+      const int chunks = __shfl_sync(FULL_MASK, x.cn - x.c0, 0);
+#pragma unroll 1
+      for (int c = 0; c < chunks; ++c, ++it) {
+        const int b = it & 1;
+        bool ok = wait_warp(&vready[b], (it >> 1) & 1, ERR_KV8_PV_WAIT);
+        ok = wait_warp(&pready[b], (it >> 1) & 1, ERR_KV8_PV_WAIT) && ok;
+        if (ok) {
+          tc_fence_after();
+          const uint64_t v = d_v + (b * S::VW >> 4);
+          // (16 tokens further: 8 columns of P; the address field of V, in units of 16 bytes)
+#pragma unroll
+          for (int i = 0; i < AT_CHUNK / 16; ++i)
+            mma_f16_ts(tmem + TMEM_O + b * 128, tmem + b * TMEM_S + 8 * i, v + i * VBY, ID, i > 0 || c >= 2);
+        }
+        tc_commit(&pvdone[b]);
+      }
+    }
+  } else if (role == CONV) {
+    // ================= widening of V, and the split of q =================
+    // q of a piece, the qi-th with chunks.
+    auto split_q = [&](const Piece& x, int qi) {
+      // lanes of a row (8 values each), rows of a warp at a time, and of all four
+      constexpr int LPR = D / 8, RPW = 32 / LPR, STEP = 4 * RPW;
+      if (qi >= QB) wait_warp(&qfree[qi % QB], ((qi / QB) - 1) & 1, ERR_KV8_S_WAIT);
+      uint8_t* qh = sm + S::OFF_Q + (qi % QB) * 2 * S::QT;
+      const int col = (lane % LPR) * 8, r0 = k * RPW + lane / LPR;
+      int i = (x.row0 + r0) / p.group, j = x.row0 + r0 - i * p.group;
+#pragma unroll 1
+      for (int rb = 0; rb < x.rows; rb += 4 * STEP) {
+        uint4 w[4];
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {  // (the loads of four rounds together)
+          w[n] = make_uint4(0u, 0u, 0u, 0u);
+          if (rb + n * STEP + r0 < x.rows)
+            w[n] = __ldg(reinterpret_cast<const uint4*>(p.q + (x.q0 + i) * p.q_tok + (x.h * p.group + j) * p.q_head + col));
+          for (j += STEP; j >= p.group; j -= p.group) ++i;
+        }
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          const int r = rb + n * STEP + r0;
+          const uint32_t in[4] = {w[n].x, w[n].y, w[n].z, w[n].w};
+          uint32_t top = 0;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) top = max(top, max(in[e] & 0x7fffu, (in[e] >> 16) & 0x7fffu));
+#pragma unroll
+          for (int o = LPR / 2; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(FULL_MASK, top, o));
+          // the largest moves to [128, 256); a row with an infinity or a NaN is all NaN
+          const int sh = min(7 - (min(max(static_cast<int>(top >> 7), 1), 254) - 127), 120);
+          const float up = __uint_as_float(static_cast<uint32_t>(127 + sh) << 23);
+          uint32_t hi[2] = {0u, 0u}, lo[2] = {0u, 0u};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const __half2 y = __floats2half2_rn(__uint_as_float(in[e] << 16) * up,
+                                                __uint_as_float(in[e] & 0xffff0000u) * up);
+            const uint16_t h2 = f16x2_to_e4m3x2(*reinterpret_cast<const uint32_t*>(&y));
+            const uint32_t b2 = e4m3x2_to_f16x2(h2);
+            const __half2 rest = __hsub2(y, *reinterpret_cast<const __half2*>(&b2));
+            hi[e >> 1] |= uint32_t(h2) << (16 * (e & 1));
+            lo[e >> 1] |= uint32_t(f16x2_to_e4m3x2(*reinterpret_cast<const uint32_t*>(&rest))) << (16 * (e & 1));
           }
-#pragma unroll
-          for (int n = 0; n < 4; ++n) {
-            const int r = rb + n * STEP + r0;
-            const uint32_t in[4] = {w[n].x, w[n].y, w[n].z, w[n].w};
-            uint32_t top = 0;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) top = max(top, max(in[e] & 0x7fffu, (in[e] >> 16) & 0x7fffu));
-#pragma unroll
-            for (int o = LPR / 2; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(FULL_MASK, top, o));
-            // the largest moves to [128, 256); a row with an infinity or a NaN is all NaN
-            const int sh = min(7 - (min(max(static_cast<int>(top >> 7), 1), 254) - 127), 120);
-            const float up = __uint_as_float(static_cast<uint32_t>(127 + sh) << 23);
-            uint32_t hi[2] = {0u, 0u}, lo[2] = {0u, 0u};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const __half2 y = __floats2half2_rn(__uint_as_float(in[e] << 16) * up,
-                                                  __uint_as_float(in[e] & 0xffff0000u) * up);
-              const uint16_t h2 = f16x2_to_e4m3x2(*reinterpret_cast<const uint32_t*>(&y));
-              const uint32_t b2 = e4m3x2_to_f16x2(h2);
-              const __half2 rest = __hsub2(y, *reinterpret_cast<const __half2*>(&b2));
-              hi[e >> 1] |= uint32_t(h2) << (16 * (e & 1));
-              lo[e >> 1] |= uint32_t(f16x2_to_e4m3x2(*reinterpret_cast<const uint32_t*>(&rest))) << (16 * (e & 1));
-            }
-            if (r < x.rows) {
-              if (col == 0)
-                s_fr[qi % PIECE_RING][r] = top >= 0x7f80u ? NAN : p.scale2 * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
-              const int at = r * D + ((((col >> 4) ^ swz<D>(r)) << 4) | (col & 15));
-              *reinterpret_cast<uint2*>(qh + at) = make_uint2(hi[0], hi[1]);
-              *reinterpret_cast<uint2*>(qh + S::QT + at) = make_uint2(lo[0], lo[1]);
-            }
+          if (r < x.rows) {
+            if (col == 0)
+              s_fr[qi % PIECE_RING][r] = top >= 0x7f80u ? NAN : p.scale2 * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
+            const int at = r * D + ((((col >> 4) ^ swz<D>(r)) << 4) | (col & 15));
+            *reinterpret_cast<uint2*>(qh + at) = make_uint2(hi[0], hi[1]);
+            *reinterpret_cast<uint2*>(qh + S::QT + at) = make_uint2(lo[0], lo[1]);
           }
         }
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&qready[qi % QB]);
       }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&qready[qi % QB]);
+    };
+    int it = 0, qi = 0, pi = 0;
+    Piece x, next;
+    auto take = [&](Piece& x) -> bool {
+      if (!__all_sync(FULL_MASK, next_piece(pi, x))) return false;
+      if (lane == 0) piece_read(pi);
+      ++pi;
+      return true;
+    };
+    bool ok = take(next), ready = false;  // there is a next piece; its q is split
+    while (ok) {
+      x = next;
+      if (x.c0 >= x.cn) {
+        ok = take(next);
+        continue;
+      }
+      if (!ready) split_q(x, qi);
+      ready = false;
 #pragma unroll 1
       for (int c = x.c0; c < x.cn; ++c, ++it) {
         const int st = it % ST, b = it & 1, slot = it % SC_RING;
@@ -553,12 +566,18 @@ __global__ void __launch_bounds__(32 * AttnShape<D, ROWS>::WARPS, 1)
             *reinterpret_cast<uint4*>(row + (((q0 + 1) ^ f) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
           }
         }
-        if (nan) s_nan[qi % PIECE_RING] = 1;
+        if (nan) s_nan[qi % PIECE_RING] = qi + 1;
         fence_async_smem();
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(&vready[b]);
           mbar_arrive(&empty[st]);
+        }
+        // The next piece's q, while the products of two widened chunks are under way.
+        if (c == min(x.c0 + 1, x.cn - 1)) {
+          ok = take(next);
+          ready = ok && next.c0 < next.cn;
+          if (ready) split_q(next, qi + 1);
         }
       }
       ++qi;
@@ -606,14 +625,20 @@ __global__ void __launch_bounds__(32 * AttnShape<D, ROWS>::WARPS, 1)
         };
         // 1. The row's largest score of the chunk, and whether it asks for a new maximum.
         float nref = m == -INFINITY ? 0.f : -m, top = -INFINITY;
-#pragma unroll 1
-        for (int w0 = 0; w0 < AT_CHUNK; w0 += 32) {
-          float s[32];
-          tmem_ld32(t_s + w0, s);
-          score16(w0, s, s_sc[slot][w0 >> p.page_log2], nref);
-          score16(w0 + 16, s + 16, s_sc[slot][(w0 + 16) >> p.page_log2], nref);
+        float s[2][32];  // (a block is read while the one before is worked on)
+        tmem_ld32_begin(t_s, s[0]);
+        auto look = [&](int w0, float* now, float* next) {
+          tmem_ld_end(now);
+          if (w0 + 32 < AT_CHUNK) tmem_ld32_begin(t_s + w0 + 32, next);
+          score16(w0, now, s_sc[slot][w0 >> p.page_log2], nref);
+          score16(w0 + 16, now + 16, s_sc[slot][(w0 + 16) >> p.page_log2], nref);
 #pragma unroll
-          for (int n = 0; n < 32; n += 2) top = max3(top, s[n], s[n + 1]);
+          for (int n = 0; n < 32; n += 2) top = max3(top, now[n], now[n + 1]);
+        };
+#pragma unroll 1
+        for (int w0 = 0; w0 < AT_CHUNK; w0 += 64) {
+          look(w0, s[0], s[1]);
+          look(w0 + 32, s[1], s[0]);
         }
         // (rows that are not there have m = 0)
         const bool anew = (has && top > RAISE) || (m == -INFINITY && lim > 0);
@@ -635,19 +660,19 @@ __global__ void __launch_bounds__(32 * AttnShape<D, ROWS>::WARPS, 1)
           }
         }
         // 2. The weights, over the scores that have been read (16 columns of pairs for 32 of S).
-#pragma unroll 1
-        for (int w0 = 0; w0 < AT_CHUNK; w0 += 32) {
-          float s[32];
+        tmem_ld32_begin(t_s, s[0]);
+        auto weigh = [&](int w0, float* now, float* next) {
           uint32_t h[16];
-          tmem_ld32(t_s + w0, s);
+          tmem_ld_end(now);
+          if (w0 + 32 < AT_CHUNK) tmem_ld32_begin(t_s + w0 + 32, next);
 #pragma unroll
           for (int q = 0; q < 32; q += 16) {
             const PageScale sc = s_sc[slot][(w0 + q) >> p.page_log2];
-            score16(w0 + q, s + q, sc, nref);
+            score16(w0 + q, now + q, sc, nref);
             float2 part = make_float2(0.f, 0.f);
 #pragma unroll
             for (int n = q; n < q + 16; n += 2) {
-              const float2 e = make_float2(ex2(s[n]), ex2(s[n + 1]));
+              const float2 e = make_float2(ex2(now[n]), ex2(now[n + 1]));
               part = __fadd2_rn(part, e);
               const __half2 hh = __floats2half2_rn(e.x, e.y);
               h[n / 2] = *reinterpret_cast<const uint32_t*>(&hh);
@@ -655,6 +680,11 @@ __global__ void __launch_bounds__(32 * AttnShape<D, ROWS>::WARPS, 1)
             l = fmaf(part.x + part.y, sc.inv_v, l);
           }
           tmem_st16u(t_s + w0 / 2, h);
+        };
+#pragma unroll 1
+        for (int w0 = 0; w0 < AT_CHUNK; w0 += 64) {
+          weigh(w0, s[0], s[1]);
+          weigh(w0 + 32, s[1], s[0]);
         }
         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
         tc_fence_before();
@@ -700,7 +730,7 @@ __global__ void __launch_bounds__(32 * AttnShape<D, ROWS>::WARPS, 1)
           p.lse[at] = total == 0.f ? -INFINITY : (top + log2f(total)) * LN2_F;
         }
       }
-      const bool nans = chunks > 0 && s_nan[qi % PIECE_RING];
+      const bool nans = chunks > 0 && s_nan[qi % PIECE_RING] == qi + 1;
 #pragma unroll 1
       for (int w0 = g * (D / 2); w0 < (g + 1) * (D / 2); w0 += 16) {
         float y[16];

@@ -29,6 +29,12 @@ struct AttnParams {
 
 // ------------------------------------------------------------------------ the deal of work
 
+// Each tile counts HEAD_UNITS more than its chunks, at its front, for what it costs beside them
+// (its q, its first maxima, its outputs), so that runs of many short tiles take no longer than
+// others.  Measured: 3 chunks' time for 128 rows, 1 for few.
+template <int ROWS>
+constexpr int HEAD_UNITS = ROWS == 128 ? 3 : 1;
+
 struct SeqUnits {
   int n, len, tiles, chunks;
   int64_t q0, units;
@@ -43,7 +49,7 @@ __device__ __forceinline__ SeqUnits seq_units(const AttnParams& p, int64_t b) {
   u.q0 = r.q0;
   u.tiles = (r.n * p.group + ROWS - 1) / ROWS;
   u.chunks = max(1, (r.len + AT_CHUNK - 1) / AT_CHUNK);
-  u.units = int64_t(u.tiles) * p.c.heads * u.chunks;
+  u.units = int64_t(u.tiles) * p.c.heads * (u.chunks + HEAD_UNITS<ROWS>);
   return u;
 }
 
@@ -90,16 +96,65 @@ __device__ __forceinline__ Run find_run(const AttnParams& p, int64_t run, int ru
   return r;
 }
 
-// A piece of a run: the chunks [c0, c1) of one tile, of which [c0, cn) are seen by some row of
-// it.  The loading warp works the pieces out and leaves them in a ring for the others.
-struct Piece {
-  int64_t q0;         // the sequence's first row of q
-  int64_t table;      // its row of the block table, as an offset
-  int n, len;         // its new tokens and its cached ones
-  int h, row0, rows;  // key / value head; the tile's first row and its rows
-  int c0, cn, end;    // tokens that the tile's last row sees
-  int whole;          // 1: all of the tile's chunks; 0: a part; -1: there is no further piece
-  int slot;           // of the workspace, for a part
+// The pieces of a run, in order: the chunks [c0, c1) of one tile each.
+template <int ROWS>
+struct Pieces {
+  const AttnParams& p;
+  const Run run;
+  int64_t b, u;       // the next unit, and its sequence
+  SeqUnits sq;
+  int h, tile, at;    // its head and tile, and its place among the tile's units
+  int c0, c1, count;  // the piece; pieces so far
+  int ph, ptile;
+  int64_t pb;
+  SeqUnits psq;
+  __device__ __forceinline__ Pieces(const AttnParams& p_, const Run& r) : p(p_), run(r), b(r.b), u(r.u), h(0), tile(0), at(0), count(0) {
+    if (u < run.u_end) {
+      sq = seq_units<ROWS>(p, b);
+      const uint32_t in = static_cast<uint32_t>(u - run.first);  // a sequence's units fit 32 bits (host)
+      const uint32_t len = sq.chunks + HEAD_UNITS<ROWS>, item = in / len;
+      at = static_cast<int>(in - item * len);
+      h = item / sq.tiles;
+      tile = item - h * sq.tiles;
+    }
+  }
+  __device__ __forceinline__ bool next() {
+    while (u < run.u_end) {
+      while (sq.units == 0) sq = seq_units<ROWS>(p, ++b);  // sequences without new tokens
+      const int len = sq.chunks + HEAD_UNITS<ROWS>;
+      const int to = static_cast<int>(min(int64_t(len), at + (run.u_end - u)));
+      c0 = max(0, at - HEAD_UNITS<ROWS>);
+      c1 = max(0, to - HEAD_UNITS<ROWS>);
+      ph = h;
+      ptile = tile;
+      pb = b;
+      psq = sq;
+      u += to - at;
+      at = to;
+      if (at == len) {
+        at = 0;
+        if (++tile == sq.tiles) {
+          tile = 0;
+          if (++h == p.c.heads) {
+            h = 0;
+            if (u < run.u_end) sq = seq_units<ROWS>(p, ++b);
+          }
+        }
+      }
+      if (c1 > c0) {
+        ++count;
+        return true;
+      }
+    }
+    return false;
+  }
+  __device__ __forceinline__ int rows() const { return min(ROWS, psq.n * p.group - ptile * ROWS); }
+  // tokens that the tile's last row sees
+  __device__ __forceinline__ int end() const {
+    return max(0, min(psq.len, psq.len - psq.n + (ptile * ROWS + rows() - 1) / p.group + 1));
+  }
+  __device__ __forceinline__ int whole() const { return c0 == 0 && c1 == psq.chunks ? 1 : 0; }
+  __device__ __forceinline__ int slot() const { return 2 * static_cast<int>(blockIdx.x) + (count > 1); }
 };
 
 struct PageScale {  // of the tokens of one page
@@ -158,10 +213,11 @@ __global__ void __launch_bounds__(32 * JOIN_ROWS<ROWS>) kv8_join_kernel(const At
   if (edge >= run.u_end) return;
   const SeqUnits sq = seq_units<ROWS>(p, run.b);
   const uint32_t in = static_cast<uint32_t>(edge - run.first);
-  const uint32_t item = in / sq.chunks;
-  const int64_t i0 = run.first + int64_t(item) * sq.chunks, i1 = i0 + sq.chunks;  // the tile's units
-  if (edge == i0) return;                  // the boundary lies between two tiles
-  if (edge - run.per > i0) return;         // an earlier boundary lies inside this tile too
+  const uint32_t len = sq.chunks + HEAD_UNITS<ROWS>, item = in / len;
+  // the tile's units, and the first of its chunks
+  const int64_t i0 = run.first + int64_t(item) * len, i1 = i0 + len, ic = i0 + HEAD_UNITS<ROWS>;
+  if (edge <= ic) return;                  // the boundary lies before the tile's chunks
+  if (edge - run.per > ic) return;         // an earlier boundary lies among them too
   const int64_t r0 = blockIdx.x, r1 = (i1 - 1) / run.per;  // runs that hold parts
   const int h = item / sq.tiles, tile = item - h * sq.tiles;
   const int row = tile * ROWS + r;

@@ -47,7 +47,7 @@ struct FewPiece {
   int64_t q0;
   int n, len, h, row0, rows;
   int h0, hn, end;  // its stages' first and one behind the last; tokens that its last row sees
-  int whole, slot;  // as in kv8_attn.cu; chunks
+  int whole, slot;  // as in kv8_attn.cu
 };
 
 // d += a b for a 16 x 16 tile a and a 16 x 8 tile b.
@@ -113,41 +113,27 @@ __global__ void __launch_bounds__(32 * FW_WARPS + 32, FW_CTAS) kv8_few_kernel(co
     const Run run = find_run<RT>(p, blockIdx.x, gridDim.x);
     const int part_log2 = min(p.page_log2, 6), part = 1 << part_log2, parts = FW_HALF >> part_log2;
     const int bytes = part * D;
-    int64_t b = run.b, u = run.u;
-    SeqUnits sq{};
-    int tile = 0, h = 0, c0 = 0;
-    if (u < run.u_end) {
-      sq = seq_units<RT>(p, b);
-      const uint32_t in = static_cast<uint32_t>(u - run.first);  // a sequence's units fit 32 bits (host)
-      const uint32_t item = in / sq.chunks;
-      c0 = static_cast<int>(in - item * sq.chunks);
-      h = item / sq.tiles;
-      tile = item - h * sq.tiles;
-    }
+    Pieces<RT> w(p, run);
     int it = 0, pi = 0;
     bool ok_run = true;
     while (ok_run) {
       const int e = pi % FW_PIECES;
       if (pi >= FW_PIECES) ok_run = wait(&pc_empty[e], ((pi / FW_PIECES) - 1) & 1, ERR_KV8_EMPTY_WAIT);
-      if (!ok_run || u >= run.u_end) {
+      if (!ok_run || !w.next()) {
         if (lane == 0) {
           s_piece[e].whole = -1;
           mbar_arrive(&pc_full[e]);
         }
         break;
       }
-      while (sq.units == 0) sq = seq_units<RT>(p, ++b);  // sequences without new tokens
-      const int c1 = static_cast<int>(min(int64_t(sq.chunks), c0 + (run.u_end - u)));
-      const int rows = min(RT, sq.n * p.group - tile * RT);
-      const int end = max(0, min(sq.len, sq.len - sq.n + (tile * RT + rows - 1) / p.group + 1));
-      const int h0 = 2 * c0, hn = max(h0, min(2 * c1, (end + FW_HALF - 1) / FW_HALF));
+      const int end = w.end(), h = w.ph;
+      const int h0 = 2 * w.c0, hn = max(h0, min(2 * w.c1, (end + FW_HALF - 1) / FW_HALF));
       if (lane == 0) {
-        s_piece[e] = FewPiece{sq.q0, sq.n, sq.len, h, tile * RT, rows, h0, hn, end,
-                              c0 == 0 && c1 == sq.chunks ? 1 : 0, 2 * static_cast<int>(blockIdx.x) + (pi > 0)};
+        s_piece[e] = FewPiece{w.psq.q0, w.psq.n, w.psq.len, h, w.ptile * RT, w.rows(), h0, hn, end, w.whole(), w.slot()};
         mbar_arrive(&pc_full[e]);
       }
       ++pi;
-      const int32_t* tab = p.table + b * p.table_stride;
+      const int32_t* tab = p.table + w.pb * p.table_stride;
       auto page_of = [&](int c) {
         const int tok = c * FW_HALF + lane * part;
         return lane < parts && c < hn && tok < end ? __ldg(tab + (tok >> p.page_log2)) : -2;
@@ -181,7 +167,7 @@ __global__ void __launch_bounds__(32 * FW_WARPS + 32, FW_CTAS) kv8_few_kernel(co
         }
         if (lane < parts) {
           const PageScale sc{ks, log2f(vs), 1.f / vs, ok ? 1 : 0};
-          for (int w = 0; w < part / 16; ++w) s_sc[slot][lane * (part / 16) + w] = sc;
+          for (int n = 0; n < part / 16; ++n) s_sc[slot][lane * (part / 16) + n] = sc;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive_expect_tx(&full[st], 2u * bytes * __popc(have));
@@ -191,19 +177,6 @@ __global__ void __launch_bounds__(32 * FW_WARPS + 32, FW_CTAS) kv8_few_kernel(co
           uint8_t* dst = fw_smem + st * 2 * S::TILE + lane * bytes;
           bulk_g2s(dst, p.c.k + off, bytes, &full[st]);
           bulk_g2s(dst + S::TILE, p.c.v + off, bytes, &full[st]);
-        }
-      }
-      // on to the next tile
-      u += c1 - c0;
-      c0 = c1;
-      if (c0 == sq.chunks) {
-        c0 = 0;
-        if (++tile == sq.tiles) {
-          tile = 0;
-          if (++h == p.c.heads) {
-            h = 0;
-            if (u < run.u_end) sq = seq_units<RT>(p, ++b);
-          }
         }
       }
     }
