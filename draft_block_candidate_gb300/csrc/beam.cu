@@ -27,7 +27,7 @@ static __device__ uint32_t g_err_beam;
 //
 // One CTA per batch entry; bound by latency.  A few warps for each beam join its segments'
 // sorted lists (the records of four segments are read at a time); then a thread for each
-// candidate finds its rank, the number of better ones, by a binary search in each beam's list,
+// candidate finds its rank, the number of better ones, by binary searches in the beams' lists,
 // so that no step waits for the one before as in a merge that takes one candidate at a time.
 
 // Order-preserving key: unsigned comparison of keys = comparison of the doubles.
@@ -37,7 +37,7 @@ __device__ __forceinline__ uint64_t double_key(double d) {
 }
 
 constexpr int BM_MAX = 32;   // beams, and entries taken
-constexpr int BM_WARPS = 8;  // at least as many warps join lists
+constexpr int BM_WARPS = 32;  // up to as many warps join lists
 
 // (m, s) takes (om, os): s 2^m + os 2^om.
 __device__ __forceinline__ void join_sum(float& m, float& s, float om, float os) {
@@ -109,6 +109,18 @@ __global__ void __launch_bounds__(32 * BM_MAX)
       s_s[warp] = s;
     }
   }
+  // the warps' lists of a beam, two by two
+  for (int d = 1; d < per; d *= 2) {
+    __syncthreads();
+    if (w < beams && live && !done && part % (2 * d) == 0 && part + d < per) {
+      float v = s_v[warp][lane];
+      int id = s_id[warp][lane];
+      bitonic_merge(v, id, s_v[warp + d][lane], s_id[warp + d][lane], lane);
+      s_v[warp][lane] = v;
+      s_id[warp][lane] = id;
+      if (lane == 0) join_sum(s_m[warp], s_s[warp], s_m[warp + d], s_s[warp + d]);
+    }
+  }
   __syncthreads();
   const int i = warp;  // from here a warp for each beam
   int left = 0;
@@ -124,12 +136,8 @@ __global__ void __launch_bounds__(32 * BM_MAX)
         key = double_key(own);
         value = static_cast<float>(own);
       } else {
-        float v = s_v[i * per][lane], m = s_m[i * per], s = s_s[i * per];
-        int id = s_id[i * per][lane];
-        for (int k = 1; k < per; ++k) {
-          bitonic_merge(v, id, s_v[i * per + k][lane], s_id[i * per + k][lane], lane);
-          join_sum(m, s, s_m[i * per + k], s_s[i * per + k]);
-        }
+        const float v = s_v[i * per][lane], m = s_m[i * per], s = s_s[i * per];
+        const int id = s_id[i * per][lane];
         if (s > 0.f) {  // a row with no finite logit has no candidate
           int e;
           float f = frexpf(s, &e);
@@ -151,17 +159,21 @@ __global__ void __launch_bounds__(32 * BM_MAX)
   __syncthreads();
   if (i < beams && lane < left) {
     int rank = lane;
-    for (int j = 0; j < beams && rank < M; ++j) {
-      if (j == i) continue;
-      // entries of beam j's list before this candidate: better, or equal in a lower beam
-      int lo = 0, hi = s_left[j];
-      while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        const uint64_t x = s_key[j][mid];
-        if (x > key || (x == key && j < i)) lo = mid + 1;
-        else hi = mid;
-      }
-      rank += lo;
+    // entries of the other beams' lists before this candidate (better, or equal in a lower beam),
+    // four lists at a time: the steps of their searches overlap
+    for (int j0 = 0; j0 < beams && rank < M; j0 += 4) {
+      int lo[4] = {0, 0, 0, 0};
+#pragma unroll
+      for (int step = 32; step >= 1; step >>= 1)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int j = min(j0 + q, beams - 1), to = lo[q] + step;
+          const uint64_t x = s_key[j][min(to, BM_MAX) - 1];
+          if (to <= s_left[j] && (x > key || (x == key && j < i))) lo[q] = to;
+        }
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (j0 + q < beams && j0 + q != i) rank += lo[q];
     }
     if (rank < M) {
       o_score[rank] = value;
@@ -360,7 +372,7 @@ lilicorr_status lilicorr_beam_select(const void* logits, lilicorr_dtype ldtype, 
                                   finished, stream);
   if (e == cudaSuccess) {
     PdlScope pdl(true);
-    e = launch_k(beam_merge_kernel, dim3(static_cast<unsigned>(batch)), dim3(32 * beams * std::max(1, BM_WARPS / beams)), 0,
+    e = launch_k(beam_merge_kernel, dim3(static_cast<unsigned>(batch)), dim3(32 * beams * std::max(1, std::min(BM_WARPS / beams, (pl.P + 3) / 4))), 0,
                  stream, static_cast<const char*>(workspace), scores, finished, static_cast<int>(beams),
                  pl.P, pl.K, static_cast<int>(M), static_cast<int>(pad_id), out_score, out_token,
                  out_parent);

@@ -29,6 +29,7 @@ struct AppendParams {
   int64_t table_stride;
   int cols;      // pages of a table row
   int max_new, grow;  // pages a sequence can touch in one call
+  int page_log2, row_log2;  // of a page's tokens, and of a row's vectors of 8 values
 };
 
 // 2^k as above, from the bits of the largest magnitude (finite, >= 0).
@@ -41,7 +42,7 @@ __device__ __forceinline__ float page_scale(float amax) {
 }
 
 template <int VPT>  // 8-element vectors a thread holds of a page
-__global__ void __launch_bounds__(AP_THREADS) kv8_append_kernel(const AppendParams p, int D) {
+__global__ void __launch_bounds__(AP_THREADS) kv8_append_kernel(const AppendParams p) {
   __shared__ uint32_t s_max[AP_THREADS / 32];
   const int tid = threadIdx.x;
   int64_t u = blockIdx.x;
@@ -51,77 +52,95 @@ __global__ void __launch_bounds__(AP_THREADS) kv8_append_kernel(const AppendPara
   u /= p.c.heads;
   const int g = static_cast<int>(u % p.grow);
   const int64_t b = u / p.grow;
-  const int page = p.c.page;
+  const int page = p.c.page, D = 8 << p.row_log2;
   const SeqRange r = seq_range(p.q_start, p.kv_len, b, p.total, p.max_new,
-                               int64_t(p.cols) * page, &g_err_kv8);
+                               int64_t(p.cols) << p.page_log2, &g_err_kv8);
   const int before = r.len - r.n;
   if (r.n == 0) return;
   if (before < 0) {
     if (tid == 0) atomicOr(&g_err_kv8, ERR_KV8_LENGTH);
     return;
   }
-  const int at = before / page + g;  // this page's column of the table
-  if (int64_t(at) * page >= r.len) return;
+  const int at = (before >> p.page_log2) + g;  // this page's column of the table
+  const int pos0 = at << p.page_log2;
+  if (pos0 >= r.len) return;
   const int id = __ldg(p.table + b * p.table_stride + at);
-  const int pos0 = at * page;
   const bool has_old = pos0 < before;
-  int src = id;
-  if (has_old && p.tail_src) {
-    src = __ldg(p.tail_src + b);
-    if (src < 0) src = id;
+  int src = has_old && p.tail_src ? __ldg(p.tail_src + b) : -1;
+
+  // the new rows, which wait for no table entry
+  const __nv_bfloat16* x = (which ? p.v : p.k) + h * (which ? p.v_head : p.k_head);
+  const int64_t tok = which ? p.v_tok : p.k_tok;
+  const int vrow = 1 << p.row_log2;
+  const int lo_row = max(before - pos0, 0), hi_row = min(r.len - pos0, page);  // of the page
+  const int64_t row0 = r.q0 + pos0 - before;
+  uint4 w[VPT];
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int e = tid + i * AP_THREADS, row = e >> p.row_log2;
+    w[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (row >= lo_row && row < hi_row)
+      w[i] = __ldcs(reinterpret_cast<const uint4*>(x + (row0 + row) * tok + (e & (vrow - 1)) * 8));
   }
+  if (src < 0) src = id;
   if (id < 0 || id >= p.c.n_pages || src >= p.c.n_pages) {
     if (tid == 0) atomicOr(&g_err_kv8, ERR_KV8_PAGE);
     return;
   }
-  const __nv_bfloat16* x = which ? p.v : p.k;
-  const int64_t tok = which ? p.v_tok : p.k_tok, hd = which ? p.v_head : p.k_head;
   uint8_t* codes = (which ? p.c.v : p.c.k) + (int64_t(id) * p.c.heads + h) * page * D;
   float* scales = which ? p.c.vs : p.c.ks;
+  const float was = has_old ? __ldcg(scales + int64_t(src) * p.c.heads + h) : 0.f;
 
-  const int vrow = D / 8, nvec = page * vrow;
-  uint4 w[VPT];
-  uint32_t top = 0;  // bits of the largest finite magnitude (of bf16, so 15 bits)
-#pragma unroll
-  for (int i = 0; i < VPT; ++i) {
-    const int e = tid + i * AP_THREADS;
-    const int row = e / vrow, pos = pos0 + row;
-    w[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (e < nvec && pos >= before && pos < r.len)
-      w[i] = __ldcs(reinterpret_cast<const uint4*>(x + (r.q0 + pos - before) * tok + h * hd +
-                                                   (e - row * vrow) * 8));
-  }
+  // The largest magnitude, in bf16 (NaN is passed over); infinities are looked for where it is one.
+  __nv_bfloat162 top2 = __floats2bfloat162_rn(0.f, 0.f);
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const uint32_t q[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t lo = q[j] & 0x7fffu, hi = (q[j] >> 16) & 0x7fffu;
-      if (lo < 0x7f80u) top = max(top, lo);
-      if (hi < 0x7f80u) top = max(top, hi);
-    }
+    for (int j = 0; j < 4; ++j) top2 = __hmax2(top2, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&q[j])));
   }
-  top = __reduce_max_sync(FULL_MASK, top);
+  float amax = fmaxf(__low2float(top2), __high2float(top2));
+  if (isinf(amax)) {
+    uint32_t top = 0;  // bits of the largest finite magnitude
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const uint32_t q[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t lo = q[j] & 0x7fffu, hi = (q[j] >> 16) & 0x7fffu;
+        if (lo < 0x7f80u) top = max(top, lo);
+        if (hi < 0x7f80u) top = max(top, hi);
+      }
+    }
+    amax = __uint_as_float(top << 16);
+  }
+  // (magnitudes compare as their bits do)
+  uint32_t top = __reduce_max_sync(FULL_MASK, __float_as_uint(amax));
   if ((tid & 31) == 0) s_max[tid >> 5] = top;
-  const float was = has_old ? __ldcg(scales + int64_t(src) * p.c.heads + h) : 0.f;
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < AP_THREADS / 32; ++i) top = max(top, s_max[i]);
-  const float now = fmaxf(page_scale(__uint_as_float(top << 16)), was);
+  const float now = fmaxf(page_scale(__uint_as_float(top)), was);
+  const float inv = 1.f / now;
   // a scale of the caller's own need not be a power of two; then the quotient is divided out
   const bool pow2 = (__float_as_uint(now) & 0x7fffffu) == 0;
-  const float inv = 1.f / now;
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    const int e = tid + i * AP_THREADS;
-    const int row = e / vrow, pos = pos0 + row;
-    if (e < nvec && pos >= before && pos < r.len) {
+    const int e = tid + i * AP_THREADS, row = e >> p.row_log2;
+    if (row >= lo_row && row < hi_row) {
       const uint32_t q[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
       uint16_t o[4];
+      if (pow2) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float lo = __uint_as_float(q[j] << 16), hi = __uint_as_float(q[j] & 0xffff0000u);
-        o[j] = pow2 ? f32x2_to_e4m3x2(lo * inv, hi * inv) : f32x2_to_e4m3x2(lo / now, hi / now);
+        for (int j = 0; j < 4; ++j)
+          o[j] = f32x2_to_e4m3x2(__uint_as_float(q[j] << 16) * inv, __uint_as_float(q[j] & 0xffff0000u) * inv);
+      } else {
+#pragma unroll 1
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t z = j == 0 ? q[0] : j == 1 ? q[1] : j == 2 ? q[2] : q[3];
+          const uint16_t c = f32x2_to_e4m3x2(__uint_as_float(z << 16) / now, __uint_as_float(z & 0xffff0000u) / now);
+          if (j == 0) o[0] = c; else if (j == 1) o[1] = c; else if (j == 2) o[2] = c; else o[3] = c;
+        }
       }
       *reinterpret_cast<uint2*>(codes + int64_t(e) * 8) =
           make_uint2(o[0] | uint32_t(o[1]) << 16, o[2] | uint32_t(o[3]) << 16);
@@ -131,7 +150,7 @@ __global__ void __launch_bounds__(AP_THREADS) kv8_append_kernel(const AppendPara
   if (has_old && (src != id || now != was)) {
     const uint8_t* from = (which ? p.c.v : p.c.k) + (int64_t(src) * p.c.heads + h) * page * D;
     const float f = was / now;
-    const int nold = (min(before, pos0 + page) - pos0) * vrow;
+    const int nold = min(before - pos0, page) << p.row_log2;
     for (int e = tid; e < nold; e += AP_THREADS) {
       uint2 c = *reinterpret_cast<const uint2*>(from + int64_t(e) * 8);
       if (now != was) {
@@ -238,17 +257,19 @@ lilicorr_status lilicorr_kv8_append(const lilicorr_kv8_cache* cache, const void*
   prm.cols = cols;
   prm.max_new = max_new;
   const int page = cache->page, D = cache->head_dim;
+  while ((1 << prm.page_log2) < page) ++prm.page_log2;
+  while ((8 << prm.row_log2) < D) ++prm.row_log2;
   prm.grow = std::min<int>((max_new + page - 2) / page + 1, cols);
   const int64_t ctas = batch * prm.grow * cache->kv_heads * 2;
   if (ctas > INT_MAX) return fail(LILICORR_ERR_INVALID_ARG, "batch * max_new * kv_heads is too large for one call");
   const int vpt = (page * D / 8 + AP_THREADS - 1) / AP_THREADS;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const dim3 grid(static_cast<unsigned>(ctas));
-  if (vpt <= 1) kv8_append_kernel<1><<<grid, AP_THREADS, 0, st>>>(prm, D);
-  else if (vpt <= 2) kv8_append_kernel<2><<<grid, AP_THREADS, 0, st>>>(prm, D);
-  else if (vpt <= 4) kv8_append_kernel<4><<<grid, AP_THREADS, 0, st>>>(prm, D);
-  else if (vpt <= 8) kv8_append_kernel<8><<<grid, AP_THREADS, 0, st>>>(prm, D);
-  else kv8_append_kernel<16><<<grid, AP_THREADS, 0, st>>>(prm, D);
+  if (vpt <= 1) kv8_append_kernel<1><<<grid, AP_THREADS, 0, st>>>(prm);
+  else if (vpt <= 2) kv8_append_kernel<2><<<grid, AP_THREADS, 0, st>>>(prm);
+  else if (vpt <= 4) kv8_append_kernel<4><<<grid, AP_THREADS, 0, st>>>(prm);
+  else if (vpt <= 8) kv8_append_kernel<8><<<grid, AP_THREADS, 0, st>>>(prm);
+  else kv8_append_kernel<16><<<grid, AP_THREADS, 0, st>>>(prm);
   note_launch();
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return fail(LILICORR_ERR_CUDA, cudaGetErrorString(e));

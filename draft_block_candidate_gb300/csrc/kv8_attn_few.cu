@@ -38,7 +38,10 @@ constexpr float P_LOG2 = 14.f;          // log2 of the largest weight as it is h
 template <int D, int RT>
 struct FewShape {
   static constexpr int TILE = FW_HALF * D;              // bytes of a stage's keys, or values
-  static constexpr int STAGES = D == 128 ? (RT == 8 ? 5 : 4) : 6;
+  // An even number, so that a stage is always the same pair's: a barrier's wait tells only the
+  // parity of a phase, and a pair that skipped phases could take an older one for its own.
+  static constexpr int STAGES = D == 128 ? 4 : 6;
+  static_assert(STAGES % 2 == 0);
   static constexpr int RING = STAGES * 2 * TILE;
   static constexpr int SMEM = RING + FW_WARPS * RT * (D + 4) * 4;
 };

@@ -478,6 +478,48 @@ def test_attention_same_bits_in_graphs_and_on_another_stream(lc):
         assert torch.equal(o, want) and torch.equal(l, wl)
 
 
+@pytest.mark.parametrize("new,group,D,page", [(1, 4, 128, 64), (1, 12, 128, 16), (1, 2, 64, 32), (16, 8, 128, 64), (4, 8, 32, 128)])
+def test_attention_many_stages_give_the_same_bits_every_time(lc, new, group, D, page):
+    """Long runs of copies through the rings, from pages all over a large pool."""
+    seqs = [(new, 200 + (i * 977) % 9000) for i in range(40)]
+    q_start, kv_len, table, n_pages = make_batch(seqs, page, 7)
+    heads = 4
+    wide = -(-(1 << 28) // (heads * page * D))  # a pool of 2^28 values, the pages in use spread over it
+    spread = torch.randperm(max(wide, n_pages), generator=torch.Generator().manual_seed(1))[:n_pages].to(torch.int32).cuda()
+    table = torch.where(table >= 0, spread[table.clamp_min(0).long()], table).contiguous()
+    cache = lc.KV8Cache(max(wide, n_pages), heads, page, D)
+    fill(lc, cache, q_start, kv_len, table, 17)
+    q = torch.randn(40 * new, heads * group, D, generator=gen(18), device="cuda").to(torch.bfloat16)
+    want, wl = lc.kv8_attention(q, cache, q_start, kv_len, table, new, lse=True)
+    for _ in range(25):
+        out, lse = lc.kv8_attention(q, cache, q_start, kv_len, table, new, lse=True)
+        assert torch.equal(out, want) and torch.equal(lse, wl)
+    for b in (3, 39):
+        one = torch.tensor([0, new], dtype=torch.int32, device="cuda")
+        check_attention(lc, q[b * new:(b + 1) * new, :group].contiguous(), lc.KV8Cache.from_tensors(*(
+            t[:, :1].contiguous() for t in (cache.k, cache.v, cache.k_scale, cache.v_scale))),
+            one, kv_len[b:b + 1], table[b:b + 1], new)
+
+
+def test_attention_scores_that_rise_by_any_amount(lc):
+    """Keys that grow along the sequence: maxima move in every chunk, by little and by more than
+    f16 or f32 weights could hold."""
+    for rise in (0.02, 0.5, 40.0, 600.0):
+        for new, group in ((1, 4), (8, 4)):
+            n = 700
+            q_start, kv_len, table, n_pages = make_batch([(new, n), (new, n - 130)], 32, 9)
+            cache = make_cache(lc, n_pages, 1, 32, 64, 10)
+            g = gen(11)
+            q = torch.randn(2 * new, group, 64, generator=g, device="cuda").to(torch.bfloat16)
+            dir_ = q.float().mean((0, 1))
+            at = torch.arange(n, device="cuda", dtype=torch.float32)
+            k = (torch.randn(n, 1, 64, generator=g, device="cuda") + (at * rise / n)[:, None, None] * dir_).to(torch.bfloat16)
+            v = torch.randn(n, 1, 64, generator=g, device="cuda").to(torch.bfloat16)
+            starts = torch.tensor([0, n, 2 * n - 130], dtype=torch.int32, device="cuda")
+            lc.kv8_append(cache, torch.cat([k, k[:n - 130]]), torch.cat([v, v[:n - 130]]), starts, kv_len, table, n)
+            check_attention(lc, (q.float() * 4).to(torch.bfloat16), cache, q_start, kv_len, table, new)
+
+
 # ------------------------------------------------------------------------- used together
 
 def test_beam_decoding_with_the_cache(lc):
