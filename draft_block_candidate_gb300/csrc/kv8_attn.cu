@@ -16,12 +16,11 @@
 //     O[rows, D]         += P V      kind::f16: P from tensor memory, V widened from e4m3 (exact)
 // Warps: one deals out the pieces of the CTA's run and brings their chunks (K through a swizzled
 // tensor map, V by plain bulk copies) into a ring of stages; one issues the S products and one
-// the O products (a thread takes some 80 cycles to issue one, so each kind has its own); four
-// widen V and split the tile's q; and two groups take the softmax, a thread a row.  The groups
-// take turns at the chunks, each with its own S, its own running maximum and sums and its own O
-// in tensor memory, so that neither waits for the other; the two are put together at the
-// tile's end.  A group has four warps for 128 rows, one for 32 (a warp reaches the 32 lanes of
-// tensor memory of its place among four).
+// the O products; four widen V and split the tile's q; and two groups of four take the softmax, a
+// thread a row.  The groups take turns at the chunks: one looks for a chunk's maxima while the
+// other forms the weights of the chunk before, and three buffers of S (which P then takes) let
+// the products run ahead.  Maxima and O are the groups' in common, sums their own: a group
+// decides on a chunk's maxima after the other has on the chunk before.
 //
 // A row's maximum m moves only where a score passes it by more than 2^14: weights are then at
 // most 2^14, inside f16, and O is scaled in tensor memory only then, by the warp that owns its
@@ -42,6 +41,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 
 #include "kv8_attn.cuh"
@@ -105,30 +105,37 @@ __device__ __forceinline__ void tmem_ld16(uint32_t t, float* v) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
-// The same for 32 columns in two steps: what is read may be used after tmem_ld_end of it, which
-// ends all reads of the warp.
-__device__ __forceinline__ void tmem_ld32_begin(uint32_t t, float* v) {
+// The same in two steps: what is read may be used after tmem_ld_end of it, which ends all reads
+// of the warp.
+__device__ __forceinline__ void tmem_ld16_begin(uint32_t t, float* v) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
       : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
         "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]),
-        "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]),
-        "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]),
-        "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+        "=f"(v[14]), "=f"(v[15])
       : "r"(t));
 }
 __device__ __forceinline__ void tmem_ld_end(float* v) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
                : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]),
-                 "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]),
-                 "+f"(v[14]), "+f"(v[15]), "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]),
-                 "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]), "+f"(v[24]), "+f"(v[25]),
-                 "+f"(v[26]), "+f"(v[27]), "+f"(v[28])
+                 "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]),
+                 "+f"(v[13]), "+f"(v[14]), "+f"(v[15])
                :
                : "memory");
-  asm volatile("" : "+f"(v[29]), "+f"(v[30]), "+f"(v[31]));
+}
+// Whether a phase has ended; waits for it up to a microsecond or so.  A wait takes at most
+// WAIT_TRIES of them, about a second.
+constexpr uint32_t WAIT_TRIES = 1u << 20;
+__device__ __forceinline__ bool try_wait_us(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_addr(bar)), "r"(parity), "r"(1000u)
+      : "memory");
+  return ok != 0;
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
@@ -144,13 +151,10 @@ __device__ __forceinline__ void tmem_st16(uint32_t t, const float* v) {
       : "memory");
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
-__device__ __forceinline__ void tmem_st16u(uint32_t t, const uint32_t* v) {  // (not waited for)
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(t),
-      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
-      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
-      : "memory");
+__device__ __forceinline__ void tmem_st8(uint32_t t, const uint32_t* v) {  // (not waited for)
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(t), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
 }
 
 // Shared-memory tiles of rows of 32, 64 or 128 bytes (wider ones are several tiles of 128), in
@@ -189,42 +193,30 @@ __device__ __forceinline__ uint32_t nan_codes(uint32_t w) {  // 0xff in each byt
 template <int D, int ROWS>
 struct AttnShape {
   static constexpr int KT = AT_CHUNK * D;               // bytes of a chunk's keys, or values
-  static constexpr int STAGES = D < 128 ? 4 : 2;
+  static constexpr int KS = D < 128 ? 4 : 3;            // chunks of keys in flight or in use
+  static constexpr int VS = D < 128 ? 4 : 2;            // and of values
   static constexpr int VW = 2 * KT;                     // widened values; two buffers
   static constexpr int QB = 2;                          // buffers of q
   static constexpr int QT = ROWS * D;                   // bytes of q hi, or lo
-  static constexpr int OFF_V = STAGES * 2 * KT;
+  static constexpr int OFF_VR = KS * KT;                // values as they come
+  static constexpr int OFF_V = OFF_VR + VS * KT;
   static constexpr int OFF_Q = OFF_V + 2 * VW;
-  // a product reads 128 rows of q, whatever lies behind a tile of 32
-  static constexpr int SMEM = 1024 + OFF_Q + QB * 2 * QT + (128 - ROWS) * D;
+  static constexpr int SMEM = 1024 + OFF_Q + QB * 2 * QT;
   static constexpr int QUARTERS = ROWS / 32;            // softmax warps of a group
-  static constexpr int WARPS = 2 * QUARTERS + 7;
+  static constexpr int WARPS = 2 * QUARTERS + 11;
   static constexpr int CONSUMERS = WARPS - 1;           // warps that read the pieces
 };
-constexpr int TMEM_COLS = 512, TMEM_S = 128, TMEM_O = 256;  // S of chunk i at 128 (i % 2), O at 256 + 128 (i % 2)
+constexpr int TMEM_COLS = 512, TMEM_S = 128, TMEM_O = 384;  // S and P of chunk i at 128 (i % 3), O at 384
 
-enum Role : int { SOFT0, SOFT1, CONV, LOAD, S_MMA, O_MMA };
-// Role of a warp and its number within it.  Softmax warps sit where their quarter of the lanes
-// is (warp % 4): 0..3 and 4..7 for 128 rows, 0 and 4 for 32.
-template <int ROWS>
+enum Role : int { SOFT0, SOFT1, CONV, SPLIT, LOAD, S_MMA, O_MMA };
+// Role of a warp and its number within it.  (Softmax warps sit where their quarter of the lanes
+// is: warp % 4.)
 __device__ __forceinline__ Role role_of(int warp, int& k) {
-  if (ROWS == 128) {
-    k = warp & 3;
-    if (warp < 8) return warp < 4 ? SOFT0 : SOFT1;
-    if (warp < 12) return CONV;
-    return static_cast<Role>(LOAD + warp - 12);
-  }
-  k = 0;
-  if (warp == 0) return SOFT0;
-  if (warp == 4) return SOFT1;
-  if (warp < 6) {
-    k = warp < 4 ? warp - 1 : 3;
-    return CONV;
-  }
-  return static_cast<Role>(LOAD + warp - 6);
+  k = warp & 3;
+  return static_cast<Role>(warp < 16 ? warp >> 2 : LOAD + warp - 16);
 }
 
-constexpr int SC_RING = 8, PIECE_RING = 4;  // deeper than any warp runs ahead of the softmax
+constexpr int SC_RING = 8, PIECE_RING = 4, FR_RING = 8;  // deeper than any warp runs ahead of the softmax
 constexpr float RAISE = 14.f;               // log2 of how far a score may pass its reference
 
 // A piece of the CTA's run: the chunks [c0, cn) of a tile that some row of it sees.
@@ -238,40 +230,90 @@ struct Piece {
   int slot;           // of the workspace, for a part
 };
 
+// A row's D sums by f; scores of tokens that it does not see (lim on), or whose page was not
+// loaded, to what its factor makes -inf of.  Out of line for the same reason.
+template <int D>
+__device__ __noinline__ void scale_columns(uint32_t t, float f) {
+#pragma unroll 1
+  for (int w0 = 0; w0 < D; w0 += 16) {
+    float o[16];
+    tmem_ld16(t + w0, o);
+#pragma unroll
+    for (int n = 0; n < 16; ++n) o[n] *= f;
+    tmem_st16(t + w0, o);
+  }
+}
+__device__ __forceinline__ float score_factor(float fr, const PageScale& sc) {
+  const float a = fr * sc.k;
+  return a == 0.f ? FLT_MIN : a;  // (never 0, so that a score of infinity stays one)
+}
+__device__ __noinline__ void mask_scores(uint32_t t, int lim, float fr, const PageScale* scales, int page_log2) {
+#pragma unroll 1
+  for (int w0 = 0; w0 < AT_CHUNK; w0 += 16) {
+    const PageScale sc = scales[w0 >> page_log2];
+    const int see = sc.ok ? lim - w0 : 0;
+    if (__all_sync(FULL_MASK, see >= 16)) continue;
+    const float no = score_factor(fr, sc) < 0.f ? INFINITY : -INFINITY;
+    float s[16];
+    tmem_ld16(t + w0, s);
+#pragma unroll
+    for (int n = 0; n < 16; ++n)
+      if (n >= see) s[n] = no;
+    tmem_st16(t + w0, s);
+  }
+}
+
+// NaN into the columns [w0, w1) of a row's outputs, or of its part, where a token of [t0, t1) has one.
+__device__ __noinline__ void put_nans(const Kv8 c, const int32_t* table, int page_log2, int D, int h, int t0, int t1,
+                                      int w0, int w1, __nv_bfloat16* out, float* part) {
+#pragma unroll 1
+  for (int t = t0; t < t1; ++t) {
+    const int id = __ldg(table + (t >> page_log2));
+    if (id < 0 || id >= c.n_pages) continue;
+    const uint8_t* v = c.v + ((int64_t(id) * c.heads + h) * c.page + (t & (c.page - 1))) * D;
+#pragma unroll 1
+    for (int w = w0; w < w1; ++w)
+      if ((v[w] & 0x7f) == 0x7f) {
+        if (out) out[w] = __float2bfloat16_rn(NAN);
+        else part[w] = NAN;
+      }
+  }
+}
+
 template <int D, int ROWS>
 __global__ void __launch_bounds__(32 * AttnShape<D, ROWS>::WARPS, 1)
     kv8_attention_kernel(const __grid_constant__ CUtensorMap tm, const AttnParams p) {
   using S = AttnShape<D, ROWS>;
-  constexpr int ST = S::STAGES, QB = S::QB, NQ = S::QUARTERS;
+  constexpr int KS = S::KS, VS = S::VS, QB = S::QB, NQ = S::QUARTERS;
   extern __shared__ uint8_t at_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(at_raw) + 1023) & ~uintptr_t(1023));
-  __shared__ __align__(8) uint64_t full[ST], empty[ST], sready[2], vready[2], pready[2], pvdone[2],
-      qready[QB], qfree[QB], pc_full[PIECE_RING], pc_empty[PIECE_RING], met[NQ], left[NQ];
+  // (sready: of chunk i at i % 6, so that a group meets every phase of its own)
+  __shared__ __align__(8) uint64_t kfull[KS], kempty[KS], vfull[VS], vempty[VS], sready[6], vready[2], pready[3], pvdone[3],
+      qready[QB], qfree[QB], pc_full[PIECE_RING], pc_empty[PIECE_RING], decided[NQ], met[NQ], left[NQ];
   __shared__ Piece s_piece[PIECE_RING];
   __shared__ PageScale s_sc[SC_RING][8];
-  __shared__ float s_fr[PIECE_RING][ROWS], s_m[2][ROWS], s_l[2][ROWS];
+  __shared__ float s_fr[FR_RING][ROWS], s_m[2][ROWS];
+  __shared__ float2 s_ml[2][ROWS];
   __shared__ int s_nan[PIECE_RING];  // 1 + the piece in whose V a NaN was taken out
   __shared__ uint32_t s_tmem;
-  __shared__ volatile int s_fail;
+  __shared__ volatile uint32_t s_fail;
 
   const int tid = threadIdx.x, warp = __shfl_sync(FULL_MASK, tid >> 5, 0), lane = tid & 31;
   int k;
-  const Role role = role_of<ROWS>(warp, k);
+  const Role role = role_of(warp, k);
   if (tid == 0) {
-    for (int i = 0; i < ST; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1 + 4); }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&sready[i], 1);
-      mbar_init(&vready[i], 4);
-      mbar_init(&pready[i], NQ);
-      mbar_init(&pvdone[i], 1);
-    }
+    for (int i = 0; i < KS; ++i) { mbar_init(&kfull[i], 1); mbar_init(&kempty[i], 1); }
+    for (int i = 0; i < VS; ++i) { mbar_init(&vfull[i], 1); mbar_init(&vempty[i], 4); }
+    for (int i = 0; i < 6; ++i) mbar_init(&sready[i], 1);
+    for (int i = 0; i < 3; ++i) { mbar_init(&pready[i], NQ); mbar_init(&pvdone[i], 1); }
+    for (int i = 0; i < 2; ++i) mbar_init(&vready[i], 4);
     for (int i = 0; i < QB; ++i) { mbar_init(&qready[i], 4); mbar_init(&qfree[i], 1); }
     for (int i = 0; i < PIECE_RING; ++i) {
       mbar_init(&pc_full[i], 1);
       mbar_init(&pc_empty[i], S::CONSUMERS);
       s_nan[i] = 0;
     }
-    for (int i = 0; i < NQ; ++i) { mbar_init(&met[i], 2); mbar_init(&left[i], 2); }
+    for (int i = 0; i < NQ; ++i) { mbar_init(&decided[i], 1); mbar_init(&met[i], 2); mbar_init(&left[i], 2); }
     fence_mbar_init();
     s_fail = 0;
   }
@@ -289,18 +331,30 @@ __global__ void __launch_bounds__(32 * AttnShape<D, ROWS>::WARPS, 1)
   pdl_wait();
   pdl_trigger();
 
-  auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t site) -> bool {
-    return mbar_try_wait(bar, parity) || wait_slow(bar, parity, site, &s_fail);
-  };
+  // A wait by a whole warp.  The first one that gives up makes every later one give up soon, and
+  // the roles' loops end.
   auto wait_warp = [&](uint64_t* bar, uint32_t parity, uint32_t site) -> bool {
-    return __all_sync(FULL_MASK, wait(bar, parity, site));
+#pragma unroll 1
+    for (uint32_t i = 0; !__all_sync(FULL_MASK, try_wait_us(bar, parity)); ++i)
+      if (__any_sync(FULL_MASK, i == WAIT_TRIES || s_fail != 0)) {
+        if (s_fail == 0) s_fail = site;
+        return false;
+      }
+    return true;
   };
-  // The next piece, read by a warp (lanes: all, or one of a warp whose others do nothing).
+  // The next piece, read by a warp.
   auto next_piece = [&](int pi, Piece& x) -> bool {
     const int e = pi % PIECE_RING;
-    if (!wait(&pc_full[e], (pi / PIECE_RING) & 1, ERR_KV8_FULL_WAIT)) return false;
+    if (!wait_warp(&pc_full[e], (pi / PIECE_RING) & 1, ERR_KV8_FULL_WAIT)) return false;
     x = s_piece[e];
     return x.whole >= 0;
+  };
+  auto next_chunks = [&](int pi) -> int {  // how many it has; -1: there is none
+    const int e = pi % PIECE_RING;
+    if (!wait_warp(&pc_full[e], (pi / PIECE_RING) & 1, ERR_KV8_FULL_WAIT)) return -1;
+    const int n = __shfl_sync(FULL_MASK, s_piece[e].whole < 0 ? -1 : max(s_piece[e].cn - s_piece[e].c0, 0), 0);
+    if (lane == 0 && n >= 0) mbar_arrive(&pc_empty[e]);
+    return n;
   };
   auto piece_read = [&](int pi) { mbar_arrive(&pc_empty[pi % PIECE_RING]); };
 
@@ -309,7 +363,20 @@ __global__ void __launch_bounds__(32 * AttnShape<D, ROWS>::WARPS, 1)
     const Run run = find_run<ROWS>(p, blockIdx.x, gridDim.x);
     const int part = p.c.page, parts = AT_CHUNK >> p.page_log2, bytes = part * D;
     Pieces<ROWS> w(p, run);
-    int it = 0, pi = 0;
+    int it = 0, kit = 0, vit = 0, pi = 0;  // (kit, vit: chunks whose keys, values are on their way)
+    // The values of a chunk follow the keys of the next one: their stages come free later.
+    bool v_ok = false;
+    unsigned v_have = 0;
+    int64_t v_ph = 0;
+    auto load_v = [&]() -> bool {
+      const int st = vit % VS;
+      if (vit >= VS && !wait_warp(&vempty[st], ((vit / VS) - 1) & 1, ERR_KV8_EMPTY_WAIT)) return false;
+      if (lane == 0) mbar_arrive_expect_tx(&vfull[st], bytes * __popc(v_have));
+      __syncwarp();
+      if (v_ok) bulk_g2s(sm + S::OFF_VR + st * S::KT + lane * bytes, p.c.v + v_ph * bytes, bytes, &vfull[st]);
+      ++vit;
+      return true;
+    };
     // Pieces are left one ahead of the one that is loaded, so that its q can be made ready.
     auto leave = [&](Piece& x) -> bool {
       const int e = pi % PIECE_RING;
@@ -352,7 +419,7 @@ __global__ void __launch_bounds__(32 * AttnShape<D, ROWS>::WARPS, 1)
       read_scales(id1);
 #pragma unroll 1
       for (int c = c0; c < cn; ++c, ++it) {
-        const int st = it % ST, slot = it % SC_RING;
+        const int st = it % KS, slot = it % SC_RING;
         const int id = id1;
         const float ks = ks1, vs = vs1;
         id1 = id2;
@@ -362,55 +429,57 @@ __global__ void __launch_bounds__(32 * AttnShape<D, ROWS>::WARPS, 1)
         if (id != -2 && !ok) atomicOr(&g_err_kv8_attn, ERR_KV8_PAGE);
         const int64_t ph = int64_t(ok ? id : 0) * p.c.heads + h;
         const unsigned have = __ballot_sync(FULL_MASK, ok);
-        if (it >= ST && !wait_warp(&empty[st], ((it / ST) - 1) & 1, ERR_KV8_EMPTY_WAIT)) {
-          ok_run = false;
-          break;
-        }
+        ok_run = it < KS || wait_warp(&kempty[st], ((it / KS) - 1) & 1, ERR_KV8_EMPTY_WAIT);
+        if (!ok_run) break;
         // (whoever waits for the stage, or for what is made from it, sees its scales)
         if (lane < 8) s_sc[slot][lane] = PageScale{ks, log2f(vs), 1.f / vs, ok ? 1 : 0};
         __syncwarp();
-        uint8_t* dst = sm + st * 2 * S::KT + lane * bytes;
-        if (lane == 0) mbar_arrive_expect_tx(&full[st], 2u * bytes * __popc(have));
+        if (lane == 0) mbar_arrive_expect_tx(&kfull[st], bytes * __popc(have));
         __syncwarp();
-        if (ok) {
-          tma_load3(dst, &tm, 0, 0, static_cast<int>(ph), &full[st]);
-          bulk_g2s(dst + S::KT, p.c.v + ph * bytes, bytes, &full[st]);
-        }
+        if (ok) tma_load3(sm + st * S::KT + lane * bytes, &tm, 0, 0, static_cast<int>(ph), &kfull[st]);
+        ++kit;
+        if (c > c0 && !(ok_run = load_v())) break;
+        v_ok = ok;
+        v_have = have;
+        v_ph = ph;
       }
+      // (now, not behind the next piece's first keys: who reads that piece may need these first)
+      if (ok_run && cn > c0) ok_run = load_v();
       now = next;
       ok_run = ok_run && more;
     }
-    if (s_fail)  // what is in flight has to land
-      for (int i = max(0, it - ST); i < it; ++i)
-        mbar_wait_bounded(&full[i % ST], (i / ST) & 1, &g_err_kv8_attn, ERR_KV8_EMPTY_WAIT);
+    if (s_fail) {  // what is in flight has to land
+      for (int i = max(0, kit - KS); i < kit; ++i)
+        mbar_wait_bounded(&kfull[i % KS], (i / KS) & 1, &g_err_kv8_attn, ERR_KV8_EMPTY_WAIT);
+      for (int i = max(0, vit - VS); i < vit; ++i)
+        mbar_wait_bounded(&vfull[i % VS], (i / VS) & 1, &g_err_kv8_attn, ERR_KV8_EMPTY_WAIT);
+    }
   } else if (role == S_MMA) {
     // ================= S = Q K^T, hi and lo =================
     constexpr uint32_t ID = tc_idesc(128, AT_CHUNK, false, false);
     const uint64_t d_k = tile_desc<D>(sm, 16), d_q = tile_desc<D>(sm + S::OFF_Q, 16);
     int it = 0, qi = 0;
-    Piece x;
-    for (int pi = 0; __all_sync(FULL_MASK, next_piece(pi, x)); ++pi) {
-      if (lane == 0) piece_read(pi);
-      const int chunks = __shfl_sync(FULL_MASK, x.cn - x.c0, 0);
+    int chunks;
+    for (int pi = 0; (chunks = next_chunks(pi)) >= 0; ++pi) {
       if (chunks <= 0) continue;
       bool ok = wait_warp(&qready[qi % QB], (qi / QB) & 1, ERR_KV8_S_WAIT);
       const uint64_t q = d_q + ((qi % QB) * 2 * S::QT >> 4);
 #pragma unroll 1
       for (int c = 0; c < chunks; ++c, ++it) {
-        const int st = it % ST, b = it & 1;
-        ok = wait_warp(&full[st], (it / ST) & 1, ERR_KV8_FULL_WAIT) && ok;
-        if (it >= 2) ok = wait_warp(&pvdone[b], ((it >> 1) - 1) & 1, ERR_KV8_S_WAIT) && ok;
+        const int st = it % KS, b = it % 3;
+        ok = wait_warp(&kfull[st], (it / KS) & 1, ERR_KV8_FULL_WAIT) && ok;
+        if (it >= 3) ok = wait_warp(&pvdone[b], ((it / 3) - 1) & 1, ERR_KV8_S_WAIT) && ok;
         if (ok) {
           tc_fence_after();
-          const uint64_t kk = d_k + (st * 2 * S::KT >> 4);
+          const uint64_t kk = d_k + (st * S::KT >> 4);
+#pragma unroll 1
+          for (int lo = 0; lo < 2; ++lo)
 #pragma unroll
-          for (int d = 0; d < D / 32; ++d) mma_f8(tmem + b * TMEM_S, q + 2 * d, kk + 2 * d, ID, d > 0);
-#pragma unroll
-          for (int d = 0; d < D / 32; ++d)
-            mma_f8(tmem + b * TMEM_S, q + (S::QT >> 4) + 2 * d, kk + 2 * d, ID, true);
+            for (int d = 0; d < D / 32; ++d)
+              mma_f8(tmem + b * TMEM_S, q + lo * (S::QT >> 4) + 2 * d, kk + 2 * d, ID, lo + d > 0);
         }
-        tc_commit(&sready[b]);
-        tc_commit(&empty[st]);
+        tc_commit(&sready[it % 6]);
+        tc_commit(&kempty[st]);
       }
       tc_commit(&qfree[qi % QB]);
       ++qi;
@@ -421,105 +490,36 @@ __global__ void __launch_bounds__(32 * AttnShape<D, ROWS>::WARPS, 1)
     constexpr int VBY = D < 64 ? 64 : 128;  // bytes of a row of a tile of V
     const uint64_t d_v = tile_desc<VBY>(sm + S::OFF_V, AT_CHUNK * 128);
     int it = 0;
-    Piece x;
-    for (int pi = 0; __all_sync(FULL_MASK, next_piece(pi, x)); ++pi) {
-      if (lane == 0) piece_read(pi);
-      const int chunks = __shfl_sync(FULL_MASK, x.cn - x.c0, 0);
+    int chunks;
+    for (int pi = 0; (chunks = next_chunks(pi)) >= 0; ++pi) {
 #pragma unroll 1
       for (int c = 0; c < chunks; ++c, ++it) {
-        const int b = it & 1;
-        bool ok = wait_warp(&vready[b], (it >> 1) & 1, ERR_KV8_PV_WAIT);
-        ok = wait_warp(&pready[b], (it >> 1) & 1, ERR_KV8_PV_WAIT) && ok;
+        const int b = it % 3;
+        bool ok = wait_warp(&vready[it & 1], (it >> 1) & 1, ERR_KV8_PV_WAIT);
+        ok = wait_warp(&pready[b], (it / 3) & 1, ERR_KV8_PV_WAIT) && ok;
         if (ok) {
           tc_fence_after();
-          const uint64_t v = d_v + (b * S::VW >> 4);
+          const uint64_t v = d_v + ((it & 1) * S::VW >> 4);
           // (16 tokens further: 8 columns of P; the address field of V, in units of 16 bytes)
-#pragma unroll
+#pragma unroll 4
           for (int i = 0; i < AT_CHUNK / 16; ++i)
-            mma_f16_ts(tmem + TMEM_O + b * 128, tmem + b * TMEM_S + 8 * i, v + i * VBY, ID, i > 0 || c >= 2);
+            mma_f16_ts(tmem + TMEM_O, tmem + b * TMEM_S + 8 * i, v + i * VBY, ID, i > 0 || c > 0);
         }
         tc_commit(&pvdone[b]);
       }
     }
   } else if (role == CONV) {
     // ================= widening of V, and the split of q =================
-    // q of a piece, the qi-th with chunks.
-    auto split_q = [&](const Piece& x, int qi) {
-      // lanes of a row (8 values each), rows of a warp at a time, and of all four
-      constexpr int LPR = D / 8, RPW = 32 / LPR, STEP = 4 * RPW;
-      if (qi >= QB) wait_warp(&qfree[qi % QB], ((qi / QB) - 1) & 1, ERR_KV8_S_WAIT);
-      uint8_t* qh = sm + S::OFF_Q + (qi % QB) * 2 * S::QT;
-      const int col = (lane % LPR) * 8, r0 = k * RPW + lane / LPR;
-      int i = (x.row0 + r0) / p.group, j = x.row0 + r0 - i * p.group;
-#pragma unroll 1
-      for (int rb = 0; rb < x.rows; rb += 4 * STEP) {
-        uint4 w[4];
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {  // (the loads of four rounds together)
-          w[n] = make_uint4(0u, 0u, 0u, 0u);
-          if (rb + n * STEP + r0 < x.rows)
-            w[n] = __ldg(reinterpret_cast<const uint4*>(p.q + (x.q0 + i) * p.q_tok + (x.h * p.group + j) * p.q_head + col));
-          for (j += STEP; j >= p.group; j -= p.group) ++i;
-        }
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          const int r = rb + n * STEP + r0;
-          const uint32_t in[4] = {w[n].x, w[n].y, w[n].z, w[n].w};
-          uint32_t top = 0;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) top = max(top, max(in[e] & 0x7fffu, (in[e] >> 16) & 0x7fffu));
-#pragma unroll
-          for (int o = LPR / 2; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(FULL_MASK, top, o));
-          // the largest moves to [128, 256); a row with an infinity or a NaN is all NaN
-          const int sh = min(7 - (min(max(static_cast<int>(top >> 7), 1), 254) - 127), 120);
-          const float up = __uint_as_float(static_cast<uint32_t>(127 + sh) << 23);
-          uint32_t hi[2] = {0u, 0u}, lo[2] = {0u, 0u};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const __half2 y = __floats2half2_rn(__uint_as_float(in[e] << 16) * up,
-                                                __uint_as_float(in[e] & 0xffff0000u) * up);
-            const uint16_t h2 = f16x2_to_e4m3x2(*reinterpret_cast<const uint32_t*>(&y));
-            const uint32_t b2 = e4m3x2_to_f16x2(h2);
-            const __half2 rest = __hsub2(y, *reinterpret_cast<const __half2*>(&b2));
-            hi[e >> 1] |= uint32_t(h2) << (16 * (e & 1));
-            lo[e >> 1] |= uint32_t(f16x2_to_e4m3x2(*reinterpret_cast<const uint32_t*>(&rest))) << (16 * (e & 1));
-          }
-          if (r < x.rows) {
-            if (col == 0)
-              s_fr[qi % PIECE_RING][r] = top >= 0x7f80u ? NAN : p.scale2 * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
-            const int at = r * D + ((((col >> 4) ^ swz<D>(r)) << 4) | (col & 15));
-            *reinterpret_cast<uint2*>(qh + at) = make_uint2(hi[0], hi[1]);
-            *reinterpret_cast<uint2*>(qh + S::QT + at) = make_uint2(lo[0], lo[1]);
-          }
-        }
-      }
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&qready[qi % QB]);
-    };
-    int it = 0, qi = 0, pi = 0;
-    Piece x, next;
-    auto take = [&](Piece& x) -> bool {
-      if (!__all_sync(FULL_MASK, next_piece(pi, x))) return false;
+    int it = 0, qi = 0;  // qi: pieces with chunks
+    Piece x;
+    for (int pi = 0; next_piece(pi, x); ++pi) {
       if (lane == 0) piece_read(pi);
-      ++pi;
-      return true;
-    };
-    bool ok = take(next), ready = false;  // there is a next piece; its q is split
-    while (ok) {
-      x = next;
-      if (x.c0 >= x.cn) {
-        ok = take(next);
-        continue;
-      }
-      if (!ready) split_q(x, qi);
-      ready = false;
 #pragma unroll 1
       for (int c = x.c0; c < x.cn; ++c, ++it) {
-        const int st = it % ST, b = it & 1, slot = it % SC_RING;
-        wait_warp(&full[st], (it / ST) & 1, ERR_KV8_FULL_WAIT);
-        if (it >= 2) wait_warp(&pvdone[b], ((it >> 1) - 1) & 1, ERR_KV8_PV_WAIT);
-        const uint8_t* src = sm + st * 2 * S::KT + S::KT;
+        const int st = it % VS, b = it & 1, slot = it % SC_RING;
+        wait_warp(&vfull[st], (it / VS) & 1, ERR_KV8_FULL_WAIT);
+        if (it >= 2) wait_warp(&pvdone[(it - 2) % 3], ((it - 2) / 3) & 1, ERR_KV8_PV_WAIT);
+        uint8_t* src = sm + S::OFF_VR + st * S::KT;
         uint8_t* dst = sm + S::OFF_V + b * S::VW;
         // Chunks with tokens that some row does not see (the causal edge), with rows behind the
         // last token or with pages that were not loaded: 0 * NaN is NaN, so there V takes part
@@ -531,28 +531,36 @@ __global__ void __launch_bounds__(32 * AttnShape<D, ROWS>::WARPS, 1)
         constexpr int TOKS = 32 / LPR;                  // rows of one round
         constexpr int RB = D < 64 ? 64 : 128;
         constexpr int STEP = UPR < 4 ? UPR : 4;         // pieces of a lane in flight
-        bool nan = false;
+        // (odd rows of 128 bytes begin with their second half: no bank is met twice)
+        const int odd = UPR > LPR ? (lane / LPR) & 1 : 0;
+        auto piece_at = [&](int i) { return lane % LPR + ((i / (32 / TOKS)) ^ odd) * LPR; };
+        auto tok_at = [&](int i) { return k * 32 + (i % (32 / TOKS)) * TOKS + lane / LPR; };
+        if (edge) {  // (in the stage itself, by the lane that widens it)
+          bool nan = false;
+#pragma unroll 1
+          for (int i = 0; i < UPR; ++i) {
+            const int tok = tok_at(i);
+            uint4* at = reinterpret_cast<uint4*>(src + tok * D + piece_at(i) * 16);
+            uint4 w = *at;
+            if (c * AT_CHUNK + tok >= x.end || !s_sc[slot][tok >> p.page_log2].ok) w = make_uint4(0u, 0u, 0u, 0u);
+            const uint32_t n0 = nan_codes(w.x), n1 = nan_codes(w.y), n2 = nan_codes(w.z), n3 = nan_codes(w.w);
+            nan |= (n0 | n1 | n2 | n3) != 0;
+            *at = make_uint4(w.x & ~n0, w.y & ~n1, w.z & ~n2, w.w & ~n3);
+          }
+          if (nan) s_nan[qi % PIECE_RING] = qi + 1;
+        }
 #pragma unroll 1
         for (int k0 = 0; k0 < UPR; k0 += STEP) {
           uint4 w[STEP];
           int tok[STEP];
 #pragma unroll
           for (int i = 0; i < STEP; ++i) {
-            tok[i] = k * 32 + ((k0 + i) % (32 / TOKS)) * TOKS + lane / LPR;
-            w[i] = *reinterpret_cast<const uint4*>(src + tok[i] * D + (lane % LPR + ((k0 + i) / (32 / TOKS)) * LPR) * 16);
-          }
-          if (edge) {
-#pragma unroll
-            for (int i = 0; i < STEP; ++i) {
-              if (c * AT_CHUNK + tok[i] >= x.end || !s_sc[slot][tok[i] >> p.page_log2].ok) w[i] = make_uint4(0u, 0u, 0u, 0u);
-              const uint32_t n0 = nan_codes(w[i].x), n1 = nan_codes(w[i].y), n2 = nan_codes(w[i].z), n3 = nan_codes(w[i].w);
-              nan |= (n0 | n1 | n2 | n3) != 0;
-              w[i].x &= ~n0; w[i].y &= ~n1; w[i].z &= ~n2; w[i].w &= ~n3;
-            }
+            tok[i] = tok_at(k0 + i);
+            w[i] = *reinterpret_cast<const uint4*>(src + tok[i] * D + piece_at(k0 + i) * 16);
           }
 #pragma unroll
           for (int i = 0; i < STEP; ++i) {
-            const int piece = lane % LPR + ((k0 + i) / (32 / TOKS)) * LPR;
+            const int piece = piece_at(k0 + i);
             const uint32_t in[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
             uint32_t o[8];
 #pragma unroll
@@ -566,49 +574,112 @@ __global__ void __launch_bounds__(32 * AttnShape<D, ROWS>::WARPS, 1)
             *reinterpret_cast<uint4*>(row + (((q0 + 1) ^ f) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
           }
         }
-        if (nan) s_nan[qi % PIECE_RING] = qi + 1;
         fence_async_smem();
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(&vready[b]);
-          mbar_arrive(&empty[st]);
-        }
-        // The next piece's q, while the products of two widened chunks are under way.
-        if (c == min(x.c0 + 1, x.cn - 1)) {
-          ok = take(next);
-          ready = ok && next.c0 < next.cn;
-          if (ready) split_q(next, qi + 1);
+          mbar_arrive(&vempty[st]);
         }
       }
+      qi += x.c0 < x.cn;
+    }
+  } else if (role == SPLIT) {
+    // ================= q as the sum of two e4m3 values, a tile ahead =================
+    // lanes of a row (16 values each), rows of a warp at a time, and of all four
+    constexpr int LPR = D / 16, RPW = 32 / LPR, STEP = 4 * RPW;
+    const int piece = lane % LPR, r0 = k * RPW + lane / LPR;
+    int qi = 0;
+    Piece x;
+    for (int pi = 0; next_piece(pi, x); ++pi) {
+      if (lane == 0) piece_read(pi);
+      if (x.c0 >= x.cn) continue;
+      const int b = qi % QB;
+      if (qi >= QB) wait_warp(&qfree[b], ((qi / QB) - 1) & 1, ERR_KV8_S_WAIT);
+      const __nv_bfloat16* q = p.q + x.q0 * p.q_tok + x.h * p.group * p.q_head + piece * 16;
+      uint8_t* hi_at = sm + S::OFF_Q + b * 2 * S::QT;
+      uint4 w[2][2];
+      auto load = [&](int r, uint4* w) {
+        w[0] = w[1] = make_uint4(0u, 0u, 0u, 0u);
+        if (r >= x.rows) return;
+        const int i = (x.row0 + r) / p.group, j = x.row0 + r - i * p.group;
+        const uint4* at = reinterpret_cast<const uint4*>(q + i * p.q_tok + j * p.q_head);
+        w[0] = __ldg(at);
+        w[1] = __ldg(at + 1);
+      };
+      load(r0, w[0]);
+      load(r0 + STEP, w[1]);
+#pragma unroll 1
+      for (int r = r0; __any_sync(FULL_MASK, r < x.rows); r += STEP) {
+        const uint32_t in[8] = {w[0][0].x, w[0][0].y, w[0][0].z, w[0][0].w, w[0][1].x, w[0][1].y, w[0][1].z, w[0][1].w};
+        w[0][0] = w[1][0];
+        w[0][1] = w[1][1];
+        load(r + 2 * STEP, w[1]);
+        uint32_t top = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) top = max(top, max(in[e] & 0x7fffu, (in[e] >> 16) & 0x7fffu));
+#pragma unroll
+        for (int o = LPR / 2; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(FULL_MASK, top, o));
+        // the largest moves to [128, 256); a row with an infinity or a NaN is all NaN
+        const int sh = min(7 - (min(max(static_cast<int>(top >> 7), 1), 254) - 127), 120);
+        const float up = __uint_as_float(static_cast<uint32_t>(127 + sh) << 23);
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const __half2 y = __floats2half2_rn(__uint_as_float(in[e] << 16) * up,
+                                              __uint_as_float(in[e] & 0xffff0000u) * up);
+          const uint32_t h2 = f16x2_to_e4m3x2(*reinterpret_cast<const uint32_t*>(&y));
+          const uint32_t b2 = e4m3x2_to_f16x2(static_cast<uint16_t>(h2));
+          const __half2 rest = __hsub2(y, *reinterpret_cast<const __half2*>(&b2));
+          const uint32_t l2 = f16x2_to_e4m3x2(*reinterpret_cast<const uint32_t*>(&rest));
+          hi[e >> 1] = e & 1 ? hi[e >> 1] | h2 << 16 : h2;
+          lo[e >> 1] = e & 1 ? lo[e >> 1] | l2 << 16 : l2;
+        }
+        if (r < x.rows) {
+          if (piece == 0)
+            s_fr[qi % FR_RING][r] = top >= 0x7f80u ? NAN : p.scale2 * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
+          const int at = r * D + ((piece ^ swz<D>(r)) << 4);
+          *reinterpret_cast<uint4*>(hi_at + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4*>(hi_at + S::QT + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&qready[b]);
       ++qi;
     }
   } else {
     // ================= softmax: group g, rows 32 k + lane =================
     const int g = role == SOFT0 ? 0 : 1, r = 32 * k + lane;
     const uint32_t t_lane = static_cast<uint32_t>(32 * k) << 16;
-    const uint32_t t_s = tmem + t_lane + g * TMEM_S, t_o = tmem + t_lane + TMEM_O;
+    const uint32_t t_o = tmem + t_lane + TMEM_O;
     int it0 = 0, qi = 0;  // the piece's first chunk; pieces with chunks
     Piece x;
-    for (int pi = 0; __all_sync(FULL_MASK, next_piece(pi, x)); ++pi) {
+    for (int pi = 0; next_piece(pi, x); ++pi) {
       if (lane == 0) piece_read(pi);
       const int chunks = x.cn - x.c0;
       const bool has = r < x.rows;
       const int i = has ? (x.row0 + r) / p.group : 0, j = has ? x.row0 + r - i * p.group : 0;
       const int seen = x.len - x.n + i + 1;
-      float m = has && seen > 0 ? -INFINITY : 0.f, l = 0.f;  // a row that sees nothing needs no maximum
+      // The maximum that O stands for (s_m, the groups' in common), the one that l stands for, and
+      // the sum of this group's weights.  A row that sees nothing needs no maximum.
+      float* const common = &s_m[qi & 1][r];
+      float m = has && seen > 0 ? -INFINITY : 0.f, l = 0.f;
 #pragma unroll 1
       for (int d = (it0 ^ g) & 1; d < chunks; d += 2) {
         const int it = it0 + d, slot = it % SC_RING;
+        const uint32_t t_s = tmem + t_lane + (it % 3) * TMEM_S;
         const int lim = has ? seen - (x.c0 + d) * AT_CHUNK : AT_CHUNK;  // tokens of the chunk that the row sees
-        wait_warp(&sready[g], (it >> 1) & 1, ERR_KV8_S_WAIT);
+        wait_warp(&sready[it % 6], (it / 6) & 1, ERR_KV8_S_WAIT);
         // the tile before may still be read from O, by the other group too
         if (d < 2 && qi > 0) wait_warp(&left[k], (qi - 1) & 1, ERR_KV8_PV_WAIT);
         tc_fence_after();
-        const float fr = s_fr[qi % PIECE_RING][has ? r : 0];
+        const float fr = has && seen > 0 ? s_fr[qi % FR_RING][r] : 1.f;
+        // Tokens that a row does not see, or whose page was not loaded, get a score of -inf, in S.
         const bool masks = __any_sync(FULL_MASK, lim < AT_CHUNK || (lane < (AT_CHUNK >> p.page_log2) && !s_sc[slot][lane & 7].ok));
-        // 16 scores from w0 on, in units of log2, with a reference or without
-        auto score16 = [&](int w0, float* s, const PageScale& sc, float nref) {
-          const float a = fr * sc.k, b = sc.log2_v + nref;
+        if (masks) mask_scores(t_s, lim, fr, s_sc[slot], p.page_log2);
+        // 16 scores, in units of log2, with a reference or without
+        auto score16 = [&](float* s, const PageScale& sc, float nref) {
+          const float a = score_factor(fr, sc), b = sc.log2_v + nref;
           const float2 a2 = make_float2(a, a), b2 = make_float2(b, b);
 #pragma unroll
           for (int n = 0; n < 16; n += 2) {
@@ -616,112 +687,100 @@ __global__ void __launch_bounds__(32 * AttnShape<D, ROWS>::WARPS, 1)
             s[n] = y.x;
             s[n + 1] = y.y;
           }
-          if (masks) {
-            const int see = sc.ok ? lim - w0 : 0;
-#pragma unroll
-            for (int n = 0; n < 16; ++n)
-              if (n >= see) s[n] = -INFINITY;
-          }
         };
-        // 1. The row's largest score of the chunk, and whether it asks for a new maximum.
+        // 1. The row's largest score of the chunk.
         float nref = m == -INFINITY ? 0.f : -m, top = -INFINITY;
-        float s[2][32];  // (a block is read while the one before is worked on)
-        tmem_ld32_begin(t_s, s[0]);
+        float s[2][16];  // (a block is read while the one before is worked on)
+        tmem_ld16_begin(t_s, s[0]);
         auto look = [&](int w0, float* now, float* next) {
           tmem_ld_end(now);
-          if (w0 + 32 < AT_CHUNK) tmem_ld32_begin(t_s + w0 + 32, next);
-          score16(w0, now, s_sc[slot][w0 >> p.page_log2], nref);
-          score16(w0 + 16, now + 16, s_sc[slot][(w0 + 16) >> p.page_log2], nref);
+          if (w0 + 16 < AT_CHUNK) tmem_ld16_begin(t_s + w0 + 16, next);
+          score16(now, s_sc[slot][w0 >> p.page_log2], nref);
 #pragma unroll
-          for (int n = 0; n < 32; n += 2) top = max3(top, now[n], now[n + 1]);
+          for (int n = 0; n < 16; n += 2) top = max3(top, now[n], now[n + 1]);
         };
 #pragma unroll 1
-        for (int w0 = 0; w0 < AT_CHUNK; w0 += 64) {
+        for (int w0 = 0; w0 < AT_CHUNK; w0 += 32) {
           look(w0, s[0], s[1]);
-          look(w0 + 32, s[1], s[0]);
+          look(w0 + 16, s[1], s[0]);
+        }
+        // Whether it asks for a new maximum, once the other group has said so of the chunk before.
+        top -= nref;
+        if (it > 0) wait_warp(&decided[k], (it - 1) & 1, ERR_KV8_PV_WAIT);
+        if (d > 0) {
+          const float was = m;
+          m = *common;
+          if (was != m) l *= was == -INFINITY ? 0.f : ex2(was - m);
         }
         // (rows that are not there have m = 0)
-        const bool anew = (has && top > RAISE) || (m == -INFINITY && lim > 0);
+        const bool anew = (has && top - m > RAISE) || (m == -INFINITY && lim > 0);
         if (__any_sync(FULL_MASK, anew)) {
-          top = fmaxf(top - nref, m);
-          const float f = top == -INFINITY ? 1.f : ex2(m - top);
-          m = top;
-          nref = m == -INFINITY ? 0.f : -m;
+          const float to = fmaxf(top, m), f = to == -INFINITY ? 1.f : ex2(m - to);
+          m = to;
           l *= f;
-          if (d >= 2) {  // (S of this chunk could only come after the group's last product)
-#pragma unroll 1
-            for (int w0 = 0; w0 < D; w0 += 16) {
-              float o[16];
-              tmem_ld16(t_o + g * 128 + w0, o);
-#pragma unroll
-              for (int n = 0; n < 16; ++n) o[n] *= f;
-              tmem_st16(t_o + g * 128 + w0, o);
-            }
+          if (d > 0) {  // O holds the chunks before, once their products are done
+            wait_warp(&pvdone[(it - 1) % 3], ((it - 1) / 3) & 1, ERR_KV8_PV_WAIT);
+            tc_fence_after();
+            scale_columns<D>(t_o, f);
           }
+          *common = m;
+        } else if (d == 0) {
+          *common = m;
         }
-        // 2. The weights, over the scores that have been read (16 columns of pairs for 32 of S).
-        tmem_ld32_begin(t_s, s[0]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&decided[k]);
+        nref = m == -INFINITY ? 0.f : -m;
+        // 2. The weights, over the scores that have been read (8 columns of pairs for 16 of S).
+        tmem_ld16_begin(t_s, s[0]);
         auto weigh = [&](int w0, float* now, float* next) {
-          uint32_t h[16];
+          uint32_t h[8];
           tmem_ld_end(now);
-          if (w0 + 32 < AT_CHUNK) tmem_ld32_begin(t_s + w0 + 32, next);
+          if (w0 + 16 < AT_CHUNK) tmem_ld16_begin(t_s + w0 + 16, next);
+          const PageScale sc = s_sc[slot][w0 >> p.page_log2];
+          score16(now, sc, nref);
+          float2 part = make_float2(0.f, 0.f);
 #pragma unroll
-          for (int q = 0; q < 32; q += 16) {
-            const PageScale sc = s_sc[slot][(w0 + q) >> p.page_log2];
-            score16(w0 + q, now + q, sc, nref);
-            float2 part = make_float2(0.f, 0.f);
-#pragma unroll
-            for (int n = q; n < q + 16; n += 2) {
-              const float2 e = make_float2(ex2(now[n]), ex2(now[n + 1]));
-              part = __fadd2_rn(part, e);
-              const __half2 hh = __floats2half2_rn(e.x, e.y);
-              h[n / 2] = *reinterpret_cast<const uint32_t*>(&hh);
-            }
-            l = fmaf(part.x + part.y, sc.inv_v, l);
+          for (int n = 0; n < 16; n += 2) {
+            const float2 e = make_float2(ex2(now[n]), ex2(now[n + 1]));
+            part = __fadd2_rn(part, e);
+            const __half2 hh = __floats2half2_rn(e.x, e.y);
+            h[n / 2] = *reinterpret_cast<const uint32_t*>(&hh);
           }
-          tmem_st16u(t_s + w0 / 2, h);
+          l = fmaf(part.x + part.y, sc.inv_v, l);
+          tmem_st8(t_s + w0 / 2, h);
         };
 #pragma unroll 1
-        for (int w0 = 0; w0 < AT_CHUNK; w0 += 64) {
+        for (int w0 = 0; w0 < AT_CHUNK; w0 += 32) {
           weigh(w0, s[0], s[1]);
-          weigh(w0 + 32, s[1], s[0]);
+          weigh(w0 + 16, s[1], s[0]);
         }
         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&pready[g]);
+        if (lane == 0) mbar_arrive(&pready[it % 3]);
       }
 
-      // ---- the two groups' halves of the tile together; each writes half of the columns
+      // ---- the two groups' sums together; each writes half of the columns
       if (chunks > 0 && qi > 0) wait_warp(&left[k], (qi - 1) & 1, ERR_KV8_PV_WAIT);
-      float m1 = -INFINITY, l1 = 0.f;
-      const int mine = (chunks + 1 - ((it0 ^ g) & 1)) / 2;  // this group's chunks
+      float top = -INFINITY, total = 0.f;
       if (chunks > 0) {
-        s_m[g][r] = m;
-        s_l[g][r] = l;
+        s_ml[g][r] = make_float2(m, l);
         __syncwarp();
         if (lane == 0) mbar_arrive(&met[k]);
         wait_warp(&met[k], qi & 1, ERR_KV8_PV_WAIT);
-        m1 = s_m[g ^ 1][r];
-        l1 = s_l[g ^ 1][r];
-        // both groups' last products
+        const float2 other = s_ml[g ^ 1][r];
+        top = *common;
+        // (a sum of 0 is of no chunk, or of none that the row sees; in the groups' order)
+        const float a = l == 0.f ? 0.f : l * ex2(m - top), b = other.y == 0.f ? 0.f : other.y * ex2(other.x - top);
+        total = g == 0 ? a + b : b + a;
         const int last = it0 + chunks - 1;
-        wait_warp(&pvdone[last & 1], (last >> 1) & 1, ERR_KV8_PV_WAIT);
-        if (chunks > 1) wait_warp(&pvdone[(last - 1) & 1], ((last - 1) >> 1) & 1, ERR_KV8_PV_WAIT);
+        wait_warp(&pvdone[last % 3], (last / 3) & 1, ERR_KV8_PV_WAIT);
         tc_fence_after();
       }
-      if (l == 0.f) m = -INFINITY;  // (a NaN stays)
-      if (l1 == 0.f) m1 = -INFINITY;
-      const float top = fmaxf(m, m1), base = top == -INFINITY ? 0.f : top;
-      float f0 = ex2(m - base), f1 = ex2(m1 - base);
-      const float total = fmaf(l, f0, l1 * f1);
+      if (total == 0.f) top = -INFINITY;  // (a NaN stays)
       const int64_t at = (x.q0 + i) * p.q_heads + x.h * p.group + j;
       float* part = p.part + int64_t(x.slot) * ROWS * (D + 2);
-      if (x.whole) {
-        const float inv = total == 0.f ? 0.f : 1.f / total;  // no token seen: 0
-        f0 *= inv;
-        f1 *= inv;
-      }
+      const float f = !x.whole ? 1.f : total == 0.f ? 0.f : 1.f / total;  // no token seen: 0
       if (has && g == 0) {
         if (!x.whole) {
           part[ROWS * D + r] = top;
@@ -734,31 +793,13 @@ __global__ void __launch_bounds__(32 * AttnShape<D, ROWS>::WARPS, 1)
 #pragma unroll 1
       for (int w0 = g * (D / 2); w0 < (g + 1) * (D / 2); w0 += 16) {
         float y[16];
+        if (chunks > 0) {
+          tmem_ld16(t_o + w0, y);
 #pragma unroll
-        for (int n = 0; n < 16; ++n) y[n] = 0.f;
-        if (mine > 0) {
-          float o[16];
-          tmem_ld16(t_o + g * 128 + w0, o);
+          for (int n = 0; n < 16; ++n) y[n] *= f;
+        } else {
 #pragma unroll
-          for (int n = 0; n < 16; ++n) y[n] = o[n] * f0;
-        }
-        if (chunks > mine) {
-          float o[16];
-          tmem_ld16(t_o + (g ^ 1) * 128 + w0, o);
-#pragma unroll
-          for (int n = 0; n < 16; ++n) y[n] = fmaf(o[n], f1, y[n]);
-        }
-        if (nans) {
-          // NaN codes of V that this row sees, among the tokens where they were taken out
-          const int from = max(x.c0, max(x.len - x.n, 0) / AT_CHUNK) * AT_CHUNK;
-          for (int t = from; t < min(seen, x.cn * AT_CHUNK) && has; ++t) {
-            const int id = __ldg(p.table + x.table + (t >> p.page_log2));
-            if (id < 0 || id >= p.c.n_pages) continue;
-            const uint8_t* v = p.c.v + ((int64_t(id) * p.c.heads + x.h) * p.c.page + (t & (p.c.page - 1))) * D + w0;
-#pragma unroll
-            for (int n = 0; n < 16; ++n)
-              if ((v[n] & 0x7f) == 0x7f) y[n] = NAN;
-          }
+          for (int n = 0; n < 16; ++n) y[n] = 0.f;
         }
         if (has) {
           if (x.whole) {
@@ -778,6 +819,12 @@ __global__ void __launch_bounds__(32 * AttnShape<D, ROWS>::WARPS, 1)
           }
         }
       }
+      if (nans && has) {
+        // NaN codes of V that this row sees, among the tokens where they were taken out
+        const int from = max(x.c0, max(x.len - x.n, 0) / AT_CHUNK) * AT_CHUNK;
+        put_nans(p.c, p.table + x.table, p.page_log2, D, x.h, from, min(seen, x.cn * AT_CHUNK), g * (D / 2), (g + 1) * (D / 2),
+                 x.whole ? p.out + at * D : nullptr, part + r * D);
+      }
       if (chunks > 0) {
         tc_fence_before();
         __syncwarp();
@@ -789,6 +836,7 @@ __global__ void __launch_bounds__(32 * AttnShape<D, ROWS>::WARPS, 1)
   }
   tc_fence_before();
   __syncthreads();
+  if (tid == 0 && s_fail) atomicOr(&g_err_kv8_attn, s_fail);
   if (warp == 0) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TMEM_COLS)

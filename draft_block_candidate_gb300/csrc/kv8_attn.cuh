@@ -31,9 +31,9 @@ struct AttnParams {
 
 // Each tile counts HEAD_UNITS more than its chunks, at its front, for what it costs beside them
 // (its q, its first maxima, its outputs), so that runs of many short tiles take no longer than
-// others.  Measured: 3 chunks' time for 128 rows, 1 for few.
+// others.  Measured: 5 chunks' time for 128 rows, 1 for few.
 template <int ROWS>
-constexpr int HEAD_UNITS = ROWS == 128 ? 3 : 1;
+constexpr int HEAD_UNITS = ROWS == 128 ? 5 : 1;
 
 struct SeqUnits {
   int n, len, tiles, chunks;
