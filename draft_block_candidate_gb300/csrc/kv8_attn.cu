@@ -1,31 +1,31 @@
-// Attention of each sequence's new tokens over the 8-bit cache.
+// Attention of each sequence's new tokens over the 8-bit cache, for more than 16 query rows to a
+// (sequence, key / value head); fewer go to kv8_attn_few.cu.
 //
 // For new token i of a sequence's n, and query head j of the group that shares a key / value
 // head:  o = softmax_t(scale q . k_t) v_t  over the cached tokens t < len - n + i + 1.
 //
-// The n * group rows of a (sequence, key / value head) are taken in tiles of 32 or 128 rows; a
-// work unit is one tile against one chunk of 128 cached tokens.  The units of a call, laid out
-// by (sequence, head, tile, chunk), are dealt in equal contiguous runs to one CTA per SM, so
-// that ragged lengths, and few rows over a long axis, load the SMs alike.  A CTA that holds a
-// part of a tile's chunks leaves its maxima, sums and products in the workspace, and a second
-// kernel joins the parts in order: no atomics, the same bits every time.
+// The n * group rows of a (sequence, key / value head) are taken in tiles of 128; a work unit is
+// one tile against one chunk of 128 cached tokens.  The units of a call, laid out by (sequence,
+// head, tile, chunk), are dealt in equal contiguous runs to one CTA per SM, so that ragged
+// lengths, and few rows over a long axis, load the SMs alike.  A CTA that holds a part of a
+// tile's chunks leaves its maxima, sums and products in the workspace, and a second kernel joins
+// the parts in order: no atomics, the same bits every time.
 //
-// Per chunk, on the tensor cores, rows = the tile's (up to 128) query rows:
+// Per chunk, on the tensor cores, rows = the tile's query rows:
 //     S[rows, 128 tokens] = Q K^T    kind::f8f6f4: K as it lies in the cache, q as the sum of
 //                                    two e4m3 values (two products into one accumulator)
 //     O[rows, D]         += P V      kind::f16: P from tensor memory, V widened from e4m3 (exact)
 // Warps: one deals out the pieces of the CTA's run and brings their chunks (K through a swizzled
-// tensor map, V by plain bulk copies) into a ring of stages; one issues the S products and one
-// the O products; four widen V and split the tile's q; and two groups of four take the softmax, a
-// thread a row.  The groups take turns at the chunks: one looks for a chunk's maxima while the
-// other forms the weights of the chunk before, and three buffers of S (which P then takes) let
-// the products run ahead.  Maxima and O are the groups' in common, sums their own: a group
-// decides on a chunk's maxima after the other has on the chunk before.
+// tensor map, V by plain bulk copies) into a ring for each; one issues the S products and one the
+// O products; four split the next tile's q, four widen V; and two groups of four take the
+// softmax, a thread a row.  The groups take turns at the chunks: one looks for a chunk's maxima
+// while the other forms the weights of the chunk before, and three buffers of S (which P then
+// takes) let the products run ahead.  Maxima and O are the groups' in common, sums their own: a
+// group decides on a chunk's maxima after the other has on the chunk before.
 //
 // A row's maximum m moves only where a score passes it by more than 2^14: weights are then at
-// most 2^14, inside f16, and O is scaled in tensor memory only then, by the warp that owns its
-// lanes.  Weights are formed with the old m and thrown away in that case, while S still
-// stands.  The page's key scale multiplies the scores; the logarithm of its value scale is added
+// most 2^14, inside f16, and only then is O scaled in tensor memory, by the warp that owns its
+// lanes.  The page's key scale multiplies the scores; the logarithm of its value scale is added
 // to them, so that p' = scale_v exp(s - m) is what the second product takes, and the sums take
 // p' / scale_v.
 //
@@ -34,9 +34,14 @@
 // 2^-17 of it; p' is rounded to f16 (2^-11 of its value, 2^-25 of the weight of m below 2^-14);
 // out is rounded to bf16.
 //
-// The roles' loops share the SM's instruction cache: their code is kept small (waits that do
-// not end at once are out of line, one warp works out the pieces for all), which measured a
-// factor of two.
+// Bound: neither memory nor the tensor cores (64 sequences of 16 new tokens over 4096 cached
+// ones, 64 query and 8 key / value heads of 128: 114 us, 50.6 us of them the cache's bytes at
+// 6.7 TB/s, 40.5 us the products') but the instructions of the softmax and the widening, some
+// 5700 of a warp to a chunk, which four schedulers issue at half their rate, and 8 thousand
+// cycles of each tile outside its chunks.  The 19 warps run seven loops at once and share an
+// instruction cache: a miss takes some 300 cycles, so the loops are kept small, and what runs once a
+// tile or less is rolled or out of line.  That, the split of q by warps of its own and K and V
+// in rings of their own took the call from 152 to 114 us.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -196,7 +201,7 @@ struct AttnShape {
   static constexpr int KS = D < 128 ? 4 : 3;            // chunks of keys in flight or in use
   static constexpr int VS = D < 128 ? 4 : 2;            // and of values
   static constexpr int VW = 2 * KT;                     // widened values; two buffers
-  static constexpr int QB = 2;                          // buffers of q
+  static constexpr int QB = 2;                          // buffers of q (one: 152 -> 198 us)
   static constexpr int QT = ROWS * D;                   // bytes of q hi, or lo
   static constexpr int OFF_VR = KS * KT;                // values as they come
   static constexpr int OFF_V = OFF_VR + VS * KT;
@@ -862,7 +867,9 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// Rows of a tile.  Up to 16 go to the kernel of kv8_attn_few.cu (8 where that is all).
+// Rows of a tile.  Up to 16 go to the kernel of kv8_attn_few.cu (8 where that is all).  Measured,
+// 128 sequences of up to 8,192 tokens, 8 key / value heads of 128: 16 rows 266 us there and 305
+// here; 24 rows, two of its tiles, 513 there and 306 here.
 int tile_rows(int max_new, int group) {
   const int64_t rows = int64_t(max_new) * group;
   return rows <= 8 ? 8 : rows <= 16 ? 16 : 128;

@@ -162,20 +162,6 @@ struct PageScale {  // of the tokens of one page
   int ok;  // the page was loaded
 };
 
-// The rest of a wait that did not end at once, at most WAIT_LIMIT_CYCLES.  The first one of a CTA
-// that gives up makes every later one give up soon, and the roles' loops end.
-static __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, uint32_t site, volatile int* fail) {
-  const long long t0 = clock64();
-  for (uint32_t i = 1;; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((i & 63) == 0 && (*fail || clock64() - t0 > WAIT_LIMIT_CYCLES)) {
-      atomicOr(&g_err_kv8_attn, site);
-      *fail = 1;
-      return false;
-    }
-  }
-}
-
 // Writes a row's outputs, E columns a lane, from its products, sum of weights and maximum.
 template <int E>
 __device__ __forceinline__ void store_row(const AttnParams& p, int64_t at, int D, int lane,
@@ -199,12 +185,20 @@ __device__ __forceinline__ void store_row(const AttnParams& p, int64_t at, int D
 // of units and 16 rows; the CTAs of the first boundary inside a tile join that tile, from the run
 // that holds its first chunk to the one that holds its last, in that order: a warp for each
 // row, the weights of 32 parts at a time worked out side by side, then the parts added up.
+// What bounds it with few rows is the latency of dependent reads, so the products of 8 parts are
+// on their way before their weights are known (2 sequences over 131,072 tokens: 66 -> 58 us for
+// the whole call); a tile of 128 rows has two or three parts and many warps, and 2 do (8: 114 ->
+// 122 us for 64 sequences of 16 new tokens).
+// Two or four warps to a row, for their share of its parts each, took longer: they keep the
+// attention's last CTAs from their places (128 sequences: 202 us with one, 204, 210).
 template <int ROWS>
 constexpr int JOIN_ROWS = ROWS < 16 ? ROWS : 16;
+template <int ROWS>
+constexpr int JOIN_AHEAD = ROWS == 128 ? 2 : 8;
 
 template <int D, int ROWS>
 __global__ void __launch_bounds__(32 * JOIN_ROWS<ROWS>) kv8_join_kernel(const AttnParams p, int runs) {
-  constexpr int E = D / 32;  // columns of a lane
+  constexpr int E = D / 32, A = JOIN_AHEAD<ROWS>;  // columns of a lane
   const int lane = threadIdx.x & 31, r = blockIdx.y * JOIN_ROWS<ROWS> + (threadIdx.x >> 5);
   // Lengths and row ranges were there before the attention began: they are read, and the
   // tile is found, while it still runs.
@@ -231,37 +225,49 @@ __global__ void __launch_bounds__(32 * JOIN_ROWS<ROWS>) kv8_join_kernel(const At
 #pragma unroll
   for (int n = 0; n < E; ++n) y[n] = 0.f;
   const int count = static_cast<int>(r1 - r0) + 1;
+  auto at = [&](int k) { return parts + k * 2 * STEP + (k == 0 ? lead : 0); };
   for (int k0 = 0; k0 < count; k0 += 32) {
-    const int mine = k0 + lane;
-    const float* q = parts + mine * 2 * STEP + (mine == 0 ? lead : 0);
-    const float m = mine < count ? __ldcg(q + ROWS * D + r) : -INFINITY;
-    const float s = mine < count ? __ldcg(q + ROWS * D + ROWS + r) : 0.f;
-    float nm = fmaxf(m, mx);
+    const int mine = k0 + lane, here = min(32, count - k0);
+    const float m = lane < here ? __ldcg(at(mine) + ROWS * D + r) : -INFINITY;
+    const float s = lane < here ? __ldcg(at(mine) + ROWS * D + ROWS + r) : 0.f;
+    float wt = 0.f;
+    for (int k = 0; k < here; k += A) {
+      float z[A][E];
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) nm = fmaxf(nm, __shfl_xor_sync(FULL_MASK, nm, o));
-    const float base = nm == -INFINITY ? 0.f : nm;
-    const float w = ex2(m - base), back = ex2(mx - base);
-    float add = s * w;
+      for (int i = 0; i < A; ++i) {
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) add += __shfl_xor_sync(FULL_MASK, add, o);
-    sum = fmaf(sum, back, add);
+        for (int n = 0; n < E; ++n) z[i][n] = 0.f;
+        if (k + i >= here) continue;
+        const float* src = at(k0 + k + i) + r * D + lane * E;
+        if constexpr (E == 4) {
+          const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
+          z[i][0] = v.x; z[i][1] = v.y; z[i][2] = v.z; z[i][3] = v.w;
+        } else if constexpr (E == 2) {
+          const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
+          z[i][0] = v.x; z[i][1] = v.y;
+        } else {
+          z[i][0] = __ldcg(src);
+        }
+      }
+      if (k == 0) {
+        float nm = fmaxf(m, mx);
 #pragma unroll
-    for (int n = 0; n < E; ++n) y[n] *= back;
-    mx = nm;
-    const int here = min(32, count - k0);
-#pragma unroll 8
-    for (int k = 0; k < here; ++k) {
-      const float wk = __shfl_sync(FULL_MASK, w, k);
-      const float* src = parts + (k0 + k) * 2 * STEP + (k0 + k == 0 ? lead : 0) + r * D + lane * E;
-      if constexpr (E == 4) {
-        const float4 z = __ldcg(reinterpret_cast<const float4*>(src));
-        y[0] = fmaf(z.x, wk, y[0]); y[1] = fmaf(z.y, wk, y[1]);
-        y[2] = fmaf(z.z, wk, y[2]); y[3] = fmaf(z.w, wk, y[3]);
-      } else if constexpr (E == 2) {
-        const float2 z = __ldcg(reinterpret_cast<const float2*>(src));
-        y[0] = fmaf(z.x, wk, y[0]); y[1] = fmaf(z.y, wk, y[1]);
-      } else {
-        y[0] = fmaf(__ldcg(src), wk, y[0]);
+        for (int o = 16; o >= 1; o >>= 1) nm = fmaxf(nm, __shfl_xor_sync(FULL_MASK, nm, o));
+        const float base = nm == -INFINITY ? 0.f : nm, back = ex2(mx - base);
+        wt = ex2(m - base);  // (0 where there is no part)
+        float add = s * wt;
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) add += __shfl_xor_sync(FULL_MASK, add, o);
+        sum = fmaf(sum, back, add);
+#pragma unroll
+        for (int n = 0; n < E; ++n) y[n] *= back;
+        mx = nm;
+      }
+#pragma unroll
+      for (int i = 0; i < A; ++i) {
+        const float wk = __shfl_sync(FULL_MASK, wt, k + i);  // (k + i < 32)
+#pragma unroll
+        for (int n = 0; n < E; ++n) y[n] = fmaf(z[i][n], wk, y[n]);
       }
     }
   }

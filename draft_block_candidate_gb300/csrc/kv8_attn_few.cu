@@ -53,6 +53,20 @@ struct FewPiece {
   int whole, slot;  // as in kv8_attn.cu
 };
 
+// The rest of a wait that did not end at once, at most WAIT_LIMIT_CYCLES.  The first one of a CTA
+// that gives up makes every later one give up soon, and the roles' loops end.
+__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, uint32_t site, volatile int* fail) {
+  const long long t0 = clock64();
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 63) == 0 && (*fail || clock64() - t0 > WAIT_LIMIT_CYCLES)) {
+      atomicOr(&g_err_kv8_attn, site);
+      *fail = 1;
+      return false;
+    }
+  }
+}
+
 // d += a b for a 16 x 16 tile a and a 16 x 8 tile b.
 __device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                       uint32_t b0, uint32_t b1) {
