@@ -62,8 +62,8 @@ __global__ void __launch_bounds__(AP_THREADS) kv8_append_kernel(const AppendPara
     return;
   }
   const int at = (before >> p.page_log2) + g;  // this page's column of the table
+  if (int64_t(at) << p.page_log2 >= r.len) return;
   const int pos0 = at << p.page_log2;
-  if (pos0 >= r.len) return;
   const int id = __ldg(p.table + b * p.table_stride + at);
   const bool has_old = pos0 < before;
   int src = has_old && p.tail_src ? __ldg(p.tail_src + b) : -1;

@@ -315,6 +315,23 @@ def test_append_reports_bad_pages_and_lengths(lc):
     assert lc.device_error() == 1 << 26
 
 
+def test_append_at_the_end_of_the_longest_table(lc):
+    """Positions next to 2^31, and a bound on the new tokens that reaches beyond them."""
+    page, D = 128, 32
+    cols = ((1 << 31) - 1 - 256) // page
+    table = torch.zeros(1, cols, dtype=torch.int32, device="cuda")
+    table[0, -2:] = torch.tensor([2, 1], dtype=torch.int32)
+    cache = lc.KV8Cache(3, 1, page, D)
+    n = page + 40
+    x = torch.randn(n, 1, D, generator=gen(3), device="cuda").to(torch.bfloat16)
+    i32 = lambda *a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    lc.kv8_append(cache, x, x, i32(0, n), i32(cols * page - 5), table, 1 << 24)
+    near = lc.KV8Cache(3, 1, page, D)
+    lc.kv8_append(near, x, x, i32(0, n), i32(2 * page - 5), i32(2, 1)[None], n)
+    for a, b in ((cache.k, near.k), (cache.v, near.v), (cache.k_scale, near.k_scale)):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)) and int(b.view(torch.uint8).count_nonzero()) > 0
+
+
 # ----------------------------------------------------------------------------- kv8_attention
 
 def fill(lc, cache, q_start, kv_len, table, seed, spread=0):
