@@ -280,6 +280,7 @@ size_t lilicorr_kv8_attention_workspace_bytes(int32_t max_new, int32_t q_heads, 
                                               int32_t head_dim) {
   if (max_new < 1 || max_new > (1 << 24) || kv_heads < 1 || kv_heads > 1024 || q_heads < kv_heads ||
       q_heads % kv_heads || q_heads / kv_heads > 1024 ||
+      int64_t(max_new) * (q_heads / kv_heads) > INT_MAX - 256 ||
       (head_dim != 32 && head_dim != 64 && head_dim != 128))
     return 0;
   return kv8_attention_workspace(max_new, q_heads / kv_heads, head_dim);
@@ -299,8 +300,10 @@ lilicorr_status lilicorr_kv8_attention(const lilicorr_kv8_cache* cache, const vo
   if (!why && (!out || reinterpret_cast<uintptr_t>(out) % 16)) why = "out is null or not 16-byte aligned";
   if (!why && (q_heads < 1 || q_heads % cache->kv_heads || q_heads / cache->kv_heads > 1024))
     why = "q_heads is a multiple of kv_heads, at most 1024 times it";
-  // one sequence's work units (tiles x heads x chunks of tokens, and some for each tile) are
-  // counted in 32 bits
+  // a sequence's rows, and its work units (tiles x heads x chunks of tokens, and some for
+  // each tile), are counted in 32 bits
+  if (!why && int64_t(max_new) * (q_heads / cache->kv_heads) > INT_MAX - 256)
+    why = "max_new * q_heads / kv_heads is too large";
   if (!why && (int64_t(max_new) * (q_heads / cache->kv_heads) / 8 + 1) * cache->kv_heads *
                   ((int64_t(cols) * cache->page + 127) / 128 + 4) > UINT_MAX)
     why = "max_new * q_heads * the table's tokens are too large";

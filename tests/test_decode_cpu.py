@@ -105,6 +105,11 @@ def test_attention_refuses(lib, kw):
     assert attention(lib, **kw) == INVALID
 
 
+def test_attention_refuses_more_rows_than_32_bits_count(lib):
+    assert attention(lib, cache(kv_heads=1), heads=1024, max_new=1 << 22) == INVALID
+    assert lib.lilicorr_kv8_attention_workspace_bytes(1 << 22, 1024, 1, 128) == 0
+
+
 @pytest.mark.parametrize("kw", CACHE_BAD)
 def test_a_bad_cache_is_refused(lib, kw):
     assert append(lib, cache(**kw)) == INVALID
