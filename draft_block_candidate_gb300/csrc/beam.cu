@@ -389,14 +389,18 @@ lilicorr_status lilicorr_beam_reorder(const lilicorr_beam_state* states, int32_t
     return fail(LILICORR_ERR_INVALID_ARG, "lilicorr_beam_reorder: null pointer or no states");
   if (batch < 1 || beams < 1 || beams > BM_MAX)
     return fail(LILICORR_ERR_INVALID_ARG, "lilicorr_beam_reorder: 1 <= beams <= 32 and batch >= 1");
-  constexpr int64_t LIM = int64_t(1) << 46;  // keeps every byte offset far inside 64 bits
+  constexpr int64_t LIM = int64_t(1) << 46;
   auto bad = [&](int64_t n) { return n < 0 || n > LIM; };
+  // (a product of the two keeps far inside 64 bits)
+  auto far = [&](int64_t stride, int64_t count) { return stride > (int64_t(1) << 60) / count; };
   for (int i = 0; i < n_states; ++i) {
     const lilicorr_beam_state& s = states[i];
     if (!s.src || !s.dst || s.segments < 1 || s.seg_bytes < 1 || s.segments > LIM ||
         s.seg_bytes > (int64_t(1) << 32) - 16 || bad(s.src_batch_stride) ||
         bad(s.src_beam_stride) || bad(s.src_seg_stride) || bad(s.dst_batch_stride) ||
-        bad(s.dst_beam_stride) || bad(s.dst_seg_stride))
+        bad(s.dst_beam_stride) || bad(s.dst_seg_stride) || far(s.src_batch_stride, batch) ||
+        far(s.dst_batch_stride, batch) || far(s.src_seg_stride, s.segments) ||
+        far(s.dst_seg_stride, s.segments) || far(s.seg_bytes, s.segments))
       return fail(LILICORR_ERR_INVALID_ARG, "lilicorr_beam_reorder: a state's pointer, size or stride is out of range");
     if (!strides_apart(batch, s.dst_batch_stride, beams, s.dst_beam_stride, s.segments,
                        s.dst_seg_stride, s.seg_bytes))

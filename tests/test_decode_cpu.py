@@ -60,6 +60,14 @@ def test_reorder_refuses(lib, kw):
     assert reorder(lib, **kw) == INVALID
 
 
+def test_reorder_refuses_strides_that_pass_64_bits(lib):
+    apart = dict(src_batch_stride=1 << 45, dst_batch_stride=1 << 45, dst=1 << 40)
+    assert reorder(lib, batch=1 << 20, **apart) == INVALID
+    assert reorder(lib, batch=1 << 20, **{**apart, "src_batch_stride": 1024}) == INVALID
+    assert reorder(lib, segments=1 << 32, src_seg_stride=1 << 40, dst_seg_stride=64, dst_batch_stride=1 << 41,
+                   dst_beam_stride=1 << 39) == INVALID
+
+
 def cache(**kw):
     from draft_block_candidate_gb300 import _lib as L
     a = dict(k_pages=FAKE, v_pages=FAKE, k_scale=FAKE, v_scale=FAKE, n_pages=10, kv_heads=2, page=64, head_dim=128)
