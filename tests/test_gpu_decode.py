@@ -518,6 +518,58 @@ def test_attention_many_stages_give_the_same_bits_every_time(lc, new, group, D, 
             one, kv_len[b:b + 1], table[b:b + 1], new)
 
 
+@pytest.mark.parametrize("new,group,heads", [(16, 8, 4), (17, 1, 12), (1, 4, 8)])
+def test_attention_many_short_sequences(lc, new, group, heads):
+    """Tiles of a chunk or two, so that a CTA's roles are at several of them at once; sequences
+    without tokens among them."""
+    seqs = [(0, 30) if i % 7 == 3 else (0, 0) if i % 11 == 5 else (new, new + (i * 37) % 240) for i in range(200)]
+    q_start, kv_len, table, n_pages = make_batch(seqs, 16, 12)
+    cache = make_cache(lc, n_pages, heads, 16, 64, 13)
+    fill(lc, cache, q_start, kv_len, table, 14)
+    scale = torch.exp2(torch.randint(-20, 20, (int(q_start[-1]), heads * group, 1), generator=gen(15), device="cuda").float())
+    q = (torch.randn(int(q_start[-1]), heads * group, 64, generator=gen(16), device="cuda") * scale).to(torch.bfloat16)
+    check_attention(lc, q, cache, q_start, kv_len, table, new)
+    want = lc.kv8_attention(q, cache, q_start, kv_len, table, new)
+    for _ in range(30):
+        assert torch.equal(lc.kv8_attention(q, cache, q_start, kv_len, table, new), want)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.3, 1e-30])
+@pytest.mark.parametrize("new,group", [(2, 2), (20, 2)])
+def test_attention_of_any_scale(lc, new, group, scale):
+    q_start, kv_len, table, n_pages = make_batch([(new, 150), (new, 20)], 32, 3)
+    cache = make_cache(lc, n_pages, 2, 32, 64, 4)
+    fill(lc, cache, q_start, kv_len, table, 5)
+    q = torch.randn(2 * new, 2 * group, 64, generator=gen(6), device="cuda").to(torch.bfloat16)
+    check_attention(lc, q, cache, q_start, kv_len, table, new, scale=scale)
+
+
+def test_calls_at_once_on_two_streams(lc):
+    """Selection, append and attention of two batches, each on a stream of its own."""
+    side = [torch.cuda.Stream() for _ in range(2)]
+    work = []
+    for s in range(2):
+        seqs = [(4 + 12 * s, 300 + 900 * i) for i in range(6)]
+        q_start, kv_len, table, n_pages = make_batch(seqs, 64, s)
+        cache = make_cache(lc, n_pages, 2, 64, 128, s, garbage=False)
+        fill(lc, cache, q_start, kv_len, table, 30 + s)
+        rows = int(q_start[-1])
+        q = torch.randn(rows, 8, 128, generator=gen(s), device="cuda").to(torch.bfloat16)
+        kv = torch.randn(rows, 2, 128, generator=gen(40 + s), device="cuda").to(torch.bfloat16)
+        logits, scores = torch.randn(3, 4, 40000 + s, generator=gen(50 + s), device="cuda"), torch.zeros(3, 4, device="cuda")
+        call = lambda st, q=q, kv=kv, cache=cache, a=q_start, b=kv_len, t=table, n=seqs[0][0], x=logits, y=scores: (  # noqa: E731
+            lc.kv8_append(cache, kv, kv, a, b, t, n, stream=st), lc.kv8_attention(q, cache, a, b, t, n, lse=True, stream=st),
+            lc.beam_select(x, y, 5, stream=st))
+        torch.cuda.synchronize()
+        work.append((call, call(None)))
+    torch.cuda.synchronize()
+    for _ in range(10):
+        got = [call(st) for st, (call, _) in zip(side, work)]
+        torch.cuda.synchronize()
+        for g, (_, want) in zip(got, work):
+            assert all(torch.equal(a, b) for a, b in zip(g[1] + g[2], want[1] + want[2]))
+
+
 def test_attention_scores_that_rise_by_any_amount(lc):
     """Keys that grow along the sequence: maxima move in every chunk, by little and by more than
     f16 or f32 weights could hold."""
