@@ -235,8 +235,8 @@ struct Piece {
   int slot;           // of the workspace, for a part
 };
 
-// A row's D sums by f; scores of tokens that it does not see (lim on), or whose page was not
-// loaded, to what its factor makes -inf of.  Out of line for the same reason.
+// A row's D sums by f; -inf to the scores of tokens that it does not see (lim on), or whose page
+// was not loaded.  Out of line, so that the loops do not share the instruction cache with them.
 template <int D>
 __device__ __noinline__ void scale_columns(uint32_t t, float f) {
 #pragma unroll 1
@@ -252,18 +252,17 @@ __device__ __forceinline__ float score_factor(float fr, const PageScale& sc) {
   const float a = fr * sc.k;
   return a == 0.f ? FLT_MIN : a;  // (never 0, so that a score of infinity stays one)
 }
-__device__ __noinline__ void mask_scores(uint32_t t, int lim, float fr, const PageScale* scales, int page_log2) {
+__device__ __noinline__ void mask_scores(uint32_t t, int lim, const PageScale* scales, int page_log2) {
 #pragma unroll 1
   for (int w0 = 0; w0 < AT_CHUNK; w0 += 16) {
     const PageScale sc = scales[w0 >> page_log2];
     const int see = sc.ok ? lim - w0 : 0;
     if (__all_sync(FULL_MASK, see >= 16)) continue;
-    const float no = score_factor(fr, sc) < 0.f ? INFINITY : -INFINITY;
     float s[16];
     tmem_ld16(t + w0, s);
 #pragma unroll
     for (int n = 0; n < 16; ++n)
-      if (n >= see) s[n] = no;
+      if (n >= see) s[n] = -INFINITY;
     tmem_st16(t + w0, s);
   }
 }
@@ -593,6 +592,7 @@ __global__ void __launch_bounds__(32 * AttnShape<D, ROWS>::WARPS, 1)
     // lanes of a row (16 values each), rows of a warp at a time, and of all four
     constexpr int LPR = D / 16, RPW = 32 / LPR, STEP = 4 * RPW;
     const int piece = lane % LPR, r0 = k * RPW + lane / LPR;
+    const uint32_t sign = __float_as_uint(p.scale2) & 0x80000000u;  // q takes the scale's
     int qi = 0;
     Piece x;
     for (int pi = 0; next_piece(pi, x); ++pi) {
@@ -626,7 +626,7 @@ __global__ void __launch_bounds__(32 * AttnShape<D, ROWS>::WARPS, 1)
         for (int o = LPR / 2; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(FULL_MASK, top, o));
         // the largest moves to [128, 256); a row with an infinity or a NaN is all NaN
         const int sh = min(7 - (min(max(static_cast<int>(top >> 7), 1), 254) - 127), 120);
-        const float up = __uint_as_float(static_cast<uint32_t>(127 + sh) << 23);
+        const float up = __uint_as_float(static_cast<uint32_t>(127 + sh) << 23 | sign);
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -641,7 +641,7 @@ __global__ void __launch_bounds__(32 * AttnShape<D, ROWS>::WARPS, 1)
         }
         if (r < x.rows) {
           if (piece == 0)
-            s_fr[qi % FR_RING][r] = top >= 0x7f80u ? NAN : p.scale2 * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
+            s_fr[qi % FR_RING][r] = top >= 0x7f80u ? NAN : fabsf(p.scale2) * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
           const int at = r * D + ((piece ^ swz<D>(r)) << 4);
           *reinterpret_cast<uint4*>(hi_at + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
           *reinterpret_cast<uint4*>(hi_at + S::QT + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
@@ -681,8 +681,8 @@ __global__ void __launch_bounds__(32 * AttnShape<D, ROWS>::WARPS, 1)
         const float fr = has && seen > 0 ? s_fr[qi % FR_RING][r] : 1.f;
         // Tokens that a row does not see, or whose page was not loaded, get a score of -inf, in S.
         const bool masks = __any_sync(FULL_MASK, lim < AT_CHUNK || (lane < (AT_CHUNK >> p.page_log2) && !s_sc[slot][lane & 7].ok));
-        if (masks) mask_scores(t_s, lim, fr, s_sc[slot], p.page_log2);
-        // 16 scores, in units of log2, with a reference or without
+        if (masks) mask_scores(t_s, lim, s_sc[slot], p.page_log2);
+        // 16 scores, in units of log2, above a reference
         auto score16 = [&](float* s, const PageScale& sc, float nref) {
           const float a = score_factor(fr, sc), b = sc.log2_v + nref;
           const float2 a2 = make_float2(a, a), b2 = make_float2(b, b);
@@ -694,15 +694,18 @@ __global__ void __launch_bounds__(32 * AttnShape<D, ROWS>::WARPS, 1)
           }
         };
         // 1. The row's largest score of the chunk.
-        float nref = m == -INFINITY ? 0.f : -m, top = -INFINITY;
+        float top = -INFINITY;
         float s[2][16];  // (a block is read while the one before is worked on)
         tmem_ld16_begin(t_s, s[0]);
         auto look = [&](int w0, float* now, float* next) {
           tmem_ld_end(now);
           if (w0 + 16 < AT_CHUNK) tmem_ld16_begin(t_s + w0 + 16, next);
-          score16(now, s_sc[slot][w0 >> p.page_log2], nref);
+          // (a page's factor is positive, so that its largest product is its largest score)
+          float big = fmaxf(now[0], now[1]);
 #pragma unroll
-          for (int n = 0; n < 16; n += 2) top = max3(top, now[n], now[n + 1]);
+          for (int n = 2; n < 16; n += 2) big = max3(big, now[n], now[n + 1]);
+          const PageScale sc = s_sc[slot][w0 >> p.page_log2];
+          top = fmaxf(top, fmaf(big, score_factor(fr, sc), sc.log2_v));
         };
 #pragma unroll 1
         for (int w0 = 0; w0 < AT_CHUNK; w0 += 32) {
@@ -710,7 +713,6 @@ __global__ void __launch_bounds__(32 * AttnShape<D, ROWS>::WARPS, 1)
           look(w0 + 16, s[1], s[0]);
         }
         // Whether it asks for a new maximum, once the other group has said so of the chunk before.
-        top -= nref;
         if (it > 0) wait_warp(&decided[k], (it - 1) & 1, ERR_KV8_PV_WAIT);
         if (d > 0) {
           const float was = m;
@@ -734,7 +736,7 @@ __global__ void __launch_bounds__(32 * AttnShape<D, ROWS>::WARPS, 1)
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&decided[k]);
-        nref = m == -INFINITY ? 0.f : -m;
+        const float nref = m == -INFINITY ? 0.f : -m;
         // 2. The weights, over the scores that have been read (8 columns of pairs for 16 of S).
         tmem_ld16_begin(t_s, s[0]);
         auto weigh = [&](int w0, float* now, float* next) {
