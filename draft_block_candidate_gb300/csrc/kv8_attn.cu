@@ -34,14 +34,16 @@
 // 2^-17 of it; p' is rounded to f16 (2^-11 of its value, 2^-25 of the weight of m below 2^-14);
 // out is rounded to bf16.
 //
-// Bound: neither memory nor the tensor cores (64 sequences of 16 new tokens over 4096 cached
-// ones, 64 query and 8 key / value heads of 128: 114 us, 50.6 us of them the cache's bytes at
-// 6.7 TB/s, 40.5 us the products') but the instructions of the softmax and the widening, some
-// 5700 of a warp to a chunk, which four schedulers issue at half their rate, and 8 thousand
-// cycles of each tile outside its chunks.  The 19 warps run seven loops at once and share an
-// instruction cache: a miss takes some 300 cycles, so the loops are kept small, and what runs once a
-// tile or less is rolled or out of line.  That, the split of q by warps of its own and K and V
-// in rings of their own took the call from 152 to 114 us.
+// Bound: neither memory nor the tensor cores (64 sequences of 16 new tokens over up to 4,096
+// cached ones, 64 query and 8 key / value heads of 128: 106 us, 97 of them this kernel's; the
+// cache's bytes take 50.6 us at 6.7 TB/s, the products 40.5) but the instructions of the softmax
+// and the widening, some 5,300 of a warp to a chunk, which four schedulers issue at half their
+// rate, and 8,000 cycles of each tile outside its chunks.  The 19 warps run seven loops at once
+// and share an instruction cache, where a miss takes some 300 cycles: the loops are kept small,
+// and what runs once a tile or less is rolled or out of line.  That, the split of q by warps of
+// its own, K and V in rings of their own, one O for both groups and a third buffer of S took the
+// call from 152 to 114 us; blocks of 32 columns of S, unrolled or in registers once for both
+// passes, measured slower than these of 16.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -436,7 +438,7 @@ __global__ void __launch_bounds__(32 * AttnShape<D, ROWS>::WARPS, 1)
         ok_run = it < KS || wait_warp(&kempty[st], ((it / KS) - 1) & 1, ERR_KV8_EMPTY_WAIT);
         if (!ok_run) break;
         // (whoever waits for the stage, or for what is made from it, sees its scales)
-        if (lane < 8) s_sc[slot][lane] = PageScale{ks, log2f(vs), 1.f / vs, ok ? 1 : 0};
+        if (lane < 8) s_sc[slot][lane] = page_scale_of(ks, vs, ok);
         __syncwarp();
         if (lane == 0) mbar_arrive_expect_tx(&kfull[st], bytes * __popc(have));
         __syncwarp();
@@ -534,7 +536,7 @@ __global__ void __launch_bounds__(32 * AttnShape<D, ROWS>::WARPS, 1)
         constexpr int LPR = UPR < 4 ? UPR : 4;          // lanes on a row
         constexpr int TOKS = 32 / LPR;                  // rows of one round
         constexpr int RB = D < 64 ? 64 : 128;
-        constexpr int STEP = UPR < 4 ? UPR : 4;         // pieces of a lane in flight
+        constexpr int STEP = UPR < 2 ? UPR : 2;         // pieces of a lane in flight
         // (odd rows of 128 bytes begin with their second half: no bank is met twice)
         const int odd = UPR > LPR ? (lane / LPR) & 1 : 0;
         auto piece_at = [&](int i) { return lane % LPR + ((i / (32 / TOKS)) ^ odd) * LPR; };

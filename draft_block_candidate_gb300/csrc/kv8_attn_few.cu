@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(32 * FW_WARPS + 32, FW_CTAS) kv8_few_kernel(co
           break;
         }
         if (lane < parts) {
-          const PageScale sc{ks, log2f(vs), 1.f / vs, ok ? 1 : 0};
+          const PageScale sc = page_scale_of(ks, vs, ok);
           for (int n = 0; n < part / 16; ++n) s_sc[slot][lane * (part / 16) + n] = sc;
         }
         __syncwarp();
