@@ -25,10 +25,14 @@ static __device__ uint32_t g_err_beam;
 // near 1, and only the sums m2 + e + log2 f, the division by the float nearest log2 e that the
 // logit pass scales its logits by, and the scores themselves are doubles.
 //
-// One CTA per batch entry; bound by latency.  A few warps for each beam join its segments'
+// One CTA per batch entry; bound by latency, the logit pass by HBM (with K = 32 by the
+// instructions of its top-K: 128 entries of 16 beams, V 151,936 in bf16, take 128 us, 117 of them
+// that pass at 4.65 TB/s; one entry of 4 beams, K = 8, takes 9.9 in all).  A few warps for each beam join its segments'
 // sorted lists (the records of four segments are read at a time); then a thread for each
 // candidate finds its rank, the number of better ones, by binary searches in the beams' lists,
-// so that no step waits for the one before as in a merge that takes one candidate at a time.
+// so that no step waits for the one before as in a merge that takes one candidate at a time
+// (one entry of 4 beams, V 151,936: 11.4 us for the call with the lists joined one by one and the
+// lists searched in turn, 9.9 with them joined two by two and four searched at a time).
 
 // Order-preserving key: unsigned comparison of keys = comparison of the doubles.
 __device__ __forceinline__ uint64_t double_key(double d) {
@@ -194,7 +198,8 @@ __global__ void __launch_bounds__(32 * BM_MAX)
 // up to 16 bytes at the same place of every beam's row) of a batch entry: it reads the
 // column of every wanted parent, then writes every beam's, so a gather in place needs no
 // second buffer and no order between threads; a beam that keeps its own row in place is
-// neither read nor written.  Bound by HBM; several parents' reads of one line meet in L1.
+// neither read nor written.  Bound by HBM; several parents' reads of one line meet in L1 (caches
+// of 8 x 8 beams, 868 MB to move: 129 us, 6.7 TB/s, the copy rate).
 constexpr int BR_MAX_STATES = 16;
 constexpr int BR_THREADS = 256;
 

@@ -370,7 +370,7 @@ typedef struct {
  *   tail_src  nullable [batch]: the page that holds the rows before the first new token, where
  *             that is not the table's own (a beam that starts to write beside others after a
  *             reorder); its earlier rows are copied into the table's page.  < 0: the table's own.
- * No page may be written for two sequences, or be written for one and be the tail_src of another,
+ * No page may be written for two sequences (or twice for one), or be written for one and be the tail_src of another,
  * in one call.  lilicorr_kv8_append needs kv_len >= the new tokens (else bit 26). */
 lilicorr_status lilicorr_kv8_append(const lilicorr_kv8_cache* cache, const void* k,
                                     int64_t k_token_stride, int64_t k_head_stride, const void* v,
@@ -390,8 +390,13 @@ lilicorr_status lilicorr_kv8_append(const lilicorr_kv8_cache* cache, const void*
  *        16-byte aligned
  *   out  [total, q_heads, head_dim] bf16, contiguous, 16-byte aligned; rows outside the
  *        sequences are left as they were
- * Sums, maxima and products are f32; the softmax weights are rounded to f16 before the second
- * product (relative to the row's largest weight times value scale).  Workspace:
+ * What is not finite stays where it is seen: a NaN code in a key or value makes the rows that see
+ * it NaN (a value's in its column), and a row of q with an infinity or a NaN is NaN or what its
+ * infinite scores give.  max_new * q_heads / kv_heads is below 2^31 - 256.
+ * Sums and maxima are f32; the softmax weights are rounded to f16 before the second product
+ * (relative to the row's largest weight times value scale), and q loses what lies 2^-17 below
+ * its row's largest value.  The bits of a result do not depend on when or where its parts were
+ * worked out, but on the device's number of SMs and the other sequences of the call.  Workspace:
  * lilicorr_kv8_attention_workspace_bytes (0 for unsupported sizes; by the current device),
  * 256-byte aligned, no initial contents.  Calls that overlap must not share it.
  * Errors: LILICORR_ERR_INVALID_ARG, LILICORR_ERR_WORKSPACE, LILICORR_ERR_CUDA. */
@@ -414,7 +419,7 @@ const char* lilicorr_last_error(void);
 uint64_t lilicorr_launch_count(void);
 /* Read and clear the device-side error words of the current device (synchronises the
  * device): 0 = no error; otherwise one bit per wait site that gave up (bits 0-7 the logit
- * pass, bits 8-15 the tensor-core GEMM, bits 16-23 the tensor-core attention, bits 27-31
+ * pass, bits 8-15 the tensor-core GEMM, bits 16-23 the tensor-core attention, bits 27-30
  * the cache attention), and of the decoding entry points one bit each for an index or length in
  * device memory that was out of range (24 a parent, 25 a page, 26 a length or row range). */
 lilicorr_status lilicorr_device_error(uint32_t* code);
