@@ -223,7 +223,8 @@ __device__ __forceinline__ Role role_of(int warp, int& k) {
   return static_cast<Role>(warp < 16 ? warp >> 2 : LOAD + warp - 16);
 }
 
-constexpr int SC_RING = 8, PIECE_RING = 4, FR_RING = 8;  // deeper than any warp runs ahead of the softmax
+// deeper than any warp runs ahead of the softmax, and the softmax ahead of the outputs
+constexpr int SC_RING = 8, PIECE_RING = 4, FR_RING = 8, OUT_RING = 4;
 constexpr float RAISE = 14.f;               // log2 of how far a score may pass its reference
 
 // A piece of the CTA's run: the chunks [c0, cn) of a tile that some row of it sees.
@@ -269,16 +270,16 @@ __device__ __noinline__ void mask_scores(uint32_t t, int lim, const PageScale* s
   }
 }
 
-// NaN into the columns [w0, w1) of a row's outputs, or of its part, where a token of [t0, t1) has one.
+// NaN into the columns of a row's outputs, or of its part, where a token of [t0, t1) has one.
 __device__ __noinline__ void put_nans(const Kv8 c, const int32_t* table, int page_log2, int D, int h, int t0, int t1,
-                                      int w0, int w1, __nv_bfloat16* out, float* part) {
+                                      __nv_bfloat16* out, float* part) {
 #pragma unroll 1
   for (int t = t0; t < t1; ++t) {
     const int id = __ldg(table + (t >> page_log2));
     if (id < 0 || id >= c.n_pages) continue;
     const uint8_t* v = c.v + ((int64_t(id) * c.heads + h) * c.page + (t & (c.page - 1))) * D;
 #pragma unroll 1
-    for (int w = w0; w < w1; ++w)
+    for (int w = 0; w < D; ++w)
       if ((v[w] & 0x7f) == 0x7f) {
         if (out) out[w] = __float2bfloat16_rn(NAN);
         else part[w] = NAN;
@@ -295,11 +296,11 @@ __global__ void __launch_bounds__(32 * AttnShape<D, ROWS>::WARPS, 1)
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(at_raw) + 1023) & ~uintptr_t(1023));
   // (sready: of chunk i at i % 6, so that a group meets every phase of its own)
   __shared__ __align__(8) uint64_t kfull[KS], kempty[KS], vfull[VS], vempty[VS], sready[6], vready[2], pready[3], pvdone[3],
-      qready[QB], qfree[QB], pc_full[PIECE_RING], pc_empty[PIECE_RING], decided[NQ], met[NQ], left[NQ];
+      qready[QB], qfree[QB], pc_full[PIECE_RING], pc_empty[PIECE_RING], decided[NQ], met[OUT_RING][NQ], left;
   __shared__ Piece s_piece[PIECE_RING];
   __shared__ PageScale s_sc[SC_RING][8];
-  __shared__ float s_fr[FR_RING][ROWS], s_m[2][ROWS];
-  __shared__ float2 s_ml[2][ROWS];
+  __shared__ float s_fr[FR_RING][ROWS], s_m[OUT_RING][ROWS];
+  __shared__ float2 s_ml[OUT_RING][2][ROWS];
   __shared__ int s_nan[PIECE_RING];  // 1 + the piece in whose V a NaN was taken out
   __shared__ uint32_t s_tmem;
   __shared__ volatile uint32_t s_fail;
@@ -319,7 +320,11 @@ __global__ void __launch_bounds__(32 * AttnShape<D, ROWS>::WARPS, 1)
       mbar_init(&pc_empty[i], S::CONSUMERS);
       s_nan[i] = 0;
     }
-    for (int i = 0; i < NQ; ++i) { mbar_init(&decided[i], 1); mbar_init(&met[i], 2); mbar_init(&left[i], 2); }
+    for (int i = 0; i < NQ; ++i) {
+      mbar_init(&decided[i], 1);
+      for (int j = 0; j < OUT_RING; ++j) mbar_init(&met[j][i], 2);
+    }
+    mbar_init(&left, 4);
     fence_mbar_init();
     s_fail = 0;
   }
@@ -495,9 +500,10 @@ __global__ void __launch_bounds__(32 * AttnShape<D, ROWS>::WARPS, 1)
     constexpr uint32_t ID = tc_idesc(128, D, false, true);
     constexpr int VBY = D < 64 ? 64 : 128;  // bytes of a row of a tile of V
     const uint64_t d_v = tile_desc<VBY>(sm + S::OFF_V, AT_CHUNK * 128);
-    int it = 0;
+    int it = 0, qi = 0;
     int chunks;
     for (int pi = 0; (chunks = next_chunks(pi)) >= 0; ++pi) {
+      if (chunks > 0 && qi++ > 0) wait_warp(&left, qi & 1, ERR_KV8_PV_WAIT);  // the tile before has left O
 #pragma unroll 1
       for (int c = 0; c < chunks; ++c, ++it) {
         const int b = it % 3;
@@ -590,86 +596,159 @@ __global__ void __launch_bounds__(32 * AttnShape<D, ROWS>::WARPS, 1)
       qi += x.c0 < x.cn;
     }
   } else if (role == SPLIT) {
-    // ================= q as the sum of two e4m3 values, a tile ahead =================
+    // ====== q as the sum of two e4m3 values, a tile ahead; then the outputs of the tile before ======
     // lanes of a row (16 values each), rows of a warp at a time, and of all four
     constexpr int LPR = D / 16, RPW = 32 / LPR, STEP = 4 * RPW;
     const int piece = lane % LPR, r0 = k * RPW + lane / LPR;
     const uint32_t sign = __float_as_uint(p.scale2) & 0x80000000u;  // q takes the scale's
-    int qi = 0;
-    Piece x;
-    for (int pi = 0; next_piece(pi, x); ++pi) {
-      if (lane == 0) piece_read(pi);
-      if (x.c0 >= x.cn) continue;
-      const int b = qi % QB;
-      if (qi >= QB) wait_warp(&qfree[b], ((qi / QB) - 1) & 1, ERR_KV8_S_WAIT);
-      const __nv_bfloat16* q = p.q + x.q0 * p.q_tok + x.h * p.group * p.q_head + piece * 16;
-      uint8_t* hi_at = sm + S::OFF_Q + b * 2 * S::QT;
-      uint4 w[2][2];
-      auto load = [&](int r, uint4* w) {
-        w[0] = w[1] = make_uint4(0u, 0u, 0u, 0u);
-        if (r >= x.rows) return;
-        const int i = (x.row0 + r) / p.group, j = x.row0 + r - i * p.group;
-        const uint4* at = reinterpret_cast<const uint4*>(q + i * p.q_tok + j * p.q_head);
-        w[0] = __ldg(at);
-        w[1] = __ldg(at + 1);
-      };
-      load(r0, w[0]);
-      load(r0 + STEP, w[1]);
+    // outputs: row 32 k + lane
+    const int r = 32 * k + lane;
+    const uint32_t t_o = tmem + (static_cast<uint32_t>(32 * k) << 16) + TMEM_O;
+    int it = 0, qi = 0;  // chunks and pieces with chunks, up to x
+    Piece x, y{};
+    y.cn = -1;
+    for (int pi = 0;; ++pi) {
+      const bool more = next_piece(pi, x);
+      if (more && lane == 0) piece_read(pi);
+      if (more && x.c0 < x.cn) {
+        const int b = qi % QB;
+        if (qi >= QB) wait_warp(&qfree[b], ((qi / QB) - 1) & 1, ERR_KV8_S_WAIT);
+        const __nv_bfloat16* q = p.q + x.q0 * p.q_tok + x.h * p.group * p.q_head + piece * 16;
+        uint8_t* hi_at = sm + S::OFF_Q + b * 2 * S::QT;
+        uint4 w[2][2];
+        auto load = [&](int r, uint4* w) {
+          w[0] = w[1] = make_uint4(0u, 0u, 0u, 0u);
+          if (r >= x.rows) return;
+          const int i = (x.row0 + r) / p.group, j = x.row0 + r - i * p.group;
+          const uint4* at = reinterpret_cast<const uint4*>(q + i * p.q_tok + j * p.q_head);
+          w[0] = __ldg(at);
+          w[1] = __ldg(at + 1);
+        };
+        load(r0, w[0]);
+        load(r0 + STEP, w[1]);
 #pragma unroll 1
-      for (int r = r0; __any_sync(FULL_MASK, r < x.rows); r += STEP) {
-        const uint32_t in[8] = {w[0][0].x, w[0][0].y, w[0][0].z, w[0][0].w, w[0][1].x, w[0][1].y, w[0][1].z, w[0][1].w};
-        w[0][0] = w[1][0];
-        w[0][1] = w[1][1];
-        load(r + 2 * STEP, w[1]);
-        uint32_t top = 0;
+        for (int r = r0; __any_sync(FULL_MASK, r < x.rows); r += STEP) {
+          const uint32_t in[8] = {w[0][0].x, w[0][0].y, w[0][0].z, w[0][0].w, w[0][1].x, w[0][1].y, w[0][1].z, w[0][1].w};
+          w[0][0] = w[1][0];
+          w[0][1] = w[1][1];
+          load(r + 2 * STEP, w[1]);
+          uint32_t top = 0;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) top = max(top, max(in[e] & 0x7fffu, (in[e] >> 16) & 0x7fffu));
+          for (int e = 0; e < 8; ++e) top = max(top, max(in[e] & 0x7fffu, (in[e] >> 16) & 0x7fffu));
 #pragma unroll
-        for (int o = LPR / 2; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(FULL_MASK, top, o));
-        // the largest moves to [128, 256); a row with an infinity or a NaN is all NaN
-        const int sh = min(7 - (min(max(static_cast<int>(top >> 7), 1), 254) - 127), 120);
-        const float up = __uint_as_float(static_cast<uint32_t>(127 + sh) << 23 | sign);
-        uint32_t hi[4], lo[4];
+          for (int o = LPR / 2; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(FULL_MASK, top, o));
+          // the largest moves to [128, 256); a row with an infinity or a NaN is all NaN
+          const int sh = min(7 - (min(max(static_cast<int>(top >> 7), 1), 254) - 127), 120);
+          const float up = __uint_as_float(static_cast<uint32_t>(127 + sh) << 23 | sign);
+          uint32_t hi[4], lo[4];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const __half2 y = __floats2half2_rn(__uint_as_float(in[e] << 16) * up,
-                                              __uint_as_float(in[e] & 0xffff0000u) * up);
-          const uint32_t h2 = f16x2_to_e4m3x2(*reinterpret_cast<const uint32_t*>(&y));
-          const uint32_t b2 = e4m3x2_to_f16x2(static_cast<uint16_t>(h2));
-          const __half2 rest = __hsub2(y, *reinterpret_cast<const __half2*>(&b2));
-          const uint32_t l2 = f16x2_to_e4m3x2(*reinterpret_cast<const uint32_t*>(&rest));
-          hi[e >> 1] = e & 1 ? hi[e >> 1] | h2 << 16 : h2;
-          lo[e >> 1] = e & 1 ? lo[e >> 1] | l2 << 16 : l2;
+          for (int e = 0; e < 8; ++e) {
+            const __half2 y = __floats2half2_rn(__uint_as_float(in[e] << 16) * up,
+                                                __uint_as_float(in[e] & 0xffff0000u) * up);
+            const uint32_t h2 = f16x2_to_e4m3x2(*reinterpret_cast<const uint32_t*>(&y));
+            const uint32_t b2 = e4m3x2_to_f16x2(static_cast<uint16_t>(h2));
+            const __half2 rest = __hsub2(y, *reinterpret_cast<const __half2*>(&b2));
+            const uint32_t l2 = f16x2_to_e4m3x2(*reinterpret_cast<const uint32_t*>(&rest));
+            hi[e >> 1] = e & 1 ? hi[e >> 1] | h2 << 16 : h2;
+            lo[e >> 1] = e & 1 ? lo[e >> 1] | l2 << 16 : l2;
+          }
+          if (r < x.rows) {
+            if (piece == 0)
+              s_fr[qi % FR_RING][r] = top >= 0x7f80u ? NAN : fabsf(p.scale2) * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
+            const int at = r * D + ((piece ^ swz<D>(r)) << 4);
+            *reinterpret_cast<uint4*>(hi_at + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(hi_at + S::QT + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          }
         }
-        if (r < x.rows) {
-          if (piece == 0)
-            s_fr[qi % FR_RING][r] = top >= 0x7f80u ? NAN : fabsf(p.scale2) * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
-          const int at = r * D + ((piece ^ swz<D>(r)) << 4);
-          *reinterpret_cast<uint4*>(hi_at + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4*>(hi_at + S::QT + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&qready[b]);
+      }
+      if (y.cn >= 0) {  // y: the piece before, the (qi - 1)th with chunks if it has any
+        const bool has = r < y.rows, some = y.c0 < y.cn;
+        const int i = has ? (y.row0 + r) / p.group : 0, j = has ? y.row0 + r - i * p.group : 0;
+        float top = -INFINITY, total = 0.f;
+        if (some) {
+          const int e = (qi - 1) % OUT_RING;
+          wait_warp(&met[e][k], ((qi - 1) / OUT_RING) & 1, ERR_KV8_PV_WAIT);
+          top = s_m[e][r];
+          // the groups' sums; one of 0 is of no chunk, or of none that the row sees
+          const float2 s0 = s_ml[e][0][r], s1 = s_ml[e][1][r];
+          total = (s0.y == 0.f ? 0.f : s0.y * ex2(s0.x - top)) + (s1.y == 0.f ? 0.f : s1.y * ex2(s1.x - top));
+          wait_warp(&pvdone[(it - 1) % 3], ((it - 1) / 3) & 1, ERR_KV8_PV_WAIT);
+          tc_fence_after();
+        }
+        if (total == 0.f) top = -INFINITY;  // (a NaN stays)
+        const int64_t at = (y.q0 + i) * p.q_heads + y.h * p.group + j;
+        float* part = p.part + int64_t(y.slot) * ROWS * (D + 2);
+        const float f = !y.whole ? 1.f : total == 0.f ? 0.f : 1.f / total;  // no token seen: 0
+#pragma unroll 1
+        for (int w0 = 0; w0 < D; w0 += 16) {
+          float o[16];
+          if (some) {
+            tmem_ld16(t_o + w0, o);
+#pragma unroll
+            for (int n = 0; n < 16; ++n) o[n] *= f;
+          } else {
+#pragma unroll
+            for (int n = 0; n < 16; ++n) o[n] = 0.f;
+          }
+          if (w0 + 16 == D && some) {  // O has been read
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&left);
+          }
+          if (has && y.whole) {
+            uint32_t h[8];
+#pragma unroll
+            for (int n = 0; n < 8; ++n) {
+              const __nv_bfloat162 v = __floats2bfloat162_rn(o[2 * n], o[2 * n + 1]);
+              h[n] = *reinterpret_cast<const uint32_t*>(&v);
+            }
+            uint4* dst = reinterpret_cast<uint4*>(p.out + at * D + w0);
+            dst[0] = make_uint4(h[0], h[1], h[2], h[3]);
+            dst[1] = make_uint4(h[4], h[5], h[6], h[7]);
+          } else if (has) {
+            float4* dst = reinterpret_cast<float4*>(part + r * D + w0);
+#pragma unroll
+            for (int n = 0; n < 4; ++n) dst[n] = make_float4(o[4 * n], o[4 * n + 1], o[4 * n + 2], o[4 * n + 3]);
+          }
+        }
+        if (has && !y.whole) {
+          part[ROWS * D + r] = top;
+          part[ROWS * D + ROWS + r] = total;
+        } else if (has && p.lse) {
+          p.lse[at] = total == 0.f ? -INFINITY : (top + log2f(total)) * LN2_F;
+        }
+        if (has && some && s_nan[(qi - 1) % PIECE_RING] == qi) {
+          // NaN codes of V that this row sees, among the tokens where they were taken out
+          const int from = max(y.c0, max(y.len - y.n, 0) / AT_CHUNK) * AT_CHUNK;
+          put_nans(p.c, p.table + y.table, p.page_log2, D, y.h, from, min(y.len - y.n + i + 1, y.cn * AT_CHUNK),
+                   y.whole ? p.out + at * D : nullptr, part + r * D);
         }
       }
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&qready[b]);
-      ++qi;
+      if (!more) break;
+      y = x;
+      y.cn = max(y.cn, 0);
+      if (x.c0 < x.cn) {
+        it += x.cn - x.c0;
+        ++qi;
+      }
     }
   } else {
     // ================= softmax: group g, rows 32 k + lane =================
     const int g = role == SOFT0 ? 0 : 1, r = 32 * k + lane;
     const uint32_t t_lane = static_cast<uint32_t>(32 * k) << 16;
-    const uint32_t t_o = tmem + t_lane + TMEM_O;
     int it0 = 0, qi = 0;  // the piece's first chunk; pieces with chunks
     Piece x;
     for (int pi = 0; next_piece(pi, x); ++pi) {
       if (lane == 0) piece_read(pi);
       const int chunks = x.cn - x.c0;
       const bool has = r < x.rows;
-      const int i = has ? (x.row0 + r) / p.group : 0, j = has ? x.row0 + r - i * p.group : 0;
-      const int seen = x.len - x.n + i + 1;
+      const int seen = x.len - x.n + (has ? (x.row0 + r) / p.group : 0) + 1;
       // The maximum that O stands for (s_m, the groups' in common), the one that l stands for, and
       // the sum of this group's weights.  A row that sees nothing needs no maximum.
-      float* const common = &s_m[qi & 1][r];
+      float* const common = &s_m[qi % OUT_RING][r];
       float m = has && seen > 0 ? -INFINITY : 0.f, l = 0.f;
 #pragma unroll 1
       for (int d = (it0 ^ g) & 1; d < chunks; d += 2) {
@@ -677,8 +756,6 @@ __global__ void __launch_bounds__(32 * AttnShape<D, ROWS>::WARPS, 1)
         const uint32_t t_s = tmem + t_lane + (it % 3) * TMEM_S;
         const int lim = has ? seen - (x.c0 + d) * AT_CHUNK : AT_CHUNK;  // tokens of the chunk that the row sees
         wait_warp(&sready[it % 6], (it / 6) & 1, ERR_KV8_S_WAIT);
-        // the tile before may still be read from O, by the other group too
-        if (d < 2 && qi > 0) wait_warp(&left[k], (qi - 1) & 1, ERR_KV8_PV_WAIT);
         tc_fence_after();
         const float fr = has && seen > 0 ? s_fr[qi % FR_RING][r] : 1.f;
         // Tokens that a row does not see, or whose page was not loaded, get a score of -inf, in S.
@@ -730,7 +807,7 @@ __global__ void __launch_bounds__(32 * AttnShape<D, ROWS>::WARPS, 1)
           if (d > 0) {  // O holds the chunks before, once their products are done
             wait_warp(&pvdone[(it - 1) % 3], ((it - 1) / 3) & 1, ERR_KV8_PV_WAIT);
             tc_fence_after();
-            scale_columns<D>(t_o, f);
+            scale_columns<D>(tmem + t_lane + TMEM_O, f);
           }
           *common = m;
         } else if (d == 0) {
@@ -769,75 +846,10 @@ __global__ void __launch_bounds__(32 * AttnShape<D, ROWS>::WARPS, 1)
         if (lane == 0) mbar_arrive(&pready[it % 3]);
       }
 
-      // ---- the two groups' sums together; each writes half of the columns
-      if (chunks > 0 && qi > 0) wait_warp(&left[k], (qi - 1) & 1, ERR_KV8_PV_WAIT);
-      float top = -INFINITY, total = 0.f;
       if (chunks > 0) {
-        s_ml[g][r] = make_float2(m, l);
+        s_ml[qi % OUT_RING][g][r] = make_float2(m, l);
         __syncwarp();
-        if (lane == 0) mbar_arrive(&met[k]);
-        wait_warp(&met[k], qi & 1, ERR_KV8_PV_WAIT);
-        const float2 other = s_ml[g ^ 1][r];
-        top = *common;
-        // (a sum of 0 is of no chunk, or of none that the row sees; in the groups' order)
-        const float a = l == 0.f ? 0.f : l * ex2(m - top), b = other.y == 0.f ? 0.f : other.y * ex2(other.x - top);
-        total = g == 0 ? a + b : b + a;
-        const int last = it0 + chunks - 1;
-        wait_warp(&pvdone[last % 3], (last / 3) & 1, ERR_KV8_PV_WAIT);
-        tc_fence_after();
-      }
-      if (total == 0.f) top = -INFINITY;  // (a NaN stays)
-      const int64_t at = (x.q0 + i) * p.q_heads + x.h * p.group + j;
-      float* part = p.part + int64_t(x.slot) * ROWS * (D + 2);
-      const float f = !x.whole ? 1.f : total == 0.f ? 0.f : 1.f / total;  // no token seen: 0
-      if (has && g == 0) {
-        if (!x.whole) {
-          part[ROWS * D + r] = top;
-          part[ROWS * D + ROWS + r] = total;
-        } else if (p.lse) {
-          p.lse[at] = total == 0.f ? -INFINITY : (top + log2f(total)) * LN2_F;
-        }
-      }
-      const bool nans = chunks > 0 && s_nan[qi % PIECE_RING] == qi + 1;
-#pragma unroll 1
-      for (int w0 = g * (D / 2); w0 < (g + 1) * (D / 2); w0 += 16) {
-        float y[16];
-        if (chunks > 0) {
-          tmem_ld16(t_o + w0, y);
-#pragma unroll
-          for (int n = 0; n < 16; ++n) y[n] *= f;
-        } else {
-#pragma unroll
-          for (int n = 0; n < 16; ++n) y[n] = 0.f;
-        }
-        if (has) {
-          if (x.whole) {
-            uint32_t o[8];
-#pragma unroll
-            for (int n = 0; n < 8; ++n) {
-              const __nv_bfloat162 v = __floats2bfloat162_rn(y[2 * n], y[2 * n + 1]);
-              o[n] = *reinterpret_cast<const uint32_t*>(&v);
-            }
-            uint4* dst = reinterpret_cast<uint4*>(p.out + at * D + w0);
-            dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-            dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
-          } else {
-            float4* dst = reinterpret_cast<float4*>(part + r * D + w0);
-#pragma unroll
-            for (int n = 0; n < 4; ++n) dst[n] = make_float4(y[4 * n], y[4 * n + 1], y[4 * n + 2], y[4 * n + 3]);
-          }
-        }
-      }
-      if (nans && has) {
-        // NaN codes of V that this row sees, among the tokens where they were taken out
-        const int from = max(x.c0, max(x.len - x.n, 0) / AT_CHUNK) * AT_CHUNK;
-        put_nans(p.c, p.table + x.table, p.page_log2, D, x.h, from, min(seen, x.cn * AT_CHUNK), g * (D / 2), (g + 1) * (D / 2),
-                 x.whole ? p.out + at * D : nullptr, part + r * D);
-      }
-      if (chunks > 0) {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&left[k]);
+        if (lane == 0) mbar_arrive(&met[qi % OUT_RING][k]);
         it0 += chunks;
         ++qi;
       }
