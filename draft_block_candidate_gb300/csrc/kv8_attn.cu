@@ -200,8 +200,8 @@ __device__ __forceinline__ uint32_t nan_codes(uint32_t w) {  // 0xff in each byt
 template <int D, int ROWS>
 struct AttnShape {
   static constexpr int KT = AT_CHUNK * D;               // bytes of a chunk's keys, or values
-  static constexpr int KS = D < 128 ? 4 : 3;            // chunks of keys in flight or in use
-  static constexpr int VS = D < 128 ? 4 : 2;            // and of values
+  static constexpr int KS = D < 128 ? 4 : 2;            // chunks of keys in flight or in use
+  static constexpr int VS = D < 128 ? 4 : 3;            // and of values
   static constexpr int VW = 2 * KT;                     // widened values; two buffers
   static constexpr int QB = 2;                          // buffers of q (one: 152 -> 198 us)
   static constexpr int QT = ROWS * D;                   // bytes of q hi, or lo
@@ -375,19 +375,6 @@ __global__ void __launch_bounds__(32 * AttnShape<D, ROWS>::WARPS, 1)
     const int part = p.c.page, parts = AT_CHUNK >> p.page_log2, bytes = part * D;
     Pieces<ROWS> w(p, run);
     int it = 0, kit = 0, vit = 0, pi = 0;  // (kit, vit: chunks whose keys, values are on their way)
-    // The values of a chunk follow the keys of the next one: their stages come free later.
-    bool v_ok = false;
-    unsigned v_have = 0;
-    int64_t v_ph = 0;
-    auto load_v = [&]() -> bool {
-      const int st = vit % VS;
-      if (vit >= VS && !wait_warp(&vempty[st], ((vit / VS) - 1) & 1, ERR_KV8_EMPTY_WAIT)) return false;
-      if (lane == 0) mbar_arrive_expect_tx(&vfull[st], bytes * __popc(v_have));
-      __syncwarp();
-      if (v_ok) bulk_g2s(sm + S::OFF_VR + st * S::KT + lane * bytes, p.c.v + v_ph * bytes, bytes, &vfull[st]);
-      ++vit;
-      return true;
-    };
     // Pieces are left one ahead of the one that is loaded, so that its q can be made ready.
     auto leave = [&](Piece& x) -> bool {
       const int e = pi % PIECE_RING;
@@ -449,13 +436,14 @@ __global__ void __launch_bounds__(32 * AttnShape<D, ROWS>::WARPS, 1)
         __syncwarp();
         if (ok) tma_load3(sm + st * S::KT + lane * bytes, &tm, 0, 0, static_cast<int>(ph), &kfull[st]);
         ++kit;
-        if (c > c0 && !(ok_run = load_v())) break;
-        v_ok = ok;
-        v_have = have;
-        v_ph = ph;
+        const int sv = it % VS;
+        ok_run = it < VS || wait_warp(&vempty[sv], ((it / VS) - 1) & 1, ERR_KV8_EMPTY_WAIT);
+        if (!ok_run) break;
+        if (lane == 0) mbar_arrive_expect_tx(&vfull[sv], bytes * __popc(have));
+        __syncwarp();
+        if (ok) bulk_g2s(sm + S::OFF_VR + sv * S::KT + lane * bytes, p.c.v + ph * bytes, bytes, &vfull[sv]);
+        ++vit;
       }
-      // (now, not behind the next piece's first keys: who reads that piece may need these first)
-      if (ok_run && cn > c0) ok_run = load_v();
       now = next;
       ok_run = ok_run && more;
     }
@@ -601,6 +589,7 @@ __global__ void __launch_bounds__(32 * AttnShape<D, ROWS>::WARPS, 1)
     constexpr int LPR = D / 16, RPW = 32 / LPR, STEP = 4 * RPW;
     const int piece = lane % LPR, r0 = k * RPW + lane / LPR;
     const uint32_t sign = __float_as_uint(p.scale2) & 0x80000000u;  // q takes the scale's
+    const int step_i = STEP / p.group, step_j = STEP - step_i * p.group;
     // outputs: row 32 k + lane
     const int r = 32 * k + lane;
     const uint32_t t_o = tmem + (static_cast<uint32_t>(32 * k) << 16) + TMEM_O;
@@ -616,13 +605,20 @@ __global__ void __launch_bounds__(32 * AttnShape<D, ROWS>::WARPS, 1)
         const __nv_bfloat16* q = p.q + x.q0 * p.q_tok + x.h * p.group * p.q_head + piece * 16;
         uint8_t* hi_at = sm + S::OFF_Q + b * 2 * S::QT;
         uint4 w[2][2];
+        int i = (x.row0 + r0) / p.group, j = x.row0 + r0 - i * p.group;  // of the row that is read next
         auto load = [&](int r, uint4* w) {
           w[0] = w[1] = make_uint4(0u, 0u, 0u, 0u);
-          if (r >= x.rows) return;
-          const int i = (x.row0 + r) / p.group, j = x.row0 + r - i * p.group;
-          const uint4* at = reinterpret_cast<const uint4*>(q + i * p.q_tok + j * p.q_head);
-          w[0] = __ldg(at);
-          w[1] = __ldg(at + 1);
+          if (r < x.rows) {
+            const uint4* at = reinterpret_cast<const uint4*>(q + i * p.q_tok + j * p.q_head);
+            w[0] = __ldg(at);
+            w[1] = __ldg(at + 1);
+          }
+          i += step_i;
+          j += step_j;
+          if (j >= p.group) {
+            j -= p.group;
+            ++i;
+          }
         };
         load(r0, w[0]);
         load(r0 + STEP, w[1]);
@@ -634,9 +630,10 @@ __global__ void __launch_bounds__(32 * AttnShape<D, ROWS>::WARPS, 1)
           load(r + 2 * STEP, w[1]);
           uint32_t top = 0;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) top = max(top, max(in[e] & 0x7fffu, (in[e] >> 16) & 0x7fffu));
+          for (int e = 0; e < 8; ++e) top = __vmaxu2(top, in[e] & 0x7fff7fffu);
 #pragma unroll
-          for (int o = LPR / 2; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(FULL_MASK, top, o));
+          for (int o = LPR / 2; o >= 1; o >>= 1) top = __vmaxu2(top, __shfl_xor_sync(FULL_MASK, top, o));
+          top = max(top & 0xffffu, top >> 16);
           // the largest moves to [128, 256); a row with an infinity or a NaN is all NaN
           const int sh = min(7 - (min(max(static_cast<int>(top >> 7), 1), 254) - 127), 120);
           const float up = __uint_as_float(static_cast<uint32_t>(127 + sh) << 23 | sign);
