@@ -17,8 +17,8 @@
 //     O[rows, D]         += P V      kind::f16: P from tensor memory, V widened from e4m3 (exact)
 // Warps: one deals out the pieces of the CTA's run and brings their chunks (K through a swizzled
 // tensor map, V by plain bulk copies) into a ring for each; one issues the S products and one the
-// O products; four split the next tile's q, four widen V; and two groups of four take the
-// softmax, a thread a row.  The groups take turns at the chunks: one looks for a chunk's maxima
+// O products; four split the next tile's q and write the outputs of the one before; four widen V;
+// and two groups of four take the softmax, a thread a row.  The groups take turns at the chunks: one looks for a chunk's maxima
 // while the other forms the weights of the chunk before, and three buffers of S (which P then
 // takes) let the products run ahead.  Maxima and O are the groups' in common, sums their own: a
 // group decides on a chunk's maxima after the other has on the chunk before.
@@ -35,15 +35,16 @@
 // out is rounded to bf16.
 //
 // Bound: neither memory nor the tensor cores (64 sequences of 16 new tokens over up to 4,096
-// cached ones, 64 query and 8 key / value heads of 128: 106 us, 97 of them this kernel's; the
+// cached ones, 64 query and 8 key / value heads of 128: 94.5 us, 88 of them this kernel's; the
 // cache's bytes take 50.6 us at 6.7 TB/s, the products 40.5) but the instructions of the softmax
 // and the widening, some 5,300 of a warp to a chunk, which four schedulers issue at half their
-// rate, and 8,000 cycles of each tile outside its chunks.  The 19 warps run seven loops at once
+// rate, the first tile's q (12,000 cycles before the first product), and what a tile's change
+// leaves idle.  The 19 warps run seven loops at once
 // and share an instruction cache, where a miss takes some 300 cycles: the loops are kept small,
 // and what runs once a tile or less is rolled or out of line.  That, the split of q by warps of
 // its own, K and V in rings of their own, one O for both groups and a third buffer of S took the
-// call from 152 to 114 us; blocks of 32 columns of S, unrolled or in registers once for both
-// passes, measured slower than these of 16.
+// call from 152 to 114 us, the outputs in those warps from 106 to 102.  Blocks of 32 columns of S,
+// unrolled or kept in registers for both passes, measured slower than these of 16.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -200,8 +201,9 @@ __device__ __forceinline__ uint32_t nan_codes(uint32_t w) {  // 0xff in each byt
 template <int D, int ROWS>
 struct AttnShape {
   static constexpr int KT = AT_CHUNK * D;               // bytes of a chunk's keys, or values
-  static constexpr int KS = D < 128 ? 4 : 2;            // chunks of keys in flight or in use
-  static constexpr int VS = D < 128 ? 4 : 3;            // and of values
+  // chunks of keys, and of values, in flight or in use (D = 128: 3 and 2 took 106 us for 101)
+  static constexpr int KS = D < 128 ? 4 : 2;
+  static constexpr int VS = D < 128 ? 4 : 3;
   static constexpr int VW = 2 * KT;                     // widened values; two buffers
   static constexpr int QB = 2;                          // buffers of q (one: 152 -> 198 us)
   static constexpr int QT = ROWS * D;                   // bytes of q hi, or lo
@@ -862,6 +864,58 @@ __global__ void __launch_bounds__(32 * AttnShape<D, ROWS>::WARPS, 1)
   }
 }
 
+// Joins the parts of the tiles that several CTAs hold, in order: a grid row per boundary between
+// two runs.  A tile has two or three parts and many rows, so a warp takes JOIN_ROWS rows, whose
+// reads are under way together, and all warps are resident at once: 6.5 us of a call's 94.5 (12 of
+// 100 with a warp for each row; 2 rows 97, 8 rows 96).
+constexpr int JOIN_ROWS = 4, JOIN_WARPS = 4;
+template <int D, int ROWS>
+__global__ void __launch_bounds__(32 * JOIN_WARPS) kv8_join_kernel(const AttnParams p, int runs) {
+  constexpr int E = D / 32, R = JOIN_ROWS;  // columns of a lane
+  const int lane = threadIdx.x & 31;
+  // (lengths and row ranges were there before the attention began)
+  const JoinTile<D, ROWS> t(p, blockIdx.x, runs);
+  const int r0 = (blockIdx.y * JOIN_WARPS + (threadIdx.x >> 5)) * R, row0 = t.tile * ROWS + r0;
+  if (t.count == 0 || row0 >= t.sq.n * p.group) return;
+  const int rows = min(R, t.sq.n * p.group - row0);
+  pdl_wait();
+  float mx[R], sum[R], y[R][E];
+#pragma unroll
+  for (int q = 0; q < R; ++q) {
+    mx[q] = -INFINITY;
+    sum[q] = 0.f;
+#pragma unroll
+    for (int n = 0; n < E; ++n) y[q][n] = 0.f;
+  }
+#pragma unroll 2
+  for (int k = 0; k < t.count; ++k) {
+    const float* part = t.part(k);
+    float z[R][E], m[R], s[R];
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+      const int r = r0 + min(q, rows - 1);
+      m[q] = __ldcg(part + ROWS * D + r);
+      s[q] = __ldcg(part + ROWS * D + ROWS + r);
+      load_row<E>(part + r * D + lane * E, z[q]);
+    }
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+      const float nm = fmaxf(mx[q], m[q]), base = nm == -INFINITY ? 0.f : nm;
+      const float back = ex2(mx[q] - base), w = ex2(m[q] - base);
+      sum[q] = fmaf(s[q], w, sum[q] * back);
+#pragma unroll
+      for (int n = 0; n < E; ++n) y[q][n] = fmaf(z[q][n], w, y[q][n] * back);
+      mx[q] = nm;
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < R; ++q) {
+    if (q >= rows) break;
+    const int i = (row0 + q) / p.group;
+    store_row<E>(p, (t.sq.q0 + i) * p.q_heads + t.h * p.group + (row0 + q - i * p.group), D, lane, y[q], sum[q], mx[q]);
+  }
+}
+
 // -------------------------------------------------------------------------------- host
 
 namespace {
@@ -898,7 +952,7 @@ cudaError_t launch(const CUtensorMap& tm, const AttnParams& prm, int grid, cudaS
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   PdlScope pdl(true);
-  e = launch_k(kv8_join_kernel<D, ROWS>, dim3(grid, ROWS / JOIN_ROWS<ROWS>), dim3(32 * JOIN_ROWS<ROWS>), 0, stream, prm, grid);
+  e = launch_k(kv8_join_kernel<D, ROWS>, dim3(grid, ROWS / (JOIN_ROWS * JOIN_WARPS)), dim3(32 * JOIN_WARPS), 0, stream, prm, grid);
   if (e == cudaSuccess) note_launch(2);
   return e;
 }

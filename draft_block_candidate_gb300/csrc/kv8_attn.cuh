@@ -200,99 +200,47 @@ __device__ __forceinline__ void store_row(const AttnParams& p, int64_t at, int D
   if (p.lse && lane == 0) p.lse[at] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * LN2_F;
 }
 
-// Joins the parts of the tiles that several CTAs hold.  One CTA per boundary between two runs
-// of units and 16 rows; the CTAs of the first boundary inside a tile join that tile, from the run
-// that holds its first chunk to the one that holds its last, in that order: a warp for each
-// row, the weights of 32 parts at a time worked out side by side, then the parts added up.
-// What bounds it with few rows is the latency of dependent reads, so the products of 8 parts are
-// on their way before their weights are known (2 sequences over 131,072 tokens: 66 -> 58 us for
-// the whole call); a tile of 128 rows has two or three parts and many warps, and 2 do (8: 114 ->
-// 122 us for 64 sequences of 16 new tokens).
-// Two or four warps to a row, for their share of its parts each, took longer: they keep the
-// attention's last CTAs from their places (128 sequences: 202 us with one, 204, 210).
-template <int ROWS>
-constexpr int JOIN_ROWS = ROWS < 16 ? ROWS : 16;
-template <int ROWS>
-constexpr int JOIN_AHEAD = ROWS == 128 ? 2 : 8;
-
-template <int D, int ROWS>
-__global__ void __launch_bounds__(32 * JOIN_ROWS<ROWS>) kv8_join_kernel(const AttnParams p, int runs) {
-  constexpr int E = D / 32, A = JOIN_AHEAD<ROWS>;  // columns of a lane
-  const int lane = threadIdx.x & 31, r = blockIdx.y * JOIN_ROWS<ROWS> + (threadIdx.x >> 5);
-  // Lengths and row ranges were there before the attention began: they are read, and the
-  // tile is found, while it still runs.
-  const Run run = find_run<ROWS>(p, int64_t(blockIdx.x) + 1, runs);
-  const int64_t edge = run.u;  // first unit of run blockIdx.x + 1
-  if (edge >= run.u_end) return;
-  const SeqUnits sq = seq_units<ROWS>(p, run.b);
-  const uint32_t in = static_cast<uint32_t>(edge - run.first);
-  const uint32_t len = sq.chunks + HEAD_UNITS<ROWS>, item = in / len;
-  // the tile's units, and the first of its chunks
-  const int64_t i0 = run.first + int64_t(item) * len, i1 = i0 + len, ic = i0 + HEAD_UNITS<ROWS>;
-  if (edge <= ic) return;                  // the boundary lies before the tile's chunks
-  if (edge - run.per > ic) return;         // an earlier boundary lies among them too
-  const int64_t r0 = blockIdx.x, r1 = (i1 - 1) / run.per;  // runs that hold parts
-  const int h = item / sq.tiles, tile = item - h * sq.tiles;
-  const int row = tile * ROWS + r;
-  if (row >= sq.n * p.group) return;
-  constexpr int64_t STEP = ROWS * (D + 2);
-  // the run that holds the tile's first chunk may hold another tile's part before it
-  const float* parts = p.part + r0 * 2 * STEP;
-  const int64_t lead = r0 * run.per >= i0 ? 0 : STEP;
-  pdl_wait();
-  float mx = -INFINITY, sum = 0.f, y[E];
-#pragma unroll
-  for (int n = 0; n < E; ++n) y[n] = 0.f;
-  const int count = static_cast<int>(r1 - r0) + 1;
-  auto at = [&](int k) { return parts + k * 2 * STEP + (k == 0 ? lead : 0); };
-  for (int k0 = 0; k0 < count; k0 += 32) {
-    const int mine = k0 + lane, here = min(32, count - k0);
-    const float m = lane < here ? __ldcg(at(mine) + ROWS * D + r) : -INFINITY;
-    const float s = lane < here ? __ldcg(at(mine) + ROWS * D + ROWS + r) : 0.f;
-    float wt = 0.f;
-    for (int k = 0; k < here; k += A) {
-      float z[A][E];
-#pragma unroll
-      for (int i = 0; i < A; ++i) {
-#pragma unroll
-        for (int n = 0; n < E; ++n) z[i][n] = 0.f;
-        if (k + i >= here) continue;
-        const float* src = at(k0 + k + i) + r * D + lane * E;
-        if constexpr (E == 4) {
-          const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
-          z[i][0] = v.x; z[i][1] = v.y; z[i][2] = v.z; z[i][3] = v.w;
-        } else if constexpr (E == 2) {
-          const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
-          z[i][0] = v.x; z[i][1] = v.y;
-        } else {
-          z[i][0] = __ldcg(src);
-        }
-      }
-      if (k == 0) {
-        float nm = fmaxf(m, mx);
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) nm = fmaxf(nm, __shfl_xor_sync(FULL_MASK, nm, o));
-        const float base = nm == -INFINITY ? 0.f : nm, back = ex2(mx - base);
-        wt = ex2(m - base);  // (0 where there is no part)
-        float add = s * wt;
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) add += __shfl_xor_sync(FULL_MASK, add, o);
-        sum = fmaf(sum, back, add);
-#pragma unroll
-        for (int n = 0; n < E; ++n) y[n] *= back;
-        mx = nm;
-      }
-#pragma unroll
-      for (int i = 0; i < A; ++i) {
-        const float wk = __shfl_sync(FULL_MASK, wt, k + i);  // (k + i < 32)
-#pragma unroll
-        for (int n = 0; n < E; ++n) y[n] = fmaf(z[i][n], wk, y[n]);
-      }
-    }
+template <int E>
+__device__ __forceinline__ void load_row(const float* src, float (&z)[E]) {
+  if constexpr (E == 4) {
+    const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
+    z[0] = v.x; z[1] = v.y; z[2] = v.z; z[3] = v.w;
+  } else if constexpr (E == 2) {
+    const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
+    z[0] = v.x; z[1] = v.y;
+  } else {
+    z[0] = __ldcg(src);
   }
-  const int i = row / p.group;
-  store_row<E>(p, (sq.q0 + i) * p.q_heads + h * p.group + (row - i * p.group), D, lane, y, sum, mx);
 }
+
+// The tile that the CTAs of boundary `at` between two runs join: the one it is the first boundary
+// inside of, its parts from the run that holds its first chunk to the one that holds its last.
+template <int D, int ROWS>
+struct JoinTile {
+  static constexpr int64_t STEP = ROWS * (D + 2);
+  SeqUnits sq;
+  int h, tile, count;  // count 0: none
+  const float* parts;
+  int64_t lead;        // the run of the first chunk may hold another tile's part before it
+  __device__ __forceinline__ JoinTile(const AttnParams& p, int64_t at, int runs) : count(0) {
+    const Run run = find_run<ROWS>(p, at + 1, runs);
+    const int64_t edge = run.u;  // first unit of the run behind the boundary
+    if (edge >= run.u_end) return;
+    sq = seq_units<ROWS>(p, run.b);
+    const uint32_t in = static_cast<uint32_t>(edge - run.first);
+    const uint32_t len = sq.chunks + HEAD_UNITS<ROWS>, item = in / len;
+    // the tile's units, and the first of its chunks
+    const int64_t i0 = run.first + int64_t(item) * len, i1 = i0 + len, ic = i0 + HEAD_UNITS<ROWS>;
+    if (edge <= ic) return;            // the boundary lies before the tile's chunks
+    if (edge - run.per > ic) return;   // an earlier boundary lies among them too
+    h = item / sq.tiles;
+    tile = item - h * sq.tiles;
+    count = static_cast<int>((i1 - 1) / run.per - at) + 1;
+    parts = p.part + at * 2 * STEP;
+    lead = at * run.per >= i0 ? 0 : STEP;
+  }
+  __device__ __forceinline__ const float* part(int k) const { return parts + k * 2 * STEP + (k == 0 ? lead : 0); }
+};
 
 // A tile of at most 16 rows (kv8_attn_few.cu).
 int kv8_few_runs(int rows);
