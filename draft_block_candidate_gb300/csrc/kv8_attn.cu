@@ -18,10 +18,11 @@
 // Warps: one deals out the pieces of the CTA's run and brings their chunks (K through a swizzled
 // tensor map, V by plain bulk copies) into a ring for each; one issues the S products and one the
 // O products; four split the next tile's q and write the outputs of the one before; four widen V;
-// and two groups of four take the softmax, a thread a row.  The groups take turns at the chunks: one looks for a chunk's maxima
-// while the other forms the weights of the chunk before, and three buffers of S (which P then
-// takes) let the products run ahead.  Maxima and O are the groups' in common, sums their own: a
-// group decides on a chunk's maxima after the other has on the chunk before.
+// and two groups of four take the softmax, a thread a row.  The groups take turns at the chunks:
+// one looks for a chunk's maxima while the other forms the weights of the chunk before, and three
+// buffers of S (which P then takes) let the products run ahead.  Maxima and O are the groups' in
+// common, sums their own: a group decides on a chunk's maxima after the other has on the chunk
+// before.
 //
 // A row's maximum m moves only where a score passes it by more than 2^14: weights are then at
 // most 2^14, inside f16, and only then is O scaled in tensor memory, by the warp that owns its
@@ -39,12 +40,12 @@
 // cache's bytes take 50.6 us at 6.7 TB/s, the products 40.5) but the instructions of the softmax
 // and the widening, some 5,300 of a warp to a chunk, which four schedulers issue at half their
 // rate, the first tile's q (12,000 cycles before the first product), and what a tile's change
-// leaves idle.  The 19 warps run seven loops at once
-// and share an instruction cache, where a miss takes some 300 cycles: the loops are kept small,
-// and what runs once a tile or less is rolled or out of line.  That, the split of q by warps of
-// its own, K and V in rings of their own, one O for both groups and a third buffer of S took the
-// call from 152 to 114 us, the outputs in those warps from 106 to 102.  Blocks of 32 columns of S,
-// unrolled or kept in registers for both passes, measured slower than these of 16.
+// leaves idle.  The 19 warps run seven loops at once and share an instruction cache, where a miss
+// takes some 300 cycles: the loops are kept small, and what runs once a tile or less is rolled or
+// out of line.  That, the split of q by warps of its own, K and V in rings of their own, one O for
+// both groups and a third buffer of S took the call from 152 to 114 us, the outputs in those warps
+// from 106 to 102.  Blocks of 32 columns of S, unrolled or kept in registers for both passes,
+// measured slower than these of 16.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
