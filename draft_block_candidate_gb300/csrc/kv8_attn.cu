@@ -865,58 +865,6 @@ __global__ void __launch_bounds__(32 * AttnShape<D, ROWS>::WARPS, 1)
   }
 }
 
-// Joins the parts of the tiles that several CTAs hold, in order: a grid row per boundary between
-// two runs.  A tile has two or three parts and many rows, so a warp takes JOIN_ROWS rows, whose
-// reads are under way together, and all warps are resident at once: 6.5 us of a call's 94.5 (12 of
-// 100 with a warp for each row; 2 rows 97, 8 rows 96).
-constexpr int JOIN_ROWS = 4, JOIN_WARPS = 4;
-template <int D, int ROWS>
-__global__ void __launch_bounds__(32 * JOIN_WARPS) kv8_join_kernel(const AttnParams p, int runs) {
-  constexpr int E = D / 32, R = JOIN_ROWS;  // columns of a lane
-  const int lane = threadIdx.x & 31;
-  // (lengths and row ranges were there before the attention began)
-  const JoinTile<D, ROWS> t(p, blockIdx.x, runs);
-  const int r0 = (blockIdx.y * JOIN_WARPS + (threadIdx.x >> 5)) * R, row0 = t.tile * ROWS + r0;
-  if (t.count == 0 || row0 >= t.sq.n * p.group) return;
-  const int rows = min(R, t.sq.n * p.group - row0);
-  pdl_wait();
-  float mx[R], sum[R], y[R][E];
-#pragma unroll
-  for (int q = 0; q < R; ++q) {
-    mx[q] = -INFINITY;
-    sum[q] = 0.f;
-#pragma unroll
-    for (int n = 0; n < E; ++n) y[q][n] = 0.f;
-  }
-#pragma unroll 2
-  for (int k = 0; k < t.count; ++k) {
-    const float* part = t.part(k);
-    float z[R][E], m[R], s[R];
-#pragma unroll
-    for (int q = 0; q < R; ++q) {
-      const int r = r0 + min(q, rows - 1);
-      m[q] = __ldcg(part + ROWS * D + r);
-      s[q] = __ldcg(part + ROWS * D + ROWS + r);
-      load_row<E>(part + r * D + lane * E, z[q]);
-    }
-#pragma unroll
-    for (int q = 0; q < R; ++q) {
-      const float nm = fmaxf(mx[q], m[q]), base = nm == -INFINITY ? 0.f : nm;
-      const float back = ex2(mx[q] - base), w = ex2(m[q] - base);
-      sum[q] = fmaf(s[q], w, sum[q] * back);
-#pragma unroll
-      for (int n = 0; n < E; ++n) y[q][n] = fmaf(z[q][n], w, y[q][n] * back);
-      mx[q] = nm;
-    }
-  }
-#pragma unroll
-  for (int q = 0; q < R; ++q) {
-    if (q >= rows) break;
-    const int i = (row0 + q) / p.group;
-    store_row<E>(p, (t.sq.q0 + i) * p.q_heads + t.h * p.group + (row0 + q - i * p.group), D, lane, y[q], sum[q], mx[q]);
-  }
-}
-
 // -------------------------------------------------------------------------------- host
 
 namespace {
@@ -953,7 +901,7 @@ cudaError_t launch(const CUtensorMap& tm, const AttnParams& prm, int grid, cudaS
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   PdlScope pdl(true);
-  e = launch_k(kv8_join_kernel<D, ROWS>, dim3(grid, ROWS / (JOIN_ROWS * JOIN_WARPS)), dim3(32 * JOIN_WARPS), 0, stream, prm, grid);
+  e = launch_k(kv8_join_kernel<D, ROWS, 4, 8>, dim3(grid, 8), dim3(128), 0, stream, prm, grid);
   if (e == cudaSuccess) note_launch(2);
   return e;
 }

@@ -200,6 +200,39 @@ __device__ __forceinline__ void store_row(const AttnParams& p, int64_t at, int D
   if (p.lse && lane == 0) p.lse[at] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * LN2_F;
 }
 
+// ------------------------------------------------------------------------------- joining
+
+// The tile that boundary `at` between two runs lies inside of, among its chunks: `count` parts
+// from the run that holds its first chunk to the one that holds its last, and so count - 1
+// boundaries, of which this is number `j`.
+template <int D, int ROWS>
+struct JoinTile {
+  static constexpr int64_t STEP = ROWS * (D + 2);
+  SeqUnits sq;
+  int h, tile, count, j;  // count 0: none
+  const float* parts;
+  int64_t lead;           // the run of the first chunk may hold another tile's part before it
+  __device__ __forceinline__ JoinTile(const AttnParams& p, int64_t at, int runs) : count(0) {
+    const Run run = find_run<ROWS>(p, at + 1, runs);
+    const int64_t edge = run.u;  // first unit of the run behind the boundary
+    if (edge >= run.u_end) return;
+    sq = seq_units<ROWS>(p, run.b);
+    const uint32_t in = static_cast<uint32_t>(edge - run.first);
+    const uint32_t len = sq.chunks + HEAD_UNITS<ROWS>, item = in / len;
+    // the tile's units, and the first of its chunks
+    const int64_t i0 = run.first + int64_t(item) * len, i1 = i0 + len, ic = i0 + HEAD_UNITS<ROWS>;
+    if (edge <= ic) return;  // the boundary lies before the tile's chunks
+    h = item / sq.tiles;
+    tile = item - h * sq.tiles;
+    const int64_t r0 = ic / run.per;
+    count = static_cast<int>((i1 - 1) / run.per - r0) + 1;
+    j = static_cast<int>(at - r0);
+    parts = p.part + r0 * 2 * STEP;
+    lead = r0 * run.per >= i0 ? 0 : STEP;
+  }
+  __device__ __forceinline__ const float* part(int k) const { return parts + k * 2 * STEP + (k == 0 ? lead : 0); }
+};
+
 template <int E>
 __device__ __forceinline__ void load_row(const float* src, float (&z)[E]) {
   if constexpr (E == 4) {
@@ -213,34 +246,136 @@ __device__ __forceinline__ void load_row(const float* src, float (&z)[E]) {
   }
 }
 
-// The tile that the CTAs of boundary `at` between two runs join: the one it is the first boundary
-// inside of, its parts from the run that holds its first chunk to the one that holds its last.
-template <int D, int ROWS>
-struct JoinTile {
-  static constexpr int64_t STEP = ROWS * (D + 2);
-  SeqUnits sq;
-  int h, tile, count;  // count 0: none
-  const float* parts;
-  int64_t lead;        // the run of the first chunk may hold another tile's part before it
-  __device__ __forceinline__ JoinTile(const AttnParams& p, int64_t at, int runs) : count(0) {
-    const Run run = find_run<ROWS>(p, at + 1, runs);
-    const int64_t edge = run.u;  // first unit of the run behind the boundary
-    if (edge >= run.u_end) return;
-    sq = seq_units<ROWS>(p, run.b);
-    const uint32_t in = static_cast<uint32_t>(edge - run.first);
-    const uint32_t len = sq.chunks + HEAD_UNITS<ROWS>, item = in / len;
-    // the tile's units, and the first of its chunks
-    const int64_t i0 = run.first + int64_t(item) * len, i1 = i0 + len, ic = i0 + HEAD_UNITS<ROWS>;
-    if (edge <= ic) return;            // the boundary lies before the tile's chunks
-    if (edge - run.per > ic) return;   // an earlier boundary lies among them too
-    h = item / sq.tiles;
-    tile = item - h * sq.tiles;
-    count = static_cast<int>((i1 - 1) / run.per - at) + 1;
-    parts = p.part + at * 2 * STEP;
-    lead = at * run.per >= i0 ? 0 : STEP;
+// Row r's maximum, sum and products (a warp's, E columns a lane) of the parts [k0, k1), in order;
+// the reads of A parts are under way together.
+template <int D, int ROWS, int A>
+__device__ __forceinline__ void join_parts(const JoinTile<D, ROWS>& t, int r, int k0, int k1, float& mx, float& sum,
+                                           float (&y)[D / 32]) {
+  constexpr int E = D / 32;
+  const int lane = threadIdx.x & 31;
+  mx = -INFINITY;
+  sum = 0.f;
+#pragma unroll
+  for (int n = 0; n < E; ++n) y[n] = 0.f;
+#pragma unroll 1
+  for (int k = k0; k < k1; k += A) {
+    float m[A], s[A], z[A][E];
+#pragma unroll
+    for (int i = 0; i < A; ++i) {
+      m[i] = -INFINITY;
+      s[i] = 0.f;
+#pragma unroll
+      for (int n = 0; n < E; ++n) z[i][n] = 0.f;
+      if (k + i < k1) {
+        const float* part = t.part(k + i);
+        m[i] = __ldcg(part + ROWS * D + r);
+        s[i] = __ldcg(part + ROWS * D + ROWS + r);
+        load_row<E>(part + r * D + lane * E, z[i]);
+      }
+    }
+    float nm = mx;
+#pragma unroll
+    for (int i = 0; i < A; ++i) nm = fmaxf(nm, m[i]);
+    const float base = nm == -INFINITY ? 0.f : nm, back = ex2(mx - base);
+    sum *= back;
+#pragma unroll
+    for (int n = 0; n < E; ++n) y[n] *= back;
+#pragma unroll
+    for (int i = 0; i < A; ++i) {
+      const float w = ex2(m[i] - base);  // (0 where there is no part)
+      sum = fmaf(s[i], w, sum);
+#pragma unroll
+      for (int n = 0; n < E; ++n) y[n] = fmaf(z[i][n], w, y[n]);
+    }
+    mx = nm;
   }
-  __device__ __forceinline__ const float* part(int k) const { return parts + k * 2 * STEP + (k == 0 ? lead : 0); }
-};
+}
+
+// Joins the parts of the tiles that several CTAs hold, always in order: Y CTAs of W warps for each
+// boundary between two runs.  The CTAs of all boundaries inside a tile share its rows, and where
+// there are more warps than rows, W / rows of them share a row's parts.  What bounds it is the
+// latency of the reads, so as many as can be are under way: 8 parts of a row, or (a tile of 128 in
+// two parts, the usual case: all warps are resident at once then) two parts of four rows.  Measured,
+// the whole call: 64 sequences of 16 new tokens 94.5 us, 100.4 with a row a warp; 16 new tokens of
+// one sequence over 131,072 with one key / value head 30 us, 185 with the CTAs of one boundary at
+// work alone; two sequences' single tokens over as many, 8 heads, 55 and 58.
+template <int D, int ROWS, int W, int Y>
+__global__ void __launch_bounds__(32 * W) kv8_join_kernel(const AttnParams p, int runs) {
+  constexpr int E = D / 32, R = ROWS / (W * Y);  // columns of a lane; rows of a warp, in the usual case
+  __shared__ float s_y[W][D], s_m[W], s_l[W];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  // Lengths and row ranges were there before the attention began: they are read, and the
+  // tile is found, while it still runs.
+  const JoinTile<D, ROWS> t(p, blockIdx.x, runs);
+  if (t.count == 0) return;
+  const int rows = min(ROWS, t.sq.n * p.group - t.tile * ROWS);
+  const int ctas = (t.count - 1) * Y, mine = (ROWS + ctas - 1) / ctas;  // rows of a CTA
+  const int r0 = (t.j * Y + blockIdx.y) * mine, r1 = min(rows, r0 + mine);
+  if (r0 >= r1) return;
+  pdl_wait();
+  float mx, sum, y[E];
+  auto store = [&](int r) {
+    const int row = t.tile * ROWS + r, i = row / p.group;
+    store_row<E>(p, (t.sq.q0 + i) * p.q_heads + t.h * p.group + (row - i * p.group), D, lane, y, sum, mx);
+  };
+  if (R > 1 && t.count == 2) {
+    const int q0 = r0 + warp * R;
+    float m[2][R], s[2][R], z[2][R][E];
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int q = 0; q < R; ++q) {
+        const int r = min(q0 + q, r1 - 1);
+        m[k][q] = __ldcg(t.part(k) + ROWS * D + r);
+        s[k][q] = __ldcg(t.part(k) + ROWS * D + ROWS + r);
+        load_row<E>(t.part(k) + r * D + lane * E, z[k][q]);
+      }
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+      if (q0 + q >= r1) break;
+      mx = fmaxf(m[0][q], m[1][q]);
+      const float base = mx == -INFINITY ? 0.f : mx, a = ex2(m[0][q] - base), b = ex2(m[1][q] - base);
+      sum = fmaf(s[1][q], b, s[0][q] * a);
+#pragma unroll
+      for (int n = 0; n < E; ++n) y[n] = fmaf(z[1][q][n], b, z[0][q][n] * a);
+      store(q0 + q);
+    }
+    return;
+  }
+  // warps of a row: no more than have 8 parts each
+  const int share = mine < W ? min(W / mine, (t.count + 7) / 8) : 1;
+  if (share == 1) {
+    for (int r = r0 + warp; r < r1; r += W) {
+      join_parts<D, ROWS, 8>(t, r, 0, t.count, mx, sum, y);
+      store(r);
+    }
+    return;
+  }
+  const int r = r0 + warp / share, part = warp % share, each = (t.count + share - 1) / share;
+  if (r < r1) {
+    join_parts<D, ROWS, 8>(t, r, part * each, min(t.count, (part + 1) * each), mx, sum, y);
+#pragma unroll
+    for (int n = 0; n < E; ++n) s_y[warp][lane * E + n] = y[n];
+    if (lane == 0) {
+      s_m[warp] = mx;
+      s_l[warp] = sum;
+    }
+  }
+  __syncthreads();
+  if (r >= r1 || part != 0) return;
+  for (int k = 1; k < share; ++k) mx = fmaxf(mx, s_m[warp + k]);
+  const float base = mx == -INFINITY ? 0.f : mx, own = ex2(s_m[warp] - base);
+  sum *= own;
+#pragma unroll
+  for (int n = 0; n < E; ++n) y[n] *= own;
+  for (int k = 1; k < share; ++k) {
+    const float w = ex2(s_m[warp + k] - base);
+    sum = fmaf(s_l[warp + k], w, sum);
+#pragma unroll
+    for (int n = 0; n < E; ++n) y[n] = fmaf(s_y[warp + k][lane * E + n], w, y[n]);
+  }
+  store(r);
+}
 
 // A tile of at most 16 rows (kv8_attn_few.cu).
 int kv8_few_runs(int rows);

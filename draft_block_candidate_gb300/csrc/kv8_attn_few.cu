@@ -484,65 +484,6 @@ __global__ void __launch_bounds__(32 * FW_WARPS + 32, FW_CTAS) kv8_few_kernel(co
   }
 }
 
-// Joins the parts of the tiles that several CTAs hold, in order: a CTA per boundary between two
-// runs, a warp for each row, the weights of 32 parts at a time worked out side by side, then the
-// parts added up.  What bounds it is the latency of dependent reads, so the products of 8 parts
-// are on their way before their weights are known (2 sequences over 131,072 tokens: 66 -> 58 us
-// for the whole call).  Two or four warps to a row, for their share of its parts each, took
-// longer: they keep the attention's last CTAs from their places (128 sequences: 202 us with one,
-// 204, 210).
-template <int D, int RT>
-__global__ void __launch_bounds__(32 * RT) kv8_few_join_kernel(const AttnParams p, int runs) {
-  constexpr int E = D / 32, A = 8;  // columns of a lane; parts under way
-  const int lane = threadIdx.x & 31, r = threadIdx.x >> 5;
-  // Lengths and row ranges were there before the attention began: they are read, and the
-  // tile is found, while it still runs.
-  const JoinTile<D, RT> t(p, blockIdx.x, runs);
-  const int row = t.tile * RT + r;
-  if (t.count == 0 || row >= t.sq.n * p.group) return;
-  pdl_wait();
-  float mx = -INFINITY, sum = 0.f, y[E];
-#pragma unroll
-  for (int n = 0; n < E; ++n) y[n] = 0.f;
-  for (int k0 = 0; k0 < t.count; k0 += 32) {
-    const int here = min(32, t.count - k0);
-    const float m = lane < here ? __ldcg(t.part(k0 + lane) + RT * D + r) : -INFINITY;
-    const float s = lane < here ? __ldcg(t.part(k0 + lane) + RT * D + RT + r) : 0.f;
-    float wt = 0.f;
-    for (int k = 0; k < here; k += A) {
-      float z[A][E];
-#pragma unroll
-      for (int i = 0; i < A; ++i) {
-#pragma unroll
-        for (int n = 0; n < E; ++n) z[i][n] = 0.f;
-        if (k + i < here) load_row<E>(t.part(k0 + k + i) + r * D + lane * E, z[i]);
-      }
-      if (k == 0) {
-        float nm = fmaxf(m, mx);
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) nm = fmaxf(nm, __shfl_xor_sync(FULL_MASK, nm, o));
-        const float base = nm == -INFINITY ? 0.f : nm, back = ex2(mx - base);
-        wt = ex2(m - base);  // (0 where there is no part)
-        float add = s * wt;
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) add += __shfl_xor_sync(FULL_MASK, add, o);
-        sum = fmaf(sum, back, add);
-#pragma unroll
-        for (int n = 0; n < E; ++n) y[n] *= back;
-        mx = nm;
-      }
-#pragma unroll
-      for (int i = 0; i < A; ++i) {
-        const float wk = __shfl_sync(FULL_MASK, wt, k + i);  // (k + i < 32)
-#pragma unroll
-        for (int n = 0; n < E; ++n) y[n] = fmaf(z[i][n], wk, y[n]);
-      }
-    }
-  }
-  const int i = row / p.group;
-  store_row<E>(p, (t.sq.q0 + i) * p.q_heads + t.h * p.group + (row - i * p.group), D, lane, y, sum, mx);
-}
-
 template <int D, int RT>
 cudaError_t launch(const AttnParams& prm, int runs, cudaStream_t stream) {
   constexpr int smem = FewShape<D, RT>::SMEM;
@@ -552,7 +493,7 @@ cudaError_t launch(const AttnParams& prm, int runs, cudaStream_t stream) {
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   PdlScope pdl(true);
-  e = launch_k(kv8_few_join_kernel<D, RT>, dim3(runs), dim3(32 * RT), 0, stream, prm, runs);
+  e = launch_k(kv8_join_kernel<D, RT, RT, 1>, dim3(runs), dim3(32 * RT), 0, stream, prm, runs);
   if (e == cudaSuccess) note_launch(2);
   return e;
 }

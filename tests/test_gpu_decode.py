@@ -534,6 +534,16 @@ def test_attention_many_short_sequences(lc, new, group, heads):
         assert torch.equal(lc.kv8_attention(q, cache, q_start, kv_len, table, new), want)
 
 
+@pytest.mark.parametrize("heads", [1, 3, 8, 24, 50, 90])
+@pytest.mark.parametrize("new,group", [(1, 3), (2, 7), (19, 2), (16, 8)])
+def test_attention_tiles_in_any_number_of_parts(lc, heads, new, group):
+    q_start, kv_len, table, n_pages = make_batch([(new, 2900 + new)], 128, 3)
+    cache = make_cache(lc, n_pages, heads, 128, 32, 4)
+    fill(lc, cache, q_start, kv_len, table, 5)
+    q = torch.randn(new, heads * group, 32, generator=gen(6), device="cuda").to(torch.bfloat16)
+    check_attention(lc, q, cache, q_start, kv_len, table, new)
+
+
 @pytest.mark.parametrize("scale", [0.0, -0.3, 1e-30])
 @pytest.mark.parametrize("new,group", [(2, 2), (20, 2)])
 def test_attention_of_any_scale(lc, new, group, scale):
