@@ -31,9 +31,10 @@ struct AttnParams {
 
 // Each tile counts HEAD_UNITS more than its chunks, at its front, for what it costs beside them
 // (its q, its first maxima, its outputs), so that runs of many short tiles take no longer than
-// others.  Measured: 5 chunks' time for 128 rows, 1 for few.
+// others.  Measured: 3, 4, 5 and 6 chunks' for 128 rows, 64 sequences of 16 new tokens, 93.7, 93.7,
+// 93.5 and 94.8 us; 0, 1 and 2 for few, 128 sequences of one, 199.5, 197.1 and 198.0.
 template <int ROWS>
-constexpr int HEAD_UNITS = ROWS == 128 ? 5 : 1;
+constexpr int HEAD_UNITS = ROWS == 128 ? 4 : 1;
 
 struct SeqUnits {
   int n, len, tiles, chunks;
