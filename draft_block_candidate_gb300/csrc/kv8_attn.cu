@@ -890,7 +890,7 @@ int tile_rows(int max_new, int group) {
   const int64_t rows = int64_t(max_new) * group;
   return rows <= 8 ? 8 : rows <= 16 ? 16 : 128;
 }
-int runs_of(int rows) { return rows <= 16 ? kv8_few_runs(rows) : device_sm_count(); }
+int runs_of(int rows, int D) { return rows <= 16 ? kv8_few_runs(rows, D) : device_sm_count(); }
 
 template <int D, int ROWS>
 cudaError_t launch(const CUtensorMap& tm, const AttnParams& prm, int grid, cudaStream_t stream) {
@@ -910,7 +910,7 @@ cudaError_t launch(const CUtensorMap& tm, const AttnParams& prm, int grid, cudaS
 
 size_t kv8_attention_workspace(int max_new, int group, int D) {
   const int rows = tile_rows(max_new, group);
-  return size_t(runs_of(rows)) * 2 * rows * (D + 2) * sizeof(float);
+  return size_t(runs_of(rows, D)) * 2 * rows * (D + 2) * sizeof(float);
 }
 
 cudaError_t kv8_attention_launch(const Kv8Attention& a, cudaStream_t stream) {
@@ -943,7 +943,7 @@ cudaError_t kv8_attention_launch(const Kv8Attention& a, cudaStream_t stream) {
          D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B,
          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
-  const int grid = runs_of(rows);
+  const int grid = runs_of(rows, D);
   return D == 128 ? launch<128, 128>(tm, prm, grid, stream)
          : D == 64 ? launch<64, 128>(tm, prm, grid, stream)
                    : launch<32, 128>(tm, prm, grid, stream);

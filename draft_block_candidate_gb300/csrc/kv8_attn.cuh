@@ -379,7 +379,7 @@ __global__ void __launch_bounds__(32 * W) kv8_join_kernel(const AttnParams p, in
 }
 
 // A tile of at most 16 rows (kv8_attn_few.cu).
-int kv8_few_runs(int rows);
+int kv8_few_runs(int rows, int D);
 cudaError_t kv8_few_launch(const AttnParams& p, int D, int rows, cudaStream_t stream);
 cudaError_t kv8_few_read_device_error(uint32_t* code);
 

@@ -32,7 +32,12 @@ namespace {
 
 constexpr int FW_WARPS = 4;
 constexpr int FW_HALF = 64;             // tokens of a stage
-constexpr int FW_CTAS = 2;              // per SM
+// CTAs per SM: as many as their registers allow, since what a warp waits for is latency.  Measured
+// (8 key / value heads): D = 64, 128 sequences of up to 8,192 tokens, 4 rows: 104 us with 4 and 4
+// stages, 115 with 3 and 6, 154 with 2; 16 rows, half the sequences, 82 with 3, 94 with 2; D = 32,
+// 16 rows, 62 with 4, 71 with 3, 127 with 6.
+template <int D, int RT>
+constexpr int FW_CTAS = D == 32 ? 4 : D == 64 ? (RT == 8 ? 4 : 3) : 2;
 constexpr int FW_SC_RING = 16, FW_PIECES = 4;
 constexpr float P_LOG2 = 14.f;          // log2 of the largest weight as it is held
 
@@ -41,7 +46,7 @@ struct FewShape {
   static constexpr int TILE = FW_HALF * D;              // bytes of a stage's keys, or values
   // An even number, so that a stage is always the same pair's: a barrier's wait tells only the
   // parity of a phase, and a pair that skipped phases could take an older one for its own.
-  static constexpr int STAGES = D == 128 ? 4 : 6;
+  static constexpr int STAGES = D == 128 || (D == 64 && RT == 8) ? 4 : 6;
   static_assert(STAGES % 2 == 0);
   static constexpr int RING = STAGES * 2 * TILE;
   static constexpr int SMEM = RING + FW_WARPS * RT * (D + 4) * 4;
@@ -90,7 +95,7 @@ __device__ __forceinline__ uint32_t any_nan4(uint32_t w) { return __vcmpeq4(w & 
 // g + 8 of a block of 16 against rows 2t and 2t + 1 (of 8), and of o' the columns g D / 8 ..
 // of the same rows.  D = head dimension, RT = rows (8 or 16).
 template <int D, int RT>
-__global__ void __launch_bounds__(32 * FW_WARPS + 32, FW_CTAS) kv8_few_kernel(const AttnParams p) {
+__global__ void __launch_bounds__(32 * FW_WARPS + 32, FW_CTAS<D, RT>) kv8_few_kernel(const AttnParams p) {
   using S = FewShape<D, RT>;
   constexpr int KW = D / 16;  // words of a key row a lane reads = steps of 16 of k q^T
   constexpr int VW = D / 32;  // words of a value row a lane reads
@@ -500,14 +505,21 @@ cudaError_t launch(const AttnParams& prm, int runs, cudaStream_t stream) {
 
 }  // namespace
 
-int kv8_few_runs(int) { return FW_CTAS * device_sm_count(); }
+#define LC_FEW(f) \
+  (D == 128 ? (rows == 8 ? f(128, 8) : f(128, 16)) : D == 64 ? (rows == 8 ? f(64, 8) : f(64, 16)) : rows == 8 ? f(32, 8) : f(32, 16))
+int kv8_few_runs(int rows, int D) {
+#define LC_CTAS(DD, RT) FW_CTAS<DD, RT>
+  return LC_FEW(LC_CTAS) * device_sm_count();
+#undef LC_CTAS
+}
 
 cudaError_t kv8_few_launch(const AttnParams& p, int D, int rows, cudaStream_t stream) {
-  const int runs = kv8_few_runs(rows);
-#define LC_RT(DD) (rows == 8 ? launch<DD, 8>(p, runs, stream) : launch<DD, 16>(p, runs, stream))
-  return D == 128 ? LC_RT(128) : D == 64 ? LC_RT(64) : LC_RT(32);
-#undef LC_RT
+  const int runs = kv8_few_runs(rows, D);
+#define LC_LAUNCH(DD, RT) launch<DD, RT>(p, runs, stream)
+  return LC_FEW(LC_LAUNCH);
+#undef LC_LAUNCH
 }
+#undef LC_FEW
 
 cudaError_t kv8_few_read_device_error(uint32_t* code) {
   uint32_t v = 0, zero = 0;
