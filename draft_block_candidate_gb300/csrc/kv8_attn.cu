@@ -226,8 +226,12 @@ __device__ __forceinline__ Role role_of(int warp, int& k) {
   return static_cast<Role>(warp < 16 ? warp >> 2 : LOAD + warp - 16);
 }
 
-// deeper than any warp runs ahead of the softmax, and the softmax ahead of the outputs
-constexpr int SC_RING = 8, PIECE_RING = 4, FR_RING = 8, OUT_RING = 4;
+// Deeper than any warp runs ahead of the softmax, and the softmax ahead of the outputs.  With tiles
+// of one chunk, q is split for a tile while the softmax may be four behind it.  A softmax group
+// that has a chunk of tile t knows that the outputs up to t - 4 have been read (the chunk's scores
+// took a buffer whose products came after them), and leaves its sums for the next tile too, where
+// it has none.
+constexpr int SC_RING = 8, PIECE_RING = 4, FR_RING = 6, OUT_RING = 5;
 constexpr float RAISE = 14.f;               // log2 of how far a score may pass its reference
 
 // A piece of the CTA's run: the chunks [c0, cn) of a tile that some row of it sees.
