@@ -44,8 +44,9 @@
 // takes some 300 cycles: the loops are kept small, and what runs once a tile or less is rolled or
 // out of line.  That, the split of q by warps of its own, K and V in rings of their own, one O for
 // both groups and a third buffer of S took the call from 152 to 114 us, the outputs in those warps
-// from 106 to 102.  Blocks of 32 columns of S, unrolled or kept in registers for both passes,
-// measured slower than these of 16.
+// from 106 to 102.  Weights are formed 32 columns of S at a time (head dimension 32: 348 us with
+// 16, 335 with 32; 128: no difference), maxima 16; more columns unrolled, a block kept in registers
+// for both passes, or a third softmax group (head dimension 32: 356 us) measured slower.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -132,6 +133,29 @@ __device__ __forceinline__ void tmem_ld_end(float* v) {
                  "+f"(v[13]), "+f"(v[14]), "+f"(v[15])
                :
                : "memory");
+}
+__device__ __forceinline__ void tmem_ld32_begin(uint32_t t, float* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
+        "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]),
+        "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]),
+        "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]),
+        "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+      : "r"(t));
+}
+__device__ __forceinline__ void tmem_ld32_end(float* v) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]),
+                 "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]),
+                 "+f"(v[14]), "+f"(v[15]), "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]),
+                 "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]), "+f"(v[24]), "+f"(v[25]),
+                 "+f"(v[26]), "+f"(v[27]), "+f"(v[28])
+               :
+               : "memory");
+  asm volatile("" : "+f"(v[29]), "+f"(v[30]), "+f"(v[31]));
 }
 // Whether a phase has ended; waits for it up to a microsecond or so.  A wait takes at most
 // WAIT_TRIES of them, about a second.
@@ -301,7 +325,8 @@ __global__ void __launch_bounds__(32 * AttnShape<D, ROWS>::WARPS, 1)
   constexpr int KS = S::KS, VS = S::VS, QB = S::QB, NQ = S::QUARTERS;
   extern __shared__ uint8_t at_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(at_raw) + 1023) & ~uintptr_t(1023));
-  // (sready: of chunk i at i % 6, so that a group meets every phase of its own)
+  // (A wait tells only a phase's parity, so whoever waits for a phase has to have met the one
+  // before: sready of chunk i is at i % 6, a group's own.)
   __shared__ __align__(8) uint64_t kfull[KS], kempty[KS], vfull[VS], vempty[VS], sready[6], vready[2], pready[3], pvdone[3],
       qready[QB], qfree[QB], pc_full[PIECE_RING], pc_empty[PIECE_RING], decided[NQ], met[OUT_RING][NQ], left;
   __shared__ Piece s_piece[PIECE_RING];
@@ -820,29 +845,31 @@ __global__ void __launch_bounds__(32 * AttnShape<D, ROWS>::WARPS, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&decided[k]);
         const float nref = m == -INFINITY ? 0.f : -m;
-        // 2. The weights, over the scores that have been read (8 columns of pairs for 16 of S).
-        tmem_ld16_begin(t_s, s[0]);
-        auto weigh = [&](int w0, float* now, float* next) {
-          uint32_t h[8];
-          tmem_ld_end(now);
-          if (w0 + 16 < AT_CHUNK) tmem_ld16_begin(t_s + w0 + 16, next);
-          const PageScale sc = s_sc[slot][w0 >> p.page_log2];
-          score16(now, sc, nref);
-          float2 part = make_float2(0.f, 0.f);
-#pragma unroll
-          for (int n = 0; n < 16; n += 2) {
-            const float2 e = make_float2(ex2(now[n]), ex2(now[n + 1]));
-            part = __fadd2_rn(part, e);
-            const __half2 hh = __floats2half2_rn(e.x, e.y);
-            h[n / 2] = *reinterpret_cast<const uint32_t*>(&hh);
-          }
-          l = fmaf(part.x + part.y, sc.inv_v, l);
-          tmem_st8(t_s + w0 / 2, h);
-        };
+        // 2. The weights, over the scores that have been read (16 columns of pairs for 32 of S).
+        float z[32];
+        tmem_ld32_begin(t_s, z);
 #pragma unroll 1
         for (int w0 = 0; w0 < AT_CHUNK; w0 += 32) {
-          weigh(w0, s[0], s[1]);
-          weigh(w0 + 16, s[1], s[0]);
+          uint32_t h[2][8];
+          float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          const PageScale sc0 = s_sc[slot][w0 >> p.page_log2], sc1 = s_sc[slot][(w0 + 16) >> p.page_log2];
+          tmem_ld32_end(z);
+          score16(z, sc0, nref);
+          score16(z + 16, sc1, nref);
+#pragma unroll
+          for (int n = 0; n < 16; n += 2)
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              const float2 e = make_float2(ex2(z[16 * q + n]), ex2(z[16 * q + n + 1]));
+              part[q] = __fadd2_rn(part[q], e);
+              const __half2 hh = __floats2half2_rn(e.x, e.y);
+              h[q][n / 2] = *reinterpret_cast<const uint32_t*>(&hh);
+            }
+          if (w0 + 32 < AT_CHUNK) tmem_ld32_begin(t_s + w0 + 32, z);
+          l = fmaf(part[0].x + part[0].y, sc0.inv_v, l);
+          l = fmaf(part[1].x + part[1].y, sc1.inv_v, l);
+          tmem_st8(t_s + w0 / 2, h[0]);
+          tmem_st8(t_s + w0 / 2 + 8, h[1]);
         }
         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
         tc_fence_before();
