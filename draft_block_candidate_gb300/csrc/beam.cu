@@ -193,6 +193,87 @@ __global__ void __launch_bounds__(32 * BM_MAX)
   }
 }
 
+// The records of short rows, where the logit pass, made for long ones, has no floor that keeps a
+// row's elements from being folded into its list one by one.  One CTA per row: the row in shared
+// memory, its maximum, the sum of its exponentials, and for each warp the K best of its quarter,
+// 32 elements sorted and merged at a time where one of them passes the list's last; then the
+// four lists are merged.  Bound by latency.
+constexpr int BS_MAX_V = 1024, BS_WARPS = 4;
+
+template <typename T>
+__global__ void __launch_bounds__(32 * BS_WARPS)
+    beam_short_kernel(const T* __restrict__ logits, int V, int64_t row_stride, int K,
+                      const float* __restrict__ scores, const uint8_t* __restrict__ finished, char* __restrict__ records) {
+  __shared__ float s_x[BS_MAX_V], s_v[BS_WARPS][32], s_top[BS_WARPS], s_sum[BS_WARPS];
+  __shared__ int s_id[BS_WARPS][32];
+  const int64_t row = blockIdx.x;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_wait();
+  pdl_trigger();
+  if (!(scores[row] > -INFINITY) || (finished && finished[row])) return;  // (its record is not read)
+  const T* x = logits + row * row_stride;
+  float top = -INFINITY;
+  for (int i = tid; i < V; i += 32 * BS_WARPS) {
+    const float z = static_cast<float>(x[i]);
+    s_x[i] = z;
+    top = fmaxf(top, z);
+  }
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, o));
+  if (lane == 0) s_top[warp] = top;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < BS_WARPS; ++w) top = fmaxf(top, s_top[w]);
+  // (a row without a finite logit has the sum 0, one with a NaN or +inf a NaN: no candidates)
+  const float m2 = top == -INFINITY ? 0.f : top * 1.4426950408889634f;
+  float sum = 0.f, v = -INFINITY;
+  int id = INT_MAX;
+#pragma unroll 1
+  for (int i0 = warp * 32; i0 < V; i0 += 32 * BS_WARPS) {
+    const int i = i0 + lane;
+    float bv = i < V ? s_x[i] : -INFINITY;
+    sum += ex2(fmaf(bv, 1.4426950408889634f, -m2));
+    // (an equal value further on has a larger id, and is not better)
+    if (!__any_sync(FULL_MASK, bv > __shfl_sync(FULL_MASK, v, K - 1))) continue;
+    int bi = bv == -INFINITY ? INT_MAX : i;
+#pragma unroll
+    for (int k = 2; k <= 32; k <<= 1)
+#pragma unroll
+      for (int j = k >> 1; j >= 1; j >>= 1) {
+        const float ov = __shfl_xor_sync(FULL_MASK, bv, j);
+        const int oi = __shfl_xor_sync(FULL_MASK, bi, j);
+        // descending where the k-block is even (all of it in the last round)
+        const bool first = ((lane & j) == 0) == ((lane & k) == 0);
+        if (first ? better(ov, oi, bv, bi) : better(bv, bi, ov, oi)) {
+          bv = ov;
+          bi = oi;
+        }
+      }
+    bitonic_merge(v, id, bv, bi, lane);
+  }
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(FULL_MASK, sum, o);
+  s_v[warp][lane] = v;
+  s_id[warp][lane] = id;
+  if (lane == 0) s_sum[warp] = sum;
+  __syncthreads();
+  if (warp != 0) return;
+#pragma unroll 1
+  for (int w = 1; w < BS_WARPS; ++w) {
+    bitonic_merge(v, id, s_v[w][lane], s_id[w][lane], lane);
+    sum += s_sum[w];
+  }
+  float* rec = reinterpret_cast<float*>(records + row * (2 * K + 2) * sizeof(float));
+  if (lane == 0) {
+    rec[0] = m2;
+    rec[1] = sum;
+  }
+  if (lane < K) {
+    rec[2 + lane] = v;
+    reinterpret_cast<int32_t*>(rec)[2 + K + lane] = id;
+  }
+}
+
 // ---------------------------------------------------------------------------- reordering
 // dst[b, j] = src[b, parent[b, j]] for every state.  A thread owns one column (a vector of
 // up to 16 bytes at the same place of every beam's row) of a batch entry: it reads the
@@ -312,6 +393,14 @@ SelectPlan select_plan(int64_t batch, int32_t beams, int64_t V, int32_t M, int e
   return pl;
 }
 
+// Whether a row is one that the logit pass has no floor for: the K-th largest of its thread groups'
+// first chunks of 16 bytes, 32 groups of 16 threads or, above K = 16, 64 of 8.  Measured, the whole
+// call, 980 rows in bf16: K = 29, V 95, 500 and 1,024: 10, 17 and 25 us here, 59, 62 and 67 with the
+// logit pass; K = 4, V 95 and 500: 10 and 17 here, 51 and 24 with it; 40 rows, K = 16, V 1,024: 20
+// and 18; 4 rows, K = 8, V 768 and 1,024 (a floor): 14.8 and 17.5 here, 15.3 and 7.4 with it.  From
+// V 1,024 on few rows lose (40 rows, K = 29, V 1,800: 31 and 22).
+bool short_row(int64_t V, int es, int K) { return V <= BS_MAX_V && V * es < 16 * K * (K <= 16 ? 16 : 8); }
+
 // Whether the byte ranges that (batch, beam, segment) strides reach from one base are
 // apart from one another: nested by stride, each stride at least what lies under it.
 bool strides_apart(int64_t batch, int64_t sb, int64_t beams, int64_t sw, int64_t segs, int64_t ss,
@@ -325,6 +414,15 @@ bool strides_apart(int64_t batch, int64_t sb, int64_t beams, int64_t sw, int64_t
     extent += (x.second - 1) * x.first;
   }
   return true;
+}
+
+template <typename T>
+cudaError_t short_launch(const void* logits, int64_t rows, int64_t V, int64_t row_stride, int K, const float* scores,
+                         const uint8_t* finished, void* records, cudaStream_t stream) {
+  beam_short_kernel<T><<<static_cast<unsigned>(rows), 32 * BS_WARPS, 0, stream>>>(
+      static_cast<const T*>(logits), static_cast<int>(V), row_stride, K, scores, finished, static_cast<char*>(records));
+  note_launch();
+  return cudaGetLastError();
 }
 
 cudaError_t reorder_launch(const ReorderParams& prm, int64_t tiles, cudaStream_t stream) {
@@ -373,8 +471,10 @@ lilicorr_status lilicorr_beam_select(const void* logits, lilicorr_dtype ldtype, 
     return fail(LILICORR_ERR_WORKSPACE, "lilicorr_beam_select: workspace missing, too small or misaligned");
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
   const int64_t rows = batch * beams;
-  cudaError_t e = k1_launch_beams(logits, es, rows, V, row_stride, pl.K, pl.P, workspace, scores,
-                                  finished, stream);
+  cudaError_t e =
+      !short_row(V, es, pl.K) ? k1_launch_beams(logits, es, rows, V, row_stride, pl.K, pl.P, workspace, scores, finished, stream)
+      : es == 2 ? short_launch<__nv_bfloat16>(logits, rows, V, row_stride, pl.K, scores, finished, workspace, stream)
+                : short_launch<float>(logits, rows, V, row_stride, pl.K, scores, finished, workspace, stream);
   if (e == cudaSuccess) {
     PdlScope pdl(true);
     e = launch_k(beam_merge_kernel, dim3(static_cast<unsigned>(batch)), dim3(32 * beams * std::max(1, std::min(BM_WARPS / beams, (pl.P + 3) / 4))), 0,

@@ -295,7 +295,7 @@ lilicorr_status lilicorr_sample_walk(const float* pair_scores, const int32_t* ca
  * i * V + v ascending); ranks are decided in double, the score is rounded to f32 once.
  *   logits    [batch, beams, V] F32 or BF16, rows row_stride >= V elements apart, element
  *             aligned; -inf marks a token that may not be taken; a row without a finite
- *             logit has no candidates
+ *             logit, or with a NaN or +inf, has no candidates
  *   scores    [batch, beams] f32 cumulative log-probabilities; a beam at -inf (or NaN) is
  *             dead: it has no candidates and its logits are not read
  *   finished  nullable [batch, beams]: a nonzero beam goes on as itself, with the one

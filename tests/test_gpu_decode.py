@@ -59,7 +59,9 @@ def check_select(got, logits, scores, n_out, finished=None, pad_id=0):
 @pytest.mark.parametrize("batch,beams,V,n_out,dtype", [
     (1, 1, 1, 1, torch.float32), (1, 1, 3, 8, torch.bfloat16), (2, 3, 5, 4, torch.float32),
     (3, 4, 1001, 8, torch.bfloat16), (2, 32, 333, 32, torch.float32), (5, 7, 32003, 31, torch.bfloat16),
-    (1, 4, 151936, 8, torch.bfloat16), (30, 5, 4097, 17, torch.float32), (128, 2, 257, 2, torch.bfloat16)])
+    (1, 4, 151936, 8, torch.bfloat16), (30, 5, 4097, 17, torch.float32), (128, 2, 257, 2, torch.bfloat16),
+    (40, 3, 1024, 31, torch.bfloat16), (9, 32, 1023, 32, torch.float32), (3, 4, 1025, 30, torch.bfloat16), (2, 1, 20, 32, torch.float32),
+    (7, 5, 95, 16, torch.bfloat16), (5, 2, 127, 4, torch.float32), (2, 2, 1, 1, torch.bfloat16), (3, 1, 33, 2, torch.bfloat16)])
 def test_select_matches_reference(lc, batch, beams, V, n_out, dtype):
     g = gen(batch * 7 + V)
     x = (torch.randn(batch, beams, V, generator=g, device="cuda") * 2).to(dtype)
@@ -85,6 +87,27 @@ def test_select_dead_finished_masked_and_nan_rows(lc):
     check_select(lc.beam_select(x, s, 9, finished=done, pad_id=77), x, s, 9, done, 77)
     done[:] = True
     check_select(lc.beam_select(x, s, 8, finished=done, pad_id=-3), x, s, 8, done, -3)
+
+
+@pytest.mark.parametrize("V,dtype", [(90, torch.bfloat16), (1024, torch.bfloat16), (130, torch.float32), (5000, torch.bfloat16)])
+def test_select_short_rows_dead_finished_and_not_finite(lc, V, dtype):
+    """Rows with a NaN or +inf have no candidates, like those of a dead beam."""
+    x = torch.randn(3, 5, V, generator=gen(V), device="cuda").to(dtype)
+    s = torch.randn(3, 5, generator=gen(2), device="cuda") - 3
+    done = torch.zeros(3, 5, dtype=torch.bool, device="cuda")
+    done[0, 1] = done[1, 4] = True
+    x[0, 2, 10:] = -math.inf
+    x[1, 0] = -math.inf
+    x[2, 1:] = -math.inf
+    x[2, 1:, 3:6] = 0.5
+    y, t = x.clone(), s.clone()
+    y[0, 0, V - 1] = math.nan
+    y[1, 3, 7] = math.inf
+    y[1, 2] = math.nan
+    t[0, 0] = t[1, 3] = t[1, 2] = -math.inf
+    check_select(lc.beam_select(x, s, 32, finished=done, pad_id=5), x, s, 32, done, 5)
+    for a, b in zip(lc.beam_select(y, s, 32, finished=done), lc.beam_select(x, t, 32, finished=done)):
+        assert torch.equal(a, b)
 
 
 def test_select_ties_go_to_the_lowest_beam_and_token(lc):
