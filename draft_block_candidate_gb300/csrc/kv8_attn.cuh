@@ -306,14 +306,15 @@ __global__ void __launch_bounds__(32 * W) kv8_join_kernel(const AttnParams p, in
   __shared__ float s_y[W][D], s_m[W], s_l[W];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   // Lengths and row ranges were there before the attention began: they are read, and the
-  // tile is found, while it still runs.
+  // tile is found, while it still runs.  Every CTA waits for it before it may leave: what comes
+  // after this kernel takes its end for the attention's too.
   const JoinTile<D, ROWS> t(p, blockIdx.x, runs);
+  pdl_wait();
   if (t.count == 0) return;
   const int rows = min(ROWS, t.sq.n * p.group - t.tile * ROWS);
   const int ctas = (t.count - 1) * Y, mine = (ROWS + ctas - 1) / ctas;  // rows of a CTA
   const int r0 = (t.j * Y + blockIdx.y) * mine, r1 = min(rows, r0 + mine);
   if (r0 >= r1) return;
-  pdl_wait();
   float mx, sum, y[E];
   auto store = [&](int r) {
     const int row = t.tile * ROWS + r, i = row / p.group;
