@@ -24,15 +24,18 @@
 // common, sums their own: a group decides on a chunk's maxima after the other has on the chunk
 // before.
 //
-// A row's maximum m moves only where a score passes it by more than 2^14: weights are then at
-// most 2^14, inside f16, and only then is O scaled in tensor memory, by the warp that owns its
-// lanes.  The page's key scale multiplies the scores; the logarithm of its value scale is added
-// to them, so that p' = scale_v exp(s - m) is what the second product takes, and the sums take
-// p' / scale_v.
+// A row's maximum m moves only where a score passes it by more than 2^6, and only then is O scaled
+// in tensor memory, by the warp that owns its lanes.  Weights are 2^9 of their size beside m's: at
+// most 2^15, inside f16, and in its normal range down to 2^-23 of the weight of m, so that what many
+// tokens beside a heavy one hold together is not lost: 131,072 of them lose 2^-17 of that weight
+// at most.  (64 sequences of 16 new tokens, a call: 101.4 us; m moving at 2^4 and weights at 2^11,
+// 105.9; 2^8 and 2^7, 100.2; 2^14 and their own size, where the same tokens lose up to 2^-8, 98.1.)
+// The page's key scale multiplies the scores; the logarithm of its value scale is added to them, so
+// that p' = scale_v exp(s - m) is what the second product takes, and the sums take p' / scale_v.
 //
 // Roundings below f32: q (bf16) is moved by a power of two of its row to at most 256 and split
 // into hi + lo, exactly but for values 2^-9 below the row's largest, which are off by at most
-// 2^-17 of it; p' is rounded to f16 (2^-11 of its value, 2^-25 of the weight of m below 2^-14);
+// 2^-17 of it; p' is rounded to f16 (2^-11 of its value, 2^-34 of the weight of m below 2^-23);
 // out is rounded to bf16.
 //
 // Bound: neither memory nor the tensor cores (64 sequences of 16 new tokens over up to 4,096
@@ -256,7 +259,8 @@ __device__ __forceinline__ Role role_of(int warp, int& k) {
 // took a buffer whose products came after them), and leaves its sums for the next tile too, where
 // it has none.
 constexpr int SC_RING = 8, PIECE_RING = 4, FR_RING = 6, OUT_RING = 5;
-constexpr float RAISE = 14.f;               // log2 of how far a score may pass its reference
+constexpr float RAISE = 6.f;                // log2 of how far a score may pass its reference
+constexpr float HELD = 9.f;                 // log2 of the weight of the reference as it is held
 
 // A piece of the CTA's run: the chunks [c0, cn) of a tile that some row of it sees.
 struct Piece {
@@ -743,6 +747,7 @@ __global__ void __launch_bounds__(32 * AttnShape<D, ROWS>::WARPS, 1)
             for (int n = 0; n < 4; ++n) dst[n] = make_float4(o[4 * n], o[4 * n + 1], o[4 * n + 2], o[4 * n + 3]);
           }
         }
+        top -= HELD;  // what the products and sums stand for
         if (has && !y.whole) {
           part[ROWS * D + r] = top;
           part[ROWS * D + ROWS + r] = total;
@@ -844,7 +849,7 @@ __global__ void __launch_bounds__(32 * AttnShape<D, ROWS>::WARPS, 1)
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&decided[k]);
-        const float nref = m == -INFINITY ? 0.f : -m;
+        const float nref = m == -INFINITY ? 0.f : HELD - m;
         // 2. The weights, over the scores that have been read (16 columns of pairs for 32 of S).
         float z[32];
         tmem_ld32_begin(t_s, z);

@@ -393,9 +393,9 @@ lilicorr_status lilicorr_kv8_append(const lilicorr_kv8_cache* cache, const void*
  * What is not finite stays where it is seen: a NaN code in a key or value makes the rows that see
  * it NaN (a value's in its column), and a row of q with an infinity or a NaN is NaN or what its
  * infinite scores give.  max_new * q_heads / kv_heads is below 2^31 - 256.
- * Sums and maxima are f32; the softmax weights are rounded to f16 before the second product
- * (relative to the row's largest weight times value scale), and q loses what lies 2^-17 below
- * its row's largest value.  The bits of a result do not depend on when or where its parts were
+ * Sums and maxima are f32; the softmax weights are rounded to f16 before the second product (by
+ * 2^-11 of their value; times value scale, those below 2^-23 of the row's largest by 2^-34 of it),
+ * and q loses what lies 2^-17 below its row's largest value.  The bits of a result do not depend on when or where its parts were
  * worked out, but on the device's number of SMs and the other sequences of the call.  Workspace:
  * lilicorr_kv8_attention_workspace_bytes (0 for unsupported sizes; by the current device),
  * 256-byte aligned, no initial contents.  Calls that overlap must not share it.
