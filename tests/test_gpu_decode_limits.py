@@ -143,3 +143,24 @@ def test_attention_beside_a_heavy_token(lc, D, new, group, length, batch, where)
         within((out[b * new:(b + 1) * new], lse[b * new:(b + 1) * new]), want)
     off = (out.cpu().double().view(batch, -1) - want[0].view(1, -1)).norm(dim=1) / want[0].norm()
     assert float(off.max()) <= 2.0 ** -8
+
+
+TIGHT = [
+    # D, page, kv heads, group, [(new, length)]
+    (128, 64, 2, 4, [(1, 1000), (1, 77)]), (64, 32, 3, 5, [(1, 31), (1, 700), (1, 1)]), (32, 128, 2, 3, [(1, 129), (4, 90)]),
+    (128, 128, 1, 16, [(1, 333)]), (128, 16, 2, 8, [(2, 5000), (1, 9)]), (64, 64, 8, 1, [(9, 2100)]), (32, 16, 1, 13, [(1, 4000)]),
+    (128, 64, 2, 8, [(16, 300), (16, 16), (5, 64)]), (64, 16, 4, 4, [(16, 2000), (9, 130)]), (32, 16, 2, 24, [(9, 500), (20, 21)]),
+    (128, 32, 8, 7, [(64, 64), (64, 1300)]), (128, 128, 1, 1, [(17, 5000), (1, 1)])]
+
+
+@pytest.mark.parametrize("size,spread", [(1.0, 0), (8.0, 0), (2.0, 9)])
+@pytest.mark.parametrize("D,page,heads,group,seqs", TIGHT)
+def test_attention_is_off_by_its_own_roundings_alone(lc, D, page, heads, group, seqs, size, spread):  # noqa: F811
+    """Flat and peaked softmaxes, values of one size and of many, against what each kernel rounds."""
+    q_start, kv_len, table, n_pages = make_batch(seqs, page, D + len(seqs))
+    cache = make_cache(lc, n_pages, heads, page, D, 21)
+    fill(lc, cache, q_start, kv_len, table, 22, spread)
+    q = (size * torch.randn(int(q_start[-1]), heads * group, D, generator=gen(23), device="cuda")).to(torch.bfloat16)
+    max_new = max(n for n, _ in seqs)
+    exact = exact_attention(q, cache, q_start.cpu(), kv_len.cpu(), table, D ** -0.5, 14 if max_new * group <= 16 else HELD)
+    within(lc.kv8_attention(q, cache, q_start, kv_len, table, max_new, lse=True), exact)
