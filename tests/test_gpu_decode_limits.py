@@ -164,3 +164,80 @@ def test_attention_is_off_by_its_own_roundings_alone(lc, D, page, heads, group, 
     max_new = max(n for n, _ in seqs)
     exact = exact_attention(q, cache, q_start.cpu(), kv_len.cpu(), table, D ** -0.5, 14 if max_new * group <= 16 else HELD)
     within(lc.kv8_attention(q, cache, q_start, kv_len, table, max_new, lse=True), exact)
+
+
+# ---------------------------------------------------------------------------- scales of any size
+
+def any_scales(cache, seed, low, high):
+    """Scales spread over 2^low .. 2^high that are no powers of two."""
+    g = gen(seed)
+    for t in (cache.k_scale, cache.v_scale):
+        t.copy_(torch.exp2(low + (high - low) * torch.rand(t.shape, generator=g, device="cuda")))
+
+
+@pytest.mark.parametrize("k_range,v_range", [((-1, 1), (-1, 1)), ((-3, 0), (-60, -56)), ((-9, -1), (-60, 3)), ((-2, 1), (-70, -64)),
+                                             ((-126, -100), (-12, 20)), ((-2, 0), (60, 100))])
+@pytest.mark.parametrize("D,page,heads,group,seqs", [TIGHT[i] for i in (0, 2, 3, 7, 8, 9)])
+def test_attention_with_scales_of_any_size(lc, D, page, heads, group, seqs, k_range, v_range):  # noqa: F811
+    q_start, kv_len, table, n_pages = make_batch(seqs, page, D + len(seqs))
+    cache = make_cache(lc, n_pages, heads, page, D, 21)
+    fill(lc, cache, q_start, kv_len, table, 22)
+    any_scales(cache, 24, *k_range)
+    k_scale = cache.k_scale.clone()
+    any_scales(cache, 25, *v_range)
+    cache.k_scale.copy_(k_scale)
+    q = torch.randn(int(q_start[-1]), heads * group, D, generator=gen(23), device="cuda").to(torch.bfloat16)
+    max_new = max(n for n, _ in seqs)
+    # codes are of magnitudes up to 448: scores of some units where the keys' scales allow it
+    scale = 2.0 ** -(6 + k_range[1]) / D ** 0.5
+    exact = exact_attention(q, cache, q_start.cpu(), kv_len.cpu(), table, scale, 14 if max_new * group <= 16 else HELD)
+    within(lc.kv8_attention(q, cache, q_start, kv_len, table, max_new, scale=scale, lse=True), exact)
+
+
+@pytest.mark.parametrize("size", [2.0 ** -6, 1.0, 2.0 ** 9])
+@pytest.mark.parametrize("fork", [False, True])
+@pytest.mark.parametrize("page,D", [(16, 32), (32, 128), (128, 64)])
+def test_append_to_pages_with_scales_of_any_size(lc, page, D, fork, size):  # noqa: F811
+    """Tail pages whose scales are no powers of two, kept where they hold the new rows and outgrown where not: scales are exact, and
+    a code, new, kept or moved, stands for its value to half a step (2^-4 of it, or 2^-10 of the scale) and f32's rounding."""
+    heads, before, n = 3, page + 5, page + 4
+    seqs = [(n, before + n), (2, before + 2)]
+    q_start, kv_len, table, n_pages = make_batch(seqs, page, 7, spare=4)
+    cache = make_cache(lc, n_pages, heads, page, D, 8)
+    any_scales(cache, 9, -3, 3)
+    table_cpu = table.cpu()
+    tails = [int(table_cpu[b, 1]) for b in range(2)]
+    source, tail_src = list(tails), None
+    if fork:
+        free = sorted(set(range(n_pages)) - set(table_cpu.flatten().tolist()))
+        source = free[:2]
+        tail_src = torch.tensor(source, dtype=torch.int32, device="cuda")
+    # tail pages without NaN codes
+    for t in (cache.k, cache.v):
+        raw = t.view(torch.uint8)
+        raw[source] = torch.where((raw[source] & 0x7F) == 0x7F, 0x31, raw[source])
+    old = [(c.view(torch.uint8).clone(), s.clone()) for c, s in ((cache.k, cache.k_scale), (cache.v, cache.v_scale))]
+    g = gen(10)
+    x = [(size * 100 * torch.randn(n + 2, heads, D, generator=g, device="cuda")).to(torch.bfloat16) for _ in range(2)]
+    lc.kv8_append(cache, *x, q_start, kv_len, table, n, tail_src=tail_src)
+    value = lambda raw: raw.view(torch.float8_e4m3fn).double()  # noqa: E731
+    for (codes, scales), (raw, was), new in zip(((cache.k, cache.k_scale), (cache.v, cache.v_scale)), old, x):
+        for b, (k, total) in enumerate(seqs):
+            rows = new[int(q_start[b]):int(q_start[b]) + k].cpu().double()
+            for at in range(before // page, -(-total // page)):
+                lo, hi = max(before, at * page), min(total, (at + 1) * page)
+                dst, src = int(table_cpu[b, at]), source[b] if at * page < before else None
+                for h in range(heads):
+                    got, now = value(codes.view(torch.uint8)[dst, h].cpu()), float(scales[dst, h])
+                    part = rows[lo - before:hi - before, h]
+                    need = R.page_scale(float(part.abs().max()))
+                    assert now == (need if src is None else max(need, float(was[src, h])))
+                    want = torch.zeros(0, D, dtype=torch.float64)
+                    if src is not None:
+                        had = raw[src, h, :lo - at * page].cpu()
+                        want = value(had) * float(was[src, h])
+                        if now == float(was[src, h]):
+                            assert torch.equal(codes.view(torch.uint8)[dst, h, :lo - at * page].cpu(), had)
+                    want = torch.cat([want, part])
+                    off = (got[:want.shape[0]] * now - want).abs()
+                    assert bool((off <= torch.maximum(2.0 ** -4 * want.abs(), torch.tensor(2.0 ** -10 * now)) + 2.0 ** -22 * want.abs()).all())
