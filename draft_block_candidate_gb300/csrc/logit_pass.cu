@@ -68,7 +68,12 @@ constexpr int K1_NSTAGES = K1_NST;
 constexpr int K1_CPT = K1_STAGE_BYTES / 16 / K1_CTHREADS;  // 16-byte chunks per consumer per stage
 constexpr int KQ = 32;                                      // queue slots per warp
 constexpr float LOG2E = 1.4426950408889634f;
-constexpr float M2_INIT = -1e30f;                           // "no element yet", finite
+// "No element yet" of a record, finite.
+constexpr float M2_NONE = -1e30f;
+// Where a thread's running maximum starts.  Below it m2 = fl(x LOG2E) has steps of 256 and more, and
+// x LOG2E - m2 can pass what 2^y holds: threads that had met only tokens masked with -1e10 or -1e20
+// left an infinite sum, and the row a NaN.  From here on such tokens count as exp(x) = 0.
+constexpr float M2_INIT = -2147483648.f;
 
 // Natural-log lse of a base-2 pair (M, S), sum = S 2^M: (M + log2 S) / LOG2E, in float
 // with one rounding's worth of care.  S = f 2^e with f in [0.5, 1), so log2 S = e + log2 f
@@ -777,7 +782,7 @@ __global__ void __launch_bounds__(128) k1_merge_kernel(const char* __restrict__ 
   const int64_t r = int64_t(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
   if (r >= rows) return;
   const size_t rb = k1_record_bytes(K);
-  float v = -INFINITY, M = M2_INIT, S = 0.f;
+  float v = -INFINITY, M = M2_NONE, S = 0.f;
   int id = INT_MAX;
   for (int j = 0; j < n; ++j) {
     const char* rec = records + (int64_t(j) * rows + r) * rb;

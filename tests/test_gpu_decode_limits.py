@@ -241,3 +241,85 @@ def test_append_to_pages_with_scales_of_any_size(lc, page, D, fork, size):  # no
                     want = torch.cat([want, part])
                     off = (got[:want.shape[0]] * now - want).abs()
                     assert bool((off <= torch.maximum(2.0 ** -4 * want.abs(), torch.tensor(2.0 ** -10 * now)) + 2.0 ** -22 * want.abs()).all())
+
+
+# ----------------------------------------------------------------- selection at the ends of the types
+
+LSE_TOL = 1e-5  # the logit pass's contract for a log-partition
+
+
+def exact_select(x, s, done):
+    """Per batch entry the scores of all candidates in float64, [beams, V + 1] (-inf: none; a finished beam's own is the last)."""
+    x, s, done = x.cpu().double(), s.cpu().double(), done.cpu()
+    out = torch.full((*x.shape[:2], x.shape[2] + 1), -math.inf, dtype=torch.float64)
+    for i in range(x.shape[0]):
+        for j in range(x.shape[1]):
+            row = x[i, j]
+            if not float(s[i, j]) > -math.inf:
+                continue
+            if done[i, j]:
+                out[i, j, -1] = s[i, j]
+            elif not bool((row.isnan() | (row == math.inf)).any()) and bool((row > -math.inf).any()):
+                # (the largest is taken off first: beside it the logarithm of the sum can be far below a rounding)
+                rest = row - row.max()
+                out[i, j, :-1] = s[i, j] + (rest - torch.log(torch.exp(rest).sum()))
+    return out
+
+
+def check_candidates(got, x, s, n_out, done=None, pad_id=0):
+    """As many candidates as there are, each at a place where its score belongs."""
+    done = torch.zeros(x.shape[:2], dtype=torch.bool) if done is None else done
+    score, token, parent = (t.cpu() for t in got)
+    for i, all_ in enumerate(exact_select(x, s, done)):
+        best = torch.sort(all_.flatten(), descending=True).values
+        seen = set()
+        for k in range(n_out):
+            at, value = (int(parent[i, k]), int(token[i, k])), float(score[i, k])
+            if k >= best.numel() or best[k] == -math.inf:
+                assert (at, value) == ((0, pad_id), -math.inf), (i, k)
+                continue
+            exact = float(all_[at[0], -1 if done[i, at[0]] else at[1]])
+            assert exact > -math.inf and at not in seen and (not done[i, at[0]] or at[1] == pad_id), (i, k, at)
+            seen.add(at)
+            tol = LSE_TOL + 2.0 ** -24 * abs(exact)
+            assert abs(value - exact) <= tol and abs(exact - float(best[k])) <= 2 * tol, (i, k, at)
+
+
+BF16_MIN, F32_MIN = torch.finfo(torch.bfloat16).min, torch.finfo(torch.float32).min
+SIZES = [(2, 90, torch.bfloat16), (2, 1000, torch.float32), (2, 5001, torch.bfloat16), (3, 20000, torch.float32), (40, 3001, torch.bfloat16)]
+
+
+@pytest.mark.parametrize("mask", [-1e4, -1e9, -2.0 ** 31, -1e10, -1e20, -1e30, BF16_MIN, F32_MIN])
+@pytest.mark.parametrize("batch,V,dtype", SIZES)
+def test_select_with_finite_masks(lc, batch, V, dtype, mask):  # noqa: F811
+    """Tokens masked with a finite value of any size, alone, in long runs and all but a few."""
+    if mask == F32_MIN and dtype == torch.bfloat16:
+        mask = BF16_MIN
+    g = gen(V)
+    x = torch.randn(batch, 5, V, generator=g, device="cuda") * 2
+    s = torch.randn(batch, 5, generator=g, device="cuda") - 5
+    x[:, 1, :V // 2] = mask
+    x[:, 2, V // 3:] = mask
+    x[:, 3] = mask
+    x[:, 3, V - 2], x[:, 3, V // 2] = 0.5, -0.25
+    x[:, 4, ::3] = mask
+    x = x.to(dtype)
+    check_candidates(lc.beam_select(x, s, 32), x, s, 32)
+    few = x[:, 3:4].contiguous()
+    check_candidates(lc.beam_select(few, s[:, 3:4].contiguous(), 8), few, s[:, 3:4], 8)
+
+
+@pytest.mark.parametrize("mask", [-1e4, -2.0 ** 31, -1e10, -1e20, -1e30, BF16_MIN])
+@pytest.mark.parametrize("batch,V,dtype", [(1, 151936, torch.bfloat16), (1, 9001, torch.float32), (60, 5001, torch.bfloat16)])
+def test_log_partitions_with_finite_masks(lc, batch, V, dtype, mask):  # noqa: F811
+    x = torch.randn(batch, 4, V, generator=gen(V), device="cuda") * 2
+    x[:, 1, :V // 2] = mask
+    x[:, 2, V // 3:] = mask
+    x[:, 3] = mask
+    x[:, 3, V - 2] = 0.5
+    x = x.to(dtype)
+    ids, values, lse = lc.topk_lse(x, 4)
+    rows = x[:, 1:].double()
+    assert float((lse.double() - torch.logsumexp(rows, -1)).abs().max()) <= LSE_TOL
+    assert torch.equal(values[..., 0].double(), rows.amax(-1))
+    assert torch.equal(rows.gather(-1, ids.long()), values.double())
