@@ -42,6 +42,30 @@ __device__ __forceinline__ uint64_t double_key(double d) {
 
 constexpr int BM_MAX = 32;   // beams, and entries taken
 constexpr int BM_WARPS = 32;  // up to as many warps join lists
+// Rows whose largest logit t is of this magnitude or more (every token masked with the type's lowest
+// value, say): a record's m2 = fl(t log2 e) is off by up to 64 octaves and more there, and its sum
+// of no use.  But then floats are 64 or more apart, so that of the sum of exp(x - t) only the
+// tokens equal to t are left (e^-64 is below a double's half step): they are counted.
+constexpr float BM_FAR = 1073741824.f;
+
+// The logarithm of that number into *rest, by the whole CTA; NaN where a token is NaN.  (Out of line, as
+// all that such rows need, so that the others' code stays short.)
+template <typename T>
+__device__ __noinline__ void count_equal(const T* x, int64_t V, float top, unsigned* count, double* rest) {
+  unsigned n = 0;
+  bool nan = false;
+  for (int64_t t = threadIdx.x; t < V; t += blockDim.x) {
+    const float z = static_cast<float>(x[t]);
+    n += z == top;
+    nan |= isnan(z);
+  }
+  if (threadIdx.x == 0) *count = 0;
+  nan = __syncthreads_or(nan);
+  n = __reduce_add_sync(FULL_MASK, n);
+  if ((threadIdx.x & 31) == 0) atomicAdd(count, n);
+  __syncthreads();
+  if (threadIdx.x == 0) *rest = nan ? NAN : log(static_cast<double>(*count));
+}
 
 // (m, s) takes (om, os): s 2^m + os 2^om.
 __device__ __forceinline__ void join_sum(float& m, float& s, float om, float os) {
@@ -52,7 +76,8 @@ __device__ __forceinline__ void join_sum(float& m, float& s, float om, float os)
 
 __global__ void __launch_bounds__(32 * BM_MAX)
     beam_merge_kernel(const char* __restrict__ records, const float* __restrict__ scores,
-                      const uint8_t* __restrict__ finished, int beams, int P, int K, int M,
+                      const uint8_t* __restrict__ finished, const void* __restrict__ logits,
+                      int64_t V, int64_t row_stride, int es, int beams, int P, int K, int M,
                       int pad_id, float* __restrict__ out_score, int32_t* __restrict__ out_token,
                       int32_t* __restrict__ out_parent) {
   // lists as the warps leave them, [beam * warps of a beam][32]
@@ -62,6 +87,8 @@ __global__ void __launch_bounds__(32 * BM_MAX)
   // candidates, [beam][K]
   __shared__ uint64_t s_key[BM_MAX][BM_MAX];
   __shared__ int s_left[BM_MAX];
+  __shared__ double s_rest[BM_MAX];
+  __shared__ unsigned s_count;
   __shared__ float o_score[BM_MAX];
   __shared__ int o_token[BM_MAX], o_parent[BM_MAX];
   const int64_t b = blockIdx.x;
@@ -125,7 +152,16 @@ __global__ void __launch_bounds__(32 * BM_MAX)
       if (lane == 0) join_sum(s_m[warp], s_s[warp], s_m[warp + d], s_s[warp + d]);
     }
   }
-  __syncthreads();
+  auto is_far = [](float t) { return fabsf(t) >= BM_FAR && fabsf(t) < INFINITY; };
+  if (__syncthreads_or(lane == 0 && part == 0 && w < beams && live && !done && is_far(s_v[warp][0]))) {
+    for (int j = 0; j < beams; ++j) {
+      if (!(scores[b * beams + j] > -INFINITY) || (finished && finished[b * beams + j]) || !is_far(s_v[j * per][0])) continue;
+      const int64_t at = (b * beams + j) * row_stride;
+      if (es == 2) count_equal(static_cast<const __nv_bfloat16*>(logits) + at, V, s_v[j * per][0], &s_count, &s_rest[j]);
+      else count_equal(static_cast<const float*>(logits) + at, V, s_v[j * per][0], &s_count, &s_rest[j]);
+    }
+    __syncthreads();
+  }
   const int i = warp;  // from here a warp for each beam
   int left = 0;
   uint64_t key = 0;
@@ -142,13 +178,20 @@ __global__ void __launch_bounds__(32 * BM_MAX)
       } else {
         const float v = s_v[i * per][lane], m = s_m[i * per], s = s_s[i * per];
         const int id = s_id[i * per][lane];
-        if (s > 0.f) {  // a row with no finite logit has no candidate
-          int e;
-          float f = frexpf(s, &e);
-          if (f < 0.70710678f) { f *= 2.f; --e; }
-          const double norm = (static_cast<double>(m) + static_cast<double>(e) + static_cast<double>(log2f(f))) *
-                              (1.0 / static_cast<double>(1.4426950408889634f));
-          const double c = own + (static_cast<double>(v) - norm);
+        const float top = s_v[i * per][0];
+        const bool far = is_far(top);
+        if (far || s > 0.f) {  // a row with no finite logit has no candidate
+          double norm = top, rest = 0.;  // the log-partition is their sum
+          if (far) {
+            rest = s_rest[i];
+          } else {
+            int e;
+            float f = frexpf(s, &e);
+            if (f < 0.70710678f) { f *= 2.f; --e; }
+            norm = (static_cast<double>(m) + static_cast<double>(e) + static_cast<double>(log2f(f))) *
+                   (1.0 / static_cast<double>(1.4426950408889634f));
+          }
+          const double c = own + (static_cast<double>(v) - norm - rest);
           const bool there = lane < K && c > NONE;
           left = __popc(__ballot_sync(FULL_MASK, there));  // the list is sorted
           key = double_key(c);
@@ -478,7 +521,7 @@ lilicorr_status lilicorr_beam_select(const void* logits, lilicorr_dtype ldtype, 
   if (e == cudaSuccess) {
     PdlScope pdl(true);
     e = launch_k(beam_merge_kernel, dim3(static_cast<unsigned>(batch)), dim3(32 * beams * std::max(1, std::min(BM_WARPS / beams, (pl.P + 3) / 4))), 0,
-                 stream, static_cast<const char*>(workspace), scores, finished, static_cast<int>(beams),
+                 stream, static_cast<const char*>(workspace), scores, finished, logits, V, row_stride, es, static_cast<int>(beams),
                  pl.P, pl.K, static_cast<int>(M), static_cast<int>(pad_id), out_score, out_token,
                  out_parent);
     if (e == cudaSuccess) note_launch();

@@ -323,3 +323,32 @@ def test_log_partitions_with_finite_masks(lc, batch, V, dtype, mask):  # noqa: F
     assert float((lse.double() - torch.logsumexp(rows, -1)).abs().max()) <= LSE_TOL
     assert torch.equal(values[..., 0].double(), rows.amax(-1))
     assert torch.equal(rows.gather(-1, ids.long()), values.double())
+
+
+@pytest.mark.parametrize("value", [-2.0 ** 30, -1.5e9, -2.0 ** 31, -1e10, -1e20, -1e30, BF16_MIN, F32_MIN, 2.0 ** 30, 1e10, 3e38])
+@pytest.mark.parametrize("batch,V,dtype", SIZES)
+def test_select_rows_whose_largest_logit_is_of_any_size(lc, batch, V, dtype, value):  # noqa: F811
+    """All of a row masked with a finite value; a few tokens next to it or as far below as the type goes; rows of which
+    some token is NaN or infinite; and what a dead or finished beam has of them."""
+    if value == F32_MIN and dtype == torch.bfloat16:
+        value = BF16_MIN
+    g = gen(V + 1)
+    x = torch.randn(batch, 8, V, generator=g, device="cuda") * 2
+    s = torch.randn(batch, 8, generator=g, device="cuda") - 5
+    done = torch.zeros(batch, 8, dtype=torch.bool, device="cuda")
+    x[:, 1] = value
+    x[:, 2] = value * (1 + 2.0 ** -6 * torch.randint(0, 3, (batch, V), generator=g, device="cuda")).clamp_max(1 if abs(value) > 1e38 else 2)
+    x[:, 3] = min(value, F32_MIN * 0.99)
+    x[:, 3, 5:V:7] = value
+    x[:, 4:] = value
+    x[0, 4, V // 2] = math.nan
+    x[-1, 4, V - 1] = math.inf
+    x[:, 5, 3:] = -math.inf
+    s[:, 6] = -math.inf
+    done[:, 7] = True
+    x = x.to(dtype)
+    check_candidates(lc.beam_select(x, s, 32, finished=done, pad_id=9), x, s, 32, done, 9)
+    s[:, 0] = -math.inf
+    check_candidates(lc.beam_select(x, s, 20, finished=done, pad_id=9), x, s, 20, done, 9)
+    alone = x[:, 1:2].contiguous()
+    check_candidates(lc.beam_select(alone, s[:, 1:2].contiguous(), 5), alone, s[:, 1:2], 5)
