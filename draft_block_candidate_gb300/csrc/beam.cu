@@ -23,7 +23,9 @@ static __device__ uint32_t g_err_beam;
 // rounding.  The score is rounded to float once, as it is stored.  Double arithmetic is slow
 // on this part, so the log-partition is put together from floats, log2 S = e + log2 f with f
 // near 1, and only the sums m2 + e + log2 f, the division by the float nearest log2 e that the
-// logit pass scales its logits by, and the scores themselves are doubles.
+// logit pass scales its logits by, and the scores themselves are doubles.  The sums S are floats,
+// in an order that the rows' alignment sets: beams whose candidates differ by less than what that
+// leaves out may change places, and only rows that begin alike have S alike.
 //
 // One CTA per batch entry; bound by latency, the logit pass by HBM (with K = 32 by the
 // instructions of its top-K: 128 entries of 16 beams, V 151,936 in bf16, take 128 us, 117 of them

@@ -292,7 +292,11 @@ lilicorr_status lilicorr_sample_walk(const float* pair_scores, const int32_t* ca
  * of a batch entry,
  *   s(i, v) = scores[i] + x[i,v] - log sum_u exp(x[i,u]),
  * out_score / out_token / out_parent [batch, M] are the M best (s, v, i) by (s descending,
- * i * V + v ascending); ranks are decided in double, the score is rounded to f32 once.
+ * i * V + v ascending); the score is rounded to f32 once.  The log-partition is an f32 sum, within
+ * 1e-5, and ranks are decided in double on top of it: within a beam the order is that of its logits
+ * (then v ascending); candidates of different beams that differ by less than the log-partitions'
+ * errors may stand in either order.  Beams of equal logits and scores have equal s, and so rank by i,
+ * where their rows begin at the same place of a 16-byte line.
  *   logits    [batch, beams, V] F32 or BF16, rows row_stride >= V elements apart, element
  *             aligned; -inf marks a token that may not be taken; a row without a finite
  *             logit, or with a NaN or +inf, has no candidates

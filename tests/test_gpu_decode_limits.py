@@ -352,3 +352,28 @@ def test_select_rows_whose_largest_logit_is_of_any_size(lc, batch, V, dtype, val
     check_candidates(lc.beam_select(x, s, 20, finished=done, pad_id=9), x, s, 20, done, 9)
     alone = x[:, 1:2].contiguous()
     check_candidates(lc.beam_select(alone, s[:, 1:2].contiguous(), 5), alone, s[:, 1:2], 5)
+
+
+@pytest.mark.parametrize("V,dtype,same", [(32000, torch.bfloat16, True), (151936, torch.bfloat16, True), (5004, torch.float32, True),
+                                          (904, torch.bfloat16, True), (780, torch.float32, True), (32003, torch.bfloat16, False),
+                                          (9999, torch.float32, False), (151935, torch.bfloat16, False)])
+def test_select_among_beams_that_are_alike(lc, V, dtype, same):  # noqa: F811
+    """Beams of equal logits and scores.  Rows that begin at the same place of a 16-byte line have equal log-partitions, so
+    their candidates stand by (logit, beam, token); elsewhere those of one beam do, and beams come in
+    either order where their scores are within the log-partition's tolerance of one another."""
+    beams, n_out = 4, 30
+    row = (torch.randn(3, 1, V, generator=gen(V), device="cuda") * 3).to(dtype)
+    x = row.expand(3, beams, V).contiguous()
+    s = torch.full((3, beams), -7.25, device="cuda")
+    got = lc.beam_select(x, s, n_out)
+    check_candidates(got, x, s, n_out)
+    score, token, parent = (t.cpu() for t in got)
+    for i in range(3):
+        value = row[i, 0].cpu().float()
+        best = sorted(range(V), key=lambda t: (-float(value[t]), t))[:n_out]
+        if same:
+            want = sorted(((-float(value[t]), j, t) for t in best for j in range(beams)))[:n_out]
+            assert list(zip(parent[i].tolist(), token[i].tolist())) == [(j, t) for _, j, t in want]
+        for j in range(beams):
+            mine = token[i][parent[i] == j].tolist()
+            assert mine == best[:len(mine)]
