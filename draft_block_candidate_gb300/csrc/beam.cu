@@ -570,6 +570,10 @@ lilicorr_status lilicorr_beam_reorder(const lilicorr_beam_state* states, int32_t
       if (a0 < b1 && b0 < a1)
         return fail(LILICORR_ERR_INVALID_ARG, "lilicorr_beam_reorder: source and destination overlap without being the same");
     }
+    // (states run side by side: one that is written must be no other's)
+    for (int j = 0; j < n_states; ++j)
+      if (j != i && (s.dst == states[j].dst || s.dst == states[j].src))
+        return fail(LILICORR_ERR_INVALID_ARG, "lilicorr_beam_reorder: a destination is another state's source or destination");
   }
   ReorderParams prm{};
   int64_t tiles = 0;

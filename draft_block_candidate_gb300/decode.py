@@ -177,8 +177,9 @@ def beam_reorder(states: Sequence[torch.Tensor], parent: torch.Tensor,
     states: tensors [batch, beams, ...] of any type; behind the beams their layout must
     come down to equal contiguous pieces a uniform stride apart (a slice cache[..., :t, :]
     of a contiguous cache does).  out: tensors of the same shapes and types to write
-    instead; without it the states are gathered in place.  parent [batch, beams] int32.
-    Returns the list of written tensors."""
+    instead; without it the states are gathered in place.  States run side by side: no two may
+    share memory that is written (one tensor twice, or out=[b, a] for [a, b], is refused).
+    parent [batch, beams] int32.  Returns the list of written tensors."""
     into = list(states if out is None else out)
     if not into or len(into) != len(states):
         raise ValueError("there must be states, and out must hold one tensor for each")

@@ -330,7 +330,8 @@ typedef struct {
 /* dst[b, j] = src[b, parent[b, j]] for every state, in as few launches as there are groups of
  * 16 states.  src == dst (with equal strides) gathers in place, with no second buffer; src
  * and dst that overlap in any other way are refused, and so are destination rows that overlap
- * one another.  Different states must not share bytes that are written.  parent [batch, beams]
+ * one another, and a state whose dst is another one's dst or src.  Different states, and parent, must
+ * not share bytes that are written (they run side by side).  parent [batch, beams]
  * is device memory; a parent outside 0..beams-1 leaves its row of dst as it was and sets bit 24
  * of the device error word.  `states` is host memory, read before the call returns.
  * 1 <= beams <= 32.  Errors: LILICORR_ERR_INVALID_ARG, LILICORR_ERR_CUDA. */
