@@ -217,13 +217,11 @@ const char* batch_error(const int32_t* q_start, const int32_t* kv_len, int64_t b
   if (max_new < 1 || max_new > (1 << 24)) return "1 <= max_new <= 2^24";
   return nullptr;
 }
-const char* rows_error(const void* x, int64_t tok, int64_t head, int64_t heads, int D) {
+const char* rows_error(const void* x, int64_t tok, int64_t head) {
   if (!x) return "null pointer";
   if (reinterpret_cast<uintptr_t>(x) % 16) return "rows are 16-byte aligned";
   if (tok % 8 || head % 8) return "row strides are multiples of 8 elements";
   if (tok < 0 || head < 0 || tok > (int64_t(1) << 40) || head > (int64_t(1) << 40)) return "a row stride is out of range";
-  (void)heads;
-  (void)D;
   return nullptr;
 }
 Kv8 view(const lilicorr_kv8_cache* c) {
@@ -246,8 +244,8 @@ lilicorr_status lilicorr_kv8_append(const lilicorr_kv8_cache* cache, const void*
                                     int32_t max_new, const int32_t* tail_src, void* stream) {
   const char* why = cache_error(cache);
   if (!why) why = batch_error(q_start, kv_len, batch, block_table, table_stride, cols, total, max_new, cache->page);
-  if (!why) why = rows_error(k, k_token_stride, k_head_stride, cache->kv_heads, cache->head_dim);
-  if (!why) why = rows_error(v, v_token_stride, v_head_stride, cache->kv_heads, cache->head_dim);
+  if (!why) why = rows_error(k, k_token_stride, k_head_stride);
+  if (!why) why = rows_error(v, v_token_stride, v_head_stride);
   if (why) return fail(LILICORR_ERR_INVALID_ARG, why);
   AppendParams prm{};
   prm.c = view(cache);
@@ -300,7 +298,7 @@ lilicorr_status lilicorr_kv8_attention(const lilicorr_kv8_cache* cache, const vo
                                        void* stream) {
   const char* why = cache_error(cache);
   if (!why) why = batch_error(q_start, kv_len, batch, block_table, table_stride, cols, total, max_new, cache->page);
-  if (!why) why = rows_error(q, q_token_stride, q_head_stride, q_heads, cache->head_dim);
+  if (!why) why = rows_error(q, q_token_stride, q_head_stride);
   if (!why && (!out || reinterpret_cast<uintptr_t>(out) % 16)) why = "out is null or not 16-byte aligned";
   if (!why && (q_heads < 1 || q_heads % cache->kv_heads || q_heads / cache->kv_heads > 1024))
     why = "q_heads is a multiple of kv_heads, at most 1024 times it";
