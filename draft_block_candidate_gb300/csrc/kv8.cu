@@ -224,6 +224,11 @@ const char* rows_error(const void* x, int64_t tok, int64_t head) {
   if (tok < 0 || head < 0 || tok > (int64_t(1) << 40) || head > (int64_t(1) << 40)) return "a row stride is out of range";
   return nullptr;
 }
+// Whether [a, a + n) and [b, b + m) share a byte.
+bool overlap(const void* a, unsigned __int128 n, const void* b, unsigned __int128 m) {
+  const unsigned __int128 x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + m && y < x + n;
+}
 Kv8 view(const lilicorr_kv8_cache* c) {
   return Kv8{static_cast<uint8_t*>(c->k_pages), static_cast<uint8_t*>(c->v_pages), c->k_scale,
              c->v_scale, c->n_pages, c->kv_heads, c->page};
@@ -315,6 +320,14 @@ lilicorr_status lilicorr_kv8_attention(const lilicorr_kv8_cache* cache, const vo
   if (!workspace || workspace_bytes < kv8_attention_workspace(max_new, group, D) ||
       reinterpret_cast<uintptr_t>(workspace) % 256)
     return fail(LILICORR_ERR_WORKSPACE, "lilicorr_kv8_attention: workspace missing, too small or misaligned");
+  if (total > 0) {
+    // CTAs read q while others write what they are done with
+    using wide = unsigned __int128;
+    const wide rows = wide(total) * q_heads, o_bytes = rows * D * 2, l_bytes = lse ? rows * 4 : 0;
+    const wide q_bytes = (wide(total - 1) * q_token_stride + wide(q_heads - 1) * q_head_stride + D) * 2;
+    if (overlap(q, q_bytes, out, o_bytes) || (lse && (overlap(q, q_bytes, lse, l_bytes) || overlap(out, o_bytes, lse, l_bytes))))
+      return fail(LILICORR_ERR_INVALID_ARG, "lilicorr_kv8_attention: q, out and lse overlap");
+  }
   Kv8Attention a{};
   a.c = view(cache);
   a.q = static_cast<const __nv_bfloat16*>(q);

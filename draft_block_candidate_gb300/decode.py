@@ -341,7 +341,7 @@ def kv8_attention(q: torch.Tensor, cache: KV8Cache, q_start: torch.Tensor, kv_le
     scale: 1 / sqrt(head_dim) by default.  out [total, q_heads, head_dim] bf16 (rows outside
     the sequences keep what they hold; a new one holds zeros there).  lse: True, or a tensor
     [total, q_heads] f32 to write the natural-log sums of exponentials to (True: -inf outside
-    the sequences).  Returns out, or (out, lse)."""
+    the sequences).  q, out and lse must not overlap.  Returns out, or (out, lse)."""
     dev = cache.device.index
     qt, qh = _rows(q, "q", None, cache.head_dim, None, dev)
     total, q_heads, D = q.shape

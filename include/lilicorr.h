@@ -394,7 +394,7 @@ lilicorr_status lilicorr_kv8_append(const lilicorr_kv8_cache* cache, const void*
  *   q    [total, q_heads, head_dim] bf16, element strides by token and head, multiples of 8,
  *        16-byte aligned
  *   out  [total, q_heads, head_dim] bf16, contiguous, 16-byte aligned; rows outside the
- *        sequences are left as they were
+ *        sequences are left as they were.  q, out and lse must not overlap
  * What is not finite stays where it is seen: a NaN code in a key or value makes the rows that see
  * it NaN (a value's in its column), and a row of q with an infinity or a NaN is NaN or what its
  * infinite scores give.  max_new * q_heads / kv_heads is below 2^31 - 256.
