@@ -55,6 +55,12 @@ def _want(t, name: str, dtype, shape, dev: Optional[int], contiguous: bool = Tru
         raise ValueError(f"{name} must be contiguous")
 
 
+def _fits32(n: int, name: str) -> None:
+    """Refuses what ctypes would cut down to its low 32 bits."""
+    if not -(1 << 31) <= n < (1 << 31):
+        raise ValueError(f"{name} must fit 32 bits, got {n}")
+
+
 def _new_workspace(need: int, dev, what: str) -> torch.Tensor:
     if need == 0:
         raise LilicorrError(1, what)
@@ -71,6 +77,7 @@ def _beam_rows(logits: torch.Tensor):
     batch, beams, V = logits.shape
     if batch < 1 or beams < 1 or V < 1:
         raise ValueError("logits must not be empty")
+    _fits32(beams, "beams")
     sb, sw, sv = logits.stride()
     row = sw if beams > 1 else sb if batch > 1 else V
     if (V > 1 and sv != 1) or row < V or (batch > 1 and sb != beams * row):
@@ -81,6 +88,7 @@ def _beam_rows(logits: torch.Tensor):
 def beam_select_workspace(logits: torch.Tensor, n_out: int) -> torch.Tensor:
     """A workspace for beam_select of logits of this shape."""
     batch, beams, V, _, ld = _beam_rows(logits)
+    _fits32(n_out, "n_out")
     with torch.cuda.device(logits.device):
         n = int(L.lib().lilicorr_beam_select_workspace_bytes(batch, beams, V, n_out, ld))
         return _new_workspace(n, logits.device, "lilicorr_beam_select_workspace_bytes")
@@ -110,8 +118,7 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, n_out: int,
         _want(out[2], "parent", torch.int32, (batch, n_out), dev)
     if not 1 <= n_out <= 32 or beams > 32:
         raise ValueError("1 <= n_out <= 32 and at most 32 beams")
-    if not -(1 << 31) <= pad_id < (1 << 31):
-        raise ValueError("pad_id must fit 32 bits")
+    _fits32(pad_id, "pad_id")
     raw, ctx = _run_on(dev, stream)
 
     def call():
@@ -187,6 +194,7 @@ def beam_reorder(states: Sequence[torch.Tensor], parent: torch.Tensor,
         raise ValueError("parent must be a tensor [batch, beams]")
     batch, beams = rows = parent.shape
     dev = parent.get_device()
+    _fits32(beams, "beams")
     _want(parent, "parent", torch.int32, rows, dev)
     if dev < 0:
         raise ValueError("parent must be on a GPU")
@@ -285,6 +293,7 @@ def _sequences(q_start, kv_len, block_table, dev: int) -> tuple:
     cols = block_table.shape[1]
     if step != 1 and cols > 1:
         raise ValueError("block_table's rows must be contiguous")
+    _fits32(cols, "block_table's columns")
     return batch, (rows if batch > 1 else cols), cols
 
 
@@ -303,6 +312,7 @@ def kv8_append(cache: KV8Cache, k: torch.Tensor, v: torch.Tensor, q_start: torch
     total = k.shape[0]
     vt, vh = _rows(v, "v", cache.kv_heads, cache.head_dim, total, dev)
     batch, rows, cols = _sequences(q_start, kv_len, block_table, dev)
+    _fits32(max_new, "max_new")
     if tail_src is not None:
         _want(tail_src, "tail_src", torch.int32, (batch,), dev)
     if batch == 0 or total == 0:
@@ -324,6 +334,7 @@ def kv8_attention_workspace(q: torch.Tensor, cache: KV8Cache, block_table: torch
                             max_new: int) -> torch.Tensor:
     """A workspace for kv8_attention of q's heads, these sequences and at most max_new new
     tokens of each."""
+    _fits32(max_new, "max_new")
     with torch.cuda.device(cache.device):
         n = int(L.lib().lilicorr_kv8_attention_workspace_bytes(
             max_new, q.shape[1], cache.kv_heads, cache.head_dim))
@@ -346,6 +357,7 @@ def kv8_attention(q: torch.Tensor, cache: KV8Cache, q_start: torch.Tensor, kv_le
     qt, qh = _rows(q, "q", None, cache.head_dim, None, dev)
     total, q_heads, D = q.shape
     batch, rows, cols = _sequences(q_start, kv_len, block_table, dev)
+    _fits32(max_new, "max_new")
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     if out is not None:

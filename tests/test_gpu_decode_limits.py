@@ -377,3 +377,23 @@ def test_select_among_beams_that_are_alike(lc, V, dtype, same):  # noqa: F811
         for j in range(beams):
             mine = token[i][parent[i] == j].tolist()
             assert mine == best[:len(mine)]
+
+
+# ------------------------------------------------------------------- numbers that do not fit
+
+@pytest.mark.parametrize("wrap", [1 << 32, -(1 << 32), 1 << 40])
+def test_numbers_over_32_bits_are_refused(lc, wrap):  # noqa: F811
+    """Not cut down to their low bits, with which the call would leave out sequences."""
+    q_start, kv_len, table, n_pages = make_batch([(4, 20), (1, 3)], 16, 1)
+    cache = make_cache(lc, n_pages, 1, 16, 32, 2)
+    x = torch.randn(5, 1, 32, device="cuda").to(torch.bfloat16)
+    before = [t.clone() for t in (cache.k.view(torch.uint8), cache.v.view(torch.uint8), cache.k_scale)]
+    for call in (lambda n: lc.kv8_append(cache, x, x, q_start, kv_len, table, n), lambda n: lc.kv8_attention(x, cache, q_start, kv_len, table, n),
+                 lambda n: lc.kv8_attention_workspace(x, cache, table, n),
+                 lambda n: lc.beam_select_workspace(torch.zeros(1, 2, 50, device="cuda"), n),
+                 lambda n: lc.beam_select(torch.zeros(1, 2, 50, device="cuda"), torch.zeros(1, 2, device="cuda"), n),
+                 lambda n: lc.beam_select(torch.zeros(1, 2, 50, device="cuda"), torch.zeros(1, 2, device="cuda"), 2, pad_id=n)):
+        with pytest.raises(ValueError):
+            call(4 + wrap)
+    for a, b in zip(before, (cache.k.view(torch.uint8), cache.v.view(torch.uint8), cache.k_scale)):
+        assert torch.equal(a, b)
