@@ -281,19 +281,7 @@ __global__ void __launch_bounds__(32 * BS_WARPS)
     // (an equal value further on has a larger id, and is not better)
     if (!__any_sync(FULL_MASK, bv > __shfl_sync(FULL_MASK, v, K - 1))) continue;
     int bi = bv == -INFINITY ? INT_MAX : i;
-#pragma unroll
-    for (int k = 2; k <= 32; k <<= 1)
-#pragma unroll
-      for (int j = k >> 1; j >= 1; j >>= 1) {
-        const float ov = __shfl_xor_sync(FULL_MASK, bv, j);
-        const int oi = __shfl_xor_sync(FULL_MASK, bi, j);
-        // descending where the k-block is even (all of it in the last round)
-        const bool first = ((lane & j) == 0) == ((lane & k) == 0);
-        if (first ? better(ov, oi, bv, bi) : better(bv, bi, ov, oi)) {
-          bv = ov;
-          bi = oi;
-        }
-      }
+    warp_sort_pairs(bv, bi, lane);
     bitonic_merge(v, id, bv, bi, lane);
   }
 #pragma unroll

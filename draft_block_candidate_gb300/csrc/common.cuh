@@ -134,6 +134,25 @@ __device__ __forceinline__ bool better(float va, int ia, float vb, int ib) {
   return va > vb || (va == vb && ia < ib);
 }
 
+// Sort one (value, id) pair per lane across the warp into (value desc, id asc) order
+// (bitonic network, 15 compare-exchange steps).
+__device__ __forceinline__ void warp_sort_pairs(float& v, int& id, int lane) {
+#pragma unroll
+  for (int k = 2; k <= 32; k <<= 1) {
+#pragma unroll
+    for (int j = k >> 1; j > 0; j >>= 1) {
+      const float ov = __shfl_xor_sync(FULL_MASK, v, j);
+      const int oi = __shfl_xor_sync(FULL_MASK, id, j);
+      const bool ob = better(ov, oi, v, id);
+      const bool keep_better = ((lane & j) == 0) == ((lane & k) == 0);
+      if (keep_better ? ob : !ob) {
+        v = ov;
+        id = oi;
+      }
+    }
+  }
+}
+
 // Merge sorted list (bv, bi) (one entry per lane, descending) into (v, id): afterwards
 // (v, id) holds the best 32 of the union, sorted.
 __device__ __forceinline__ void bitonic_merge(float& v, int& id, float bv, int bi, int lane) {

@@ -181,25 +181,6 @@ __device__ __forceinline__ float warp_sort_desc(float v, int lane) {
   return v;
 }
 
-// Sort one (value, id) pair per lane across the warp into (value desc, id asc) order
-// (bitonic network, 15 compare-exchange steps).
-__device__ __forceinline__ void warp_sort_pairs(float& v, int& id, int lane) {
-#pragma unroll
-  for (int k = 2; k <= 32; k <<= 1) {
-#pragma unroll
-    for (int j = k >> 1; j > 0; j >>= 1) {
-      const float ov = __shfl_xor_sync(FULL_MASK, v, j);
-      const int oi = __shfl_xor_sync(FULL_MASK, id, j);
-      const bool ob = better(ov, oi, v, id);
-      const bool keep_better = ((lane & j) == 0) == ((lane & k) == 0);
-      if (keep_better ? ob : !ob) {
-        v = ov;
-        id = oi;
-      }
-    }
-  }
-}
-
 // Warp-uniform: fold one candidate per lane (sentinel -inf / INT_MAX for none) into the
 // sorted 32-entry queue q: sort the 32 candidates, bitonic-merge, keep the best 32.
 // Skipped when no lane beats the queue's K-th entry.
