@@ -397,3 +397,62 @@ def test_numbers_over_32_bits_are_refused(lc, wrap):  # noqa: F811
             call(4 + wrap)
     for a, b in zip(before, (cache.k.view(torch.uint8), cache.v.view(torch.uint8), cache.k_scale)):
         assert torch.equal(a, b)
+
+
+def test_select_writes_its_scores_over_those_it_was_given(lc):  # noqa: F811
+    """A loop that keeps one tensor of scores: each entry's are read before its own are written."""
+    x = torch.randn(200, 6, 5000, generator=gen(1), device="cuda")
+    s = torch.randn(200, 6, generator=gen(2), device="cuda") - 3
+    want = lc.beam_select(x, s, 6)
+    got = lc.beam_select(x, s, 6, out=(s, torch.empty_like(want[1]), torch.empty_like(want[2])))
+    assert got[0] is s and all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+# ------------------------------------------------------------------- a captured step, replayed
+
+@pytest.mark.parametrize("new,group", [(1, 4), (5, 4)])
+def test_a_captured_step_follows_what_its_tensors_hold(lc, new, group):  # noqa: F811
+    """Append, attention, selection and reordering as one graph: replays take the lengths, tables, rows and scores that
+    are there then, and leave what the calls made one by one leave."""
+    batch, beams, heads, D, page, V, steps = 2, 3, 2, 64, 16, 900, 9
+    rows = batch * beams
+    total = 70 + new * steps
+    _, _, table, n_pages = make_batch([(0, total)] * rows, page, 5)
+    w = torch.randn(heads * group * D, V, generator=gen(6), device="cuda") * 0.3
+    feed = torch.randn(steps, rows * new, heads * (group + 2), D, generator=gen(7), device="cuda").to(torch.bfloat16)
+
+    def state():
+        cache = make_cache(lc, n_pages, heads, page, D, 8, garbage=False)
+        length = torch.tensor([70 - 11 * i for i in range(rows)], dtype=torch.int32, device="cuda")
+        fill(lc, cache, None, length, table, 9)
+        return dict(cache=cache, length=length, starts=new * torch.arange(rows + 1, dtype=torch.int32, device="cuda"), x=feed[0].clone(),
+                    scores=torch.zeros(batch, beams, device="cuda"), history=torch.arange(batch * beams * 7, device="cuda").view(batch, beams, 7))
+
+    def step(s):
+        s["length"].add_(new)
+        q, k, v = s["x"].split([heads * group, heads, heads], dim=1)
+        lc.kv8_append(s["cache"], k, v, s["starts"], s["length"], table, new)
+        out, lse = lc.kv8_attention(q, s["cache"], s["starts"], s["length"], table, new, lse=True)
+        last = out.view(rows, new, heads * group * D)[:, -1].float()
+        score, token, parent = lc.beam_select((last @ w).view(batch, beams, V), s["scores"], beams)
+        s["scores"].copy_(score)
+        lc.beam_reorder([s["history"]], parent)
+        return out, lse, score, token, parent
+
+    one, many = state(), state()
+    want = []
+    for i in range(steps):
+        one["x"].copy_(feed[i])
+        want.append([t.clone() for t in step(one)] + [one["history"].clone()])
+    graph = torch.cuda.CUDAGraph()
+    held = [t.clone() for t in (many["length"], many["scores"], many["history"])]
+    with torch.cuda.graph(graph):
+        got = step(many)
+    for t, h in zip((many["length"], many["scores"], many["history"]), held):
+        assert torch.equal(t, h)  # (a capture runs nothing)
+    for i in range(steps):
+        many["x"].copy_(feed[i])
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip((*got, many["history"]), want[i])), i
+    for a, b in zip((one["cache"].k, one["cache"].v, one["cache"].k_scale), (many["cache"].k, many["cache"].v, many["cache"].k_scale)):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
