@@ -28,13 +28,14 @@ static __device__ uint32_t g_err_beam;
 // leaves out may change places, and only rows that begin alike have S alike.
 //
 // One CTA per batch entry; bound by latency, the logit pass by HBM (with K = 32 by the
-// instructions of its top-K: 128 entries of 16 beams, V 151,936 in bf16, take 128 us, 117 of them
-// that pass at 4.65 TB/s; one entry of 4 beams, K = 8, takes 9.9 in all).  A few warps for each beam join its segments'
-// sorted lists (the records of four segments are read at a time); then a thread for each
+// instructions of its top-K: 128 entries of 16 beams, V 151,936 in bf16, take 130 us, 117 of them
+// that pass at 4.65 TB/s; one entry of 4 beams, K = 8, takes 9.9 in all).  A few warps for each beam
+// join its segments' sorted lists (the records of four segments are read at a time); then a thread for each
 // candidate finds its rank, the number of better ones, by binary searches in the beams' lists,
 // so that no step waits for the one before as in a merge that takes one candidate at a time
 // (one entry of 4 beams, V 151,936: 11.4 us for the call with the lists joined one by one and the
-// lists searched in turn, 9.9 with them joined two by two and four searched at a time).
+// lists searched in turn, 9.7 with them joined two by two and four searched at a time; the look for
+// rows of very large logits adds 0.2).
 
 // Order-preserving key: unsigned comparison of keys = comparison of the doubles.
 __device__ __forceinline__ uint64_t double_key(double d) {

@@ -18,8 +18,8 @@ static __device__ uint32_t g_err_kv8;
 // appending them at once does.  Bound by HBM for prompts (2 bytes in and 1 out per value),
 // by latency for single tokens.  The rows are kept in registers between the maximum and the
 // conversion, so that they are read once, and are loaded before the table's entry is known.
-// Prompts of up to 4,096 tokens, 16 sequences, 8 heads of 128: 34 us, 5.6 TB/s, 84 % of the copy
-// rate (51 us with divisions for the rows' places, f32 maxima and a test of the scale at each
+// Prompts of up to 4,096 tokens, 16 sequences, 8 heads of 128: 34 us, 5.6 TB/s, 82 to 84 % of the
+// copy rate (51 us with divisions for the rows' places, f32 maxima and a test of the scale at each
 // value).  64 sequences' single tokens: 4.1 us, of which a
 // launch and two dependent reads are all but a little.
 constexpr int AP_THREADS = 128;

@@ -39,10 +39,10 @@
 // out is rounded to bf16.
 //
 // Bound: neither memory nor the tensor cores (64 sequences of 16 new tokens over up to 4,096
-// cached ones, 64 query and 8 key / value heads of 128: 94.5 us, 88 of them this kernel's; the
+// cached ones, 64 query and 8 key / value heads of 128: 99.9 us, 94 of them this kernel's; the
 // cache's bytes take 50.6 us at 6.7 TB/s, the products 40.5) but the instructions of the softmax
 // and the widening, some 5,300 of a warp to a chunk, which four schedulers issue at half their
-// rate, the first tile's q (12,000 cycles before the first product), and what a tile's change
+// rate (2.2 of 4), the first tile's q (12,000 cycles before the first product), and what a tile's change
 // leaves idle.  The 19 warps run seven loops at once and share an instruction cache, where a miss
 // takes some 300 cycles: the loops are kept small, and what runs once a tile or less is rolled or
 // out of line.  That, the split of q by warps of its own, K and V in rings of their own, one O for
@@ -545,7 +545,7 @@ __global__ void __launch_bounds__(32 * AttnShape<D, ROWS>::WARPS, 1)
       }
     }
   } else if (role == CONV) {
-    // ================= widening of V, and the split of q =================
+    // ================= widening of V =================
     int it = 0, qi = 0;  // qi: pieces with chunks
     Piece x;
     for (int pi = 0; next_piece(pi, x); ++pi) {
@@ -919,9 +919,10 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// Rows of a tile.  Up to 16 go to the kernel of kv8_attn_few.cu (8 where that is all).  Measured,
-// 128 sequences of up to 8,192 tokens, 8 key / value heads of 128: 16 rows 266 us there and 305
-// here; 24 rows, two of its tiles, 513 there and 306 here.
+// Rows of a tile, for all sequences of the call.  Up to 16 go to the kernel of kv8_attn_few.cu (8
+// where that is all).  Measured, 128 sequences of up to 8,192 tokens, 8 key / value heads of 128: 4
+// rows 197 us there and 267 here, 16 rows 268 and 270; 24 rows, two of its tiles, 513 there and
+// 272 here.
 int tile_rows(int max_new, int group) {
   const int64_t rows = int64_t(max_new) * group;
   return rows <= 8 ? 8 : rows <= 16 ? 16 : 128;

@@ -32,7 +32,7 @@ struct AttnParams {
 // Each tile counts HEAD_UNITS more than its chunks, at its front, for what it costs beside them
 // (its q, its first maxima, its outputs), so that runs of many short tiles take no longer than
 // others.  Measured: 3, 4, 5 and 6 chunks' for 128 rows, 64 sequences of 16 new tokens, 93.7, 93.7,
-// 93.5 and 94.8 us; 0, 1 and 2 for few, 128 sequences of one, 199.5, 197.1 and 198.0.
+// 93.5 and 94.8 us (weights not yet held up in f16); 0, 1 and 2 for few, 128 sequences of one, 199.5, 197.1 and 198.0.
 template <int ROWS>
 constexpr int HEAD_UNITS = ROWS == 128 ? 4 : 1;
 
@@ -297,9 +297,9 @@ __device__ __forceinline__ void join_parts(const JoinTile<D, ROWS>& t, int r, in
 // there are more warps than rows, W / rows of them share a row's parts.  What bounds it is the
 // latency of the reads, so as many as can be are under way: 8 parts of a row, or (a tile of 128 in
 // two parts, the usual case: all warps are resident at once then) two parts of four rows.  Measured,
-// the whole call: 64 sequences of 16 new tokens 94.5 us, 100.4 with a row a warp; 16 new tokens of
-// one sequence over 131,072 with one key / value head 30 us, 185 with the CTAs of one boundary at
-// work alone; two sequences' single tokens over as many, 8 heads, 55 and 58.
+// the whole call: 64 sequences of 16 new tokens 5.9 us less than with a row a warp (99.9 now); 16 new
+// tokens of one sequence over 131,072 with one key / value head 32 us, 185 with the CTAs of one
+// boundary at work alone; two sequences' single tokens over as many, 8 heads, 56 and 58.
 template <int D, int ROWS, int W, int Y>
 __global__ void __launch_bounds__(32 * W) kv8_join_kernel(const AttnParams p, int runs) {
   constexpr int E = D / 32, R = ROWS / (W * Y);  // columns of a lane; rows of a warp, in the usual case

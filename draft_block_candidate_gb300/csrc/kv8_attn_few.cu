@@ -2,9 +2,9 @@
 // the reading of the cache, 2 D bytes a token and head against 4 D operations a row, so what
 // counts is that the loads never wait.  A tensor-core tile of 128 rows would be one eighth full at
 // best and its barriers cost more than the products: measured, 128 sequences of up to 8,192
-// tokens, 8 key / value heads of 128, the tcgen05 kernel of kv8_attn.cu takes 305 us for any
-// number of rows, and this one 197 for 4 (6.1 TB/s of the cache, 92 % of the copy rate) and 266
-// for 16, where the softmax and the widening fill the warps.
+// tokens, 8 key / value heads of 128, the tcgen05 kernel of kv8_attn.cu takes 267 to 270 us for 4 to
+// 16 rows, and this one 197 for 4 (6.1 TB/s of the cache, 92 % of the copy rate) and 268 for 16,
+// where the softmax and the widening fill the warps.
 //
 // Here the products are warp-level f16 products (m16n8k16) with the tokens, and the head
 // dimension, as the 16 rows and 8 query rows as the columns, so that none of a tile is empty:

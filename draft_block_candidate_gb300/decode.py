@@ -229,7 +229,7 @@ class KV8Cache:
     """A paged key / value cache in e4m3 with one scale for each page and head.
 
     k, v [n_pages, kv_heads, page, head_dim] float8_e4m3fn; k_scale, v_scale
-    [n_pages, kv_heads] f32.  page in {16, 32, 64, 128}, head_dim in {32, 64, 128}."""
+    [n_pages, kv_heads] f32, positive, finite and at least 2^-126.  page in {16, 32, 64, 128}, head_dim in {32, 64, 128}."""
 
     def __init__(self, n_pages: int, kv_heads: int, page: int, head_dim: int, device="cuda"):
         shape = (n_pages, kv_heads, page, head_dim)
@@ -349,6 +349,7 @@ def kv8_attention(q: torch.Tensor, cache: KV8Cache, q_start: torch.Tensor, kv_le
 
     q [total, q_heads, head_dim] bf16 (strides by token and head multiples of 8); sequences
     as kv8_append takes them; new token i of n sees the first kv_len - n + i + 1 tokens.
+    max_new * q_heads / kv_heads of at most 16 picks a kernel for few rows for the whole call.
     scale: 1 / sqrt(head_dim) by default.  out [total, q_heads, head_dim] bf16 (rows outside
     the sequences keep what they hold; a new one holds zeros there).  lse: True, or a tensor
     [total, q_heads] f32 to write the natural-log sums of exponentials to (True: -inf outside

@@ -317,8 +317,8 @@ lilicorr_status lilicorr_beam_select(const void* logits, lilicorr_dtype ldtype, 
                                      void* workspace, size_t workspace_bytes, void* stream);
 
 /* One per-beam state of lilicorr_beam_reorder: row (b, j) starts at src + b * src_batch_stride
- * + j * src_beam_stride and is `segments` pieces of seg_bytes, src_seg_stride apart (the used
- * part of a longer cache, say); likewise dst.  Strides in bytes, not negative. */
+ * + j * src_beam_stride and is `segments` pieces of seg_bytes (at most 2^32 - 16), src_seg_stride
+ * apart (the used part of a longer cache, say); likewise dst.  Strides in bytes, not negative. */
 typedef struct {
   const void* src;
   void* dst;
@@ -342,8 +342,8 @@ lilicorr_status lilicorr_beam_reorder(const lilicorr_beam_state* states, int32_t
 /* A paged key / value cache held in 8 bits: codes are e4m3 (bias 7, largest 448, no infinity,
  * 0x7F / 0xFF NaN), and what a code stands for is code * scale[page, head].
  *   k_pages, v_pages  [n_pages, kv_heads, page, head_dim] codes, 16-byte aligned
- *   k_scale, v_scale  [n_pages, kv_heads] f32, positive and finite (powers of two where
- *                     lilicorr_kv8_append wrote them)
+ *   k_scale, v_scale  [n_pages, kv_heads] f32, positive, finite and at least 2^-126 (powers of two
+ *                     where lilicorr_kv8_append wrote them)
  *   page in {16, 32, 64, 128} tokens, head_dim in {32, 64, 128}, 1 <= kv_heads <= 1024
  * A sequence's tokens t lie in page block_table[b, t / page] at row t % page.  Device memory,
  * the caller's; the struct itself is host memory. */
@@ -397,7 +397,9 @@ lilicorr_status lilicorr_kv8_append(const lilicorr_kv8_cache* cache, const void*
  *        sequences are left as they were.  q, out and lse must not overlap
  * What is not finite stays where it is seen: a NaN code in a key or value makes the rows that see
  * it NaN (a value's in its column), and a row of q with an infinity or a NaN is NaN or what its
- * infinite scores give.  max_new * q_heads / kv_heads is below 2^31 - 256.
+ * infinite scores give.  max_new * q_heads / kv_heads is below 2^31 - 256; where it is at most 16 the
+ * whole call goes to a kernel for few rows, else to one for tiles of 128 rows, on which a sequence of
+ * one token costs as much as one of 128 rows (so single tokens are better not called beside blocks).
  * Sums and maxima are f32; the softmax weights are rounded to f16 before the second product (by
  * 2^-11 of their value; times value scale, those below 2^-23 of the row's largest by 2^-34 of it),
  * and q loses what lies 2^-17 below its row's largest value.  The bits of a result do not depend on when or where its parts were
