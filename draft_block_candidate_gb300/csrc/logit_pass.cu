@@ -98,6 +98,13 @@ __device__ __forceinline__ float lse_of(float M, float S) {
   return __fadd_rn(ph, __fadd_rn(pe, __fmaf_rn(s, IL, __fmul_rn(lo, IH))));
 }
 
+// The same for a row whose largest logit is top.  From -2^30 down floats are so far apart that the
+// log-partition rounds to top, and the pair, whose maxima start at M2_INIT, holds no more of it
+// than whether there was a NaN.
+__device__ __forceinline__ float row_lse(float M, float S, float top) {
+  return top <= -1073741824.f && !isnan(S) ? top : lse_of(M, S);
+}
+
 struct K1Partial {
   float m2, s;
   float v[KQ];
@@ -747,7 +754,7 @@ __global__ void __launch_bounds__(K1_THREADS, K1_MIN_BLOCKS) logit_pass_kernel(c
     p.cand_id[r * K + lane] = id + p.id_offset;
     p.cand_logit[r * K + lane] = v;
   }
-  if (lane == 0) p.lse[r] = lse_of(M, S);
+  if (lane == 0) p.lse[r] = row_lse(M, S, v);
 }
 
 // Merge of n vocabulary-shard records per row (one warp per row): the shards' sorted
@@ -776,7 +783,7 @@ __global__ void __launch_bounds__(128) k1_merge_kernel(const char* __restrict__ 
     cand_id[r * K + lane] = id;
     cand_logit[r * K + lane] = v;
   }
-  if (lane == 0) lse[r] = lse_of(M, S);
+  if (lane == 0) lse[r] = row_lse(M, S, v);
 }
 
 // ------------------------------------------------------------------------------ host

@@ -325,6 +325,26 @@ def test_log_partitions_with_finite_masks(lc, batch, V, dtype, mask):  # noqa: F
     assert torch.equal(rows.gather(-1, ids.long()), values.double())
 
 
+@pytest.mark.parametrize("value", [-2.0 ** 29, -1.2e9, -2e9, -2.9e9, -1e10, -1e20, F32_MIN, -math.inf])
+@pytest.mark.parametrize("batch,V,dtype", [(1, 40000, torch.bfloat16), (2, 9001, torch.float32), (60, 5001, torch.bfloat16)])
+def test_log_partitions_of_rows_masked_throughout(lc, batch, V, dtype, value):  # noqa: F811
+    """There the log-partition rounds to the largest logit; a NaN is still one."""
+    if value == F32_MIN and dtype == torch.bfloat16:
+        value = BF16_MIN
+    x = torch.full((batch, 4, V), value, device="cuda").to(dtype)
+    x[:, 2, 7] = max(value / 2, F32_MIN)
+    x[0, 3, V // 2] = math.nan
+    ids, values, lse = lc.topk_lse(x, 2)
+    want = torch.logsumexp(x[:, 1:].double(), -1)
+    assert bool(torch.isnan(lse[0, 2])) and torch.equal(lse[:, :2].double().isinf(), want[:, :2].isinf())
+    fin = torch.isfinite(want)
+    assert float(((lse.double() - want).abs()[fin] / want.abs()[fin]).max() if fin.any() else 0) <= 2.0 ** -24 + 2.0 ** -40
+    shards = torch.stack([lc.topk_lse_shard(x[..., :V // 2], 0, 2), lc.topk_lse_shard(x[..., V // 2:], V // 2, 2)])
+    _, _, merged = lc.topk_lse_merge(shards, 2)
+    assert torch.equal(merged.view(batch, 3)[fin], lse[fin])
+
+
+
 @pytest.mark.parametrize("value", [-2.0 ** 30, -1.5e9, -2.0 ** 31, -1e10, -1e20, -1e30, BF16_MIN, F32_MIN, 2.0 ** 30, 1e10, 3e38])
 @pytest.mark.parametrize("batch,V,dtype", SIZES)
 def test_select_rows_whose_largest_logit_is_of_any_size(lc, batch, V, dtype, value):  # noqa: F811
