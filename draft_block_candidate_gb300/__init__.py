@@ -12,6 +12,15 @@ from .decode import (  # noqa: F401
     kv8_attention,
     kv8_attention_workspace,
 )
+from .logits import adjust_logits  # noqa: F401
+from .pages import (  # noqa: F401
+    kv8_compact,
+    kv8_copy,
+    kv8_fork,
+    kv8_free,
+    kv8_grow,
+    kv8_pages_workspace,
+)
 from .api import (  # noqa: F401
     LilicorrError,
     Weights,

@@ -62,6 +62,17 @@ SIGNATURES = {
     "lilicorr_kv8_attention": (C.c_int, [_P, _P, C.c_int64, C.c_int64, C.c_int64, C.c_int32, _P,
                                          _P, C.c_int64, _P, C.c_int64, C.c_int32, C.c_int32,
                                          C.c_float, _P, _P, _P, C.c_size_t, _P]),
+    "lilicorr_adjust_logits": (C.c_int, [_P, _P]),
+    "lilicorr_kv8_pages_workspace_bytes": (C.c_size_t, [C.c_int64, C.c_int64]),
+    "lilicorr_kv8_fork": (C.c_int, [_P, C.c_int64, _P, C.c_int64, C.c_int64, C.c_int32, _P, C.c_int64,
+                                    C.c_int32, _P]),
+    "lilicorr_kv8_grow": (C.c_int, [_P, C.c_int64, _P, C.c_int64, C.c_int64, C.c_int32, _P, _P,
+                                    C.c_int32, C.c_int32, _P, _P, _P, C.c_size_t, _P]),
+    "lilicorr_kv8_free": (C.c_int, [_P, C.c_int64, _P, C.c_int64, C.c_int64, C.c_int32, _P, C.c_int32,
+                                    _P]),
+    "lilicorr_kv8_copy": (C.c_int, [_P, _P, C.c_int32, _P, _P, C.c_int64, _P]),
+    "lilicorr_kv8_compact": (C.c_int, [_P, C.c_int32, _P, _P, C.c_int64, _P, C.c_int32, _P, _P,
+                                       C.c_size_t, _P]),
     "lilicorr_status_string": (C.c_char_p, [C.c_int]),
     "lilicorr_last_error": (C.c_char_p, []),
     "lilicorr_launch_count": (C.c_uint64, []),
@@ -97,6 +108,21 @@ class Kv8CacheDesc(C.Structure):
     _fields_ = [("k_pages", C.c_void_p), ("v_pages", C.c_void_p), ("k_scale", C.c_void_p),
                 ("v_scale", C.c_void_p), ("n_pages", C.c_int64), ("kv_heads", C.c_int32),
                 ("page", C.c_int32), ("head_dim", C.c_int32)]
+
+
+class Adjust(C.Structure):
+    _fields_ = ([("logits", C.c_void_p), ("out", C.c_void_p), ("ldtype", C.c_int)]
+                + [(n, C.c_int64) for n in ("rows", "V", "row_stride", "out_stride", "groups")]
+                + [("history", C.c_void_p), ("history_stride", C.c_int64), ("cap", C.c_int32)]
+                + [(n, C.c_void_p) for n in ("seen", "counted_from", "repetition", "presence",
+                                             "frequency", "bias_id", "bias")]
+                + [("n_bias", C.c_int32), ("mask", C.c_void_p), ("n_masks", C.c_int64),
+                   ("mask_stride", C.c_int64), ("mask_index", C.c_void_p)])
+
+
+class Kv8Table(C.Structure):
+    _fields_ = [("table", C.c_void_p), ("out", C.c_void_p), ("rows", C.c_int64),
+                ("row_stride", C.c_int64), ("out_stride", C.c_int64), ("cols", C.c_int32)]
 
 
 class Taps(C.Structure):

@@ -25,6 +25,7 @@ enum ErrSite : uint32_t {
   ERR_KV8_EMPTY_WAIT = 1u << 28,
   ERR_KV8_S_WAIT = 1u << 29,
   ERR_KV8_PV_WAIT = 1u << 30,
+  ERR_MASK_INDEX = 1u << 31,  // a row's mask out of range
 };
 
 // About one second at GB300 clocks: any wait longer than this is treated as a failure.

@@ -23,9 +23,12 @@ size_t k1_shard_record_bytes(int K);
 cudaError_t k1_merge_launch(const void* records, int n, int64_t rows, int K, int32_t* cand_id,
                             float* cand_logit, float* lse, cudaStream_t stream);
 cudaError_t k1_read_device_error(uint32_t* code);
-// beam selection and reordering (beam.cu), 8-bit cache (kv8.cu)
+// beam selection and reordering (beam.cu), 8-bit cache (kv8.cu), its pages (pages.cu), edits of
+// logits (adjust.cu)
 cudaError_t beam_read_device_error(uint32_t* code);
 cudaError_t kv8_read_device_error(uint32_t* code);
+cudaError_t pages_read_device_error(uint32_t* code);
+cudaError_t adjust_read_device_error(uint32_t* code);
 
 // message returned by lilicorr_last_error() for this thread (lilicorr_api.cu)
 void set_last_error(const char* msg);

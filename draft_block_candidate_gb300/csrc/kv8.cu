@@ -186,15 +186,7 @@ cudaError_t kv8_read_device_error(uint32_t* code) {
   return e == cudaSuccess ? kv8_attention_read_device_error(code) : e;
 }
 
-namespace {
-
-lilicorr_status fail(lilicorr_status st, const char* msg) {
-  set_last_error(msg);
-  return st;
-}
-
-// Null where the cache's description is in order, else what is wrong with it.
-const char* cache_error(const lilicorr_kv8_cache* c) {
+const char* kv8_cache_error(const lilicorr_kv8_cache* c) {
   if (!c || !c->k_pages || !c->v_pages || !c->k_scale || !c->v_scale) return "null cache pointer";
   if (c->head_dim != 32 && c->head_dim != 64 && c->head_dim != 128) return "head_dim is 32, 64 or 128";
   if (c->page != 16 && c->page != 32 && c->page != 64 && c->page != 128) return "page is 16, 32, 64 or 128";
@@ -206,6 +198,14 @@ const char* cache_error(const lilicorr_kv8_cache* c) {
     return "scales are 4-byte aligned";
   return nullptr;
 }
+
+namespace {
+
+lilicorr_status fail(lilicorr_status st, const char* msg) {
+  set_last_error(msg);
+  return st;
+}
+
 const char* batch_error(const int32_t* q_start, const int32_t* kv_len, int64_t batch,
                         const int32_t* table, int64_t table_stride, int32_t cols, int64_t total,
                         int32_t max_new, int page) {
@@ -247,7 +247,7 @@ lilicorr_status lilicorr_kv8_append(const lilicorr_kv8_cache* cache, const void*
                                     const int32_t* q_start, const int32_t* kv_len, int64_t batch,
                                     const int32_t* block_table, int64_t table_stride, int32_t cols,
                                     int32_t max_new, const int32_t* tail_src, void* stream) {
-  const char* why = cache_error(cache);
+  const char* why = kv8_cache_error(cache);
   if (!why) why = batch_error(q_start, kv_len, batch, block_table, table_stride, cols, total, max_new, cache->page);
   if (!why) why = rows_error(k, k_token_stride, k_head_stride);
   if (!why) why = rows_error(v, v_token_stride, v_head_stride);
@@ -301,7 +301,7 @@ lilicorr_status lilicorr_kv8_attention(const lilicorr_kv8_cache* cache, const vo
                                        int32_t cols, int32_t max_new, float scale, void* out,
                                        float* lse, void* workspace, size_t workspace_bytes,
                                        void* stream) {
-  const char* why = cache_error(cache);
+  const char* why = kv8_cache_error(cache);
   if (!why) why = batch_error(q_start, kv_len, batch, block_table, table_stride, cols, total, max_new, cache->page);
   if (!why) why = rows_error(q, q_token_stride, q_head_stride);
   if (!why && (!out || reinterpret_cast<uintptr_t>(out) % 16)) why = "out is null or not 16-byte aligned";

@@ -53,6 +53,8 @@ __device__ __forceinline__ SeqRange seq_range(const int32_t* __restrict__ q_star
 }
 
 // ---- host
+// Null where the cache's description is in order, else what is wrong with it.
+const char* kv8_cache_error(const lilicorr_kv8_cache* c);
 struct Kv8Attention {
   Kv8 c;
   const __nv_bfloat16* q;

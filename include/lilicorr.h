@@ -418,6 +418,109 @@ lilicorr_status lilicorr_kv8_attention(const lilicorr_kv8_cache* cache, const vo
                                        float* lse, void* workspace, size_t workspace_bytes,
                                        void* stream);
 
+/* Penalties for repeated tokens, biases and grammar masks on logits, before they are ranked.  A row's
+ * history is that of its group (rows / groups consecutive rows share one), of which it sees the first
+ * seen[row] tokens.  With c the number of times that token v is among them, and g the same from
+ * position counted_from[group] on,
+ *   x1 = c > 0 ? (x > 0 ? x / repetition : x * repetition) : x
+ *   x2 = x1 - frequency * g - (g > 0 ? presence : 0)
+ *   x3 = x2 + the sum of v's biases in the list, in its order
+ *   out = x3, or -inf where the row's mask has a 0 for v,
+ * in 64 bits and rounded once; a token that nothing touches is copied bit for bit (a NaN that a mask
+ * takes out becomes -inf).  out is the logits themselves (with the same row stride), or apart from
+ * them; what lies behind a row's V logits is not touched.
+ *   logits, out  [rows, V] F32 or BF16, rows a stride >= V apart, element aligned
+ *   history      nullable [groups, cap] int32, rows history_stride apart; ids outside 0..V-1 are passed over
+ *   seen         [rows] int32, at most cap (else the row is left out, and bit 26 of the device error word set)
+ *   counted_from nullable [groups] int32: frequency and presence count from there (0; the end of a prompt)
+ *   repetition, presence, frequency  nullable [groups] f32 (1, 0 and 0)
+ *   bias_id, bias  [groups, n_bias], n_bias <= 1024; ids outside 0..V-1 are passed over
+ *   mask         nullable [n_masks] rows of (V + 31) / 32 words, mask_stride apart; bit v % 32 of word
+ *                v / 32 is 1 where v may be taken
+ *   mask_index   nullable [rows] int32: each row's mask, negative for none (n_masks or more: the row is
+ *                left out, and bit 31 set); without it row r has mask r
+ * Pointers but for the struct are device memory.  Errors: LILICORR_ERR_INVALID_ARG, LILICORR_ERR_CUDA. */
+typedef struct {
+  const void* logits;
+  void* out;
+  lilicorr_dtype ldtype;
+  int64_t rows, V, row_stride, out_stride, groups;
+  const int32_t* history;
+  int64_t history_stride;
+  int32_t cap;
+  const int32_t *seen, *counted_from;
+  const float *repetition, *presence, *frequency;
+  const int32_t* bias_id;
+  const float* bias;
+  int32_t n_bias;
+  const int32_t* mask;
+  int64_t n_masks, mask_stride;
+  const int32_t* mask_index;
+} lilicorr_adjust;
+lilicorr_status lilicorr_adjust_logits(const lilicorr_adjust* a, void* stream);
+
+/* ---- Pages of the 8-bit cache that sequences share ----
+ * refs [n_pages] int32 counts, for each page, the entries of block tables that name it; a page with none
+ * is free.  An entry of a table is the page that its row holds there; a negative one is none.  The calls
+ * below keep the two in step; what they decide follows from the order of rows, columns and pages alone.
+ * A page index of n_pages or more, or a page that is held but counted as free, sets bit 25 of the device
+ * error word and is passed over.
+ *
+ * lilicorr_kv8_fork: row (b, j) of the table [batch, beams, cols] becomes row (b, parent[b, j]), in
+ * place, and refs follows (hypotheses go on as their parents; a prompt's row is shared by all).  A parent
+ * outside 0..beams-1 leaves its row as it is and sets bit 24.  1 <= beams <= 32.
+ *
+ * lilicorr_kv8_grow: row r is to write tokens kv_len[r] .. kv_len[r] + new_tokens[r] - 1 next.  Each
+ * column that they touch, where the row holds no page or one that others hold too, takes a free page,
+ * lowest first, in the order of rows and columns; a page that is given up in this call is not taken in
+ * it.  tail_src[r] is the page given up in the column that holds tokens before kv_len[r] (what
+ * lilicorr_kv8_append takes of that name), else -1.  granted[r] is 1 where the row has all its pages; a
+ * row that they do not suffice for, counting those of all rows before it, is left as it was, with 0, and may not be appended
+ * to.  So is a row whose length is out of range (bit 26), whose new tokens are more than max_new (26), or
+ * that holds no page for tokens that it has (25).  Workspace: lilicorr_kv8_pages_workspace_bytes.
+ *
+ * lilicorr_kv8_free: entries of row r behind its first keep[r] tokens become -1, and refs loses them
+ * (keep 0: the row ends; the kept length after a check: rejected tokens' pages).  A negative keep leaves
+ * the row and sets bit 26.
+ *
+ * lilicorr_kv8_copy: pages src[i] of caches from[c] are copied, scales among them, to pages dst[i] of
+ * to[c] (the same caches, or others of the same heads, page and head_dim), for every c < n_caches and
+ * i < n; a negative index moves nothing.  No destination may be another move's source or destination.
+ *
+ * lilicorr_kv8_compact: with L live pages, the i-th live page from L on moves to the i-th free page below
+ * L in every cache; refs_out (refs itself, or apart from it) and the tables' `out` (themselves, or apart)
+ * are counts and entries afterwards, and live [1] is L.  Every table that refs counts is to be given.
+ * Workspace: lilicorr_kv8_pages_workspace_bytes(n_pages, 1).
+ *
+ * Workspaces are 256-byte aligned, without initial contents; calls that overlap must not share one.
+ * Errors: LILICORR_ERR_INVALID_ARG, LILICORR_ERR_WORKSPACE, LILICORR_ERR_CUDA. */
+size_t lilicorr_kv8_pages_workspace_bytes(int64_t n_pages, int64_t rows);
+lilicorr_status lilicorr_kv8_fork(int32_t* refs, int64_t n_pages, int32_t* table, int64_t batch_stride,
+                                  int64_t row_stride, int32_t cols, const int32_t* parent,
+                                  int64_t batch, int32_t beams, void* stream);
+lilicorr_status lilicorr_kv8_grow(int32_t* refs, int64_t n_pages, int32_t* table, int64_t rows,
+                                  int64_t row_stride, int32_t cols, const int32_t* kv_len,
+                                  const int32_t* new_tokens, int32_t page, int32_t max_new,
+                                  int32_t* tail_src, uint8_t* granted, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+lilicorr_status lilicorr_kv8_free(int32_t* refs, int64_t n_pages, int32_t* table, int64_t rows,
+                                  int64_t row_stride, int32_t cols, const int32_t* keep,
+                                  int32_t page, void* stream);
+lilicorr_status lilicorr_kv8_copy(const lilicorr_kv8_cache* from, const lilicorr_kv8_cache* to,
+                                  int32_t n_caches, const int32_t* src, const int32_t* dst,
+                                  int64_t n, void* stream);
+typedef struct {
+  const int32_t* table;
+  int32_t* out;
+  int64_t rows, row_stride, out_stride;
+  int32_t cols;
+} lilicorr_kv8_table;
+lilicorr_status lilicorr_kv8_compact(const lilicorr_kv8_cache* caches, int32_t n_caches,
+                                     const int32_t* refs, int32_t* refs_out, int64_t n_pages,
+                                     const lilicorr_kv8_table* tables, int32_t n_tables,
+                                     int32_t* live, void* workspace, size_t workspace_bytes,
+                                     void* stream);
+
 /* Human-readable name of a status; never NULL. */
 const char* lilicorr_status_string(lilicorr_status s);
 /* Message of the most recent CUDA failure in this thread ("" if none). */
@@ -428,7 +531,7 @@ uint64_t lilicorr_launch_count(void);
  * device): 0 = no error; otherwise one bit per wait site that gave up (bits 0-7 the logit
  * pass, bits 8-15 the tensor-core GEMM, bits 16-23 the tensor-core attention, bits 27-30
  * the cache attention), and of the decoding entry points one bit each for an index or length in
- * device memory that was out of range (24 a parent, 25 a page, 26 a length or row range). */
+ * device memory that was out of range (24 a parent, 25 a page, 26 a length or row range, 31 a mask). */
 lilicorr_status lilicorr_device_error(uint32_t* code);
 /* Self-check of the device-side timeouts (a diagnostic of this library; the pages have no
  * counterpart).  Runs the logit pass on one row of V bf16 logits (device memory, 16-byte
