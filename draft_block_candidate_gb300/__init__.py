@@ -12,6 +12,7 @@ from .decode import (  # noqa: F401
     kv8_attention,
     kv8_attention_workspace,
 )
+from .cross import cross_attention, cross_attention_workspace  # noqa: F401
 from .logits import adjust_logits  # noqa: F401
 from .pages import (  # noqa: F401
     kv8_compact,

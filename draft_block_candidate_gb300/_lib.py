@@ -73,6 +73,11 @@ SIGNATURES = {
     "lilicorr_kv8_copy": (C.c_int, [_P, _P, C.c_int32, _P, _P, C.c_int64, _P]),
     "lilicorr_kv8_compact": (C.c_int, [_P, C.c_int32, _P, _P, C.c_int64, _P, C.c_int32, _P, _P,
                                        C.c_size_t, _P]),
+    "lilicorr_cross_attention_workspace_bytes": (C.c_size_t, [C.c_int32]),
+    "lilicorr_cross_attention": (C.c_int, [_P, C.c_int64, C.c_int64, C.c_int64, C.c_int32,
+                                           _P, C.c_int64, C.c_int64, _P, C.c_int64, C.c_int64, C.c_int64,
+                                           C.c_int32, C.c_int32, _P, _P, _P, C.c_int64, C.c_int32,
+                                           C.c_float, _P, _P, _P, C.c_size_t, _P]),
     "lilicorr_status_string": (C.c_char_p, [C.c_int]),
     "lilicorr_last_error": (C.c_char_p, []),
     "lilicorr_launch_count": (C.c_uint64, []),

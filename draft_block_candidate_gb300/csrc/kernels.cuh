@@ -29,6 +29,7 @@ cudaError_t beam_read_device_error(uint32_t* code);
 cudaError_t kv8_read_device_error(uint32_t* code);
 cudaError_t pages_read_device_error(uint32_t* code);
 cudaError_t adjust_read_device_error(uint32_t* code);
+cudaError_t cross_read_device_error(uint32_t* code);  // cross_attn.cu
 
 // message returned by lilicorr_last_error() for this thread (lilicorr_api.cu)
 void set_last_error(const char* msg);

@@ -25,6 +25,7 @@ struct AttnParams {
   __nv_bfloat16* out;  // [total, q_heads, D]
   float* lse;          // [total, q_heads] or null
   float* part;         // [2 * grid][rows of a tile * (D + 2)]: products, maxima, sums
+  __device__ __forceinline__ int kv_heads() const { return c.heads; }
 };
 
 // ------------------------------------------------------------------------ the deal of work
@@ -40,17 +41,20 @@ struct SeqUnits {
   int n, len, tiles, chunks;
   int64_t q0, units;
 };
-template <int ROWS>
-__device__ __forceinline__ SeqUnits seq_units(const AttnParams& p, int64_t b) {
-  const SeqRange r = seq_range(p.q_start, p.kv_len, b, p.total, p.max_new,
-                               int64_t(p.cols) << p.page_log2, &g_err_kv8_attn);
+__device__ __forceinline__ SeqRange attn_range(const AttnParams& p, int64_t b) {
+  return seq_range(p.q_start, p.kv_len, b, p.total, p.max_new, int64_t(p.cols) << p.page_log2, &g_err_kv8_attn);
+}
+// (P: AttnParams, or the parameters of another attention that is dealt alike)
+template <int ROWS, class P>
+__device__ __forceinline__ SeqUnits seq_units(const P& p, int64_t b) {
+  const SeqRange r = attn_range(p, b);
   SeqUnits u;
   u.n = r.n;
   u.len = r.len;
   u.q0 = r.q0;
   u.tiles = (r.n * p.group + ROWS - 1) / ROWS;
   u.chunks = max(1, (r.len + AT_CHUNK - 1) / AT_CHUNK);
-  u.units = int64_t(u.tiles) * p.c.heads * (u.chunks + HEAD_UNITS<ROWS>);
+  u.units = int64_t(u.tiles) * p.kv_heads() * (u.chunks + HEAD_UNITS<ROWS>);
   return u;
 }
 
@@ -60,8 +64,8 @@ struct Run {
   int64_t u, u_end;  // this run's units
   int64_t b, first;  // the sequence of unit u, and that sequence's first unit
 };
-template <int ROWS>
-__device__ __forceinline__ Run find_run(const AttnParams& p, int64_t run, int runs) {
+template <int ROWS, class P>
+__device__ __forceinline__ Run find_run(const P& p, int64_t run, int runs) {
   const int lane = threadIdx.x & 31;
   int64_t t = 0;
 #pragma unroll 1
@@ -98,9 +102,9 @@ __device__ __forceinline__ Run find_run(const AttnParams& p, int64_t run, int ru
 }
 
 // The pieces of a run, in order: the chunks [c0, c1) of one tile each.
-template <int ROWS>
+template <int ROWS, class P = AttnParams>
 struct Pieces {
-  const AttnParams& p;
+  const P& p;
   const Run run;
   int64_t b, u;       // the next unit, and its sequence
   SeqUnits sq;
@@ -109,7 +113,7 @@ struct Pieces {
   int ph, ptile;
   int64_t pb;
   SeqUnits psq;
-  __device__ __forceinline__ Pieces(const AttnParams& p_, const Run& r) : p(p_), run(r), b(r.b), u(r.u), h(0), tile(0), at(0), count(0) {
+  __device__ __forceinline__ Pieces(const P& p_, const Run& r) : p(p_), run(r), b(r.b), u(r.u), h(0), tile(0), at(0), count(0) {
     if (u < run.u_end) {
       sq = seq_units<ROWS>(p, b);
       const uint32_t in = static_cast<uint32_t>(u - run.first);  // a sequence's units fit 32 bits (host)
@@ -136,7 +140,7 @@ struct Pieces {
         at = 0;
         if (++tile == sq.tiles) {
           tile = 0;
-          if (++h == p.c.heads) {
+          if (++h == p.kv_heads()) {
             h = 0;
             if (u < run.u_end) sq = seq_units<ROWS>(p, ++b);
           }
@@ -213,7 +217,8 @@ struct JoinTile {
   int h, tile, count, j;  // count 0: none
   const float* parts;
   int64_t lead;           // the run of the first chunk may hold another tile's part before it
-  __device__ __forceinline__ JoinTile(const AttnParams& p, int64_t at, int runs) : count(0) {
+  template <class P>
+  __device__ __forceinline__ JoinTile(const P& p, int64_t at, int runs) : count(0) {
     const Run run = find_run<ROWS>(p, at + 1, runs);
     const int64_t edge = run.u;  // first unit of the run behind the boundary
     if (edge >= run.u_end) return;
@@ -300,8 +305,8 @@ __device__ __forceinline__ void join_parts(const JoinTile<D, ROWS>& t, int r, in
 // the whole call: 64 sequences of 16 new tokens 5.9 us less than with a row a warp (99.9 now); 16 new
 // tokens of one sequence over 131,072 with one key / value head 32 us, 185 with the CTAs of one
 // boundary at work alone; two sequences' single tokens over as many, 8 heads, 56 and 58.
-template <int D, int ROWS, int W, int Y>
-__global__ void __launch_bounds__(32 * W) kv8_join_kernel(const AttnParams p, int runs) {
+template <int D, int ROWS, int W, int Y, class P = AttnParams>
+__global__ void __launch_bounds__(32 * W) kv8_join_kernel(const P p, int runs) {
   constexpr int E = D / 32, R = ROWS / (W * Y);  // columns of a lane; rows of a warp, in the usual case
   __shared__ float s_y[W][D], s_m[W], s_l[W];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;

@@ -285,6 +285,7 @@ lilicorr_status lilicorr_device_error(uint32_t* code) {
   LC_CUDA(kv8_read_device_error(code), "read device error");
   LC_CUDA(pages_read_device_error(code), "read device error");
   LC_CUDA(adjust_read_device_error(code), "read device error");
+  LC_CUDA(cross_read_device_error(code), "read device error");
   return *code ? LILICORR_ERR_DEVICE : LILICORR_OK;
 }
 

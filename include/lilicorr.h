@@ -521,6 +521,41 @@ lilicorr_status lilicorr_kv8_compact(const lilicorr_kv8_cache* caches, int32_t n
                                      int32_t* live, void* workspace, size_t workspace_bytes,
                                      void* stream);
 
+/* Attention over states of another length (an encoder's, a target's), which a request's rows share:
+ *   out[r, j] = sum_t softmax_t(scale * q[r, j] . k[t, j / group]) v[t, j / group],
+ * group = q_heads / kv_heads, over all states kv_start[b] <= t < kv_start[b] + kv_len[b] of the request
+ * b that row r belongs to: rows q_start[b] .. q_start[b+1]-1, whether they are beams, the tokens of a
+ * block or both.  Several requests may have the same states.  lse [total, q_heads] (nullable, f32) is the
+ * natural-log sum of the exponentials.  A row without states has out 0 and lse -inf, and so has one
+ * whose every score is -inf.
+ *   q      [total, q_heads, head_dim] bf16, element strides by token and head, multiples of 8, 16-byte
+ *          aligned
+ *   k, v   [total_kv, kv_heads, head_dim] bf16, likewise; rows do not overlap
+ *   q_start [batch + 1], kv_start, kv_len [batch] int32 (device memory); max_new at least every request's
+ *          rows.  A request whose rows or states are out of range is left out, and bit 26 of the device
+ *          error word set
+ *   out    [total, q_heads, head_dim] bf16, contiguous, 16-byte aligned; rows outside the requests are
+ *          left as they were
+ * head_dim is a multiple of 8, at most 128.  What is not finite stays where it is seen: an infinity or a NaN
+ * among a head's values makes that column of its rows NaN or infinite, one among the keys the rows whose
+ * scores it is part of; what lies behind a request's states has no influence.  Sums and maxima are f32;
+ * the softmax weights are rounded to bf16 before the second product.  The bits of a result do not depend
+ * on when or where its parts were worked out, but on the device's number of SMs and the other requests
+ * of the call.  Workspace: lilicorr_cross_attention_workspace_bytes (0 for unsupported sizes; by the
+ * current device), 256-byte aligned, no initial contents.  Calls that overlap must not share it.
+ * Errors: LILICORR_ERR_INVALID_ARG, LILICORR_ERR_WORKSPACE, LILICORR_ERR_CUDA. */
+size_t lilicorr_cross_attention_workspace_bytes(int32_t head_dim);
+lilicorr_status lilicorr_cross_attention(const void* q, int64_t q_token_stride,
+                                         int64_t q_head_stride, int64_t total, int32_t q_heads,
+                                         const void* k, int64_t k_token_stride,
+                                         int64_t k_head_stride, const void* v,
+                                         int64_t v_token_stride, int64_t v_head_stride,
+                                         int64_t total_kv, int32_t kv_heads, int32_t head_dim,
+                                         const int32_t* q_start, const int32_t* kv_start,
+                                         const int32_t* kv_len, int64_t batch, int32_t max_new,
+                                         float scale, void* out, float* lse, void* workspace,
+                                         size_t workspace_bytes, void* stream);
+
 /* Human-readable name of a status; never NULL. */
 const char* lilicorr_status_string(lilicorr_status s);
 /* Message of the most recent CUDA failure in this thread ("" if none). */
@@ -530,7 +565,7 @@ uint64_t lilicorr_launch_count(void);
 /* Read and clear the device-side error words of the current device (synchronises the
  * device): 0 = no error; otherwise one bit per wait site that gave up (bits 0-7 the logit
  * pass, bits 8-15 the tensor-core GEMM, bits 16-23 the tensor-core attention, bits 27-30
- * the cache attention), and of the decoding entry points one bit each for an index or length in
+ * the attention over caches and other states), and of the decoding entry points one bit each for an index or length in
  * device memory that was out of range (24 a parent, 25 a page, 26 a length or row range, 31 a mask). */
 lilicorr_status lilicorr_device_error(uint32_t* code);
 /* Self-check of the device-side timeouts (a diagnostic of this library; the pages have no

@@ -124,3 +124,41 @@ def compact(refs, tables):
         out[p] = 0
     moved = [t.cpu().clone().apply_(lambda e: to.get(e, e)) for t in tables]
     return torch.tensor(out, dtype=torch.int32), moved, list(to.items()), live
+
+
+def cross(q, k, v, q_start, kv_start, kv_len, scale):
+    """(out, lse, tolerance of out, tolerance of lse), float64, rows outside the requests NaN.
+
+    Tolerances: with p the softmax weights and D the head dimension,
+      * a score is an f32 sum of D exact products, and takes one f32 fma: it is off by at most
+        e = (D + 4) 2^-24 (scale sum|q k|) + 2^-22 |score|, and so is the lse, with one rounding of
+        the lse and a few of exp2, log2 and their sum (each below 2^-21) on top;
+      * a weight is off by that relative amount, the sum of weights too, and by its rounding to bf16
+        (2^-8 of its value at most), which the sum does not take;
+      * the f32 sums over T states in runs of 16: (T / 16 + 40) 2^-24 of sum p |v|;
+      * out is rounded to bf16 once: half a step, 2^-8 of its value at most."""
+    total, q_heads, D = q.shape
+    heads = k.shape[1]
+    group = q_heads // heads
+    out = torch.full((total, q_heads, D), math.nan, dtype=torch.float64)
+    lse = torch.full((total, q_heads), math.nan, dtype=torch.float64)
+    to, tl = torch.zeros_like(out), torch.zeros_like(lse)
+    q, k, v = (x.cpu().double() for x in (q, k, v))
+    for b in range(len(kv_len)):
+        r0, r1, t0, n = int(q_start[b]), int(q_start[b + 1]), int(kv_start[b]), int(kv_len[b])
+        for h in range(heads):
+            rows = q[r0:r1, h * group:(h + 1) * group]
+            at = (slice(r0, r1), slice(h * group, (h + 1) * group))
+            if n == 0:
+                out[at], lse[at] = 0.0, NEG
+                continue
+            kk, vv = k[t0:t0 + n, h], v[t0:t0 + n, h]
+            s = rows @ kk.T * scale
+            e = ((D + 4) * 2.0 ** -24 * (rows.abs() @ kk.abs().T) * abs(scale) + 2.0 ** -22 * s.abs()).amax(-1)
+            lse[at] = torch.logsumexp(s, -1)
+            p = torch.exp(s - lse[at][..., None])
+            out[at] = p @ vv
+            pv = p @ vv.abs()
+            to[at] = 2.0 ** -8 * out[at].abs() + (2 * e[..., None] + 2.0 ** -8 + (n / 16 + 40) * 2.0 ** -24) * pv + 1e-30
+            tl[at] = e + 2.0 ** -24 * lse[at].abs() + 2.0 ** -20
+    return out, lse, to, tl

@@ -136,6 +136,30 @@ def test_compact_refuses(lib):
         assert call(**kw) == WORKSPACE
 
 
+def cross(lib, q=FAKE, qt=1024, qh=128, total=8, heads=8, k=2 * FAKE, kt=512, kh=128, v=3 * FAKE, vt=512, vh=128, total_kv=100, kv_heads=2,
+          D=128, q_start=FAKE, kv_start=FAKE, kv_len=FAKE, batch=2, max_new=4, scale=0.1, out=8 * FAKE, lse=None, ws=FAKE, size=1 << 30):
+    return lib.lilicorr_cross_attention(q, qt, qh, total, heads, k, kt, kh, v, vt, vh, total_kv, kv_heads, D, q_start, kv_start, kv_len,
+                                        batch, max_new, scale, out, lse, ws, size, None)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(q=None), dict(k=None), dict(v=None), dict(q=FAKE + 8), dict(k=FAKE + 2), dict(qt=1020), dict(kh=4), dict(vt=-512), dict(vh=1 << 40),
+    dict(D=0), dict(D=136), dict(D=20), dict(q_start=None), dict(kv_start=None), dict(kv_len=None), dict(batch=0), dict(batch=1 << 21),
+    dict(total=0), dict(total=1 << 31), dict(total_kv=0), dict(total_kv=1 << 31), dict(max_new=0), dict(max_new=1 << 25), dict(kv_heads=0),
+    dict(kv_heads=3), dict(kv_heads=1025, heads=1025), dict(heads=0), dict(heads=2 * 1025), dict(kt=0), dict(vh=0), dict(kt=120), dict(out=None),
+    dict(out=FAKE + 8), dict(scale=float("nan")), dict(scale=float("inf")), dict(max_new=1 << 22, heads=2048), dict(out=FAKE),
+    dict(max_new=1 << 20, heads=1024, kv_heads=1024, total_kv=1 << 30, kt=1 << 18, vt=1 << 18, v=1 << 60),
+    dict(out=2 * FAKE + 1024), dict(out=3 * FAKE), dict(lse=8 * FAKE + 64), dict(lse=FAKE + 128)])
+def test_cross_refuses(lib, kw):
+    assert cross(lib, **kw) == INVALID
+
+
+def test_cross_workspace(lib):
+    f = lib.lilicorr_cross_attention_workspace_bytes
+    assert f(64) > 0 and f(128) > f(64) and f(0) == f(136) == f(12) == 0
+    assert cross(lib, ws=None) == cross(lib, ws=FAKE + 64) == cross(lib, size=64) == WORKSPACE
+
+
 def test_python_refuses_cpu_tensors_and_bad_layouts():
     import draft_block_candidate_gb300 as lc
     i32 = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
