@@ -40,6 +40,7 @@ struct CrossParams {
   int max_new;
   float scale2;  // |softmax scale| * log2 e
   uint32_t flip;  // sign bits of the scale, which q takes
+  int q_map;      // whether q comes through a tensor map
   __nv_bfloat16* out;  // [total, q_heads, D]
   float* lse;          // [total, q_heads] or null
   float* part;         // [2 * grid][256 * (padded D + 2)]: products, maxima, sums
@@ -81,7 +82,8 @@ struct CrossShape {
   static constexpr int OFF_Q = OFF_V + VS * T;
   static constexpr int SMEM = 1024 + OFF_Q + QS * T;
 };
-constexpr int CR_WARPS = 15, CR_CONSUMERS = 14, CR_PIECES = 4;
+// Warps: 0 to 3 and 4 to 7 the halves' softmax; then loads, each half's products, q.
+constexpr int CR_LOAD = 8, CR_MMA = 9, CR_Q = 11, CR_WARPS = 12, CR_READERS = CR_WARPS - 1, CR_PIECES = 6;
 constexpr int CR_S = 0, CR_O = 256;       // columns of S (and P) and O of the first half; the second's are 128 and DP further
 constexpr float CR_RAISE = 8.f;           // log2 of how far a score may pass its reference
 
@@ -107,44 +109,57 @@ __device__ __noinline__ void mask_columns(uint32_t t, int lim) {
     tmem_st16(t + w0, s);
   }
 }
+// A row's outputs by f (inlined, 8 at a time: the scores stay in registers meanwhile).
 template <int DP>
-__device__ __noinline__ void scale_outputs(uint32_t t, float f) {
+__device__ __forceinline__ void scale_outputs(uint32_t t, float f) {
 #pragma unroll 1
-  for (int w0 = 0; w0 < DP; w0 += 16) {
-    float o[16];
-    tmem_ld16(t + w0, o);
+  for (int w0 = 0; w0 < DP; w0 += 8) {
+    float o[8];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\ttcgen05.wait::ld.sync.aligned;"
+                 : "=f"(o[0]), "=f"(o[1]), "=f"(o[2]), "=f"(o[3]), "=f"(o[4]), "=f"(o[5]), "=f"(o[6]), "=f"(o[7])
+                 : "r"(t + w0)
+                 : "memory");
+    uint32_t h[8];
 #pragma unroll
-    for (int n = 0; n < 16; ++n) o[n] *= f;
-    tmem_st16(t + w0, o);
+    for (int n = 0; n < 8; ++n) h[n] = __float_as_uint(o[n] * f);
+    tmem_st8(t + w0, h);
   }
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
+
+// 16 bytes to shared memory behind the thread's back (zeros where !there); cp_wait: all of the thread's have landed.
+__device__ __forceinline__ void cp16(void* to, const void* from, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(to)), "l"(from), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 template <int DP>
 __global__ void __launch_bounds__(32 * CR_WARPS, 1)
-    cross_attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const __grid_constant__ CrossParams p) {
+    cross_attention_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
+                           const __grid_constant__ CrossParams p) {
   using S = CrossShape<DP>;
   constexpr int KS = S::KS, VS = S::VS, T = S::T, SUB = S::SUB;
   extern __shared__ uint8_t cr_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(cr_raw) + 1023) & ~uintptr_t(1023));
-  // sready, pready, pvdone: of each half, a phase for each of its chunks.  S of a chunk is made once the
-  // half's products before it are done, so who has a chunk's scores knows that.
+  // sready, pready: of each half, a phase for each of its chunks; pvdone, left: for each piece that it has
+  // chunks of; met: for each piece that the second half hands over, by turns.
   __shared__ __align__(8) uint64_t kfull[KS], kempty[KS], vfull[VS], vempty[VS], sready[2], pready[2], pvdone[2], qready[2], qfree[2],
-      left[2], pc_full[CR_PIECES], pc_empty[CR_PIECES], met[2][2][4];
+      left[2], pc_full[CR_PIECES], pc_empty[CR_PIECES], met[2][4];
   __shared__ CrossPiece s_piece[CR_PIECES];
-  __shared__ float2 s_ml[2][2][CR_HALF];  // a row's maximum and sum at the end of a piece: by the half's pieces, in turn
+  __shared__ float2 s_ml[2][CR_HALF];  // a row's maximum and sum, handed over
   __shared__ uint32_t s_tmem;
   __shared__ volatile uint32_t s_fail;
 
   const int tid = threadIdx.x, warp = __shfl_sync(FULL_MASK, tid >> 5, 0), lane = tid & 31;
   if (tid == 0) {
-    for (int i = 0; i < KS; ++i) { mbar_init(&kfull[i], 1); mbar_init(&kempty[i], 1); }
-    for (int i = 0; i < VS; ++i) { mbar_init(&vfull[i], 1); mbar_init(&vempty[i], 1); }
+    for (int i = 0; i < KS; ++i) { mbar_init(&kfull[i], 1); mbar_init(&kempty[i], 2); }
+    for (int i = 0; i < VS; ++i) { mbar_init(&vfull[i], 1); mbar_init(&vempty[i], 2); }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sready[i], 1); mbar_init(&pready[i], 4); mbar_init(&pvdone[i], 1);
-      mbar_init(&qready[i], 4); mbar_init(&qfree[i], 1); mbar_init(&left[i], 4);
-      for (int j = 0; j < 4; ++j) { mbar_init(&met[0][i][j], 1); mbar_init(&met[1][i][j], 1); }
+      mbar_init(&qready[i], 1); mbar_init(&qfree[i], 2); mbar_init(&left[i], 4);
+      for (int j = 0; j < 4; ++j) mbar_init(&met[i][j], 1);
     }
-    for (int i = 0; i < CR_PIECES; ++i) { mbar_init(&pc_full[i], 1); mbar_init(&pc_empty[i], CR_CONSUMERS); }
+    for (int i = 0; i < CR_PIECES; ++i) { mbar_init(&pc_full[i], 1); mbar_init(&pc_empty[i], CR_READERS); }
     fence_mbar_init();
     s_fail = 0;
   }
@@ -170,18 +185,22 @@ __global__ void __launch_bounds__(32 * CR_WARPS, 1)
       }
     return true;
   };
-  // The next piece, read by a warp.
-  auto next_piece = [&](int pi, CrossPiece& x) -> bool {
-    const int e = pi % CR_PIECES;
-    if (!wait_warp(&pc_full[e], (pi / CR_PIECES) & 1, ERR_KV8_FULL_WAIT)) return false;
-    x = s_piece[e];
-    if (x.whole < 0) return false;
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&pc_empty[e]);
-    return true;
+  // The next piece with chunks (or, `all`, any), read by a warp.
+  auto next_piece = [&](int& pi, CrossPiece& x, bool all) -> bool {
+#pragma unroll 1
+    for (;;) {
+      const int e = pi % CR_PIECES;
+      if (!wait_warp(&pc_full[e], (pi / CR_PIECES) & 1, ERR_KV8_FULL_WAIT)) return false;
+      x = s_piece[e];
+      if (x.whole < 0) return false;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&pc_empty[e]);
+      ++pi;
+      if (all || x.c0 < x.cn) return true;
+    }
   };
 
-  if (warp == 12) {
+  if (warp == CR_LOAD) {
     // ====== the run's pieces, and their keys and values ======
     const Run run = find_run<CR_ROWS>(p, blockIdx.x, gridDim.x);
     Pieces<CR_ROWS, CrossParams> w(p, run);
@@ -236,295 +255,179 @@ __global__ void __launch_bounds__(32 * CR_WARPS, 1)
       for (int i = max(0, vit - VS); i < vit; ++i)
         mbar_wait_bounded(&vfull[i % VS], (i / VS) & 1, &g_err_kv8_attn, ERR_KV8_EMPTY_WAIT);
     }
-  } else if (warp == 13) {
-    // ================= S = Q K^T =================
-    constexpr uint32_t ID = tc_idesc(128, AT_CHUNK, false, false, true);
-    const uint64_t d_k = tile_desc<128>(sm, 16), d_q = tile_desc<128>(sm + S::OFF_Q, 16);
-    int it = 0, qs = 0, n0 = 0, n1 = 0;  // chunks; halves of q; chunks of each half
+  } else if (warp >= CR_MMA && warp < CR_Q) {
+    // ====== half g's products: S of its next chunk takes the place of P of the one before, and so is issued
+    // behind the product that reads it (the tensor cores do what one thread issues in order) ======
+    constexpr uint32_t ID_S = tc_idesc(128, AT_CHUNK, false, false, true), ID_O = tc_idesc(128, DP, false, true, true);
+    const int g = warp - CR_MMA;
+    const uint64_t d_k = tile_desc<128>(sm, 16), d_q = tile_desc<128>(sm + S::OFF_Q, 16), d_v = tile_desc<128>(sm + S::OFF_V, SUB);
+    const uint32_t t_s = tmem + CR_S + g * 128, t_o = tmem + CR_O + g * DP;
+    int pi = 0, it = 0, n = 0, t = 0, qs = 0;  // chunks; the half's chunks and pieces; halves of q
     CrossPiece x;
-    for (int pi = 0; next_piece(pi, x); ++pi) {
-      if (x.c0 >= x.cn) continue;
+    while (next_piece(pi, x, false)) {
       const bool two = x.rows > CR_HALF;
-      bool ok = wait_warp(&qready[qs & 1], (qs >> 1) & 1, ERR_KV8_S_WAIT);
-      if (two) ok = wait_warp(&qready[(qs + 1) & 1], ((qs + 1) >> 1) & 1, ERR_KV8_S_WAIT) && ok;
+      const int step = two ? 1 : 2, d0 = two ? 0 : g, chunks = x.cn - x.c0;
+      const int slot = (qs + (two ? g : 0)) & 1;
+      const uint64_t q = d_q + (slot * T >> 4);
+      // (a half without a chunk waits too: what it leaves below is then of this use of the slot)
+      bool ok = wait_warp(&qready[slot], ((qs + (two ? g : 0)) >> 1) & 1, ERR_KV8_S_WAIT);
+      if (d0 < chunks) {
+        if (t++ > 0) ok = wait_warp(&left[g], t & 1, ERR_KV8_PV_WAIT) && ok;  // the piece before has left O
+      }
 #pragma unroll 1
-      for (int c = x.c0; c < x.cn; ++c, ++it) {
-        const int st = it % KS;
-        ok = wait_warp(&kfull[st], (it / KS) & 1, ERR_KV8_FULL_WAIT) && ok;
-        const uint64_t k = d_k + (st * T >> 4);
-        auto half = [&](int g, int& n) {
-          if (n > 0) ok = wait_warp(&pvdone[g], (n - 1) & 1, ERR_KV8_S_WAIT) && ok;
-          if (ok) {
-            tc_fence_after();
-            const uint64_t q = d_q + (((qs + (two ? g : 0)) & 1) * T >> 4);
+      for (int d = 0; d < chunks; ++d, ++it) {
+        const int sk = it % KS, sv = it % VS;
+        ok = wait_warp(&kfull[sk], (it / KS) & 1, ERR_KV8_FULL_WAIT) && ok;
+        if (!two && (d & 1) != g) {  // the other half's
+          if (lane == 0) mbar_arrive(&kempty[sk]);
+          wait_warp(&vfull[sv], (it / VS) & 1, ERR_KV8_PV_WAIT);
+          if (lane == 0) mbar_arrive(&vempty[sv]);
+          continue;
+        }
+        if (ok) {
+          tc_fence_after();
+          const uint64_t k = d_k + (sk * T >> 4);
 #pragma unroll
-            for (int d = 0; d < DP / 16; ++d) {
-              const int at = (d / 4) * (SUB >> 4) + (d % 4) * 2;
-              mma_f16(tmem + CR_S + g * 128, q + at, k + at, ID, d > 0);
-            }
+          for (int i = 0; i < DP / 16; ++i) {
+            const int at = (i / 4) * (SUB >> 4) + (i % 4) * 2;
+            mma_f16(t_s, q + at, k + at, ID_S, i > 0);
           }
-          tc_commit(&sready[g]);
-          ++n;
-        };
-        if (two || ((c - x.c0) & 1) == 0) half(0, n0);
-        if (two || ((c - x.c0) & 1) == 1) half(1, n1);
-        tc_commit(&kempty[st]);
-      }
-      tc_commit(&qfree[qs & 1]);
-      ++qs;
-      if (two) {
-        tc_commit(&qfree[qs & 1]);
-        ++qs;
-      }
-    }
-  } else if (warp == 14) {
-    // ================= O += P V =================
-    constexpr uint32_t ID = tc_idesc(128, DP, false, true, true);
-    const uint64_t d_v = tile_desc<128>(sm + S::OFF_V, SUB);
-    int it = 0, n0 = 0, n1 = 0, t0 = 0, t1 = 0;  // chunks; chunks of each half, pieces of each half
-    CrossPiece x;
-    for (int pi = 0; next_piece(pi, x); ++pi) {
-      const bool two = x.rows > CR_HALF;
-#pragma unroll 1
-      for (int c = x.c0; c < x.cn; ++c, ++it) {
-        const int st = it % VS, rem = min(AT_CHUNK, x.len - c * AT_CHUNK), steps = (rem + 15) / 16;
-        bool ok = wait_warp(&vfull[st], (it / VS) & 1, ERR_KV8_PV_WAIT);
+        }
+        tc_commit(&sready[g]);
+        tc_commit(&kempty[sk]);
+        if (d + step >= chunks) {  // q has been read (the slot waits for both halves)
+          tc_commit(&qfree[slot]);
+          if (two) tc_commit(&qfree[slot]);
+        }
+        const int rem = min(AT_CHUNK, x.len - (x.c0 + d) * AT_CHUNK), steps = (rem + 15) / 16;
+        ok = wait_warp(&vfull[sv], (it / VS) & 1, ERR_KV8_PV_WAIT) && ok;
         if (rem & 15) {  // rows behind the last state: weights of 0, which no NaN may meet
-          uint8_t* v = sm + S::OFF_V + st * T + rem * 128;
-          const int n = (steps * 16 - rem) * 8;
-          for (int i = lane; i < n; i += 32)
+          uint8_t* v = sm + S::OFF_V + sv * T + rem * 128;
+          const int all = (steps * 16 - rem) * 8;
+          for (int i = lane; i < all; i += 32)
 #pragma unroll
             for (int j = 0; j < DP / 64; ++j) *reinterpret_cast<uint4*>(v + j * SUB + i * 16) = make_uint4(0u, 0u, 0u, 0u);
           fence_async_smem();
           __syncwarp();
         }
-        const uint64_t v = d_v + (st * T >> 4);
-        auto half = [&](int g, int& n, int& t, bool first) {
-          if (first && t++ > 0) ok = wait_warp(&left[g], t & 1, ERR_KV8_PV_WAIT) && ok;  // the piece before has left O
-          ok = wait_warp(&pready[g], n & 1, ERR_KV8_PV_WAIT) && ok;
-          if (ok) {
-            tc_fence_after();
-            // (16 states further: 8 columns of P; 16 rows of V)
-#pragma unroll 4
-            for (int i = 0; i < steps; ++i)
-              mma_f16_ts(tmem + CR_O + g * DP, tmem + CR_S + g * 128 + 8 * i, v + i * 128, ID, i > 0 || !first);
-          }
-          tc_commit(&pvdone[g]);
-          ++n;
-        };
-        const int d = c - x.c0;
-        if (two || (d & 1) == 0) half(0, n0, t0, d == 0);
-        if (two || (d & 1) == 1) half(1, n1, t1, d == (two ? 0 : 1));
-        tc_commit(&vempty[st]);
-      }
-    }
-  } else if (warp >= 8) {
-    // ====== q of a tile, ahead; then the outputs of the tile before ======
-    const int k = warp & 3;
-    constexpr int LPR = DP / 8, RPW = 32 / LPR;  // lanes of a row (8 values each), rows of a warp at a time
-    const int piece = lane % LPR;
-    const uint32_t t_lane = static_cast<uint32_t>(32 * k) << 16;
-    int qs = 0, n[2] = {0, 0}, t[2] = {0, 0};  // halves of q; up to piece y: chunks and pieces of each half
-    auto bring = [&](const CrossPiece& x, int row0, int rows) {  // rows [row0, row0 + rows) of the request
-      const int s = qs & 1;
-      if (qs > 1) wait_warp(&qfree[s], ((qs >> 1) - 1) & 1, ERR_KV8_S_WAIT);
-      uint8_t* to = sm + S::OFF_Q + s * T + (piece / 8) * SUB;
-      const __nv_bfloat16* q = p.q + x.q0 * p.q_tok + int64_t(x.h) * p.group * p.q_head + piece * 8;
-      constexpr int A = 8;  // reads under way
-#pragma unroll 1
-      for (int r0 = k * RPW + lane / LPR; r0 < CR_HALF; r0 += 4 * RPW * A) {
-        uint4 w[A];
-#pragma unroll
-        for (int a = 0; a < A; ++a) {
-          const int r = r0 + a * 4 * RPW;
-          w[a] = make_uint4(0u, 0u, 0u, 0u);
-          if (r < rows && piece * 8 < p.D) {
-            const int i = (row0 + r) / p.group, j = row0 + r - i * p.group;
-            w[a] = __ldg(reinterpret_cast<const uint4*>(q + i * p.q_tok + j * p.q_head));
-            w[a].x ^= p.flip; w[a].y ^= p.flip; w[a].z ^= p.flip; w[a].w ^= p.flip;
-          }
-        }
-#pragma unroll
-        for (int a = 0; a < A; ++a) {
-          const int r = r0 + a * 4 * RPW;
-          if (r < CR_HALF) *reinterpret_cast<uint4*>(to + r * 128 + (((piece & 7) ^ (r & 7)) << 4)) = w[a];
-        }
-      }
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&qready[s]);
-      ++qs;
-    };
-    // Row `row` of piece y's tile from o = f0 O0 + f1 O1, 16 columns at a time; `mine`: whether it is there.
-    auto write = [&](const CrossPiece& y, int row, bool mine, bool use0, float f0, bool use1, float f1, float m, float l) {
-      const int i = mine ? (y.row0 + row) / p.group : 0, j = mine ? y.row0 + row - i * p.group : 0;
-      const int64_t at = (y.q0 + i) * p.q_heads + int64_t(y.h) * p.group + j;
-      float* part = p.part + int64_t(y.slot) * CR_ROWS * (DP + 2);
-#pragma unroll 1
-      for (int w0 = 0; w0 < DP; w0 += 16) {
-        float o[16], z[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) o[e] = 0.f;
-        if (use0) {
-          tmem_ld16(tmem + t_lane + CR_O + w0, o);
-#pragma unroll
-          for (int e = 0; e < 16; ++e) o[e] *= f0;
-        }
-        if (use1) {
-          tmem_ld16(tmem + t_lane + CR_O + DP + w0, z);
-#pragma unroll
-          for (int e = 0; e < 16; ++e) o[e] = use0 ? fmaf(z[e], f1, o[e]) : z[e] * f1;
-        }
-        if (w0 + 16 == DP) {  // O has been read
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            if (use0) mbar_arrive(&left[0]);
-            if (use1) mbar_arrive(&left[1]);
-          }
-        }
-        if (mine && y.whole) {
-          uint32_t h[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const __nv_bfloat162 v = __floats2bfloat162_rn(o[2 * e], o[2 * e + 1]);
-            h[e] = *reinterpret_cast<const uint32_t*>(&v);
-          }
-          uint4* dst = reinterpret_cast<uint4*>(p.out + at * p.D + w0);
-          if (w0 < p.D) dst[0] = make_uint4(h[0], h[1], h[2], h[3]);
-          if (w0 + 8 < p.D) dst[1] = make_uint4(h[4], h[5], h[6], h[7]);
-        } else if (mine) {
-          float4* dst = reinterpret_cast<float4*>(part + row * DP + w0);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-        }
-      }
-      if (mine && !y.whole) {
-        part[CR_ROWS * DP + row] = m;
-        part[CR_ROWS * DP + CR_ROWS + row] = l;
-      } else if (mine && p.lse) {
-        p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * LN2_F;
-      }
-    };
-    CrossPiece x, y{};
-    y.whole = -1;
-    for (int pi = 0;; ++pi) {
-      const bool more = next_piece(pi, x);
-      if (more && x.c0 < x.cn) {
-        bring(x, x.row0, min(x.rows, CR_HALF));
-        if (x.rows > CR_HALF) bring(x, x.row0 + CR_HALF, x.rows - CR_HALF);
-      }
-      if (y.whole >= 0) {
-        const bool two = y.rows > CR_HALF;
-        const int r = 32 * k + lane;
-        // a half's maximum and sum, once its products are done
-        auto half = [&](int g) {
-          const int e = (t[g] - 1) & 1;
-          wait_warp(&met[e][g][k], ((t[g] - 1) >> 1) & 1, ERR_KV8_PV_WAIT);
-          const float2 ml = s_ml[e][g][r];
-          wait_warp(&pvdone[g], (n[g] - 1) & 1, ERR_KV8_PV_WAIT);
+        ok = wait_warp(&pready[g], n & 1, ERR_KV8_PV_WAIT) && ok;
+        if (ok) {
           tc_fence_after();
-          return ml;
-        };
-        const int chunks = y.cn - y.c0;
-        if (two && chunks > 0) {
-          for (int g = 0; g < 2; ++g) {
-            const float2 ml = half(g);
-            const float f = !y.whole ? 1.f : ml.y == 0.f ? 0.f : 1.f / ml.y;
-            write(y, g * CR_HALF + r, g * CR_HALF + r < y.rows, g == 0, f, g == 1, f, ml.y == 0.f ? -INFINITY : ml.x, ml.y);
-          }
-        } else if (chunks > 0) {
-          const float2 a = half(0), b = chunks > 1 ? half(1) : make_float2(-INFINITY, 0.f);
-          const float top = fmaxf(a.y == 0.f ? -INFINITY : a.x, b.y == 0.f ? -INFINITY : b.x);
-          float f0 = a.y == 0.f ? 0.f : ex2(a.x - top), f1 = b.y == 0.f ? 0.f : ex2(b.x - top);
-          const float l = a.y * f0 + b.y * f1;
-          if (y.whole) {
-            const float inv = l == 0.f ? 0.f : 1.f / l;
-            f0 *= inv;
-            f1 *= inv;
-          }
-          write(y, r, r < y.rows, true, f0, chunks > 1, f1, top, l);
-        } else {  // no states
-          write(y, r, r < y.rows, false, 0.f, false, 0.f, -INFINITY, 0.f);
-          write(y, CR_HALF + r, CR_HALF + r < y.rows, false, 0.f, false, 0.f, -INFINITY, 0.f);
+          const uint64_t v = d_v + (sv * T >> 4);
+          // (16 states further: 8 columns of P; 16 rows of V)
+#pragma unroll 4
+          for (int i = 0; i < steps; ++i) mma_f16_ts(t_o, t_s + 8 * i, v + i * 128, ID_O, i > 0 || d > d0);
         }
+        if (d + step >= chunks) tc_commit(&pvdone[g]);
+        tc_commit(&vempty[sv]);
+        ++n;
       }
-      if (!more) break;
-      y = x;
-      const int chunks = x.cn - x.c0, two = x.rows > CR_HALF;
-      n[0] += two ? chunks : (chunks + 1) / 2;
-      n[1] += two ? chunks : chunks / 2;
-      t[0] += chunks > 0;
-      t[1] += chunks > (two ? 0 : 1);
+      if (d0 >= chunks && lane == 0) mbar_arrive(&qfree[slot]);
+      qs += two ? 2 : 1;
+    }
+  } else if (warp == CR_Q) {
+    // ====== q of a tile, ahead ======
+    constexpr int LPR = DP / 8, RPW = 32 / LPR;  // lanes of a row (8 values each), rows at a time
+    const int piece = lane % LPR;
+    int qs = 0, pi = 0;
+    CrossPiece x;
+    while (next_piece(pi, x, false)) {
+#pragma unroll 1
+      for (int half = 0; half * CR_HALF < x.rows; ++half, ++qs) {
+        const int s = qs & 1, row0 = x.row0 + half * CR_HALF, rows = x.rows - half * CR_HALF;
+        if (qs > 1) wait_warp(&qfree[s], ((qs >> 1) - 1) & 1, ERR_KV8_S_WAIT);
+        uint8_t* to = sm + S::OFF_Q + s * T;
+        if (p.q_map) {  // whole tokens of a group's heads; rows behind the last are other requests', or zeros
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&qready[s], T);
+#pragma unroll
+            for (int i = 0; i < DP / 64; ++i)
+              tma_load3(to + i * SUB, &tq, 64 * i, x.h * p.group, static_cast<int>(x.q0) + row0 / p.group, &qready[s]);
+          }
+          __syncwarp();
+          continue;
+        }
+        const __nv_bfloat16* q = p.q + x.q0 * p.q_tok + int64_t(x.h) * p.group * p.q_head + piece * 8;
+        int i = (row0 + lane / LPR) / p.group, j = row0 + lane / LPR - i * p.group;
+#pragma unroll 2
+        for (int r = lane / LPR; r < CR_HALF; r += RPW) {
+          const bool there = r < rows && piece * 8 < p.D;
+          cp16(to + (piece / 8) * SUB + r * 128 + (((piece & 7) ^ (r & 7)) << 4), there ? q + i * p.q_tok + j * p.q_head : p.q, there);
+          for (j += RPW; j >= p.group; j -= p.group) ++i;
+        }
+        cp_wait();
+        if (p.flip) {  // a negative scale
+#pragma unroll 1
+          for (int r = lane / LPR; r < CR_HALF; r += RPW) {
+            uint4* at = reinterpret_cast<uint4*>(to + (piece / 8) * SUB + r * 128 + (((piece & 7) ^ (r & 7)) << 4));
+            uint4 w = *at;
+            w.x ^= p.flip; w.y ^= p.flip; w.z ^= p.flip; w.w ^= p.flip;
+            *at = w;
+          }
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&qready[s]);
+      }
     }
   } else {
-    // ================= softmax: half g, rows 32 k + lane of it =================
+    // ====== softmax: half g, rows 32 k + lane of it; then the tile's outputs ======
     const int g = warp >> 2, k = warp & 3, r = 32 * k + lane;
-    const uint32_t t_s = tmem + (static_cast<uint32_t>(32 * k) << 16) + CR_S + g * 128;
-    const uint32_t t_o = tmem + (static_cast<uint32_t>(32 * k) << 16) + CR_O + g * DP;
+    const uint32_t t_lane = tmem + (static_cast<uint32_t>(32 * k) << 16);
+    const uint32_t t_s = t_lane + CR_S + g * 128, t_o = t_lane + CR_O + g * DP;
     const float a = p.scale2;
-    int n = 0, t = 0;  // chunks and pieces of this half
+    // This half's chunks; before x: each half's pieces, and those that the second handed over.
+    int n = 0, pi = 0, t[2] = {0, 0}, u = 0;
     CrossPiece x;
-    for (int pi = 0; next_piece(pi, x); ++pi) {
+    while (next_piece(pi, x, true)) {
       const bool two = x.rows > CR_HALF;
-      const int step = two ? 1 : 2, chunks = x.cn - x.c0;
-      float m = -INFINITY, l = 0.f;
-      int d = two ? 0 : g;
-      if (d >= chunks) continue;
+      const int step = two ? 1 : 2, d0 = two ? 0 : g, chunks = x.cn - x.c0;
+      // (a row that is not there has weights of 0)
+      float m = (two ? g * CR_HALF : 0) + r < x.rows ? -INFINITY : INFINITY, l = 0.f;
 #pragma unroll 1
-      for (; d < chunks; d += step, ++n) {
+      for (int d = d0; d < chunks; d += step, ++n) {
         const int lim = x.len - (x.c0 + d) * AT_CHUNK;
         wait_warp(&sready[g], n & 1, ERR_KV8_S_WAIT);
         tc_fence_after();
         if (lim < AT_CHUNK) mask_columns(t_s, lim);
-        // 1. the row's largest score
-        float top = -INFINITY;
-        {
-          float s[2][16];  // (a block is read while the one before is worked on)
-          tmem_ld16_begin(t_s, s[0]);
-          auto look = [&](int w0, float* now, float* next) {
-            tmem_ld_end(now);
-            if (w0 + 16 < AT_CHUNK) tmem_ld16_begin(t_s + w0 + 16, next);
-            float big = fmaxf(now[0], now[1]);
+        float z[4][32];
 #pragma unroll
-            for (int e = 2; e < 16; e += 2) big = max3(big, now[e], now[e + 1]);
-            top = fmaxf(top, big);
-          };
-#pragma unroll 1
-          for (int w0 = 0; w0 < AT_CHUNK; w0 += 32) {
-            look(w0, s[0], s[1]);
-            look(w0 + 16, s[1], s[0]);
-          }
+        for (int w = 0; w < 4; ++w) tmem_ld32_begin(t_s + 32 * w, z[w]);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) tmem_ld32_end(z[w]);
+        // 1. the row's largest score
+        float big[4];
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          big[w] = fmaxf(z[w][0], z[w][1]);
+#pragma unroll
+          for (int e = 2; e < 32; e += 2) big[w] = max3(big[w], z[w][e], z[w][e + 1]);
         }
-        top *= a;  // (positive)
+        const float top = max3(fmaxf(big[0], big[1]), big[2], big[3]) * a;  // (a is positive)
         const bool anew = top - m > CR_RAISE || m == -INFINITY;
         if (__any_sync(FULL_MASK, anew)) {
           const float to = fmaxf(top, m), f = to == -INFINITY || l == 0.f ? 1.f : ex2(m - to);
           m = to;
           l *= f;
-          if (d >= step) scale_outputs<DP>(t_o, f);  // (the products of the chunks before are done)
+          if (d > d0) scale_outputs<DP>(t_o, f);  // (the products of the chunks before were done ahead of S)
         }
         const float nref = m == -INFINITY ? 0.f : -m;
         const float2 a2 = make_float2(a, a), b2 = make_float2(nref, nref);
-        // 2. the weights, over the scores that have been read (16 columns of pairs for 32 of S)
-        float z[32];
+        // 2. the weights, in the scores' place (16 columns of pairs for 32)
         float2 sum[2] = {make_float2(l, 0.f), make_float2(0.f, 0.f)};
-        tmem_ld32_begin(t_s, z);
-#pragma unroll 1
-        for (int w0 = 0; w0 < AT_CHUNK; w0 += 32) {
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
           uint32_t h[16];
-          tmem_ld32_end(z);
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            const float2 y = __ffma2_rn(make_float2(z[2 * e], z[2 * e + 1]), a2, b2);
-            const float2 w = make_float2(ex2(y.x), ex2(y.y));
-            sum[e & 1] = __fadd2_rn(sum[e & 1], w);
-            const __nv_bfloat162 v = __floats2bfloat162_rn(w.x, w.y);
-            h[e] = *reinterpret_cast<const uint32_t*>(&v);
+            const float2 y = __ffma2_rn(make_float2(z[w][2 * e], z[w][2 * e + 1]), a2, b2);
+            const float2 v = make_float2(ex2(y.x), ex2(y.y));
+            sum[e & 1] = __fadd2_rn(sum[e & 1], v);
+            const __nv_bfloat162 c = __floats2bfloat162_rn(v.x, v.y);
+            h[e] = *reinterpret_cast<const uint32_t*>(&c);
           }
-          if (w0 + 32 < AT_CHUNK) tmem_ld32_begin(t_s + w0 + 32, z);
-          tmem_st8(t_s + w0 / 2, h);
-          tmem_st8(t_s + w0 / 2 + 8, h + 8);
+          tmem_st8(t_s + 16 * w, h);
+          tmem_st8(t_s + 16 * w + 8, h + 8);
         }
         l = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
@@ -532,10 +435,92 @@ __global__ void __launch_bounds__(32 * CR_WARPS, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&pready[g]);
       }
-      s_ml[t & 1][g][r] = make_float2(m, l);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&met[t & 1][g][k]);
-      ++t;
+
+      // The outputs.  Where both halves stand for the same rows, the first one writes them.
+      const bool both = !two && chunks > 1;
+      if (g == 1 && both) {
+        s_ml[u & 1][r] = make_float2(m, l);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&met[u & 1][k]);
+      } else if (d0 < chunks || chunks == 0) {
+        const int row = (two ? g * CR_HALF : 0) + r;
+        const bool there = row < x.rows && (chunks > 0 || two || g == 0);
+        float f0 = 1.f, f1 = 0.f;
+        if (l == 0.f) m = -INFINITY;  // (a NaN stays)
+        if (both) {
+          wait_warp(&met[u & 1][k], (u >> 1) & 1, ERR_KV8_PV_WAIT);
+          const float2 ml = s_ml[u & 1][r];
+          const float top = fmaxf(m, ml.y == 0.f ? -INFINITY : ml.x);
+          f0 = l == 0.f ? 0.f : ex2(m - top);
+          f1 = ml.y == 0.f ? 0.f : ex2(ml.x - top);
+          l = l * f0 + ml.y * f1;
+          m = top;
+          wait_warp(&pvdone[1], t[1] & 1, ERR_KV8_PV_WAIT);
+        }
+        if (chunks > 0) {
+          wait_warp(&pvdone[g], t[g] & 1, ERR_KV8_PV_WAIT);
+          tc_fence_after();
+        }
+        if (x.whole) {
+          const float inv = l == 0.f ? 0.f : 1.f / l;
+          f0 *= inv;
+          f1 *= inv;
+        }
+        const int i = there ? (x.row0 + row) / p.group : 0, j = there ? x.row0 + row - i * p.group : 0;
+        const int64_t at = (x.q0 + i) * p.q_heads + int64_t(x.h) * p.group + j;
+        float* part = p.part + int64_t(x.slot) * CR_ROWS * (DP + 2);
+#pragma unroll 1
+        for (int w0 = 0; w0 < DP; w0 += 32) {
+          float o[32];
+          if (chunks > 0) {
+            tmem_ld32_begin(t_o + w0, o);
+            tmem_ld32_end(o);
+          }
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = chunks > 0 ? o[e] * f0 : 0.f;
+          if (both) {
+            float z[32];
+            tmem_ld32_begin(t_lane + CR_O + DP + w0, z);
+            tmem_ld32_end(z);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = fmaf(z[e], f1, o[e]);
+          }
+          if (w0 + 32 == DP && chunks > 0) {  // O has been read
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(&left[g]);
+              if (both) mbar_arrive(&left[1]);
+            }
+          }
+          if (there && x.whole) {
+            uint4* dst = reinterpret_cast<uint4*>(p.out + at * p.D + w0);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              uint32_t h[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const __nv_bfloat162 v = __floats2bfloat162_rn(o[8 * q + 2 * e], o[8 * q + 2 * e + 1]);
+                h[e] = *reinterpret_cast<const uint32_t*>(&v);
+              }
+              if (w0 + 8 * q < p.D) dst[q] = make_uint4(h[0], h[1], h[2], h[3]);
+            }
+          } else if (there) {
+            float4* dst = reinterpret_cast<float4*>(part + row * DP + w0);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          }
+        }
+        if (there && !x.whole) {
+          part[CR_ROWS * DP + row] = m;
+          part[CR_ROWS * DP + CR_ROWS + row] = l;
+        } else if (there && p.lse) {
+          p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * LN2_F;
+        }
+      }
+      t[0] += chunks > 0;
+      t[1] += chunks > (two ? 0 : 1);
+      u += both;
     }
   }
   tc_fence_before();
@@ -575,14 +560,15 @@ const char* rows_error(const void* x, int64_t tok, int64_t head) {
   return nullptr;
 }
 
-// Boxes of 128 states of one head, 64 values wide; what lies behind the head dimension reads as zeros.
-cudaError_t state_map(CUtensorMap* tm, const void* x, int D, int heads, int64_t total, int64_t tok, int64_t head) {
+// Boxes of 128 rows, `group` heads of 128 / group tokens, 64 values wide; what lies behind the head dimension
+// reads as zeros.
+cudaError_t rows_map(CUtensorMap* tm, const void* x, int D, int heads, int64_t total, int64_t tok, int64_t head, int group) {
   auto fn = encode_fn();
   if (!fn) return cudaErrorInvalidValue;
   const cuuint64_t dims[3] = {cuuint64_t(D), cuuint64_t(heads), cuuint64_t(total)};
   // (a dimension of one has no stride of its own)
   const cuuint64_t strides[2] = {cuuint64_t(heads > 1 ? head : D) * 2, cuuint64_t(total > 1 ? tok : D) * 2};
-  const cuuint32_t box[3] = {64, 1, AT_CHUNK}, estr[3] = {1, 1, 1};
+  const cuuint32_t box[3] = {64, cuuint32_t(group), cuuint32_t(AT_CHUNK / group)}, estr[3] = {1, 1, 1};
   return fn(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(x), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
              ? cudaSuccess
@@ -590,12 +576,12 @@ cudaError_t state_map(CUtensorMap* tm, const void* x, int D, int heads, int64_t 
 }
 
 template <int DP>
-cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const CrossParams& p, cudaStream_t stream) {
+cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CrossParams& p, cudaStream_t stream) {
   constexpr int smem = CrossShape<DP>::SMEM;
   const int grid = device_sm_count();
   cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void*>(cross_attention_kernel<DP>), smem);
   if (e != cudaSuccess) return e;
-  cross_attention_kernel<DP><<<grid, 32 * CR_WARPS, smem, stream>>>(tk, tv, p);
+  cross_attention_kernel<DP><<<grid, 32 * CR_WARPS, smem, stream>>>(tq, tk, tv, p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   PdlScope pdl(true);
@@ -666,11 +652,15 @@ lilicorr_status lilicorr_cross_attention(const void* q, int64_t q_token_stride, 
   p.out = static_cast<__nv_bfloat16*>(out);
   p.lse = lse;
   p.part = static_cast<float*>(workspace);
-  CUtensorMap tk, tv;
-  cudaError_t e = state_map(&tk, k, head_dim, kv_heads, total_kv, k_token_stride, k_head_stride);
-  if (e == cudaSuccess) e = state_map(&tv, v, head_dim, kv_heads, total_kv, v_token_stride, v_head_stride);
+  CUtensorMap tq{}, tk, tv;
+  cudaError_t e = rows_map(&tk, k, head_dim, kv_heads, total_kv, k_token_stride, k_head_stride, 1);
+  if (e == cudaSuccess) e = rows_map(&tv, v, head_dim, kv_heads, total_kv, v_token_stride, v_head_stride, 1);
   if (e != cudaSuccess) return fail(LILICORR_ERR_INVALID_ARG, "lilicorr_cross_attention: no tensor map for these strides");
-  e = head_dim <= 64 ? launch<64>(tk, tv, p, static_cast<cudaStream_t>(stream)) : launch<128>(tk, tv, p, static_cast<cudaStream_t>(stream));
+  // q through a map too where tiles begin with a group's first head (else, or with a negative scale, or rows
+  // that overlap, by copies of 16 bytes)
+  p.q_map = AT_CHUNK % p.group == 0 && !p.flip && (q_heads == 1 || q_head_stride >= head_dim) && (total == 1 || q_token_stride >= head_dim) &&
+            rows_map(&tq, q, head_dim, q_heads, total, q_token_stride, q_head_stride, p.group) == cudaSuccess;
+  e = head_dim <= 64 ? launch<64>(tq, tk, tv, p, static_cast<cudaStream_t>(stream)) : launch<128>(tq, tk, tv, p, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return fail(LILICORR_ERR_CUDA, cudaGetErrorString(e));
   return LILICORR_OK;
 }
