@@ -143,8 +143,8 @@ __global__ void __launch_bounds__(32 * CR_WARPS, 1)
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(cr_raw) + 1023) & ~uintptr_t(1023));
   // sready, pready: of each half, a phase for each of its chunks; pvdone, left: for each piece that it has
   // chunks of; met: for each piece that the second half hands over, by turns.
-  __shared__ __align__(8) uint64_t kfull[KS], kempty[KS], vfull[VS], vempty[VS], sready[2], pready[2], pvdone[2], qready[2], qfree[2],
-      left[2], pc_full[CR_PIECES], pc_empty[CR_PIECES], met[2][4];
+  __shared__ __align__(8) uint64_t kfull[KS], kempty[KS], vfull[VS], vempty[VS], sready[2], pready[2][2], pvdone[2], qready[2], qfree[2],
+      left[2], pc_full[CR_PIECES], pc_empty[CR_PIECES], met[2][4], turn[2][4];
   __shared__ CrossPiece s_piece[CR_PIECES];
   __shared__ float2 s_ml[2][CR_HALF];  // a row's maximum and sum, handed over
   __shared__ uint32_t s_tmem;
@@ -155,9 +155,9 @@ __global__ void __launch_bounds__(32 * CR_WARPS, 1)
     for (int i = 0; i < KS; ++i) { mbar_init(&kfull[i], 1); mbar_init(&kempty[i], 2); }
     for (int i = 0; i < VS; ++i) { mbar_init(&vfull[i], 1); mbar_init(&vempty[i], 2); }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sready[i], 1); mbar_init(&pready[i], 4); mbar_init(&pvdone[i], 1);
+      mbar_init(&sready[i], 1); mbar_init(&pready[0][i], 4); mbar_init(&pready[1][i], 4); mbar_init(&pvdone[i], 1);
       mbar_init(&qready[i], 1); mbar_init(&qfree[i], 2); mbar_init(&left[i], 4);
-      for (int j = 0; j < 4; ++j) mbar_init(&met[i][j], 1);
+      for (int j = 0; j < 4; ++j) { mbar_init(&met[i][j], 1); mbar_init(&turn[i][j], 1); }
     }
     for (int i = 0; i < CR_PIECES; ++i) { mbar_init(&pc_full[i], 1); mbar_init(&pc_empty[i], CR_READERS); }
     fence_mbar_init();
@@ -271,58 +271,75 @@ __global__ void __launch_bounds__(32 * CR_WARPS, 1)
       const uint64_t q = d_q + (slot * T >> 4);
       // (a half without a chunk waits too: what it leaves below is then of this use of the slot)
       bool ok = wait_warp(&qready[slot], ((qs + (two ? g : 0)) >> 1) & 1, ERR_KV8_S_WAIT);
-      if (d0 < chunks) {
-        if (t++ > 0) ok = wait_warp(&left[g], t & 1, ERR_KV8_PV_WAIT) && ok;  // the piece before has left O
-      }
-#pragma unroll 1
-      for (int d = 0; d < chunks; ++d, ++it) {
-        const int sk = it % KS, sv = it % VS;
-        ok = wait_warp(&kfull[sk], (it / KS) & 1, ERR_KV8_FULL_WAIT) && ok;
-        if (!two && (d & 1) != g) {  // the other half's
-          if (lane == 0) mbar_arrive(&kempty[sk]);
-          wait_warp(&vfull[sv], (it / VS) & 1, ERR_KV8_PV_WAIT);
-          if (lane == 0) mbar_arrive(&vempty[sv]);
-          continue;
-        }
+      auto keys = [&](int d) {  // waits for chunk d's keys
+        const int i = it + d;
+        ok = wait_warp(&kfull[i % KS], (i / KS) & 1, ERR_KV8_FULL_WAIT) && ok;
+        if (!two && (d & 1) != g && lane == 0) mbar_arrive(&kempty[i % KS]);  // the other half's
+      };
+      auto scores = [&](int d) {
+        const int i = (it + d) % KS;
         if (ok) {
           tc_fence_after();
-          const uint64_t k = d_k + (sk * T >> 4);
+          const uint64_t k = d_k + (i * T >> 4);
 #pragma unroll
-          for (int i = 0; i < DP / 16; ++i) {
-            const int at = (i / 4) * (SUB >> 4) + (i % 4) * 2;
-            mma_f16(t_s, q + at, k + at, ID_S, i > 0);
+          for (int e = 0; e < DP / 16; ++e) {
+            const int at = (e / 4) * (SUB >> 4) + (e % 4) * 2;
+            mma_f16(t_s, q + at, k + at, ID_S, e > 0);
           }
         }
         tc_commit(&sready[g]);
-        tc_commit(&kempty[sk]);
+        tc_commit(&kempty[i]);
         if (d + step >= chunks) {  // q has been read (the slot waits for both halves)
           tc_commit(&qfree[slot]);
           if (two) tc_commit(&qfree[slot]);
         }
+      };
+      for (int d = 0; d <= d0 && d < chunks; ++d) keys(d);
+      if (d0 < chunks) scores(d0);
+      else if (lane == 0) mbar_arrive(&qfree[slot]);
+      // What a chunk's products need besides its weights, and the keys of the half's next one, is waited for first.
+#pragma unroll 1
+      for (int d = 0; d < chunks; ++d) {
+        const int i = it + d, sv = i % VS;
+        ok = wait_warp(&vfull[sv], (i / VS) & 1, ERR_KV8_PV_WAIT) && ok;
+        if (!two && (d & 1) != g) {
+          if (lane == 0) mbar_arrive(&vempty[sv]);
+          continue;
+        }
         const int rem = min(AT_CHUNK, x.len - (x.c0 + d) * AT_CHUNK), steps = (rem + 15) / 16;
-        ok = wait_warp(&vfull[sv], (it / VS) & 1, ERR_KV8_PV_WAIT) && ok;
         if (rem & 15) {  // rows behind the last state: weights of 0, which no NaN may meet
           uint8_t* v = sm + S::OFF_V + sv * T + rem * 128;
           const int all = (steps * 16 - rem) * 8;
-          for (int i = lane; i < all; i += 32)
+          for (int e = lane; e < all; e += 32)
 #pragma unroll
-            for (int j = 0; j < DP / 64; ++j) *reinterpret_cast<uint4*>(v + j * SUB + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+            for (int j = 0; j < DP / 64; ++j) *reinterpret_cast<uint4*>(v + j * SUB + e * 16) = make_uint4(0u, 0u, 0u, 0u);
           fence_async_smem();
           __syncwarp();
         }
-        ok = wait_warp(&pready[g], n & 1, ERR_KV8_PV_WAIT) && ok;
-        if (ok) {
-          tc_fence_after();
-          const uint64_t v = d_v + (sv * T >> 4);
-          // (16 states further: 8 columns of P; 16 rows of V)
+        // (not so where the halves take turns: the keys are two chunks away, on their way from memory)
+        if (two && d + 1 < chunks) keys(d + 1);
+        if (d == d0 && t++ > 0) ok = wait_warp(&left[g], t & 1, ERR_KV8_PV_WAIT) && ok;  // the piece before has left O
+        const uint64_t v = d_v + (sv * T >> 4);
+#pragma unroll 1
+        for (int part = 0; part < 2; ++part) {  // the weights of 64 states each
+          ok = wait_warp(&pready[part][g], n & 1, ERR_KV8_PV_WAIT) && ok;
+          if (ok) {
+            tc_fence_after();
+            // (16 states further: 8 columns of P; 16 rows of V)
 #pragma unroll 4
-          for (int i = 0; i < steps; ++i) mma_f16_ts(t_o, t_s + 8 * i, v + i * 128, ID_O, i > 0 || d > d0);
+            for (int e = 4 * part; e < min(steps, 4 * part + 4); ++e) mma_f16_ts(t_o, t_s + 8 * e, v + e * 128, ID_O, e > 0 || d > d0);
+          }
         }
-        if (d + step >= chunks) tc_commit(&pvdone[g]);
-        tc_commit(&vempty[sv]);
+        if (!two) {
+          tc_commit(&vempty[sv]);
+          for (int e = d + 1; e <= d + step && e < chunks; ++e) keys(e);
+        }
+        if (d + step < chunks) scores(d + step);
+        else tc_commit(&pvdone[g]);
+        if (two) tc_commit(&vempty[sv]);
         ++n;
       }
-      if (d0 >= chunks && lane == 0) mbar_arrive(&qfree[slot]);
+      it += chunks;
       qs += two ? 2 : 1;
     }
   } else if (warp == CR_Q) {
@@ -377,18 +394,30 @@ __global__ void __launch_bounds__(32 * CR_WARPS, 1)
     const uint32_t t_s = t_lane + CR_S + g * 128, t_o = t_lane + CR_O + g * DP;
     const float a = p.scale2;
     // This half's chunks; before x: each half's pieces, and those that the second handed over.
-    int n = 0, pi = 0, t[2] = {0, 0}, u = 0;
+    int n = 0, pi = 0, t[2] = {0, 0}, u = 0, v = 0;
     CrossPiece x;
     while (next_piece(pi, x, true)) {
       const bool two = x.rows > CR_HALF;
       const int step = two ? 1 : 2, d0 = two ? 0 : g, chunks = x.cn - x.c0;
+      const bool any = (two ? g * CR_HALF : 0) + 32 * k < x.rows;  // of the warp's rows
       // (a row that is not there has weights of 0)
       float m = (two ? g * CR_HALF : 0) + r < x.rows ? -INFINITY : INFINITY, l = 0.f;
 #pragma unroll 1
       for (int d = d0; d < chunks; d += step, ++n) {
         const int lim = x.len - (x.c0 + d) * AT_CHUNK;
+        // Where both halves take every chunk they take turns, so that one's products run beside the other's weights.
+        if (two && (g == 1 || v > 0)) wait_warp(&turn[1 - g][k], (v - (g == 0)) & 1, ERR_KV8_S_WAIT);
         wait_warp(&sready[g], n & 1, ERR_KV8_S_WAIT);
         tc_fence_after();
+        if (!any) {  // rows that are not there: weights of any value
+          if (lane == 0) {
+            mbar_arrive(&pready[0][g]);
+            mbar_arrive(&pready[1][g]);
+            if (two) mbar_arrive(&turn[g][k]);
+          }
+          v += two;
+          continue;
+        }
         if (lim < AT_CHUNK) mask_columns(t_s, lim);
         float z[4][32];
 #pragma unroll
@@ -428,12 +457,18 @@ __global__ void __launch_bounds__(32 * CR_WARPS, 1)
           }
           tmem_st8(t_s + 16 * w, h);
           tmem_st8(t_s + 16 * w + 8, h + 8);
+          if (w & 1) {
+            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&pready[w >> 1][g]);
+          }
         }
         l = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&pready[g]);
+        if (two) {
+          if (lane == 0) mbar_arrive(&turn[g][k]);
+          ++v;
+        }
       }
 
       // The outputs.  Where both halves stand for the same rows, the first one writes them.
@@ -570,7 +605,7 @@ cudaError_t rows_map(CUtensorMap* tm, const void* x, int D, int heads, int64_t t
   const cuuint64_t strides[2] = {cuuint64_t(heads > 1 ? head : D) * 2, cuuint64_t(total > 1 ? tok : D) * 2};
   const cuuint32_t box[3] = {64, cuuint32_t(group), cuuint32_t(AT_CHUNK / group)}, estr[3] = {1, 1, 1};
   return fn(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(x), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+            CU_TENSOR_MAP_SWIZZLE_128B, D <= 64 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
              ? cudaSuccess
              : cudaErrorInvalidValue;
 }
