@@ -80,7 +80,8 @@ struct CrossShape {
   static constexpr int QS = 2;                      // halves of q
   static constexpr int OFF_V = KS * T;
   static constexpr int OFF_Q = OFF_V + VS * T;
-  static constexpr int SMEM = 1024 + OFF_Q + QS * T;
+  static constexpr int OFF_ST = OFF_Q + QS * T;     // 32 outputs of 32 rows for each softmax warp
+  static constexpr int SMEM = 1024 + OFF_ST + 8 * 2048;
 };
 // Warps: 0 to 3 and 4 to 7 the halves' softmax; then loads, each half's products, q.
 constexpr int CR_LOAD = 8, CR_MMA = 9, CR_Q = 11, CR_WARPS = 12, CR_READERS = CR_WARPS - 1, CR_PIECES = 6;
@@ -178,7 +179,7 @@ __global__ void __launch_bounds__(32 * CR_WARPS, 1)
   // roles' loops end.
   auto wait_warp = [&](uint64_t* bar, uint32_t parity, uint32_t site) -> bool {
 #pragma unroll 1
-    for (uint32_t i = 0; !__all_sync(FULL_MASK, try_wait_us(bar, parity)); ++i)
+    for (uint32_t i = 0; !__all_sync(FULL_MASK, mbar_try_wait(bar, parity)); ++i)
       if (__any_sync(FULL_MASK, i == WAIT_TRIES || s_fail != 0)) {
         if (s_fail == 0) s_fail = site;
         return false;
@@ -282,13 +283,9 @@ __global__ void __launch_bounds__(32 * CR_WARPS, 1)
           tc_fence_after();
           const uint64_t k = d_k + (i * T >> 4);
 #pragma unroll
-          for (int e = 0; e < DP / 16; ++e) {
-            const int at = (e / 4) * (SUB >> 4) + (e % 4) * 2;
-            mma_f16(t_s, q + at, k + at, ID_S, e > 0);
-          }
+          for (int e = 0; e < DP / 64; ++e) mma_f16_x4(t_s, q + e * (SUB >> 4), k + e * (SUB >> 4), ID_S, e > 0);
         }
-        tc_commit(&sready[g]);
-        tc_commit(&kempty[i]);
+        tc_commit2(&sready[g], &kempty[i]);
         if (d + step >= chunks) {  // q has been read (the slot waits for both halves)
           tc_commit(&qfree[slot]);
           if (two) tc_commit(&qfree[slot]);
@@ -319,16 +316,23 @@ __global__ void __launch_bounds__(32 * CR_WARPS, 1)
         // (not so where the halves take turns: the keys are two chunks away, on their way from memory)
         if (two && d + 1 < chunks) keys(d + 1);
         if (d == d0 && t++ > 0) ok = wait_warp(&left[g], t & 1, ERR_KV8_PV_WAIT) && ok;  // the piece before has left O
+        // 64 states at a time (16 further: 8 columns of P, 16 rows of V)
         const uint64_t v = d_v + (sv * T >> 4);
+        ok = wait_warp(&pready[0][g], n & 1, ERR_KV8_PV_WAIT) && ok;
+        tc_fence_after();
+        if (ok && steps >= 4) {
+          mma_f16_ts4(t_o, t_s, v, ID_O, d > d0);
+        } else if (ok) {
 #pragma unroll 1
-        for (int part = 0; part < 2; ++part) {  // the weights of 64 states each
-          ok = wait_warp(&pready[part][g], n & 1, ERR_KV8_PV_WAIT) && ok;
-          if (ok) {
-            tc_fence_after();
-            // (16 states further: 8 columns of P; 16 rows of V)
-#pragma unroll 4
-            for (int e = 4 * part; e < min(steps, 4 * part + 4); ++e) mma_f16_ts(t_o, t_s + 8 * e, v + e * 128, ID_O, e > 0 || d > d0);
-          }
+          for (int e = 0; e < steps; ++e) mma_f16_ts(t_o, t_s + 8 * e, v + e * 128, ID_O, e > 0 || d > d0);
+        }
+        ok = wait_warp(&pready[1][g], n & 1, ERR_KV8_PV_WAIT) && ok;
+        tc_fence_after();
+        if (ok && steps == 8) {
+          mma_f16_ts4(t_o, t_s + 32, v + 512, ID_O, true);
+        } else if (ok) {
+#pragma unroll 1
+          for (int e = 4; e < steps; ++e) mma_f16_ts(t_o, t_s + 8 * e, v + e * 128, ID_O, true);
         }
         if (!two) {
           tc_commit(&vempty[sv]);
@@ -393,6 +397,7 @@ __global__ void __launch_bounds__(32 * CR_WARPS, 1)
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(32 * k) << 16);
     const uint32_t t_s = t_lane + CR_S + g * 128, t_o = t_lane + CR_O + g * DP;
     const float a = p.scale2;
+    uint8_t* stage = sm + S::OFF_ST + warp * 2048;
     // This half's chunks; before x: each half's pieces, and those that the second handed over.
     int n = 0, pi = 0, t[2] = {0, 0}, u = 0, v = 0;
     CrossPiece x;
@@ -405,8 +410,6 @@ __global__ void __launch_bounds__(32 * CR_WARPS, 1)
 #pragma unroll 1
       for (int d = d0; d < chunks; d += step, ++n) {
         const int lim = x.len - (x.c0 + d) * AT_CHUNK;
-        // Where both halves take every chunk they take turns, so that one's products run beside the other's weights.
-        if (two && (g == 1 || v > 0)) wait_warp(&turn[1 - g][k], (v - (g == 0)) & 1, ERR_KV8_S_WAIT);
         wait_warp(&sready[g], n & 1, ERR_KV8_S_WAIT);
         tc_fence_after();
         if (!any) {  // rows that are not there: weights of any value
@@ -424,6 +427,8 @@ __global__ void __launch_bounds__(32 * CR_WARPS, 1)
         for (int w = 0; w < 4; ++w) tmem_ld32_begin(t_s + 32 * w, z[w]);
 #pragma unroll
         for (int w = 0; w < 4; ++w) tmem_ld32_end(z[w]);
+        // Where both halves take every chunk they take turns, so that one's products run beside the other's weights.
+        if (two && (g == 1 || v > 0)) wait_warp(&turn[1 - g][k], (v - (g == 0)) & 1, ERR_KV8_S_WAIT);
         // 1. the row's largest score
         float big[4];
 #pragma unroll
@@ -528,8 +533,8 @@ __global__ void __launch_bounds__(32 * CR_WARPS, 1)
               if (both) mbar_arrive(&left[1]);
             }
           }
-          if (there && x.whole) {
-            uint4* dst = reinterpret_cast<uint4*>(p.out + at * p.D + w0);
+          if (x.whole) {
+            // through shared memory, so that four lanes write 64 bytes of a row
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               uint32_t h[4];
@@ -538,8 +543,18 @@ __global__ void __launch_bounds__(32 * CR_WARPS, 1)
                 const __nv_bfloat162 v = __floats2bfloat162_rn(o[8 * q + 2 * e], o[8 * q + 2 * e + 1]);
                 h[e] = *reinterpret_cast<const uint32_t*>(&v);
               }
-              if (w0 + 8 * q < p.D) dst[q] = make_uint4(h[0], h[1], h[2], h[3]);
+              *reinterpret_cast<uint4*>(stage + lane * 64 + ((q ^ (lane >> 1 & 3)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
             }
+            __syncwarp();
+            const int q = lane & 3;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int rr = 8 * e + (lane >> 2);
+              const int64_t to = __shfl_sync(FULL_MASK, at, rr);
+              const uint4 v = *reinterpret_cast<const uint4*>(stage + rr * 64 + ((q ^ (rr >> 1 & 3)) << 4));
+              if (__shfl_sync(FULL_MASK, static_cast<int>(there), rr) && w0 + 8 * q < p.D) *reinterpret_cast<uint4*>(p.out + to * p.D + w0 + 8 * q) = v;
+            }
+            __syncwarp();
           } else if (there) {
             float4* dst = reinterpret_cast<float4*>(part + row * DP + w0);
 #pragma unroll
