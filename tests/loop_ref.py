@@ -13,8 +13,7 @@ def allowed(mask_row, v: int) -> bool:
 
 def adjust(x, history=None, seen=None, counted_from=None, repetition=None, presence=None, frequency=None, bias_ids=None,
            bias_values=None, mask=None, mask_index=None):
-    """(values, magnitudes) of logits x [rows, V] in 64 bits: the sums' terms are off by 2^-50 of the
-    magnitudes at most, and the result is rounded once on top."""
+    """(values, sums of the terms' magnitudes) of logits x [rows, V] in 64 bits."""
     cpu = lambda t: None if t is None else t.cpu()  # noqa: E731
     history, seen, counted_from, repetition, presence, frequency, bias_ids, bias_values, mask, mask_index = map(
         cpu, (history, seen, counted_from, repetition, presence, frequency, bias_ids, bias_values, mask, mask_index))

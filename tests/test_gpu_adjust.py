@@ -1,7 +1,10 @@
 """Penalties, biases and masks on logits against the float64 form in loop_ref.
 
-Tolerance: the arithmetic is in 64 bits, off by 2^-50 of the terms' magnitudes at most, and is rounded
-once, by half a step of the type; a token that nothing touches is bit for bit the logit."""
+Tolerance: a value is kept as a pair of floats.  A product or quotient is a pair, off by 2^-47 of itself (its
+low part, 2^-24 of it, is rounded, and so is the quotient's remainder times a reciprocal); a sum of pairs
+adds their low parts, each at most 2^-23 of the sum so far, with two roundings of 2^-24: 2^-46 of the terms'
+magnitudes for each of the terms.  Then it is rounded once, by half a step of the type.  A token that nothing
+touches is bit for bit the logit."""
 import math
 
 import pytest
@@ -65,11 +68,14 @@ def make(rows, V, dtype, groups, cap, n_bias, masks, seed):
 def check(got, x, kw):
     want, mag = R.adjust(x, **kw)
     y = got.cpu().double()
-    inf = torch.isinf(want)
-    assert torch.equal(y[inf], want[inf])
+    nan = want.isnan()  # (what passes the type's largest is infinite, in 64 bits it need not be)
+    assert torch.equal(y.isnan(), nan)
+    inf = torch.isinf(want.to(x.dtype)) | nan
+    assert torch.equal(y[inf & ~nan], want.to(x.dtype).double()[inf & ~nan])
     assert not torch.isinf(y[~inf]).any()
     half = torch.finfo(x.dtype).eps / 2
-    assert ((y - want).abs()[~inf] <= (half * want.abs() + 2.0 ** -50 * mag + 2.0 ** -133)[~inf]).all()
+    terms = 4 + (kw["bias_ids"].shape[1] if "bias_ids" in kw else 0)
+    assert ((y - want).abs()[~inf] <= (half * want.abs() + terms * 2.0 ** -46 * mag + 2.0 ** -133)[~inf]).all()
     same = (want == x.cpu().double()) & ~inf  # what nothing moved
     assert torch.equal(got.cpu()[same], x.cpu()[same])
 
@@ -141,7 +147,7 @@ def test_adjust_infinities_nan_and_the_lowest_value(lc, dtype):
 
 
 def test_adjust_cancelling_terms_keep_their_bits(lc):
-    """A count of thousands against a bias of the same size: 64-bit arithmetic, one rounding."""
+    """A count of thousands against a bias of the same size, which leave 2^-10 of themselves: one rounding."""
     x = torch.tensor([[1.0009765625, 2.0]], device="cuda")
     hist = torch.zeros(1, 30000, dtype=torch.int32, device="cuda")
     freq = torch.tensor([0.1], device="cuda")
@@ -150,8 +156,35 @@ def test_adjust_cancelling_terms_keep_their_bits(lc):
     kw = dict(history=hist, seen=seen, frequency=freq, bias_ids=torch.zeros(1, 1, dtype=torch.int32, device="cuda"), bias_values=bias)
     got = lc.adjust_logits(x, out=torch.empty_like(x), **kw)
     want = float(x[0, 0]) - float(freq[0].double()) * 30000 + 3000.0
-    assert abs(float(got[0, 0]) - want) <= 2.0 ** -24 * abs(want) + 2.0 ** -40
+    assert abs(float(got[0, 0]) - want) <= 2.0 ** -24 * abs(want) + 5 * 2.0 ** -46 * 6001
     assert float(got[0, 1]) == 2.0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_adjust_values_near_the_ends_of_the_type(lc, dtype):
+    """Products that overflow, sums that come back from there, subnormals, exact zeros, odd penalties."""
+    V = 64
+    x = torch.zeros(4, V, device="cuda")
+    x[0] = torch.linspace(-3.3e38, 3.3e38, V)
+    x[1] = torch.linspace(-1, 1, V) * 1e-38
+    x[2] = 5.0
+    x[3] = torch.linspace(-9, 9, V)
+    x = x.to(dtype)
+    hist = torch.arange(V, dtype=torch.int32, device="cuda").expand(4, V).contiguous()
+    kw = dict(history=hist, seen=torch.full((4,), V, dtype=torch.int32, device="cuda"),
+              repetition=torch.tensor([1.5, 1.5, 1.0, 1e-3], device="cuda"), presence=torch.tensor([-2e38, 0, 5.0, 0], device="cuda"),
+              bias_ids=hist[:, :8].contiguous(), bias_values=torch.full((4, 8), 0.25, device="cuda"))
+    check(lc.adjust_logits(x, out=torch.empty_like(x), **kw), x, kw)
+
+
+def test_adjust_ties_of_bf16_are_told_by_the_whole_sum(lc):
+    """Sums a hair above and below a bf16 tie, by less than a float's step: rounded to their own side."""
+    tie = 1 + 2.0 ** -8  # between 1 and 1 + 2^-7
+    x = torch.full((3, 2), 1.0, device="cuda").to(torch.bfloat16)
+    ids = torch.zeros(3, 2, dtype=torch.int32, device="cuda")
+    bias = torch.tensor([[2.0 ** -8, 2.0 ** -40], [2.0 ** -8, -2.0 ** -40], [2.0 ** -8, 0.0]], device="cuda")
+    got = lc.adjust_logits(x, bias_ids=ids, bias_values=bias)
+    assert tie == 1.00390625 and got[:, 0].tolist() == [1.0078125, 1.0, 1.0] and got[:, 1].tolist() == [1.0] * 3
 
 
 def test_adjust_rows_out_of_range_are_left_out_and_reported(lc):
