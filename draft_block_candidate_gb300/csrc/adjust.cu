@@ -22,10 +22,16 @@ static __device__ uint32_t g_err_adjust;
 // way; writes the logits with the mask; and then writes the touched tokens over, each lane those among its
 // own words, one at a time, so that the warp's 64-bit arithmetic is full.  Where there is only a mask a CTA
 // has no words and takes AJ_SPAN pieces.  In place, what a mask leaves or takes whole is not read.
-constexpr int AJ_THREADS = 256, AJ_WARPS = AJ_THREADS / 32;
+constexpr int AJ_THREADS = 256;
 constexpr int AJ_VECS = 4;                                // vectors of 16 bytes of a lane
 constexpr int AJ_PIECE = AJ_THREADS * AJ_VECS * 16;       // bytes
-constexpr int AJ_SPAN = 4;
+#ifndef AJ_CTAS
+#define AJ_CTAS 6
+#endif
+#ifndef AJ_SPAN_
+#define AJ_SPAN_ 4
+#endif
+constexpr int AJ_SPAN = AJ_SPAN_;
 constexpr int AJ_MAX_BIAS = 1024;
 // a token's word: how often it counts, whether it has a bias, whether it was seen without counting
 constexpr uint32_t AJ_BIAS = 1u << 30, AJ_SEEN = 1u << 31, AJ_COUNT = AJ_BIAS - 1;
@@ -145,8 +151,9 @@ __device__ __forceinline__ uint4 masked(uint4 v, uint32_t bits) {
     uint32_t* q = reinterpret_cast<uint32_t*>(&v);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint32_t b = bits >> (2 * i);
-      const uint32_t keep = (b & 1 ? 0xffffu : 0u) | (b & 2 ? 0xffff0000u : 0u);
+      // two bits to the tops of two bytes, each of which is then spread over a half
+      uint32_t keep;
+      asm("prmt.b32 %0, %1, 0, 0x9988;" : "=r"(keep) : "r"((bits >> (2 * i) & 3) * 0x4080u));
       q[i] = (q[i] & keep) | (0xff80ff80u & ~keep);
     }
     return v;
@@ -193,7 +200,7 @@ struct Piece {
 #pragma unroll
     for (int i = 0; i < AJ_VECS; ++i) {
       const int v = first + i * 32 + lane;
-      if (v < vecs && !(INPLACE && bits[i] == (1u << E) - 1)) *reinterpret_cast<uint4*>(o + head + v * E) = masked<T>(w[i], bits[i]);
+      if (v < vecs && !(INPLACE && bits[i] == (1u << E) - 1)) *reinterpret_cast<uint4*>(o + head + v * E) = m ? masked<T>(w[i], bits[i]) : w[i];
     }
     const int tail = head + vecs * E, ends = head + n - tail;
     if (static_cast<int>(threadIdx.x) < ends) {
@@ -205,11 +212,12 @@ struct Piece {
 };
 
 template <typename T, bool INPLACE, bool TOUCH>
-__global__ void __launch_bounds__(AJ_THREADS) adjust_kernel(const AdjustParams p) {
-  constexpr int TOKENS = AJ_PIECE / sizeof(T), SPAN = TOUCH ? 1 : AJ_SPAN, OWN = TOKENS / AJ_WARPS;
+__global__ void __launch_bounds__(AJ_THREADS, AJ_CTAS) adjust_kernel(const AdjustParams p) {
+  constexpr int TOKENS = AJ_PIECE / sizeof(T), SPAN = TOUCH ? 1 : AJ_SPAN;
   __shared__ __align__(16) uint32_t s_word[TOUCH ? TOKENS : 4];
+  __shared__ uint32_t s_touched[TOUCH ? TOKENS / 32 : 1];  // a bit a token
   __shared__ __align__(16) int s_id[TOUCH ? AJ_MAX_BIAS : 4];
-  const int tid = threadIdx.x, lane = tid & 31;
+  const int tid = threadIdx.x;
   const int64_t r = blockIdx.x / p.pieces;
   const int first = static_cast<int>(blockIdx.x - r * p.pieces) * TOKENS * SPAN;
   const int64_t h = r / p.per;
@@ -243,39 +251,55 @@ __global__ void __launch_bounds__(AJ_THREADS) adjust_kernel(const AdjustParams p
     const int t0 = first, n = min(TOKENS, p.V - t0);
     const Piece<T, INPLACE> piece(x + t0, o + t0, m, words, t0, n);
     for (int i = tid * 4; i < n; i += AJ_THREADS * 4) *reinterpret_cast<uint4*>(s_word + i) = make_uint4(0u, 0u, 0u, 0u);
+    for (int i = tid; i < TOKENS / 32; i += AJ_THREADS) s_touched[i] = 0;
     // (an id that is no token's is none of the piece's)
     for (int i = tid; i < (p.n_bias + 3) / 4 * 4; i += AJ_THREADS) {
       const int id = i < p.n_bias ? __ldg(p.bias_id + h * p.n_bias + i) : -1;
       s_id[i] = id < t0 || id - t0 >= n ? -1 : id - t0;
     }
     __syncthreads();
-    const int32_t* hist = p.hist + h * p.hist_stride;
-#pragma unroll 8
-    for (int i = tid; i < seen; i += AJ_THREADS) {
-      const int at = __ldg(hist + i) - t0;
-      if (static_cast<uint32_t>(at) < static_cast<uint32_t>(n)) {
+    auto count = [&](int id, int i) {
+      const uint32_t at = static_cast<uint32_t>(id - t0);
+      if (at < static_cast<uint32_t>(n)) {
         if (i >= from) atomicAdd(s_word + at, 1u);
         else atomicOr(s_word + at, AJ_SEEN);
+        atomicOr(s_touched + (at >> 5), 1u << (at & 31));
       }
+    };
+    const int32_t* hist = p.hist + h * p.hist_stride;
+    // (by fours from the first 16-byte boundary on)
+    const int lead = min(seen, static_cast<int>((16 - reinterpret_cast<uintptr_t>(hist) % 16) % 16 / 4)), fours = (seen - lead) / 4;
+    if (tid < lead) count(__ldg(hist + tid), tid);
+    if (tid < seen - lead - 4 * fours) count(__ldg(hist + lead + 4 * fours + tid), lead + 4 * fours + tid);
+#pragma unroll 4
+    for (int f = tid; f < fours; f += AJ_THREADS) {
+      const int i = lead + 4 * f;
+      const int4 q = __ldg(reinterpret_cast<const int4*>(hist + i));
+      count(q.x, i);
+      count(q.y, i + 1);
+      count(q.z, i + 2);
+      count(q.w, i + 3);
     }
     for (int i = tid; i < p.n_bias; i += AJ_THREADS)
-      if (s_id[i] >= 0) atomicOr(s_word + s_id[i], AJ_BIAS);
+      if (s_id[i] >= 0) {
+        atomicOr(s_word + s_id[i], AJ_BIAS);
+        atomicOr(s_touched + (s_id[i] >> 5), 1u << (s_id[i] & 31));
+      }
     piece.write();
     __syncthreads();
-    // the lane's touched tokens: bit j is own + 32 j
-    const int own = (tid >> 5) * OWN + lane;
+    // the touched ones among the lane's 32 tokens that may be taken
     uint32_t todo = 0;
-#pragma unroll
-    for (int j = 0; j < OWN / 32; ++j)
-      if (own + 32 * j < n && s_word[own + 32 * j] != 0) todo |= 1u << j;
+    if (tid < TOKENS / 32) {
+      todo = s_touched[tid];
+      if (m && todo) todo &= __ldg(m + (t0 >> 5) + tid);
+    }
     if (!__any_sync(FULL_MASK, todo != 0)) return;
     Penalties pen{p.rep ? __ldg(p.rep + h) : 1.f, 0.f, 0.f, p.freq ? __ldg(p.freq + h) : 0.f, p.pres ? __ldg(p.pres + h) : 0.f,
                   p.rep != nullptr, s_id, p.bias + h * p.n_bias, p.n_bias};
     pen.inv = 1.f / pen.rho;
     pen.inv_lo = fmaf(-pen.inv, pen.rho, 1.f) * pen.inv;
     for (; todo; todo &= todo - 1) {
-      const int t = own + 32 * (__ffs(todo) - 1);
-      if (m && !allowed(m, t0 + t)) continue;
+      const int t = 32 * tid + __ffs(todo) - 1;
       touch(o + t0 + t, static_cast<float>(x[t0 + t]), s_word[t], t, pen);
     }
   }
