@@ -1,5 +1,7 @@
 // Penalties for repeated tokens, biases and grammar masks on logits, before they are ranked.
+#include <algorithm>
 #include <climits>
+#include <type_traits>
 
 #include "kernels.cuh"
 
@@ -14,27 +16,27 @@ static __device__ uint32_t g_err_adjust;
 // Only the tokens of the history and of the bias list need arithmetic.  They are few, and penalties
 // and biases may all but cancel, so sums are kept as pairs of floats, hi + lo, off by 2^-47 of their
 // terms' magnitudes for each term, and rounded once; where that does not do (values near the ends of
-// the type, or not finite, counts of 2^24 and more) in 64 bits, which are slow on this part (with them
-// throughout, and a quotient for each warp, the large case below took 121 us).
+// the type, or not finite, counts of 2^24 and more) in 64 bits, which are slow on this part.
 //
-// One CTA for each piece of 16 KB of a row.  It counts the history's tokens that lie in its piece in shared
-// memory, a word a token (integer sums: any order gives the same), while the piece's logits are on their
-// way; writes the logits with the mask; and then writes the touched tokens over, each lane those among its
-// own words, one at a time, so that the warp's 64-bit arithmetic is full.  Where there is only a mask a CTA
-// has no words and takes AJ_SPAN pieces.  In place, what a mask leaves or takes whole is not read.
-constexpr int AJ_THREADS = 256;
-constexpr int AJ_VECS = 4;                                // vectors of 16 bytes of a lane
-constexpr int AJ_PIECE = AJ_THREADS * AJ_VECS * 16;       // bytes
-#ifndef AJ_CTAS
-#define AJ_CTAS 6
-#endif
-#ifndef AJ_SPAN_
-#define AJ_SPAN_ 4
-#endif
-constexpr int AJ_SPAN = AJ_SPAN_;
+// One CTA for each piece of 32 KB of a row: it reads the piece (a warp's vectors after one coalesced load of their
+// mask; in place, what a mask leaves or takes whole is not read), works out meanwhile which of the history's tokens
+// lie in the piece and how often they count, writes the piece with its mask, and then the touched tokens over, while
+// their logits are still near.  It goes over the history twice: first each token sets its bit of a bit map of the
+// piece, whose running sums then give every token that is there a place in a list; then each token counts at its
+// place.  Neither pass waits for what its atomic operations find, and all sums are of integers.  Where there is only
+// a mask a kernel without all that does.
+//
+// Tried and dropped (256 rows of 151,936 in bf16 with histories of up to 4,096, 64 biases and 16 grammars): a word for
+// each of a piece's tokens to count in, cleared and searched, 57 us (209 with 64-bit arithmetic and loops with few lanes
+// at work); two kernels, the second a CTA a row for the touched tokens alone, 41 with a table of the ids by their hash
+// and 43 with a bit map of the row: the tokens' logits are read and written one by one once the row has left the L2 cache.
+constexpr int AJ_THREADS = 512;
+constexpr int AJ_VECS = 4;                           // vectors of 16 bytes of a lane
+constexpr int AJ_PIECE = AJ_THREADS * AJ_VECS * 16;  // bytes
 constexpr int AJ_MAX_BIAS = 1024;
-// a token's word: how often it counts, whether it has a bias, whether it was seen without counting
-constexpr uint32_t AJ_BIAS = 1u << 30, AJ_SEEN = 1u << 31, AJ_COUNT = AJ_BIAS - 1;
+#ifndef AJ_CTAS
+#define AJ_CTAS 3
+#endif
 
 struct AdjustParams {
   const void* x;
@@ -53,7 +55,8 @@ struct AdjustParams {
   int64_t mask_stride;
   int n_masks;
   const int32_t* mask_index;
-  int pieces;
+  int rows;
+  int list;    // touched tokens of a piece, at most
 };
 
 template <typename T>
@@ -62,6 +65,9 @@ template <>
 __device__ __forceinline__ float minus_inf<float>() { return -INFINITY; }
 template <>
 __device__ __forceinline__ __nv_bfloat16 minus_inf<__nv_bfloat16>() { return __ushort_as_bfloat16(0xff80); }
+
+// ------------------------------------------------------------------------- touched tokens
+
 // (hi, lo) + (c, d), hi again the float nearest the sum of the two.
 __device__ __forceinline__ void add_pair(float& hi, float& lo, float c, float d) {
   const float s = hi + c, b = s - hi, e = (hi - (s - b)) + (c - b);
@@ -78,58 +84,47 @@ __device__ __forceinline__ void store_value(__nv_bfloat16* p, float hi, float lo
 __device__ __forceinline__ void store_double(float* p, double y) { *p = static_cast<float>(y); }
 __device__ __forceinline__ void store_double(__nv_bfloat16* p, double y) { *p = __double2bfloat16(y); }
 
-// A touched token's value; id: its place in the piece.
+// A touched token's value from its logit, whether it was seen, how often it counts, and the biases of entries
+// [e0, e1) of the list whose id is its own.
 struct Penalties {
   float rho, inv, inv_lo, freq, pres;  // inv + inv_lo = 1 / rho, but for 2^-46
-  bool rep;
-  const int* ids;  // padded to a multiple of 4 with ids of no token
+  int rep;
+  const int* ids;
   const float* bias;
-  int n_bias;
 };
 template <typename T>
-__device__ __noinline__ void touch_double(T* o, float x, uint32_t word, int id, const Penalties& p);
-
+__device__ __noinline__ void touch_double(T* o, float x, bool seen, uint32_t g, int id, int e0, int e1, const Penalties* p) {
+  double y = x;
+  if (seen && p->rep) y = y > 0 ? y / p->rho : y * p->rho;
+  if (g) y -= static_cast<double>(p->freq) * g + p->pres;
+  for (int i = e0; i < e1; ++i)
+    if (p->ids[i] == id) y += __ldg(p->bias + i);
+  store_double(o, y);
+}
 template <typename T>
-__device__ __forceinline__ void touch(T* o, float x, uint32_t word, int id, const Penalties& p) {
+__device__ __forceinline__ void touch(T* o, float x, bool seen, uint32_t g, int id, int e0, int e1, const Penalties* p) {
   float hi = x, lo = 0.f;
-  const uint32_t g = word & AJ_COUNT;
-  if ((word & ~AJ_BIAS) != 0 && p.rep) {
-    const float f = x > 0.f ? p.inv : p.rho, d = x > 0.f ? p.inv_lo : 0.f;
+  if (seen && p->rep) {
+    const float f = x > 0.f ? p->inv : p->rho, d = x > 0.f ? p->inv_lo : 0.f;
     const float y = x * f;
     lo = fmaf(x, f, -y) + x * d;
     hi = y + lo;
     lo = (y - hi) + lo;
   }
   if (g) {
-    const float n = static_cast<float>(g), t = p.freq * n;
-    add_pair(hi, lo, -t, -fmaf(p.freq, n, -t));
-    add_pair(hi, lo, -p.pres, 0.f);
+    const float n = static_cast<float>(g), t = p->freq * n;
+    add_pair(hi, lo, -t, -fmaf(p->freq, n, -t));
+    add_pair(hi, lo, -p->pres, 0.f);
   }
-  if (word & AJ_BIAS)
 #pragma unroll 1
-    for (int i = 0; i < p.n_bias; i += 4) {
-      const int4 q = *reinterpret_cast<const int4*>(p.ids + i);
-      if (q.x != id && q.y != id && q.z != id && q.w != id) continue;
-      if (q.x == id) add_pair(hi, lo, __ldg(p.bias + i), 0.f);
-      if (q.y == id) add_pair(hi, lo, __ldg(p.bias + i + 1), 0.f);
-      if (q.z == id) add_pair(hi, lo, __ldg(p.bias + i + 2), 0.f);
-      if (q.w == id) add_pair(hi, lo, __ldg(p.bias + i + 3), 0.f);
-    }
+  for (int i = e0; i < e1; ++i)
+    if (p->ids[i] == id) add_pair(hi, lo, __ldg(p->bias + i), 0.f);
   const float size = fabsf(hi);
   if (size > 7.9e-31f && size < 1.3e36f && fabsf(lo) <= size && g < (1u << 24)) store_value(o, hi, lo);
-  else touch_double(o, x, word, id, p);
+  else touch_double(o, x, seen, g, id, e0, e1, p);
 }
-template <typename T>
-__device__ __noinline__ void touch_double(T* o, float x, uint32_t word, int id, const Penalties& p) {
-  double y = x;
-  const uint32_t g = word & AJ_COUNT;
-  if ((word & ~AJ_BIAS) != 0 && p.rep) y = y > 0 ? y / p.rho : y * p.rho;
-  if (g) y -= static_cast<double>(p.freq) * g + p.pres;
-  if (word & AJ_BIAS)
-    for (int i = 0; i < p.n_bias; ++i)
-      if (p.ids[i] == id) y += __ldg(p.bias + i);
-  store_double(o, y);
-}
+
+// ------------------------------------------------------------------------------ the mask
 
 // Whether token t may be taken.
 __device__ __forceinline__ bool allowed(const uint32_t* m, int t) { return __ldg(m + (t >> 5)) >> (t & 31) & 1; }
@@ -148,61 +143,68 @@ __device__ __forceinline__ uint4 masked(uint4 v, uint32_t bits) {
     const uint32_t ninf = 0xff800000u;
     return make_uint4(bits & 1 ? v.x : ninf, bits & 2 ? v.y : ninf, bits & 4 ? v.z : ninf, bits & 8 ? v.w : ninf);
   } else {
-    uint32_t* q = reinterpret_cast<uint32_t*>(&v);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      // two bits to the tops of two bytes, each of which is then spread over a half
+    // four bits to the tops of four bytes, each of which is then spread over a half
+    const uint32_t lo = (bits & 15) * 0x10204080u, hi = (bits >> 4 & 15) * 0x10204080u;
+    auto put = [](uint32_t& x, uint32_t tops, auto which) {
       uint32_t keep;
-      asm("prmt.b32 %0, %1, 0, 0x9988;" : "=r"(keep) : "r"((bits >> (2 * i) & 3) * 0x4080u));
-      q[i] = (q[i] & keep) | (0xff80ff80u & ~keep);
-    }
+      asm("prmt.b32 %0, %1, 0, %2;" : "=r"(keep) : "r"(tops), "n"(decltype(which)::value));
+      x = (x & keep) | (0xff80ff80u & ~keep);
+    };
+    put(v.x, lo, std::integral_constant<int, 0x9988>());
+    put(v.y, lo, std::integral_constant<int, 0xbbaa>());
+    put(v.z, hi, std::integral_constant<int, 0x9988>());
+    put(v.w, hi, std::integral_constant<int, 0xbbaa>());
     return v;
   }
 }
 
-// Writes tokens [t0, t0 + n) of a row with their mask: a piece of 16 KB, a warp's 32 * AJ_VECS vectors of it.
+// Tokens [t0, t0 + n) of a row: a piece, a warp's 32 * AJ_VECS vectors of it.  Read, and written with their mask.
 template <typename T, bool INPLACE>
 struct Piece {
   static constexpr int E = 16 / sizeof(T);
+  static constexpr uint32_t FULL = (1u << E) - 1;
   uint4 w[AJ_VECS];
-  uint32_t bits[AJ_VECS];  // of a vector's elements
-  const T* x;
-  T* o;
-  const uint32_t* m;
-  int t0, n, head, vecs;  // elements before the first whole vector; vectors
-  bool same;              // whether input and output lie alike to the 16-byte grid
+  uint32_t bits;  // of a vector's elements, 8 bits for each vector
+  int head, left;  // elements before the first whole vector; the lane's vectors, which are 32 apart, reach this far
 
-  __device__ __forceinline__ Piece(const T* x_, T* o_, const uint32_t* m_, int words, int t0_, int n_) : x(x_), o(o_), m(m_), t0(t0_), n(n_) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const uintptr_t ax = reinterpret_cast<uintptr_t>(x), ao = reinterpret_cast<uintptr_t>(o);
-    same = INPLACE || ax % 16 == ao % 16;
-    head = min(n, static_cast<int>((16 - ao % 16) % 16 / sizeof(T)));
-    vecs = (n - head) / E;
-    if (!same || (INPLACE && !m)) return;
-    const int first = warp * 32 * AJ_VECS;
-    uint32_t block = ~0u;
-    if (m && first < vecs) block = mask_block(m, words, t0 + head + first * E, lane);
+  __device__ __forceinline__ void read(const T* x, const T* o, const uint32_t* m, int words, int t0, int n) {
+    const int lane = threadIdx.x & 31, first = (threadIdx.x >> 5) * 32 * AJ_VECS;
+    head = min(n, static_cast<int>((16 - reinterpret_cast<uintptr_t>(o) % 16) % 16 / sizeof(T)));
+    left = (n - head) / E - first - lane;
+    bits = ~0u;
+    if (INPLACE ? !m : (reinterpret_cast<uintptr_t>(x) ^ reinterpret_cast<uintptr_t>(o)) % 16 != 0) {
+      left = 0;  // (nothing to write, or rows that lie differently to the 16-byte grid)
+      return;
+    }
+    const T* from = x + head + (first + lane) * E;
+    if (m && left + lane > 0) {
+      const uint32_t block = mask_block(m, words, t0 + head + first * E, lane);
+      bits = 0;
+#pragma unroll
+      for (int i = 0; i < AJ_VECS; ++i) bits |= (__shfl_sync(FULL_MASK, block, i * E + lane * E / 32) >> (lane * E & 31) & FULL) << (8 * i);
+    }
 #pragma unroll
     for (int i = 0; i < AJ_VECS; ++i) {
-      const int v = first + i * 32 + lane;
-      bits[i] = __shfl_sync(FULL_MASK, block, (i * 32 + lane) * E / 32) >> (lane * E & 31) & ((1u << E) - 1);
+      const uint32_t b = bits >> (8 * i) & FULL;
       w[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (v < vecs && bits[i] != 0 && !(INPLACE && bits[i] == (1u << E) - 1)) w[i] = *reinterpret_cast<const uint4*>(x + head + v * E);
+      if (32 * i < left && b != 0 && !(INPLACE && b == FULL)) w[i] = *reinterpret_cast<const uint4*>(from + i * 32 * E);
     }
   }
-  __device__ __forceinline__ void write() const {
+  __device__ __forceinline__ void write(const T* x, T* o, const uint32_t* m, int t0, int n) const {
     if (INPLACE && !m) return;
-    if (!same) {  // rows that lie differently to the 16-byte grid
+    if (!INPLACE && (reinterpret_cast<uintptr_t>(x) ^ reinterpret_cast<uintptr_t>(o)) % 16 != 0) {
       for (int t = threadIdx.x; t < n; t += AJ_THREADS) o[t] = !m || allowed(m, t0 + t) ? x[t] : minus_inf<T>();
       return;
     }
     const int lane = threadIdx.x & 31, first = (threadIdx.x >> 5) * 32 * AJ_VECS;
+    T* to = o + head + (first + lane) * E;
 #pragma unroll
     for (int i = 0; i < AJ_VECS; ++i) {
-      const int v = first + i * 32 + lane;
-      if (v < vecs && !(INPLACE && bits[i] == (1u << E) - 1)) *reinterpret_cast<uint4*>(o + head + v * E) = m ? masked<T>(w[i], bits[i]) : w[i];
+      const uint32_t b = bits >> (8 * i) & FULL;
+      if (32 * i < left && !(INPLACE && b == FULL)) *reinterpret_cast<uint4*>(to + i * 32 * E) = m ? masked<T>(w[i], b) : w[i];
     }
-    const int tail = head + vecs * E, ends = head + n - tail;
+    // the ends
+    const int tail = head + (n - head) / E * E, ends = head + n - tail;
     if (static_cast<int>(threadIdx.x) < ends) {
       const int t = threadIdx.x < head ? threadIdx.x : tail + threadIdx.x - head;
       if (m && !allowed(m, t0 + t)) o[t] = minus_inf<T>();
@@ -211,97 +213,155 @@ struct Piece {
   }
 };
 
-template <typename T, bool INPLACE, bool TOUCH>
-__global__ void __launch_bounds__(AJ_THREADS, AJ_CTAS) adjust_kernel(const AdjustParams p) {
-  constexpr int TOKENS = AJ_PIECE / sizeof(T), SPAN = TOUCH ? 1 : AJ_SPAN;
-  __shared__ __align__(16) uint32_t s_word[TOUCH ? TOKENS : 4];
-  __shared__ uint32_t s_touched[TOUCH ? TOKENS / 32 : 1];  // a bit a token
-  __shared__ __align__(16) int s_id[TOUCH ? AJ_MAX_BIAS : 4];
-  const int tid = threadIdx.x;
-  const int64_t r = blockIdx.x / p.pieces;
-  const int first = static_cast<int>(blockIdx.x - r * p.pieces) * TOKENS * SPAN;
-  const int64_t h = r / p.per;
-  const int words = (p.V + 31) >> 5;
-  int seen = 0, from = 0, mi = -1;
-  bool ok = true;
-  if (TOUCH && p.hist) {
-    seen = __ldg(p.seen + r);
-    from = p.from ? __ldg(p.from + h) : 0;
-    if (seen < 0 || seen > p.cap) {
-      if (tid == 0) atomicOr(&g_err_adjust, ERR_KV8_LENGTH);
-      ok = false;
-    }
-  }
-  if (p.mask) {
-    mi = p.mask_index ? __ldg(p.mask_index + r) : static_cast<int>(r);
-    if (mi >= p.n_masks) {
-      if (tid == 0) atomicOr(&g_err_adjust, ERR_MASK_INDEX);
-      ok = false;
-    }
-  }
-  if (!ok) return;  // the row is left out
-  const uint32_t* m = mi >= 0 ? p.mask + mi * p.mask_stride : nullptr;
-  const T* x = static_cast<const T*>(p.x) + r * p.x_stride;
-  T* o = static_cast<T*>(p.out) + r * p.out_stride;
-  if constexpr (!TOUCH) {
+// A row's mask, if any.  False where the row is to be left out.
+__device__ __forceinline__ bool row_mask(const AdjustParams& p, int64_t r, const uint32_t*& m) {
+  m = nullptr;
+  if (!p.mask) return true;
+  const int i = p.mask_index ? __ldg(p.mask_index + r) : static_cast<int>(r);
+  if (i >= p.n_masks) return false;
+  if (i >= 0) m = p.mask + i * p.mask_stride;
+  return true;
+}
+// The tokens that a row sees.  False where the row is to be left out.
+__device__ __forceinline__ bool row_seen(const AdjustParams& p, int64_t r, int& seen) {
+  seen = p.hist ? __ldg(p.seen + r) : 0;
+  return seen >= 0 && seen <= p.cap;
+}
+
+// ------------------------------------------------------------------------------- kernels
+
+template <typename T, bool INPLACE>
+__global__ void __launch_bounds__(AJ_THREADS, 4) adjust_mask_kernel(const AdjustParams p) {
+  constexpr int TOKENS = AJ_PIECE / sizeof(T);
+  const int64_t r = blockIdx.z * gridDim.y + blockIdx.y;  // (fits 32 bits: host)
+  const int t0 = static_cast<int>(blockIdx.x) * TOKENS, n = min(TOKENS, p.V - t0);
+  const uint32_t* m = nullptr;
+  const bool has = r < p.rows && row_mask(p, r, m);
+  if (r < p.rows && !has && threadIdx.x == 0) atomicOr(&g_err_adjust, ERR_MASK_INDEX);
+  if (!has) return;  // the row is left out
+  const T* x = static_cast<const T*>(p.x) + r * p.x_stride + t0;
+  T* o = static_cast<T*>(p.out) + r * p.out_stride + t0;
+  Piece<T, INPLACE> piece;
+  piece.read(x, o, m, (p.V + 31) >> 5, t0, n);
+  piece.write(x, o, m, t0, n);
+}
+
+// Calls f(id, position) for the first `seen` tokens of a history: by fours from the first 16-byte boundary on,
+// `ahead` being the thread's first ones.
+template <typename F>
+__device__ __forceinline__ void each_token(const int32_t* hist, int lead, int seen, int4 ahead, F f) {
+  const int tid = threadIdx.x, fours = (seen - lead) / 4;
+  if (tid < min(lead, seen)) f(__ldg(hist + tid), tid);
+  if (tid < seen - lead - 4 * fours) f(__ldg(hist + lead + 4 * fours + tid), lead + 4 * fours + tid);
 #pragma unroll 1
-    for (int t0 = first; t0 < min(p.V, first + TOKENS * SPAN); t0 += TOKENS)
-      Piece<T, INPLACE>(x + t0, o + t0, m, words, t0, min(TOKENS, p.V - t0)).write();
-  } else {
-    const int t0 = first, n = min(TOKENS, p.V - t0);
-    const Piece<T, INPLACE> piece(x + t0, o + t0, m, words, t0, n);
-    for (int i = tid * 4; i < n; i += AJ_THREADS * 4) *reinterpret_cast<uint4*>(s_word + i) = make_uint4(0u, 0u, 0u, 0u);
-    for (int i = tid; i < TOKENS / 32; i += AJ_THREADS) s_touched[i] = 0;
-    // (an id that is no token's is none of the piece's)
-    for (int i = tid; i < (p.n_bias + 3) / 4 * 4; i += AJ_THREADS) {
-      const int id = i < p.n_bias ? __ldg(p.bias_id + h * p.n_bias + i) : -1;
-      s_id[i] = id < t0 || id - t0 >= n ? -1 : id - t0;
-    }
-    __syncthreads();
-    auto count = [&](int id, int i) {
-      const uint32_t at = static_cast<uint32_t>(id - t0);
-      if (at < static_cast<uint32_t>(n)) {
-        if (i >= from) atomicAdd(s_word + at, 1u);
-        else atomicOr(s_word + at, AJ_SEEN);
-        atomicOr(s_touched + (at >> 5), 1u << (at & 31));
-      }
-    };
-    const int32_t* hist = p.hist + h * p.hist_stride;
-    // (by fours from the first 16-byte boundary on)
-    const int lead = min(seen, static_cast<int>((16 - reinterpret_cast<uintptr_t>(hist) % 16) % 16 / 4)), fours = (seen - lead) / 4;
-    if (tid < lead) count(__ldg(hist + tid), tid);
-    if (tid < seen - lead - 4 * fours) count(__ldg(hist + lead + 4 * fours + tid), lead + 4 * fours + tid);
-#pragma unroll 4
-    for (int f = tid; f < fours; f += AJ_THREADS) {
-      const int i = lead + 4 * f;
-      const int4 q = __ldg(reinterpret_cast<const int4*>(hist + i));
-      count(q.x, i);
-      count(q.y, i + 1);
-      count(q.z, i + 2);
-      count(q.w, i + 3);
-    }
-    for (int i = tid; i < p.n_bias; i += AJ_THREADS)
-      if (s_id[i] >= 0) {
-        atomicOr(s_word + s_id[i], AJ_BIAS);
-        atomicOr(s_touched + (s_id[i] >> 5), 1u << (s_id[i] & 31));
-      }
-    piece.write();
-    __syncthreads();
-    // the touched ones among the lane's 32 tokens that may be taken
-    uint32_t todo = 0;
-    if (tid < TOKENS / 32) {
-      todo = s_touched[tid];
-      if (m && todo) todo &= __ldg(m + (t0 >> 5) + tid);
-    }
-    if (!__any_sync(FULL_MASK, todo != 0)) return;
-    Penalties pen{p.rep ? __ldg(p.rep + h) : 1.f, 0.f, 0.f, p.freq ? __ldg(p.freq + h) : 0.f, p.pres ? __ldg(p.pres + h) : 0.f,
-                  p.rep != nullptr, s_id, p.bias + h * p.n_bias, p.n_bias};
-    pen.inv = 1.f / pen.rho;
-    pen.inv_lo = fmaf(-pen.inv, pen.rho, 1.f) * pen.inv;
-    for (; todo; todo &= todo - 1) {
-      const int t = 32 * tid + __ffs(todo) - 1;
-      touch(o + t0 + t, static_cast<float>(x[t0 + t]), s_word[t], t, pen);
-    }
+  for (int i = tid; i < fours; i += AJ_THREADS) {
+    const int4 q = ahead;
+    if (i + AJ_THREADS < fours) ahead = __ldg(reinterpret_cast<const int4*>(hist + lead) + i + AJ_THREADS);
+    const int at = lead + 4 * i;
+    f(q.x, at);
+    f(q.y, at + 1);
+    f(q.z, at + 2);
+    f(q.w, at + 3);
+  }
+}
+
+template <typename T, bool INPLACE>
+__global__ void __launch_bounds__(AJ_THREADS, AJ_CTAS) adjust_touch_kernel(const AdjustParams p) {
+  constexpr int TOKENS = AJ_PIECE / sizeof(T), WORDS = TOKENS / 32;
+  static_assert(WORDS <= AJ_THREADS, "a word of the bit map for each thread");
+  extern __shared__ __align__(16) uint32_t s_count[];                       // [list] how often a token of the list counts
+  uint16_t* const s_token = reinterpret_cast<uint16_t*>(s_count + p.list);  // [list] its place in the piece
+  __shared__ __align__(16) uint32_t s_map[WORDS];                           // a bit a token
+  __shared__ uint16_t s_place[WORDS];                                       // tokens of the list before a word's
+  __shared__ __align__(16) int s_id[AJ_MAX_BIAS];
+  __shared__ uint32_t s_biased[WORDS];                                      // a bit a token of the bias list
+  __shared__ int s_sum[AJ_THREADS / 32];
+  __shared__ int s_twice;  // whether a token of the piece has several biases
+  __shared__ Penalties s_pen;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const uint32_t row = blockIdx.z * gridDim.y + blockIdx.y;  // (row and group fit 32 bits: host)
+  if (row >= static_cast<uint32_t>(p.rows)) return;
+  const int64_t r = row, h = p.per == 1 ? row : row / static_cast<uint32_t>(p.per);
+  const int t0 = static_cast<int>(blockIdx.x) * TOKENS, n = min(TOKENS, p.V - t0);
+  // the first tokens of the history are read before it is known how many are seen
+  const int32_t* hist = p.hist + h * p.hist_stride;
+  const int lead = static_cast<int>((16 - reinterpret_cast<uintptr_t>(hist) % 16) % 16 / 4);
+  int4 ahead = make_int4(-1, -1, -1, -1);
+  if (p.hist && lead + 4 * tid + 4 <= p.cap) ahead = __ldg(reinterpret_cast<const int4*>(hist + lead) + tid);
+  const uint32_t* m;
+  int seen;
+  const bool has = row_mask(p, r, m), counts = row_seen(p, r, seen);
+  if (tid == 0 && !has) atomicOr(&g_err_adjust, ERR_MASK_INDEX);
+  if (tid == 0 && !counts) atomicOr(&g_err_adjust, ERR_KV8_LENGTH);
+  if (!has || !counts) return;  // the row is left out
+  const T* x = static_cast<const T*>(p.x) + r * p.x_stride + t0;
+  T* o = static_cast<T*>(p.out) + r * p.out_stride + t0;
+  Piece<T, INPLACE> piece;
+  piece.read(x, o, m, (p.V + 31) >> 5, t0, n);
+  const int from = p.from ? __ldg(p.from + h) : 0;
+  if (tid < WORDS) s_map[tid] = s_biased[tid] = 0;
+  for (int i = tid; i < p.n_bias; i += AJ_THREADS) s_id[i] = __ldg(p.bias_id + h * p.n_bias + i);
+  if (tid == AJ_THREADS - 1) {
+    Penalties q{p.rep ? __ldg(p.rep + h) : 1.f, 0.f, 0.f, p.freq ? __ldg(p.freq + h) : 0.f, p.pres ? __ldg(p.pres + h) : 0.f,
+                p.rep != nullptr, s_id, p.bias + h * p.n_bias};
+    q.inv = 1.f / q.rho;
+    q.inv_lo = fmaf(-q.inv, q.rho, 1.f) * q.inv;
+    s_pen = q;
+    s_twice = 0;
+  }
+  __syncthreads();
+  // 1. which tokens there are
+  each_token(hist, lead, seen, ahead, [&](int id, int) {
+    const uint32_t t = static_cast<uint32_t>(id - t0);
+    if (t < static_cast<uint32_t>(n)) atomicOr(s_map + (t >> 5), 1u << (t & 31));
+  });
+  for (int i = tid; i < p.n_bias; i += AJ_THREADS) {
+    const uint32_t t = static_cast<uint32_t>(s_id[i] - t0);
+    if (t < static_cast<uint32_t>(n) && (atomicOr(s_biased + (t >> 5), 1u << (t & 31)) >> (t & 31) & 1)) s_twice = 1;
+  }
+  __syncthreads();
+  // their places in the list, a word of the map for each thread
+  const uint32_t word = tid < WORDS ? s_map[tid] : 0;
+  int at = __popc(word);
+#pragma unroll
+  for (int k = 1; k < 32; k <<= 1) {
+    const int y = __shfl_up_sync(FULL_MASK, at, k);
+    if (lane >= k) at += y;
+  }
+  if (lane == 31) s_sum[tid >> 5] = at;
+  __syncthreads();
+  int all = lane < AJ_THREADS / 32 ? s_sum[lane] : 0;
+  at += __reduce_add_sync(FULL_MASK, lane < tid >> 5 ? all : 0) - __popc(word);
+  all = __reduce_add_sync(FULL_MASK, all);
+  if (tid < WORDS) s_place[tid] = static_cast<uint16_t>(at);
+  for (uint32_t b = word; b; b &= b - 1, ++at) {
+    s_token[at] = static_cast<uint16_t>(32 * tid + __ffs(b) - 1);
+    s_count[at] = 0;
+  }
+  __syncthreads();
+  auto place = [&](uint32_t t) { return s_place[t >> 5] + __popc(s_map[t >> 5] & ((1u << (t & 31)) - 1)); };
+  // 2. how often they count
+  each_token(hist, lead, seen, ahead, [&](int id, int i) {
+    const uint32_t t = static_cast<uint32_t>(id - t0);
+    if (i >= from && t < static_cast<uint32_t>(n)) atomicAdd(s_count + place(t), 1u);
+  });
+  piece.write(x, o, m, t0, n);
+  __syncthreads();
+  for (int i = tid; i < all; i += AJ_THREADS) {
+    const int t = s_token[i];
+    if (!(s_biased[t >> 5] >> (t & 31) & 1) && (!m || allowed(m, t0 + t))) touch(o + t, static_cast<float>(x[t]), true, s_count[i], 0, 0, 0, &s_pen);
+  }
+  // tokens of the bias list, by the first entry that names them (from the last warps on, whose lists are the shortest)
+  const bool twice = s_twice;
+  for (int i = AJ_THREADS - 1 - tid; i < p.n_bias; i += AJ_THREADS) {
+    const int id = s_id[i];
+    const uint32_t t = static_cast<uint32_t>(id - t0);
+    if (t >= static_cast<uint32_t>(n) || (m && !allowed(m, id))) continue;
+    int j = twice ? 0 : i;
+    while (s_id[j] != id) ++j;
+    if (j < i) continue;
+    const bool there = s_map[t >> 5] >> (t & 31) & 1;
+    touch(o + t, static_cast<float>(x[t]), there, there ? s_count[place(t)] : 0u, id, i, twice ? p.n_bias : i + 1, &s_pen);
   }
 }
 
@@ -322,14 +382,21 @@ lilicorr_status fail(lilicorr_status st, const char* msg) {
 }
 
 template <typename T>
-cudaError_t adjust_launch(const AdjustParams& p, int64_t rows, bool touch, cudaStream_t stream) {
-  const dim3 grid(static_cast<unsigned>(rows * p.pieces));
-  auto go = [&](auto kernel) { kernel<<<grid, AJ_THREADS, 0, stream>>>(p); };
+cudaError_t adjust_launch(const AdjustParams& p, int64_t pieces, bool touch, cudaStream_t stream) {
   const bool inplace = p.x == p.out;
-  if (touch) inplace ? go(adjust_kernel<T, true, true>) : go(adjust_kernel<T, false, true>);
-  else inplace ? go(adjust_kernel<T, true, false>) : go(adjust_kernel<T, false, false>);
-  note_launch();
-  return cudaGetLastError();
+  const int smem = touch ? p.list * 6 : 0;
+  constexpr int Y = 32768;  // (rows that pass the grid's second dimension go on in its third)
+  const dim3 grid(static_cast<unsigned>(pieces), std::min(p.rows, Y), (p.rows - 1) / Y + 1);
+  auto go = [&](auto kern) -> cudaError_t {
+    cudaError_t e = smem > 32 * 1024 ? allow_dynamic_smem(reinterpret_cast<const void*>(kern), smem) : cudaSuccess;
+    if (e != cudaSuccess) return e;
+    kern<<<grid, AJ_THREADS, smem, stream>>>(p);
+    e = cudaGetLastError();
+    if (e == cudaSuccess) note_launch();
+    return e;
+  };
+  if (touch) return inplace ? go(adjust_touch_kernel<T, true>) : go(adjust_touch_kernel<T, false>);
+  return inplace ? go(adjust_mask_kernel<T, true>) : go(adjust_mask_kernel<T, false>);
 }
 
 }  // namespace
@@ -353,8 +420,8 @@ extern "C" lilicorr_status lilicorr_adjust_logits(const lilicorr_adjust* a, void
                                 o < x + uintptr_t((a->rows - 1) * a->row_stride + a->V) * es)
     return bad("lilicorr_adjust_logits: out is the logits themselves, or shares nothing with them");
   if (a->groups < 1 || a->rows % a->groups) return bad("lilicorr_adjust_logits: groups divides rows");
-  if (a->history && (!a->seen || a->cap < 1 || a->cap >= 1 << 30 || a->history_stride < a->cap || a->history_stride > LIM))
-    return bad("lilicorr_adjust_logits: history needs seen, a capacity below 2^30 and a stride of at least it");
+  if (a->history && (!a->seen || a->cap < 1 || a->cap >= 1 << 29 || a->history_stride < a->cap || a->history_stride > LIM))
+    return bad("lilicorr_adjust_logits: history needs seen, a capacity below 2^29 and a stride of at least it");
   if (!a->history && (a->repetition || a->presence || a->frequency || a->counted_from))
     return bad("lilicorr_adjust_logits: penalties need a history");
   if (a->n_bias < 0 || a->n_bias > AJ_MAX_BIAS || (a->n_bias > 0 && (!a->bias_id || !a->bias)))
@@ -376,11 +443,14 @@ extern "C" lilicorr_status lilicorr_adjust_logits(const lilicorr_adjust* a, void
   p.n_masks = static_cast<int>(a->n_masks); p.mask_index = a->mask_index;
   const bool touch = a->history || a->n_bias > 0;
   if (!touch && !a->mask && a->logits == a->out) return LILICORR_OK;
-  const int64_t tokens = int64_t(AJ_PIECE / es) * (touch ? 1 : AJ_SPAN);
-  p.pieces = static_cast<int>((a->V + tokens - 1) / tokens);
-  if (a->rows * p.pieces > INT_MAX) return bad("lilicorr_adjust_logits: rows * V is too large for one call");
-  const cudaError_t e = es == 2 ? adjust_launch<__nv_bfloat16>(p, a->rows, touch, static_cast<cudaStream_t>(stream))
-                                : adjust_launch<float>(p, a->rows, touch, static_cast<cudaStream_t>(stream));
+  const int64_t tokens = AJ_PIECE / es;
+  const int64_t pieces = (a->V + tokens - 1) / tokens;
+  p.rows = static_cast<int>(a->rows);
+  if (a->rows > INT_MAX - 65536 || a->rows * pieces > INT_MAX) return bad("lilicorr_adjust_logits: rows * V is too large for one call");
+  // a piece's list holds every token that the history may bring into it
+  p.list = static_cast<int>(std::max<int64_t>(4, (std::min<int64_t>(a->history ? a->cap : 0, std::min(tokens, a->V)) + 3) / 4 * 4));
+  const cudaError_t e = es == 2 ? adjust_launch<__nv_bfloat16>(p, pieces, touch, static_cast<cudaStream_t>(stream))
+                                : adjust_launch<float>(p, pieces, touch, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return fail(LILICORR_ERR_CUDA, cudaGetErrorString(e));
   return LILICORR_OK;
 }

@@ -28,7 +28,7 @@ def adjust(lib, null=False, **kw):
     dict(null=True), dict(logits=None), dict(out=None), dict(ldtype=2), dict(rows=0), dict(rows=1 << 31), dict(V=0),
     dict(V=1 << 31, row_stride=1 << 31, out_stride=1 << 31), dict(row_stride=999), dict(out_stride=999), dict(logits=FAKE + 1),
     dict(out_stride=1008), dict(out=FAKE + 4000), dict(out=FAKE - 2), dict(groups=0), dict(groups=3), dict(seen=None), dict(cap=0),
-    dict(cap=1 << 30, history_stride=1 << 30), dict(history_stride=63), dict(history=None, repetition=FAKE),
+    dict(cap=1 << 29, history_stride=1 << 29), dict(history_stride=63), dict(history=None, repetition=FAKE),
     dict(history=None, counted_from=FAKE), dict(n_bias=-1), dict(n_bias=1025, bias_id=FAKE, bias=FAKE), dict(n_bias=3),
     dict(n_bias=3, bias_id=FAKE), dict(mask=FAKE, n_masks=0, mask_stride=32), dict(mask=FAKE, n_masks=8, mask_stride=31),
     dict(mask=FAKE, n_masks=7, mask_stride=32), dict(mask_index=FAKE),
