@@ -30,13 +30,11 @@ static __device__ uint32_t g_err_adjust;
 // each of a piece's tokens to count in, cleared and searched, 57 us (209 with 64-bit arithmetic and loops with few lanes
 // at work); two kernels, the second a CTA a row for the touched tokens alone, 41 with a table of the ids by their hash
 // and 43 with a bit map of the row: the tokens' logits are read and written one by one once the row has left the L2 cache.
-constexpr int AJ_THREADS = 512;
-constexpr int AJ_VECS = 4;                           // vectors of 16 bytes of a lane
+// (512 threads of four vectors: 47.4 us for 44.7 in the large case below.)
+constexpr int AJ_THREADS = 256;
+constexpr int AJ_VECS = 8;                           // vectors of 16 bytes of a lane
 constexpr int AJ_PIECE = AJ_THREADS * AJ_VECS * 16;  // bytes
 constexpr int AJ_MAX_BIAS = 1024;
-#ifndef AJ_CTAS
-#define AJ_CTAS 3
-#endif
 
 struct AdjustParams {
   const void* x;
@@ -164,28 +162,33 @@ struct Piece {
   static constexpr int E = 16 / sizeof(T);
   static constexpr uint32_t FULL = (1u << E) - 1;
   uint4 w[AJ_VECS];
-  uint32_t bits;  // of a vector's elements, 8 bits for each vector
+  uint32_t bits[AJ_VECS / 4];  // of a vector's elements, 8 bits for each vector
   int head, left;  // elements before the first whole vector; the lane's vectors, which are 32 apart, reach this far
 
   __device__ __forceinline__ void read(const T* x, const T* o, const uint32_t* m, int words, int t0, int n) {
     const int lane = threadIdx.x & 31, first = (threadIdx.x >> 5) * 32 * AJ_VECS;
     head = min(n, static_cast<int>((16 - reinterpret_cast<uintptr_t>(o) % 16) % 16 / sizeof(T)));
     left = (n - head) / E - first - lane;
-    bits = ~0u;
+#pragma unroll
+    for (int i = 0; i < AJ_VECS / 4; ++i) bits[i] = ~0u;
     if (INPLACE ? !m : (reinterpret_cast<uintptr_t>(x) ^ reinterpret_cast<uintptr_t>(o)) % 16 != 0) {
       left = 0;  // (nothing to write, or rows that lie differently to the 16-byte grid)
       return;
     }
     const T* from = x + head + (first + lane) * E;
     if (m && left + lane > 0) {
-      const uint32_t block = mask_block(m, words, t0 + head + first * E, lane);
-      bits = 0;
 #pragma unroll
-      for (int i = 0; i < AJ_VECS; ++i) bits |= (__shfl_sync(FULL_MASK, block, i * E + lane * E / 32) >> (lane * E & 31) & FULL) << (8 * i);
+      for (int k = 0; k < AJ_VECS / 4; ++k) {
+        bits[k] = 0;
+        constexpr int PER = 4 * E;  // vectors, by a block of 1,024 tokens (f32: half of it)
+        const uint32_t block = mask_block(m, words, t0 + head + first * E + k * 32 * PER, lane);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) bits[k] |= (__shfl_sync(FULL_MASK, block, i * E + lane * E / 32) >> (lane * E & 31) & FULL) << (8 * i);
+      }
     }
 #pragma unroll
     for (int i = 0; i < AJ_VECS; ++i) {
-      const uint32_t b = bits >> (8 * i) & FULL;
+      const uint32_t b = bits[i / 4] >> (8 * (i % 4)) & FULL;
       w[i] = make_uint4(0u, 0u, 0u, 0u);
       if (32 * i < left && b != 0 && !(INPLACE && b == FULL)) w[i] = *reinterpret_cast<const uint4*>(from + i * 32 * E);
     }
@@ -200,7 +203,7 @@ struct Piece {
     T* to = o + head + (first + lane) * E;
 #pragma unroll
     for (int i = 0; i < AJ_VECS; ++i) {
-      const uint32_t b = bits >> (8 * i) & FULL;
+      const uint32_t b = bits[i / 4] >> (8 * (i % 4)) & FULL;
       if (32 * i < left && !(INPLACE && b == FULL)) *reinterpret_cast<uint4*>(to + i * 32 * E) = m ? masked<T>(w[i], b) : w[i];
     }
     // the ends
@@ -266,9 +269,9 @@ __device__ __forceinline__ void each_token(const int32_t* hist, int lead, int se
 }
 
 template <typename T, bool INPLACE>
-__global__ void __launch_bounds__(AJ_THREADS, AJ_CTAS) adjust_touch_kernel(const AdjustParams p) {
+__global__ void __launch_bounds__(AJ_THREADS, 4) adjust_touch_kernel(const AdjustParams p) {
   constexpr int TOKENS = AJ_PIECE / sizeof(T), WORDS = TOKENS / 32;
-  static_assert(WORDS <= AJ_THREADS, "a word of the bit map for each thread");
+  constexpr int EACH = WORDS > AJ_THREADS ? WORDS / AJ_THREADS : 1;  // words of the bit map for each thread
   extern __shared__ __align__(16) uint32_t s_count[];                       // [list] how often a token of the list counts
   uint16_t* const s_token = reinterpret_cast<uint16_t*>(s_count + p.list);  // [list] its place in the piece
   __shared__ __align__(16) uint32_t s_map[WORDS];                           // a bit a token
@@ -299,7 +302,7 @@ __global__ void __launch_bounds__(AJ_THREADS, AJ_CTAS) adjust_touch_kernel(const
   Piece<T, INPLACE> piece;
   piece.read(x, o, m, (p.V + 31) >> 5, t0, n);
   const int from = p.from ? __ldg(p.from + h) : 0;
-  if (tid < WORDS) s_map[tid] = s_biased[tid] = 0;
+  for (int i = tid; i < WORDS; i += AJ_THREADS) s_map[i] = s_biased[i] = 0;
   for (int i = tid; i < p.n_bias; i += AJ_THREADS) s_id[i] = __ldg(p.bias_id + h * p.n_bias + i);
   if (tid == AJ_THREADS - 1) {
     Penalties q{p.rep ? __ldg(p.rep + h) : 1.f, 0.f, 0.f, p.freq ? __ldg(p.freq + h) : 0.f, p.pres ? __ldg(p.pres + h) : 0.f,
@@ -321,8 +324,14 @@ __global__ void __launch_bounds__(AJ_THREADS, AJ_CTAS) adjust_touch_kernel(const
   }
   __syncthreads();
   // their places in the list, a word of the map for each thread
-  const uint32_t word = tid < WORDS ? s_map[tid] : 0;
-  int at = __popc(word);
+  uint32_t word[EACH];
+  int mine = 0;
+#pragma unroll
+  for (int i = 0; i < EACH; ++i) {
+    word[i] = tid * EACH < WORDS ? s_map[tid * EACH + i] : 0;
+    mine += __popc(word[i]);
+  }
+  int at = mine;
 #pragma unroll
   for (int k = 1; k < 32; k <<= 1) {
     const int y = __shfl_up_sync(FULL_MASK, at, k);
@@ -331,13 +340,17 @@ __global__ void __launch_bounds__(AJ_THREADS, AJ_CTAS) adjust_touch_kernel(const
   if (lane == 31) s_sum[tid >> 5] = at;
   __syncthreads();
   int all = lane < AJ_THREADS / 32 ? s_sum[lane] : 0;
-  at += __reduce_add_sync(FULL_MASK, lane < tid >> 5 ? all : 0) - __popc(word);
+  at += __reduce_add_sync(FULL_MASK, lane < tid >> 5 ? all : 0) - mine;
   all = __reduce_add_sync(FULL_MASK, all);
-  if (tid < WORDS) s_place[tid] = static_cast<uint16_t>(at);
-  for (uint32_t b = word; b; b &= b - 1, ++at) {
-    s_token[at] = static_cast<uint16_t>(32 * tid + __ffs(b) - 1);
-    s_count[at] = 0;
-  }
+  if (tid * EACH < WORDS)
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) {
+      s_place[tid * EACH + i] = static_cast<uint16_t>(at);
+      for (uint32_t b = word[i]; b; b &= b - 1, ++at) {
+        s_token[at] = static_cast<uint16_t>(32 * (tid * EACH + i) + __ffs(b) - 1);
+        s_count[at] = 0;
+      }
+    }
   __syncthreads();
   auto place = [&](uint32_t t) { return s_place[t >> 5] + __popc(s_map[t >> 5] & ((1u << (t & 31)) - 1)); };
   // 2. how often they count

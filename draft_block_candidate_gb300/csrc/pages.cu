@@ -289,9 +289,9 @@ __global__ void __cluster_dims__(CL_CTAS, 1, 1) __launch_bounds__(CL_THREADS) pa
 
 // ---------------------------------------------------------------------------------- moving
 // Page src[i] of every cache is copied to page dst[i]; where `count` is given, the first *count of
-// them.  The flat run of 16-byte vectors of all pages is dealt in tiles, so that small pages fill
-// CTAs as well as large ones.
-constexpr int MV_THREADS = 256, MV_VECS = 4, MV_TILE = MV_THREADS * MV_VECS, MV_CACHES = 16, MV_TABLES = 8;
+// them.  A CTA takes a tile of 32 KB of a page, or as many small pages as fill one, at a time.  Bound by
+// HBM.
+constexpr int MV_THREADS = 256, MV_VECS = 8, MV_TILE = MV_THREADS * MV_VECS, MV_CACHES = 16, MV_TABLES = 8;
 
 struct MoveCache {
   const uint4 *k, *v;
@@ -308,6 +308,8 @@ struct MoveTable {
 struct MoveParams {
   MoveCache c[MV_CACHES];
   int n_caches, heads, vecs;  // vectors of a page
+  int tiles, pages;           // of a page, of a tile: one of them is 1
+  uint32_t inv;               // 2^32 / vecs, rounded up: e * inv >> 32 is e / vecs for a tile's vectors
   int64_t n_src, n_dst;       // pages of the caches
   const int32_t *src, *dst, *count, *map;
   int64_t n;
@@ -317,31 +319,49 @@ struct MoveParams {
 
 __device__ __forceinline__ void move_pages(const MoveParams& p, int cta, int ctas) {
   const int64_t n = p.count ? min(p.n, int64_t(__ldcg(p.count))) : p.n;
-  const int64_t total = n * p.n_caches * 2 * p.vecs;
-  for (int64_t t0 = int64_t(cta) * MV_TILE; t0 < total; t0 += int64_t(ctas) * MV_TILE) {
-    const int64_t u0 = t0 / p.vecs;  // unit: (cache, keys or values, move)
-    const uint32_t in0 = static_cast<uint32_t>(t0 - u0 * p.vecs);
+  // tiles of one cache's keys, or values
+  const int64_t half = p.pages > 1 ? (n + p.pages - 1) / p.pages : n * p.tiles, all = half * p.n_caches * 2;
+  int c2 = 0;
+  int64_t base = 0;  // of cache and keys or values c2
+  for (int64_t tile = cta; tile < all; tile += ctas) {
+    while (tile - base >= half) {
+      base += half;
+      ++c2;
+    }
+    const int64_t at = tile - base;
+    const MoveCache& c = p.c[c2 >> 1];
+    const bool is_v = c2 & 1;
+    int64_t m0 = at * p.pages;
+    uint32_t e0 = 0;
+    if (p.tiles > 1) {
+      m0 = at < UINT_MAX ? static_cast<uint32_t>(at) / static_cast<uint32_t>(p.tiles) : at / p.tiles;
+      e0 = static_cast<uint32_t>(at - m0 * p.tiles) * MV_TILE;
+    }
     uint4 w[MV_VECS];
     uint4* to[MV_VECS];
 #pragma unroll
     for (int i = 0; i < MV_VECS; ++i) {
-      const uint32_t e = in0 + i * MV_THREADS + threadIdx.x, du = e / p.vecs, off = e - du * p.vecs;
-      const int64_t u = u0 + du;
+      uint32_t e = e0 + i * MV_THREADS + threadIdx.x;
+      int64_t m = m0;
       to[i] = nullptr;
-      if (t0 + i * MV_THREADS + threadIdx.x >= total) continue;
-      const int64_t half = u / n, m = u - half * n;
-      const int a = __ldcg(p.src + m), b = __ldcg(p.dst + m);
+      if (p.pages > 1) {
+        const uint32_t k = __umulhi(e, p.inv);
+        e -= k * p.vecs;
+        m += k;
+        if (k >= static_cast<uint32_t>(p.pages) || m >= n) continue;
+      } else if (e >= static_cast<uint32_t>(p.vecs)) {
+        continue;
+      }
+      const int a = __ldg(p.src + m), b = __ldg(p.dst + m);
       if (a >= p.n_src || b >= p.n_dst) {
-        if (off == 0) atomicOr(&g_err_pages, ERR_KV8_PAGE);
+        if (e == 0) atomicOr(&g_err_pages, ERR_KV8_PAGE);
         continue;
       }
       if (a < 0 || b < 0) continue;
-      const MoveCache& c = p.c[half >> 1];
-      const bool is_v = half & 1;
-      w[i] = __ldcs((is_v ? c.v : c.k) + int64_t(a) * p.vecs + off);
-      to[i] = (is_v ? c.to_v : c.to_k) + int64_t(b) * p.vecs + off;
-      if (off < static_cast<uint32_t>(p.heads))  // (a page has more vectors than heads)
-        (is_v ? c.to_vs : c.to_ks)[int64_t(b) * p.heads + off] = (is_v ? c.vs : c.ks)[int64_t(a) * p.heads + off];
+      w[i] = __ldcs((is_v ? c.v : c.k) + int64_t(a) * p.vecs + e);
+      to[i] = (is_v ? c.to_v : c.to_k) + int64_t(b) * p.vecs + e;
+      if (e < static_cast<uint32_t>(p.heads))  // (a page has more vectors than heads)
+        (is_v ? c.to_vs : c.to_ks)[int64_t(b) * p.heads + e] = (is_v ? c.vs : c.ks)[int64_t(a) * p.heads + e];
     }
 #pragma unroll
     for (int i = 0; i < MV_VECS; ++i)
@@ -563,14 +583,17 @@ const char* caches_error(const lilicorr_kv8_cache* c, int32_t n, const lilicorr_
 void put_caches(MoveParams& p, const lilicorr_kv8_cache* from, const lilicorr_kv8_cache* to, int n) {
   p.n_caches = n;
   p.heads = from->kv_heads;
-  p.vecs = static_cast<int>(int64_t(from->kv_heads) * from->page * from->head_dim / 16);
+  p.vecs = static_cast<int>(int64_t(from->kv_heads) * from->page * from->head_dim / 16);  // 32 at least
+  p.tiles = (p.vecs - 1) / MV_TILE + 1;
+  p.pages = std::max(1, MV_TILE / p.vecs);
+  p.inv = static_cast<uint32_t>(((int64_t(1) << 32) + p.vecs - 1) / p.vecs);
   p.n_src = from->n_pages;
   p.n_dst = to->n_pages;
   for (int i = 0; i < n; ++i)
     p.c[i] = MoveCache{static_cast<const uint4*>(from[i].k_pages), static_cast<const uint4*>(from[i].v_pages), static_cast<uint4*>(to[i].k_pages),
                        static_cast<uint4*>(to[i].v_pages), from[i].k_scale, from[i].v_scale, to[i].k_scale, to[i].v_scale};
 }
-int64_t tiles_of(const MoveParams& p) { return (p.n * p.n_caches * 2 * p.vecs + MV_TILE - 1) / MV_TILE; }
+int64_t tiles_of(const MoveParams& p) { return (p.pages > 1 ? (p.n + p.pages - 1) / p.pages : p.n * p.tiles) * p.n_caches * 2; }
 
 }  // namespace
 }  // namespace lilicorr

@@ -61,6 +61,24 @@ def _fits32(n: int, name: str) -> None:
         raise ValueError(f"{name} must fit 32 bits, got {n}")
 
 
+@functools.lru_cache(maxsize=4096)
+def _row_layout(shape, st):
+    """(rows, columns, row stride) of rows that lie a uniform stride apart, else None."""
+    cols = shape[-1]
+    rows, row = 1, cols
+    for n, s in zip(reversed(shape[:-1]), reversed(st[:-1])):
+        if n == 1:
+            continue
+        if rows == 1:
+            row = s
+        elif s != rows * row:
+            return None
+        rows *= n
+    if (cols > 1 and st[-1] != 1) or (rows > 1 and row < cols):
+        return None
+    return rows, cols, row
+
+
 def _new_workspace(need: int, dev, what: str) -> torch.Tensor:
     if need == 0:
         raise LilicorrError(1, what)

@@ -9,7 +9,7 @@ import torch
 
 from . import _lib as L
 from .api import _check, _ldtype
-from .decode import _run_on, _want
+from .decode import _row_layout, _run_on, _want
 
 # lilicorr_adjust, as bytes (a ctypes structure of as many fields takes three times as long to fill)
 _ADJUST = struct.Struct("=QQi4x5qQqi4x7Qi4xQqqQ")
@@ -19,20 +19,10 @@ def _logit_rows(t, name: str):
     """(rows, V, row stride) of logits [..., V] whose rows lie a uniform stride apart."""
     if not isinstance(t, torch.Tensor) or t.dim() < 1:
         raise ValueError(f"{name} must be a tensor [..., V]")
-    shape, st = t.shape, t.stride()
-    V = shape[-1]
-    rows, row = 1, V
-    for n, s in zip(reversed(shape[:-1]), reversed(st[:-1])):
-        if n == 1:
-            continue
-        if rows == 1:
-            row = s
-        elif s != rows * row:
-            raise ValueError(f"{name}'s rows must be a uniform stride apart")
-        rows *= n
-    if V > 1 and st[-1] != 1 or (rows > 1 and row < V):
-        raise ValueError(f"{name}'s rows must be contiguous and not overlap")
-    return rows, V, max(row, V)
+    lay = _row_layout(t.shape, t.stride())
+    if lay is None:
+        raise ValueError(f"{name}'s rows must be contiguous, a uniform stride apart, and not overlap")
+    return lay[0], lay[1], max(lay[2], lay[1])
 
 
 def _table(t, name: str, rows: Optional[int], cols: Optional[int], dev: int):

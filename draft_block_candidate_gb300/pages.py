@@ -5,63 +5,58 @@ refs [n_pages] int32 (torch.zeros to begin with) counts the entries of block tab
 page; an entry is the page that its row holds there, or negative."""
 from __future__ import annotations
 
+import struct
 from typing import Optional, Sequence
 
 import torch
 
 from . import _lib as L
 from .api import _check
-from .decode import KV8Cache, _fits32, _new_workspace, _run_on, _want
+from .decode import KV8Cache, _fits32, _new_workspace, _row_layout, _run_on, _want
 
 
 def _pool(refs) -> tuple:
     """(device, pages) of the counts of holders."""
-    if not isinstance(refs, torch.Tensor) or refs.dim() != 1 or not refs.is_cuda:
-        raise ValueError("refs must be a tensor [n_pages] on a GPU")
-    dev = refs.get_device()
-    _want(refs, "refs", torch.int32, refs.shape, dev)
-    return dev, refs.shape[0]
+    if isinstance(refs, torch.Tensor):
+        dev, shape = refs.get_device(), refs.shape
+        if refs.dtype is torch.int32 and len(shape) == 1 and dev >= 0 and refs.is_contiguous():
+            return dev, shape[0]
+        if len(shape) == 1 and dev >= 0:
+            _want(refs, "refs", torch.int32, shape, dev)
+    raise ValueError("refs must be a tensor [n_pages] on a GPU")
 
 
 def _rows_of(table, dev: int, name: str = "table") -> tuple:
     """(rows, columns, row stride) of a table [..., cols] whose rows lie a uniform stride apart."""
     if not isinstance(table, torch.Tensor) or table.dtype is not torch.int32 or table.dim() < 2:
         raise ValueError(f"{name} must be an int32 tensor [..., cols]")
-    if table.get_device() != dev or not table.is_cuda:
+    if table.get_device() != dev:
         raise ValueError(f"{name} is on {table.device}, expected cuda:{dev}")
-    shape, st = table.shape, table.stride()
-    cols = shape[-1]
-    rows, row = 1, cols
-    for n, s in zip(reversed(shape[:-1]), reversed(st[:-1])):
-        if n == 1:
-            continue
-        if rows == 1:
-            row = s
-        elif s != rows * row:
-            raise ValueError(f"{name}'s rows must be a uniform stride apart")
-        rows *= n
-    if (cols > 1 and st[-1] != 1) or (rows > 1 and row < cols):
-        raise ValueError(f"{name}'s rows must be contiguous and not overlap")
-    _fits32(cols, f"{name}'s columns")
-    return rows, cols, row
+    lay = _row_layout(table.shape, table.stride())
+    if lay is None:
+        raise ValueError(f"{name}'s rows must be contiguous, a uniform stride apart, and not overlap")
+    _fits32(lay[1], f"{name}'s columns")
+    return lay
 
 
-def _per_row(t, name: str, dtype, table, dev: int) -> None:
+def _per_row(t, name: str, dtype, lead, dev: int) -> None:
     """A value for each row: of the table's shape without its columns, or flat."""
-    lead = table.shape[:-1]
-    if isinstance(t, torch.Tensor) and t.dim() == 1:
-        lead = (lead.numel(),)
+    if isinstance(t, torch.Tensor):
+        if t.dtype is dtype and t.shape == lead and t.get_device() == dev and t.is_contiguous():
+            return
+        if t.dim() == 1:
+            lead = (lead.numel(),)
     _want(t, name, dtype, lead, dev)
 
 
-def _call(ctx, fn: str, args) -> None:
+def _call(ctx, fn, name: str, args) -> None:
     if ctx is None:
-        st = getattr(L.lib(), fn)(*args)
+        st = fn(*args)
     else:
         with ctx:
-            st = getattr(L.lib(), fn)(*args)
+            st = fn(*args)
     if st:
-        _check(st, fn)
+        _check(st, name)
 
 
 def kv8_pages_workspace(n_pages: int, rows: int, device="cuda") -> torch.Tensor:
@@ -89,8 +84,8 @@ def kv8_fork(refs: torch.Tensor, table: torch.Tensor, parent: torch.Tensor, stre
     if beams == 1:
         sw = cols
     raw, ctx = _run_on(dev, stream)
-    _call(ctx, "lilicorr_kv8_fork", (refs.data_ptr(), n_pages, table.data_ptr(), sb if batch > 1 else beams * sw, sw, cols,
-                                     parent.data_ptr(), batch, beams, raw))
+    _call(ctx, L.lib().lilicorr_kv8_fork, "lilicorr_kv8_fork",
+          (refs.data_ptr(), n_pages, table.data_ptr(), sb if batch > 1 else beams * sw, sw, cols, parent.data_ptr(), batch, beams, raw))
 
 
 def kv8_grow(refs: torch.Tensor, table: torch.Tensor, kv_len: torch.Tensor, new_tokens: torch.Tensor, page: int, max_new: int,
@@ -103,15 +98,16 @@ def kv8_grow(refs: torch.Tensor, table: torch.Tensor, kv_len: torch.Tensor, new_
     -1, and whether the row has its pages; `out` may hold the two preallocated."""
     dev, n_pages = _pool(refs)
     rows, cols, row = _rows_of(table, dev)
-    _per_row(kv_len, "kv_len", torch.int32, table, dev)
-    _per_row(new_tokens, "new_tokens", torch.int32, table, dev)
+    lead = table.shape[:-1]
+    _per_row(kv_len, "kv_len", torch.int32, lead, dev)
+    _per_row(new_tokens, "new_tokens", torch.int32, lead, dev)
     _fits32(page, "page")
     _fits32(max_new, "max_new")
     if out is not None:
         if len(out) != 2:
             raise ValueError("out must hold tail_src and granted")
-        _per_row(out[0], "tail_src", torch.int32, table, dev)
-        _per_row(out[1], "granted", torch.bool, table, dev)
+        _per_row(out[0], "tail_src", torch.int32, lead, dev)
+        _per_row(out[1], "granted", torch.bool, lead, dev)
     if workspace is not None:
         _want(workspace, "workspace", torch.uint8, (workspace.numel(),), dev)
     raw, ctx = _run_on(dev, stream)
@@ -119,12 +115,11 @@ def kv8_grow(refs: torch.Tensor, table: torch.Tensor, kv_len: torch.Tensor, new_
     def call():
         o, ws = out, workspace
         if o is None:
-            lead = table.shape[:-1]
             o = (torch.empty(lead, dtype=torch.int32, device=table.device), torch.empty(lead, dtype=torch.bool, device=table.device))
         if rows > 0:
             if ws is None:
                 ws = kv8_pages_workspace(n_pages, rows, table.device)
-            _call(None, "lilicorr_kv8_grow", (refs.data_ptr(), n_pages, table.data_ptr(), rows, row, cols, kv_len.data_ptr(),
+            _call(None, L.lib().lilicorr_kv8_grow, "lilicorr_kv8_grow", (refs.data_ptr(), n_pages, table.data_ptr(), rows, row, cols, kv_len.data_ptr(),
                                               new_tokens.data_ptr(), page, max_new, o[0].data_ptr(), o[1].data_ptr(), ws.data_ptr(),
                                               ws.numel(), raw))
         return tuple(o)
@@ -141,20 +136,31 @@ def kv8_free(refs: torch.Tensor, table: torch.Tensor, keep: torch.Tensor, page: 
     that is left after a check gives back what rejected tokens had."""
     dev, n_pages = _pool(refs)
     rows, cols, row = _rows_of(table, dev)
-    _per_row(keep, "keep", torch.int32, table, dev)
+    _per_row(keep, "keep", torch.int32, table.shape[:-1], dev)
     _fits32(page, "page")
     if rows == 0 or cols == 0:
         return
     raw, ctx = _run_on(dev, stream)
-    _call(ctx, "lilicorr_kv8_free", (refs.data_ptr(), n_pages, table.data_ptr(), rows, row, cols, keep.data_ptr(), page, raw))
+    _call(ctx, L.lib().lilicorr_kv8_free, "lilicorr_kv8_free", (refs.data_ptr(), n_pages, table.data_ptr(), rows, row, cols, keep.data_ptr(), page, raw))
 
 
-def _descriptions(caches: Sequence[KV8Cache]):
-    if not caches or not all(isinstance(c, KV8Cache) for c in caches):
-        raise ValueError("there must be caches, KV8Cache objects")
-    if any(c.device != caches[0].device for c in caches):
-        raise ValueError("caches must be on one device")
-    return (L.Kv8CacheDesc * len(caches))(*(c._desc for c in caches))
+def _descriptions(caches: Sequence[KV8Cache]) -> bytes:
+    """Their descriptions, one behind the other."""
+    if not caches:
+        raise ValueError("there must be caches")
+    device = None
+    for c in caches:
+        if not isinstance(c, KV8Cache):
+            raise ValueError("caches must be KV8Cache objects")
+        if device is None:
+            device = c.device
+        elif c.device != device:
+            raise ValueError("caches must be on one device")
+    return b"".join([c._desc for c in caches])
+
+
+# lilicorr_kv8_table, as bytes
+_TABLE = struct.Struct("=QQqqqi4x")
 
 
 def kv8_copy(caches: Sequence[KV8Cache], src: torch.Tensor, dst: torch.Tensor, into: Optional[Sequence[KV8Cache]] = None,
@@ -174,7 +180,7 @@ def kv8_copy(caches: Sequence[KV8Cache], src: torch.Tensor, dst: torch.Tensor, i
     if src.shape[0] == 0:
         return
     raw, ctx = _run_on(dev, stream)
-    _call(ctx, "lilicorr_kv8_copy", (have, to, len(caches), src.data_ptr(), dst.data_ptr(), src.shape[0], raw))
+    _call(ctx, L.lib().lilicorr_kv8_copy, "lilicorr_kv8_copy", (have, to, len(caches), src.data_ptr(), dst.data_ptr(), src.shape[0], raw))
 
 
 def kv8_compact(caches: Sequence[KV8Cache], refs: torch.Tensor, tables: Sequence[torch.Tensor], out=None,
@@ -201,7 +207,7 @@ def kv8_compact(caches: Sequence[KV8Cache], refs: torch.Tensor, tables: Sequence
             raise ValueError("out's tables must have the tables' shapes")
         orow = row if o is t else _rows_of(o, dev, "a table of out")[2]
         if rows and cols:
-            packed.append(L.Kv8Table(t.data_ptr(), o.data_ptr(), rows, row, orow, cols))
+            packed.append(_TABLE.pack(t.data_ptr(), o.data_ptr(), rows, row, orow, cols))
     if workspace is not None:
         _want(workspace, "workspace", torch.uint8, (workspace.numel(),), dev)
     raw, ctx = _run_on(dev, stream)
@@ -209,8 +215,8 @@ def kv8_compact(caches: Sequence[KV8Cache], refs: torch.Tensor, tables: Sequence
     def call():
         live = torch.empty(1, dtype=torch.int32, device=refs.device)
         ws = kv8_pages_workspace(n_pages, 1, refs.device) if workspace is None else workspace
-        _call(None, "lilicorr_kv8_compact", (have, len(caches), refs.data_ptr(), refs_to.data_ptr(), n_pages,
-                                             (L.Kv8Table * len(packed))(*packed), len(packed), live.data_ptr(), ws.data_ptr(),
+        _call(None, L.lib().lilicorr_kv8_compact, "lilicorr_kv8_compact", (have, len(caches), refs.data_ptr(), refs_to.data_ptr(), n_pages,
+                                             b"".join(packed), len(packed), live.data_ptr(), ws.data_ptr(),
                                              ws.numel(), raw))
         return live
 
