@@ -93,35 +93,55 @@ __global__ void __launch_bounds__(FR_THREADS) page_free_kernel(int32_t* refs, in
 }
 
 // ------------------------------------------------------------- what the whole pool decides
-// Two kernels number pages in their order: one cluster of CL_CTAS CTAs, a run of pages (and of rows)
-// for each warp, counts exchanged through distributed shared memory.
-constexpr int CL_CTAS = 8, CL_WARPS = 16, CL_THREADS = 32 * CL_WARPS, CL_ALL = CL_CTAS * CL_WARPS;
+// Two kernels number pages in their order: a run of pages (and of rows) for each warp of one cluster of CL_CTAS
+// CTAs, counts exchanged through distributed shared memory; or of one CTA alone, where a pool is so small that the
+// cluster's barriers cost more than they save.
+constexpr int CL_CTAS = 8, CL_WARPS = 16, CL_THREADS = 32 * CL_WARPS;
+constexpr int CL_SMALL = 4096;  // pages and rows of one CTA, at most
 
-// Sum of `mine` (a warp's, the same in its lanes) over the warps before this one, and over all.
-// Every thread of the cluster calls it; a is shared memory of CL_WARPS + 2 CL_CTAS values.
-struct Place {
-  int64_t before, all;
+template <int CTAS>
+__device__ __forceinline__ int cluster_rank() {
+  return CTAS == 1 ? 0 : static_cast<int>(cg::this_cluster().block_rank());
+}
+template <int CTAS>
+__device__ __forceinline__ void cluster_sync() {
+  if (CTAS == 1) __syncthreads();
+  else cg::this_cluster().sync();
+}
+// Sums of `mine` (a warp's, the same in its lanes) over the warps before this one, and over all.  Every thread of
+// the cluster calls it; a is shared memory of CL_WARPS values.
+struct Counts {
+  int64_t x;  // rows may want more pages than there are
+  int y;
 };
-__device__ __forceinline__ Place cluster_place(cg::cluster_group& cl, int64_t mine, int64_t* a) {
-  const int warp = threadIdx.x >> 5, rank = cl.block_rank();
-  if ((threadIdx.x & 31) == 0) a[warp] = mine;
-  cl.sync();
-  Place p{0, 0};
-  // (128 numbers: each lane reads four)
-  const int lane = threadIdx.x & 31, me = rank * CL_WARPS + warp;
+struct Place {
+  Counts before, all;
+};
+__device__ __forceinline__ int64_t warp_sum(int64_t v) {
 #pragma unroll
-  for (int i = 0; i < CL_ALL / 32; ++i) {
+  for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(FULL_MASK, v, o);
+  return v;
+}
+template <int CTAS>
+__device__ __forceinline__ Place cluster_place(Counts mine, Counts* a) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, me = cluster_rank<CTAS>() * CL_WARPS + warp;
+  if (lane == 0) a[warp] = mine;
+  cluster_sync<CTAS>();
+  Counts sum{0, 0}, before = sum;
+#pragma unroll
+  for (int i = 0; i < (CTAS * CL_WARPS + 31) / 32; ++i) {
     const int w = i * 32 + lane;
-    const int64_t v = *cl.map_shared_rank(a + w % CL_WARPS, w / CL_WARPS);
-    p.all += v;
-    if (w < me) p.before += v;
+    if (w < CTAS * CL_WARPS) {
+      const Counts v = CTAS == 1 ? a[w] : *cg::this_cluster().map_shared_rank(a + w % CL_WARPS, w / CL_WARPS);
+      sum.x += v.x;
+      sum.y += v.y;
+      if (w < me) {
+        before.x += v.x;
+        before.y += v.y;
+      }
+    }
   }
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) {
-    p.before += __shfl_xor_sync(FULL_MASK, p.before, o);
-    p.all += __shfl_xor_sync(FULL_MASK, p.all, o);
-  }
-  return p;
+  return Place{{warp_sum(before.x), __reduce_add_sync(FULL_MASK, before.y)}, {warp_sum(sum.x), __reduce_add_sync(FULL_MASK, sum.y)}};
 }
 
 // Calls f(page, holders) for the pages of [lo, hi), 32 lanes side by side, UNROLL reads under way;
@@ -162,13 +182,20 @@ struct GrowParams {
   int group_log2;        // lanes of a row
 };
 
-__global__ void __cluster_dims__(CL_CTAS, 1, 1) __launch_bounds__(CL_THREADS) page_grow_kernel(const GrowParams p) {
-  __shared__ int64_t s_a[CL_WARPS], s_b[CL_WARPS];
-  cg::cluster_group cl = cg::this_cluster();
-  const int lane = threadIdx.x & 31, w = cl.block_rank() * CL_WARPS + (threadIdx.x >> 5);
+template <int CTAS>
+__global__ void __launch_bounds__(CL_THREADS) page_grow_kernel(const GrowParams p) {
+  constexpr int ALL = CTAS * CL_WARPS;
+  __shared__ Counts s_a[CL_WARPS];
+  const int lane = threadIdx.x & 31, w = cluster_rank<CTAS>() * CL_WARPS + (threadIdx.x >> 5);
   const int G = 1 << p.group_log2, sub = lane >> p.group_log2, in = lane & (G - 1), per = 32 >> p.group_log2;
+  // this warp's pages: how many are free
+  const int64_t some = ((p.n_pages + ALL - 1) / ALL + 31) / 32 * 32;
+  const int64_t p0 = min(p.n_pages, w * some), p1 = min(p.n_pages, p0 + some);
+  int free = 0;
+  each_page<8>(p.refs, p0, p1, [&](int64_t, int v, bool in_run) { free += in_run && v == 0; });
+  free = __reduce_add_sync(FULL_MASK, free);
   // this warp's rows
-  const int64_t each = ((p.rows + CL_ALL - 1) / CL_ALL + per - 1) / per * per;
+  const int64_t each = ((p.rows + ALL - 1) / ALL + per - 1) / per * per;
   const int64_t r0 = min(p.rows, w * each), r1 = min(p.rows, r0 + each);
   // columns [c0, c1) that row r writes; whether the first one holds tokens before
   struct Span {
@@ -198,19 +225,26 @@ __global__ void __cluster_dims__(CL_CTAS, 1, 1) __launch_bounds__(CL_THREADS) pa
     if (r < r1) s = span(r);
     int32_t* row = p.table + r * p.row_stride;
     uint32_t err = s.ok ? 0u : uint32_t(ERR_KV8_LENGTH);
-    // pages that are there
+    // a column's page, and how many hold it (a lane's first column, which mostly is its only one, is kept)
+    int id0 = 0, held0 = 1;
     if (s.ok)
       for (int c = s.c0 + in; c < s.c1; c += G) {
         const int id = row[c];
-        if (id >= p.n_pages || (id < 0 && s.tail && c == s.c0) || (id >= 0 && __ldcg(p.refs + id) < 1)) err = ERR_KV8_PAGE;
+        int held = 0;
+        if (id >= p.n_pages || (id < 0 && s.tail && c == s.c0) || (id >= 0 && (held = __ldcg(p.refs + id)) < 1)) err = ERR_KV8_PAGE;
+        if (c < s.c0 + G) {
+          id0 = id;
+          held0 = held;
+        }
       }
     const bool ok = sum_group(err != 0) == 0;
     if (err) atomicOr(&g_err_pages, err);
     int need = 0;
     if (ok)
       for (int c = s.c0 + in; c < s.c1; c += G) {
-        const int id = row[c];
-        if (id >= 0 && __ldcg(p.refs + id) <= 1) continue;
+        const bool kept = c < s.c0 + G;
+        const int id = kept ? id0 : row[c];
+        if (id >= 0 && (kept ? held0 : __ldcg(p.refs + id)) <= 1) continue;
         ++need;
         row[c] = id < 0 ? -1 : -2 - id;
       }
@@ -218,29 +252,21 @@ __global__ void __cluster_dims__(CL_CTAS, 1, 1) __launch_bounds__(CL_THREADS) pa
     if (r < r1 && in == 0) p.need[r] = ok ? need : -1;
     mine += in == 0 ? need : 0;
   }
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) mine += __shfl_xor_sync(FULL_MASK, mine, o);
-  // this warp's pages
-  const int64_t some = ((p.n_pages + CL_ALL - 1) / CL_ALL + 31) / 32 * 32;
-  const int64_t p0 = min(p.n_pages, w * some), p1 = min(p.n_pages, p0 + some);
-  int64_t free = 0;
-  each_page<8>(p.refs, p0, p1, [&](int64_t, int v, bool in_run) { free += in_run && v == 0; });
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) free += __shfl_xor_sync(FULL_MASK, free, o);
-
-  const Place want = cluster_place(cl, mine, s_a), have = cluster_place(cl, free, s_b);
+  const Place at_w = cluster_place<CTAS>(Counts{warp_sum(mine), free}, s_a);
+  const int64_t want = at_w.all.x;
+  const int have = at_w.all.y;
   // the free pages that are wanted, in order
-  int64_t at = have.before;
-  if (free > 0 && at < want.all)
+  int at = at_w.before.y;
+  if (free > 0 && at < want)
     each_page<8>(p.refs, p0, p1, [&](int64_t page, int v, bool in_run) {
       const unsigned b = __ballot_sync(FULL_MASK, in_run && v == 0);
-      const int64_t k = at + __popc(b & ((1u << lane) - 1));
-      if ((b >> lane & 1) && k < want.all) p.list[k] = static_cast<int32_t>(page);
+      const int k = at + __popc(b & ((1u << lane) - 1));
+      if ((b >> lane & 1) && k < want) p.list[k] = static_cast<int32_t>(page);
       at += __popc(b);
     });
-  cl.sync();  // (the list is there, and nobody reads counts of holders any more)
+  cluster_sync<CTAS>();  // (the list is there, and nobody reads counts of holders any more)
 
-  int64_t start = want.before;
+  int64_t start = at_w.before.x;
   for (int64_t rb = r0; rb < r1; rb += per) {
     const int64_t r = rb + sub;
     const int need = r < r1 ? p.need[r] : 0;
@@ -252,7 +278,7 @@ __global__ void __cluster_dims__(CL_CTAS, 1, 1) __launch_bounds__(CL_THREADS) pa
       all += v;
     }
     start += all;
-    const bool ok = need == 0 || (need > 0 && k + need <= have.all);
+    const bool ok = need == 0 || (need > 0 && k + need <= have);
     int tail = -1;
     Span s{0, 0, true, false};
     if (r < r1 && need > 0) s = span(r);
@@ -407,25 +433,22 @@ struct PlanParams {
   int32_t* live;
 };
 
-__global__ void __cluster_dims__(CL_CTAS, 1, 1) __launch_bounds__(CL_THREADS) page_plan_kernel(const PlanParams p) {
-  __shared__ int64_t s_a[CL_WARPS], s_b[CL_WARPS];
-  cg::cluster_group cl = cg::this_cluster();
-  const int lane = threadIdx.x & 31, w = cl.block_rank() * CL_WARPS + (threadIdx.x >> 5);
-  const int64_t some = ((p.n_pages + CL_ALL - 1) / CL_ALL + 31) / 32 * 32;
+template <int CTAS>
+__global__ void __launch_bounds__(CL_THREADS) page_plan_kernel(const PlanParams p) {
+  constexpr int ALL = CTAS * CL_WARPS;
+  __shared__ Counts s_a[CL_WARPS], s_b[CL_WARPS];
+  const int lane = threadIdx.x & 31, w = cluster_rank<CTAS>() * CL_WARPS + (threadIdx.x >> 5);
+  const int64_t some = ((p.n_pages + ALL - 1) / ALL + 31) / 32 * 32;
   const int64_t p0 = min(p.n_pages, w * some), p1 = min(p.n_pages, p0 + some);
-  int64_t mine = 0;
+  int mine = 0;
   each_page<8>(p.refs, p0, p1, [&](int64_t, int v, bool in_run) { mine += in_run && v > 0; });
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) mine += __shfl_xor_sync(FULL_MASK, mine, o);
-  const Place live = cluster_place(cl, mine, s_a);
-  const int64_t L = live.all;
+  const Place live = cluster_place<CTAS>(Counts{0, __reduce_add_sync(FULL_MASK, mine)}, s_a);
+  const int L = live.all.y;
   // live pages from L on, in this warp's run
-  int64_t high = 0;
-  each_page<8>(p.refs, max(p0, L), p1, [&](int64_t, int v, bool in_run) { high += in_run && v > 0; });
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) high += __shfl_xor_sync(FULL_MASK, high, o);
-  const Place far = cluster_place(cl, high, s_b);
-  int64_t l = live.before, f = far.before;
+  int high = 0;
+  each_page<8>(p.refs, max(p0, int64_t(L)), p1, [&](int64_t, int v, bool in_run) { high += in_run && v > 0; });
+  const Place far = cluster_place<CTAS>(Counts{0, __reduce_add_sync(FULL_MASK, high)}, s_b);
+  int l = live.before.y, f = far.before.y;
   each_page<8>(p.refs, p0, p1, [&](int64_t page, int v, bool in_run) {
     const unsigned b = __ballot_sync(FULL_MASK, in_run && v > 0), low = (1u << lane) - 1;
     const unsigned up = __ballot_sync(FULL_MASK, in_run && v > 0 && page >= L);
@@ -436,18 +459,18 @@ __global__ void __cluster_dims__(CL_CTAS, 1, 1) __launch_bounds__(CL_THREADS) pa
     f += __popc(up);
   });
   if (w == 0 && lane == 0) {
-    *p.count = static_cast<int32_t>(far.all);
-    *p.live = static_cast<int32_t>(L);
+    *p.count = far.all.y;
+    *p.live = L;
   }
-  cl.sync();
-  const int64_t thread = int64_t(cl.block_rank()) * CL_THREADS + threadIdx.x;
-  for (int64_t i = thread; i < far.all; i += CL_CTAS * CL_THREADS) {
+  cluster_sync<CTAS>();
+  const int64_t thread = int64_t(cluster_rank<CTAS>()) * CL_THREADS + threadIdx.x;
+  for (int64_t i = thread; i < far.all.y; i += CTAS * CL_THREADS) {
     const int a = __ldcg(p.src + i), b = __ldcg(p.dst + i);
     p.map[a] = b;
     p.to[b] = __ldcg(p.refs + a);
   }
-  cl.sync();
-  for (int64_t i = thread; i < p.n_pages; i += CL_CTAS * CL_THREADS) {
+  cluster_sync<CTAS>();
+  for (int64_t i = thread; i < p.n_pages; i += CTAS * CL_THREADS) {
     if (i >= L) p.to[i] = 0;
     else if (p.to != p.refs) {
       const int v = __ldcg(p.refs + i);
@@ -477,6 +500,30 @@ constexpr int64_t LIM = int64_t(1) << 40;
 bool aligned4(const void* p) { return reinterpret_cast<uintptr_t>(p) % 4 == 0; }
 bool page_ok(int page) { return page == 16 || page == 32 || page == 64 || page == 128; }
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
+
+// One CTA, or one cluster of CL_CTAS.
+template <class P>
+cudaError_t launch_cluster(void (*one)(P), void (*many)(P), bool small, const P& p, cudaStream_t stream) {
+  if (small) {
+    one<<<1, CL_THREADS, 0, stream>>>(p);
+  } else {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(CL_CTAS);
+    cfg.blockDim = dim3(CL_THREADS);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = CL_CTAS;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, many, p);
+    if (e != cudaSuccess) return e;
+  }
+  const cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess) note_launch();
+  return e;
+}
 
 // Null where the counts and a table's rows are in order, else what is wrong.
 const char* pool_error(const int32_t* refs, int64_t n_pages) {
@@ -544,9 +591,8 @@ lilicorr_status lilicorr_kv8_grow(int32_t* refs, int64_t n_pages, int32_t* table
   p.need = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + align256(size_t(n_pages) * 4) * 2);
   const int most = (max_new + page - 2) / page + 1;
   while (p.group_log2 < 5 && (1 << p.group_log2) < most) ++p.group_log2;
-  page_grow_kernel<<<CL_CTAS, CL_THREADS, 0, static_cast<cudaStream_t>(stream)>>>(p);
-  note_launch();
-  return done(cudaGetLastError());
+  return done(launch_cluster(page_grow_kernel<1>, page_grow_kernel<CL_CTAS>, n_pages <= CL_SMALL && rows * most <= CL_SMALL, p,
+                             static_cast<cudaStream_t>(stream)));
 }
 
 lilicorr_status lilicorr_kv8_free(int32_t* refs, int64_t n_pages, int32_t* table, int64_t rows, int64_t row_stride, int32_t cols,
@@ -652,9 +698,7 @@ lilicorr_status lilicorr_kv8_compact(const lilicorr_kv8_cache* caches, int32_t n
   pl.count = reinterpret_cast<int32_t*>(ws + 2 * part);
   pl.live = live;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  page_plan_kernel<<<CL_CTAS, CL_THREADS, 0, st>>>(pl);
-  note_launch();
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = launch_cluster(page_plan_kernel<1>, page_plan_kernel<CL_CTAS>, n_pages <= CL_SMALL, pl, st);
   for (int i = 0, j = 0; e == cudaSuccess && (i < n_caches || j < n_tables); i += MV_CACHES, j += MV_TABLES) {
     MoveParams p{};
     const int nc = std::max(0, std::min(n_caches - i, MV_CACHES));
