@@ -485,6 +485,16 @@ __global__ void __launch_bounds__(32 * CR_WARPS, 1)
       } else if (d0 < chunks || chunks == 0) {
         const int row = (two ? g * CR_HALF : 0) + r;
         const bool there = row < x.rows && (chunks > 0 || two || g == 0);
+        // where the row goes; and 16 bytes of 32 columns of four rows that the lane stores for the warp
+        const int i = there ? (x.row0 + row) / p.group : 0, j = there ? x.row0 + row - i * p.group : 0;
+        const int64_t at = there ? (x.q0 + i) * p.q_heads + int64_t(x.h) * p.group + j : -1;
+        const int piece = lane & 3;
+        __nv_bfloat16* to[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int64_t y = __shfl_sync(FULL_MASK, at, 8 * e + (lane >> 2));
+          to[e] = y < 0 ? nullptr : p.out + y * p.D + 8 * piece;
+        }
         float f0 = 1.f, f1 = 0.f;
         if (l == 0.f) m = -INFINITY;  // (a NaN stays)
         if (both) {
@@ -502,12 +512,10 @@ __global__ void __launch_bounds__(32 * CR_WARPS, 1)
           tc_fence_after();
         }
         if (x.whole) {
-          const float inv = l == 0.f ? 0.f : 1.f / l;
+          const float inv = l == 0.f ? 0.f : __frcp_rn(l);
           f0 *= inv;
           f1 *= inv;
         }
-        const int i = there ? (x.row0 + row) / p.group : 0, j = there ? x.row0 + row - i * p.group : 0;
-        const int64_t at = (x.q0 + i) * p.q_heads + int64_t(x.h) * p.group + j;
         float* part = p.part + int64_t(x.slot) * CR_ROWS * (DP + 2);
 #pragma unroll 1
         for (int w0 = 0; w0 < DP; w0 += 32) {
@@ -516,8 +524,17 @@ __global__ void __launch_bounds__(32 * CR_WARPS, 1)
             tmem_ld32_begin(t_o + w0, o);
             tmem_ld32_end(o);
           }
+          if (chunks > 0) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = chunks > 0 ? o[e] * f0 : 0.f;
+            for (int e = 0; e < 32; e += 2) {
+              const float2 y = __fmul2_rn(make_float2(o[e], o[e + 1]), make_float2(f0, f0));
+              o[e] = y.x;
+              o[e + 1] = y.y;
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = 0.f;
+          }
           if (both) {
             float z[32];
             tmem_ld32_begin(t_lane + CR_O + DP + w0, z);
@@ -546,13 +563,11 @@ __global__ void __launch_bounds__(32 * CR_WARPS, 1)
               *reinterpret_cast<uint4*>(stage + lane * 64 + ((q ^ (lane >> 1 & 3)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
             }
             __syncwarp();
-            const int q = lane & 3;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const int rr = 8 * e + (lane >> 2);
-              const int64_t to = __shfl_sync(FULL_MASK, at, rr);
-              const uint4 v = *reinterpret_cast<const uint4*>(stage + rr * 64 + ((q ^ (rr >> 1 & 3)) << 4));
-              if (__shfl_sync(FULL_MASK, static_cast<int>(there), rr) && w0 + 8 * q < p.D) *reinterpret_cast<uint4*>(p.out + to * p.D + w0 + 8 * q) = v;
+              const uint4 v = *reinterpret_cast<const uint4*>(stage + rr * 64 + ((piece ^ (rr >> 1 & 3)) << 4));
+              if (to[e] && w0 + 8 * piece < p.D) *reinterpret_cast<uint4*>(to[e] + w0) = v;
             }
             __syncwarp();
           } else if (there) {
