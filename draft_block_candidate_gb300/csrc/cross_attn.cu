@@ -650,7 +650,9 @@ cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorM
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   PdlScope pdl(true);
-  e = launch_k(kv8_join_kernel<DP, CR_ROWS, 4, 16, CrossParams>, dim3(grid, 16), dim3(128), 0, stream, p, grid);
+  // (a warp takes four rows of a tile in two parts)
+  const int most = static_cast<int>(std::min<int64_t>(CR_ROWS, int64_t(p.max_new) * p.group));
+  e = launch_k(kv8_join_kernel<DP, CR_ROWS, 4, 16, CrossParams>, dim3(grid, (most + 15) / 16), dim3(128), 0, stream, p, grid, (most + 15) / 16 * 16);
   if (e == cudaSuccess) note_launch(2);
   return e;
 }

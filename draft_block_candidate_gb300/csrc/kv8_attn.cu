@@ -768,7 +768,7 @@ cudaError_t launch(const CUtensorMap& tm, const AttnParams& prm, int grid, cudaS
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   PdlScope pdl(true);
-  e = launch_k(kv8_join_kernel<D, ROWS, 4, 8>, dim3(grid, 8), dim3(128), 0, stream, prm, grid);
+  e = launch_k(kv8_join_kernel<D, ROWS, 4, 8>, dim3(grid, 8), dim3(128), 0, stream, prm, grid, ROWS);
   if (e == cudaSuccess) note_launch(2);
   return e;
 }

@@ -498,7 +498,7 @@ cudaError_t launch(const AttnParams& prm, int runs, cudaStream_t stream) {
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   PdlScope pdl(true);
-  e = launch_k(kv8_join_kernel<D, RT, RT, 1>, dim3(runs), dim3(32 * RT), 0, stream, prm, runs);
+  e = launch_k(kv8_join_kernel<D, RT, RT, 1>, dim3(runs), dim3(32 * RT), 0, stream, prm, runs, RT);
   if (e == cudaSuccess) note_launch(2);
   return e;
 }
