@@ -263,11 +263,11 @@ __global__ void __launch_bounds__(32 * CR_WARPS, 1)
     const int g = warp - CR_MMA;
     const uint64_t d_k = tile_desc<128>(sm, 16), d_q = tile_desc<128>(sm + S::OFF_Q, 16), d_v = tile_desc<128>(sm + S::OFF_V, SUB);
     const uint32_t t_s = tmem + CR_S + g * 128, t_o = tmem + CR_O + g * DP;
-    int pi = 0, it = 0, n = 0, t = 0, qs = 0;  // chunks; the half's chunks and pieces; halves of q
+    int pi = 0, it = 0, n = 0, t = 0, qs = 0, i0 = 0;  // chunks; the half's chunks and pieces; halves of q; chunks taken in turn
     CrossPiece x;
     while (next_piece(pi, x, false)) {
       const bool two = x.rows > CR_HALF;
-      const int step = two ? 1 : 2, d0 = two ? 0 : g, chunks = x.cn - x.c0;
+      const int step = two ? 1 : 2, d0 = two ? 0 : (g - i0) & 1, chunks = x.cn - x.c0;
       const int slot = (qs + (two ? g : 0)) & 1;
       const uint64_t q = d_q + (slot * T >> 4);
       // (a half without a chunk waits too: what it leaves below is then of this use of the slot)
@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(32 * CR_WARPS, 1)
       auto keys = [&](int d) {  // waits for chunk d's keys
         const int i = it + d;
         ok = wait_warp(&kfull[i % KS], (i / KS) & 1, ERR_KV8_FULL_WAIT) && ok;
-        if (!two && (d & 1) != g && lane == 0) mbar_arrive(&kempty[i % KS]);  // the other half's
+        if (!two && ((d ^ d0) & 1) && lane == 0) mbar_arrive(&kempty[i % KS]);  // the other half's
       };
       auto scores = [&](int d) {
         const int i = (it + d) % KS;
@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(32 * CR_WARPS, 1)
       for (int d = 0; d < chunks; ++d) {
         const int i = it + d, sv = i % VS;
         ok = wait_warp(&vfull[sv], (i / VS) & 1, ERR_KV8_PV_WAIT) && ok;
-        if (!two && (d & 1) != g) {
+        if (!two && ((d ^ d0) & 1)) {
           if (lane == 0) mbar_arrive(&vempty[sv]);
           continue;
         }
@@ -344,6 +344,7 @@ __global__ void __launch_bounds__(32 * CR_WARPS, 1)
         ++n;
       }
       it += chunks;
+      i0 += two ? 0 : chunks;
       qs += two ? 2 : 1;
     }
   } else if (warp == CR_Q) {
@@ -398,12 +399,14 @@ __global__ void __launch_bounds__(32 * CR_WARPS, 1)
     const uint32_t t_s = t_lane + CR_S + g * 128, t_o = t_lane + CR_O + g * DP;
     const float a = p.scale2;
     uint8_t* stage = sm + S::OFF_ST + warp * 2048;
-    // This half's chunks; before x: each half's pieces, and those that the second handed over.
-    int n = 0, pi = 0, t[2] = {0, 0}, u = 0, v = 0;
+    // This half's chunks; before x: each half's pieces, those that one half handed over to the other, chunks of tiles
+    // that both took, and chunks taken in turn.
+    int n = 0, pi = 0, t[2] = {0, 0}, u = 0, v = 0, i0 = 0;
     CrossPiece x;
     while (next_piece(pi, x, true)) {
       const bool two = x.rows > CR_HALF;
-      const int step = two ? 1 : 2, d0 = two ? 0 : g, chunks = x.cn - x.c0;
+      const int step = two ? 1 : 2, chunks = x.cn - x.c0;
+      const int f = two ? g : i0 & 1, d0 = two || g == f ? 0 : 1;  // f: the half that takes the first chunk
       const bool any = (two ? g * CR_HALF : 0) + 32 * k < x.rows;  // of the warp's rows
       // (a row that is not there has weights of 0)
       float m = (two ? g * CR_HALF : 0) + r < x.rows ? -INFINITY : INFINITY, l = 0.f;
@@ -476,15 +479,16 @@ __global__ void __launch_bounds__(32 * CR_WARPS, 1)
         }
       }
 
-      // The outputs.  Where both halves stand for the same rows, the first one writes them.
+      // The outputs.  Where both halves stand for the same rows, the one that had the first chunk writes them.
       const bool both = !two && chunks > 1;
-      if (g == 1 && both) {
+      const int o = 1 - g;
+      if (g != f && both) {
         s_ml[u & 1][r] = make_float2(m, l);
         __syncwarp();
         if (lane == 0) mbar_arrive(&met[u & 1][k]);
       } else if (d0 < chunks || chunks == 0) {
         const int row = (two ? g * CR_HALF : 0) + r;
-        const bool there = row < x.rows && (chunks > 0 || two || g == 0);
+        const bool there = row < x.rows && (chunks > 0 || two || g == f);
         // where the row goes; and 16 bytes of 32 columns of four rows that the lane stores for the warp
         const int i = there ? (x.row0 + row) / p.group : 0, j = there ? x.row0 + row - i * p.group : 0;
         const int64_t at = there ? (x.q0 + i) * p.q_heads + int64_t(x.h) * p.group + j : -1;
@@ -505,7 +509,7 @@ __global__ void __launch_bounds__(32 * CR_WARPS, 1)
           f1 = ml.y == 0.f ? 0.f : ex2(ml.x - top);
           l = l * f0 + ml.y * f1;
           m = top;
-          wait_warp(&pvdone[1], t[1] & 1, ERR_KV8_PV_WAIT);
+          wait_warp(&pvdone[o], t[o] & 1, ERR_KV8_PV_WAIT);
         }
         if (chunks > 0) {
           wait_warp(&pvdone[g], t[g] & 1, ERR_KV8_PV_WAIT);
@@ -517,37 +521,41 @@ __global__ void __launch_bounds__(32 * CR_WARPS, 1)
           f1 *= inv;
         }
         float* part = p.part + int64_t(x.slot) * CR_ROWS * (DP + 2);
+        if (!any && chunks > 0 && lane == 0) {
+          mbar_arrive(&left[g]);
+          if (both) mbar_arrive(&left[o]);
+        }
 #pragma unroll 1
-        for (int w0 = 0; w0 < DP; w0 += 32) {
-          float o[32];
+        for (int w0 = any ? 0 : DP; w0 < DP; w0 += 32) {
+          float y[32];
           if (chunks > 0) {
-            tmem_ld32_begin(t_o + w0, o);
-            tmem_ld32_end(o);
+            tmem_ld32_begin(t_o + w0, y);
+            tmem_ld32_end(y);
           }
           if (chunks > 0) {
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
-              const float2 y = __fmul2_rn(make_float2(o[e], o[e + 1]), make_float2(f0, f0));
-              o[e] = y.x;
-              o[e + 1] = y.y;
+              const float2 yy = __fmul2_rn(make_float2(y[e], y[e + 1]), make_float2(f0, f0));
+              y[e] = yy.x;
+              y[e + 1] = yy.y;
             }
           } else {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = 0.f;
+            for (int e = 0; e < 32; ++e) y[e] = 0.f;
           }
           if (both) {
             float z[32];
-            tmem_ld32_begin(t_lane + CR_O + DP + w0, z);
+            tmem_ld32_begin(t_lane + CR_O + o * DP + w0, z);
             tmem_ld32_end(z);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = fmaf(z[e], f1, o[e]);
+            for (int e = 0; e < 32; ++e) y[e] = fmaf(z[e], f1, y[e]);
           }
           if (w0 + 32 == DP && chunks > 0) {  // O has been read
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
               mbar_arrive(&left[g]);
-              if (both) mbar_arrive(&left[1]);
+              if (both) mbar_arrive(&left[o]);
             }
           }
           if (x.whole) {
@@ -557,7 +565,7 @@ __global__ void __launch_bounds__(32 * CR_WARPS, 1)
               uint32_t h[4];
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                const __nv_bfloat162 v = __floats2bfloat162_rn(o[8 * q + 2 * e], o[8 * q + 2 * e + 1]);
+                const __nv_bfloat162 v = __floats2bfloat162_rn(y[8 * q + 2 * e], y[8 * q + 2 * e + 1]);
                 h[e] = *reinterpret_cast<const uint32_t*>(&v);
               }
               *reinterpret_cast<uint4*>(stage + lane * 64 + ((q ^ (lane >> 1 & 3)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
@@ -573,7 +581,7 @@ __global__ void __launch_bounds__(32 * CR_WARPS, 1)
           } else if (there) {
             float4* dst = reinterpret_cast<float4*>(part + row * DP + w0);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+            for (int e = 0; e < 8; ++e) dst[e] = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
           }
         }
         if (there && !x.whole) {
@@ -583,9 +591,10 @@ __global__ void __launch_bounds__(32 * CR_WARPS, 1)
           p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * LN2_F;
         }
       }
-      t[0] += chunks > 0;
-      t[1] += chunks > (two ? 0 : 1);
+      t[f] += chunks > 0;
+      t[1 - f] += chunks > (two ? 0 : 1);
       u += both;
+      i0 += two ? 0 : chunks;
     }
   }
   tc_fence_before();
