@@ -33,9 +33,11 @@ struct AttnParams {
 // Each tile counts HEAD_UNITS more than its chunks, at its front, for what it costs beside them
 // (its q, its first maxima, its outputs), so that runs of many short tiles take no longer than
 // others.  Measured: 3, 4, 5 and 6 chunks' for 128 rows, 64 sequences of 16 new tokens, 93.7, 93.7,
-// 93.5 and 94.8 us (weights not yet held up in f16); 0, 1 and 2 for few, 128 sequences of one, 199.5, 197.1 and 198.0.
+// 93.5 and 94.8 us (weights not yet held up in f16); 0, 1 and 2 for few, 128 sequences of one,
+// 199.5, 197.1 and 198.0; 0, 1, 2 and 3 for 256 (cross attention, 8 requests of 2,048 rows), 511,
+// 474, 443 and 443.
 template <int ROWS>
-constexpr int HEAD_UNITS = ROWS == 128 ? 4 : 1;
+constexpr int HEAD_UNITS = ROWS == 128 ? 4 : ROWS == 256 ? 2 : 1;
 
 struct SeqUnits {
   int n, len, tiles, chunks;
