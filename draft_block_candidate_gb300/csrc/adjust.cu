@@ -18,22 +18,25 @@ static __device__ uint32_t g_err_adjust;
 // terms' magnitudes for each term, and rounded once; where that does not do (values near the ends of
 // the type, or not finite, counts of 2^24 and more) in 64 bits, which are slow on this part.
 //
-// One CTA for each piece of 32 KB of a row: it reads the piece (a warp's vectors after one coalesced load of their
-// mask; in place, what a mask leaves or takes whole is not read), works out meanwhile which of the history's tokens
-// lie in the piece and how often they count, writes the piece with its mask, and then the touched tokens over, while
-// their logits are still near.  It goes over the history twice: first each token sets its bit of a bit map of the
-// piece, whose running sums then give every token that is there a place in a list; then each token counts at its
-// place.  Neither pass waits for what its atomic operations find, and all sums are of integers.  Where there is only
-// a mask a kernel without all that does.
+// One CTA for each piece of a row: it reads the piece (a warp's vectors after one coalesced load of their mask; in
+// place, what a mask leaves or takes whole is not read), works out meanwhile which of the history's tokens lie in the
+// piece and how often they count, writes the piece with its mask, and then the touched tokens over, while their logits
+// are still near.  It goes over the history twice: first each token sets its bit of a bit map of the piece, whose
+// running sums then give every token that is there a place in a list; then each token counts at its place.  Neither
+// pass waits for what its atomic operations find, and all sums are of integers.  Where there is only a mask a kernel
+// without all that does.
 //
-// Tried and dropped (256 rows of 151,936 in bf16 with histories of up to 4,096, 64 biases and 16 grammars): a word for
-// each of a piece's tokens to count in, cleared and searched, 57 us (209 with 64-bit arithmetic and loops with few lanes
-// at work); two kernels, the second a CTA a row for the touched tokens alone, 41 with a table of the ids by their hash
-// and 43 with a bit map of the row: the tokens' logits are read and written one by one once the row has left the L2 cache.
-// (512 threads of four vectors: 47.4 us for 44.7 in the large case below.)
-constexpr int AJ_THREADS = 256;
-constexpr int AJ_VECS = 8;                           // vectors of 16 bytes of a lane
-constexpr int AJ_PIECE = AJ_THREADS * AJ_VECS * 16;  // bytes
+// Measured: 256 rows of 151,936 in bf16 with histories of up to 4,096, 64 biases and 16 grammars 41.5 us, of which the
+// histories are 13 (30 without them: every piece goes over all of its row's, and instructions bound it); with a
+// mask alone, 512 rows in place, 33 (25 at a copy's rate for the sectors that a mask takes in part).  Pieces of 64 KB by 512 threads,
+// 41.5 us; of 32 KB by 256, 45, and by 512, 51; of 48 KB by 384, 43; with a mask alone 256 threads are better (33 for 36).
+// Tried and dropped: a word for each of a piece's tokens to count in, cleared and searched, 57 us (209 with 64-bit
+// arithmetic and loops with few lanes at work); two kernels, the second a CTA a row for the touched tokens alone, 41 with
+// a table of the ids by their hash and 43 with a bit map of the row, when this took 45: the tokens' logits are read and
+// written one by one once the row has left the L2 cache.
+constexpr int AJ_VECS = 8;                                // vectors of 16 bytes of a lane
+constexpr int AJ_MASK = 256, AJ_TOUCH = 512;              // threads of a CTA of either kernel
+constexpr int aj_bytes(int threads) { return threads * AJ_VECS * 16; }  // of a piece
 constexpr int AJ_MAX_BIAS = 1024;
 
 struct AdjustParams {
@@ -157,7 +160,7 @@ __device__ __forceinline__ uint4 masked(uint4 v, uint32_t bits) {
 }
 
 // Tokens [t0, t0 + n) of a row: a piece, a warp's 32 * AJ_VECS vectors of it.  Read, and written with their mask.
-template <typename T, bool INPLACE>
+template <typename T, bool INPLACE, int THREADS>
 struct Piece {
   static constexpr int E = 16 / sizeof(T);
   static constexpr uint32_t FULL = (1u << E) - 1;
@@ -196,7 +199,7 @@ struct Piece {
   __device__ __forceinline__ void write(const T* x, T* o, const uint32_t* m, int t0, int n) const {
     if (INPLACE && !m) return;
     if (!INPLACE && (reinterpret_cast<uintptr_t>(x) ^ reinterpret_cast<uintptr_t>(o)) % 16 != 0) {
-      for (int t = threadIdx.x; t < n; t += AJ_THREADS) o[t] = !m || allowed(m, t0 + t) ? x[t] : minus_inf<T>();
+      for (int t = threadIdx.x; t < n; t += THREADS) o[t] = !m || allowed(m, t0 + t) ? x[t] : minus_inf<T>();
       return;
     }
     const int lane = threadIdx.x & 31, first = (threadIdx.x >> 5) * 32 * AJ_VECS;
@@ -234,8 +237,8 @@ __device__ __forceinline__ bool row_seen(const AdjustParams& p, int64_t r, int& 
 // ------------------------------------------------------------------------------- kernels
 
 template <typename T, bool INPLACE>
-__global__ void __launch_bounds__(AJ_THREADS, 4) adjust_mask_kernel(const AdjustParams p) {
-  constexpr int TOKENS = AJ_PIECE / sizeof(T);
+__global__ void __launch_bounds__(AJ_MASK, 4) adjust_mask_kernel(const AdjustParams p) {
+  constexpr int TOKENS = aj_bytes(AJ_MASK) / sizeof(T);
   const int64_t r = blockIdx.z * gridDim.y + blockIdx.y;  // (fits 32 bits: host)
   const int t0 = static_cast<int>(blockIdx.x) * TOKENS, n = min(TOKENS, p.V - t0);
   const uint32_t* m = nullptr;
@@ -244,41 +247,44 @@ __global__ void __launch_bounds__(AJ_THREADS, 4) adjust_mask_kernel(const Adjust
   if (!has) return;  // the row is left out
   const T* x = static_cast<const T*>(p.x) + r * p.x_stride + t0;
   T* o = static_cast<T*>(p.out) + r * p.out_stride + t0;
-  Piece<T, INPLACE> piece;
+  Piece<T, INPLACE, AJ_MASK> piece;
   piece.read(x, o, m, (p.V + 31) >> 5, t0, n);
   piece.write(x, o, m, t0, n);
 }
 
-// Calls f(id, position) for the first `seen` tokens of a history: by fours from the first 16-byte boundary on,
-// `ahead` being the thread's first ones.
+// Calls f(ids, position) for the first `seen` tokens of a history, by fours: from the first 16-byte boundary on, `ahead`
+// being the thread's first ones, then for the ends (whose other ids are -1).
 template <typename F>
 __device__ __forceinline__ void each_token(const int32_t* hist, int lead, int seen, int4 ahead, F f) {
-  const int tid = threadIdx.x, fours = (seen - lead) / 4;
-  if (tid < min(lead, seen)) f(__ldg(hist + tid), tid);
-  if (tid < seen - lead - 4 * fours) f(__ldg(hist + lead + 4 * fours + tid), lead + 4 * fours + tid);
+  const int tid = threadIdx.x, fours = max(0, seen - lead) / 4, tail = lead + 4 * fours;
 #pragma unroll 1
-  for (int i = tid; i < fours; i += AJ_THREADS) {
+  for (int i = tid; i < fours; i += AJ_TOUCH) {
     const int4 q = ahead;
-    if (i + AJ_THREADS < fours) ahead = __ldg(reinterpret_cast<const int4*>(hist + lead) + i + AJ_THREADS);
-    const int at = lead + 4 * i;
-    f(q.x, at);
-    f(q.y, at + 1);
-    f(q.z, at + 2);
-    f(q.w, at + 3);
+    if (i + AJ_TOUCH < fours) ahead = __ldg(reinterpret_cast<const int4*>(hist + lead) + i + AJ_TOUCH);
+    f(q, lead + 4 * i);
   }
+  const int at = tid < 4 ? tid : tail + tid - 4;  // (lead is at most 3, and so is what is left)
+  if (tid < 8 && at < (tid < 4 ? min(lead, seen) : seen)) f(make_int4(__ldg(hist + at), -1, -1, -1), at);
+}
+// Atomic operations on shared memory where t < n, without a branch.
+__device__ __forceinline__ void or_below(uint32_t t, uint32_t n, uint32_t at, uint32_t v) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.lt.u32 p, %0, %1;\n\t@p red.shared.or.b32 [%2], %3;\n\t}" ::"r"(t), "r"(n), "r"(at), "r"(v) : "memory");
+}
+__device__ __forceinline__ void add_below(uint32_t t, uint32_t n, uint32_t at, uint32_t v) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.lt.u32 p, %0, %1;\n\t@p red.shared.add.u32 [%2], %3;\n\t}" ::"r"(t), "r"(n), "r"(at), "r"(v) : "memory");
 }
 
 template <typename T, bool INPLACE>
-__global__ void __launch_bounds__(AJ_THREADS, 4) adjust_touch_kernel(const AdjustParams p) {
-  constexpr int TOKENS = AJ_PIECE / sizeof(T), WORDS = TOKENS / 32;
-  constexpr int EACH = WORDS > AJ_THREADS ? WORDS / AJ_THREADS : 1;  // words of the bit map for each thread
+__global__ void __launch_bounds__(AJ_TOUCH, 2) adjust_touch_kernel(const AdjustParams p) {
+  constexpr int TOKENS = aj_bytes(AJ_TOUCH) / sizeof(T), WORDS = TOKENS / 32;
+  constexpr int EACH = WORDS > AJ_TOUCH ? WORDS / AJ_TOUCH : 1;  // words of the bit map for each thread
   extern __shared__ __align__(16) uint32_t s_count[];                       // [list] how often a token of the list counts
   uint16_t* const s_token = reinterpret_cast<uint16_t*>(s_count + p.list);  // [list] its place in the piece
   __shared__ __align__(16) uint32_t s_map[WORDS];                           // a bit a token
   __shared__ uint16_t s_place[WORDS];                                       // tokens of the list before a word's
   __shared__ __align__(16) int s_id[AJ_MAX_BIAS];
   __shared__ uint32_t s_biased[WORDS];                                      // a bit a token of the bias list
-  __shared__ int s_sum[AJ_THREADS / 32];
+  __shared__ int s_sum[AJ_TOUCH / 32];
   __shared__ int s_twice;  // whether a token of the piece has several biases
   __shared__ Penalties s_pen;
   const int tid = threadIdx.x, lane = tid & 31;
@@ -299,12 +305,12 @@ __global__ void __launch_bounds__(AJ_THREADS, 4) adjust_touch_kernel(const Adjus
   if (!has || !counts) return;  // the row is left out
   const T* x = static_cast<const T*>(p.x) + r * p.x_stride + t0;
   T* o = static_cast<T*>(p.out) + r * p.out_stride + t0;
-  Piece<T, INPLACE> piece;
+  Piece<T, INPLACE, AJ_TOUCH> piece;
   piece.read(x, o, m, (p.V + 31) >> 5, t0, n);
   const int from = p.from ? __ldg(p.from + h) : 0;
-  for (int i = tid; i < WORDS; i += AJ_THREADS) s_map[i] = s_biased[i] = 0;
-  for (int i = tid; i < p.n_bias; i += AJ_THREADS) s_id[i] = __ldg(p.bias_id + h * p.n_bias + i);
-  if (tid == AJ_THREADS - 1) {
+  for (int i = tid; i < WORDS; i += AJ_TOUCH) s_map[i] = s_biased[i] = 0;
+  for (int i = tid; i < p.n_bias; i += AJ_TOUCH) s_id[i] = __ldg(p.bias_id + h * p.n_bias + i);
+  if (tid == AJ_TOUCH - 1) {
     Penalties q{p.rep ? __ldg(p.rep + h) : 1.f, 0.f, 0.f, p.freq ? __ldg(p.freq + h) : 0.f, p.pres ? __ldg(p.pres + h) : 0.f,
                 p.rep != nullptr, s_id, p.bias + h * p.n_bias};
     q.inv = 1.f / q.rho;
@@ -314,12 +320,16 @@ __global__ void __launch_bounds__(AJ_THREADS, 4) adjust_touch_kernel(const Adjus
   }
   __syncthreads();
   // 1. which tokens there are
-  each_token(hist, lead, seen, ahead, [&](int id, int) {
-    const uint32_t t = static_cast<uint32_t>(id - t0);
-    if (t < static_cast<uint32_t>(n)) atomicOr(s_map + (t >> 5), 1u << (t & 31));
+  each_token(hist, lead, seen, ahead, [&](int4 q, int) {
+    const int id[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t t = static_cast<uint32_t>(id[k]) - t0;
+      or_below(t, n, smem_addr(s_map) + (t >> 5) * 4, __funnelshift_l(0u, 1u, t));
+    }
   });
-  for (int i = tid; i < p.n_bias; i += AJ_THREADS) {
-    const uint32_t t = static_cast<uint32_t>(s_id[i] - t0);
+  for (int i = tid; i < p.n_bias; i += AJ_TOUCH) {
+    const uint32_t t = static_cast<uint32_t>(s_id[i]) - t0;
     if (t < static_cast<uint32_t>(n) && (atomicOr(s_biased + (t >> 5), 1u << (t & 31)) >> (t & 31) & 1)) s_twice = 1;
   }
   __syncthreads();
@@ -339,7 +349,7 @@ __global__ void __launch_bounds__(AJ_THREADS, 4) adjust_touch_kernel(const Adjus
   }
   if (lane == 31) s_sum[tid >> 5] = at;
   __syncthreads();
-  int all = lane < AJ_THREADS / 32 ? s_sum[lane] : 0;
+  int all = lane < AJ_TOUCH / 32 ? s_sum[lane] : 0;
   at += __reduce_add_sync(FULL_MASK, lane < tid >> 5 ? all : 0) - mine;
   all = __reduce_add_sync(FULL_MASK, all);
   if (tid * EACH < WORDS)
@@ -353,22 +363,29 @@ __global__ void __launch_bounds__(AJ_THREADS, 4) adjust_touch_kernel(const Adjus
     }
   __syncthreads();
   auto place = [&](uint32_t t) { return s_place[t >> 5] + __popc(s_map[t >> 5] & ((1u << (t & 31)) - 1)); };
-  // 2. how often they count
-  each_token(hist, lead, seen, ahead, [&](int id, int i) {
-    const uint32_t t = static_cast<uint32_t>(id - t0);
-    if (i >= from && t < static_cast<uint32_t>(n)) atomicAdd(s_count + place(t), 1u);
+  // 2. how often they count, where a penalty asks for it
+  if (p.freq || p.pres) each_token(hist, lead, seen, ahead, [&](int4 q, int i) {
+    const int id[4] = {q.x, q.y, q.z, q.w};
+    uint32_t t[4], at[4] = {};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      t[k] = i + k >= from ? static_cast<uint32_t>(id[k]) - t0 : UINT_MAX;
+      if (t[k] < static_cast<uint32_t>(n)) at[k] = smem_addr(s_count) + 4 * place(t[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) add_below(t[k], n, at[k], 1u);
   });
   piece.write(x, o, m, t0, n);
   __syncthreads();
-  for (int i = tid; i < all; i += AJ_THREADS) {
+  for (int i = tid; i < all; i += AJ_TOUCH) {
     const int t = s_token[i];
     if (!(s_biased[t >> 5] >> (t & 31) & 1) && (!m || allowed(m, t0 + t))) touch(o + t, static_cast<float>(x[t]), true, s_count[i], 0, 0, 0, &s_pen);
   }
   // tokens of the bias list, by the first entry that names them (from the last warps on, whose lists are the shortest)
   const bool twice = s_twice;
-  for (int i = AJ_THREADS - 1 - tid; i < p.n_bias; i += AJ_THREADS) {
+  for (int i = AJ_TOUCH - 1 - tid; i < p.n_bias; i += AJ_TOUCH) {
     const int id = s_id[i];
-    const uint32_t t = static_cast<uint32_t>(id - t0);
+    const uint32_t t = static_cast<uint32_t>(id) - t0;
     if (t >= static_cast<uint32_t>(n) || (m && !allowed(m, id))) continue;
     int j = twice ? 0 : i;
     while (s_id[j] != id) ++j;
@@ -403,7 +420,7 @@ cudaError_t adjust_launch(const AdjustParams& p, int64_t pieces, bool touch, cud
   auto go = [&](auto kern) -> cudaError_t {
     cudaError_t e = smem > 32 * 1024 ? allow_dynamic_smem(reinterpret_cast<const void*>(kern), smem) : cudaSuccess;
     if (e != cudaSuccess) return e;
-    kern<<<grid, AJ_THREADS, smem, stream>>>(p);
+    kern<<<grid, touch ? AJ_TOUCH : AJ_MASK, smem, stream>>>(p);
     e = cudaGetLastError();
     if (e == cudaSuccess) note_launch();
     return e;
@@ -456,7 +473,7 @@ extern "C" lilicorr_status lilicorr_adjust_logits(const lilicorr_adjust* a, void
   p.n_masks = static_cast<int>(a->n_masks); p.mask_index = a->mask_index;
   const bool touch = a->history || a->n_bias > 0;
   if (!touch && !a->mask && a->logits == a->out) return LILICORR_OK;
-  const int64_t tokens = AJ_PIECE / es;
+  const int64_t tokens = aj_bytes(touch ? AJ_TOUCH : AJ_MASK) / es;
   const int64_t pieces = (a->V + tokens - 1) / tokens;
   p.rows = static_cast<int>(a->rows);
   if (a->rows > INT_MAX - 65536 || a->rows * pieces > INT_MAX) return bad("lilicorr_adjust_logits: rows * V is too large for one call");

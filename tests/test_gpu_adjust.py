@@ -99,6 +99,17 @@ def test_adjust_matches_reference(lc, rows, V, groups, cap, n_bias, masks, dtype
     check(got, keep, kw)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("V", [32768, 32767, 65536])
+def test_adjust_every_token_seen(lc, dtype, V):
+    x, kw = make(3, V, dtype, 3, 70000, 9, 2, V)
+    for h in kw["history"]:  # all of them, at places that differ from row to row
+        at = torch.randperm(70000, device="cuda", generator=gen(4))[:V]
+        h[at] = torch.randperm(V, device="cuda", generator=gen(5)).to(torch.int32)
+    kw["seen"][1] = 70000
+    check(lc.adjust_logits(x, out=torch.empty_like(x), **kw), x, kw)
+
+
 @pytest.mark.parametrize("which", ["repetition", "presence", "frequency", "seen"])
 def test_adjust_each_penalty_alone(lc, which):
     x, kw = make(4, 300, torch.float32, 2, 100, 0, 0, 5)
