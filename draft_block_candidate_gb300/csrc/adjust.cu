@@ -88,7 +88,7 @@ __device__ __forceinline__ void store_double(__nv_bfloat16* p, double y) { *p = 
 // A touched token's value from its logit, whether it was seen, how often it counts, and the biases of entries
 // [e0, e1) of the list whose id is its own.
 struct Penalties {
-  float rho, inv, inv_lo, freq, pres;  // inv + inv_lo = 1 / rho, but for 2^-46
+  float rho, inv, inv_lo, freq, pres;  // inv + inv_lo = 1 / rho, but for 2^-46 (NaN for a large rho)
   int rep;
   const int* ids;
   const float* bias;
@@ -313,7 +313,8 @@ __global__ void __launch_bounds__(AJ_TOUCH, 2) adjust_touch_kernel(const AdjustP
   if (tid == AJ_TOUCH - 1) {
     Penalties q{p.rep ? __ldg(p.rep + h) : 1.f, 0.f, 0.f, p.freq ? __ldg(p.freq + h) : 0.f, p.pres ? __ldg(p.pres + h) : 0.f,
                 p.rep != nullptr, s_id, p.bias + h * p.n_bias};
-    q.inv = 1.f / q.rho;
+    // (what is left of a reciprocal near the least normal number has too few bits: in 64 bits then)
+    q.inv = fabsf(q.rho) < 1.2e30f ? 1.f / q.rho : NAN;
     q.inv_lo = fmaf(-q.inv, q.rho, 1.f) * q.inv;
     s_pen = q;
     s_twice = 0;

@@ -188,6 +188,23 @@ def test_adjust_values_near_the_ends_of_the_type(lc, dtype):
     check(lc.adjust_logits(x, out=torch.empty_like(x), **kw), x, kw)
 
 
+@pytest.mark.parametrize("rho", [3.4e38, -2.9e38, 1.3e30, 1.1e30, 1.2e-38, 1e-40, 0.0])
+def test_adjust_penalties_near_the_ends_of_their_type(lc, rho):
+    """Logits whose quotient, or product, is an ordinary number again: its bits are all there."""
+    V = 512
+    x = torch.logspace(-38, 38, V, device="cuda") * torch.where(torch.arange(V, device="cuda") % 2 == 0, 1.0, -1.0)
+    hist = torch.arange(V, dtype=torch.int32, device="cuda")[None]
+    rep = torch.tensor([rho], device="cuda")
+    got = lc.adjust_logits(x[None].contiguous(), out=torch.empty(1, V, device="cuda"), history=hist,
+                           seen=torch.tensor([V], dtype=torch.int32, device="cuda"), repetition=rep)[0]
+    want = torch.where(x > 0, x.double() / rep.double(), x.double() * rep.double())
+    far = want.abs() >= 2.0 ** 128 * (1 - 2.0 ** -25)  # rounded to an infinity
+    assert torch.equal(got[far].double(), torch.sign(want[far]) * math.inf)
+    # a product or quotient by itself, off by 2^-46 of its size, rounded once (by half of the smallest step below 2^-126)
+    near = want[~far]
+    assert ((got[~far].double() - near).abs() <= near.abs() * (2.0 ** -24 + 2.0 ** -46) + 2.0 ** -150).all()
+
+
 def test_adjust_ties_of_bf16_are_told_by_the_whole_sum(lc):
     """Sums a hair above and below a bf16 tie, by less than a float's step: rounded to their own side."""
     tie = 1 + 2.0 ** -8  # between 1 and 1 + 2^-7
