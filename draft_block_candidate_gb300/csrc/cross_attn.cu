@@ -250,12 +250,9 @@ __global__ void __launch_bounds__(32 * CR_WARPS, 1)
       now = next;
       ok_run = ok_run && more;
     }
-    if (s_fail) {  // what is in flight has to land
-      for (int i = max(0, kit - KS); i < kit; ++i)
-        mbar_wait_bounded(&kfull[i % KS], (i / KS) & 1, &g_err_kv8_attn, ERR_KV8_EMPTY_WAIT);
-      for (int i = max(0, vit - VS); i < vit; ++i)
-        mbar_wait_bounded(&vfull[i % VS], (i / VS) & 1, &g_err_kv8_attn, ERR_KV8_EMPTY_WAIT);
-    }
+    // what is in flight has to land (it has, unless a wait gave up)
+    for (int i = max(0, kit - KS); i < kit; ++i) mbar_wait_bounded(&kfull[i % KS], (i / KS) & 1, &g_err_kv8_attn, ERR_KV8_EMPTY_WAIT);
+    for (int i = max(0, vit - VS); i < vit; ++i) mbar_wait_bounded(&vfull[i % VS], (i / VS) & 1, &g_err_kv8_attn, ERR_KV8_EMPTY_WAIT);
   } else if (warp >= CR_MMA && warp < CR_Q) {
     // ====== half g's products: S of its next chunk takes the place of P of the one before, and so is issued
     // behind the product that reads it (the tensor cores do what one thread issues in order) ======
@@ -392,6 +389,7 @@ __global__ void __launch_bounds__(32 * CR_WARPS, 1)
         if (lane == 0) mbar_arrive(&qready[s]);
       }
     }
+    for (int i = max(0, qs - S::QS); i < qs; ++i) mbar_wait_bounded(&qready[i & 1], (i >> 1) & 1, &g_err_kv8_attn, ERR_KV8_S_WAIT);
   } else {
     // ====== softmax: half g, rows 32 k + lane of it; then the tile's outputs ======
     const int g = warp >> 2, k = warp & 3, r = 32 * k + lane;
@@ -698,7 +696,7 @@ lilicorr_status lilicorr_cross_attention(const void* q, int64_t q_token_stride, 
   if (!why && int64_t(max_new) * (q_heads / kv_heads) > INT_MAX - 256) why = "max_new * q_heads / kv_heads is too large";
   if (!why && (int64_t(max_new) * (q_heads / kv_heads) / CR_ROWS + 1) * kv_heads * ((total_kv + 127) / 128 + 8) > UINT_MAX)
     why = "max_new * q_heads * the states are too large";
-  if (!why && !std::isfinite(scale)) why = "scale is not finite";
+  if (!why && !std::isfinite(scale * LOG2E_F)) why = "scale, or scale * log2 e, is not finite";
   if (why) return fail(LILICORR_ERR_INVALID_ARG, why);
   if (!workspace || workspace_bytes < workspace_of(head_dim) || reinterpret_cast<uintptr_t>(workspace) % 256)
     return fail(LILICORR_ERR_WORKSPACE, "lilicorr_cross_attention: workspace missing, too small or misaligned");

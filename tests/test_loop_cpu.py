@@ -147,7 +147,7 @@ def cross(lib, q=FAKE, qt=1024, qh=128, total=8, heads=8, k=2 * FAKE, kt=512, kh
     dict(D=0), dict(D=136), dict(D=20), dict(q_start=None), dict(kv_start=None), dict(kv_len=None), dict(batch=0), dict(batch=1 << 21),
     dict(total=0), dict(total=1 << 31), dict(total_kv=0), dict(total_kv=1 << 31), dict(max_new=0), dict(max_new=1 << 25), dict(kv_heads=0),
     dict(kv_heads=3), dict(kv_heads=1025, heads=1025), dict(heads=0), dict(heads=2 * 1025), dict(kt=0), dict(vh=0), dict(kt=120), dict(out=None),
-    dict(out=FAKE + 8), dict(scale=float("nan")), dict(scale=float("inf")), dict(max_new=1 << 22, heads=2048), dict(out=FAKE),
+    dict(out=FAKE + 8), dict(scale=float("nan")), dict(scale=float("inf")), dict(scale=-3e38), dict(max_new=1 << 22, heads=2048), dict(out=FAKE),
     dict(max_new=1 << 20, heads=1024, kv_heads=1024, total_kv=1 << 30, kt=1 << 18, vt=1 << 18, v=1 << 60),
     dict(out=2 * FAKE + 1024), dict(out=3 * FAKE), dict(lse=8 * FAKE + 64), dict(lse=FAKE + 128)])
 def test_cross_refuses(lib, kw):
