@@ -426,11 +426,12 @@ lilicorr_status lilicorr_kv8_attention(const lilicorr_kv8_cache* cache, const vo
  *   x2 = x1 - frequency * g - (g > 0 ? presence : 0)
  *   x3 = x2 + the sum of v's biases in the list, in its order
  *   out = x3, or -inf where the row's mask has a 0 for v,
- * in 64 bits and rounded once; a token that nothing touches is copied bit for bit (a NaN that a mask
+ * in pairs of f32 (off by 2^-46 of the terms' magnitudes for each of them), or in 64 bits where those do
+ * not do, and rounded once; a token that nothing touches is copied bit for bit (a NaN that a mask
  * takes out becomes -inf).  out is the logits themselves (with the same row stride), or apart from
  * them; what lies behind a row's V logits is not touched.
  *   logits, out  [rows, V] F32 or BF16, rows a stride >= V apart, element aligned
- *   history      nullable [groups, cap] int32, rows history_stride apart; ids outside 0..V-1 are passed over
+ *   history      nullable [groups, cap] int32, cap < 2^29, rows history_stride apart; ids outside 0..V-1 are passed over
  *   seen         [rows] int32, at most cap (else the row is left out, and bit 26 of the device error word set)
  *   counted_from nullable [groups] int32: frequency and presence count from there (0; the end of a prompt)
  *   repetition, presence, frequency  nullable [groups] f32 (1, 0 and 0)
@@ -463,8 +464,9 @@ lilicorr_status lilicorr_adjust_logits(const lilicorr_adjust* a, void* stream);
  * refs [n_pages] int32 counts, for each page, the entries of block tables that name it; a page with none
  * is free.  An entry of a table is the page that its row holds there; a negative one is none.  The calls
  * below keep the two in step; what they decide follows from the order of rows, columns and pages alone.
- * A page index of n_pages or more, or a page that is held but counted as free, sets bit 25 of the device
- * error word and is passed over.
+ * A page index of n_pages or more sets bit 25 of the device error word and is passed over, and so does a
+ * page that is held but counted as free where a call comes upon it (grow and free look at the pages that
+ * they touch, compact at those behind the live ones, fork at none).
  *
  * lilicorr_kv8_fork: row (b, j) of the table [batch, beams, cols] becomes row (b, parent[b, j]), in
  * place, and refs follows (hypotheses go on as their parents; a prompt's row is shared by all).  A parent

@@ -214,6 +214,22 @@ def test_copy_into_other_caches_and_bad_pages(lc):
         assert all(torch.equal(x, y) for x, y in zip(parts(c), w))
 
 
+def test_copy_of_pages_behind_32_bits(lc):
+    """Pages whose first vector of 16 bytes is the 2^31-th and further."""
+    n = (1 << 35) // (8 * 128 * 128) + 40
+    c = lc.KV8Cache(n, 8, 128, 128)
+    low, high = [3, 4, 5], [n - 40, n - 39, n - 1]
+    g = torch.Generator(device="cuda").manual_seed(7)
+    for t in parts(c):
+        for p in low + [n - 20]:
+            t[p] = torch.randint(0, 200, t[p].shape, generator=g, device="cuda").to(t.dtype)
+    src, dst = torch.tensor(low + [n - 20], dtype=torch.int32).cuda(), torch.tensor(high + [6], dtype=torch.int32).cuda()
+    lc.kv8_copy([c], src, dst)
+    for t in parts(c):
+        for p, q in zip(src.tolist(), dst.tolist()):
+            assert torch.equal(t[p], t[q])
+
+
 @pytest.mark.parametrize("n,held,layers", [(1, 0, 1), (1, 1, 1), (2, 1, 1), (40, 11, 2), (300, 150, 3), (300, 299, 1), (5000, 40, 17), (128, 0, 1)])
 @pytest.mark.parametrize("inplace", [False, True])
 def test_compact_matches_reference(lc, n, held, layers, inplace):
