@@ -11,10 +11,13 @@
 // memory and a group of four softmax warps, a thread a row.  Where the tile has more than 128 rows both
 // halves take every chunk, so that a chunk's keys and values are read from shared memory for 256 rows;
 // where it has fewer, both halves stand for the same rows and take the chunks in turn, and the outputs
-// are joined as they are written.  While one group forms its weights the tensor cores work for the other.
-// Warps: two groups of four for the softmax; four that bring q of the next tile and write the outputs of
-// the one before; one that loads keys and values through tensor maps; one that issues S = Q K^T and one
-// that issues O += P V.
+// are joined as they are written.  While one group forms its weights the tensor cores work for the other:
+// in tiles of 256 rows the groups' warps take turns from a row's maximum to its last weight, and a chunk's
+// weights are handed over by 64 columns, so that the second product begins halfway.
+// Warps: two groups of four for the softmax, which also write the outputs (through 2 KB of shared memory
+// each, so that four lanes write 64 bytes of a row); one that deals the run's pieces and loads keys and
+// values through tensor maps; one for each half that issues its products, S of the next chunk right behind
+// the O that reads the P in its place; one that brings the next tile's q.
 //
 // Roundings below f32: the weights are bf16 (off by 2^-8 of their value at most) for the second product, whose operands
 // have one type; the sums take them unrounded.  A row's maximum moves only where a score passes it by
@@ -452,6 +455,8 @@ __global__ void __launch_bounds__(32 * CR_WARPS, 1)
         float2 sum[2] = {make_float2(l, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
+          // (64 wide, where the products are half as long, the other half may begin earlier)
+          if (DP == 64 && w == 2 && two && lane == 0) mbar_arrive(&turn[g][k]);
           uint32_t h[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
@@ -471,10 +476,8 @@ __global__ void __launch_bounds__(32 * CR_WARPS, 1)
           }
         }
         l = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-        if (two) {
-          if (lane == 0) mbar_arrive(&turn[g][k]);
-          ++v;
-        }
+        if (DP != 64 && two && lane == 0) mbar_arrive(&turn[g][k]);
+        v += two;
       }
 
       // The outputs.  Where both halves stand for the same rows, the one that had the first chunk writes them.
