@@ -159,59 +159,70 @@ __device__ __forceinline__ uint4 masked(uint4 v, uint32_t bits) {
   }
 }
 
-// Tokens [t0, t0 + n) of a row: a piece, a warp's 32 * AJ_VECS vectors of it.  Read, and written with their mask.
+// Tokens [t0, t0 + n) of a row: a piece, a warp's 32 * AJ_VECS vectors of it, 32 apart for a lane.
 template <typename T, bool INPLACE, int THREADS>
 struct Piece {
   static constexpr int E = 16 / sizeof(T);
   static constexpr uint32_t FULL = (1u << E) - 1;
-  uint4 w[AJ_VECS];
   uint32_t bits[AJ_VECS / 4];  // of a vector's elements, 8 bits for each vector
-  int head, left;  // elements before the first whole vector; the lane's vectors, which are 32 apart, reach this far
+  int head, left;              // elements before the first whole vector; the lane's vectors reach this far
 
-  __device__ __forceinline__ void read(const T* x, const T* o, const uint32_t* m, int words, int t0, int n) {
-    const int lane = threadIdx.x & 31, first = (threadIdx.x >> 5) * 32 * AJ_VECS;
+  __device__ __forceinline__ static int first() { return (threadIdx.x >> 5) * 32 * AJ_VECS + (threadIdx.x & 31); }
+  __device__ __forceinline__ uint32_t of(int i) const { return bits[i / 4] >> (8 * (i % 4)) & FULL; }
+  // Whether x and o lie alike to the 16-byte grid.
+  __device__ __forceinline__ static bool alike(const T* x, const T* o) {
+    return INPLACE || (reinterpret_cast<uintptr_t>(x) ^ reinterpret_cast<uintptr_t>(o)) % 16 == 0;
+  }
+  __device__ __forceinline__ void look(const T* x, const T* o, const uint32_t* m, int words, int t0, int n) {
+    const int lane = threadIdx.x & 31;
     head = min(n, static_cast<int>((16 - reinterpret_cast<uintptr_t>(o) % 16) % 16 / sizeof(T)));
-    left = (n - head) / E - first - lane;
+    left = (n - head) / E - first();
+    if ((INPLACE && !m) || !alike(x, o)) left = -lane;  // (nothing to write, or one by one; no warp has vectors then)
 #pragma unroll
     for (int i = 0; i < AJ_VECS / 4; ++i) bits[i] = ~0u;
-    if (INPLACE ? !m : (reinterpret_cast<uintptr_t>(x) ^ reinterpret_cast<uintptr_t>(o)) % 16 != 0) {
-      left = 0;  // (nothing to write, or rows that lie differently to the 16-byte grid)
-      return;
-    }
-    const T* from = x + head + (first + lane) * E;
     if (m && left + lane > 0) {
 #pragma unroll
       for (int k = 0; k < AJ_VECS / 4; ++k) {
         bits[k] = 0;
         constexpr int PER = 4 * E;  // vectors, by a block of 1,024 tokens (f32: half of it)
-        const uint32_t block = mask_block(m, words, t0 + head + first * E + k * 32 * PER, lane);
+        const uint32_t block = mask_block(m, words, t0 + head + (first() - lane) * E + k * 32 * PER, lane);
 #pragma unroll
         for (int i = 0; i < 4; ++i) bits[k] |= (__shfl_sync(FULL_MASK, block, i * E + lane * E / 32) >> (lane * E & 31) & FULL) << (8 * i);
       }
     }
+  }
+  // Whether vector i is read.
+  __device__ __forceinline__ bool wanted(int i) const { return 32 * i < left && of(i) != 0 && !(INPLACE && of(i) == FULL); }
+  __device__ __forceinline__ void prefetch(const T* x) const {
 #pragma unroll
-    for (int i = 0; i < AJ_VECS; ++i) {
-      const uint32_t b = bits[i / 4] >> (8 * (i % 4)) & FULL;
+    for (int i = 0; i < AJ_VECS; ++i)
+      if (wanted(i)) asm volatile("prefetch.global.L2 [%0];" ::"l"(x + head + (first() + 32 * i) * E));
+  }
+  // Vectors FROM .. FROM + N - 1, written with their mask.
+  template <int FROM, int N>
+  __device__ __forceinline__ void move(const T* x, T* o, const uint32_t* m) const {
+    uint4 w[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
       w[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (32 * i < left && b != 0 && !(INPLACE && b == FULL)) w[i] = *reinterpret_cast<const uint4*>(from + i * 32 * E);
+      if (wanted(FROM + i)) w[i] = *reinterpret_cast<const uint4*>(x + head + (first() + 32 * (FROM + i)) * E);
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const uint32_t b = of(FROM + i);
+      if (32 * (FROM + i) < left && !(INPLACE && b == FULL))
+        *reinterpret_cast<uint4*>(o + head + (first() + 32 * (FROM + i)) * E) = m ? masked<T>(w[i], b) : w[i];
     }
   }
-  __device__ __forceinline__ void write(const T* x, T* o, const uint32_t* m, int t0, int n) const {
+  // What no vector holds.
+  __device__ __forceinline__ void ends(const T* x, T* o, const uint32_t* m, int t0, int n) const {
     if (INPLACE && !m) return;
-    if (!INPLACE && (reinterpret_cast<uintptr_t>(x) ^ reinterpret_cast<uintptr_t>(o)) % 16 != 0) {
+    if (!alike(x, o)) {
       for (int t = threadIdx.x; t < n; t += THREADS) o[t] = !m || allowed(m, t0 + t) ? x[t] : minus_inf<T>();
       return;
     }
-    const int lane = threadIdx.x & 31, first = (threadIdx.x >> 5) * 32 * AJ_VECS;
-    T* to = o + head + (first + lane) * E;
-#pragma unroll
-    for (int i = 0; i < AJ_VECS; ++i) {
-      const uint32_t b = bits[i / 4] >> (8 * (i % 4)) & FULL;
-      if (32 * i < left && !(INPLACE && b == FULL)) *reinterpret_cast<uint4*>(to + i * 32 * E) = m ? masked<T>(w[i], b) : w[i];
-    }
-    // the ends
-    const int tail = head + (n - head) / E * E, ends = head + n - tail;
-    if (static_cast<int>(threadIdx.x) < ends) {
+    const int tail = head + (n - head) / E * E, all = head + n - tail;
+    if (static_cast<int>(threadIdx.x) < all) {
       const int t = threadIdx.x < head ? threadIdx.x : tail + threadIdx.x - head;
       if (m && !allowed(m, t0 + t)) o[t] = minus_inf<T>();
       else if (!INPLACE) o[t] = x[t];
@@ -248,8 +259,9 @@ __global__ void __launch_bounds__(AJ_MASK, 4) adjust_mask_kernel(const AdjustPar
   const T* x = static_cast<const T*>(p.x) + r * p.x_stride + t0;
   T* o = static_cast<T*>(p.out) + r * p.out_stride + t0;
   Piece<T, INPLACE, AJ_MASK> piece;
-  piece.read(x, o, m, (p.V + 31) >> 5, t0, n);
-  piece.write(x, o, m, t0, n);
+  piece.look(x, o, m, (p.V + 31) >> 5, t0, n);
+  piece.template move<0, AJ_VECS>(x, o, m);
+  piece.ends(x, o, m, t0, n);
 }
 
 // Calls f(ids, position) for the first `seen` tokens of a history, by fours: from the first 16-byte boundary on, `ahead`
@@ -275,7 +287,7 @@ __device__ __forceinline__ void add_below(uint32_t t, uint32_t n, uint32_t at, u
 }
 
 template <typename T, bool INPLACE>
-__global__ void __launch_bounds__(AJ_TOUCH, 2) adjust_touch_kernel(const AdjustParams p) {
+__global__ void __launch_bounds__(AJ_TOUCH, 3) adjust_touch_kernel(const AdjustParams p) {
   constexpr int TOKENS = aj_bytes(AJ_TOUCH) / sizeof(T), WORDS = TOKENS / 32;
   constexpr int EACH = WORDS > AJ_TOUCH ? WORDS / AJ_TOUCH : 1;  // words of the bit map for each thread
   extern __shared__ __align__(16) uint32_t s_count[];                       // [list] how often a token of the list counts
@@ -306,7 +318,8 @@ __global__ void __launch_bounds__(AJ_TOUCH, 2) adjust_touch_kernel(const AdjustP
   const T* x = static_cast<const T*>(p.x) + r * p.x_stride + t0;
   T* o = static_cast<T*>(p.out) + r * p.out_stride + t0;
   Piece<T, INPLACE, AJ_TOUCH> piece;
-  piece.read(x, o, m, (p.V + 31) >> 5, t0, n);
+  piece.look(x, o, m, (p.V + 31) >> 5, t0, n);
+  piece.prefetch(x);
   const int from = p.from ? __ldg(p.from + h) : 0;
   for (int i = tid; i < WORDS; i += AJ_TOUCH) s_map[i] = s_biased[i] = 0;
   for (int i = tid; i < p.n_bias; i += AJ_TOUCH) s_id[i] = __ldg(p.bias_id + h * p.n_bias + i);
@@ -376,7 +389,9 @@ __global__ void __launch_bounds__(AJ_TOUCH, 2) adjust_touch_kernel(const AdjustP
 #pragma unroll
     for (int k = 0; k < 4; ++k) add_below(t[k], n, at[k], 1u);
   });
-  piece.write(x, o, m, t0, n);
+  piece.template move<0, AJ_VECS / 2>(x, o, m);
+  piece.template move<AJ_VECS / 2, AJ_VECS / 2>(x, o, m);
+  piece.ends(x, o, m, t0, n);
   __syncthreads();
   for (int i = tid; i < all; i += AJ_TOUCH) {
     const int t = s_token[i];
