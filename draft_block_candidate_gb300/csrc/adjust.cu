@@ -18,21 +18,22 @@ static __device__ uint32_t g_err_adjust;
 // terms' magnitudes for each term, and rounded once; where that does not do (values near the ends of
 // the type, or not finite, counts of 2^24 and more) in 64 bits, which are slow on this part.
 //
-// One CTA for each piece of a row: it reads the piece (a warp's vectors after one coalesced load of their mask; in
-// place, what a mask leaves or takes whole is not read), works out meanwhile which of the history's tokens lie in the
-// piece and how often they count, writes the piece with its mask, and then the touched tokens over, while their logits
-// are still near.  It goes over the history twice: first each token sets its bit of a bit map of the piece, whose
-// running sums then give every token that is there a place in a list; then each token counts at its place.  Neither
-// pass waits for what its atomic operations find, and all sums are of integers.  Where there is only a mask a kernel
-// without all that does.
+// One CTA for each piece of a row.  A mask alone: it reads the piece (a warp's vectors after one coalesced load of their
+// mask; in place, what a mask leaves or takes whole is not read) and writes it.  Else it sends for the piece's vectors to
+// the L2 cache, works out meanwhile which of the history's tokens lie in the piece and how often they count, copies the
+// piece with its mask, and writes the touched tokens over, while their logits are still near.  It goes over the history
+// twice: first each token sets its bit of a bit map of the piece, whose running sums then give every token that is there
+// a place in a list; then each token counts at its place.  Neither pass waits for what its atomic operations find, and
+// all sums are of integers.
 //
-// Measured: 256 rows of 151,936 in bf16 with histories of up to 4,096, 64 biases and 16 grammars 41.5 us, of which the
-// histories are 13 (30 without them: every piece goes over all of its row's, and instructions bound it); with a
-// mask alone, 512 rows in place, 33 (25 at a copy's rate for the sectors that a mask takes in part).  Pieces of 64 KB by 512 threads,
-// 41.5 us; of 32 KB by 256, 45, and by 512, 51; of 48 KB by 384, 43; with a mask alone 256 threads are better (33 for 36).
+// Bound by its steps' latency and its instructions: 256 rows of 151,936 in bf16 with histories of up to 4,096, 64 biases
+// and 16 grammars 35 us (23 at the copy rate), so that as many CTAs as can be share an SM: four of 512 threads, at 32
+// registers, 35.0 us, three 35.9, two that hold the piece in registers meanwhile 41.5.  Pieces of 64 KB go over a history
+// half as often as those of 32 KB: those take 40.5 with 256 threads.  A mask alone, 512 rows in place, 33 us (25 at the copy
+// rate for the sectors that a mask takes in part); 256 threads, 37 with 512.
 // Tried and dropped: a word for each of a piece's tokens to count in, cleared and searched, 57 us (209 with 64-bit
 // arithmetic and loops with few lanes at work); two kernels, the second a CTA a row for the touched tokens alone, 41 with
-// a table of the ids by their hash and 43 with a bit map of the row, when this took 45: the tokens' logits are read and
+// a table of the ids by their hash and 43 with a bit map of the row, when one took 45: the tokens' logits are read and
 // written one by one once the row has left the L2 cache.
 constexpr int AJ_VECS = 8;                                // vectors of 16 bytes of a lane
 constexpr int AJ_MASK = 256, AJ_TOUCH = 512;              // threads of a CTA of either kernel
@@ -248,7 +249,7 @@ __device__ __forceinline__ bool row_seen(const AdjustParams& p, int64_t r, int& 
 // ------------------------------------------------------------------------------- kernels
 
 template <typename T, bool INPLACE>
-__global__ void __launch_bounds__(AJ_MASK, 4) adjust_mask_kernel(const AdjustParams p) {
+__global__ void __launch_bounds__(AJ_MASK, 5) adjust_mask_kernel(const AdjustParams p) {
   constexpr int TOKENS = aj_bytes(AJ_MASK) / sizeof(T);
   const int64_t r = blockIdx.z * gridDim.y + blockIdx.y;  // (fits 32 bits: host)
   const int t0 = static_cast<int>(blockIdx.x) * TOKENS, n = min(TOKENS, p.V - t0);
@@ -287,7 +288,7 @@ __device__ __forceinline__ void add_below(uint32_t t, uint32_t n, uint32_t at, u
 }
 
 template <typename T, bool INPLACE>
-__global__ void __launch_bounds__(AJ_TOUCH, 3) adjust_touch_kernel(const AdjustParams p) {
+__global__ void __launch_bounds__(AJ_TOUCH, 4) adjust_touch_kernel(const AdjustParams p) {
   constexpr int TOKENS = aj_bytes(AJ_TOUCH) / sizeof(T), WORDS = TOKENS / 32;
   constexpr int EACH = WORDS > AJ_TOUCH ? WORDS / AJ_TOUCH : 1;  // words of the bit map for each thread
   extern __shared__ __align__(16) uint32_t s_count[];                       // [list] how often a token of the list counts
