@@ -172,7 +172,7 @@ __device__ __forceinline__ void each_page(const int32_t* refs, int64_t lo, int64
 //
 // A column's decision stands in its entry until the pages are dealt: -1 where it holds none, -2 - p
 // where it gives up its hold of page p.  Bound by its dependent reads and its barriers: 1,024 rows of 16
-// new tokens on a pool of some 30,000 pages 13 us, 4 rows on a small one 5.5.  Pages and rows are counted
+// new tokens on a pool of 52,396 pages 13 us, 4 rows on a small one 5.5.  Pages and rows are counted
 // behind one barrier (with one for each, a small step's three kernels took 12.4 us for 8.3).
 struct GrowParams {
   int32_t* refs;
