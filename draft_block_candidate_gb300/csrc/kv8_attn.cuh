@@ -315,7 +315,14 @@ __global__ void __launch_bounds__(32 * W) kv8_join_kernel(const P p, int runs, i
   // Lengths and row ranges were there before the attention began: they are read, and the
   // tile is found, while it still runs.  Every CTA waits for it before it may leave: what comes
   // after this kernel takes its end for the attention's too.
-  const JoinTile<D, ROWS> t(p, blockIdx.x, runs);
+  using Tile = JoinTile<D, ROWS>;
+  __shared__ __align__(16) unsigned char s_tile[sizeof(Tile)];
+  if (warp == 0) {  // (one warp's instructions: the search by every one held the reads up)
+    const Tile found(p, blockIdx.x, runs);
+    if (lane == 0) *reinterpret_cast<Tile*>(s_tile) = found;
+  }
+  __syncthreads();
+  const Tile t = *reinterpret_cast<const Tile*>(s_tile);
   pdl_wait();
   if (t.count == 0) return;
   const int rows = min(ROWS, t.sq.n * p.group - t.tile * ROWS);
