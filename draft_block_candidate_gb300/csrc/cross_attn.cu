@@ -15,9 +15,9 @@
 // in tiles of 256 rows the groups' warps take turns from a row's maximum to its last weight, and a chunk's
 // weights are handed over by 64 columns, so that the second product begins halfway.
 // Warps: two groups of four for the softmax, which also write the outputs (through 2 KB of shared memory
-// each, so that four lanes write 64 bytes of a row); one that deals the run's pieces and loads keys and
-// values through tensor maps; one for each half that issues its products, S of the next chunk right behind
-// the O that reads the P in its place; one that brings the next tile's q.
+// each, so that four lanes write 64 bytes of a row); one that loads keys and values through tensor maps; one
+// for each half that issues its products, S of the next chunk right behind the O that reads the P in its
+// place; one that finds the run's pieces and brings their tiles' q.
 //
 // Roundings below f32: the weights are bf16 (off by 2^-8 of their value at most) for the second product, whose operands
 // have one type; the sums take them unrounded.  A row's maximum moves only where a score passes it by
@@ -86,8 +86,8 @@ struct CrossShape {
   static constexpr int OFF_ST = OFF_Q + QS * T;     // 32 outputs of 32 rows for each softmax warp
   static constexpr int SMEM = 1024 + OFF_ST + 8 * 2048;
 };
-// Warps: 0 to 3 and 4 to 7 the halves' softmax; then loads, each half's products, q.
-constexpr int CR_LOAD = 8, CR_MMA = 9, CR_Q = 11, CR_WARPS = 12, CR_READERS = CR_WARPS - 1, CR_PIECES = 6;
+// Warps: 0 to 3 and 4 to 7 the halves' softmax; then keys and values, each half's products, pieces and q.
+constexpr int CR_LOAD = 8, CR_MMA = 9, CR_Q = 11, CR_WARPS = 12, CR_READERS = CR_WARPS - 1, CR_PIECES = 6, CR_AHEAD = 2;
 constexpr int CR_S = 0, CR_O = 256;       // columns of S (and P) and O of the first half; the second's are 128 and DP further
 constexpr float CR_RAISE = 8.f;           // log2 of how far a score may pass its reference
 
@@ -205,53 +205,31 @@ __global__ void __launch_bounds__(32 * CR_WARPS, 1)
   };
 
   if (warp == CR_LOAD) {
-    // ====== the run's pieces, and their keys and values ======
-    const Run run = find_run<CR_ROWS>(p, blockIdx.x, gridDim.x);
-    Pieces<CR_ROWS, CrossParams> w(p, run);
+    // ====== keys and values ======
     int it = 0, kit = 0, vit = 0, pi = 0;  // (kit, vit: chunks whose keys, values are on their way)
-    // Pieces are left one ahead of the one that is loaded, so that its q can be made ready.
-    auto leave = [&](CrossPiece& x) -> bool {
-      const int e = pi % CR_PIECES;
-      bool ok = pi < CR_PIECES || wait_warp(&pc_empty[e], ((pi / CR_PIECES) - 1) & 1, ERR_KV8_EMPTY_WAIT);
-      ok = ok && w.next();
-      if (ok)
-        x = CrossPiece{w.psq.q0, __ldg(p.kv_start + w.pb), w.psq.len, w.ph, w.ptile * CR_ROWS, w.rows(), w.c0,
-                       max(w.c0, min(w.c1, (w.psq.len + AT_CHUNK - 1) / AT_CHUNK)), w.whole(), w.slot()};
-      else
-        x.whole = -1;
-      if (lane == 0) {
-        s_piece[e] = x;
-        mbar_arrive(&pc_full[e]);
-      }
-      ++pi;
-      return ok;
-    };
-    CrossPiece now{}, next{};
-    bool ok_run = leave(now);
-    while (ok_run) {
-      const bool more = leave(next);
+    CrossPiece x;
+    bool ok = true;
+    while (ok && next_piece(pi, x, false)) {
 #pragma unroll 1
-      for (int c = now.c0; c < now.cn; ++c, ++it) {
+      for (int c = x.c0; c < x.cn; ++c, ++it) {
         auto load = [&](const CUtensorMap* tm, uint8_t* to, uint64_t* full) {
           if (lane == 0) {
             mbar_arrive_expect_tx(full, T);
 #pragma unroll
-            for (int i = 0; i < DP / 64; ++i) tma_load3(to + i * SUB, tm, 64 * i, now.h, now.kv0 + c * AT_CHUNK, full);
+            for (int i = 0; i < DP / 64; ++i) tma_load3(to + i * SUB, tm, 64 * i, x.h, x.kv0 + c * AT_CHUNK, full);
           }
           __syncwarp();
         };
         const int sk = it % KS, sv = it % VS;
-        ok_run = it < KS || wait_warp(&kempty[sk], ((it / KS) - 1) & 1, ERR_KV8_EMPTY_WAIT);
-        if (!ok_run) break;
+        ok = it < KS || wait_warp(&kempty[sk], ((it / KS) - 1) & 1, ERR_KV8_EMPTY_WAIT);
+        if (!ok) break;
         load(&tk, sm + sk * T, &kfull[sk]);
         ++kit;
-        ok_run = it < VS || wait_warp(&vempty[sv], ((it / VS) - 1) & 1, ERR_KV8_EMPTY_WAIT);
-        if (!ok_run) break;
+        ok = it < VS || wait_warp(&vempty[sv], ((it / VS) - 1) & 1, ERR_KV8_EMPTY_WAIT);
+        if (!ok) break;
         load(&tv, sm + S::OFF_V + sv * T, &vfull[sv]);
         ++vit;
       }
-      now = next;
-      ok_run = ok_run && more;
     }
     // what is in flight has to land (it has, unless a wait gave up)
     for (int i = max(0, kit - KS); i < kit; ++i) mbar_wait_bounded(&kfull[i % KS], (i / KS) & 1, &g_err_kv8_attn, ERR_KV8_EMPTY_WAIT);
@@ -348,14 +326,38 @@ __global__ void __launch_bounds__(32 * CR_WARPS, 1)
       qs += two ? 2 : 1;
     }
   } else if (warp == CR_Q) {
-    // ====== q of a tile, ahead ======
+    // ====== the run's pieces, and q of their tiles, ahead ======
     constexpr int LPR = DP / 8, RPW = 32 / LPR;  // lanes of a row (8 values each), rows at a time
     const int piece = lane % LPR;
+    const Run run = find_run<CR_ROWS>(p, blockIdx.x, gridDim.x);
+    Pieces<CR_ROWS, CrossParams> w(p, run);
     int qs = 0, pi = 0;
-    CrossPiece x;
-    while (next_piece(pi, x, false)) {
+    auto leave = [&]() -> bool {
+      const int e = pi % CR_PIECES;
+      bool ok = pi < CR_PIECES || wait_warp(&pc_empty[e], ((pi / CR_PIECES) - 1) & 1, ERR_KV8_EMPTY_WAIT);
+      ok = ok && w.next();
+      CrossPiece x{};
+      x.whole = -1;
+      if (ok)
+        x = CrossPiece{w.psq.q0, __ldg(p.kv_start + w.pb), w.psq.len, w.ph, w.ptile * CR_ROWS, w.rows(), w.c0,
+                       max(w.c0, min(w.c1, (w.psq.len + AT_CHUNK - 1) / AT_CHUNK)), w.whole(), w.slot()};
+      if (lane == 0) {
+        s_piece[e] = x;
+        mbar_arrive(&pc_full[e]);
+      }
+      __syncwarp();
+      ++pi;
+      return ok;
+    };
+    // Finding a piece takes as long as a short one's products, so pieces are left ahead, but not so
+    // that the first ones' q waits for it.
+    bool more = leave();
 #pragma unroll 1
-      for (int half = 0; half * CR_HALF < x.rows; ++half, ++qs) {
+    for (int j = 0;; ++j) {
+      const CrossPiece x = s_piece[j % CR_PIECES];  // (written over by piece j + CR_PIECES)
+      if (x.whole < 0) break;
+#pragma unroll 1
+      for (int half = 0; x.c0 < x.cn && half * CR_HALF < x.rows; ++half, ++qs) {
         const int s = qs & 1, row0 = x.row0 + half * CR_HALF, rows = x.rows - half * CR_HALF;
         if (qs > 1) wait_warp(&qfree[s], ((qs >> 1) - 1) & 1, ERR_KV8_S_WAIT);
         uint8_t* to = sm + S::OFF_Q + s * T;
@@ -391,6 +393,7 @@ __global__ void __launch_bounds__(32 * CR_WARPS, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&qready[s]);
       }
+      while (more && pi < min(2 * j + 2, j + 1 + CR_AHEAD)) more = leave();
     }
     for (int i = max(0, qs - S::QS); i < qs; ++i) mbar_wait_bounded(&qready[i & 1], (i >> 1) & 1, &g_err_kv8_attn, ERR_KV8_S_WAIT);
   } else {
