@@ -264,10 +264,7 @@ __global__ void __launch_bounds__(32 * CR_WARPS, 1)
           for (int e = 0; e < DP / 64; ++e) mma_f16_x4(t_s, q + e * (SUB >> 4), k + e * (SUB >> 4), ID_S, e > 0);
         }
         tc_commit2(&sready[g], &kempty[i]);
-        if (d + step >= chunks) {  // q has been read (the slot waits for both halves)
-          tc_commit(&qfree[slot]);
-          if (two) tc_commit(&qfree[slot]);
-        }
+        if (d + step >= chunks) tc_commit(&qfree[slot]);  // q has been read (the slot waits for both halves)
       };
       for (int d = 0; d <= d0 && d < chunks; ++d) keys(d);
       if (d0 < chunks) scores(d0);
@@ -294,6 +291,11 @@ __global__ void __launch_bounds__(32 * CR_WARPS, 1)
         // (not so where the halves take turns: the keys are two chunks away, on their way from memory)
         if (two && d + 1 < chunks) keys(d + 1);
         if (d == d0 && t++ > 0) ok = wait_warp(&left[g], t & 1, ERR_KV8_PV_WAIT) && ok;  // the piece before has left O
+        // A wait tells only a phase's parity: a half waits for the other one's q too, so that it misses none of a slot's.
+        if (two && d == 0) {
+          ok = wait_warp(&qready[1 - slot], ((qs + 1 - g) >> 1) & 1, ERR_KV8_S_WAIT) && ok;
+          if (lane == 0) mbar_arrive(&qfree[1 - slot]);
+        }
         // 64 states at a time (16 further: 8 columns of P, 16 rows of V)
         const uint64_t v = d_v + (sv * T >> 4);
         ok = wait_warp(&pready[0][g], n & 1, ERR_KV8_PV_WAIT) && ok;
