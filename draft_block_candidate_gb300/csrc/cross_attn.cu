@@ -421,13 +421,16 @@ __global__ void __launch_bounds__(32 * CR_WARPS, 1)
         const int lim = x.len - (x.c0 + d) * AT_CHUNK;
         wait_warp(&sready[g], n & 1, ERR_KV8_S_WAIT);
         tc_fence_after();
-        if (!any) {  // rows that are not there: weights of any value
+        if (!any) {  // rows that are not there: weights of any value (and turns that are handed on)
           if (lane == 0) {
             mbar_arrive(&pready[0][g]);
             mbar_arrive(&pready[1][g]);
-            if (two) mbar_arrive(&turn[g][k]);
           }
-          v += two;
+          if (two) {
+            if (g == 1 || v > 0) wait_warp(&turn[1 - g][k], (v - (g == 0)) & 1, ERR_KV8_S_WAIT);
+            if (lane == 0) mbar_arrive(&turn[g][k]);
+            ++v;
+          }
           continue;
         }
         if (lim < AT_CHUNK) mask_columns(t_s, lim);

@@ -78,6 +78,14 @@ def test_cross_matches_reference(lc, seqs, heads, group, D):
     check(lc, *make(seqs, heads, group, D, len(seqs) + D), max(n for n, _ in seqs))
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("heads,group", [(40, 1), (2, 3)])
+def test_cross_tiles_of_one_and_two_halves_in_turn(lc, heads, group, D):
+    """Second halves that hold a few rows, over many chunks, and tiles of one half's rows between them."""
+    seqs = [(129, 3000), (3, 100), (140, 1500), (33, 64), (161, 2500), (5, 700), (1, 1), (192, 1000), (250, 1800), (128, 300), (130, 129)]
+    check(lc, *make(seqs, heads, group, D, D + heads), 250)
+
+
 def test_cross_many_short_requests(lc):
     seqs = [(1 + i % 5, (i * 37) % 200) for i in range(300)]
     check(lc, *make(seqs, 2, 2, 64, 3), 5)
