@@ -31,6 +31,10 @@ static __device__ uint32_t g_err_adjust;
 // registers, 35.0 us, three 35.9, two that hold the piece in registers meanwhile 41.5.  Pieces of 64 KB go over a history
 // half as often as those of 32 KB: those take 40.5 with 256 threads.  A mask alone, 512 rows in place, 33 us (25 at the copy
 // rate for the sectors that a mask takes in part); 256 threads, 37 with 512.
+// A history's tokens are at most as many as it is long, so lists grow with it, and fewer CTAs share an SM: lists end at
+// 8,192 tokens, and a piece with more different ones takes them a list at a time (256 rows with histories of 32,768, 161 us
+// with whole lists, 88; 84 with lists of 4,096, but those make 64 x 4 rows of 32,003 tokens 73 for 50).  That loop stands apart,
+// for such histories alone: in every call's kernel it took 16 short rows from 8.4 to 10.3 us.
 // Tried and dropped: a word for each of a piece's tokens to count in, cleared and searched, 57 us (209 with 64-bit
 // arithmetic and loops with few lanes at work); two kernels, the second a CTA a row for the touched tokens alone, 41 with
 // a table of the ids by their hash and 43 with a bit map of the row, when one took 45: the tokens' logits are read and
@@ -39,6 +43,7 @@ constexpr int AJ_VECS = 8;                                // vectors of 16 bytes
 constexpr int AJ_MASK = 256, AJ_TOUCH = 512;              // threads of a CTA of either kernel
 constexpr int aj_bytes(int threads) { return threads * AJ_VECS * 16; }  // of a piece
 constexpr int AJ_MAX_BIAS = 1024;
+constexpr int AJ_LIST = 8192;                             // touched tokens of a piece at a time, at most
 
 struct AdjustParams {
   const void* x;
@@ -58,7 +63,7 @@ struct AdjustParams {
   int n_masks;
   const int32_t* mask_index;
   int rows;
-  int list;    // touched tokens of a piece, at most
+  int list;    // touched tokens of a piece at a time, at most
 };
 
 template <typename T>
@@ -287,7 +292,70 @@ __device__ __forceinline__ void add_below(uint32_t t, uint32_t n, uint32_t at, u
   asm volatile("{\n\t.reg .pred p;\n\tsetp.lt.u32 p, %0, %1;\n\t@p red.shared.add.u32 [%2], %3;\n\t}" ::"r"(t), "r"(n), "r"(at), "r"(v) : "memory");
 }
 
-template <typename T, bool INPLACE>
+// A piece's touched tokens from the list'th on (of a history with that many different ones in the piece), a list at a
+// time: what the kernel does with the first ones, out of its way.
+template <typename T>
+struct Rest {
+  const T* x;
+  T* o;
+  const uint32_t *m, *map, *biased;
+  const uint16_t* place;
+  const int* id;
+  uint32_t* count;
+  uint16_t* token;
+  const int32_t* hist;
+  const Penalties* pen;
+  int t0, n, words, lead, seen, from, list, all, n_bias;
+  bool counts, twice;
+};
+template <typename T>
+__device__ __noinline__ void touch_rest(const Rest<T>& r) {
+  const int tid = threadIdx.x;
+  auto place = [&](uint32_t t) { return static_cast<uint32_t>(r.place[t >> 5] + __popc(r.map[t >> 5] & ((1u << (t & 31)) - 1))); };
+#pragma unroll 1
+  for (uint32_t w0 = r.list; w0 < static_cast<uint32_t>(r.all); w0 += r.list) {
+    __syncthreads();
+#pragma unroll 1
+    for (int w = tid; w < r.words; w += AJ_TOUCH) {
+      uint32_t k = r.place[w] - w0;
+      for (uint32_t b = r.map[w]; b; b &= b - 1, ++k)
+        if (k < static_cast<uint32_t>(r.list)) {
+          r.token[k] = static_cast<uint16_t>(32 * w + __ffs(b) - 1);
+          r.count[k] = 0;
+        }
+    }
+    __syncthreads();
+    if (r.counts) {
+      const int4 ahead = r.lead + 4 * tid + 4 <= r.seen ? __ldg(reinterpret_cast<const int4*>(r.hist + r.lead) + tid) : make_int4(-1, -1, -1, -1);
+      each_token(r.hist, r.lead, r.seen, ahead, [&](int4 q, int i) {
+        const int id[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll 1
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t t = static_cast<uint32_t>(id[j]) - r.t0, k = t < static_cast<uint32_t>(r.n) && i + j >= r.from ? place(t) - w0 : UINT_MAX;
+          add_below(k, r.list, smem_addr(r.count) + 4 * k, 1u);
+        }
+      });
+      __syncthreads();
+    }
+    for (int i = tid; i < min(r.list, r.all - static_cast<int>(w0)); i += AJ_TOUCH) {
+      const int t = r.token[i];
+      if (!(r.biased[t >> 5] >> (t & 31) & 1) && (!r.m || allowed(r.m, r.t0 + t))) touch(r.o + t, static_cast<float>(r.x[t]), true, r.count[i], 0, 0, 0, r.pen);
+    }
+    for (int i = tid; i < r.n_bias; i += AJ_TOUCH) {
+      const int id = r.id[i];
+      const uint32_t t = static_cast<uint32_t>(id) - r.t0;
+      if (t >= static_cast<uint32_t>(r.n) || (r.m && !allowed(r.m, id)) || !(r.map[t >> 5] >> (t & 31) & 1)) continue;
+      const uint32_t k = place(t) - w0;
+      int j = 0;
+      while (r.id[j] != id) ++j;
+      if (j < i || k >= static_cast<uint32_t>(r.list)) continue;
+      touch(r.o + t, static_cast<float>(r.x[t]), true, r.count[k], id, i, r.n_bias, r.pen);
+    }
+  }
+}
+
+// LONG: histories that may bring more tokens into a piece than a list of AJ_LIST holds.
+template <typename T, bool INPLACE, bool LONG>
 __global__ void __launch_bounds__(AJ_TOUCH, 4) adjust_touch_kernel(const AdjustParams p) {
   constexpr int TOKENS = aj_bytes(AJ_TOUCH) / sizeof(T), WORDS = TOKENS / 32;
   constexpr int EACH = WORDS > AJ_TOUCH ? WORDS / AJ_TOUCH : 1;  // words of the bit map for each thread
@@ -372,6 +440,7 @@ __global__ void __launch_bounds__(AJ_TOUCH, 4) adjust_touch_kernel(const AdjustP
     for (int i = 0; i < EACH; ++i) {
       s_place[tid * EACH + i] = static_cast<uint16_t>(at);
       for (uint32_t b = word[i]; b; b &= b - 1, ++at) {
+        if (LONG && at >= p.list) continue;  // (of touch_rest)
         s_token[at] = static_cast<uint16_t>(32 * (tid * EACH + i) + __ffs(b) - 1);
         s_count[at] = 0;
       }
@@ -381,20 +450,20 @@ __global__ void __launch_bounds__(AJ_TOUCH, 4) adjust_touch_kernel(const AdjustP
   // 2. how often they count, where a penalty asks for it
   if (p.freq || p.pres) each_token(hist, lead, seen, ahead, [&](int4 q, int i) {
     const int id[4] = {q.x, q.y, q.z, q.w};
-    uint32_t t[4], at[4] = {};
+    uint32_t at[4] = {UINT_MAX, UINT_MAX, UINT_MAX, UINT_MAX};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      t[k] = i + k >= from ? static_cast<uint32_t>(id[k]) - t0 : UINT_MAX;
-      if (t[k] < static_cast<uint32_t>(n)) at[k] = smem_addr(s_count) + 4 * place(t[k]);
+      const uint32_t t = i + k >= from ? static_cast<uint32_t>(id[k]) - t0 : UINT_MAX;
+      if (t < static_cast<uint32_t>(n)) at[k] = place(t);
     }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) add_below(t[k], n, at[k], 1u);
+    for (int k = 0; k < 4; ++k) add_below(at[k], LONG ? p.list : UINT_MAX, smem_addr(s_count) + 4 * at[k], 1u);
   });
   piece.template move<0, AJ_VECS / 2>(x, o, m);
   piece.template move<AJ_VECS / 2, AJ_VECS / 2>(x, o, m);
   piece.ends(x, o, m, t0, n);
   __syncthreads();
-  for (int i = tid; i < all; i += AJ_TOUCH) {
+  for (int i = tid; i < (LONG ? min(all, p.list) : all); i += AJ_TOUCH) {
     const int t = s_token[i];
     if (!(s_biased[t >> 5] >> (t & 31) & 1) && (!m || allowed(m, t0 + t))) touch(o + t, static_cast<float>(x[t]), true, s_count[i], 0, 0, 0, &s_pen);
   }
@@ -408,8 +477,13 @@ __global__ void __launch_bounds__(AJ_TOUCH, 4) adjust_touch_kernel(const AdjustP
     while (s_id[j] != id) ++j;
     if (j < i) continue;
     const bool there = s_map[t >> 5] >> (t & 31) & 1;
-    touch(o + t, static_cast<float>(x[t]), there, there ? s_count[place(t)] : 0u, id, i, twice ? p.n_bias : i + 1, &s_pen);
+    const int k = there ? place(t) : 0;
+    if (LONG && k >= p.list) continue;
+    touch(o + t, static_cast<float>(x[t]), there, there ? s_count[k] : 0u, id, i, twice ? p.n_bias : i + 1, &s_pen);
   }
+  if (LONG && all > p.list)
+    touch_rest<T>(Rest<T>{x, o, m, s_map, s_biased, s_place, s_id, s_count, s_token, hist, &s_pen, t0, n, WORDS, lead, seen, from, p.list, all, p.n_bias,
+                          p.freq || p.pres, twice});
 }
 
 cudaError_t adjust_read_device_error(uint32_t* code) {
@@ -442,7 +516,8 @@ cudaError_t adjust_launch(const AdjustParams& p, int64_t pieces, bool touch, cud
     if (e == cudaSuccess) note_launch();
     return e;
   };
-  if (touch) return inplace ? go(adjust_touch_kernel<T, true>) : go(adjust_touch_kernel<T, false>);
+  if (touch && p.cap > AJ_LIST) return inplace ? go(adjust_touch_kernel<T, true, true>) : go(adjust_touch_kernel<T, false, true>);
+  if (touch) return inplace ? go(adjust_touch_kernel<T, true, false>) : go(adjust_touch_kernel<T, false, false>);
   return inplace ? go(adjust_mask_kernel<T, true>) : go(adjust_mask_kernel<T, false>);
 }
 
@@ -494,8 +569,8 @@ extern "C" lilicorr_status lilicorr_adjust_logits(const lilicorr_adjust* a, void
   const int64_t pieces = (a->V + tokens - 1) / tokens;
   p.rows = static_cast<int>(a->rows);
   if (a->rows > INT_MAX - 65536 || a->rows * pieces > INT_MAX) return bad("lilicorr_adjust_logits: rows * V is too large for one call");
-  // a piece's list holds every token that the history may bring into it
-  p.list = static_cast<int>(std::max<int64_t>(4, (std::min<int64_t>(a->history ? a->cap : 0, std::min(tokens, a->V)) + 3) / 4 * 4));
+  // a piece's list holds every token that the history may bring into it, or as many of them as leave room for other CTAs
+  p.list = static_cast<int>(std::max<int64_t>(4, (std::min<int64_t>({a->history ? a->cap : 0, tokens, a->V, AJ_LIST}) + 3) / 4 * 4));
   const cudaError_t e = es == 2 ? adjust_launch<__nv_bfloat16>(p, pieces, touch, static_cast<cudaStream_t>(stream))
                                 : adjust_launch<float>(p, pieces, touch, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return fail(LILICORR_ERR_CUDA, cudaGetErrorString(e));

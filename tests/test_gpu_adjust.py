@@ -110,6 +110,18 @@ def test_adjust_every_token_seen(lc, dtype, V):
     check(lc.adjust_logits(x, out=torch.empty_like(x), **kw), x, kw)
 
 
+@pytest.mark.parametrize("which", [("repetition",), ("repetition", "presence")])
+@pytest.mark.parametrize("V", [8192, 8193, 16385])
+def test_adjust_more_different_tokens_than_a_list_holds(lc, which, V):
+    x, kw = make(2, V, torch.float32, 2, 20000, 40, 0, V)
+    for h in kw["history"]:
+        h[:V] = torch.randperm(V, device="cuda", generator=gen(6)).to(torch.int32)
+    kw["seen"][:] = torch.tensor([V, 20000])
+    kw = {k: v for k, v in kw.items() if k in ("history", "seen", "bias_ids", "bias_values") + which}
+    keep = x.clone()
+    check(lc.adjust_logits(x, **kw), keep, kw)
+
+
 @pytest.mark.parametrize("which", ["repetition", "presence", "frequency", "seen"])
 def test_adjust_each_penalty_alone(lc, which):
     x, kw = make(4, 300, torch.float32, 2, 100, 0, 0, 5)
