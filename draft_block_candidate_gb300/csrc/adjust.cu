@@ -92,20 +92,29 @@ __device__ __forceinline__ void store_double(float* p, double y) { *p = static_c
 __device__ __forceinline__ void store_double(__nv_bfloat16* p, double y) { *p = __double2bfloat16(y); }
 
 // A touched token's value from its logit, whether it was seen, how often it counts, and the biases of entries
-// [e0, e1) of the list whose id is its own.
+// [e0, e1) of the list whose id is its own, as that of e0 is.
 struct Penalties {
   float rho, inv, inv_lo, freq, pres;  // inv + inv_lo = 1 / rho, but for 2^-46 (NaN for a large rho)
   int rep;
   const int* ids;
   const float* bias;
 };
+// The first entry from i on whose id this is (n: none), four at a time.
+__device__ __forceinline__ int next_entry(const int* ids, int i, int n, int id) {
+#pragma unroll 1
+  for (; i < n; i = (i | 3) + 1) {
+    const int4 v = *reinterpret_cast<const int4*>(ids + (i & ~3));
+    const uint32_t hit = ((v.x == id) | (v.y == id) << 1 | (v.z == id) << 2 | (v.w == id) << 3) & ~0u << (i & 3);
+    if (hit) return min(n, (i & ~3) + __ffs(hit) - 1);
+  }
+  return n;
+}
 template <typename T>
 __device__ __noinline__ void touch_double(T* o, float x, bool seen, uint32_t g, int id, int e0, int e1, const Penalties* p) {
   double y = x;
   if (seen && p->rep) y = y > 0 ? y / p->rho : y * p->rho;
   if (g) y -= static_cast<double>(p->freq) * g + p->pres;
-  for (int i = e0; i < e1; ++i)
-    if (p->ids[i] == id) y += __ldg(p->bias + i);
+  for (int i = e0; i < e1; i = next_entry(p->ids, i + 1, e1, id)) y += __ldg(p->bias + i);
   store_double(o, y);
 }
 template <typename T>
@@ -124,8 +133,7 @@ __device__ __forceinline__ void touch(T* o, float x, bool seen, uint32_t g, int 
     add_pair(hi, lo, -p->pres, 0.f);
   }
 #pragma unroll 1
-  for (int i = e0; i < e1; ++i)
-    if (p->ids[i] == id) add_pair(hi, lo, __ldg(p->bias + i), 0.f);
+  for (int i = e0; i < e1; i = next_entry(p->ids, i + 1, e1, id)) add_pair(hi, lo, __ldg(p->bias + i), 0.f);
   const float size = fabsf(hi);
   if (size > 7.9e-31f && size < 1.3e36f && fabsf(lo) <= size && g < (1u << 24)) store_value(o, hi, lo);
   else touch_double(o, x, seen, g, id, e0, e1, p);
@@ -306,7 +314,7 @@ struct Rest {
   const int32_t* hist;
   const Penalties* pen;
   int t0, n, words, lead, seen, from, list, all, n_bias;
-  bool counts, twice;
+  bool counts;
 };
 template <typename T>
 __device__ __noinline__ void touch_rest(const Rest<T>& r) {
@@ -346,9 +354,7 @@ __device__ __noinline__ void touch_rest(const Rest<T>& r) {
       const uint32_t t = static_cast<uint32_t>(id) - r.t0;
       if (t >= static_cast<uint32_t>(r.n) || (r.m && !allowed(r.m, id)) || !(r.map[t >> 5] >> (t & 31) & 1)) continue;
       const uint32_t k = place(t) - w0;
-      int j = 0;
-      while (r.id[j] != id) ++j;
-      if (j < i || k >= static_cast<uint32_t>(r.list)) continue;
+      if (next_entry(r.id, 0, i, id) < i || k >= static_cast<uint32_t>(r.list)) continue;
       touch(r.o + t, static_cast<float>(r.x[t]), true, r.count[k], id, i, r.n_bias, r.pen);
     }
   }
@@ -366,7 +372,7 @@ __global__ void __launch_bounds__(AJ_TOUCH, 4) adjust_touch_kernel(const AdjustP
   __shared__ __align__(16) int s_id[AJ_MAX_BIAS];
   __shared__ uint32_t s_biased[WORDS];                                      // a bit a token of the bias list
   __shared__ int s_sum[AJ_TOUCH / 32];
-  __shared__ int s_twice;  // whether a token of the piece has several biases
+  __shared__ uint32_t s_twice[32];  // bit t % 1024: tokens of the piece that have several biases, and others
   __shared__ Penalties s_pen;
   const int tid = threadIdx.x, lane = tid & 31;
   const uint32_t row = blockIdx.z * gridDim.y + blockIdx.y;  // (row and group fit 32 bits: host)
@@ -391,6 +397,7 @@ __global__ void __launch_bounds__(AJ_TOUCH, 4) adjust_touch_kernel(const AdjustP
   piece.prefetch(x);
   const int from = p.from ? __ldg(p.from + h) : 0;
   for (int i = tid; i < WORDS; i += AJ_TOUCH) s_map[i] = s_biased[i] = 0;
+  if (tid < 32) s_twice[tid] = 0;
   for (int i = tid; i < p.n_bias; i += AJ_TOUCH) s_id[i] = __ldg(p.bias_id + h * p.n_bias + i);
   if (tid == AJ_TOUCH - 1) {
     Penalties q{p.rep ? __ldg(p.rep + h) : 1.f, 0.f, 0.f, p.freq ? __ldg(p.freq + h) : 0.f, p.pres ? __ldg(p.pres + h) : 0.f,
@@ -399,7 +406,6 @@ __global__ void __launch_bounds__(AJ_TOUCH, 4) adjust_touch_kernel(const AdjustP
     q.inv = fabsf(q.rho) < 1.2e30f ? 1.f / q.rho : NAN;
     q.inv_lo = fmaf(-q.inv, q.rho, 1.f) * q.inv;
     s_pen = q;
-    s_twice = 0;
   }
   __syncthreads();
   // 1. which tokens there are
@@ -413,7 +419,8 @@ __global__ void __launch_bounds__(AJ_TOUCH, 4) adjust_touch_kernel(const AdjustP
   });
   for (int i = tid; i < p.n_bias; i += AJ_TOUCH) {
     const uint32_t t = static_cast<uint32_t>(s_id[i]) - t0;
-    if (t < static_cast<uint32_t>(n) && (atomicOr(s_biased + (t >> 5), 1u << (t & 31)) >> (t & 31) & 1)) s_twice = 1;
+    if (t < static_cast<uint32_t>(n) && (atomicOr(s_biased + (t >> 5), 1u << (t & 31)) >> (t & 31) & 1))
+      atomicOr(s_twice + ((t >> 5) & 31), 1u << (t & 31));
   }
   __syncthreads();
   // their places in the list, a word of the map for each thread
@@ -468,14 +475,12 @@ __global__ void __launch_bounds__(AJ_TOUCH, 4) adjust_touch_kernel(const AdjustP
     if (!(s_biased[t >> 5] >> (t & 31) & 1) && (!m || allowed(m, t0 + t))) touch(o + t, static_cast<float>(x[t]), true, s_count[i], 0, 0, 0, &s_pen);
   }
   // tokens of the bias list, by the first entry that names them (from the last warps on, whose lists are the shortest)
-  const bool twice = s_twice;
   for (int i = AJ_TOUCH - 1 - tid; i < p.n_bias; i += AJ_TOUCH) {
     const int id = s_id[i];
     const uint32_t t = static_cast<uint32_t>(id) - t0;
     if (t >= static_cast<uint32_t>(n) || (m && !allowed(m, id))) continue;
-    int j = twice ? 0 : i;
-    while (s_id[j] != id) ++j;
-    if (j < i) continue;
+    const bool twice = s_twice[(t >> 5) & 31] >> (t & 31) & 1;
+    if (twice && next_entry(s_id, 0, i, id) < i) continue;
     const bool there = s_map[t >> 5] >> (t & 31) & 1;
     const int k = there ? place(t) : 0;
     if (LONG && k >= p.list) continue;
@@ -483,7 +488,7 @@ __global__ void __launch_bounds__(AJ_TOUCH, 4) adjust_touch_kernel(const AdjustP
   }
   if (LONG && all > p.list)
     touch_rest<T>(Rest<T>{x, o, m, s_map, s_biased, s_place, s_id, s_count, s_token, hist, &s_pen, t0, n, WORDS, lead, seen, from, p.list, all, p.n_bias,
-                          p.freq || p.pres, twice});
+                          p.freq || p.pres});
 }
 
 cudaError_t adjust_read_device_error(uint32_t* code) {
