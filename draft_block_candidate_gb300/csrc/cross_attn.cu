@@ -47,7 +47,26 @@ struct CrossParams {
   __nv_bfloat16* out;  // [total, q_heads, D]
   float* lse;          // [total, q_heads] or null
   float* part;         // [2 * grid][256 * (padded D + 2)]: products, maxima, sums
+  int half;            // rows of a tile's half
+  uint64_t tile_inv;   // 2^40 / (2 half), rounded up: exact quotients of less than 2^32 by 2^8 and less
   __device__ __forceinline__ int kv_heads() const { return heads; }
+};
+
+// Rows of a tile and its halves that are used: all, or whole tokens' where a group does not divide 128 (as one kernel the
+// usual case was 1 to 3 % slower).
+struct CrossFull : CrossParams {
+  __device__ __forceinline__ int half_rows() const { return 128; }
+  template <int ROWS>
+  __device__ __forceinline__ int tile_rows() const { return ROWS; }
+  template <int ROWS>
+  __device__ __forceinline__ int tiles(int rows) const { return (rows + ROWS - 1) / ROWS; }
+};
+struct CrossPart : CrossParams {
+  __device__ __forceinline__ int half_rows() const { return half; }
+  template <int ROWS>
+  __device__ __forceinline__ int tile_rows() const { return 2 * half; }
+  template <int ROWS>
+  __device__ __forceinline__ int tiles(int rows) const { return static_cast<int>((uint64_t(rows + 2 * half - 1) * tile_inv) >> 40); }
 };
 
 __device__ __forceinline__ SeqRange attn_range(const CrossParams& p, int64_t b) {
@@ -137,10 +156,10 @@ __device__ __forceinline__ void cp16(void* to, const void* from, bool there) {
 }
 __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
-template <int DP>
+template <int DP, class P>
 __global__ void __launch_bounds__(32 * CR_WARPS, 1)
     cross_attention_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
-                           const __grid_constant__ CrossParams p) {
+                           const __grid_constant__ P p) {
   using S = CrossShape<DP>;
   constexpr int KS = S::KS, VS = S::VS, T = S::T, SUB = S::SUB;
   extern __shared__ uint8_t cr_raw[];
@@ -244,7 +263,7 @@ __global__ void __launch_bounds__(32 * CR_WARPS, 1)
     int pi = 0, it = 0, n = 0, t = 0, qs = 0, i0 = 0;  // chunks; the half's chunks and pieces; halves of q; chunks taken in turn
     CrossPiece x;
     while (next_piece(pi, x, false)) {
-      const bool two = x.rows > CR_HALF;
+      const bool two = x.rows > p.half_rows();
       const int step = two ? 1 : 2, d0 = two ? 0 : (g - i0) & 1, chunks = x.cn - x.c0;
       const int slot = (qs + (two ? g : 0)) & 1;
       const uint64_t q = d_q + (slot * T >> 4);
@@ -332,7 +351,7 @@ __global__ void __launch_bounds__(32 * CR_WARPS, 1)
     constexpr int LPR = DP / 8, RPW = 32 / LPR;  // lanes of a row (8 values each), rows at a time
     const int piece = lane % LPR;
     const Run run = find_run<CR_ROWS>(p, blockIdx.x, gridDim.x);
-    Pieces<CR_ROWS, CrossParams> w(p, run);
+    Pieces<CR_ROWS, P> w(p, run);
     int qs = 0, pi = 0;
     auto leave = [&]() -> bool {
       const int e = pi % CR_PIECES;
@@ -341,7 +360,7 @@ __global__ void __launch_bounds__(32 * CR_WARPS, 1)
       CrossPiece x{};
       x.whole = -1;
       if (ok)
-        x = CrossPiece{w.psq.q0, __ldg(p.kv_start + w.pb), w.psq.len, w.ph, w.ptile * CR_ROWS, w.rows(), w.c0,
+        x = CrossPiece{w.psq.q0, __ldg(p.kv_start + w.pb), w.psq.len, w.ph, w.row0(), w.rows(), w.c0,
                        max(w.c0, min(w.c1, (w.psq.len + AT_CHUNK - 1) / AT_CHUNK)), w.whole(), w.slot()};
       if (lane == 0) {
         s_piece[e] = x;
@@ -359,13 +378,13 @@ __global__ void __launch_bounds__(32 * CR_WARPS, 1)
       const CrossPiece x = s_piece[j % CR_PIECES];  // (written over by piece j + CR_PIECES)
       if (x.whole < 0) break;
 #pragma unroll 1
-      for (int half = 0; x.c0 < x.cn && half * CR_HALF < x.rows; ++half, ++qs) {
-        const int s = qs & 1, row0 = x.row0 + half * CR_HALF, rows = x.rows - half * CR_HALF;
+      for (int half = 0; x.c0 < x.cn && half * p.half_rows() < x.rows; ++half, ++qs) {
+        const int s = qs & 1, row0 = x.row0 + half * p.half_rows(), rows = min(p.half_rows(), x.rows - half * p.half_rows());
         if (qs > 1) wait_warp(&qfree[s], ((qs >> 1) - 1) & 1, ERR_KV8_S_WAIT);
         uint8_t* to = sm + S::OFF_Q + s * T;
         if (p.q_map) {  // whole tokens of a group's heads; rows behind the last are other requests', or zeros
           if (lane == 0) {
-            mbar_arrive_expect_tx(&qready[s], T);
+            mbar_arrive_expect_tx(&qready[s], p.half_rows() * (DP / 64) * 128);
 #pragma unroll
             for (int i = 0; i < DP / 64; ++i)
               tma_load3(to + i * SUB, &tq, 64 * i, x.h * p.group, static_cast<int>(x.q0) + row0 / p.group, &qready[s]);
@@ -410,12 +429,13 @@ __global__ void __launch_bounds__(32 * CR_WARPS, 1)
     int n = 0, pi = 0, t[2] = {0, 0}, u = 0, v = 0, i0 = 0;
     CrossPiece x;
     while (next_piece(pi, x, true)) {
-      const bool two = x.rows > CR_HALF;
+      const bool two = x.rows > p.half_rows();
       const int step = two ? 1 : 2, chunks = x.cn - x.c0;
       const int f = two ? g : i0 & 1, d0 = two || g == f ? 0 : 1;  // f: the half that takes the first chunk
-      const bool any = (two ? g * CR_HALF : 0) + 32 * k < x.rows;  // of the warp's rows
+      const int base = two ? g * p.half_rows() : 0, end = min(x.rows, base + p.half_rows());  // the half's rows of the tile
+      const bool any = base + 32 * k < end;                                     // of the warp's rows
       // (a row that is not there has weights of 0)
-      float m = (two ? g * CR_HALF : 0) + r < x.rows ? -INFINITY : INFINITY, l = 0.f;
+      float m = base + r < end ? -INFINITY : INFINITY, l = 0.f;
 #pragma unroll 1
       for (int d = d0; d < chunks; d += step, ++n) {
         const int lim = x.len - (x.c0 + d) * AT_CHUNK;
@@ -496,8 +516,8 @@ __global__ void __launch_bounds__(32 * CR_WARPS, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&met[u & 1][k]);
       } else if (d0 < chunks || chunks == 0) {
-        const int row = (two ? g * CR_HALF : 0) + r;
-        const bool there = row < x.rows && (chunks > 0 || two || g == f);
+        const int row = base + r;
+        const bool there = row < end && (chunks > 0 || two || g == f);
         // where the row goes; and 16 bytes of 32 columns of four rows that the lane stores for the warp
         const int i = there ? (x.row0 + row) / p.group : 0, j = there ? x.row0 + row - i * p.group : 0;
         const int64_t at = there ? (x.q0 + i) * p.q_heads + int64_t(x.h) * p.group + j : -1;
@@ -658,19 +678,21 @@ cudaError_t rows_map(CUtensorMap* tm, const void* x, int D, int heads, int64_t t
              : cudaErrorInvalidValue;
 }
 
-template <int DP>
-cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CrossParams& p, cudaStream_t stream) {
+template <int DP, class P>
+cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CrossParams& params, cudaStream_t stream) {
+  P p;
+  static_cast<CrossParams&>(p) = params;
   constexpr int smem = CrossShape<DP>::SMEM;
   const int grid = device_sm_count();
-  cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void*>(cross_attention_kernel<DP>), smem);
+  cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void*>(cross_attention_kernel<DP, P>), smem);
   if (e != cudaSuccess) return e;
-  cross_attention_kernel<DP><<<grid, 32 * CR_WARPS, smem, stream>>>(tq, tk, tv, p);
+  cross_attention_kernel<DP, P><<<grid, 32 * CR_WARPS, smem, stream>>>(tq, tk, tv, p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   PdlScope pdl(true);
   // (a warp takes four rows of a tile in two parts)
-  const int most = static_cast<int>(std::min<int64_t>(CR_ROWS, int64_t(p.max_new) * p.group));
-  e = launch_k(kv8_join_kernel<DP, CR_ROWS, 4, 16, CrossParams>, dim3(grid, (most + 15) / 16), dim3(128), 0, stream, p, grid, (most + 15) / 16 * 16);
+  const int most = static_cast<int>(std::min<int64_t>(2 * p.half, int64_t(p.max_new) * p.group));
+  e = launch_k(kv8_join_kernel<DP, CR_ROWS, 4, 16, P>, dim3(grid, (most + 15) / 16), dim3(128), 0, stream, p, grid, (most + 15) / 16 * 16);
   if (e == cudaSuccess) note_launch(2);
   return e;
 }
@@ -703,9 +725,11 @@ lilicorr_status lilicorr_cross_attention(const void* q, int64_t q_token_stride, 
                (total_kv > 1 && (k_token_stride < head_dim || v_token_stride < head_dim))))
     why = "rows of keys and values do not overlap";
   if (!why && (!out || reinterpret_cast<uintptr_t>(out) % 16)) why = "out is null or not 16-byte aligned";
+  // Halves of whole tokens, which a tensor map brings, but where that would leave a quarter of the rows empty.
+  const int group = why ? 1 : q_heads / kv_heads, whole = AT_CHUNK / group * group, half = whole >= 96 ? whole : CR_HALF;
   // a request's rows, and its work units, are counted in 32 bits
-  if (!why && int64_t(max_new) * (q_heads / kv_heads) > INT_MAX - 256) why = "max_new * q_heads / kv_heads is too large";
-  if (!why && (int64_t(max_new) * (q_heads / kv_heads) / CR_ROWS + 1) * kv_heads * ((total_kv + 127) / 128 + 8) > UINT_MAX)
+  if (!why && int64_t(max_new) * group > INT_MAX - 256) why = "max_new * q_heads / kv_heads is too large";
+  if (!why && (int64_t(max_new) * group / (2 * half) + 1) * kv_heads * ((total_kv + 127) / 128 + 8) > UINT_MAX)
     why = "max_new * q_heads * the states are too large";
   if (!why && !std::isfinite(scale * LOG2E_F)) why = "scale, or scale * log2 e, is not finite";
   if (why) return fail(LILICORR_ERR_INVALID_ARG, why);
@@ -729,7 +753,8 @@ lilicorr_status lilicorr_cross_attention(const void* q, int64_t q_token_stride, 
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.q_tok = q_token_stride; p.q_head = q_head_stride;
   p.total = total; p.total_kv = total_kv;
-  p.q_heads = q_heads; p.group = q_heads / kv_heads; p.heads = kv_heads; p.D = head_dim;
+  p.q_heads = q_heads; p.group = group; p.heads = kv_heads; p.D = head_dim;
+  p.half = half; p.tile_inv = ((uint64_t(1) << 40) + 2 * half - 1) / (2 * half);
   p.q_start = q_start; p.kv_start = kv_start; p.kv_len = kv_len;
   p.batch = batch; p.max_new = max_new;
   p.scale2 = std::max(std::fabs(scale) * LOG2E_F, FLT_MIN);  // (never 0, so that a score of infinity stays one)
@@ -741,11 +766,13 @@ lilicorr_status lilicorr_cross_attention(const void* q, int64_t q_token_stride, 
   cudaError_t e = rows_map(&tk, k, head_dim, kv_heads, total_kv, k_token_stride, k_head_stride, 1);
   if (e == cudaSuccess) e = rows_map(&tv, v, head_dim, kv_heads, total_kv, v_token_stride, v_head_stride, 1);
   if (e != cudaSuccess) return fail(LILICORR_ERR_INVALID_ARG, "lilicorr_cross_attention: no tensor map for these strides");
-  // q through a map too where tiles begin with a group's first head (else, or with a negative scale, or rows
-  // that overlap, by copies of 16 bytes)
-  p.q_map = AT_CHUNK % p.group == 0 && !p.flip && (q_heads == 1 || q_head_stride >= head_dim) && (total == 1 || q_token_stride >= head_dim) &&
+  // q through a map too where halves are whole tokens (else, or with a negative scale, or rows that overlap, by copies
+  // of 16 bytes: 9 requests of 602 rows over 1,303 states, three rows to a head, 155 us that way)
+  p.q_map = half % group == 0 && !p.flip && (q_heads == 1 || q_head_stride >= head_dim) && (total == 1 || q_token_stride >= head_dim) &&
             rows_map(&tq, q, head_dim, q_heads, total, q_token_stride, q_head_stride, p.group) == cudaSuccess;
-  e = head_dim <= 64 ? launch<64>(tq, tk, tv, p, static_cast<cudaStream_t>(stream)) : launch<128>(tq, tk, tv, p, static_cast<cudaStream_t>(stream));
+  auto go = [&](auto f) { return f(tq, tk, tv, p, static_cast<cudaStream_t>(stream)); };
+  if (head_dim <= 64) e = half == CR_HALF ? go(launch<64, CrossFull>) : go(launch<64, CrossPart>);
+  else e = half == CR_HALF ? go(launch<128, CrossFull>) : go(launch<128, CrossPart>);
   if (e != cudaSuccess) return fail(LILICORR_ERR_CUDA, cudaGetErrorString(e));
   return LILICORR_OK;
 }

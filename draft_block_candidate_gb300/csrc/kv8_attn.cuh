@@ -26,6 +26,11 @@ struct AttnParams {
   float* lse;          // [total, q_heads] or null
   float* part;         // [2 * grid][rows of a tile * (D + 2)]: products, maxima, sums
   __device__ __forceinline__ int kv_heads() const { return c.heads; }
+  // Rows of a tile that are used, and the tiles of so many rows.
+  template <int ROWS>
+  __device__ __forceinline__ int tile_rows() const { return ROWS; }
+  template <int ROWS>
+  __device__ __forceinline__ int tiles(int rows) const { return (rows + ROWS - 1) / ROWS; }
 };
 
 // ------------------------------------------------------------------------ the deal of work
@@ -54,7 +59,7 @@ __device__ __forceinline__ SeqUnits seq_units(const P& p, int64_t b) {
   u.n = r.n;
   u.len = r.len;
   u.q0 = r.q0;
-  u.tiles = (r.n * p.group + ROWS - 1) / ROWS;
+  u.tiles = p.template tiles<ROWS>(r.n * p.group);
   u.chunks = max(1, (r.len + AT_CHUNK - 1) / AT_CHUNK);
   u.units = int64_t(u.tiles) * p.kv_heads() * (u.chunks + HEAD_UNITS<ROWS>);
   return u;
@@ -155,10 +160,11 @@ struct Pieces {
     }
     return false;
   }
-  __device__ __forceinline__ int rows() const { return min(ROWS, psq.n * p.group - ptile * ROWS); }
+  __device__ __forceinline__ int row0() const { return ptile * p.template tile_rows<ROWS>(); }
+  __device__ __forceinline__ int rows() const { return min(p.template tile_rows<ROWS>(), psq.n * p.group - row0()); }
   // tokens that the tile's last row sees
   __device__ __forceinline__ int end() const {
-    return max(0, min(psq.len, psq.len - psq.n + (ptile * ROWS + rows() - 1) / p.group + 1));
+    return max(0, min(psq.len, psq.len - psq.n + (row0() + rows() - 1) / p.group + 1));
   }
   __device__ __forceinline__ int whole() const { return c0 == 0 && c1 == psq.chunks ? 1 : 0; }
   __device__ __forceinline__ int slot() const { return 2 * static_cast<int>(blockIdx.x) + (count > 1); }
@@ -325,13 +331,13 @@ __global__ void __launch_bounds__(32 * W) kv8_join_kernel(const P p, int runs, i
   const Tile t = *reinterpret_cast<const Tile*>(s_tile);
   pdl_wait();
   if (t.count == 0) return;
-  const int rows = min(ROWS, t.sq.n * p.group - t.tile * ROWS);
+  const int row0 = t.tile * p.template tile_rows<ROWS>(), rows = min(p.template tile_rows<ROWS>(), t.sq.n * p.group - row0);
   const int cy = gridDim.y, ctas = (t.count - 1) * cy, mine = (most + ctas - 1) / ctas;  // rows of a CTA
   const int r0 = (t.j * cy + blockIdx.y) * mine, r1 = min(rows, r0 + mine);
   if (r0 >= r1) return;
   float mx, sum, y[E];
   auto store = [&](int r) {
-    const int row = t.tile * ROWS + r, i = row / p.group;
+    const int row = row0 + r, i = row / p.group;
     store_row<E>(p, (t.sq.q0 + i) * p.q_heads + t.h * p.group + (row - i * p.group), D, lane, y, sum, mx);
   };
   if (R > 1 && t.count == 2) {

@@ -86,6 +86,18 @@ def test_cross_tiles_of_one_and_two_halves_in_turn(lc, heads, group, D):
     check(lc, *make(seqs, heads, group, D, D + heads), 250)
 
 
+@pytest.mark.parametrize("group", [7, 50, 97, 100, 128, 130])
+@pytest.mark.parametrize("scale", [0.2, -0.3])
+def test_cross_groups_that_fill_no_half(lc, group, scale):
+    """Halves of whole tokens (7, 97, 100), halves that split tokens (50, 130), and q with its signs turned over."""
+    check(lc, *make([(5, 300), (1, 40), (9, 129), (0, 7), (4, 1)], 1, group, 64, group), 9, scale=scale)
+
+
+@pytest.mark.parametrize("D", [80, 128])
+def test_cross_long_rows_of_three_to_a_head(lc, D):
+    check(lc, *make([(170, 700), (84, 300), (85, 129), (3, 90)], 2, 3, D, D), 170)
+
+
 def test_cross_many_short_requests(lc):
     seqs = [(1 + i % 5, (i * 37) % 200) for i in range(300)]
     check(lc, *make(seqs, 2, 2, 64, 3), 5)
