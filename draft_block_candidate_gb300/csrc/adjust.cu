@@ -117,9 +117,9 @@ __device__ __noinline__ void touch_double(T* o, float x, bool seen, uint32_t g, 
   for (int i = e0; i < e1; i = next_entry(p->ids, i + 1, e1, id)) y += __ldg(p->bias + i);
   store_double(o, y);
 }
-template <typename T>
-__device__ __forceinline__ void touch(T* o, float x, bool seen, uint32_t g, int id, int e0, int e1, const Penalties* p) {
-  float hi = x, lo = 0.f;
+__device__ __forceinline__ void add_penalties(float& hi, float& lo, float x, bool seen, uint32_t g, const Penalties* p) {
+  hi = x;
+  lo = 0.f;
   if (seen && p->rep) {
     const float f = x > 0.f ? p->inv : p->rho, d = x > 0.f ? p->inv_lo : 0.f;
     const float y = x * f;
@@ -132,11 +132,42 @@ __device__ __forceinline__ void touch(T* o, float x, bool seen, uint32_t g, int 
     add_pair(hi, lo, -t, -fmaf(p->freq, n, -t));
     add_pair(hi, lo, -p->pres, 0.f);
   }
+}
+// Whether the pair does (else the value is formed again in 64 bits).
+__device__ __forceinline__ bool pair_does(float hi, float lo, uint32_t g) {
+  const float size = fabsf(hi);
+  return size > 7.9e-31f && size < 1.3e36f && fabsf(lo) <= size && g < (1u << 24);
+}
+template <typename T>
+__device__ __forceinline__ void touch(T* o, float x, bool seen, uint32_t g, int id, int e0, int e1, const Penalties* p) {
+  float hi, lo;
+  add_penalties(hi, lo, x, seen, g, p);
 #pragma unroll 1
   for (int i = e0; i < e1; i = next_entry(p->ids, i + 1, e1, id)) add_pair(hi, lo, __ldg(p->bias + i), 0.f);
-  const float size = fabsf(hi);
-  if (size > 7.9e-31f && size < 1.3e36f && fabsf(lo) <= size && g < (1u << 24)) store_value(o, hi, lo);
+  if (pair_does(hi, lo, g)) store_value(o, hi, lo);
   else touch_double(o, x, seen, g, id, e0, e1, p);
+}
+// The same by a warp, for a token whose entry i may not be the only one (nothing where it is not the first).  (Each lane
+// by itself: 752 rows of 2,563 with 253 biases, some ten of them twice, 56 us for 33; a call out of line, which needs a
+// stack, 16 short rows 10.4 for 8.9.)
+template <typename T>
+__device__ __forceinline__ void touch_many(T* o, float x, bool seen, uint32_t g, int i, int n, const Penalties* p) {
+  const int lane = threadIdx.x & 31, id = p->ids[i];
+  float hi, lo;
+  add_penalties(hi, lo, x, seen, g, p);
+#pragma unroll 1
+  for (int c = 0; c < n; c += 32) {
+    uint32_t hit = __ballot_sync(FULL_MASK, c + lane < n && p->ids[min(c + lane, n - 1)] == id);
+#pragma unroll 1
+    for (; hit; hit &= hit - 1) {
+      const int j = c + __ffs(hit) - 1;
+      if (j < i) return;
+      add_pair(hi, lo, __ldg(p->bias + j), 0.f);
+    }
+  }
+  if (lane != 0) return;
+  if (pair_does(hi, lo, g)) store_value(o, hi, lo);
+  else touch_double(o, x, seen, g, id, i, n, p);
 }
 
 // ------------------------------------------------------------------------------ the mask
@@ -475,16 +506,28 @@ __global__ void __launch_bounds__(AJ_TOUCH, 4) adjust_touch_kernel(const AdjustP
     if (!(s_biased[t >> 5] >> (t & 31) & 1) && (!m || allowed(m, t0 + t))) touch(o + t, static_cast<float>(x[t]), true, s_count[i], 0, 0, 0, &s_pen);
   }
   // tokens of the bias list, by the first entry that names them (from the last warps on, whose lists are the shortest)
-  for (int i = AJ_TOUCH - 1 - tid; i < p.n_bias; i += AJ_TOUCH) {
-    const int id = s_id[i];
+#pragma unroll 1
+  for (int i0 = 0; i0 < p.n_bias; i0 += AJ_TOUCH) {
+    const int i = i0 + AJ_TOUCH - 1 - tid, id = i < p.n_bias ? s_id[i] : -1;
     const uint32_t t = static_cast<uint32_t>(id) - t0;
-    if (t >= static_cast<uint32_t>(n) || (m && !allowed(m, id))) continue;
-    const bool twice = s_twice[(t >> 5) & 31] >> (t & 31) & 1;
-    if (twice && next_entry(s_id, 0, i, id) < i) continue;
-    const bool there = s_map[t >> 5] >> (t & 31) & 1;
-    const int k = there ? place(t) : 0;
-    if (LONG && k >= p.list) continue;
-    touch(o + t, static_cast<float>(x[t]), there, there ? s_count[k] : 0u, id, i, twice ? p.n_bias : i + 1, &s_pen);
+    bool mine = t < static_cast<uint32_t>(n) && (!m || allowed(m, id)), there = false, twice = false;
+    float v = 0.f;
+    uint32_t g = 0;
+    if (mine) {
+      there = s_map[t >> 5] >> (t & 31) & 1;
+      twice = s_twice[(t >> 5) & 31] >> (t & 31) & 1;
+      const int k = there ? place(t) : 0;
+      if (there) g = s_count[LONG ? min(k, p.list - 1) : k];
+      if (LONG && k >= p.list) mine = false;  // (of touch_rest)
+      else v = static_cast<float>(x[t]);
+    }
+    if (mine && !twice) touch(o + t, v, there, g, id, i, i + 1, &s_pen);
+#pragma unroll 1
+    for (uint32_t many = __ballot_sync(FULL_MASK, mine && twice); many; many &= many - 1) {
+      const int l = __ffs(many) - 1;
+      touch_many(o + __shfl_sync(FULL_MASK, t, l), __shfl_sync(FULL_MASK, v, l), __shfl_sync(FULL_MASK, there, l), __shfl_sync(FULL_MASK, g, l),
+                 __shfl_sync(FULL_MASK, i, l), p.n_bias, &s_pen);
+    }
   }
   if (LONG && all > p.list)
     touch_rest<T>(Rest<T>{x, o, m, s_map, s_biased, s_place, s_id, s_count, s_token, hist, &s_pen, t0, n, WORDS, lead, seen, from, p.list, all, p.n_bias,
