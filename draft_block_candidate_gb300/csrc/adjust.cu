@@ -27,8 +27,8 @@ static __device__ uint32_t g_err_adjust;
 // all sums are of integers.
 //
 // Bound by its steps' latency and its instructions: 256 rows of 151,936 in bf16 with histories of up to 4,096, 64 biases
-// and 16 grammars 35 us (23 at the copy rate), so that as many CTAs as can be share an SM: four of 512 threads, at 32
-// registers, 35.0 us, three 35.9, two that hold the piece in registers meanwhile 41.5.  Pieces of 64 KB go over a history
+// and 16 grammars 35.5 us (23.6 at the copy rate), so that as many CTAs as can be share an SM: four of 512 threads, at 32
+// registers, 35.0 us (before tokens of several biases went to a warp), three 35.9, two that hold the piece in registers meanwhile 41.5.  Pieces of 64 KB go over a history
 // half as often as those of 32 KB: those take 40.5 with 256 threads.  A mask alone, 512 rows in place, 33 us (25 at the copy
 // rate for the sectors that a mask takes in part); 256 threads, 37 with 512.
 // A history's tokens are at most as many as it is long, so lists grow with it, and fewer CTAs share an SM: lists end at
