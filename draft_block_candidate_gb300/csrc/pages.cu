@@ -172,8 +172,9 @@ __device__ __forceinline__ void each_page(const int32_t* refs, int64_t lo, int64
 // page of the row's own: where it holds none, or one that others hold too, it takes a free one.  Free
 // pages are taken lowest first, in the order of rows and columns.
 //
-// A column's decision stands in its entry until the pages are dealt: -1 where it holds none, -2 - p
-// where it gives up its hold of page p.  Bound by its dependent reads and its barriers: 1,024 rows of 16
+// Rows are written where they get their pages and nowhere else.  Until the pages are dealt the workspace says
+// which columns take one: a bit of a row's word for each where no row writes more than 31, else by how many
+// held each page before the call (by those counts alone a step of 1,024 rows took 18.7 us for 18.0).  Bound by its dependent reads and its barriers: 1,024 rows of 16
 // new tokens on a pool of 52,396 pages 13 us, 4 rows on a small one 5.5.  Pages and rows are counted
 // behind one barrier (with one for each, a small step's three kernels took 12.4 us for 8.3).
 struct GrowParams {
@@ -185,8 +186,9 @@ struct GrowParams {
   const int32_t *kv_len, *fresh;
   int32_t* tail_src;
   uint8_t* granted;
-  int32_t *need, *list;  // workspace: [rows], [n_pages]
-  int group_log2;        // lanes of a row
+  int32_t *need, *list, *held;  // workspace: [rows] columns that take a page, or how many; [n_pages]; [n_pages]
+  int steps;                    // columns that a row writes, at most
+  int group_log2;               // lanes of a row
 };
 
 template <int CTAS>
@@ -225,6 +227,8 @@ __global__ void __launch_bounds__(CL_THREADS) page_grow_kernel(const GrowParams 
     for (int o = G / 2; o >= 1; o >>= 1) v += __shfl_xor_sync(FULL_MASK, v, o);
     return v;
   };
+  const bool bits = p.steps <= 31;  // (and so a column a lane)
+  auto pages_of = [&](int need) { return need < 0 ? 0 : bits ? __popc(need) : need; };
   int64_t mine = 0;
   for (int64_t rb = r0; rb < r1; rb += per) {
     const int64_t r = rb + sub;
@@ -251,13 +255,16 @@ __global__ void __launch_bounds__(CL_THREADS) page_grow_kernel(const GrowParams 
       for (int c = s.c0 + in; c < s.c1; c += G) {
         const bool kept = c < s.c0 + G;
         const int id = kept ? id0 : row[c];
-        if (id >= 0 && (kept ? held0 : __ldcg(p.refs + id)) <= 1) continue;
-        ++need;
-        row[c] = id < 0 ? -1 : -2 - id;
+        if (id >= 0) {
+          const int held = kept ? held0 : __ldcg(p.refs + id);
+          if (!bits) p.held[id] = held;  // (the same by whoever comes upon it)
+          if (held <= 1) continue;
+        }
+        need += bits ? 1 << in : 1;
       }
     need = sum_group(need);
     if (r < r1 && in == 0) p.need[r] = ok ? need : -1;
-    mine += in == 0 ? need : 0;
+    mine += in == 0 ? pages_of(need) : 0;
   }
   const Place at_w = cluster_place<CTAS>(Counts{warp_sum(mine), free}, s_a);
   const int64_t want = at_w.all.x;
@@ -276,38 +283,33 @@ __global__ void __launch_bounds__(CL_THREADS) page_grow_kernel(const GrowParams 
   int64_t start = at_w.before.x;
   for (int64_t rb = r0; rb < r1; rb += per) {
     const int64_t r = rb + sub;
-    const int need = r < r1 ? p.need[r] : 0;
+    const int word = r < r1 ? p.need[r] : 0, need = pages_of(word);
     // where the row's pages begin
     int64_t k = start, all = 0;
     for (int i = 0; i < per; ++i) {
-      const int v = max(0, __shfl_sync(FULL_MASK, need, i << p.group_log2));
+      const int v = __shfl_sync(FULL_MASK, need, i << p.group_log2);
       if (i < sub) k += v;
       all += v;
     }
     start += all;
-    const bool ok = need == 0 || (need > 0 && k + need <= have);
+    const bool ok = word == 0 || (word > 0 && k + need <= have);
     int tail = -1;
     Span s{0, 0, true, false};
     if (r < r1 && need > 0) s = span(r);
     int32_t* row = p.table + r * p.row_stride;
-    const int steps = (p.max_new + p.page - 2) / p.page + 1;  // columns of any row, at most
-    for (int c0 = 0; c0 < steps; c0 += G) {
+    for (int c0 = 0; c0 < p.steps; c0 += G) {
       const int c = s.c0 + c0 + in;
       const bool here = c < s.c1;
       const int e = here ? row[c] : 0;
-      const bool give = here && e < 0;
+      const bool give = here && (bits ? word >> in & 1 : e < 0 || p.held[e] > 1);
       const unsigned b = __ballot_sync(FULL_MASK, give) >> (sub << p.group_log2) & (G == 32 ? FULL_MASK : (1u << G) - 1);
-      if (give) {
-        if (ok) {
-          const int id = __ldcg(p.list + k + __popc(b & ((1u << in) - 1)));
-          row[c] = id;
-          p.refs[id] = 1;
-          if (e <= -2) {
-            atomicSub(p.refs + (-2 - e), 1);
-            if (c == s.c0 && s.tail) tail = -2 - e;
-          }
-        } else {
-          row[c] = e <= -2 ? -2 - e : -1;
+      if (give && ok) {
+        const int id = __ldcg(p.list + k + __popc(b & ((1u << in) - 1)));
+        row[c] = id;
+        p.refs[id] = 1;
+        if (e >= 0) {
+          atomicSub(p.refs + e, 1);
+          if (c == s.c0 && s.tail) tail = e;
         }
       }
       k += __popc(b);
@@ -598,8 +600,9 @@ lilicorr_status lilicorr_kv8_grow(int32_t* refs, int64_t n_pages, int32_t* table
   p.cols = cols; p.page = page; p.max_new = max_new;
   p.kv_len = kv_len; p.fresh = new_tokens; p.tail_src = tail_src; p.granted = granted;
   p.list = static_cast<int32_t*>(workspace);
+  p.held = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + align256(size_t(n_pages) * 4));
   p.need = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + align256(size_t(n_pages) * 4) * 2);
-  const int most = (max_new + page - 2) / page + 1;
+  const int most = p.steps = (max_new + page - 2) / page + 1;
   while (p.group_log2 < 5 && (1 << p.group_log2) < most) ++p.group_log2;
   return done(launch_cluster(page_grow_kernel<1>, page_grow_kernel<CL_CTAS>, n_pages <= CL_SMALL && rows * most <= CL_SMALL_COLUMNS, p,
                              static_cast<cudaStream_t>(stream)));

@@ -1,0 +1,44 @@
+"""Calls at the limits of the operators around the loop: rows without pages for them, nothing to do at all,
+many requests of which few have rows, groups of heads that fill no half."""
+import pytest
+import torch
+
+from tests import loop_ref as R
+from tests.test_gpu_pages import pool, same
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def lc():
+    import __graft_entry__
+    __graft_entry__.build()
+    import draft_block_candidate_gb300 as lc
+    lc.device_error()
+    return lc
+
+
+@pytest.fixture(autouse=True)
+def _no_device_error(lc):
+    yield
+    assert lc.device_error() == 0
+
+
+@pytest.mark.parametrize("batch,beams,cols,page,new,spare", [
+    (1, 4, 3, 16, 40, 3), (3, 5, 9, 32, 70, 6), (40, 16, 5, 16, 64, 100), (2, 32, 300, 16, 30, 20), (1, 3, 260, 16, 1500, 60)])
+def test_grow_leaves_a_refused_row_as_it_was(lc, batch, beams, cols, page, new, spare):
+    """Any negative entry is none, and a row without pages for all its tokens keeps the one it had."""
+    g = torch.Generator().manual_seed(cols)
+    refs, table, kv_len = pool(batch, beams, cols, page, spare, cols, capacity=cols + new // page + 2)
+    refs[(refs == 0).nonzero()[spare:]] = 1  # (pages of others)
+    none = -torch.randint(1, 50, table.shape, generator=g, dtype=torch.int32)
+    none[torch.rand(table.shape, generator=g) < 0.1] = -(1 << 31)
+    table = torch.where(table < 0, none, table)
+    add = torch.randint(0, new + 1, kv_len.shape, generator=g, dtype=torch.int32)
+    flat = table.view(batch * beams, -1)
+    want = R.grow(refs, flat, kv_len.flatten(), add.flatten(), page)
+    assert not want[3].all()
+    refs, table = refs.cuda(), table.cuda()
+    tail, granted = lc.kv8_grow(refs, table, kv_len.cuda(), add.cuda(), page, new)
+    assert same(refs, want[0]) and same(table.view(batch * beams, -1), want[1])
+    assert same(tail.flatten(), want[2]) and same(granted.flatten(), want[3])
