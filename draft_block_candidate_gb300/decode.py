@@ -66,6 +66,8 @@ def _row_layout(shape, st):
     """(rows, columns, row stride) of rows that lie a uniform stride apart, else None."""
     cols = shape[-1]
     rows, row = 1, cols
+    if 0 in shape[:-1]:  # no rows, whatever their strides
+        return 0, cols, cols
     for n, s in zip(reversed(shape[:-1]), reversed(st[:-1])):
         if n == 1:
             continue

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from tests import loop_ref as R
-from tests.test_gpu_pages import pool, same
+from tests.test_gpu_pages import make_caches, pool, same
 
 pytestmark = pytest.mark.gpu
 
@@ -42,3 +42,15 @@ def test_grow_leaves_a_refused_row_as_it_was(lc, batch, beams, cols, page, new, 
     tail, granted = lc.kv8_grow(refs, table, kv_len.cuda(), add.cuda(), page, new)
     assert same(refs, want[0]) and same(table.view(batch * beams, -1), want[1])
     assert same(tail.flatten(), want[2]) and same(granted.flatten(), want[3])
+
+
+def test_pages_without_rows(lc):
+    refs = torch.ones(5, dtype=torch.int32, device="cuda")
+    for lead in ((0,), (4, 0), (0, 3)):
+        table, n = torch.zeros(*lead, 6, dtype=torch.int32, device="cuda"), torch.zeros(lead, dtype=torch.int32, device="cuda")
+        tail, granted = lc.kv8_grow(refs, table, n, n, 16, 1)
+        assert tail.shape == granted.shape == lead
+        lc.kv8_free(refs, table, n, 16)
+        caches = make_caches(lc, 1, 5, 1, 16, 32, 1)
+        assert lc.kv8_compact(caches, refs, [table]).tolist() == [5]
+    assert refs.tolist() == [1] * 5
