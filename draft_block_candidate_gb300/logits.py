@@ -86,7 +86,7 @@ def adjust_logits(logits: torch.Tensor, history: Optional[torch.Tensor] = None, 
             raise ValueError("at most 1024 biases")
     elif bias_values is not None:
         raise ValueError("biases need ids and values")
-    if groups < 1 or rows % groups:
+    if rows and (groups < 1 or rows % groups):
         raise ValueError(f"{groups} groups do not divide {rows} rows")
     for t, name, dtype in ((counted_from, "counted_from", torch.int32), (repetition, "repetition", torch.float32),
                            (presence, "presence", torch.float32), (frequency, "frequency", torch.float32)):

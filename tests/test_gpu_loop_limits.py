@@ -44,6 +44,21 @@ def test_grow_leaves_a_refused_row_as_it_was(lc, batch, beams, cols, page, new, 
     assert same(tail.flatten(), want[2]) and same(granted.flatten(), want[3])
 
 
+def test_adjust_without_rows_or_tokens(lc):
+    f32 = lambda *s: torch.zeros(*s, device="cuda")  # noqa: E731
+    e = torch.zeros(0, dtype=torch.int32, device="cuda")
+    words = torch.zeros(3, 4, dtype=torch.int32, device="cuda")
+    for x in (f32(0, 100), f32(4, 0, 100), f32(0, 3, 100)):
+        assert lc.adjust_logits(x) is x
+        assert lc.adjust_logits(x, mask=words, mask_index=e) is x
+        assert lc.adjust_logits(x, mask=words[:0]) is x
+        assert lc.adjust_logits(x, history=e.view(0, 1), seen=e, presence=f32(0), bias_ids=e.view(0, 2), bias_values=f32(0, 2)) is x
+        out = torch.empty_like(x)
+        assert lc.adjust_logits(x, out=out) is out
+    x = f32(3, 0)
+    assert lc.adjust_logits(x, mask=words[:, :0]) is x
+
+
 def test_pages_without_rows(lc):
     refs = torch.ones(5, dtype=torch.int32, device="cuda")
     for lead in ((0,), (4, 0), (0, 3)):
