@@ -66,6 +66,10 @@ def cross_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_start: 
     raw, ctx = _run_on(dev, stream)
 
     def call():
+        if total_kv == 0:  # a state that no request may have stands for none, so that who asks for one is reported
+            none = torch.zeros(1, kv_heads, D, dtype=torch.bfloat16, device=q.device)
+            return cross_attention(q, none, none, q_start, (kv_start == 0).int() * 2 - 1, kv_len, max_new, scale, out, new_lse or lse,
+                                   workspace)
         lib = L.lib()
         o, norm, ws = out, lse, workspace
         if o is None:

@@ -4,6 +4,7 @@ import pytest
 import torch
 
 from tests import loop_ref as R
+from tests.test_gpu_cross import check, i32
 from tests.test_gpu_pages import make_caches, pool, same
 
 pytestmark = pytest.mark.gpu
@@ -69,3 +70,17 @@ def test_pages_without_rows(lc):
         caches = make_caches(lc, 1, 5, 1, 16, 32, 1)
         assert lc.kv8_compact(caches, refs, [table]).tolist() == [5]
     assert refs.tolist() == [1] * 5
+
+
+def test_cross_without_states(lc):
+    """Keys and values of no states: rows of requests have out 0 and lse -inf, whoever asks for states is reported."""
+    q = torch.randn(6, 4, 64, device="cuda").to(torch.bfloat16)
+    k = torch.zeros(0, 2, 64, dtype=torch.bfloat16, device="cuda")
+    check(lc, q, k, k, i32(0, 2, 5), i32(0, 0), i32(0, 0), 3)
+    new, lse = lc.cross_attention(q, k, k, i32(0, 2, 5), i32(0, 0), i32(0, 0), 3, lse=True)
+    assert not new.any() and bool((lse == R.NEG).all())
+    for start, length in ((0, 1), (1, 0), (-1, 1), (-1, 0), (0, -1)):
+        out = torch.full_like(q, 7)
+        lc.cross_attention(q, k, k, i32(0, 2, 5), i32(start, 0), i32(length, 0), 3, out=out)
+        assert lc.device_error() == 1 << 26
+        assert bool((out[:2] == 7).all()) and not out[2:5].any() and bool((out[5] == 7).all())
