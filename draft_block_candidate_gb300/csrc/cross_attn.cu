@@ -480,7 +480,7 @@ __global__ void __launch_bounds__(32 * CR_WARPS, 1)
         const float nref = m == -INFINITY ? 0.f : -m;
         const float2 a2 = make_float2(a, a), b2 = make_float2(nref, nref);
         // 2. the weights, in the scores' place (16 columns of pairs for 32)
-        float2 sum[2] = {make_float2(l, 0.f), make_float2(0.f, 0.f)};
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};  // (of the chunk: small weights beside a heavy l)
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
           // (64 wide, where the products are half as long, the other half may begin earlier)
@@ -503,7 +503,7 @@ __global__ void __launch_bounds__(32 * CR_WARPS, 1)
             if (lane == 0) mbar_arrive(&pready[w >> 1][g]);
           }
         }
-        l = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         if (DP != 64 && two && lane == 0) mbar_arrive(&turn[g][k]);
         v += two;
       }

@@ -84,3 +84,23 @@ def test_cross_without_states(lc):
         lc.cross_attention(q, k, k, i32(0, 2, 5), i32(start, 0), i32(length, 0), 3, out=out)
         assert lc.device_error() == 1 << 26
         assert bool((out[:2] == 7).all()) and not out[2:5].any() and bool((out[5] == 7).all())
+
+
+@pytest.mark.parametrize("rows", [1, 129])
+@pytest.mark.parametrize("D", [64, 128])
+def test_cross_sums_keep_small_weights_beside_a_heavy_one(lc, rows, D):
+    """Weights below half a step of the heavy one's, which come to 2^-8 of it together: the sum of a row takes
+    128 of them at a time, so it is off by (T / 128 + 8) 2^-24 at most, and its logarithm, with the score's
+    2^-22 and a few roundings below 2^-20, too.  As many requests as keep each tile on one part of the GPU."""
+    T, batch, score = 65536, 304, 16.75  # (a product that bf16 and f32 hold: 8 times that, by 1 / 8)
+    k = torch.zeros(T, 1, D, dtype=torch.bfloat16, device="cuda")
+    k[0, 0, 0] = score
+    v = torch.ones_like(k)
+    q = torch.zeros(batch * rows, 1, D, dtype=torch.bfloat16, device="cuda")
+    q[:, :, 0] = 8
+    start = torch.zeros(batch, dtype=torch.int32, device="cuda")
+    q_start = torch.arange(batch + 1, dtype=torch.int32, device="cuda") * rows
+    out, lse = lc.cross_attention(q, k, v, q_start, start, start + T, rows, scale=0.125, lse=True)
+    assert bool(((out.double() - 1).abs() <= 2.0 ** -8 + (T / 128 + 8) * 2.0 ** -24).all())
+    want = score + torch.log1p((T - 1) * torch.tensor(-score).double().exp()).item()
+    assert (lse.double() - want).abs().max() <= (T / 128 + 8) * 2.0 ** -24 + 2.0 ** -22 * score + 2.0 ** -24 * want + 2.0 ** -20
