@@ -197,16 +197,8 @@ __global__ void __launch_bounds__(32 * CR_WARPS, 1)
   pdl_wait();
   pdl_trigger();
 
-  // A wait by a whole warp.  The first one that gives up makes every later one give up soon, and the
-  // roles' loops end.
-  auto wait_warp = [&](uint64_t* bar, uint32_t parity, uint32_t site) -> bool {
-#pragma unroll 1
-    for (uint32_t i = 0; !__all_sync(FULL_MASK, mbar_try_wait(bar, parity)); ++i)
-      if (__any_sync(FULL_MASK, i == WAIT_TRIES || s_fail != 0)) {
-        if (s_fail == 0) s_fail = site;
-        return false;
-      }
-    return true;
+  auto wait_warp = [&](uint64_t* bar, uint32_t parity, uint32_t site, uint32_t times = 1) {
+    return mbar_wait_warp(bar, parity, site, s_fail, times);
   };
   // The next piece with chunks (or, `all`, any), read by a warp.
   auto next_piece = [&](int& pi, CrossPiece& x, bool all) -> bool {
@@ -352,10 +344,11 @@ __global__ void __launch_bounds__(32 * CR_WARPS, 1)
     const int piece = lane % LPR;
     const Run run = find_run<CR_ROWS>(p, blockIdx.x, gridDim.x);
     Pieces<CR_ROWS, P> w(p, run);
+    const uint32_t times = wait_times(run.per);  // (a place in the ring, or of q, may be held for all of a piece)
     int qs = 0, pi = 0;
     auto leave = [&]() -> bool {
       const int e = pi % CR_PIECES;
-      bool ok = pi < CR_PIECES || wait_warp(&pc_empty[e], ((pi / CR_PIECES) - 1) & 1, ERR_KV8_EMPTY_WAIT);
+      bool ok = pi < CR_PIECES || wait_warp(&pc_empty[e], ((pi / CR_PIECES) - 1) & 1, ERR_KV8_EMPTY_WAIT, times);
       ok = ok && w.next();
       CrossPiece x{};
       x.whole = -1;
@@ -380,7 +373,7 @@ __global__ void __launch_bounds__(32 * CR_WARPS, 1)
 #pragma unroll 1
       for (int half = 0; x.c0 < x.cn && half * p.half_rows() < x.rows; ++half, ++qs) {
         const int s = qs & 1, row0 = x.row0 + half * p.half_rows(), rows = min(p.half_rows(), x.rows - half * p.half_rows());
-        if (qs > 1) wait_warp(&qfree[s], ((qs >> 1) - 1) & 1, ERR_KV8_S_WAIT);
+        if (qs > 1) wait_warp(&qfree[s], ((qs >> 1) - 1) & 1, ERR_KV8_S_WAIT, times);
         uint8_t* to = sm + S::OFF_Q + s * T;
         if (p.q_map) {  // whole tokens of a group's heads; rows behind the last are other requests', or zeros
           if (lane == 0) {

@@ -222,16 +222,8 @@ __global__ void __launch_bounds__(32 * AttnShape<D, ROWS>::WARPS, 1)
   pdl_wait();
   pdl_trigger();
 
-  // A wait by a whole warp.  The first one that gives up makes every later one give up soon, and
-  // the roles' loops end.
-  auto wait_warp = [&](uint64_t* bar, uint32_t parity, uint32_t site) -> bool {
-#pragma unroll 1
-    for (uint32_t i = 0; !__all_sync(FULL_MASK, try_wait_us(bar, parity)); ++i)
-      if (__any_sync(FULL_MASK, i == WAIT_TRIES || s_fail != 0)) {
-        if (s_fail == 0) s_fail = site;
-        return false;
-      }
-    return true;
+  auto wait_warp = [&](uint64_t* bar, uint32_t parity, uint32_t site, uint32_t times = 1) {
+    return mbar_wait_warp(bar, parity, site, s_fail, times);
   };
   // The next piece, read by a warp.
   auto next_piece = [&](int pi, Piece& x) -> bool {
@@ -547,7 +539,7 @@ __global__ void __launch_bounds__(32 * AttnShape<D, ROWS>::WARPS, 1)
         float top = -INFINITY, total = 0.f;
         if (some) {
           const int e = (qi - 1) % OUT_RING;
-          wait_warp(&met[e][k], ((qi - 1) / OUT_RING) & 1, ERR_KV8_PV_WAIT);
+          wait_warp(&met[e][k], ((qi - 1) / OUT_RING) & 1, ERR_KV8_PV_WAIT, wait_times(y.cn - y.c0));  // (for all of the piece)
           top = s_m[e][r];
           // the groups' sums; one of 0 is of no chunk, or of none that the row sees
           const float2 s0 = s_ml[e][0][r], s1 = s_ml[e][1][r];

@@ -148,19 +148,27 @@ __device__ __forceinline__ void tmem_ld32_end(float* v) {
                : "memory");
   asm volatile("" : "+f"(v[29]), "+f"(v[30]), "+f"(v[31]));
 }
-// Whether a phase has ended; waits for it up to a microsecond or so.  A wait takes at most
-// WAIT_TRIES of them, about a second.
-constexpr uint32_t WAIT_TRIES = 1u << 20;
-__device__ __forceinline__ bool try_wait_us(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_addr(bar)), "r"(parity), "r"(1000u)
-      : "memory");
-  return ok != 0;
+// A wait by a whole warp, at most `times` times WAIT_LIMIT_CYCLES (a try that fails takes some 4 us, so the clock's low
+// half tells).  The first one of a CTA that gives up makes every later one give up soon, and the roles' loops end.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, uint32_t site, volatile uint32_t& fail, uint32_t times = 1) {
+  uint32_t since = static_cast<uint32_t>(clock());
+#pragma unroll 1
+  while (!__all_sync(FULL_MASK, mbar_try_wait(bar, parity))) {
+    if (__any_sync(FULL_MASK, static_cast<uint32_t>(clock()) - since > static_cast<uint32_t>(WAIT_LIMIT_CYCLES) || fail != 0)) {
+      if (times > 1 && !__any_sync(FULL_MASK, fail != 0)) {
+        --times;
+        since = static_cast<uint32_t>(clock());
+        continue;
+      }
+      if (fail == 0) fail = site;
+      return false;
+    }
+  }
+  return true;
 }
+// `times` of a wait that may last as long as a CTA's work on so many chunks of 128 tokens, which takes 10,000 cycles a chunk
+// at most (2^16 of them a time: three times that).
+__device__ __forceinline__ uint32_t wait_times(int64_t chunks) { return 1 + static_cast<uint32_t>(min(chunks >> 16, int64_t(1) << 24)); }
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));

@@ -1,10 +1,12 @@
 """Calls at the limits of the operators around the loop: rows without pages for them, nothing to do at all,
 many requests of which few have rows, groups of heads that fill no half."""
+import math
+
 import pytest
 import torch
 
 from tests import loop_ref as R
-from tests.test_gpu_cross import check, i32
+from tests.test_gpu_cross import check, i32, make
 from tests.test_gpu_pages import make_caches, pool, same
 
 pytestmark = pytest.mark.gpu
@@ -104,3 +106,71 @@ def test_cross_sums_keep_small_weights_beside_a_heavy_one(lc, rows, D):
     assert bool(((out.double() - 1).abs() <= 2.0 ** -8 + (T / 128 + 8) * 2.0 ** -24).all())
     want = score + torch.log1p((T - 1) * torch.tensor(-score).double().exp()).item()
     assert (lse.double() - want).abs().max() <= (T / 128 + 8) * 2.0 ** -24 + 2.0 ** -22 * score + 2.0 ** -24 * want + 2.0 ** -20
+
+
+MANY = 1 << 20
+
+
+def sparse(rows, lens, device="cuda"):
+    """(q_start, lengths) of 2^20 requests of which a few, far apart, have rows."""
+    at = torch.linspace(0, MANY - 1, len(rows)).long()
+    n, t = torch.zeros(MANY, dtype=torch.long), torch.zeros(MANY, dtype=torch.int32)
+    n[at], t[at] = torch.tensor(rows), torch.tensor(lens, dtype=torch.int32)
+    return at, torch.cat([torch.zeros(1, dtype=torch.long), n.cumsum(0)]).int().to(device), t.to(device)
+
+
+def test_cross_many_requests_without_rows(lc):
+    """Runs of work that go on behind hundreds of thousands of requests without any."""
+    rows, lens = [2, 300, 1, 3], [70000, 129, 1, 90000]
+    q, k, v, few_start, kv_start, kv_len = make(list(zip(rows, lens)), 2, 2, 64, 5)
+    at, q_start, length = sparse(rows, lens)
+    start = torch.zeros(MANY, dtype=torch.int32, device="cuda")
+    start[at.cuda()] = kv_start
+    want = lc.cross_attention(q, k, v, few_start, kv_start, kv_len, 300)
+    assert torch.equal(lc.cross_attention(q, k, v, q_start, start, length, 300), want)
+
+
+@pytest.mark.parametrize("new", [2, 40])
+def test_cache_attention_many_requests_without_rows(lc, new):
+    rows, lens, cols = [new, 1, new - 1], [31900, 128, 30000], 250
+    cache = make_caches(lc, 1, 500, 4, 128, 64, 2)[0]
+    for t in (cache.k, cache.v):  # (no NaN among the codes)
+        b = t.view(torch.uint8)
+        b[(b & 127) == 127] = 3
+    q = torch.randn(sum(rows), 4, 64, device="cuda").to(torch.bfloat16)
+    at, q_start, length = sparse(rows, lens)
+    pages = torch.randperm(500, generator=torch.Generator().manual_seed(1)).int().cuda()
+    small = torch.stack([pages[:cols], pages[:cols].flip(0), pages[cols:2 * cols]])
+    table = torch.full((MANY, cols), -1, dtype=torch.int32, device="cuda")
+    table[at.cuda()] = small
+    want = lc.kv8_attention(q, cache, i32(0, *torch.tensor(rows).cumsum(0).tolist()), i32(*lens), small, new)
+    assert torch.equal(lc.kv8_attention(q, cache, q_start, length, table, new), want)
+
+
+def test_cross_tiles_that_take_longer_than_a_wait(lc):
+    """A CTA's first tile holds the places of q of its second one for more than a second."""
+    n, rows = 144 << 20, 228 * 256
+    k, v = (torch.full((n, 1, 8), x, dtype=torch.bfloat16, device="cuda") for x in (0.0, 1.0))
+    q = torch.ones(rows, 1, 8, dtype=torch.bfloat16, device="cuda")
+    out, lse = lc.cross_attention(q, k, v, i32(0, rows), i32(0), i32(n), rows, lse=True)
+    # The tensor cores drop what a product has 2^-25 below the first bit of the sum that it is added to: weights of 1
+    # are added up exactly to 2^26, and from there on not at all.
+    assert bool(((out >= (1 - 2.0 ** -8) * 2.0 ** 26 / n) & (out <= 1)).all())
+    assert (lse.double() - math.log(n)).abs().max() <= (n / 128 + 8) * 2.0 ** -24
+
+
+def test_cache_attention_tiles_that_take_longer_than_a_wait(lc):
+    """The outputs of a tile are waited for while its tokens are gone over."""
+    D, page = 32, 128
+    n, rows = 140 << 20, 228 * 128
+    cache = lc.KV8Cache(1, 1, page, D)
+    cache.k.view(torch.uint8).fill_(0)
+    cache.v.view(torch.uint8).fill_(0x38)  # 1
+    cache.k_scale.fill_(1)
+    cache.v_scale.fill_(1)
+    table = torch.zeros(1, n // page, dtype=torch.int32, device="cuda")
+    q = torch.ones(rows, 1, D, dtype=torch.bfloat16, device="cuda")
+    out, lse = lc.kv8_attention(q, cache, i32(0, rows), i32(n), table, rows, lse=True)
+    assert bool(((out >= (1 - 2.0 ** -8) * 2.0 ** 26 / n) & (out <= 1)).all())  # (as above)
+    seen = torch.arange(n - rows + 1, n + 1, device="cuda").double()
+    assert (lse[:, 0].double() - seen.log()).abs().max() <= (n / 16 + 40) * 2.0 ** -24
