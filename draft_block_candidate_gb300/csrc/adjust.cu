@@ -550,6 +550,15 @@ lilicorr_status fail(lilicorr_status st, const char* msg) {
   return st;
 }
 
+// Whether [b, b + n) shares a byte with one of the rows of `bytes` from o on, `stride` apart.
+using wide = unsigned __int128;
+bool rows_meet(const void* o, int64_t rows, wide stride, wide bytes, const void* b, wide n) {
+  const wide x = reinterpret_cast<uintptr_t>(o), y = reinterpret_cast<uintptr_t>(b);
+  if (!b || y + n <= x || y >= x + (rows - 1) * stride + bytes) return false;
+  const wide r = y <= x ? 0 : (y - x) / stride;  // the last row that begins no later than b, or the first
+  return y < x + r * stride + bytes || y + n > x + (r + 1) * stride;
+}
+
 template <typename T>
 cudaError_t adjust_launch(const AdjustParams& p, int64_t pieces, bool touch, cudaStream_t stream) {
   const bool inplace = p.x == p.out;
@@ -586,8 +595,8 @@ extern "C" lilicorr_status lilicorr_adjust_logits(const lilicorr_adjust* a, void
   const uintptr_t x = reinterpret_cast<uintptr_t>(a->logits), o = reinterpret_cast<uintptr_t>(a->out);
   if (x % es || o % es) return bad("lilicorr_adjust_logits: logits are element aligned");
   if (a->logits == a->out ? a->row_stride != a->out_stride
-                          : x < o + uintptr_t((a->rows - 1) * a->out_stride + a->V) * es &&
-                                o < x + uintptr_t((a->rows - 1) * a->row_stride + a->V) * es)
+                          : x < o + (wide(a->rows - 1) * a->out_stride + a->V) * es &&
+                                o < x + (wide(a->rows - 1) * a->row_stride + a->V) * es)
     return bad("lilicorr_adjust_logits: out is the logits themselves, or shares nothing with them");
   if (a->groups < 1 || a->rows % a->groups) return bad("lilicorr_adjust_logits: groups divides rows");
   if (a->history && (!a->seen || a->cap < 1 || a->cap >= 1 << 29 || a->history_stride < a->cap || a->history_stride > LIM))
@@ -600,6 +609,15 @@ extern "C" lilicorr_status lilicorr_adjust_logits(const lilicorr_adjust* a, void
                   (!a->mask_index && a->n_masks < a->rows)))
     return bad("lilicorr_adjust_logits: masks have (V + 31) / 32 words, one for each row or an index");
   if (!a->mask && a->mask_index) return bad("lilicorr_adjust_logits: an index needs masks");
+  // CTAs read what they need of these while others write
+  auto met = [&](const void* b, int64_t rows, int64_t row, int64_t stride) {
+    return rows_meet(a->out, a->rows, wide(a->out_stride) * es, wide(a->V) * es, b, (wide(rows - 1) * stride + row) * 4);
+  };
+  if (met(a->history, a->groups, a->cap, a->history_stride) || met(a->seen, a->rows, 1, 1) || met(a->counted_from, a->groups, 1, 1) ||
+      met(a->repetition, a->groups, 1, 1) || met(a->presence, a->groups, 1, 1) || met(a->frequency, a->groups, 1, 1) ||
+      (a->n_bias > 0 && (met(a->bias_id, a->groups, a->n_bias, a->n_bias) || met(a->bias, a->groups, a->n_bias, a->n_bias))) ||
+      met(a->mask, a->n_masks, (a->V + 31) / 32, a->mask_stride) || met(a->mask_index, a->rows, 1, 1))
+    return bad("lilicorr_adjust_logits: out shares memory with what is read besides the logits");
   AdjustParams p{};
   p.x = a->logits; p.out = a->out;
   p.x_stride = a->row_stride; p.out_stride = a->out_stride;

@@ -429,7 +429,7 @@ lilicorr_status lilicorr_kv8_attention(const lilicorr_kv8_cache* cache, const vo
  * in pairs of f32 (off by 2^-46 of the terms' magnitudes for each of them), or in 64 bits where those do
  * not do, and rounded once; a token that nothing touches is copied bit for bit (a NaN that a mask
  * takes out becomes -inf).  out is the logits themselves (with the same row stride), or apart from
- * them; what lies behind a row's V logits is not touched.
+ * them, and apart from all else that is read; what lies behind a row's V logits is not touched.
  *   logits, out  [rows, V] F32 or BF16, rows a stride >= V apart, element aligned
  *   history      nullable [groups, cap] int32, cap < 2^29, rows history_stride apart; ids outside 0..V-1 are passed over
  *   seen         [rows] int32, at most cap (else the row is left out, and bit 26 of the device error word set)

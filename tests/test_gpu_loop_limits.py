@@ -62,6 +62,25 @@ def test_adjust_without_rows_or_tokens(lc):
     assert lc.adjust_logits(x, mask=words[:, :0]) is x
 
 
+def test_adjust_takes_what_lies_between_the_rows(lc):
+    """What is read may lie behind a row's last token, but not among those that are written."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    buf = torch.zeros(8, 1024, dtype=torch.bfloat16, device="cuda")
+    x = buf[:, :1000]
+    x.copy_(torch.randn(8, 1000, generator=g, device="cuda"))
+    history = torch.randint(0, 1000, (2, 40), generator=g, device="cuda", dtype=torch.int32)
+    seen, penalty = i32(3, 40, 0, 7, 22, 40, 1, 39), torch.tensor([0.5, 1.5], device="cuda")
+    want = lc.adjust_logits(x, history=history, seen=seen, presence=penalty, out=torch.empty_like(x))
+    raw = buf.view(torch.uint8).flatten()
+    there = raw[3 * 2048 + 2000:][:32].view(torch.int32)
+    there.copy_(seen)
+    lc.adjust_logits(x, history=history, seen=there, presence=penalty)
+    assert torch.equal(x, want) and torch.equal(there, seen)
+    for at in (3 * 2048 + 1996, 3 * 2048 + 2020, 0):
+        with pytest.raises(lc.LilicorrError):
+            lc.adjust_logits(x, history=history, seen=raw[at:][:32].view(torch.int32), presence=penalty)
+
+
 def test_pages_without_rows(lc):
     refs = torch.ones(5, dtype=torch.int32, device="cuda")
     for lead in ((0,), (4, 0), (0, 3)):
