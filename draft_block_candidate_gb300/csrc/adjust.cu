@@ -594,6 +594,8 @@ extern "C" lilicorr_status lilicorr_adjust_logits(const lilicorr_adjust* a, void
     return bad("lilicorr_adjust_logits: rows, V or a row stride is out of range");
   const uintptr_t x = reinterpret_cast<uintptr_t>(a->logits), o = reinterpret_cast<uintptr_t>(a->out);
   if (x % es || o % es) return bad("lilicorr_adjust_logits: logits are element aligned");
+  if (!word_aligned({a->history, a->seen, a->counted_from, a->repetition, a->presence, a->frequency, a->bias_id, a->bias, a->mask, a->mask_index}))
+    return bad("lilicorr_adjust_logits: what is read besides the logits is 4-byte aligned");
   if (a->logits == a->out ? a->row_stride != a->out_stride
                           : x < o + (wide(a->rows - 1) * a->out_stride + a->V) * es &&
                                 o < x + (wide(a->rows - 1) * a->row_stride + a->V) * es)

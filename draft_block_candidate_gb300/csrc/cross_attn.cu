@@ -709,6 +709,7 @@ lilicorr_status lilicorr_cross_attention(const void* q, int64_t q_token_stride, 
   if (!why) why = rows_error(v, v_token_stride, v_head_stride);
   if (!why && !dim_ok(head_dim)) why = "head_dim is a multiple of 8, at most 128";
   if (!why && (!q_start || !kv_start || !kv_len)) why = "null pointer";
+  if (!why && !word_aligned({q_start, kv_start, kv_len, lse})) why = "row ranges, lengths and lse are 4-byte aligned";
   if (!why && (batch < 1 || batch > (1 << 20))) why = "1 <= batch <= 2^20";
   if (!why && (total < 1 || total > INT_MAX || total_kv < 1 || total_kv > INT_MAX - 256)) why = "rows are out of range";
   if (!why && (max_new < 1 || max_new > (1 << 24))) why = "1 <= max_new <= 2^24";

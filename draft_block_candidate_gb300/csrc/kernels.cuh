@@ -1,6 +1,7 @@
 // Host-side launchers of the rerank kernels (one declaration shared by all units).
 #pragma once
 
+#include <initializer_list>
 #include <utility>
 
 #include "common.cuh"
@@ -30,6 +31,13 @@ cudaError_t kv8_read_device_error(uint32_t* code);
 cudaError_t pages_read_device_error(uint32_t* code);
 cudaError_t adjust_read_device_error(uint32_t* code);
 cudaError_t cross_read_device_error(uint32_t* code);  // cross_attn.cu
+
+// Whether arrays of 32-bit words begin where such words do (null: there is none).
+inline bool word_aligned(std::initializer_list<const void*> arrays) {
+  for (const void* a : arrays)
+    if (reinterpret_cast<uintptr_t>(a) % 4) return false;
+  return true;
+}
 
 // message returned by lilicorr_last_error() for this thread (lilicorr_api.cu)
 void set_last_error(const char* msg);

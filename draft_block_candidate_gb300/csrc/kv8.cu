@@ -210,6 +210,7 @@ const char* batch_error(const int32_t* q_start, const int32_t* kv_len, int64_t b
                         const int32_t* table, int64_t table_stride, int32_t cols, int64_t total,
                         int32_t max_new, int page) {
   if (!q_start || !kv_len || !table) return "null pointer";
+  if (!word_aligned({q_start, kv_len, table})) return "row ranges, lengths and tables are 4-byte aligned";
   if (batch < 1 || batch > (1 << 20)) return "1 <= batch <= 2^20";
   if (cols < 1 || int64_t(cols) * page > INT_MAX - 256) return "a table row holds 1 page to 2^31 tokens";
   if (table_stride < cols) return "table_stride is at least its columns";
@@ -251,6 +252,7 @@ lilicorr_status lilicorr_kv8_append(const lilicorr_kv8_cache* cache, const void*
   if (!why) why = batch_error(q_start, kv_len, batch, block_table, table_stride, cols, total, max_new, cache->page);
   if (!why) why = rows_error(k, k_token_stride, k_head_stride);
   if (!why) why = rows_error(v, v_token_stride, v_head_stride);
+  if (!why && !word_aligned({tail_src})) why = "tail_src is 4-byte aligned";
   if (why) return fail(LILICORR_ERR_INVALID_ARG, why);
   AppendParams prm{};
   prm.c = view(cache);
@@ -305,6 +307,7 @@ lilicorr_status lilicorr_kv8_attention(const lilicorr_kv8_cache* cache, const vo
   if (!why) why = batch_error(q_start, kv_len, batch, block_table, table_stride, cols, total, max_new, cache->page);
   if (!why) why = rows_error(q, q_token_stride, q_head_stride);
   if (!why && (!out || reinterpret_cast<uintptr_t>(out) % 16)) why = "out is null or not 16-byte aligned";
+  if (!why && !word_aligned({lse})) why = "lse is 4-byte aligned";
   if (!why && (q_heads < 1 || q_heads % cache->kv_heads || q_heads / cache->kv_heads > 1024))
     why = "q_heads is a multiple of kv_heads, at most 1024 times it";
   // a sequence's rows, and its work units (tiles x heads x chunks of tokens, and some for

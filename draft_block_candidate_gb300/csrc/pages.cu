@@ -509,7 +509,6 @@ lilicorr_status fail(lilicorr_status st, const char* msg) {
 lilicorr_status done(cudaError_t e) { return e == cudaSuccess ? LILICORR_OK : fail(LILICORR_ERR_CUDA, cudaGetErrorString(e)); }
 
 constexpr int64_t LIM = int64_t(1) << 40;
-bool aligned4(const void* p) { return reinterpret_cast<uintptr_t>(p) % 4 == 0; }
 bool page_ok(int page) { return page == 16 || page == 32 || page == 64 || page == 128; }
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
@@ -539,11 +538,11 @@ cudaError_t launch_cluster(void (*one)(P), void (*many)(P), bool small, const P&
 
 // Null where the counts and a table's rows are in order, else what is wrong.
 const char* pool_error(const int32_t* refs, int64_t n_pages) {
-  if (!refs || !aligned4(refs)) return "refs is null or misaligned";
+  if (!refs || !word_aligned({refs})) return "refs is null or misaligned";
   return n_pages < 1 || n_pages > INT_MAX ? "1 <= n_pages < 2^31" : nullptr;
 }
 const char* table_error(const int32_t* table, int64_t rows, int64_t stride, int32_t cols) {
-  if (!table || !aligned4(table)) return "a table is null or misaligned";
+  if (!table || !word_aligned({table})) return "a table is null or misaligned";
   if (rows < 1 || rows > INT_MAX || cols < 1 || cols > INT_MAX - 1024) return "a table's size is out of range";
   if (stride < cols || stride > LIM) return "a table's row stride is at least its columns";
   return nullptr;
@@ -567,7 +566,7 @@ lilicorr_status lilicorr_kv8_fork(int32_t* refs, int64_t n_pages, int32_t* table
   if (!why) why = table_error(table, batch, beams > 1 ? row_stride : cols, cols);
   if (!why && (beams < 1 || beams > FK_MAX)) why = "1 <= beams <= 32";
   if (!why && batch > 1 && (batch_stride < (beams - 1) * row_stride + cols || batch_stride > LIM)) why = "batch_stride is at least its rows";
-  if (!why && (!parent || !aligned4(parent))) why = "parent is null or misaligned";
+  if (!why && (!parent || !word_aligned({parent}))) why = "parent is null or misaligned";
   if (why) return fail(LILICORR_ERR_INVALID_ARG, why);
   const int tiles = (cols + FK_THREADS - 1) / FK_THREADS;
   if (batch > INT_MAX / tiles) return fail(LILICORR_ERR_INVALID_ARG, "batch * cols is too large for one call");
@@ -591,6 +590,7 @@ lilicorr_status lilicorr_kv8_grow(int32_t* refs, int64_t n_pages, int32_t* table
   if (!why && int64_t(cols) * page > INT_MAX - 256) why = "a table row holds 1 page to 2^31 tokens";
   if (!why && (max_new < 1 || max_new > 1 << 24)) why = "1 <= max_new <= 2^24";
   if (!why && (!kv_len || !new_tokens || !tail_src || !granted)) why = "null pointer";
+  if (!why && !word_aligned({kv_len, new_tokens, tail_src})) why = "lengths and tail_src are 4-byte aligned";
   if (why) return fail(LILICORR_ERR_INVALID_ARG, why);
   if (!workspace || workspace_bytes < lilicorr_kv8_pages_workspace_bytes(n_pages, rows) || reinterpret_cast<uintptr_t>(workspace) % 256)
     return fail(LILICORR_ERR_WORKSPACE, "lilicorr_kv8_grow: workspace missing, too small or misaligned");
@@ -613,7 +613,7 @@ lilicorr_status lilicorr_kv8_free(int32_t* refs, int64_t n_pages, int32_t* table
   const char* why = pool_error(refs, n_pages);
   if (!why) why = table_error(table, rows, rows > 1 ? row_stride : cols, cols);
   if (!why && !page_ok(page)) why = "page is 16, 32, 64 or 128";
-  if (!why && (!keep || !aligned4(keep))) why = "keep is null or misaligned";
+  if (!why && (!keep || !word_aligned({keep}))) why = "keep is null or misaligned";
   const int tiles = (cols - 1) / FR_THREADS + 1;
   if (!why && rows > INT_MAX / tiles) why = "rows * cols is too large for one call";
   if (why) return fail(LILICORR_ERR_INVALID_ARG, why);
@@ -664,7 +664,7 @@ lilicorr_status lilicorr_kv8_copy(const lilicorr_kv8_cache* from, const lilicorr
   if (n_caches < 1 || !from || !to) return fail(LILICORR_ERR_INVALID_ARG, "lilicorr_kv8_copy: no caches");
   const char* why = caches_error(from, n_caches, from[0], true);
   if (!why) why = caches_error(to, n_caches, from[0], false);
-  if (!why && (!src || !dst || !aligned4(src) || !aligned4(dst))) why = "src or dst is null or misaligned";
+  if (!why && (!src || !dst || !word_aligned({src, dst}))) why = "src or dst is null or misaligned";
   if (!why && (n < 1 || n > INT_MAX)) why = "1 <= n < 2^31";
   if (why) return fail(LILICORR_ERR_INVALID_ARG, why);
   for (int i = 0; i < n_caches; i += MV_CACHES) {
@@ -696,7 +696,7 @@ lilicorr_status lilicorr_kv8_compact(const lilicorr_kv8_cache* caches, int32_t n
     if (!why) why = table_error(t.out, t.rows, t.rows > 1 ? t.out_stride : t.cols, t.cols);
     if (!why && t.table == t.out && t.row_stride != t.out_stride) why = "a table in place keeps its stride";
   }
-  if (!why && (!live || !aligned4(live))) why = "live is null or misaligned";
+  if (!why && (!live || !word_aligned({live}))) why = "live is null or misaligned";
   if (why) return fail(LILICORR_ERR_INVALID_ARG, why);
   if (!workspace || workspace_bytes < lilicorr_kv8_pages_workspace_bytes(n_pages, 1) || reinterpret_cast<uintptr_t>(workspace) % 256)
     return fail(LILICORR_ERR_WORKSPACE, "lilicorr_kv8_compact: workspace missing, too small or misaligned");

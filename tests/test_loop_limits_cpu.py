@@ -46,3 +46,39 @@ def test_adjust_refuses_to_write_what_it_reads(lib, name, size, out):
     """In place and apart: at the first and last byte of the rows, across a row's beginning, within one."""
     for at in (out - size + 4, out, out + 1996, out + 2048 - size + 4, out + 3000, out + 7 * 2048 + 1996):
         assert adjust(lib, out=out, **{name: at}) == INVALID, at - out
+
+
+@pytest.mark.parametrize("name", [n for n, _ in ARRAYS])
+def test_adjust_refuses_misaligned_arrays(lib, name):
+    at = (2 + [n for n, _ in ARRAYS].index(name)) * FAR
+    assert adjust(lib, **{name: at + 2}) == INVALID
+
+
+@pytest.mark.parametrize("name", ["kv", "new", "tail"])
+def test_grow_refuses_misaligned_arrays(lib, name):
+    a = dict(kv=3 * FAR, new=4 * FAR, tail=5 * FAR)
+    a[name] += 2
+    assert lib.lilicorr_kv8_grow(FAR, 100, 2 * FAR, 4, 8, 8, a["kv"], a["new"], 64, 4, a["tail"], 6 * FAR, 7 * FAR, 1 << 20, None) == INVALID
+
+
+@pytest.mark.parametrize("name", ["q_start", "kv_start", "kv_len", "lse"])
+def test_cross_refuses_misaligned_arrays(lib, name):
+    a = dict(q_start=4 * FAR, kv_start=5 * FAR, kv_len=6 * FAR, lse=9 * FAR)
+    a[name] += 2
+    assert lib.lilicorr_cross_attention(FAR, 1024, 128, 8, 8, 2 * FAR, 512, 128, 3 * FAR, 512, 128, 100, 2, 128, a["q_start"], a["kv_start"], a["kv_len"],
+                                        2, 4, 0.1, 8 * FAR, a["lse"], 10 * FAR, 1 << 30, None) == INVALID
+    assert b"4-byte aligned" in lib.lilicorr_last_error()  # (without a GPU's driver there is no tensor map either)
+
+
+@pytest.mark.parametrize("name", ["q_start", "kv_len", "table", "lse", "tail"])
+def test_the_cache_refuses_misaligned_arrays(lib, name):
+    from draft_block_candidate_gb300 import _lib as L
+    cache = C.byref(L.Kv8CacheDesc(k_pages=FAR, v_pages=2 * FAR, k_scale=3 * FAR, v_scale=4 * FAR, n_pages=10, kv_heads=2, page=64, head_dim=128))
+    a = dict(q_start=5 * FAR, kv_len=6 * FAR, table=7 * FAR, lse=8 * FAR, tail=9 * FAR)
+    a[name] += 2
+    if name != "tail":
+        assert lib.lilicorr_kv8_attention(cache, 10 * FAR, 1024, 128, 8, 8, a["q_start"], a["kv_len"], 2, a["table"], 4, 4, 4, 0.1, 11 * FAR, a["lse"],
+                                          12 * FAR, 1 << 30, None) == INVALID
+    if name != "lse":
+        assert lib.lilicorr_kv8_append(cache, 10 * FAR, 256, 128, 11 * FAR, 256, 128, 8, a["q_start"], a["kv_len"], 2, a["table"], 4, 4, 4, a["tail"],
+                                       None) == INVALID
