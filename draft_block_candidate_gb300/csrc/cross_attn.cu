@@ -737,11 +737,11 @@ lilicorr_status lilicorr_cross_attention(const void* q, int64_t q_token_stride, 
     return x < y + m && y < x + n;
   };
   const wide o_bytes = wide(total) * q_heads * head_dim * 2, l_bytes = wide(total) * q_heads * 4;
-  const void* in[3] = {q, k, v};
-  const wide in_bytes[3] = {extent(total, q_token_stride, q_heads, q_head_stride), extent(total_kv, k_token_stride, kv_heads, k_head_stride),
-                            extent(total_kv, v_token_stride, kv_heads, v_head_stride)};
+  const void* in[6] = {q, k, v, q_start, kv_start, kv_len};
+  const wide in_bytes[6] = {extent(total, q_token_stride, q_heads, q_head_stride), extent(total_kv, k_token_stride, kv_heads, k_head_stride),
+                            extent(total_kv, v_token_stride, kv_heads, v_head_stride), wide(batch + 1) * 4, wide(batch) * 4, wide(batch) * 4};
   bool overlap = lse && meet(out, o_bytes, lse, l_bytes);
-  for (int i = 0; i < 3; ++i) overlap = overlap || meet(in[i], in_bytes[i], out, o_bytes) || (lse && meet(in[i], in_bytes[i], lse, l_bytes));
+  for (int i = 0; i < 6; ++i) overlap = overlap || meet(in[i], in_bytes[i], out, o_bytes) || (lse && meet(in[i], in_bytes[i], lse, l_bytes));
   if (overlap) return fail(LILICORR_ERR_INVALID_ARG, "lilicorr_cross_attention: out and lse overlap one another, or what is read");
   CrossParams p{};
   p.q = static_cast<const __nv_bfloat16*>(q);

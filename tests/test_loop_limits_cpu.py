@@ -61,13 +61,28 @@ def test_grow_refuses_misaligned_arrays(lib, name):
     assert lib.lilicorr_kv8_grow(FAR, 100, 2 * FAR, 4, 8, 8, a["kv"], a["new"], 64, 4, a["tail"], 6 * FAR, 7 * FAR, 1 << 20, None) == INVALID
 
 
+def cross(lib, **kw):
+    """(status, message) of a call whose arrays lie far apart."""
+    a = dict(q=FAR, k=2 * FAR, v=3 * FAR, q_start=4 * FAR, kv_start=5 * FAR, kv_len=6 * FAR, out=8 * FAR, lse=9 * FAR)
+    a.update(kw)
+    st = lib.lilicorr_cross_attention(a["q"], 1024, 128, 8, 8, a["k"], 512, 128, a["v"], 512, 128, 100, 2, 128, a["q_start"], a["kv_start"], a["kv_len"],
+                                      2, 4, 0.1, a["out"], a["lse"], 10 * FAR, 1 << 30, None)
+    return st, lib.lilicorr_last_error()  # (without a GPU's driver there is no tensor map, which is refused alike)
+
+
 @pytest.mark.parametrize("name", ["q_start", "kv_start", "kv_len", "lse"])
 def test_cross_refuses_misaligned_arrays(lib, name):
-    a = dict(q_start=4 * FAR, kv_start=5 * FAR, kv_len=6 * FAR, lse=9 * FAR)
-    a[name] += 2
-    assert lib.lilicorr_cross_attention(FAR, 1024, 128, 8, 8, 2 * FAR, 512, 128, 3 * FAR, 512, 128, 100, 2, 128, a["q_start"], a["kv_start"], a["kv_len"],
-                                        2, 4, 0.1, 8 * FAR, a["lse"], 10 * FAR, 1 << 30, None) == INVALID
-    assert b"4-byte aligned" in lib.lilicorr_last_error()  # (without a GPU's driver there is no tensor map either)
+    at = dict(q_start=4, kv_start=5, kv_len=6, lse=9)[name] * FAR
+    st, why = cross(lib, **{name: at + 2})
+    assert st == INVALID and b"4-byte aligned" in why
+
+
+@pytest.mark.parametrize("name,size", [("q_start", 12), ("kv_start", 8), ("kv_len", 8)])
+def test_cross_refuses_to_write_what_it_reads(lib, name, size):
+    """At the first and the last word of out (8 x 8 x 128 bf16) and of lse (8 x 8)."""
+    for at in (8 * FAR + 4 - size, 8 * FAR + 8 * 8 * 128 * 2 - 4, 9 * FAR + 4 - size, 9 * FAR + 8 * 8 * 4 - 4):
+        st, why = cross(lib, **{name: at})
+        assert st == INVALID and b"overlap" in why
 
 
 @pytest.mark.parametrize("name", ["q_start", "kv_len", "table", "lse", "tail"])
