@@ -7,7 +7,7 @@ import torch
 
 from tests import loop_ref as R
 from tests.test_gpu_cross import check, i32, make
-from tests.test_gpu_pages import make_caches, pool, same
+from tests.test_gpu_pages import count, make_caches, pool, same
 
 pytestmark = pytest.mark.gpu
 
@@ -193,3 +193,60 @@ def test_cache_attention_tiles_that_take_longer_than_a_wait(lc):
     assert bool(((out >= (1 - 2.0 ** -8) * 2.0 ** 26 / n) & (out <= 1)).all())  # (as above)
     seen = torch.arange(n - rows + 1, n + 1, device="cuda").double()
     assert (lse[:, 0].double() - seen.log()).abs().max() <= (n / 16 + 40) * 2.0 ** -24
+
+
+@pytest.mark.parametrize("group", [43, 47, 65, 95])
+@pytest.mark.parametrize("D,scale", [(64, 0.2), (64, -0.3), (128, 0.1), (80, -0.15)])
+def test_cross_groups_whose_tokens_straddle_halves_and_tiles(lc, group, D, scale):
+    check(lc, *make([(9, 300), (1, 40), (13, 129), (0, 7), (3, 1), (6, 700)], 2, group, D, group), 13, scale=scale)
+
+
+@pytest.mark.parametrize("group", [1, 4, 3])
+def test_cross_requests_of_the_same_states_under_a_negative_scale(lc, group):
+    q, k, v, *_ = make([(5, 300), (140, 200), (9, 100)], 2, group, 64, group)
+    check(lc, q, k, v, i32(0, 5, 145, 154), i32(7, 7, 60), i32(290, 290, 237), 140, scale=-0.25)
+
+
+def test_grow_and_the_append_that_takes_its_tails_replayed(lc):
+    """Captured together and replayed for three tokens: forked rows leave a shared tail page, whose tokens go with them."""
+    page, D, heads, beams = 16, 32, 2, 3
+
+    def state():
+        table = torch.full((beams, 4), -1, dtype=torch.int32, device="cuda")
+        table[:, 0] = 2
+        refs, n = count(table.cpu(), 12).cuda(), torch.full((beams,), 14, dtype=torch.int32, device="cuda")
+        return refs, table, n, make_caches(lc, 1, 12, heads, page, D, 9)[0]
+
+    one, q_start = torch.ones(beams, dtype=torch.int32, device="cuda"), i32(*range(beams + 1))
+    ws = lc.kv8_pages_workspace(12, beams)
+    kv = torch.randn(3, 2, beams, heads, D, device="cuda").to(torch.bfloat16)
+
+    def step(refs, table, n, cache, k, v, out):
+        lc.kv8_grow(refs, table, n, one, page, 1, out=out, workspace=ws)
+        n.add_(1)
+        lc.kv8_append(cache, k, v, q_start, n, table, 1, tail_src=out[0])
+
+    runs = []
+    for captured in (False, True):
+        s = state()
+        k, v = torch.empty_like(kv[0, 0]), torch.empty_like(kv[0, 0])
+        out = torch.empty(beams, dtype=torch.int32, device="cuda"), torch.empty(beams, dtype=torch.bool, device="cuda")
+        if captured:
+            spare = state()
+            step(*spare, k, v, out)
+            gr = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(gr):
+                step(*s, k, v, out)
+        tails = []
+        for i in range(3):
+            k.copy_(kv[i, 0]), v.copy_(kv[i, 1])
+            gr.replay() if captured else step(*s, k, v, out)
+            tails.append(out[0].tolist())
+            assert out[1].all()
+        assert tails == [[2] * beams, [-1] * beams, [-1] * beams]
+        runs.append(s)
+    (ra, ta, na, ca), (rb, tb, nb, cb) = runs
+    assert torch.equal(ra, rb) and torch.equal(ta, tb) and na.tolist() == nb.tolist() == [17] * beams
+    assert ta.tolist() == [[0, 2, -1, -1], [1, 4, -1, -1], [3, 5, -1, -1]]  # (page 2 fell free at the first token)
+    for x, y in zip((ca.k, ca.v, ca.k_scale, ca.v_scale), (cb.k, cb.v, cb.k_scale, cb.v_scale)):
+        assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
