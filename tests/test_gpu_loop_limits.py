@@ -250,3 +250,52 @@ def test_grow_and_the_append_that_takes_its_tails_replayed(lc):
     assert ta.tolist() == [[0, 2, -1, -1], [1, 4, -1, -1], [3, 5, -1, -1]]  # (page 2 fell free at the first token)
     for x, y in zip((ca.k, ca.v, ca.k_scale, ca.v_scale), (cb.k, cb.v, cb.k_scale, cb.v_scale)):
         assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+
+
+@pytest.mark.parametrize("inplace", [False, True])
+@pytest.mark.parametrize("mask_alone", [False, True])
+def test_adjust_more_rows_than_a_grid_holds_side_by_side(lc, inplace, mask_alone):
+    rows, V = 70001, 37
+    g = torch.Generator(device="cuda").manual_seed(8)
+    x = torch.randn(rows, V, generator=g, device="cuda")
+    masks = torch.randint(-(1 << 31), 1 << 31, (3, 2), generator=g, device="cuda").int()
+    index = torch.randint(-1, 3, (rows,), generator=g, device="cuda").int()
+    allowed = ((masks[:, :, None] >> torch.arange(32, device="cuda")) & 1).view(3, 64)[:, :V].bool()
+    allowed = torch.cat([allowed, torch.ones(1, V, dtype=torch.bool, device="cuda")])[index.long()]
+    kw, want = {}, x.double()
+    if not mask_alone:
+        history = torch.randint(0, V, (rows, 3), generator=g, device="cuda").int()
+        seen = torch.randint(0, 4, (rows,), generator=g, device="cuda").int()
+        kw = dict(history=history, seen=seen, frequency=torch.rand(rows, generator=g, device="cuda"))
+        there = torch.arange(3, device="cuda") < seen[:, None]
+        want = want - torch.zeros_like(want).scatter_add_(1, history.long(), there.double()) * kw["frequency"].double()[:, None]
+    want = torch.where(allowed, want, R.NEG)
+    got = lc.adjust_logits(x, mask=masks, mask_index=index, out=None if inplace else torch.empty_like(x), **kw)
+    assert (got is x) == inplace
+    inside = allowed & want.isfinite()
+    assert bool((got[~inside] == R.NEG).all())
+    # a sum of at most two terms of up to 3 x 1 and 6 in all, off by 2^-46 of each, rounded once
+    assert ((got.double() - want).abs()[inside] <= 2.0 ** -24 * want.abs()[inside] + 2.0 ** -42).all()
+
+
+@pytest.mark.parametrize("layers,n_tables", [(1, 19), (35, 3), (17, 8), (16, 9)])
+def test_compact_more_tables_and_caches_than_a_launch_takes(lc, layers, n_tables):
+    n = 60
+    g = torch.Generator().manual_seed(layers)
+    caches = make_caches(lc, layers, n, 1, 16, 32, 3)
+    pages = torch.randperm(n, generator=g)[:31].int()
+    flat = torch.full((n_tables * 20,), -1, dtype=torch.int32)
+    flat[torch.randperm(flat.numel(), generator=g)[:31]] = pages
+    tables = [t.clone() for t in flat.view(n_tables, 2, 10)]
+    refs = count(flat, n)
+    wrefs, wtab, moves, live = R.compact(refs, tables)
+    want = [[t.clone() for t in (c.k.view(torch.uint8), c.v.view(torch.uint8), c.k_scale, c.v_scale)] for c in caches]
+    for parts in want:
+        for t in parts:
+            for a, b in moves:
+                t[b] = t[a]
+    refs, tables = refs.cuda(), [t.cuda() for t in tables]
+    assert lc.kv8_compact(caches, refs, tables).tolist() == [live]
+    assert same(refs, wrefs) and all(same(t, w) for t, w in zip(tables, wtab))
+    for c, w in zip(caches, want):
+        assert all(torch.equal(x, y) for x, y in zip((c.k.view(torch.uint8), c.v.view(torch.uint8), c.k_scale, c.v_scale), w))
