@@ -14,7 +14,7 @@ static __device__ uint32_t g_err_adjust;
 //   x1 = c > 0 ? (x > 0 ? x / rho : x rho) : x,  x2 = x1 - freq g - [g > 0] pres,  x3 = x2 + bias_v,
 //   y = allowed(v) ? x3 : -inf.
 // Only the tokens of the history and of the bias list need arithmetic.  They are few, and penalties
-// and biases may all but cancel, so sums are kept as pairs of floats, hi + lo, off by 2^-47 of their
+// and biases may all but cancel, so sums are kept as pairs of floats, hi + lo, off by 2^-46 of their
 // terms' magnitudes for each term, and rounded once; where that does not do (values near the ends of
 // the type, or not finite, counts of 2^24 and more) in 64 bits, which are slow on this part.
 //
@@ -27,10 +27,13 @@ static __device__ uint32_t g_err_adjust;
 // all sums are of integers.
 //
 // Bound by its steps' latency and its instructions: 256 rows of 151,936 in bf16 with histories of up to 4,096, 64 biases
-// and 16 grammars 35.5 us (23.6 at the copy rate), so that as many CTAs as can be share an SM: four of 512 threads, at 32
-// registers, 35.0 us (before tokens of several biases went to a warp), three 35.9, two that hold the piece in registers meanwhile 41.5.  Pieces of 64 KB go over a history
-// half as often as those of 32 KB: those take 40.5 with 256 threads.  A mask alone, 512 rows in place, 33 us (25 at the copy
-// rate for the sectors that a mask takes in part); 256 threads, 37 with 512.
+// and 16 grammars 33.7 us in a graph (23.6 at the copy rate), so that as many CTAs as can be share an SM: four of 512
+// threads, at 32 registers, of which it spills eight or so (1,280 CTAs are two waves of 608, and 64 more).  Measured when
+// each change was made: four CTAs 35.0, three 35.9, two that hold the piece in registers meanwhile 41.5; pieces of 32 KB,
+// which go over a history twice as often, 40.5 with 256 threads.  The piece is the same for small calls, where fewer CTAs
+// than SMs are at work (16 rows of 32,003 in f32 7.0 us), and for penalties in place, where each of a row's pieces still
+// goes over its history (the large case without masks and biases 23 us).  A mask alone, 512 rows in place, 31 us (25 at
+// the copy rate for the sectors that a mask takes in part); 256 threads, 37 with 512.
 // A history's tokens are at most as many as it is long, so lists grow with it, and fewer CTAs share an SM: lists end at
 // 8,192 tokens, and a piece with more different ones takes them a list at a time (256 rows with histories of 32,768, 161 us
 // with whole lists, 88; 84 with lists of 4,096, but those make 64 x 4 rows of 32,003 tokens 73 for 50).  That loop stands apart,
@@ -378,7 +381,8 @@ __device__ __noinline__ void touch_rest(const Rest<T>& r) {
     }
     for (int i = tid; i < min(r.list, r.all - static_cast<int>(w0)); i += AJ_TOUCH) {
       const int t = r.token[i];
-      if (!(r.biased[t >> 5] >> (t & 31) & 1) && (!r.m || allowed(r.m, r.t0 + t))) touch(r.o + t, static_cast<float>(r.x[t]), true, r.count[i], 0, 0, 0, r.pen);
+      if (!(r.biased[t >> 5] >> (t & 31) & 1) && (!r.m || allowed(r.m, r.t0 + t)))
+        touch(r.o + t, static_cast<float>(r.x[t]), true, r.count[i], 0, 0, 0, r.pen);
     }
     for (int i = tid; i < r.n_bias; i += AJ_TOUCH) {
       const int id = r.id[i];

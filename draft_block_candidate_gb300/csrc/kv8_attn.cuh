@@ -307,12 +307,13 @@ __device__ __forceinline__ void join_parts(const JoinTile<D, ROWS>& t, int r, in
 
 // Joins the parts of the tiles that several CTAs hold, always in order: Y CTAs of W warps for each
 // boundary between two runs (or fewer, for tiles of no more than `most` rows in all, 1 / Y of a tile's
-// to a CTA).  The CTAs of all boundaries inside a tile share its rows, and where there are more warps than rows, W / rows of them share a row's parts.  What bounds it is the
-// latency of the reads, so as many as can be are under way: 8 parts of a row, or (a tile of 128 in
-// two parts, the usual case: all warps are resident at once then) two parts of four rows.  Measured,
-// the whole call: 64 sequences of 16 new tokens 5.9 us less than with a row a warp (99.9 now); 16 new
-// tokens of one sequence over 131,072 with one key / value head 32 us, 185 with the CTAs of one
-// boundary at work alone; two sequences' single tokens over as many, 8 heads, 56 and 58.
+// to a CTA).  The CTAs of all boundaries inside a tile share its rows, and where there are more warps
+// than rows, W / rows of them share a row's parts.  What bounds it is the latency of the reads, so as
+// many as can be are under way: 8 parts of a row, or (a tile of 128 in two parts, the usual case: all
+// warps are resident at once then) two parts of four rows.  Measured, the whole call: 64 sequences of 16
+// new tokens 5.9 us less than with a row a warp (100.4 now); 16 new tokens of one sequence over 131,072
+// with one key / value head 32 us, 185 with the CTAs of one boundary at work alone; two sequences'
+// single tokens over as many, 8 heads, 56 and 58.
 template <int D, int ROWS, int W, int Y, class P = AttnParams>
 __global__ void __launch_bounds__(32 * W) kv8_join_kernel(const P p, int runs, int most) {
   constexpr int E = D / 32, R = ROWS / (W * Y);  // columns of a lane; rows of a warp, in the usual case

@@ -174,9 +174,12 @@ __device__ __forceinline__ void each_page(const int32_t* refs, int64_t lo, int64
 //
 // Rows are written where they get their pages and nowhere else.  Until the pages are dealt the workspace says
 // which columns take one: a bit of a row's word for each where no row writes more than 31, else by how many
-// held each page before the call (by those counts alone a step of 1,024 rows took 18.7 us for 18.0).  Bound by its dependent reads and its barriers: 1,024 rows of 16
-// new tokens on a pool of 52,396 pages 13 us, 4 rows on a small one 5.5.  Pages and rows are counted
-// behind one barrier (with one for each, a small step's three kernels took 12.4 us for 8.3).
+// held each page before the call (by those counts alone a step of 1,024 rows took 18.7 us for 18.0).
+//
+// Bound by its dependent reads and its barriers: 1,024 rows of 16 new tokens on a pool of 52,396 pages 13 us,
+// 4 rows on a small one 5.5; every count is read, so that a step of 4 rows on a pool of 300,000 takes 23.5 us in
+// all.  Pages and rows are counted behind one barrier (with one for each, a small step's three kernels took 12.4 us
+// for 8.3).
 struct GrowParams {
   int32_t* refs;
   int64_t n_pages;

@@ -541,7 +541,8 @@ lilicorr_status lilicorr_kv8_compact(const lilicorr_kv8_cache* caches, int32_t n
  * head_dim is a multiple of 8, at most 128.  What is not finite stays where it is seen: an infinity or a NaN
  * among a head's values makes that column of its rows NaN or infinite, one among the keys the rows whose
  * scores it is part of; what lies behind a request's states has no influence.  Sums and maxima are f32;
- * the softmax weights are rounded to bf16 before the second product.  The bits of a result do not depend
+ * the softmax weights are rounded to bf16 before the second product, whose sums drop what a product has 2^-25
+ * below them (values of one sign over T states: up to T 2^-26 of their sum, where one SM goes over them all).  The bits of a result do not depend
  * on when or where its parts were worked out, but on the device's number of SMs and the other requests
  * of the call.  Workspace: lilicorr_cross_attention_workspace_bytes (0 for unsupported sizes; by the
  * current device), 256-byte aligned, no initial contents.  Calls that overlap must not share it.
