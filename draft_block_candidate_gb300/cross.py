@@ -31,7 +31,7 @@ def cross_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_start: 
     and head multiples of 8; head_dim a multiple of 8, at most 128).  Request b has rows
     q_start[b] .. q_start[b+1]-1 of q (its beams, the tokens of a block, or both; at most
     max_new) and states kv_start[b] .. kv_start[b] + kv_len[b] - 1 of k and v; int32.  A padded
-    batch [batch, T, ...] of states is k.flatten(0, 1) with kv_start = b * T.
+    batch [batch, T, ...] of states is k.flatten(0, 1) with kv_start = b * T.  k and v may hold no states at all.
     scale: 1 / sqrt(head_dim) by default.  out [total, q_heads, head_dim] bf16 (rows outside the
     requests keep what they hold; a new one holds zeros there).  lse: True, or a tensor
     [total, q_heads] f32 to write the natural-log sums of exponentials to (True: -inf outside

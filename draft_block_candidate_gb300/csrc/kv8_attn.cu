@@ -39,7 +39,7 @@
 // out is rounded to bf16.
 //
 // Bound: neither memory nor the tensor cores (64 sequences of 16 new tokens over up to 4,096
-// cached ones, 64 query and 8 key / value heads of 128: 99.9 us, 94 of them this kernel's; the
+// cached ones, 64 query and 8 key / value heads of 128: 100.2 us, 94 of them this kernel's; the
 // cache's bytes take 50.6 us at 6.7 TB/s, the products 40.5) but the instructions of the softmax
 // and the widening, some 5,300 of a warp to a chunk, which four schedulers issue at half their
 // rate (2.2 of 4), the first tile's q (12,000 cycles before the first product), and what a tile's change

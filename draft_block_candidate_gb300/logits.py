@@ -46,7 +46,7 @@ def adjust_logits(logits: torch.Tensor, history: Optional[torch.Tensor] = None, 
     """lilicorr_adjust_logits: penalties for repeated tokens, biases and grammar masks.
 
     logits [..., V] bf16/f32 (rows a uniform stride >= V apart), edited in place, or into
-    `out` of the same shape and type.  history [groups, cap] int32 token ids (groups divides
+    `out` of the same shape and type, which shares nothing with them or with what else is read.  history [groups, cap] int32 token ids (groups divides
     the rows; consecutive rows share one: the beams or the drafted rows of a request), of
     which row r sees the first seen[r] ([rows] int32); repetition, presence and frequency
     [groups] f32, the last two counting from position counted_from ([groups] int32) on.

@@ -532,7 +532,7 @@ lilicorr_status lilicorr_kv8_compact(const lilicorr_kv8_cache* caches, int32_t n
  * whose every score is -inf.
  *   q      [total, q_heads, head_dim] bf16, element strides by token and head, multiples of 8, 16-byte
  *          aligned
- *   k, v   [total_kv, kv_heads, head_dim] bf16, likewise; rows do not overlap
+ *   k, v   [total_kv, kv_heads, head_dim] bf16, likewise, total_kv >= 1; rows do not overlap
  *   q_start [batch + 1], kv_start, kv_len [batch] int32 (device memory); max_new at least every request's
  *          rows.  A request whose rows or states are out of range is left out, and bit 26 of the device
  *          error word set
